@@ -34,11 +34,12 @@
 #include "elementwise.cuh"
 #include "gemm.cuh"
 #include "gns.h"
+#include "runtime.cuh"
 
 namespace gns {
 namespace {
-
 thread_local std::string g_last_error;
+}  // namespace
 
 int fail(int code, const std::string& msg) {
     g_last_error = msg;
@@ -49,39 +50,17 @@ int cuda_fail(cudaError_t e, const char* what) {
     return fail(GNS_ERR_CUDA, std::string(what) + ": " + cudaGetErrorString(e));
 }
 
-#define CK(call)                                                        \
-    do {                                                                \
-        cudaError_t e_ = static_cast<cudaError_t>(call);                \
-        if (e_ != cudaSuccess) return cuda_fail(e_, #call);             \
-    } while (0)
-
-#define RET(call)                 \
-    do {                          \
-        int r_ = (call);          \
-        if (r_ != GNS_OK) return r_; \
-    } while (0)
+namespace {
 
 constexpr float kQuintic[3] = {3.4445f, -4.7750f, 2.0315f};
 
 size_t align_up(size_t v, size_t a) { return (v + a - 1) / a * a; }
 long long round_up_ll(long long v, long long a) { return (v + a - 1) / a * a; }
 
-struct DeviceState {
-    int device = -1;
-    int num_sms = 0;
-    int cc_major = 0, cc_minor = 0;
-    char* ws = nullptr;
-    size_t ws_bytes = 0;
-    int* err = nullptr;      // status block: [0] status word, [1] abort mark (see DevStatus)
-    int epoch = 0;           // number of the current call on this device
-    DevStatus status{};      // the current call's device-side error reporting
-    float* stage = nullptr;  // device staging for the host-buffer entry point
-    size_t stage_bytes = 0;
-    cudaStream_t h2d = nullptr, d2h = nullptr;  // copy streams of the host-buffer entry point
-};
-
 std::mutex g_mu;
 std::map<int, DeviceState> g_dev;
+
+}  // namespace
 
 int get_state(DeviceState** out) {
     int dev = 0;
@@ -107,13 +86,12 @@ int get_state(DeviceState** out) {
 }
 
 // Bound of every device-side wait: 2 s, or GNS_WAIT_LIMIT_MS.
-unsigned long long wait_limit_ns() {
+static unsigned long long wait_limit_ns() {
     const char* e = std::getenv("GNS_WAIT_LIMIT_MS");
     if (e && std::atoll(e) > 0) return static_cast<unsigned long long>(std::atoll(e)) * 1000000ull;
     return kDefaultWaitLimitNs;
 }
 
-// Starts a call on a device: a new epoch for its kernels' abort mark.
 void begin_call(DeviceState& st) {
     st.epoch = st.epoch == 0x7fffffff ? 1 : st.epoch + 1;
     st.status = DevStatus{st.err, st.epoch, 0, wait_limit_ns()};
@@ -136,6 +114,8 @@ int ensure_workspace(DeviceState& st, size_t bytes) {
     st.ws_bytes = want;
     return GNS_OK;
 }
+
+namespace {
 
 // ---------------------------------------------------------------------------
 // Allocation-free variant of gns_orthogonalize_batched.
@@ -170,16 +150,10 @@ std::map<int, NoAllocDevice> g_noalloc;
 // bracketed by a pair of CUDA events on its own stream; gns_profile_read()
 // turns them into per-class launch counts and summed durations.
 
-enum KernelClass { kClsGemm = 0, kClsNorm = 1, kClsMuon = 2, kClsCopy = 3, kNumCls = 4 };
-
 std::atomic<long long> g_launches{0};
 std::atomic<bool> g_profiling{false};
 std::mutex g_prof_mu;
-struct ProfRec {
-    cudaEvent_t a, b;
-    int cls;
-};
-std::vector<ProfRec> g_recs;
+std::vector<LaunchMark> g_recs;
 std::vector<cudaEvent_t> g_event_pool;
 
 cudaEvent_t take_event() {
@@ -196,27 +170,27 @@ cudaEvent_t take_event() {
     return e;
 }
 
-template <typename F>
-int counted_launch(int cls, cudaStream_t s, F&& fn) {
-    ProfRec rec{nullptr, nullptr, cls};
-    const bool prof = g_profiling.load();
-    if (prof) {
+}  // namespace
+
+LaunchMark launch_begin(int cls, cudaStream_t s) {
+    LaunchMark m{nullptr, nullptr, cls};
+    if (g_profiling.load()) {
         std::lock_guard<std::mutex> lk(g_prof_mu);
-        rec.a = take_event();
-        rec.b = take_event();
-        if (rec.a) cudaEventRecord(rec.a, s);
+        m.a = take_event();
+        m.b = take_event();
+        if (m.a) cudaEventRecord(m.a, s);
     }
-    const int r = fn();
-    g_launches.fetch_add(1);
-    if (prof && rec.a && rec.b) {
-        cudaEventRecord(rec.b, s);
-        std::lock_guard<std::mutex> lk(g_prof_mu);
-        g_recs.push_back(rec);
-    }
-    return r;
+    return m;
 }
 
-#define LAUNCH(cls, call) CK(counted_launch((cls), s, [&]() { return static_cast<int>(call); }))
+void launch_end(const LaunchMark& m, cudaStream_t s) {
+    g_launches.fetch_add(1);
+    if (m.a && m.b) {
+        cudaEventRecord(m.b, s);
+        std::lock_guard<std::mutex> lk(g_prof_mu);
+        g_recs.push_back(m);
+    }
+}
 
 // ------------------------------------------------------------ tensor maps
 
@@ -232,6 +206,8 @@ PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
     }
     return fn;
 }
+
+namespace {
 
 // A set of G row-major matrices in device memory.
 struct Mat {
@@ -1531,7 +1507,7 @@ int64_t gns_launch_count(void) { return g_launches.load(); }
 void gns_profile_enable(int on) { g_profiling.store(on != 0); }
 
 int gns_profile_read(int64_t* counts, double* ms, int max_classes) {
-    std::vector<ProfRec> recs;
+    std::vector<LaunchMark> recs;
     {
         std::lock_guard<std::mutex> lk(g_prof_mu);
         recs.swap(g_recs);

@@ -1,0 +1,89 @@
+// Host-side runtime shared by the C ABI translation units: error texts, the
+// per-device state with its cached workspace, launch accounting and the
+// tensor-map encoder. Defined in api.cu.
+#pragma once
+
+#include <cuda_runtime.h>
+#include <cudaTypedefs.h>
+
+#include <cstddef>
+#include <string>
+
+#include "gns.h"
+#include "ptx.cuh"
+
+namespace gns {
+
+// Records the text gns_last_error() returns and passes the code on.
+int fail(int code, const std::string& msg);
+int cuda_fail(cudaError_t e, const char* what);
+
+#define CK(call)                                                        \
+    do {                                                                \
+        cudaError_t e_ = static_cast<cudaError_t>(call);                \
+        if (e_ != cudaSuccess) return cuda_fail(e_, #call);             \
+    } while (0)
+
+#define RET(call)                 \
+    do {                          \
+        int r_ = (call);          \
+        if (r_ != GNS_OK) return r_; \
+    } while (0)
+
+struct DeviceState {
+    int device = -1;
+    int num_sms = 0;
+    int cc_major = 0, cc_minor = 0;
+    char* ws = nullptr;
+    size_t ws_bytes = 0;
+    int* err = nullptr;      // status block: [0] status word, [1] abort mark (see DevStatus)
+    int epoch = 0;           // number of the current call on this device
+    DevStatus status{};      // the current call's device-side error reporting
+    float* stage = nullptr;  // device staging for the host-buffer entry point
+    size_t stage_bytes = 0;
+    cudaStream_t h2d = nullptr, d2h = nullptr;  // copy streams of the host-buffer entry point
+};
+
+// State of the current device, created on first use.
+int get_state(DeviceState** out);
+
+// Starts a call on a device: a new epoch for its kernels' abort mark.
+void begin_call(DeviceState& st);
+
+int ensure_workspace(DeviceState& st, size_t bytes);
+
+// Kernel classes of gns_profile_read().
+enum KernelClass {
+    kClsGemm = 0,
+    kClsNorm = 1,
+    kClsMuon = 2,
+    kClsCopy = 3,
+    kClsFp8Gemm = 4,
+    kClsFp8Cast = 5,
+    kClsMoe = 6,
+    kClsDropout = 7,
+    kNumCls = 8
+};
+
+// Accounting around one launch (see gns_launch_count, gns_profile_enable).
+struct LaunchMark {
+    cudaEvent_t a, b;  // null unless profiling is on
+    int cls;
+};
+LaunchMark launch_begin(int cls, cudaStream_t s);
+void launch_end(const LaunchMark& m, cudaStream_t s);
+
+template <typename F>
+int counted_launch(int cls, cudaStream_t s, F&& fn) {
+    const LaunchMark m = launch_begin(cls, s);
+    const int r = fn();
+    launch_end(m, s);
+    return r;
+}
+
+#define LAUNCH(cls, call) CK(::gns::counted_launch((cls), s, [&]() { return static_cast<int>(call); }))
+
+// The driver's tensor-map encoder (null when unavailable).
+PFN_cuTensorMapEncodeTiled_v12000 encode_fn();
+
+}  // namespace gns
