@@ -253,6 +253,161 @@ int gns_muon_update(uint16_t* W_bf16, const uint16_t* O_fp16, int rows, int cols
 int gns_symm_gemm(const void* A, const void* B, const void* C, void* D, int G, int n, int k,
                   float alpha, float beta, void* stream);
 
+/* ---------------------------------------------------------------------------
+ * Operators of a training block around the optimizer: counter-based dropout,
+ * the routing of tokens to experts, and linear layers on block-scaled 8-bit
+ * operands, dense or grouped by expert.
+ *
+ * Matrices are row-major with a row stride (ld..., in elements) of at least
+ * their columns. Sums are fp32 and each result is rounded once to its type.
+ * Calls are asynchronous and write only what they name; those that need a
+ * workspace (gns_moe_sort beyond 4096 slots, gns_fp8_linear, products of few
+ * rows) use the library's, under the rule stated at the top of this file.
+ */
+typedef enum { GNS_BF16 = 0, GNS_FP16 = 1, GNS_FP32 = 2 } gns_dtype;
+
+/* 8-bit formats: e4m3 (largest value 448, no infinity) and e5m2 (57344). */
+typedef enum { GNS_E4M3 = 0, GNS_E5M2 = 1 } gns_fp8_format;
+
+#define GNS_MAX_EXPERTS 1024
+
+/*
+ * gns_dropout: y = residual + (u >= t ? x * 65536 / (65536 - t) : 0) over rows
+ * x cols elements, t = round(65536 p), residual NULL for none. u is the
+ * element's 16-bit draw: Philox4x32-10, key = seed, counter (g >> 3, step with
+ * its top bit set), g = base_index + row * cols + col; element g takes the
+ * half (g & 1), low first, of output word (g & 7) >> 1. No mask is stored: the
+ * backward pass is the same call on the gradient with the same p, seed, step
+ * and base_index and no residual (the residual's gradient is the gradient
+ * itself). A dropped element contributes 0 whatever its value.
+ *   p           in [0, 1]; p = 1 drops everything.
+ *   step        below 2^63 (muon_step's draws of the same seed and step are others).
+ *   y           may be x or residual itself.
+ */
+int gns_dropout(const void* x, const void* residual, void* y, int64_t rows, int64_t cols, int64_t ldx, int64_t ldr,
+                int64_t ldy, int dtype, double p, uint64_t seed, uint64_t step, int64_t base_index, void* stream);
+
+/*
+ * gns_moe_sort: stable counting sort of the n = tokens * topk slots (slot s:
+ * choice s % topk of token s / topk) by expert.
+ *   experts  device int32 or int64 (id_bytes 4 or 8) [tokens][topk]. An id
+ *            outside 0 .. num_experts - 1 is a slot without an expert
+ *            (dropped over capacity, padding).
+ *   offsets  device int32 [num_experts + 1], written: expert e owns the sorted
+ *            rows offsets[e] .. offsets[e + 1] - 1; rows from
+ *            offsets[num_experts] on are those of the slots without an expert.
+ *   rows     device int32 [n], written: the sorted row of each slot.
+ *   slots    device int32 [n], written: the slot of each sorted row.
+ * 1 <= num_experts <= GNS_MAX_EXPERTS.
+ */
+int gns_moe_sort(const void* experts, int id_bytes, int tokens, int topk, int num_experts, int32_t* offsets,
+                 int32_t* rows, int32_t* slots, void* stream);
+
+/*
+ * gns_moe_gather: y[rows[s]] = x[s / topk] (cols elements) for every slot s
+ * with an expert; the rows of the others are set to zero. Its gradient is
+ * gns_moe_combine with weights NULL. offsets and rows as written by
+ * gns_moe_sort; x has tokens rows, y tokens * topk.
+ */
+int gns_moe_gather(const void* x, int64_t ldx, int tokens, int topk, int num_experts, int cols, int dtype,
+                   const int32_t* offsets, const int32_t* rows, void* y, int64_t ldy, void* stream);
+
+/*
+ * gns_moe_combine: out[t] = sum over the slots s of token t that have an
+ * expert, in slot order, of weights[s] * y[rows[s]] (weights fp32 [n], NULL
+ * for 1). A token without any expert gets 0.
+ */
+int gns_moe_combine(const void* y, int64_t ldy, const float* weights, int tokens, int topk, int num_experts, int cols,
+                    int dtype, const int32_t* offsets, const int32_t* rows, void* out, int64_t ldo, void* stream);
+
+/*
+ * gns_moe_combine_backward: the gradients of gns_moe_combine,
+ * dy[rows[s]] = weights[s] * dout[s / topk] and
+ * dweights[s] = sum_c dout[s / topk][c] * y[rows[s]][c]; both 0 for slots
+ * without an expert. dweights (and then y) may be NULL.
+ */
+int gns_moe_combine_backward(const void* dout, int64_t lddo, const void* y, int64_t ldy, const float* weights,
+                             int tokens, int topk, int num_experts, int cols, int dtype, const int32_t* offsets,
+                             const int32_t* rows, void* dy, int64_t lddy, float* dweights, void* stream);
+
+/*
+ * gns_fp8_quantize: the 8-bit forms of a rows x cols matrix, with a scale for
+ * each block of 128 values: s = the smallest power of two (at least 2^-126)
+ * with amax / s <= the format's largest value, amax over the block's finite
+ * values; q = x / s rounded to nearest even; NaN and infinities become NaN.
+ *   slots, topk    row r is read from x[slots[r] / topk] (slots NULL: x[r]):
+ *                  the gather of gns_moe_gather on the way.
+ *   q_rows         row form (or NULL): [rows][ld_rows], blocks along the row;
+ *                  scale_rows [ceil(cols / 128)][ld_scale_rows >= rows].
+ *   q_cols         column form (or NULL): [128 * blocks][ld_cols], blocks of
+ *                  128 rows along each column; scale_cols
+ *                  [blocks][ld_scale_cols >= cols]. Without offsets blocks =
+ *                  ceil(rows / 128). With offsets ([groups + 1], as written
+ *                  by gns_moe_sort) each group starts a block of its own, in
+ *                  group order; the caller provides for
+ *                  floor((rows + 127 min(rows, groups)) / 128) blocks, and
+ *                  those past the last group's are not written. Rows past a
+ *                  group's end are zero.
+ *                  With offsets and a column form, rows past
+ *                  offsets[groups] of the row form are not written.
+ * 8-bit rows are 16-byte aligned (ld a multiple of 16 that covers the
+ * columns; the columns up to the next multiple of 16 are written as zero).
+ * Column scales have 16-byte aligned rows.
+ */
+int gns_fp8_quantize(const void* x, int64_t ldx, int dtype, int rows, int cols, const int32_t* slots, int topk,
+                     const int32_t* offsets, int groups, int format, void* q_rows, int64_t ld_rows, float* scale_rows,
+                     int64_t ld_scale_rows, void* q_cols, int64_t ld_cols, float* scale_cols, int64_t ld_scale_cols,
+                     void* stream);
+
+/*
+ * gns_fp8_quantize_weight: the 8-bit form of `groups` N x K weight matrices
+ * (stride_w elements apart) in blocks of 128 x 128: q [groups][N][ldq], scale
+ * [groups][ceil(N / 128)][ceil(K / 128)], scaled as by gns_fp8_quantize.
+ */
+int gns_fp8_quantize_weight(const void* w, int64_t ldw, int64_t stride_w, int dtype, int groups, int N, int K,
+                            int format, void* q, int64_t ldq, float* scale, void* stream);
+
+/*
+ * gns_fp8_matmul: y[r] = a[r] . w[g]^T for the rows r of each group g, [rows][N],
+ * from the row form of a ([rows][K]) and 8-bit weights:
+ *   y[r][n] = sum over the blocks b of 128 along K of
+ *             scale_a[b][r] scale_w[g][n / 128][b] sum_{k in b} a[r][k] w[g][n][k].
+ * Any fp32 scales are taken; the product of two must stay in fp32's range.
+ *   offsets  [groups + 1] as written by gns_moe_sort; rows past
+ *            offsets[groups] of y are set to zero. NULL with groups = 1: all
+ *            rows are one group's.
+ */
+int gns_fp8_matmul(const void* a, int64_t lda, const float* scale_a, int64_t ld_scale_a, int format_a, int rows,
+                   const void* w, int64_t ldw, const float* scale_w, int format_w, int groups, int N, int K,
+                   const int32_t* offsets, void* y, int64_t ldy, int out_dtype, void* stream);
+
+/*
+ * gns_fp8_matmul_dgrad: the data gradient dx[r] = dy[r] . w[g], [rows][K], from
+ * the row form of dy ([rows][N]) and the same 8-bit weights.
+ */
+int gns_fp8_matmul_dgrad(const void* dy, int64_t lddy, const float* scale_dy, int64_t ld_scale_dy, int format_dy,
+                         int rows, const void* w, int64_t ldw, const float* scale_w, int format_w, int groups, int N,
+                         int K, const int32_t* offsets, void* dx, int64_t lddx, int out_dtype, void* stream);
+
+/*
+ * gns_fp8_matmul_wgrad: the weight gradient dw[g] = dy_g^T . x_g, N x K, over
+ * the rows of group g (zero for a group without rows), from the column forms
+ * of dy and x made with the same offsets. The dw[g] are stride_dw elements apart.
+ */
+int gns_fp8_matmul_wgrad(const void* dy, int64_t lddy, const float* scale_dy, int64_t ld_scale_dy, int format_dy,
+                         const void* x, int64_t ldx, const float* scale_x, int64_t ld_scale_x, int format_x, int rows,
+                         int groups, int N, int K, const int32_t* offsets, void* dw, int64_t lddw, int64_t stride_dw,
+                         int out_dtype, void* stream);
+
+/*
+ * gns_fp8_linear: the layer as a serving program calls it: x cast as by
+ * gns_fp8_quantize (e4m3, row form, row r read from x[slots[r] / topk]), then
+ * gns_fp8_matmul. Up to eight rows run as one kernel that casts on the way.
+ */
+int gns_fp8_linear(const void* x, int64_t ldx, int dtype, int rows, const int32_t* slots, int topk,
+                   const int32_t* offsets, const void* w, int64_t ldw, const float* scale_w, int format_w, int groups,
+                   int N, int K, void* y, int64_t ldy, int out_dtype, void* stream);
+
 /* Synchronizes `stream`, returns the device status word of the current device
  * as a gns_status (GNS_OK, GNS_ERR_NONFINITE or GNS_ERR_TIMEOUT) and clears it.
  * It reads both the allocating entry points' word and, once the
@@ -297,8 +452,9 @@ void gns_profile_enable(int on);
  * (ms[k]) since the previous read; then forgets them. Classes: 0 tcgen05
  * GEMM, 1 norm + scale + cast to fp16 (with the momentum update inside
  * muon_step), 2 Muon elementwise (update / write-back, standalone momentum),
- * 3 output copy. Writes min(max_classes, 4) entries of each non-null array
- * and returns the number of classes (4), or a negative gns_status. */
+ * 3 output copy, 4 8-bit products, 5 8-bit casts, 6 expert routing, 7 dropout.
+ * Writes min(max_classes, 8) entries of each non-null array and returns the
+ * number of classes (8), or a negative gns_status. */
 int gns_profile_read(int64_t* counts, double* ms, int max_classes);
 
 /* Workspace bytes currently held on the current device. */

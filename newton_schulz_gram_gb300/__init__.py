@@ -12,13 +12,20 @@ import ctypes
 import torch
 
 from ._lib import GnsError, GnsTensor, check, load
+from .block import (Fp8Cols, Fp8Rows, Fp8Weight, MoeRoute, gns_dropout, gns_dropout_backward, gns_fp8_linear,
+                    gns_fp8_matmul, gns_fp8_matmul_dgrad, gns_fp8_matmul_wgrad, gns_fp8_quantize,
+                    gns_fp8_quantize_weight, gns_moe_combine, gns_moe_combine_backward, gns_moe_gather,
+                    gns_moe_gather_backward, gns_moe_sort)
 
 __all__ = ["gns_orthogonalize_batched", "gns_orthogonalize_batched_host",
            "gns_orthogonalize_batched_noalloc", "gns_orthogonalize_batched_schedule", "muon_step", "normuon_step", "dion3_step",
            "gns_muon_momentum", "gns_muon_update", "gns_symm_gemm", "gns_get_status",
            "gns_status_string", "gns_last_error", "gns_workspace_bytes", "gns_release",
            "gns_launch_count", "gns_profile_enable", "gns_profile_read", "KERNEL_CLASSES",
-           "GnsError", "QUINTIC", "load"]
+           "gns_dropout", "gns_dropout_backward", "gns_moe_sort", "gns_moe_gather", "gns_moe_gather_backward",
+           "gns_moe_combine", "gns_moe_combine_backward", "gns_fp8_quantize", "gns_fp8_quantize_weight",
+           "gns_fp8_matmul", "gns_fp8_matmul_dgrad", "gns_fp8_matmul_wgrad", "gns_fp8_linear", "MoeRoute", "Fp8Rows",
+           "Fp8Cols", "Fp8Weight", "GnsError", "QUINTIC", "load"]
 
 QUINTIC = (3.4445, -4.7750, 2.0315)
 
@@ -257,7 +264,8 @@ def gns_last_error():
     return load().gns_last_error().decode(errors="replace")
 
 
-KERNEL_CLASSES = ("gemm_tc", "norm_cast", "muon_elementwise", "copy_rows")
+KERNEL_CLASSES = ("gemm_tc", "norm_cast", "muon_elementwise", "copy_rows", "fp8_gemm", "fp8_cast", "moe",
+                  "dropout")
 
 
 def gns_launch_count():

@@ -15,6 +15,7 @@ GNS_STATUS = {
 
 # Every symbol include/gns.h declares, with (restype, argtypes).
 _vp, _i, _f, _u64, _i64 = ctypes.c_void_p, ctypes.c_int, ctypes.c_float, ctypes.c_uint64, ctypes.c_int64
+_d = ctypes.c_double
 
 
 class GnsTensor(ctypes.Structure):
@@ -37,6 +38,20 @@ PROTOTYPES = {
     "gns_muon_momentum": (_i, [_vp, _vp, _i64, _f, _vp]),
     "gns_muon_update": (_i, [_vp, _vp, _i, _i, _f, _f, _f, _u64, _u64, _i64, _vp]),
     "gns_symm_gemm": (_i, [_vp, _vp, _vp, _vp, _i, _i, _i, _f, _f, _vp]),
+    "gns_dropout": (_i, [_vp, _vp, _vp, _i64, _i64, _i64, _i64, _i64, _i, _d, _u64, _u64, _i64, _vp]),
+    "gns_moe_sort": (_i, [_vp, _i, _i, _i, _i, _vp, _vp, _vp, _vp]),
+    "gns_moe_gather": (_i, [_vp, _i64, _i, _i, _i, _i, _i, _vp, _vp, _vp, _i64, _vp]),
+    "gns_moe_combine": (_i, [_vp, _i64, _vp, _i, _i, _i, _i, _i, _vp, _vp, _vp, _i64, _vp]),
+    "gns_moe_combine_backward": (_i, [_vp, _i64, _vp, _i64, _vp, _i, _i, _i, _i, _i, _vp, _vp, _vp, _i64, _vp, _vp]),
+    "gns_fp8_quantize": (_i, [_vp, _i64, _i, _i, _i, _vp, _i, _vp, _i, _i, _vp, _i64, _vp, _i64, _vp, _i64, _vp, _i64,
+                              _vp]),
+    "gns_fp8_quantize_weight": (_i, [_vp, _i64, _i64, _i, _i, _i, _i, _i, _vp, _i64, _vp, _vp]),
+    "gns_fp8_matmul": (_i, [_vp, _i64, _vp, _i64, _i, _i, _vp, _i64, _vp, _i, _i, _i, _i, _vp, _vp, _i64, _i, _vp]),
+    "gns_fp8_matmul_dgrad": (_i, [_vp, _i64, _vp, _i64, _i, _i, _vp, _i64, _vp, _i, _i, _i, _i, _vp, _vp, _i64, _i,
+                                  _vp]),
+    "gns_fp8_matmul_wgrad": (_i, [_vp, _i64, _vp, _i64, _i, _vp, _i64, _vp, _i64, _i, _i, _i, _i, _i, _vp, _vp, _i64,
+                                  _i64, _i, _vp]),
+    "gns_fp8_linear": (_i, [_vp, _i64, _i, _i, _vp, _i, _vp, _vp, _i64, _vp, _i, _i, _i, _i, _vp, _i64, _i, _vp]),
     "gns_get_status": (_i, [_vp]),
     "gns_test_bounded_wait": (_i, [_i, _i64, _vp]),
     "gns_status_string": (ctypes.c_char_p, [_i]),

@@ -1,0 +1,393 @@
+"""Operators of a training block around the optimizer: counter-based dropout,
+routing of tokens to experts, and linear layers on block-scaled 8-bit operands.
+
+Each function marshals tensors and calls the C entry point of the same name
+(include/gns.h states what it computes); outputs are new tensors on the
+stream of the call. Gradients are functions of their own, as for the
+optimizer steps: nothing here records an autograd graph.
+"""
+from __future__ import annotations
+
+from typing import NamedTuple
+
+import torch
+
+from ._lib import check, load
+
+DTYPES = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
+FORMATS = {"e4m3": 0, "e5m2": 1}
+_FP8 = {"e4m3": torch.float8_e4m3fn, "e5m2": torch.float8_e5m2}
+_FP8_FORMAT = {torch.float8_e4m3fn: 0, torch.float8_e5m2: 1}
+BLOCK = 128
+
+
+class MoeRoute(NamedTuple):
+    """A sorted routing (gns_moe_sort): expert e owns the sorted rows
+    offsets[e] .. offsets[e + 1] - 1; rows[t, j] is the sorted row of token t's
+    j-th choice and slots its inverse. Rows from offsets[-1] on belong to no
+    expert."""
+    offsets: torch.Tensor  # int32 [num_experts + 1]
+    rows: torch.Tensor     # int32 [tokens, topk]
+    slots: torch.Tensor    # int32 [tokens * topk]
+
+
+class Fp8Rows(NamedTuple):
+    """Row form of a matrix: q [rows, cols rounded up to 16], scale [ceil(cols / 128), rows]."""
+    q: torch.Tensor
+    scale: torch.Tensor
+    cols: int
+
+
+class Fp8Cols(NamedTuple):
+    """Column form: q [128 * blocks, cols rounded up to 16], scale [blocks, cols rounded up to 4]."""
+    q: torch.Tensor
+    scale: torch.Tensor
+    rows: int
+    cols: int
+
+
+class Fp8Weight(NamedTuple):
+    """8-bit weights: q [groups, N, K rounded up to 16], scale [groups, ceil(N / 128), ceil(K / 128)]."""
+    q: torch.Tensor
+    scale: torch.Tensor
+    cols: int
+    grouped: bool  # made from a [groups, N, K] tensor
+
+
+def _ptr(t):
+    return None if t is None else t.data_ptr()
+
+
+def _on(t, stream):
+    return torch.cuda.current_stream(t.device).cuda_stream if stream is None else stream.cuda_stream
+
+
+def _new(shape, dtype, like, stream):
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=like.device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=like.device)
+
+
+def _typed(t, name, dtypes=DTYPES):
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.dtype not in dtypes:
+        raise TypeError(f"{name} must be one of {sorted(str(d) for d in dtypes)}, got {t.dtype}")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+
+
+def _same_device(like, **tensors):
+    for name, t in tensors.items():
+        if t is not None and t.device != like.device:
+            raise ValueError(f"{name} is on {t.device}, not on {like.device}")
+
+
+def _matrix(t, name, dtypes=DTYPES):
+    """A 2D tensor with unit column stride; returns its row stride."""
+    _typed(t, name, dtypes)
+    if t.dim() != 2:
+        raise ValueError(f"{name} must be 2D")
+    if t.shape[1] > 1 and t.stride(1) != 1:
+        raise ValueError(f"{name} must have contiguous rows")
+    ld = t.stride(0) if t.shape[0] > 1 else max(t.shape[1], 1)
+    if ld < t.shape[1]:
+        raise ValueError(f"{name} must have rows that do not overlap")
+    return ld
+
+
+def _contiguous(t, dtype, name):
+    _typed(t, name, {dtype: 0})
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+
+
+def _up(v, a):
+    return -(-v // a) * a
+
+
+# ------------------------------------------------------------------ dropout
+
+def _rows_of(t, name):
+    """(rows, cols, row stride) of a contiguous tensor or a 2D one with contiguous rows."""
+    _typed(t, name)
+    if t.is_contiguous():
+        cols = t.shape[-1] if t.dim() else 1
+        return (t.numel() // cols if cols else 0), cols, cols
+    return t.shape[0] if t.dim() == 2 else 0, t.shape[-1], _matrix(t, name)
+
+
+def gns_dropout(x, p, seed, step, residual=None, base_index=0, out=None, stream=None):
+    """residual + dropout(x): each element is kept, scaled by 1 / (1 - p), where
+    its draw keyed by (seed, step, base_index + element index) says so, p being
+    rounded to a multiple of 2^-16. x: bf16, fp16 or fp32, contiguous or 2D
+    with contiguous rows. out may be x or residual."""
+    rows, cols, ldx = _rows_of(x, "x")
+    ldr = 0
+    for name, t in (("residual", residual), ("out", out)):
+        if t is not None and (t.dtype != x.dtype or t.shape != x.shape):
+            raise ValueError(f"{name} must have the type and shape of x")
+    if residual is not None:
+        ldr = _rows_of(residual, "residual")[2]
+    if out is None:
+        out = _new(x.shape, x.dtype, x, stream)
+    ldy = _rows_of(out, "out")[2]
+    _same_device(x, residual=residual, out=out)
+    check(load().gns_dropout(x.data_ptr(), _ptr(residual), out.data_ptr(), rows, cols, ldx, ldr, ldy, DTYPES[x.dtype],
+                             p, seed, step, base_index, _on(x, stream)), "gns_dropout")
+    return out
+
+
+def gns_dropout_backward(dout, p, seed, step, base_index=0, out=None, stream=None):
+    """The gradient of gns_dropout's x (its residual's gradient is dout itself)."""
+    return gns_dropout(dout, p, seed, step, base_index=base_index, out=out, stream=stream)
+
+
+# ------------------------------------------------------------------ routing
+
+def gns_moe_sort(experts, num_experts, stream=None):
+    """Sort the slots of experts ([tokens, topk], int32 or int64; ids outside
+    0 .. num_experts - 1 are slots without an expert) by expert."""
+    _typed(experts, "experts", {torch.int32: 0, torch.int64: 0})
+    if experts.dim() != 2 or experts.shape[1] < 1:
+        raise ValueError("experts must be [tokens, topk] with topk >= 1")
+    if not experts.is_contiguous():
+        raise ValueError("experts must be contiguous")
+    tokens, topk = experts.shape
+    n = tokens * topk
+    # One allocation: rows and slots first, the offsets behind them.
+    buf = _new((2 * n + num_experts + 1 if num_experts >= 0 else 0,), torch.int32, experts, stream)
+    rows, slots, offsets = buf[:n].view(tokens, topk), buf[n:2 * n], buf[2 * n:]
+    check(load().gns_moe_sort(experts.data_ptr(), experts.element_size(), tokens, topk, num_experts,
+                              offsets.data_ptr(), rows.data_ptr(), slots.data_ptr(), _on(experts, stream)),
+          "gns_moe_sort")
+    return MoeRoute(offsets, rows, slots)
+
+
+def _route_sizes(route):
+    for name, t in route._asdict().items():
+        _contiguous(t, torch.int32, f"route.{name}")
+    tokens, topk = route.rows.shape
+    return tokens, topk, route.offsets.shape[0] - 1
+
+
+def gns_moe_gather(x, route, stream=None):
+    """Rows of x ([tokens, cols]) at their sorted places, [tokens * topk, cols];
+    zero for slots without an expert."""
+    ldx = _matrix(x, "x")
+    tokens, topk, experts = _route_sizes(route)
+    if x.shape[0] != tokens:
+        raise ValueError("x must have one row per token of the route")
+    _same_device(x, route=route.rows)
+    y = _new((tokens * topk, x.shape[1]), x.dtype, x, stream)
+    check(load().gns_moe_gather(x.data_ptr(), ldx, tokens, topk, experts, x.shape[1], DTYPES[x.dtype],
+                                route.offsets.data_ptr(), route.rows.data_ptr(), y.data_ptr(), x.shape[1],
+                                _on(x, stream)), "gns_moe_gather")
+    return y
+
+
+def gns_moe_combine(y, weights, route, stream=None):
+    """out[t] = sum_j weights[t, j] * y[route.rows[t, j]] over the choices that
+    have an expert; weights fp32 [tokens, topk], or None for 1."""
+    ldy = _matrix(y, "y")
+    tokens, topk, experts = _route_sizes(route)
+    if y.shape[0] != tokens * topk:
+        raise ValueError("y must have one row per slot of the route")
+    if weights is not None:
+        _contiguous(weights, torch.float32, "weights")
+        if weights.shape != route.rows.shape:
+            raise ValueError("weights must be [tokens, topk]")
+    _same_device(y, route=route.rows, weights=weights)
+    out = _new((tokens, y.shape[1]), y.dtype, y, stream)
+    check(load().gns_moe_combine(y.data_ptr(), ldy, _ptr(weights), tokens, topk, experts, y.shape[1], DTYPES[y.dtype],
+                                 route.offsets.data_ptr(), route.rows.data_ptr(), out.data_ptr(), y.shape[1],
+                                 _on(y, stream)), "gns_moe_combine")
+    return out
+
+
+def gns_moe_gather_backward(dy, route, stream=None):
+    """The gradient of gns_moe_gather's x: each token's rows of dy summed."""
+    return gns_moe_combine(dy, None, route, stream=stream)
+
+
+def gns_moe_combine_backward(dout, y, weights, route, stream=None):
+    """The gradients (dy, dweights) of gns_moe_combine; y None: (dy, None)."""
+    lddo = _matrix(dout, "dout")
+    tokens, topk, experts = _route_sizes(route)
+    if dout.shape[0] != tokens:
+        raise ValueError("dout must have one row per token of the route")
+    _contiguous(weights, torch.float32, "weights")
+    if weights.shape != route.rows.shape:
+        raise ValueError("weights must be [tokens, topk]")
+    cols, ldy, dweights = dout.shape[1], 0, None
+    if y is not None:
+        ldy = _matrix(y, "y", {dout.dtype: 0})
+        if y.shape != (tokens * topk, cols):
+            raise ValueError("y must be [tokens * topk, cols]")
+        dweights = _new((tokens, topk), torch.float32, dout, stream)
+    _same_device(dout, y=y, route=route.rows, weights=weights)
+    dy = _new((tokens * topk, cols), dout.dtype, dout, stream)
+    check(load().gns_moe_combine_backward(dout.data_ptr(), lddo, _ptr(y), ldy, weights.data_ptr(), tokens, topk, experts,
+                                          cols, DTYPES[dout.dtype], route.offsets.data_ptr(), route.rows.data_ptr(),
+                                          dy.data_ptr(), cols, _ptr(dweights), _on(dout, stream)),
+          "gns_moe_combine_backward")
+    return dy, dweights
+
+
+# --------------------------------------------------------- 8-bit operands
+
+def _format(fmt):
+    if fmt not in FORMATS:
+        raise ValueError(f"fmt must be one of {sorted(FORMATS)}")
+    return FORMATS[fmt]
+
+
+def gns_fp8_quantize(x, fmt="e4m3", route=None, gather=False, rows=True, cols=True, stream=None):
+    """The 8-bit forms (Fp8Rows, Fp8Cols) of x, None for one not asked for. With
+    a route the blocks of the column form start at each expert's first row: x
+    is in sorted order, or, with gather, in token order and sorted on the way."""
+    ldx = _matrix(x, "x")
+    f = _format(fmt)
+    if not rows and not cols:
+        raise ValueError("rows or cols must be asked for")
+    n, c = x.shape
+    groups, topk, slots, offsets = 1, 1, None, None
+    if route is not None:
+        tokens, topk, groups = _route_sizes(route)
+        n = tokens * topk
+        if x.shape[0] != (tokens if gather else n):
+            raise ValueError("x must have one row per token (gather) or per slot of the route")
+        _same_device(x, route=route.rows)
+        slots, offsets = (route.slots if gather else None), route.offsets
+        blocks = (n + (BLOCK - 1) * min(n, groups)) // BLOCK
+    elif gather:
+        raise ValueError("gather needs a route")
+    else:
+        blocks = -(-n // BLOCK)
+    ld = _up(c, 16)
+    q_r = s_r = q_c = s_c = None
+    if rows:
+        q_r = _new((n, ld), _FP8[fmt], x, stream)
+        s_r = _new((-(-c // BLOCK), n), torch.float32, x, stream)
+    if cols:
+        q_c = _new((blocks * BLOCK, ld), _FP8[fmt], x, stream)
+        s_c = _new((blocks, _up(c, 4)), torch.float32, x, stream)
+    check(load().gns_fp8_quantize(x.data_ptr(), ldx, DTYPES[x.dtype], n, c, _ptr(slots), topk, _ptr(offsets), groups, f,
+                                  _ptr(q_r), ld, _ptr(s_r), n, _ptr(q_c), ld, _ptr(s_c), _up(c, 4), _on(x, stream)),
+          "gns_fp8_quantize")
+    return (Fp8Rows(q_r, s_r, c) if rows else None), (Fp8Cols(q_c, s_c, n, c) if cols else None)
+
+
+def gns_fp8_quantize_weight(w, fmt="e4m3", stream=None):
+    """The 8-bit form of weights w, [N, K] or [groups, N, K], in blocks of 128 x 128."""
+    _typed(w, "w")
+    f = _format(fmt)
+    if w.dim() not in (2, 3):
+        raise ValueError("w must be [N, K] or [groups, N, K]")
+    grouped = w.dim() == 3
+    if not grouped:
+        ldw, stride, (groups, (n, k)) = _matrix(w, "w"), 0, (1, w.shape)
+    else:
+        if not w.is_contiguous():
+            raise ValueError("grouped weights must be contiguous")
+        groups, n, k = w.shape
+        ldw, stride = k, n * k
+    ld = _up(k, 16)
+    q = _new((groups, n, ld), _FP8[fmt], w, stream)
+    scale = _new((groups, -(-n // BLOCK), -(-k // BLOCK)), torch.float32, w, stream)
+    check(load().gns_fp8_quantize_weight(w.data_ptr(), ldw, stride, DTYPES[w.dtype], groups, n, k, f, q.data_ptr(), ld,
+                                         scale.data_ptr(), _on(w, stream)), "gns_fp8_quantize_weight")
+    return Fp8Weight(q, scale, k, grouped)
+
+
+def _weight_args(w, route):
+    if not isinstance(w, Fp8Weight):
+        raise TypeError("w must be an Fp8Weight")
+    groups, n, _ = w.q.shape
+    if w.grouped != (route is not None):
+        raise ValueError("weights of several experts go with a route, a single matrix without one")
+    if route is not None and route.offsets.shape[0] != groups + 1:
+        raise ValueError("the route and the weights differ in the number of experts")
+    return groups, n, w.cols
+
+
+def _row_product(entry, a, w, route, contraction, out_cols, out_dtype, stream):
+    if not isinstance(a, Fp8Rows):
+        raise TypeError("the first operand must be an Fp8Rows")
+    groups, n, k = _weight_args(w, route)
+    rows = a.q.shape[0]
+    if a.cols != contraction:
+        raise ValueError(f"the operands' inner sizes differ: {a.cols} and {contraction}")
+    if route is not None and route.slots.shape[0] != rows:
+        raise ValueError("the operand must have one row per slot of the route")
+    if out_dtype not in DTYPES:
+        raise TypeError(f"out_dtype must be one of {sorted(str(d) for d in DTYPES)}")
+    _same_device(a.q, w=w.q, route=None if route is None else route.offsets)
+    y = _new((rows, out_cols), out_dtype, a.q, stream)
+    check(getattr(load(), entry)(a.q.data_ptr(), a.q.shape[1], a.scale.data_ptr(), a.scale.shape[1], _FP8_FORMAT[a.q.dtype],
+                                 rows, w.q.data_ptr(), w.q.shape[2], w.scale.data_ptr(), _FP8_FORMAT[w.q.dtype], groups,
+                                 n, k, None if route is None else route.offsets.data_ptr(), y.data_ptr(), out_cols,
+                                 DTYPES[out_dtype], _on(a.q, stream)), entry)
+    return y
+
+
+def gns_fp8_matmul(a, w, route=None, out_dtype=torch.bfloat16, stream=None):
+    """a w^T, [rows, N]: a Fp8Rows [rows, K] (in sorted order with a route), w Fp8Weight."""
+    return _row_product("gns_fp8_matmul", a, w, route, w.cols, w.q.shape[1], out_dtype, stream)
+
+
+def gns_fp8_matmul_dgrad(dy, w, route=None, out_dtype=torch.bfloat16, stream=None):
+    """The data gradient dy w, [rows, K]: dy Fp8Rows [rows, N]."""
+    return _row_product("gns_fp8_matmul_dgrad", dy, w, route, w.q.shape[1], w.cols, out_dtype, stream)
+
+
+def gns_fp8_matmul_wgrad(dy, x, route=None, out_dtype=torch.bfloat16, stream=None):
+    """The weight gradient dy^T x, [N, K] ([experts, N, K] with a route): dy and x Fp8Cols."""
+    if not isinstance(dy, Fp8Cols) or not isinstance(x, Fp8Cols):
+        raise TypeError("dy and x must be Fp8Cols")
+    if dy.rows != x.rows or dy.q.shape[0] != x.q.shape[0]:
+        raise ValueError("dy and x differ in their rows")
+    if out_dtype not in DTYPES:
+        raise TypeError(f"out_dtype must be one of {sorted(str(d) for d in DTYPES)}")
+    groups = 1
+    if route is not None:
+        tokens, topk, groups = _route_sizes(route)
+        blocks = (tokens * topk + (BLOCK - 1) * min(tokens * topk, groups)) // BLOCK
+        if tokens * topk != x.rows or x.scale.shape[0] != blocks:
+            raise ValueError("the operands were not cast with this route")
+    elif x.scale.shape[0] != -(-x.rows // BLOCK):
+        raise ValueError("operands cast with a route need it here too")
+    _same_device(x.q, dy=dy.q, route=None if route is None else route.offsets)
+    n, k = dy.cols, x.cols
+    dw = _new((n, k) if route is None else (groups, n, k), out_dtype, x.q, stream)
+    check(load().gns_fp8_matmul_wgrad(dy.q.data_ptr(), dy.q.shape[1], dy.scale.data_ptr(), dy.scale.shape[1],
+                                      _FP8_FORMAT[dy.q.dtype], x.q.data_ptr(), x.q.shape[1], x.scale.data_ptr(),
+                                      x.scale.shape[1], _FP8_FORMAT[x.q.dtype], x.rows, groups, n, k,
+                                      None if route is None else route.offsets.data_ptr(), dw.data_ptr(), k, n * k,
+                                      DTYPES[out_dtype], _on(x.q, stream)), "gns_fp8_matmul_wgrad")
+    return dw
+
+
+def gns_fp8_linear(x, w, route=None, out_dtype=torch.bfloat16, stream=None):
+    """x w^T as a serving program calls it: x ([tokens, K], bf16, fp16 or fp32) is
+    cast on the way (and, with a route, gathered to its sorted rows: the result
+    is [tokens * topk, N] in sorted order)."""
+    ldx = _matrix(x, "x")
+    groups, n, k = _weight_args(w, route)
+    if x.shape[1] != k:
+        raise ValueError(f"the operands' inner sizes differ: {x.shape[1]} and {k}")
+    if out_dtype not in DTYPES:
+        raise TypeError(f"out_dtype must be one of {sorted(str(d) for d in DTYPES)}")
+    rows, topk, slots, offsets = x.shape[0], 1, None, None
+    if route is not None:
+        tokens, topk, _ = _route_sizes(route)
+        if tokens != rows:
+            raise ValueError("x must have one row per token of the route")
+        rows, slots, offsets = tokens * topk, route.slots, route.offsets
+    _same_device(x, w=w.q, route=offsets)
+    y = _new((rows, n), out_dtype, x, stream)
+    check(load().gns_fp8_linear(x.data_ptr(), ldx, DTYPES[x.dtype], rows, _ptr(slots), topk, _ptr(offsets),
+                                w.q.data_ptr(), w.q.shape[2], w.scale.data_ptr(), _FP8_FORMAT[w.q.dtype], groups, n, k,
+                                y.data_ptr(), n, DTYPES[out_dtype], _on(x, stream)), "gns_fp8_linear")
+    return y

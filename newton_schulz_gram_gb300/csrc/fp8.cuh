@@ -1,0 +1,116 @@
+// Block-scaled 8-bit operands and their products: launchers (fp8_cast.cu,
+// fp8_gemm.cu, fp8_rows.cu).
+#pragma once
+
+#include <cstdint>
+#include <cuda.h>
+#include <cuda_runtime.h>
+
+#include "ptx.cuh"
+
+namespace gns {
+
+constexpr int kFp8Block = 128;
+
+// The cast of a rows x cols matrix; see gns_fp8_quantize. Either output may
+// be null. With offsets the token blocks of the column form are those of the
+// G groups of rows, and rows past offsets[G] are not written.
+struct CastJob {
+    const void* x;
+    long long ldx;
+    int dtype;
+    int rows, cols;
+    const int* slots;  // source row of row r is slots[r] / topk (null: r)
+    int topk;
+    const int* offsets;  // or null: one group of all rows
+    int G;
+    int fmt;
+    uint8_t* q_rows;
+    float* s_rows;
+    long long ld_rows, lds_rows;
+    uint8_t* q_cols;
+    float* s_cols;
+    long long ld_cols, lds_cols;
+};
+
+int launch_fp8_cast(const CastJob& job, int num_sms, cudaStream_t s);
+
+// The cast of G matrices of rows x cols in blocks of 128 x 128.
+struct CastWeightJob {
+    const void* w;
+    long long ldw, stride_w;
+    int dtype, G, rows, cols, fmt;
+    uint8_t* q;
+    long long ldq;  // matrices are rows * ldq apart
+    float* scale;   // [G][ceil(rows / 128)][ceil(cols / 128)]
+};
+
+int launch_fp8_cast_weight(const CastWeightJob& job, cudaStream_t s);
+
+// Largest number of 128-row token blocks that `rows` rows in G groups need.
+__host__ __device__ inline int fp8_max_blocks(long long rows, int G) {
+    const long long g = rows < G ? rows : G;
+    return static_cast<int>((rows + (kFp8Block - 1) * g) / kFp8Block);
+}
+
+__device__ __forceinline__ int blocks_of(int count) { return (count + kFp8Block - 1) / kFp8Block; }
+
+// One tcgen05 product per group g of rows (fp8_gemm.cu):
+//   forward / data gradient: D[r][n] over the group's rows r, contraction
+//     K; A is the row form, B the group's weights, [N][K] (b_mn = 0) or its
+//     stored transpose [K][N] (b_mn = 1);
+//   weight gradient (wgrad = 1): D[g][m][n], contraction the group's rows; A
+//     and B are column forms, [blocks * 128][M] and [blocks * 128][N].
+struct Fp8GemmJob {
+    CUtensorMap mapA, mapB;
+    int wgrad, b_mn;
+    int fmt_a, fmt_b;
+    int G;
+    const int* offsets;  // or null: one group of all rows
+    int rows;            // rows of all groups (capacity when offsets is given)
+    int M, N, K;         // M: wgrad only; K: not for wgrad
+    const float* sA;     // [k block or token block][row or m], row stride ldsA
+    long long ldsA;
+    const float* sB;     // weights: scale of (g, n block, k block) at g * sB_g + nb * sB_n + kb * sB_k
+    long long sB_g, sB_n, sB_k;  // wgrad: [token block][n], row stride sB_k
+    void* D;
+    long long ldd, strideD;
+    int out_dtype;
+    float* partial;      // split > 1: fp32 [split][rows][N]
+    int split;           // forward / data gradient of one group only
+    DevStatus st;
+};
+
+// Tile rows for a product of M rows (of all groups) by N columns: 128 (one
+// CTA) or 256 (a pair). B's tensor map has boxes of fp8_gemm_b_box rows.
+int fp8_gemm_tile_rows(int M, int N, int G, bool grouped, int num_sms);
+inline int fp8_gemm_b_box(int tile_rows, bool b_mn) { return b_mn || tile_rows == 256 ? 128 : 256; }
+
+int launch_fp8_gemm(const Fp8GemmJob& job, int tile_rows, int num_sms, cudaStream_t s);
+
+// The split of the contraction that fills the machine, 1 for none.
+int fp8_gemm_split(int rows, int N, int K, int num_sms);
+
+// The product of few rows (fp8_rows.cu): D[r][n] = x_r . w[g(r)][n], x cast on
+// the way as by launch_fp8_cast.
+struct Fp8RowsJob {
+    const void* x;
+    long long ldx;
+    int dtype;
+    const int* slots;
+    int topk;
+    const int* offsets;
+    int G, rows, N, K;
+    int fmt_w;
+    const uint8_t* w;
+    long long ldw, stride_w;
+    const float* sw;  // [G][ceil(N / 128)][ceil(K / 128)]
+    void* D;
+    long long ldd;
+    int out_dtype;
+};
+
+constexpr int kFp8FewRows = 8;
+int launch_fp8_rows(const Fp8RowsJob& job, cudaStream_t s);
+
+}  // namespace gns

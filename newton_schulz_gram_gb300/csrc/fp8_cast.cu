@@ -1,0 +1,297 @@
+// Casts to 8-bit floating point with a power-of-two scale for each block of
+// 128 values: along a row (the contraction of the forward and data-gradient
+// products), along a column (that of the weight gradient), or 128 x 128 of a
+// weight matrix.
+//
+//   s = the smallest power of two with amax / s <= 1.75 * 2^e  (448 = 1.75 * 2^8
+//       for e4m3, 57344 = 1.75 * 2^15 for e5m2), at least 2^-126,
+//   q = x / s rounded to nearest even.
+//
+// The scale is a power of two so that x / s and s q are exact: the only
+// rounding is the one to 8 bits, and a value's 8-bit form does not depend on
+// how the scale was applied. amax is taken over the finite values; NaN and
+// infinities become NaN and leave their block's other values alone.
+//
+// One block of threads holds a 128 x 128 tile in registers, so the row and the
+// column form (and the gather of a token's row to its places) come from one
+// read of x. Bound: HBM, 2 bytes read and 1 (2 for both forms) written per
+// value of 16 bits.
+#include <algorithm>
+
+#include "blockops.cuh"
+#include "fp8.cuh"
+#include "fp8_convert.cuh"
+#include "ptx.cuh"
+
+namespace gns {
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kPasses = 8;   // 16 rows each; a thread owns 8 columns of one row per pass
+constexpr int kWarps = kThreads / 32;
+
+enum CastMode { kRowForm = 1, kColForm = 2, kBothForms = 3, kBlockForm = 4 };
+
+template <bool E5M2>
+__device__ __forceinline__ uint2 cast8(const float (&v)[8], const float (&inv)[8]) {
+    uint2 o;
+    o.x = cast_pair<E5M2>(v[0] * inv[0], v[1] * inv[1]) | (cast_pair<E5M2>(v[2] * inv[2], v[3] * inv[3]) << 16);
+    o.y = cast_pair<E5M2>(v[4] * inv[4], v[5] * inv[5]) | (cast_pair<E5M2>(v[6] * inv[6], v[7] * inv[7]) << 16);
+    return o;
+}
+
+// One tile: rows r0 .. r0 + nrows - 1 of the matrix (source rows through
+// `src`), columns c0 .. c0 + 127.
+struct Tile {
+    int r0, nrows, c0;
+    long long qc_row;  // first row of the tile in the column form
+    int sc_row;        // its row of column scales
+};
+
+template <typename T, int MODE, bool E5M2>
+__device__ __forceinline__ void cast_tile(const Tile& tl, const T* x, long long ldx, const int* slots, int topk,
+                                          int cols, bool vec, uint8_t* q_rows, long long ld_rows, float* s_rows,
+                                          long long lds_rows, uint8_t* q_cols, long long ld_cols, float* s_cols,
+                                          long long lds_cols, float (&part)[kWarps][128], float (&inv_col)[128]) {
+    constexpr int kTop = E5M2 ? 15 : 8;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int cl = (threadIdx.x & 15) * 8;  // this thread's columns within the tile
+    const int rl = threadIdx.x >> 4;        // its row within a pass
+    const int c = tl.c0 + cl;
+    Pack<T, 8> raw[kPasses];
+#pragma unroll
+    for (int p = 0; p < kPasses; ++p) {
+        const int r = 16 * p + rl;
+        raw[p].clear();
+        if (r < tl.nrows && c < cols) {
+            const int row = tl.r0 + r;
+            const T* a = x + static_cast<long long>(slots ? slots[row] / topk : row) * ldx + c;
+            if (vec && c + 8 <= cols) {
+                raw[p].load(a);
+            } else {
+                T* e = reinterpret_cast<T*>(raw[p].p);
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                    if (c + i < cols) e[i] = a[i];
+            }
+        }
+    }
+    float cmax[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) cmax[i] = 0.0f;
+#pragma unroll
+    for (int p = 0; p < kPasses; ++p) {
+        float v[8];
+        raw[p].get(v);
+        float rmax = 0.0f;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const float a = finite_abs(v[i]);
+            if (MODE & kRowForm) rmax = fmaxf(rmax, a);
+            if (MODE & (kColForm | kBlockForm)) cmax[i] = fmaxf(cmax[i], a);
+        }
+        if (MODE & kRowForm) {
+#pragma unroll
+            for (int m = 8; m > 0; m >>= 1) rmax = fmaxf(rmax, __shfl_xor_sync(0xffffffffu, rmax, m));
+            const uint32_t e = scale_exponent(rmax, kTop);
+            const float inv = exp_inverse(e);
+            const int r = 16 * p + rl;
+            if (r < tl.nrows) {
+                if (c < ld_rows) {
+                    float w[8], iv[8];
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        w[i] = no_infinity(v[i]);
+                        iv[i] = inv;
+                    }
+                    *reinterpret_cast<uint2*>(q_rows + static_cast<long long>(tl.r0 + r) * ld_rows + c) =
+                        cast8<E5M2>(w, iv);
+                }
+                if (cl == 0) s_rows[static_cast<long long>(tl.c0 / 128) * lds_rows + tl.r0 + r] = exp_value(e);
+            }
+        }
+    }
+    if (MODE & (kColForm | kBlockForm)) {
+        if (MODE & kBlockForm) {  // one maximum for the tile
+            float m = cmax[0];
+#pragma unroll
+            for (int i = 1; i < 8; ++i) m = fmaxf(m, cmax[i]);
+#pragma unroll
+            for (int d = 16; d > 0; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
+            if (lane == 0) part[warp][0] = m;
+        } else {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) cmax[i] = fmaxf(cmax[i], __shfl_xor_sync(0xffffffffu, cmax[i], 16));
+            if (lane < 16) {
+#pragma unroll
+                for (int i = 0; i < 8; i += 4)
+                    *reinterpret_cast<float4*>(&part[warp][cl + i]) =
+                        make_float4(cmax[i], cmax[i + 1], cmax[i + 2], cmax[i + 3]);
+            }
+        }
+        __syncthreads();
+        if (MODE & kColForm) {
+            if (threadIdx.x < 128) {
+                float m = part[0][threadIdx.x];
+#pragma unroll
+                for (int w = 1; w < kWarps; ++w) m = fmaxf(m, part[w][threadIdx.x]);
+                const uint32_t e = scale_exponent(m, kTop);
+                inv_col[threadIdx.x] = exp_inverse(e);
+                if (tl.c0 + static_cast<int>(threadIdx.x) < cols)
+                    s_cols[static_cast<long long>(tl.sc_row) * lds_cols + tl.c0 + threadIdx.x] = exp_value(e);
+            }
+            __syncthreads();
+        }
+        float iv[8];
+        if (MODE & kBlockForm) {
+            float m = part[0][0];
+#pragma unroll
+            for (int w = 1; w < kWarps; ++w) m = fmaxf(m, part[w][0]);
+            const uint32_t e = scale_exponent(m, kTop);
+            if (threadIdx.x == 0) *s_cols = exp_value(e);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) iv[i] = exp_inverse(e);
+        } else {
+#pragma unroll
+            for (int i = 0; i < 8; i += 4) {
+                const float4 f = *reinterpret_cast<const float4*>(&inv_col[cl + i]);
+                iv[i] = f.x, iv[i + 1] = f.y, iv[i + 2] = f.z, iv[i + 3] = f.w;
+            }
+        }
+#pragma unroll
+        for (int p = 0; p < kPasses; ++p) {
+            const int r = 16 * p + rl;
+            // The column form is zero to the end of its last block of 128
+            // rows (the rows past nrows were loaded as zero).
+            if (c < ld_cols && (!(MODE & kBlockForm) || r < tl.nrows)) {
+                float v[8];
+                raw[p].get(v);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) v[i] = no_infinity(v[i]);
+                *reinterpret_cast<uint2*>(q_cols + (tl.qc_row + r) * ld_cols + c) = cast8<E5M2>(v, iv);
+            }
+        }
+        __syncthreads();  // part and inv_col are free for the next tile
+    }
+}
+
+// blockIdx.y: token block; blockIdx.x: the first of the `span` column blocks.
+template <typename T, int MODE, bool E5M2>
+__global__ void __launch_bounds__(kThreads) fp8_cast_kernel(CastJob j, bool vec, int span) {
+    __shared__ float part[kWarps][128];
+    __shared__ __align__(16) float inv_col[128];
+    __shared__ int found[3];
+    grid_dependency_wait();
+    grid_launch_dependents();
+    Tile tl;
+    if (j.offsets) {
+        // The group that owns this token block: thread t sums the blocks of
+        // groups t * per .. t * per + per - 1.
+        const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+        const int per = (j.G + kThreads - 1) / kThreads;
+        const int g0 = threadIdx.x * per;
+        int mine = 0;
+        if (threadIdx.x == 0) found[0] = -1;
+        for (int i = 0; i < per && g0 + i < j.G; ++i) mine += blocks_of(j.offsets[g0 + i + 1] - j.offsets[g0 + i]);
+        int scan = mine;
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) {
+            const int v = __shfl_up_sync(0xffffffffu, scan, d);
+            if (lane >= d) scan += v;
+        }
+        if (lane == 31) part[0][warp] = __int_as_float(scan);
+        __syncthreads();
+        int start = scan - mine;
+        for (int w = 0; w < warp; ++w) start += __float_as_int(part[0][w]);
+        const int b = blockIdx.y;
+        if (b >= start && b < start + mine) {
+            for (int i = 0; i < per && g0 + i < j.G; ++i) {
+                const int beg = j.offsets[g0 + i], n = j.offsets[g0 + i + 1] - beg;
+                const int nb = blocks_of(n);
+                if (b < start + nb) {
+                    found[1] = beg + (b - start) * kFp8Block;
+                    found[2] = min(n - (b - start) * kFp8Block, kFp8Block);
+                    found[0] = 1;
+                    break;
+                }
+                start += nb;
+            }
+        }
+        __syncthreads();
+        if (found[0] < 0) return;  // past the last group's blocks
+        tl.r0 = found[1];
+        tl.nrows = found[2];
+    } else {
+        tl.r0 = blockIdx.y * kFp8Block;
+        tl.nrows = min(j.rows - tl.r0, kFp8Block);
+    }
+    tl.qc_row = static_cast<long long>(blockIdx.y) * kFp8Block;
+    tl.sc_row = blockIdx.y;
+    const int nblk = (j.cols + kFp8Block - 1) / kFp8Block;
+    for (int cb = blockIdx.x * span; cb < min(nblk, static_cast<int>(blockIdx.x + 1) * span); ++cb) {
+        tl.c0 = cb * kFp8Block;
+        cast_tile<T, MODE, E5M2>(tl, static_cast<const T*>(j.x), j.ldx, j.slots, j.topk, j.cols, vec, j.q_rows, j.ld_rows,
+                                 j.s_rows, j.lds_rows, j.q_cols, j.ld_cols, j.s_cols, j.lds_cols, part, inv_col);
+    }
+}
+
+template <typename T, bool E5M2>
+__global__ void __launch_bounds__(kThreads) fp8_cast_weight_kernel(CastWeightJob j, bool vec) {
+    __shared__ float part[kWarps][128];
+    __shared__ __align__(16) float inv_col[128];
+    grid_dependency_wait();
+    grid_launch_dependents();
+    const int nb = (j.rows + kFp8Block - 1) / kFp8Block, kb = (j.cols + kFp8Block - 1) / kFp8Block;
+    for (int g = blockIdx.z; g < j.G; g += gridDim.z) {
+        Tile tl;
+        tl.r0 = blockIdx.y * kFp8Block;
+        tl.nrows = min(j.rows - tl.r0, kFp8Block);
+        tl.c0 = blockIdx.x * kFp8Block;
+        tl.qc_row = static_cast<long long>(g) * j.rows + tl.r0;
+        tl.sc_row = 0;
+        float* scale = j.scale + (static_cast<long long>(g) * nb + blockIdx.y) * kb + blockIdx.x;
+        cast_tile<T, kBlockForm, E5M2>(tl, static_cast<const T*>(j.w) + g * j.stride_w, j.ldw, nullptr, 1, j.cols, vec,
+                                       nullptr, 0, nullptr, 0, j.q, j.ldq, scale, 0, part, inv_col);
+    }
+}
+
+template <typename T, bool E5M2>
+int cast_typed(const CastJob& j, int num_sms, cudaStream_t s) {
+    const bool vec = (reinterpret_cast<uintptr_t>(j.x) & 15) == 0 && j.ldx * static_cast<int>(sizeof(T)) % 16 == 0;
+    const int nblk = (j.cols + kFp8Block - 1) / kFp8Block;
+    const int tblk = j.offsets ? fp8_max_blocks(j.rows, j.G) : (j.rows + kFp8Block - 1) / kFp8Block;
+    // With groups a block looks its token block up first, so it takes several
+    // column blocks then, as long as that leaves about eight blocks per SM.
+    int span = 1;
+    if (j.offsets)
+        while (span < 8 && static_cast<long long>(tblk) * ((nblk + 2 * span - 1) / (2 * span)) >= 8LL * num_sms) span *= 2;
+    const dim3 grid((nblk + span - 1) / span, tblk);
+    auto run = [&](auto k) { return static_cast<int>(launch_after(k, grid, dim3(kThreads), 0, s, j, vec, span)); };
+    if (j.q_rows && j.q_cols) return run(fp8_cast_kernel<T, kBothForms, E5M2>);
+    if (j.q_rows) return run(fp8_cast_kernel<T, kRowForm, E5M2>);
+    return run(fp8_cast_kernel<T, kColForm, E5M2>);
+}
+
+}  // namespace
+
+int launch_fp8_cast(const CastJob& j, int num_sms, cudaStream_t s) {
+    return by_dtype(j.dtype, [&](auto t) {
+        using T = decltype(t);
+        return j.fmt == GNS_E5M2 ? cast_typed<T, true>(j, num_sms, s) : cast_typed<T, false>(j, num_sms, s);
+    });
+}
+
+int launch_fp8_cast_weight(const CastWeightJob& j, cudaStream_t s) {
+    return by_dtype(j.dtype, [&](auto t) {
+        using T = decltype(t);
+        const bool vec = (reinterpret_cast<uintptr_t>(j.w) & 15) == 0 && j.ldw * static_cast<int>(sizeof(T)) % 16 == 0 &&
+                         j.stride_w * static_cast<int>(sizeof(T)) % 16 == 0;
+        const dim3 grid((j.cols + kFp8Block - 1) / kFp8Block, (j.rows + kFp8Block - 1) / kFp8Block,
+                        std::min(j.G, 65535));
+        return static_cast<int>(j.fmt == GNS_E5M2
+                                    ? launch_after(fp8_cast_weight_kernel<T, true>, grid, dim3(kThreads), 0, s, j, vec)
+                                    : launch_after(fp8_cast_weight_kernel<T, false>, grid, dim3(kThreads), 0, s, j, vec));
+    });
+}
+
+}  // namespace gns
