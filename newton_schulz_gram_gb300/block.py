@@ -54,51 +54,64 @@ class Fp8Weight(NamedTuple):
     grouped: bool  # made from a [groups, N, K] tensor
 
 
+# The helpers below run on every call of operators that take a few microseconds
+# on the GPU, so each tests what is usual in one expression and looks for the
+# reason of a refusal only when that fails.
+
+_raw_stream = torch._C._cuda_getCurrentRawStream  # the current stream's handle, without a Stream object around it
+_empty = torch.empty
+
+
 def _ptr(t):
     return None if t is None else t.data_ptr()
 
 
 def _on(t, stream):
-    return torch.cuda.current_stream(t.device).cuda_stream if stream is None else stream.cuda_stream
+    return _raw_stream(t.get_device()) if stream is None else stream.cuda_stream
 
 
 def _new(shape, dtype, like, stream):
     if stream is None:
-        return torch.empty(shape, dtype=dtype, device=like.device)
+        return _empty(shape, dtype=dtype, device=like.device)
     with torch.cuda.stream(stream):
-        return torch.empty(shape, dtype=dtype, device=like.device)
+        return _empty(shape, dtype=dtype, device=like.device)
 
 
 def _typed(t, name, dtypes=DTYPES):
+    if isinstance(t, torch.Tensor) and t.dtype in dtypes and t.is_cuda:
+        return
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     if t.dtype not in dtypes:
         raise TypeError(f"{name} must be one of {sorted(str(d) for d in dtypes)}, got {t.dtype}")
-    if not t.is_cuda:
-        raise ValueError(f"{name} must be a CUDA tensor")
+    raise ValueError(f"{name} must be a CUDA tensor")
 
 
-def _same_device(like, **tensors):
-    for name, t in tensors.items():
-        if t is not None and t.device != like.device:
-            raise ValueError(f"{name} is on {t.device}, not on {like.device}")
+def _same_device(like, name, t):
+    if t is not None and t.get_device() != like.get_device():
+        raise ValueError(f"{name} is on {t.device}, not on {like.device}")
 
 
 def _matrix(t, name, dtypes=DTYPES):
-    """A 2D tensor with unit column stride; returns its row stride."""
+    """A 2D tensor with unit column stride; returns (rows, columns, row stride)."""
     _typed(t, name, dtypes)
     if t.dim() != 2:
         raise ValueError(f"{name} must be 2D")
-    if t.shape[1] > 1 and t.stride(1) != 1:
+    rows, cols = t.shape
+    if t.is_contiguous():
+        return rows, cols, cols or 1
+    ld, inner = t.stride()
+    if cols > 1 and inner != 1:
         raise ValueError(f"{name} must have contiguous rows")
-    ld = t.stride(0) if t.shape[0] > 1 else max(t.shape[1], 1)
-    if ld < t.shape[1]:
+    if rows <= 1:
+        ld = cols or 1
+    if ld < cols:
         raise ValueError(f"{name} must have rows that do not overlap")
-    return ld
+    return rows, cols, ld
 
 
 def _contiguous(t, dtype, name):
-    _typed(t, name, {dtype: 0})
+    _typed(t, name, {dtype})
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
 
@@ -110,12 +123,12 @@ def _up(v, a):
 # ------------------------------------------------------------------ dropout
 
 def _rows_of(t, name):
-    """(rows, cols, row stride) of a contiguous tensor or a 2D one with contiguous rows."""
+    """(rows, cols, row stride) of a contiguous tensor (one row) or a 2D one with contiguous rows."""
     _typed(t, name)
     if t.is_contiguous():
-        cols = t.shape[-1] if t.dim() else 1
-        return (t.numel() // cols if cols else 0), cols, cols
-    return t.shape[0] if t.dim() == 2 else 0, t.shape[-1], _matrix(t, name)
+        n = t.numel()
+        return 1, n, n
+    return _matrix(t, name)
 
 
 def gns_dropout(x, p, seed, step, residual=None, base_index=0, out=None, stream=None):
@@ -124,16 +137,23 @@ def gns_dropout(x, p, seed, step, residual=None, base_index=0, out=None, stream=
     rounded to a multiple of 2^-16. x: bf16, fp16 or fp32, contiguous or 2D
     with contiguous rows. out may be x or residual."""
     rows, cols, ldx = _rows_of(x, "x")
-    ldr = 0
-    for name, t in (("residual", residual), ("out", out)):
-        if t is not None and (t.dtype != x.dtype or t.shape != x.shape):
-            raise ValueError(f"{name} must have the type and shape of x")
-    if residual is not None:
-        ldr = _rows_of(residual, "residual")[2]
+    one_row = rows == 1
     if out is None:
         out = _new(x.shape, x.dtype, x, stream)
-    ldy = _rows_of(out, "out")[2]
-    _same_device(x, residual=residual, out=out)
+    others = [out] if residual is None else [out, residual]
+    for t in others:
+        if t.dtype != x.dtype or t.shape != x.shape:
+            raise ValueError("residual and out must have the type and shape of x")
+        _same_device(x, "residual or out", t)
+        one_row = one_row and t.is_contiguous()
+    if one_row:
+        ldr = ldy = ldx
+    else:  # some tensor has gaps between its rows: all are walked row by row
+        if x.dim() != 2:
+            raise ValueError("tensors that are not contiguous must be 2D")
+        rows, cols, ldx = _matrix(x, "x")
+        ldy = _matrix(out, "out")[2]
+        ldr = 0 if residual is None else _matrix(residual, "residual")[2]
     check(load().gns_dropout(x.data_ptr(), _ptr(residual), out.data_ptr(), rows, cols, ldx, ldr, ldy, DTYPES[x.dtype],
                              p, seed, step, base_index, _on(x, stream)), "gns_dropout")
     return out
@@ -155,54 +175,64 @@ def gns_moe_sort(experts, num_experts, stream=None):
     if not experts.is_contiguous():
         raise ValueError("experts must be contiguous")
     tokens, topk = experts.shape
-    n = tokens * topk
-    # One allocation: rows and slots first, the offsets behind them.
-    buf = _new((2 * n + num_experts + 1 if num_experts >= 0 else 0,), torch.int32, experts, stream)
-    rows, slots, offsets = buf[:n].view(tokens, topk), buf[n:2 * n], buf[2 * n:]
+    if num_experts < 1:
+        raise ValueError("num_experts must be at least 1")
+    rows = _new((tokens, topk), torch.int32, experts, stream)
+    slots = _new((tokens * topk,), torch.int32, experts, stream)
+    offsets = _new((num_experts + 1,), torch.int32, experts, stream)
     check(load().gns_moe_sort(experts.data_ptr(), experts.element_size(), tokens, topk, num_experts,
                               offsets.data_ptr(), rows.data_ptr(), slots.data_ptr(), _on(experts, stream)),
           "gns_moe_sort")
     return MoeRoute(offsets, rows, slots)
 
 
-def _route_sizes(route):
-    for name, t in route._asdict().items():
-        _contiguous(t, torch.int32, f"route.{name}")
-    tokens, topk = route.rows.shape
-    return tokens, topk, route.offsets.shape[0] - 1
+def _route_sizes(route, like):
+    offsets, rows, slots = route
+    i32 = torch.int32
+    if not (offsets.dtype is i32 and rows.dtype is i32 and slots.dtype is i32 and offsets.is_contiguous()
+            and rows.is_contiguous() and slots.is_contiguous() and rows.dim() == 2):
+        for name, t in route._asdict().items():
+            _contiguous(t, i32, f"route.{name}")
+        raise ValueError("route.rows must be [tokens, topk]")
+    _same_device(like, "the route", rows)
+    tokens, topk = rows.shape
+    return tokens, topk, offsets.shape[0] - 1
 
 
 def gns_moe_gather(x, route, stream=None):
     """Rows of x ([tokens, cols]) at their sorted places, [tokens * topk, cols];
     zero for slots without an expert."""
-    ldx = _matrix(x, "x")
-    tokens, topk, experts = _route_sizes(route)
-    if x.shape[0] != tokens:
+    n, cols, ldx = _matrix(x, "x")
+    tokens, topk, experts = _route_sizes(route, x)
+    if n != tokens:
         raise ValueError("x must have one row per token of the route")
-    _same_device(x, route=route.rows)
-    y = _new((tokens * topk, x.shape[1]), x.dtype, x, stream)
-    check(load().gns_moe_gather(x.data_ptr(), ldx, tokens, topk, experts, x.shape[1], DTYPES[x.dtype],
-                                route.offsets.data_ptr(), route.rows.data_ptr(), y.data_ptr(), x.shape[1],
-                                _on(x, stream)), "gns_moe_gather")
+    y = _new((tokens * topk, cols), x.dtype, x, stream)
+    check(load().gns_moe_gather(x.data_ptr(), ldx, tokens, topk, experts, cols, DTYPES[x.dtype],
+                                route.offsets.data_ptr(), route.rows.data_ptr(), y.data_ptr(), cols, _on(x, stream)),
+          "gns_moe_gather")
     return y
+
+
+def _route_weights(weights, route, like):
+    _contiguous(weights, torch.float32, "weights")
+    if weights.shape != route.rows.shape:
+        raise ValueError("weights must be [tokens, topk]")
+    _same_device(like, "weights", weights)
 
 
 def gns_moe_combine(y, weights, route, stream=None):
     """out[t] = sum_j weights[t, j] * y[route.rows[t, j]] over the choices that
     have an expert; weights fp32 [tokens, topk], or None for 1."""
-    ldy = _matrix(y, "y")
-    tokens, topk, experts = _route_sizes(route)
-    if y.shape[0] != tokens * topk:
+    n, cols, ldy = _matrix(y, "y")
+    tokens, topk, experts = _route_sizes(route, y)
+    if n != tokens * topk:
         raise ValueError("y must have one row per slot of the route")
     if weights is not None:
-        _contiguous(weights, torch.float32, "weights")
-        if weights.shape != route.rows.shape:
-            raise ValueError("weights must be [tokens, topk]")
-    _same_device(y, route=route.rows, weights=weights)
-    out = _new((tokens, y.shape[1]), y.dtype, y, stream)
-    check(load().gns_moe_combine(y.data_ptr(), ldy, _ptr(weights), tokens, topk, experts, y.shape[1], DTYPES[y.dtype],
-                                 route.offsets.data_ptr(), route.rows.data_ptr(), out.data_ptr(), y.shape[1],
-                                 _on(y, stream)), "gns_moe_combine")
+        _route_weights(weights, route, y)
+    out = _new((tokens, cols), y.dtype, y, stream)
+    check(load().gns_moe_combine(y.data_ptr(), ldy, _ptr(weights), tokens, topk, experts, cols, DTYPES[y.dtype],
+                                 route.offsets.data_ptr(), route.rows.data_ptr(), out.data_ptr(), cols, _on(y, stream)),
+          "gns_moe_combine")
     return out
 
 
@@ -213,20 +243,18 @@ def gns_moe_gather_backward(dy, route, stream=None):
 
 def gns_moe_combine_backward(dout, y, weights, route, stream=None):
     """The gradients (dy, dweights) of gns_moe_combine; y None: (dy, None)."""
-    lddo = _matrix(dout, "dout")
-    tokens, topk, experts = _route_sizes(route)
-    if dout.shape[0] != tokens:
+    n, cols, lddo = _matrix(dout, "dout")
+    tokens, topk, experts = _route_sizes(route, dout)
+    if n != tokens:
         raise ValueError("dout must have one row per token of the route")
-    _contiguous(weights, torch.float32, "weights")
-    if weights.shape != route.rows.shape:
-        raise ValueError("weights must be [tokens, topk]")
-    cols, ldy, dweights = dout.shape[1], 0, None
+    _route_weights(weights, route, dout)
+    ldy, dweights = 0, None
     if y is not None:
-        ldy = _matrix(y, "y", {dout.dtype: 0})
-        if y.shape != (tokens * topk, cols):
+        ny, ncols, ldy = _matrix(y, "y", {dout.dtype})
+        if ny != tokens * topk or ncols != cols:
             raise ValueError("y must be [tokens * topk, cols]")
+        _same_device(dout, "y", y)
         dweights = _new((tokens, topk), torch.float32, dout, stream)
-    _same_device(dout, y=y, route=route.rows, weights=weights)
     dy = _new((tokens * topk, cols), dout.dtype, dout, stream)
     check(load().gns_moe_combine_backward(dout.data_ptr(), lddo, _ptr(y), ldy, weights.data_ptr(), tokens, topk, experts,
                                           cols, DTYPES[dout.dtype], route.offsets.data_ptr(), route.rows.data_ptr(),
@@ -247,18 +275,16 @@ def gns_fp8_quantize(x, fmt="e4m3", route=None, gather=False, rows=True, cols=Tr
     """The 8-bit forms (Fp8Rows, Fp8Cols) of x, None for one not asked for. With
     a route the blocks of the column form start at each expert's first row: x
     is in sorted order, or, with gather, in token order and sorted on the way."""
-    ldx = _matrix(x, "x")
+    n, c, ldx = _matrix(x, "x")
     f = _format(fmt)
     if not rows and not cols:
         raise ValueError("rows or cols must be asked for")
-    n, c = x.shape
     groups, topk, slots, offsets = 1, 1, None, None
     if route is not None:
-        tokens, topk, groups = _route_sizes(route)
-        n = tokens * topk
-        if x.shape[0] != (tokens if gather else n):
+        tokens, topk, groups = _route_sizes(route, x)
+        if n != (tokens if gather else tokens * topk):
             raise ValueError("x must have one row per token (gather) or per slot of the route")
-        _same_device(x, route=route.rows)
+        n = tokens * topk
         slots, offsets = (route.slots if gather else None), route.offsets
         blocks = (n + (BLOCK - 1) * min(n, groups)) // BLOCK
     elif gather:
@@ -287,7 +313,7 @@ def gns_fp8_quantize_weight(w, fmt="e4m3", stream=None):
         raise ValueError("w must be [N, K] or [groups, N, K]")
     grouped = w.dim() == 3
     if not grouped:
-        ldw, stride, (groups, (n, k)) = _matrix(w, "w"), 0, (1, w.shape)
+        (n, k, ldw), stride, groups = _matrix(w, "w"), 0, 1
     else:
         if not w.is_contiguous():
             raise ValueError("grouped weights must be contiguous")
@@ -323,7 +349,8 @@ def _row_product(entry, a, w, route, contraction, out_cols, out_dtype, stream):
         raise ValueError("the operand must have one row per slot of the route")
     if out_dtype not in DTYPES:
         raise TypeError(f"out_dtype must be one of {sorted(str(d) for d in DTYPES)}")
-    _same_device(a.q, w=w.q, route=None if route is None else route.offsets)
+    _same_device(a.q, "w", w.q)
+    _same_device(a.q, "the route", None if route is None else route.offsets)
     y = _new((rows, out_cols), out_dtype, a.q, stream)
     check(getattr(load(), entry)(a.q.data_ptr(), a.q.shape[1], a.scale.data_ptr(), a.scale.shape[1], _FP8_FORMAT[a.q.dtype],
                                  rows, w.q.data_ptr(), w.q.shape[2], w.scale.data_ptr(), _FP8_FORMAT[w.q.dtype], groups,
@@ -352,13 +379,13 @@ def gns_fp8_matmul_wgrad(dy, x, route=None, out_dtype=torch.bfloat16, stream=Non
         raise TypeError(f"out_dtype must be one of {sorted(str(d) for d in DTYPES)}")
     groups = 1
     if route is not None:
-        tokens, topk, groups = _route_sizes(route)
+        tokens, topk, groups = _route_sizes(route, x.q)
         blocks = (tokens * topk + (BLOCK - 1) * min(tokens * topk, groups)) // BLOCK
         if tokens * topk != x.rows or x.scale.shape[0] != blocks:
             raise ValueError("the operands were not cast with this route")
     elif x.scale.shape[0] != -(-x.rows // BLOCK):
         raise ValueError("operands cast with a route need it here too")
-    _same_device(x.q, dy=dy.q, route=None if route is None else route.offsets)
+    _same_device(x.q, "dy", dy.q)
     n, k = dy.cols, x.cols
     dw = _new((n, k) if route is None else (groups, n, k), out_dtype, x.q, stream)
     check(load().gns_fp8_matmul_wgrad(dy.q.data_ptr(), dy.q.shape[1], dy.scale.data_ptr(), dy.scale.shape[1],
@@ -373,19 +400,19 @@ def gns_fp8_linear(x, w, route=None, out_dtype=torch.bfloat16, stream=None):
     """x w^T as a serving program calls it: x ([tokens, K], bf16, fp16 or fp32) is
     cast on the way (and, with a route, gathered to its sorted rows: the result
     is [tokens * topk, N] in sorted order)."""
-    ldx = _matrix(x, "x")
+    rows, inner, ldx = _matrix(x, "x")
     groups, n, k = _weight_args(w, route)
-    if x.shape[1] != k:
-        raise ValueError(f"the operands' inner sizes differ: {x.shape[1]} and {k}")
+    if inner != k:
+        raise ValueError(f"the operands' inner sizes differ: {inner} and {k}")
     if out_dtype not in DTYPES:
         raise TypeError(f"out_dtype must be one of {sorted(str(d) for d in DTYPES)}")
-    rows, topk, slots, offsets = x.shape[0], 1, None, None
+    topk, slots, offsets = 1, None, None
     if route is not None:
-        tokens, topk, _ = _route_sizes(route)
+        tokens, topk, _ = _route_sizes(route, x)
         if tokens != rows:
             raise ValueError("x must have one row per token of the route")
         rows, slots, offsets = tokens * topk, route.slots, route.offsets
-    _same_device(x, w=w.q, route=offsets)
+    _same_device(x, "w", w.q)
     y = _new((rows, n), out_dtype, x, stream)
     check(load().gns_fp8_linear(x.data_ptr(), ldx, DTYPES[x.dtype], rows, _ptr(slots), topk, _ptr(offsets),
                                 w.q.data_ptr(), w.q.shape[2], w.scale.data_ptr(), _FP8_FORMAT[w.q.dtype], groups, n, k,

@@ -227,9 +227,10 @@ int gns_fp8_quantize(const void* x, int64_t ldx, int dtype, int rows, int cols, 
     if (rows < 0 || rows > kMaxRows || cols < 1) return invalid("rows must be in 0..8388480 and cols >= 1");
     if (bad_dtype(dtype)) return invalid("unknown dtype");
     if (bad_format(format)) return invalid("unknown 8-bit format");
-    if (!q_rows && !q_cols) return invalid("null pointer");
     if (slots && topk < 1) return invalid("topk >= 1 required");
     if (offsets && (groups < 1 || groups > kMaxExperts)) return invalid("groups must be in 1..GNS_MAX_EXPERTS");
+    if (rows == 0) return GNS_OK;
+    if (!q_rows && !q_cols) return invalid("null pointer");
     if (q_rows) {
         RET(check_q(q_rows, cols, ld_rows));
         if (!scale_rows) return invalid("null pointer");
@@ -241,7 +242,6 @@ int gns_fp8_quantize(const void* x, int64_t ldx, int dtype, int rows, int cols, 
         if (misaligned(scale_cols, 16) || ld_scale_cols % 4 || ld_scale_cols < cols)
             return invalid("column scales need 16-byte aligned rows that cover the columns");
     }
-    if (rows == 0) return GNS_OK;
     if (!x) return invalid("null pointer");
     if (ldx < cols) return invalid("a row stride must cover the columns");
     DeviceState* st = nullptr;
