@@ -81,12 +81,10 @@ struct Fp8GemmJob {
     DevStatus st;
 };
 
-// Tile rows for a product of M rows (of all groups) by N columns: 128 (one
-// CTA) or 256 (a pair). B's tensor map has boxes of fp8_gemm_b_box rows.
-int fp8_gemm_tile_rows(int M, int N, int G, bool grouped, int num_sms);
-inline int fp8_gemm_b_box(int tile_rows, bool b_mn) { return b_mn || tile_rows == 256 ? 128 : 256; }
+// Rows of the boxes of B's tensor map.
+inline int fp8_gemm_b_box(bool b_mn) { return b_mn ? 128 : 256; }
 
-int launch_fp8_gemm(const Fp8GemmJob& job, int tile_rows, int num_sms, cudaStream_t s);
+int launch_fp8_gemm(const Fp8GemmJob& job, int num_sms, cudaStream_t s);
 
 // The split of the contraction that fills the machine, 1 for none.
 int fp8_gemm_split(int rows, int N, int K, int num_sms);

@@ -6,23 +6,25 @@
 //
 // with blocks of 128 along the contraction. The tensor core sums one block's
 // 128 products in fp32 (kind::f8f6f4, TMEM); the epilogue warps then add
-// sA sB times that partial sum to fp32 accumulators in registers. So a block
-// costs one read of its 128 x 256 TMEM accumulator besides its MMAs: at full
-// MMA rate a block takes about 512 cycles per SM, the TMEM reads 256 and the
-// scaled adds 128 (packed pairs; 256 when both scales vary along the tile), so
-// the tensor core stays the bound as long as the two overlap.
+// sA sB times that partial sum to fp32 accumulators in registers. A block is
+// 512 cycles of MMA for a 128 x 256 tile; the epilogue's share of it (TMEM
+// reads 256 cycles, scaled adds 256 per scheduler) has to run beside the next
+// block's MMAs, which write the other half of TMEM.
 //
-// One CTA (CG = 1, 128 x 256 tiles) or a pair (CG = 2, 256 x 256 tiles, paired
-// MMAs; each CTA stages 128 rows of each operand, so a k block moves 32 KB per
-// SM instead of 48 KB from L2) per SM (pair) walks the tiles with a static
-// stride. Warp roles:
+// One CTA per SM walks 128 x 256 tiles with a static stride. Warp roles:
 //   warp 0     TMA producer of 128-byte-wide k blocks (128-byte swizzle)
 //   warp 1     TMEM owner, MMA issuer; k block i goes to accumulator buffer
 //              i & 1 (256 columns each)
-//   warps 4-11 epilogue: lane quarter warp & 3, column half of the tile
-//              (warp - 4) >> 2, 128 accumulators per thread. The first
+//   warp 2     scale producer: cp.async of a k block's row and column scales
+//              into a ring of shared-memory slots, several blocks ahead
+//   warps 4-11 epilogue: lane quarter warp & 3, columns 128 ((warp - 4) >> 2)
+//              to + 127 of the tile, 128 accumulators per thread. The first
 //              warpgroup gives registers up for them: 40 + 2 x 232 per lane of
 //              the 3 x 168 the block is launched with.
+// Measured and left: CTA pairs (256 x 256 tiles, paired MMAs) load a third less
+// from L2, but their accumulator hand-shake crosses CTAs once per block
+// (8192 x 14336 x 4096 forward: 954 us against 551); sixteen epilogue warps of
+// 64 columns hide no more latency than eight (598 us).
 // Operands whose contraction runs along the stored rows (the weights of the
 // data gradient, both operands of the weight gradient) are read MN-major
 // through the shared-memory descriptor; nothing is transposed in memory.
@@ -41,50 +43,47 @@ constexpr int BN = 256;
 constexpr int BK = kFp8Block;
 constexpr int kEpiWarps = 8;
 constexpr int kEpiWarp0 = 4;
+constexpr int kCols = 128;  // columns of an epilogue warp
 constexpr int kThreads = 32 * (kEpiWarp0 + kEpiWarps);
 constexpr int kBand = 16;  // tile rows walked together (their A stays in L2 while the columns pass)
 constexpr uint32_t kTmemCols = 2 * BN;
 constexpr uint32_t A_BYTES = BM * BK;
+constexpr uint32_t B_BYTES = BN * BK;
 constexpr uint32_t kBoxBytes = 128 * 128;
+constexpr int STAGES = 3;
+constexpr int kStageRow = 128;                    // bytes of a row staged for the output stores
+constexpr int kStageBytes = 32 * kStageRow;        // per epilogue warp
 
-template <int CG>
-struct Cfg {
-    static constexpr int STAGES = CG == 1 ? 4 : 6;
-    static constexpr uint32_t B_BYTES = BN / CG * BK;
-    static constexpr int TM = BM * CG;
-};
+// A scale slot holds kSlotBlocks k blocks' scales, for each the 128 row scales
+// and then its two column-half scales, or 256 column scales (weight gradient).
+// One barrier wait per k block costs the epilogue about 150 cycles of the 800
+// it has; a slot of four shares it.
+constexpr int kScaleSlots = 3;
+constexpr int kSlotBlocks = 4;
+template <bool WGRAD>
+constexpr int kScaleFloats = WGRAD ? BM + BN : BM + 4;
+template <bool WGRAD>
+constexpr int kSlotFloats = kSlotBlocks * kScaleFloats<WGRAD>;
 
-__host__ __device__ constexpr int num_bars(int stages) { return 2 * stages + 5; }
+constexpr int kNumBars = 2 * STAGES + 5 + 2 * kScaleSlots;
 
 struct Groups {
     int offs[kMaxExperts + 2];  // first row of each group; offs[G + 1]: all rows
     int pre[kMaxExperts + 2];   // tile rows (weight gradient: token blocks) of the groups before
 };
 
-template <int CG>
-constexpr int smem_bytes() {
-    return 1024 + Cfg<CG>::STAGES * static_cast<int>(A_BYTES + Cfg<CG>::B_BYTES) + kEpiWarps * 2 * 128 * 4 +
-           num_bars(Cfg<CG>::STAGES) * 8 + 16 + static_cast<int>(sizeof(Groups));
-}
-static_assert(smem_bytes<1>() <= 232448 && smem_bytes<2>() <= 232448, "shared memory budget");
+constexpr int kSmemBytes = 1024 + STAGES * static_cast<int>(A_BYTES + B_BYTES) + kScaleSlots * kSlotFloats<true> * 4 +
+                           kEpiWarps * kStageBytes + kNumBars * 8 + 16 + static_cast<int>(sizeof(Groups));
+static_assert(kSmemBytes <= 232448, "shared memory budget");
 
-template <int CG>
 __device__ __forceinline__ void tc_mma_f8(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
                                           uint32_t accumulate) {
-    if constexpr (CG == 1)
-        asm volatile(
-            "{\n\t.reg .pred p;\n\t"
-            "setp.ne.b32 p, %4, 0;\n\t"
-            "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
-            "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
-            : "memory");
-    else
-        asm volatile(
-            "{\n\t.reg .pred p;\n\t"
-            "setp.ne.b32 p, %4, 0;\n\t"
-            "tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
-            "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
-            : "memory");
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+        "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
+        : "memory");
 }
 
 // Instruction descriptor of kind::f8f6f4, fp32 accumulator.
@@ -94,35 +93,6 @@ __device__ __forceinline__ uint32_t idesc_f8(int M, int N, int fmt_a, int fmt_b,
            | (static_cast<uint32_t>(fmt_b) << 10)
            | (a_mn << 15) | (b_mn << 16)
            | (static_cast<uint32_t>(N >> 3) << 17) | (static_cast<uint32_t>(M >> 4) << 24);
-}
-
-// acc (two fp32) += {v0, v1} * s (two fp32), each rounded once.
-__device__ __forceinline__ void fma2(uint64_t& acc, uint32_t v0, uint32_t v1, uint64_t s) {
-    // volatile: keeps its place between the TMEM loads (a chunk is used before
-    // the next one is loaded, which the register budget counts on).
-    asm volatile("{\n\t.reg .b64 t;\n\tmov.b64 t, {%1, %2};\n\tfma.rn.f32x2 %0, t, %3, %0;\n\t}"
-        : "+l"(acc)
-        : "r"(v0), "r"(v1), "l"(s));
-}
-__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
-    uint64_t r;
-    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-    return r;
-}
-__device__ __forceinline__ uint64_t pack2(float lo, float hi) {
-    uint64_t r;
-    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
-    return r;
-}
-__device__ __forceinline__ uint64_t pack2u(uint32_t lo, uint32_t hi) {
-    uint64_t r;
-    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "r"(lo), "r"(hi));
-    return r;
-}
-__device__ __forceinline__ float2 unpack2(uint64_t v) {
-    float2 f;
-    asm("mov.b64 {%0, %1}, %2;" : "=f"(f.x), "=f"(f.y) : "l"(v));
-    return f;
 }
 
 // mbar_wait with its bounded spin inline: a call in the epilogue's loop would
@@ -140,11 +110,47 @@ __device__ __forceinline__ bool mbar_wait_here(uint32_t bar, uint32_t parity, co
     return true;
 }
 
+// Whether the phase is complete, without waiting.
+__device__ __forceinline__ bool mbar_test(uint32_t bar, uint32_t parity) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(bar), "r"(parity)
+        : "memory");
+    return ok != 0;
+}
+
 // tcgen05.wait::ld that the uses of v depend on.
 __device__ __forceinline__ void tmem_ld_wait_for(uint32_t (&v)[32]) {
-    tmem_ld_wait();
-#pragma unroll
-    for (int i = 0; i < 32; ++i) asm volatile("" : "+r"(v[i]));
+    asm volatile("tcgen05.wait::ld.sync.aligned;"
+        : "+r"(v[0]), "+r"(v[1]), "+r"(v[2]), "+r"(v[3]), "+r"(v[4]), "+r"(v[5]), "+r"(v[6]), "+r"(v[7]),
+          "+r"(v[8]), "+r"(v[9]), "+r"(v[10]), "+r"(v[11]), "+r"(v[12]), "+r"(v[13]), "+r"(v[14]),
+          "+r"(v[15]), "+r"(v[16]), "+r"(v[17]), "+r"(v[18]), "+r"(v[19]), "+r"(v[20]), "+r"(v[21]),
+          "+r"(v[22]), "+r"(v[23]), "+r"(v[24]), "+r"(v[25]), "+r"(v[26]), "+r"(v[27]), "+r"(v[28]),
+          "+r"(v[29]), "+r"(v[30]), "+r"(v[31])
+        :
+        : "memory");
+}
+
+// BYTES from global to shared memory, zeros where `in` is false (then `safe`,
+// which is not read, stands for the address).
+template <int BYTES>
+__device__ __forceinline__ void copy_async(uint32_t dst, const float* src, bool in, const float* safe) {
+    const int n = in ? BYTES : 0;
+    const float* p = in ? src : safe;
+    if constexpr (BYTES == 16)
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(p), "r"(n) : "memory");
+    else
+        asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(p), "r"(n) : "memory");
+}
+
+__device__ __forceinline__ float ld_shared_f32(uint32_t addr) {
+    float v;
+    asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
+    return v;
 }
 
 struct Tile {
@@ -160,9 +166,7 @@ struct Walk {
     const Groups* gr;
 };
 
-template <int CG>
 __device__ __forceinline__ Tile decode(const Walk& w, int t) {
-    constexpr int TM = Cfg<CG>::TM;
     Tile tl;
     tl.split = 0;
     int local, rows;
@@ -193,7 +197,7 @@ __device__ __forceinline__ Tile decode(const Walk& w, int t) {
     const int h = min(kBand, rows - band * kBand);
     const int nt = rem / h;
     tl.n0 = nt * BN;
-    tl.m0 = (band * kBand + rem - nt * h) * TM;
+    tl.m0 = (band * kBand + rem - nt * h) * BM;
     if (w.wgrad) {
         tl.kb0 = w.gr->pre[tl.g];
         tl.kb1 = w.gr->pre[tl.g + 1];
@@ -213,67 +217,96 @@ __device__ __forceinline__ void drain_wait(uint32_t bar, uint32_t parity, uint64
     }
 }
 
-__device__ __forceinline__ void st_global_v8(void* p, const uint32_t (&a)[8]) {
-    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(a[0]), "r"(a[1]), "r"(a[2]),
-                 "r"(a[3]), "r"(a[4]), "r"(a[5]), "r"(a[6]), "r"(a[7])
-                 : "memory");
-}
-
-template <typename T>
-__device__ __forceinline__ uint32_t pack_pair(float2 f) {
-    if constexpr (sizeof(T) == 2) {
-        const T lo = from_f32<T>(f.x), hi = from_f32<T>(f.y);
-        return static_cast<uint32_t>(*reinterpret_cast<const uint16_t*>(&lo)) |
-               (static_cast<uint32_t>(*reinterpret_cast<const uint16_t*>(&hi)) << 16);
+// One 32-bit word of two 16-bit results, or of one 32-bit result.
+__device__ __forceinline__ uint32_t pack_pair(float lo, float hi, bool bf16) {
+    if (bf16) {
+        const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
+        return *reinterpret_cast<const uint32_t*>(&h);
     }
-    return 0;
+    return pack_half2(lo, hi);
 }
 
-// The thread's 128 columns from column n0 of one row (ncol of them inside
-// the matrix), straight from its registers: 32-byte stores where the row
-// allows them, single elements otherwise.
-template <typename T>
-__device__ __forceinline__ void store_row(T* row, const uint64_t (&acc)[64], int ncol, bool direct) {
-    constexpr int PER = 32 / sizeof(T);
+// The warp's 32 rows x kCols columns (a thread holds one row), clipped to
+// rows x ncol, to d (row stride ldd elements of ES bytes). Rows go through
+// shared memory, 128 bytes of each at a time (16-byte pieces, piece index XOR
+// row mod 8), so that a store instruction writes four whole 128-byte lines
+// where rows start on 16-byte boundaries, and runs of neighbouring elements
+// where they do not. Straight from the registers a store would touch 32 rows:
+// a 128 x 256 tile took 4000 cycles that way.
+template <int ES>
+__device__ __forceinline__ void store_tile(uint32_t stage, uint8_t* d, long long ldd, int rows, int ncol,
+                                           const float (&acc)[kCols], bool bf16, bool aligned, int lane) {
+    constexpr int PASS = kStageRow / ES;  // columns per pass
+    constexpr int PIECE = 16 / ES;        // elements of a 16-byte piece
 #pragma unroll
-    for (int c = 0; c < 128; c += PER) {
-        if (direct && c + PER <= ncol) {
-            uint32_t w[8];
+    for (int p = 0; p < kCols / PASS; ++p) {
+        const int left = ncol - p * PASS;  // columns from here on
+        if (left <= 0) break;
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                if constexpr (sizeof(T) == 2) {
-                    w[i] = pack_pair<T>(unpack2(acc[c / 2 + i]));
-                } else {
-                    const float2 f = unpack2(acc[(c + i) / 2]);
-                    w[i] = __float_as_uint(i & 1 ? f.y : f.x);
+        for (int k = 0; k < 8; ++k) {
+            uint32_t w[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                if constexpr (ES == 2)
+                    w[e] = pack_pair(acc[p * PASS + 8 * k + 2 * e], acc[p * PASS + 8 * k + 2 * e + 1], bf16);
+                else
+                    w[e] = __float_as_uint(acc[p * PASS + 4 * k + e]);
+            }
+            st_shared_v4(stage + lane * kStageRow + ((k ^ (lane & 7)) << 4), w[0], w[1], w[2], w[3]);
+        }
+        __syncwarp();
+        uint8_t* dp = d + static_cast<long long>(p) * kStageRow;
+        if (aligned) {
+            const int k = lane & 7, r0 = lane >> 3;
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                const int r = 4 * j + r0;
+                const uint4 v = ld_shared_v4(stage + r * kStageRow + ((k ^ (r & 7)) << 4));
+                uint8_t* a = dp + r * ldd * ES + 16 * k;
+                if (r < rows) {
+                    if ((k + 1) * PIECE <= left) {
+                        *reinterpret_cast<uint4*>(a) = v;
+                    } else {
+                        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+                        for (int e = 0; e < PIECE; ++e) {
+                            if (k * PIECE + e >= left) continue;
+                            if constexpr (ES == 2)
+                                reinterpret_cast<uint16_t*>(a)[e] = static_cast<uint16_t>(w[e / 2] >> (16 * (e & 1)));
+                            else
+                                reinterpret_cast<uint32_t*>(a)[e] = w[e];
+                        }
+                    }
                 }
             }
-            st_global_v8(row + c, w);
         } else {
+            for (int r = 0; r < min(rows, 32); ++r) {
 #pragma unroll
-            for (int i = 0; i < PER; i += 2) {
-                const float2 f = unpack2(acc[(c + i) / 2]);
-                if (c + i < ncol) row[c + i] = from_f32<T>(f.x);
-                if (c + i + 1 < ncol) row[c + i + 1] = from_f32<T>(f.y);
+                for (int c = lane; c < PASS; c += 32) {
+                    const uint32_t at = stage + r * kStageRow + (((c / PIECE) ^ (r & 7)) << 4) + (c % PIECE) * ES;
+                    if (c < left) {
+                        if constexpr (ES == 2)
+                            *reinterpret_cast<uint16_t*>(dp + r * ldd * ES + c * ES) = ld_shared_u16(at);
+                        else
+                            *reinterpret_cast<float*>(dp + r * ldd * ES + c * ES) = ld_shared_f32(at);
+                    }
+                }
             }
         }
+        __syncwarp();  // read before the next pass overwrites
     }
 }
 
-template <int CG, bool WGRAD>
+template <bool WGRAD>
 __global__ void __launch_bounds__(kThreads, 1) fp8_gemm_kernel(const __grid_constant__ Fp8GemmJob P) {
-    constexpr int STAGES = Cfg<CG>::STAGES;
-    constexpr int TM = Cfg<CG>::TM;
-    constexpr int BNH = BN / CG;
-    constexpr uint32_t B_BYTES = Cfg<CG>::B_BYTES;
-
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     uint8_t* sA = smem;
     uint8_t* sB = sA + STAGES * A_BYTES;
-    float* scales = reinterpret_cast<float*>(sB + STAGES * B_BYTES);  // [kEpiWarps][2][128]
-    uint64_t* bars = reinterpret_cast<uint64_t*>(scales + kEpiWarps * 2 * 128);
-    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + num_bars(STAGES));
+    float* scales = reinterpret_cast<float*>(sB + STAGES * B_BYTES);
+    uint8_t* staging = reinterpret_cast<uint8_t*>(scales + kScaleSlots * kSlotFloats<true>);
+    uint64_t* bars = reinterpret_cast<uint64_t*>(staging + kEpiWarps * kStageBytes);
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + kNumBars);
     Groups* gr = reinterpret_cast<Groups*>(tmem_slot + 4);
 
     const uint32_t full0 = smem_u32(bars);
@@ -281,11 +314,12 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_gemm_kernel(const __grid_cons
     const uint32_t accf0 = smem_u32(bars + 2 * STAGES);
     const uint32_t acce0 = smem_u32(bars + 2 * STAGES + 2);
     const uint32_t drain_bar = smem_u32(bars + 2 * STAGES + 4);
+    const uint32_t sfull0 = smem_u32(bars + 2 * STAGES + 5);
+    const uint32_t sempty0 = sfull0 + 8 * kScaleSlots;
 
     const int warp = threadIdx.x >> 5;
     const int lane = threadIdx.x & 31;
     const DevStatus& err = P.st;
-    const uint32_t rank = CG > 1 ? cluster_ctarank() : 0;
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < STAGES; ++s) {
@@ -294,16 +328,20 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_gemm_kernel(const __grid_cons
         }
         for (int b = 0; b < 2; ++b) {
             mbar_init(accf0 + 8 * b, 1);
-            mbar_init(acce0 + 8 * b, kEpiWarps * CG);
+            mbar_init(acce0 + 8 * b, kEpiWarps);
         }
         mbar_init(drain_bar, 1);
+        for (int b = 0; b < kScaleSlots; ++b) {
+            mbar_init(sfull0 + 8 * b, 32);
+            mbar_init(sempty0 + 8 * b, kEpiWarps);
+        }
         fence_mbar_init();
         prefetch_tmap(&P.mapA);
         prefetch_tmap(&P.mapB);
     }
     if (warp == 1) {
-        tmem_alloc<CG>(smem_u32(tmem_slot), kTmemCols);
-        tmem_relinquish<CG>();
+        tmem_alloc<1>(smem_u32(tmem_slot), kTmemCols);
+        tmem_relinquish<1>();
     }
     grid_dependency_wait();
     grid_launch_dependents();
@@ -320,7 +358,7 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_gemm_kernel(const __grid_cons
         const int g0 = threadIdx.x * per;
         auto units = [&](int g) {
             const int c = gr->offs[g + 1] - gr->offs[g];
-            return WGRAD ? (c + BK - 1) / BK : (c + TM - 1) / TM;
+            return WGRAD ? (c + BK - 1) / BK : (c + BM - 1) / BM;
         };
         int mine = 0;
         for (int i = 0; i < per && g0 + i < n; ++i) mine += units(g0 + i);
@@ -340,7 +378,7 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_gemm_kernel(const __grid_cons
             if (g0 + i == G) gr->pre[n] = start;
         }
     } else if (threadIdx.x == 0) {
-        const int u = WGRAD ? (P.rows + BK - 1) / BK : (P.rows + TM - 1) / TM;
+        const int u = WGRAD ? (P.rows + BK - 1) / BK : (P.rows + BM - 1) / BM;
         gr->offs[0] = 0;
         gr->offs[1] = gr->offs[2] = P.rows;
         gr->pre[0] = 0;
@@ -348,20 +386,19 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_gemm_kernel(const __grid_cons
     }
     tc_fence_before();
     __syncthreads();
-    if constexpr (CG > 1) cluster_sync();
     tc_fence_after();
     const uint32_t tmem_base = *tmem_slot;
 
     Walk w;
     w.G = G;
     w.ntn = (P.N + BN - 1) / BN;
-    w.mtn = WGRAD ? (P.M + TM - 1) / TM : 0;
+    w.mtn = WGRAD ? (P.M + BM - 1) / BM : 0;
     w.split = P.split;
     w.wgrad = WGRAD;
     w.total_kb = WGRAD ? 0 : (P.K + BK - 1) / BK;
     w.gr = gr;
     const int total = WGRAD ? G * w.mtn * w.ntn : gr->pre[G + 1] * w.ntn * P.split;
-    const int first = static_cast<int>(blockIdx.x) / CG, stride = static_cast<int>(gridDim.x) / CG;
+    const int first = static_cast<int>(blockIdx.x), stride = static_cast<int>(gridDim.x);
     const bool a_mn = WGRAD, b_mn = WGRAD || P.b_mn;
 
     if (warp < kEpiWarp0) {
@@ -373,9 +410,8 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_gemm_kernel(const __grid_cons
                 int issued = 0;
                 bool ok = true;
                 for (int t = first; ok && t < total; t += stride) {
-                    const Tile tl = decode<CG>(w, t);
-                    const int arow = (WGRAD ? 0 : gr->offs[tl.g]) + tl.m0 + BM * static_cast<int>(rank);
-                    const int brow = tl.n0 + BNH * static_cast<int>(rank);
+                    const Tile tl = decode(w, t);
+                    const int arow = (WGRAD ? 0 : gr->offs[tl.g]) + tl.m0;
                     const int gb = WGRAD ? 0 : tl.g;
                     for (int kb = tl.kb0; kb < tl.kb1; ++kb) {
                         if (!mbar_wait(empty0 + 8 * stage, phase ^ 1, err)) {
@@ -384,29 +420,16 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_gemm_kernel(const __grid_cons
                         }
                         const uint32_t fb = full0 + 8 * stage;
                         const uint32_t da = smem_u32(sA + stage * A_BYTES), db = smem_u32(sB + stage * B_BYTES);
-                        if constexpr (CG == 1) {
-                            mbar_arrive_expect_tx(fb, A_BYTES + B_BYTES);
-                            if (a_mn)
-                                tma_load_3d(da, &P.mapA, fb, arow, kb * BK, 0);
-                            else
-                                tma_load_3d(da, &P.mapA, fb, kb * BK, arow, 0);
-                            if (b_mn) {
-                                for (int h = 0; h < BNH / 128; ++h)
-                                    tma_load_3d(db + h * kBoxBytes, &P.mapB, fb, brow + 128 * h, kb * BK, gb);
-                            } else {
-                                tma_load_3d(db, &P.mapB, fb, kb * BK, brow, gb);
-                            }
+                        mbar_arrive_expect_tx(fb, A_BYTES + B_BYTES);
+                        if (a_mn)
+                            tma_load_3d(da, &P.mapA, fb, arow, kb * BK, 0);
+                        else
+                            tma_load_3d(da, &P.mapA, fb, kb * BK, arow, 0);
+                        if (b_mn) {
+                            for (int h = 0; h < BN / 128; ++h)
+                                tma_load_3d(db + h * kBoxBytes, &P.mapB, fb, tl.n0 + 128 * h, kb * BK, gb);
                         } else {
-                            if (rank == 0) mbar_arrive_expect_tx(fb, 2 * (A_BYTES + B_BYTES));
-                            const uint32_t lead_fb = map_to_rank(fb, 0);
-                            if (a_mn)
-                                tma_load_3d_pair(da, &P.mapA, lead_fb, arow, kb * BK, 0);
-                            else
-                                tma_load_3d_pair(da, &P.mapA, lead_fb, kb * BK, arow, 0);
-                            if (b_mn)
-                                tma_load_3d_pair(db, &P.mapB, lead_fb, brow, kb * BK, gb);
-                            else
-                                tma_load_3d_pair(db, &P.mapB, lead_fb, kb * BK, brow, gb);
+                            tma_load_3d(db, &P.mapB, fb, kb * BK, tl.n0, gb);
                         }
                         ++issued;
                         if (++stage == STAGES) {
@@ -416,33 +439,31 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_gemm_kernel(const __grid_cons
                     }
                 }
                 // Loads still in flight land before the CTA ends.
-                if (CG == 1 || rank == 0) {
-                    const int pending = issued < STAGES ? issued : STAGES;
-                    for (int i = 0; i < pending; ++i) {
-                        if (stage == 0) {
-                            stage = STAGES;
-                            phase ^= 1;
-                        }
-                        --stage;
-                        drain_wait(full0 + 8 * stage, phase, err.limit_ns);
+                const int pending = issued < STAGES ? issued : STAGES;
+                for (int i = 0; i < pending; ++i) {
+                    if (stage == 0) {
+                        stage = STAGES;
+                        phase ^= 1;
                     }
+                    --stage;
+                    drain_wait(full0 + 8 * stage, phase, err.limit_ns);
                 }
             }
             __syncwarp();
         } else if (warp == 1) {
-            // ------------------------------------------- MMA issuer (pair leader)
-            if (lane == 0 && rank == 0) {
+            // ------------------------------------------- MMA issuer
+            if (lane == 0) {
                 uint32_t stage = 0, phase = 0;
                 int it = 0;  // k blocks issued; the accumulator buffer is it & 1
                 bool ok = true;
-                const uint32_t idesc = idesc_f8(TM, BN, P.fmt_a, P.fmt_b, a_mn, b_mn);
+                const uint32_t idesc = idesc_f8(BM, BN, P.fmt_a, P.fmt_b, a_mn, b_mn);
                 const uint64_t a0 = a_mn ? sw128_mnmajor_desc(smem_u32(sA), kBoxBytes) : sw128_kmajor_desc(smem_u32(sA));
                 const uint64_t b0 = b_mn ? sw128_mnmajor_desc(smem_u32(sB), kBoxBytes) : sw128_kmajor_desc(smem_u32(sB));
                 // A 32-wide k step: 32 bytes along a K-major row, or 32 rows of an MN-major tile.
                 const uint32_t a_step = a_mn ? (4096 >> 4) : (32 >> 4);
                 const uint32_t b_step = b_mn ? (4096 >> 4) : (32 >> 4);
                 for (int t = first; ok && t < total; t += stride) {
-                    const Tile tl = decode<CG>(w, t);
+                    const Tile tl = decode(w, t);
                     for (int kb = tl.kb0; kb < tl.kb1; ++kb, ++it) {
                         const int buf = it & 1;
                         if (!mbar_wait(acce0 + 8 * buf, ((it >> 1) & 1) ^ 1, err) ||
@@ -455,14 +476,9 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_gemm_kernel(const __grid_cons
                         const uint64_t bdesc = b0 + ((stage * B_BYTES) >> 4);
 #pragma unroll
                         for (int kk = 0; kk < BK / 32; ++kk)
-                            tc_mma_f8<CG>(tmem_base + buf * BN, adesc + a_step * kk, bdesc + b_step * kk, idesc, kk != 0);
-                        if constexpr (CG == 1) {
-                            tc_commit<1>(empty0 + 8 * stage);
-                            tc_commit<1>(accf0 + 8 * buf);
-                        } else {
-                            tc_commit_pair(empty0 + 8 * stage);
-                            tc_commit_pair(accf0 + 8 * buf);
-                        }
+                            tc_mma_f8(tmem_base + buf * BN, adesc + a_step * kk, bdesc + b_step * kk, idesc, kk != 0);
+                        tc_commit<1>(empty0 + 8 * stage);
+                        tc_commit<1>(accf0 + 8 * buf);
                         if (++stage == STAGES) {
                             stage = 0;
                             phase ^= 1;
@@ -470,9 +486,51 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_gemm_kernel(const __grid_cons
                     }
                 }
                 // All MMAs issued by this thread must finish before TMEM is freed.
-                tc_commit<CG>(drain_bar);
+                tc_commit<1>(drain_bar);
                 drain_wait(drain_bar, 0, err.limit_ns);
             }
+            __syncwarp();
+        } else if (warp == 2) {
+            // ----------------------------------------------- scale producer
+            const uint32_t ring = smem_u32(scales);
+            int slot = 0;
+            uint32_t phase = 0;
+            bool ok = true;
+            for (int t = first; ok && t < total; t += stride) {
+                const Tile tl = decode(w, t);
+                const int local = tl.m0 + lane;
+                const int rows = WGRAD ? P.M : gr->offs[tl.g + 1] - gr->offs[tl.g];
+                const float* pa = P.sA + (WGRAD ? 0 : gr->offs[tl.g]) + local;
+                const float* pb = P.sB + (WGRAD ? tl.n0 + 4 * lane
+                                                : tl.g * P.sB_g + static_cast<long long>(tl.n0 / kFp8Block + lane) * P.sB_n);
+                for (int kb0 = tl.kb0; kb0 < tl.kb1; kb0 += kSlotBlocks) {
+                    if (!__all_sync(0xffffffffu, mbar_wait(sempty0 + 8 * slot, phase ^ 1, err))) {
+                        ok = false;
+                        break;
+                    }
+                    const int end = min(kb0 + kSlotBlocks, tl.kb1);
+                    for (int kb = kb0; kb < end; ++kb) {
+                        const uint32_t dst = ring + 4 * (slot * kSlotFloats<WGRAD> + (kb - kb0) * kScaleFloats<WGRAD>);
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+                            copy_async<4>(dst + 4 * (lane + 32 * i), pa + kb * P.ldsA + 32 * i, local + 32 * i < rows, P.sA);
+                        if constexpr (WGRAD) {
+#pragma unroll
+                            for (int i = 0; i < 2; ++i)
+                                copy_async<16>(dst + 4 * (BM + 4 * lane + 128 * i), pb + kb * P.sB_k + 128 * i,
+                                               tl.n0 + 4 * lane + 128 * i < P.sB_k, P.sB);
+                        } else if (lane < 2) {
+                            copy_async<4>(dst + 4 * (BM + lane), pb + kb * P.sB_k, tl.n0 + 128 * lane < P.N, P.sB);
+                        }
+                    }
+                    asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(sfull0 + 8 * slot) : "memory");
+                    if (++slot == kScaleSlots) {
+                        slot = 0;
+                        phase ^= 1;
+                    }
+                }
+            }
+            asm volatile("cp.async.wait_all;" ::: "memory");
             __syncwarp();
         }
     } else {
@@ -480,119 +538,116 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_gemm_kernel(const __grid_cons
         asm volatile("setmaxnreg.inc.sync.aligned.u32 232;");
         const int q = warp & 3;           // TMEM lane quarter this warp may read
         const int ew = warp - kEpiWarp0;
-        const int half = ew >> 2;         // columns 128 half .. 128 half + 127 of the tile
-        float* sbuf = scales + ew * 256;  // two k blocks' column scales (weight gradient)
-        const uint32_t sbuf_u32 = smem_u32(sbuf);
-        const uint32_t acce_lead = CG == 2 ? map_to_rank(acce0, 0) : acce0;
-        const uint32_t tmem_warp = tmem_base + (static_cast<uint32_t>(q * 32) << 16) + half * 128;
-        int it = 0;
+        const int cq = (ew >> 2) * kCols;  // its first column within the tile
+        const uint32_t ring = smem_u32(scales);
+        const uint32_t tmem_warp = tmem_base + (static_cast<uint32_t>(q * 32) << 16) + cq;
+        int it = 0;    // k blocks added
+        int slot = 0;  // scale slot and its phase
+        uint32_t sphase = 0;
         bool ok = true;
         for (int t = first; ok && t < total; t += stride) {
-            const Tile tl = decode<CG>(w, t);
-            const int local = tl.m0 + BM * static_cast<int>(rank) + q * 32 + lane;
+            const Tile tl = decode(w, t);
             const int rows = WGRAD ? P.M : gr->offs[tl.g + 1] - gr->offs[tl.g];
-            const bool live = local < rows;
-            const int row = WGRAD ? local : gr->offs[tl.g] + local;
-            const int col = tl.n0 + 128 * half;
-            // Scales are read two k blocks ahead of their use.
-            const float* pa = P.sA + row;
-            const float* pb = WGRAD ? P.sB + col + 4 * lane
-                                    : P.sB + tl.g * P.sB_g + static_cast<long long>(col / kFp8Block) * P.sB_n;
-            const bool b_in = WGRAD ? col + 4 * lane < P.sB_k : col < P.N;
-            float sa[2] = {0.0f, 0.0f};
-            float sb[2] = {0.0f, 0.0f};
-            float4 sv[2];
-            auto fetch = [&](int kb, int slot) {
-                if (kb >= tl.kb1) return;
-                sa[slot] = live ? __ldg(pa + kb * P.ldsA) : 0.0f;
-                if constexpr (WGRAD)
-                    sv[slot] = b_in ? __ldg(reinterpret_cast<const float4*>(pb + kb * P.sB_k)) : make_float4(0, 0, 0, 0);
-                else
-                    sb[slot] = b_in ? __ldg(pb + kb * P.sB_k) : 0.0f;
-            };
-            fetch(tl.kb0, 0);
-            fetch(tl.kb0 + 1, 1);
-            uint64_t acc[64];
+            const int col = tl.n0 + cq;
+            float acc[kCols];
 #pragma unroll
-            for (int i = 0; i < 64; ++i) acc[i] = 0;
-            int slot = 0;
+            for (int i = 0; i < kCols; ++i) acc[i] = 0.0f;
+            // A chunk of 32 columns is loaded from TMEM while the one before it
+            // is added; the next k block's barrier is polled ahead of its use
+            // (a poll, like every shared-memory access, takes some 150 cycles
+            // beside the MMAs' operand reads).
+            bool ready = false;
+            float s = 0.0f;
 #pragma unroll 1
             for (int kb = tl.kb0; kb < tl.kb1; ++kb, ++it) {
-                const int buf = it & 1;
-                float s = WGRAD ? sa[0] : sa[0] * sb[0];
-                if constexpr (WGRAD) {
-                    *reinterpret_cast<float4*>(sbuf + 128 * slot + 4 * lane) = sv[0];
-                    sv[0] = sv[1];
-                    __syncwarp();
-                }
-                sa[0] = sa[1];
-                sb[0] = sb[1];
-                fetch(kb + 2, 1);
-                const uint64_t s2 = pack2(s, s);
-                if (!__all_sync(0xffffffffu, mbar_wait_here(accf0 + 8 * buf, (it >> 1) & 1, err))) {
-                    ok = false;
-                    break;
+                const int in_slot = (kb - tl.kb0) % kSlotBlocks;
+                const uint32_t acc_tmem = tmem_warp + (it & 1) * BN;
+                const uint32_t sc = ring + 4 * (slot * kSlotFloats<WGRAD> + in_slot * kScaleFloats<WGRAD>);
+                if (!__all_sync(0xffffffffu, ready)) {
+                    ok = (in_slot != 0 || mbar_wait_here(sfull0 + 8 * slot, sphase, err)) &&
+                         mbar_wait_here(accf0 + 8 * (it & 1), (it >> 1) & 1, err);
+                    if (!__all_sync(0xffffffffu, ok)) {
+                        ok = false;
+                        break;
+                    }
                 }
                 tc_fence_after();
+                uint32_t v[2][32];
+                tmem_ld_32x32b_x32(acc_tmem, v[0]);
+                s = ld_shared_f32(sc + 4 * (q * 32 + lane));
+                if (!WGRAD) s *= ld_shared_f32(sc + 4 * (BM + cq / kFp8Block));
 #pragma unroll
-                for (int c = 0; c < 4; ++c) {
-                    uint32_t v[32];
-                    tmem_ld_32x32b_x32(tmem_warp + buf * BN + 32 * c, v);
-                    tmem_ld_wait_for(v);
-                    if (c == 3) {  // the accumulator is in registers: the next MMAs may overwrite it
+                for (int c = 0; c < kCols / 32; ++c) {
+                    const uint32_t(&x)[32] = v[c & 1];
+                    tmem_ld_wait_for(v[c & 1]);
+                    if (c + 1 < kCols / 32) {
+                        tmem_ld_32x32b_x32(acc_tmem + 32 * (c + 1), v[(c + 1) & 1]);
+                    } else {  // all in registers: the next MMAs may overwrite the accumulator
                         tc_fence_before();
                         __syncwarp();
-                        if (lane == 0) {
-                            if constexpr (CG == 1)
-                                mbar_arrive(acce0 + 8 * buf);
-                            else
-                                mbar_arrive_cluster(acce_lead + 8 * buf);
-                        }
+                        if (lane == 0) mbar_arrive(acce0 + 8 * (it & 1));
+                        ready = in_slot != kSlotBlocks - 1 && kb + 1 < tl.kb1 &&
+                                mbar_test(accf0 + 8 * ((it + 1) & 1), ((it + 1) >> 1) & 1);
                     }
                     if constexpr (WGRAD) {
 #pragma unroll
                         for (int i = 0; i < 8; ++i) {
-                            const uint4 f = ld_shared_v4(sbuf_u32 + 4 * (128 * slot + 32 * c + 4 * i));
-                            fma2(acc[16 * c + 2 * i], v[4 * i], v[4 * i + 1], mul2(s2, pack2u(f.x, f.y)));
-                            fma2(acc[16 * c + 2 * i + 1], v[4 * i + 2], v[4 * i + 3], mul2(s2, pack2u(f.z, f.w)));
+                            const uint4 f = ld_shared_v4(sc + 4 * (BM + cq + 32 * c + 4 * i));
+                            const uint32_t g[4] = {f.x, f.y, f.z, f.w};
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) {
+                                const int j = 4 * i + e;
+                                acc[32 * c + j] = fmaf(__uint_as_float(x[j]), s * __uint_as_float(g[e]), acc[32 * c + j]);
+                            }
                         }
                     } else {
 #pragma unroll
-                        for (int i = 0; i < 16; ++i) fma2(acc[16 * c + i], v[2 * i], v[2 * i + 1], s2);
+                        for (int j = 0; j < 32; ++j)
+                            acc[32 * c + j] = fmaf(__uint_as_float(x[j]), s, acc[32 * c + j]);
                     }
                 }
-                slot ^= 1;
+                if (in_slot == kSlotBlocks - 1 || kb + 1 == tl.kb1) {
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(sempty0 + 8 * slot);
+                    if (++slot == kScaleSlots) {
+                        slot = 0;
+                        sphase ^= 1;
+                    }
+                }
             }
             if (!ok) break;
-            if (!live || col >= P.N) continue;
-            const int ncol = P.N - col;
+            // Rows of this warp inside the group (of D) and columns inside D.
+            const int wrows = rows - tl.m0 - q * 32, ncol = P.N - col;
+            if (wrows <= 0 || ncol <= 0) continue;
+            const int es = P.out_dtype == GNS_FP32 || P.split > 1 ? 4 : 2;
+            const uint32_t stage = smem_u32(staging + ew * kStageBytes);
+            const long long row0 = (WGRAD ? 0 : gr->offs[tl.g]) + tl.m0 + q * 32;
+            uint8_t* d;
+            long long ldd;
+            bool aligned;
             if (P.split > 1) {
-                float* d = P.partial + (static_cast<long long>(tl.split) * P.rows + row) * P.N + col;
-                store_row<float>(d, acc, ncol, P.N % 8 == 0);
-                continue;
+                d = reinterpret_cast<uint8_t*>(P.partial + (static_cast<long long>(tl.split) * P.rows + row0) * P.N + col);
+                ldd = P.N;
+                aligned = P.N % 4 == 0;
+            } else {
+                d = static_cast<uint8_t*>(P.D) + ((WGRAD ? tl.g * P.strideD : 0LL) + row0 * P.ldd + col) * es;
+                ldd = P.ldd;
+                aligned = ((reinterpret_cast<uintptr_t>(P.D) | static_cast<uintptr_t>(P.ldd * es) |
+                            static_cast<uintptr_t>(P.strideD * es)) & 15) == 0;
             }
-            const long long at = (WGRAD ? tl.g * P.strideD : 0LL) + static_cast<long long>(row) * P.ldd + col;
-            const int es = P.out_dtype == GNS_FP32 ? 4 : 2;
-            const bool direct = ((reinterpret_cast<uintptr_t>(P.D) | static_cast<uintptr_t>(P.ldd * es) |
-                                  static_cast<uintptr_t>(P.strideD * es)) & 31) == 0;
-            if (P.out_dtype == GNS_BF16)
-                store_row(static_cast<__nv_bfloat16*>(P.D) + at, acc, ncol, direct);
-            else if (P.out_dtype == GNS_FP16)
-                store_row(static_cast<__half*>(P.D) + at, acc, ncol, direct);
+            if (es == 2)
+                store_tile<2>(stage, d, ldd, wrows, ncol, acc, P.out_dtype == GNS_BF16, aligned, lane);
             else
-                store_row(static_cast<float*>(P.D) + at, acc, ncol, direct);
+                store_tile<4>(stage, d, ldd, wrows, ncol, acc, false, aligned, lane);
         }
         __syncwarp();
     }
 
     tc_fence_before();
     __syncthreads();
-    // The leader's MMAs read the peer's shared memory and the peer's loads and
-    // epilogues arrive on the leader's barriers: neither leaves before the other.
-    if constexpr (CG > 1) cluster_sync();
     if (warp == 1) {
         tc_fence_after();
-        tmem_dealloc<CG>(tmem_base, kTmemCols);
+        tmem_dealloc<1>(tmem_base, kTmemCols);
     }
 }
 
@@ -613,56 +668,23 @@ __global__ void __launch_bounds__(256) fp8_reduce_kernel(const float* partial, i
 
 constexpr int kMaxDevices = 64;
 
-template <int CG, bool WGRAD>
+template <bool WGRAD>
 int launch_variant(const Fp8GemmJob& job, long long max_tiles, int num_sms, cudaStream_t s) {
-    // Per device: the shared-memory opt-in and the clusters that fit at once.
-    static int clusters[kMaxDevices];
+    static bool configured[kMaxDevices];  // the shared-memory opt-in is per device
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
     if (dev < 0 || dev >= kMaxDevices) return cudaErrorInvalidDevice;
-    cudaLaunchConfig_t cfg = {};
-    cfg.blockDim = dim3(kThreads);
-    cfg.dynamicSmemBytes = smem_bytes<CG>();
-    cfg.stream = s;
-    cudaLaunchAttribute attr[2];
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = CG;
-    attr[0].val.clusterDim.y = 1;
-    attr[0].val.clusterDim.z = 1;
-    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[1].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = attr;
-    if (clusters[dev] == 0) {
-        e = cudaFuncSetAttribute(fp8_gemm_kernel<CG, WGRAD>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                 smem_bytes<CG>());
+    if (!configured[dev]) {
+        e = cudaFuncSetAttribute(fp8_gemm_kernel<WGRAD>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
         if (e != cudaSuccess) return e;
-        int n = 0;
-        cfg.gridDim = dim3(CG * (num_sms / CG > 0 ? num_sms / CG : 1));
-        cfg.numAttrs = 1;
-        if (cudaOccupancyMaxActiveClusters(&n, fp8_gemm_kernel<CG, WGRAD>, &cfg) != cudaSuccess || n <= 0) {
-            cudaGetLastError();
-            n = num_sms / CG;
-        }
-        clusters[dev] = n > 0 ? n : 1;
+        configured[dev] = true;
     }
-    const int fit = std::max(1, std::min(clusters[dev], num_sms / CG));
-    cfg.gridDim = dim3(CG * static_cast<unsigned>(std::min<long long>(fit, max_tiles)));
-    cfg.numAttrs = 2;
-    return cudaLaunchKernelEx(&cfg, fp8_gemm_kernel<CG, WGRAD>, job);
+    const unsigned grid = static_cast<unsigned>(std::min<long long>(num_sms, max_tiles));
+    return launch_after(fp8_gemm_kernel<WGRAD>, dim3(grid), dim3(kThreads), kSmemBytes, s, job);
 }
 
 }  // namespace
-
-int fp8_gemm_tile_rows(int M, int N, int G, bool grouped, int num_sms) {
-    // Pairs (256-row tiles) halve the L2 traffic of a k block's B; single CTAs
-    // waste fewer rows on ragged groups and fill the machine sooner.
-    const long long per = grouped ? (M + G - 1) / G : M;
-    const long long tn = (N + BN - 1) / BN;
-    const long long pairs = (grouped ? G : 1) * ((per + 255) / 256) * tn;
-    if (per <= 384 && grouped) return 128;
-    return per > 128 && 2 * pairs >= num_sms ? 256 : 128;
-}
 
 int fp8_gemm_split(int rows, int N, int K, int num_sms) {
     const long long tiles = static_cast<long long>((rows + BM - 1) / BM) * ((N + BN - 1) / BN);
@@ -672,19 +694,18 @@ int fp8_gemm_split(int rows, int N, int K, int num_sms) {
     return static_cast<int>(std::max<long long>(1, std::min<long long>(num_sms / tiles, kb / 4)));
 }
 
-int launch_fp8_gemm(const Fp8GemmJob& job, int tile_rows, int num_sms, cudaStream_t s) {
+int launch_fp8_gemm(const Fp8GemmJob& job, int num_sms, cudaStream_t s) {
     const long long tn = (job.N + BN - 1) / BN;
-    const long long tm = job.wgrad
-                             ? static_cast<long long>(job.G) * ((job.M + tile_rows - 1) / tile_rows)
-                             : (job.offsets ? (job.rows + static_cast<long long>(tile_rows - 1) * (std::min(job.rows, job.G) + 1)) / tile_rows
-                                            : (job.rows + tile_rows - 1) / tile_rows);
+    long long tm;  // tile rows, an upper bound where the groups are on the device
+    if (job.wgrad)
+        tm = static_cast<long long>(job.G) * ((job.M + BM - 1) / BM);
+    else if (job.offsets)
+        tm = (job.rows + static_cast<long long>(BM - 1) * (std::min(job.rows, job.G) + 1)) / BM;
+    else
+        tm = (job.rows + BM - 1) / BM;
     const long long tiles = tm * tn * job.split;
     if (tiles <= 0) return cudaSuccess;
-    int e;
-    if (tile_rows == 256)
-        e = job.wgrad ? launch_variant<2, true>(job, tiles, num_sms, s) : launch_variant<2, false>(job, tiles, num_sms, s);
-    else
-        e = job.wgrad ? launch_variant<1, true>(job, tiles, num_sms, s) : launch_variant<1, false>(job, tiles, num_sms, s);
+    const int e = job.wgrad ? launch_variant<true>(job, tiles, num_sms, s) : launch_variant<false>(job, tiles, num_sms, s);
     if (e != cudaSuccess || job.split <= 1) return e;
     const long long elems = static_cast<long long>(job.rows) * job.N;
     return by_dtype(job.out_dtype, [&](auto t) {

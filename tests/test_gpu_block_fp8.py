@@ -152,8 +152,8 @@ def test_products(gns, out, tokens, n, k):
                 "e5m2" if k % 2 else "e4m3")
 
 
-def test_products_on_cta_pairs(gns):
-    """Enough tiles for pairs of CTAs in all three products, ragged at every edge."""
+def test_products_of_many_tiles(gns):
+    """More tiles than SMs in all three products, ragged at every edge."""
     rng = np.random.default_rng(1)
     check_dense(gns, loud(2300, 2190, 0, torch.bfloat16, rng), loud(2420, 2190, 0, torch.bfloat16, rng),
                 loud(2300, 2420, 0, torch.bfloat16, rng), torch.float32)
