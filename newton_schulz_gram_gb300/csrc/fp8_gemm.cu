@@ -17,6 +17,9 @@
 //              i & 1 (256 columns each)
 //   warp 2     scale producer: cp.async of a k block's row and column scales
 //              into a ring of shared-memory slots, several blocks ahead
+//   warp 3     scheduler: decodes the CTA's tiles ahead of their use (the
+//              divisions and the search for a tile's group took the other
+//              roles 2200 cycles per tile) into a ring of records
 //   warps 4-11 epilogue: lane quarter warp & 3, columns 128 ((warp - 4) >> 2)
 //              to + 127 of the tile, 128 accumulators per thread. The first
 //              warpgroup gives registers up for them: 40 + 2 x 232 per lane of
@@ -65,7 +68,21 @@ constexpr int kScaleFloats = WGRAD ? BM + BN : BM + 4;
 template <bool WGRAD>
 constexpr int kSlotFloats = kSlotBlocks * kScaleFloats<WGRAD>;
 
-constexpr int kNumBars = 2 * STAGES + 5 + 2 * kScaleSlots;
+constexpr int kTileSlots = 4;
+constexpr int kTileReaders = 3 + kEpiWarps;  // producer, MMA issuer, scale producer, epilogue warps
+
+constexpr int kNumBars = 2 * STAGES + 5 + 2 * kScaleSlots + 2 * kTileSlots;
+
+// A tile as the roles see it.
+struct Tile {
+    int g;         // group; G: the rows past the last group (all zero); -1: no more tiles
+    int m0, n0;    // origin: row within the group (weight gradient: row of D), column
+    int kb0, kb1;  // k blocks
+    int split;
+    int row0;      // first row of the group in A and D (0 for the weight gradient)
+    int rows;      // rows of the group (weight gradient: of D)
+};
+static_assert(sizeof(Tile) == 32, "read as two 16-byte pieces");
 
 struct Groups {
     int offs[kMaxExperts + 2];  // first row of each group; offs[G + 1]: all rows
@@ -73,7 +90,7 @@ struct Groups {
 };
 
 constexpr int kSmemBytes = 1024 + STAGES * static_cast<int>(A_BYTES + B_BYTES) + kScaleSlots * kSlotFloats<true> * 4 +
-                           kEpiWarps * kStageBytes + kNumBars * 8 + 16 + static_cast<int>(sizeof(Groups));
+                           kEpiWarps * kStageBytes + kTileSlots * static_cast<int>(sizeof(Tile)) + kNumBars * 8 + 16 + static_cast<int>(sizeof(Groups));
 static_assert(kSmemBytes <= 232448, "shared memory budget");
 
 __device__ __forceinline__ void tc_mma_f8(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
@@ -153,16 +170,9 @@ __device__ __forceinline__ float ld_shared_f32(uint32_t addr) {
     return v;
 }
 
-struct Tile {
-    int g;          // group; G: the rows past the last group (all zero)
-    int m0, n0;     // origin: row within the group (weight gradient: row of D), column
-    int kb0, kb1;   // k blocks
-    int split;
-};
-
-// What every role needs to walk the tiles.
+// What the scheduler needs to decode tiles.
 struct Walk {
-    int G, ntn, mtn, split, wgrad, total_kb, units;
+    int G, M, ntn, mtn, split, wgrad, total_kb;
     const Groups* gr;
 };
 
@@ -207,6 +217,8 @@ __device__ __forceinline__ Tile decode(const Walk& w, int t) {
         tl.kb0 = static_cast<int>(static_cast<long long>(w.total_kb) * tl.split / w.split);
         tl.kb1 = static_cast<int>(static_cast<long long>(w.total_kb) * (tl.split + 1) / w.split);
     }
+    tl.row0 = w.wgrad ? 0 : w.gr->offs[tl.g];
+    tl.rows = w.wgrad ? w.M : w.gr->offs[tl.g + 1] - tl.row0;
     return tl;
 }
 
@@ -258,10 +270,16 @@ __device__ __forceinline__ void store_tile(uint32_t stage, uint8_t* d, long long
         uint8_t* dp = d + static_cast<long long>(p) * kStageRow;
         if (aligned) {
             const int k = lane & 7, r0 = lane >> 3;
+            uint4 piece[8];  // all reads first: each takes some 200 cycles beside the MMAs
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
                 const int r = 4 * j + r0;
-                const uint4 v = ld_shared_v4(stage + r * kStageRow + ((k ^ (r & 7)) << 4));
+                piece[j] = ld_shared_v4(stage + r * kStageRow + ((k ^ (r & 7)) << 4));
+            }
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                const int r = 4 * j + r0;
+                const uint4 v = piece[j];
                 uint8_t* a = dp + r * ldd * ES + 16 * k;
                 if (r < rows) {
                     if ((k + 1) * PIECE <= left) {
@@ -305,7 +323,8 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_gemm_kernel(const __grid_cons
     uint8_t* sB = sA + STAGES * A_BYTES;
     float* scales = reinterpret_cast<float*>(sB + STAGES * B_BYTES);
     uint8_t* staging = reinterpret_cast<uint8_t*>(scales + kScaleSlots * kSlotFloats<true>);
-    uint64_t* bars = reinterpret_cast<uint64_t*>(staging + kEpiWarps * kStageBytes);
+    Tile* tiles = reinterpret_cast<Tile*>(staging + kEpiWarps * kStageBytes);
+    uint64_t* bars = reinterpret_cast<uint64_t*>(tiles + kTileSlots);
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + kNumBars);
     Groups* gr = reinterpret_cast<Groups*>(tmem_slot + 4);
 
@@ -316,6 +335,8 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_gemm_kernel(const __grid_cons
     const uint32_t drain_bar = smem_u32(bars + 2 * STAGES + 4);
     const uint32_t sfull0 = smem_u32(bars + 2 * STAGES + 5);
     const uint32_t sempty0 = sfull0 + 8 * kScaleSlots;
+    const uint32_t tfull0 = sempty0 + 8 * kScaleSlots;
+    const uint32_t tempty0 = tfull0 + 8 * kTileSlots;
 
     const int warp = threadIdx.x >> 5;
     const int lane = threadIdx.x & 31;
@@ -334,6 +355,10 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_gemm_kernel(const __grid_cons
         for (int b = 0; b < kScaleSlots; ++b) {
             mbar_init(sfull0 + 8 * b, 32);
             mbar_init(sempty0 + 8 * b, kEpiWarps);
+        }
+        for (int b = 0; b < kTileSlots; ++b) {
+            mbar_init(tfull0 + 8 * b, 1);
+            mbar_init(tempty0 + 8 * b, kTileReaders);
         }
         fence_mbar_init();
         prefetch_tmap(&P.mapA);
@@ -389,16 +414,22 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_gemm_kernel(const __grid_cons
     tc_fence_after();
     const uint32_t tmem_base = *tmem_slot;
 
-    Walk w;
-    w.G = G;
-    w.ntn = (P.N + BN - 1) / BN;
-    w.mtn = WGRAD ? (P.M + BM - 1) / BM : 0;
-    w.split = P.split;
-    w.wgrad = WGRAD;
-    w.total_kb = WGRAD ? 0 : (P.K + BK - 1) / BK;
-    w.gr = gr;
-    const int total = WGRAD ? G * w.mtn * w.ntn : gr->pre[G + 1] * w.ntn * P.split;
-    const int first = static_cast<int>(blockIdx.x), stride = static_cast<int>(gridDim.x);
+    // The CTA's i-th tile, from ring slot i mod kTileSlots; false after the
+    // last one or when a wait gave up. Called by a thread or by whole warps.
+    const uint32_t tiles_u32 = smem_u32(tiles);
+    auto take = [&](int i, Tile& tl, bool whole_warp) -> bool {
+        const int slot = i % kTileSlots;
+        bool got = mbar_wait_here(tfull0 + 8 * slot, (i / kTileSlots) & 1, err);
+        if (whole_warp) got = __all_sync(0xffffffffu, got);
+        if (!got) return false;
+        const uint32_t at = tiles_u32 + slot * static_cast<uint32_t>(sizeof(Tile));
+        const uint4 a = ld_shared_v4(at), b = ld_shared_v4(at + 16);
+        tl = Tile{static_cast<int>(a.x), static_cast<int>(a.y), static_cast<int>(a.z), static_cast<int>(a.w),
+                  static_cast<int>(b.x), static_cast<int>(b.y), static_cast<int>(b.z), static_cast<int>(b.w)};
+        if (whole_warp) __syncwarp();
+        if (!whole_warp || lane == 0) mbar_arrive(tempty0 + 8 * slot);
+        return tl.g >= 0;
+    };
     const bool a_mn = WGRAD, b_mn = WGRAD || P.b_mn;
 
     if (warp < kEpiWarp0) {
@@ -409,9 +440,9 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_gemm_kernel(const __grid_cons
                 uint32_t stage = 0, phase = 0;
                 int issued = 0;
                 bool ok = true;
-                for (int t = first; ok && t < total; t += stride) {
-                    const Tile tl = decode(w, t);
-                    const int arow = (WGRAD ? 0 : gr->offs[tl.g]) + tl.m0;
+                Tile tl;
+                for (int i = 0; ok && take(i, tl, false); ++i) {
+                    const int arow = tl.row0 + tl.m0;
                     const int gb = WGRAD ? 0 : tl.g;
                     for (int kb = tl.kb0; kb < tl.kb1; ++kb) {
                         if (!mbar_wait(empty0 + 8 * stage, phase ^ 1, err)) {
@@ -462,8 +493,8 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_gemm_kernel(const __grid_cons
                 // A 32-wide k step: 32 bytes along a K-major row, or 32 rows of an MN-major tile.
                 const uint32_t a_step = a_mn ? (4096 >> 4) : (32 >> 4);
                 const uint32_t b_step = b_mn ? (4096 >> 4) : (32 >> 4);
-                for (int t = first; ok && t < total; t += stride) {
-                    const Tile tl = decode(w, t);
+                Tile tl;
+                for (int i = 0; ok && take(i, tl, false); ++i) {
                     for (int kb = tl.kb0; kb < tl.kb1; ++kb, ++it) {
                         const int buf = it & 1;
                         if (!mbar_wait(acce0 + 8 * buf, ((it >> 1) & 1) ^ 1, err) ||
@@ -496,11 +527,10 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_gemm_kernel(const __grid_cons
             int slot = 0;
             uint32_t phase = 0;
             bool ok = true;
-            for (int t = first; ok && t < total; t += stride) {
-                const Tile tl = decode(w, t);
+            Tile tl;
+            for (int i = 0; ok && take(i, tl, true); ++i) {
                 const int local = tl.m0 + lane;
-                const int rows = WGRAD ? P.M : gr->offs[tl.g + 1] - gr->offs[tl.g];
-                const float* pa = P.sA + (WGRAD ? 0 : gr->offs[tl.g]) + local;
+                const float* pa = P.sA + tl.row0 + local;
                 const float* pb = P.sB + (WGRAD ? tl.n0 + 4 * lane
                                                 : tl.g * P.sB_g + static_cast<long long>(tl.n0 / kFp8Block + lane) * P.sB_n);
                 for (int kb0 = tl.kb0; kb0 < tl.kb1; kb0 += kSlotBlocks) {
@@ -513,7 +543,7 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_gemm_kernel(const __grid_cons
                         const uint32_t dst = ring + 4 * (slot * kSlotFloats<WGRAD> + (kb - kb0) * kScaleFloats<WGRAD>);
 #pragma unroll
                         for (int i = 0; i < 4; ++i)
-                            copy_async<4>(dst + 4 * (lane + 32 * i), pa + kb * P.ldsA + 32 * i, local + 32 * i < rows, P.sA);
+                            copy_async<4>(dst + 4 * (lane + 32 * i), pa + kb * P.ldsA + 32 * i, local + 32 * i < tl.rows, P.sA);
                         if constexpr (WGRAD) {
 #pragma unroll
                             for (int i = 0; i < 2; ++i)
@@ -532,7 +562,33 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_gemm_kernel(const __grid_cons
             }
             asm volatile("cp.async.wait_all;" ::: "memory");
             __syncwarp();
+        } else if (lane == 0) {
+            // ---------------------------------------------------- scheduler
+            Walk w;
+            w.G = G;
+            w.M = P.M;
+            w.ntn = (P.N + BN - 1) / BN;
+            w.mtn = WGRAD ? (P.M + BM - 1) / BM : 0;
+            w.split = P.split;
+            w.wgrad = WGRAD;
+            w.total_kb = WGRAD ? 0 : (P.K + BK - 1) / BK;
+            w.gr = gr;
+            const int total = WGRAD ? G * w.mtn * w.ntn : gr->pre[G + 1] * w.ntn * P.split;
+            int t = static_cast<int>(blockIdx.x);
+            for (int i = 0;; ++i, t += static_cast<int>(gridDim.x)) {
+                Tile tl{};
+                tl.g = -1;
+                if (t < total) tl = decode(w, t);
+                const int slot = i % kTileSlots;
+                if (!mbar_wait(tempty0 + 8 * slot, ((i / kTileSlots) & 1) ^ 1, err)) break;
+                const uint32_t at = tiles_u32 + slot * static_cast<uint32_t>(sizeof(Tile));
+                st_shared_v4(at, tl.g, tl.m0, tl.n0, tl.kb0);
+                st_shared_v4(at + 16, tl.kb1, tl.split, tl.row0, tl.rows);
+                mbar_arrive(tfull0 + 8 * slot);
+                if (tl.g < 0) break;
+            }
         }
+        __syncwarp();
     } else {
         // ---------------------------------------------------------- epilogue
         asm volatile("setmaxnreg.inc.sync.aligned.u32 232;");
@@ -545,9 +601,8 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_gemm_kernel(const __grid_cons
         int slot = 0;  // scale slot and its phase
         uint32_t sphase = 0;
         bool ok = true;
-        for (int t = first; ok && t < total; t += stride) {
-            const Tile tl = decode(w, t);
-            const int rows = WGRAD ? P.M : gr->offs[tl.g + 1] - gr->offs[tl.g];
+        Tile tl;
+        for (int i = 0; ok && take(i, tl, true); ++i) {
             const int col = tl.n0 + cq;
             float acc[kCols];
 #pragma unroll
@@ -617,11 +672,11 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_gemm_kernel(const __grid_cons
             }
             if (!ok) break;
             // Rows of this warp inside the group (of D) and columns inside D.
-            const int wrows = rows - tl.m0 - q * 32, ncol = P.N - col;
+            const int wrows = tl.rows - tl.m0 - q * 32, ncol = P.N - col;
             if (wrows <= 0 || ncol <= 0) continue;
             const int es = P.out_dtype == GNS_FP32 || P.split > 1 ? 4 : 2;
             const uint32_t stage = smem_u32(staging + ew * kStageBytes);
-            const long long row0 = (WGRAD ? 0 : gr->offs[tl.g]) + tl.m0 + q * 32;
+            const long long row0 = tl.row0 + tl.m0 + q * 32;
             uint8_t* d;
             long long ldd;
             bool aligned;
