@@ -78,9 +78,10 @@ int product(const void* a, int64_t lda, const float* sa, int64_t ld_sa, int fmt_
     if (ld_sa < rows) return invalid("a scale's row stride must cover the rows");
     if (ldd < out) return invalid("the output's row stride must cover its columns");
     Fp8GemmJob j{};
+    const int cg = fp8_gemm_cg(rows, out, groups, offsets != nullptr, st->num_sms);
     j.split = offsets ? 1 : fp8_gemm_split(rows, out, inner, st->num_sms);
     RET(map_u8(&j.mapA, a, inner, rows, 1, lda, lda * rows, 128));
-    RET(map_u8(&j.mapB, w, K, N, groups, ldw, ldw * N, fp8_gemm_b_box(dgrad)));
+    RET(map_u8(&j.mapB, w, K, N, groups, ldw, ldw * N, fp8_gemm_b_box(cg, dgrad)));
     j.b_mn = dgrad;
     j.fmt_a = fmt_a;
     j.fmt_b = fmt_w;
@@ -105,7 +106,7 @@ int product(const void* a, int64_t lda, const float* sa, int64_t ld_sa, int fmt_
     }
     begin_call(*st);
     j.st = st->status;
-    LAUNCH(kClsFp8Gemm, launch_fp8_gemm(j, st->num_sms, s));
+    LAUNCH(kClsFp8Gemm, launch_fp8_gemm(j, cg, st->num_sms, s));
     return GNS_OK;
 }
 
@@ -333,6 +334,7 @@ int gns_fp8_matmul_wgrad(const void* dy, int64_t lddy, const float* scale_dy, in
             return invalid("column scales need 16-byte aligned rows that cover the columns");
     Fp8GemmJob j{};
     const int64_t qrows = offsets ? static_cast<int64_t>(fp8_max_blocks(rows, groups)) * kFp8Block : up(rows, kFp8Block);
+    const int cg = fp8_gemm_cg(N, K, groups, false, st->num_sms);
     RET(map_u8(&j.mapA, dy, N, qrows, 1, lddy, lddy * qrows, 128));
     RET(map_u8(&j.mapB, x, K, qrows, 1, ldx, ldx * qrows, 128));
     j.wgrad = 1;
@@ -355,7 +357,7 @@ int gns_fp8_matmul_wgrad(const void* dy, int64_t lddy, const float* scale_dy, in
     j.split = 1;
     begin_call(*st);
     j.st = st->status;
-    LAUNCH(kClsFp8Gemm, launch_fp8_gemm(j, st->num_sms, s));
+    LAUNCH(kClsFp8Gemm, launch_fp8_gemm(j, cg, st->num_sms, s));
     return GNS_OK;
 }
 

@@ -81,10 +81,13 @@ struct Fp8GemmJob {
     DevStatus st;
 };
 
+// CTAs per tile (1: 128 x 256 tiles, 2: a pair, 256 x 256) for a product with M
+// rows (of all groups; the weight gradient: of each D) and N columns.
+int fp8_gemm_cg(int M, int N, int G, bool grouped, int num_sms);
 // Rows of the boxes of B's tensor map.
-inline int fp8_gemm_b_box(bool b_mn) { return b_mn ? 128 : 256; }
+inline int fp8_gemm_b_box(int cg, bool b_mn) { return b_mn || cg == 2 ? 128 : 256; }
 
-int launch_fp8_gemm(const Fp8GemmJob& job, int num_sms, cudaStream_t s);
+int launch_fp8_gemm(const Fp8GemmJob& job, int cg, int num_sms, cudaStream_t s);
 
 // The split of the contraction that fills the machine, 1 for none.
 int fp8_gemm_split(int rows, int N, int K, int num_sms);

@@ -4,34 +4,39 @@
 //
 //   D[m][n] = sum over k blocks b of  sA(m, b) sB(n, b) sum_{k in b} A[m][k] B[n][k]
 //
-// with blocks of 128 along the contraction. The tensor core sums one block's
-// 128 products in fp32 (kind::f8f6f4, TMEM); the epilogue warps then add
-// sA sB times that partial sum to fp32 accumulators in registers. A block is
-// 512 cycles of MMA for a 128 x 256 tile; the epilogue's share of it (TMEM
-// reads 256 cycles, scaled adds 256 per scheduler) has to run beside the next
-// block's MMAs, which write the other half of TMEM.
+// with blocks of 128 along the contraction and power-of-two scales. The tensor
+// core applies the scales itself (kind::mxf8f6f4, block_scale): it takes one
+// 8-bit exponent per row of A and of B and 32-wide k step, so a block of 128 is
+// four steps with the same exponent, and the sum stays in TMEM in fp32. That
+// accumulator truncates, an error that grows with the steps (at a contraction
+// of 4096 up to 2.9e-6 of the result, far below a 16-bit result's rounding), so
+// fp32 results are summed in segments of kSegment blocks, each segment added to
+// the stored result with one rounding (6e-7 at any length).
+// Applying the scales in registers instead, which any fp32 scale would need,
+// reads the accumulator once per block: 1220 cycles per block beside the 512 of
+// its MMAs (8192 x 14336 x 4096 forward: 470 us, with scaled MMAs 378).
 //
-// One CTA per SM walks 128 x 256 tiles with a static stride. Warp roles:
+// One CTA (CG = 1, 128 x 256 tiles) or a pair (CG = 2, 256 x 256 tiles, paired
+// MMAs; each CTA stages 128 rows of each operand) per SM (pair) walks the tiles
+// with a static stride. Warp roles:
 //   warp 0     TMA producer of 128-byte-wide k blocks (128-byte swizzle)
-//   warp 1     TMEM owner, MMA issuer; k block i goes to accumulator buffer
-//              i & 1 (256 columns each)
-//   warp 2     scale producer: cp.async of a k block's row and column scales
-//              into a ring of shared-memory slots, several blocks ahead
-//   warp 3     scheduler: decodes the CTA's tiles ahead of their use (the
-//              divisions and the search for a tile's group took the other
-//              roles 2200 cycles per tile) into a ring of records
-//   warps 4-11 epilogue: lane quarter warp & 3, columns 128 ((warp - 4) >> 2)
-//              to + 127 of the tile, 128 accumulators per thread. The first
-//              warpgroup gives registers up for them: 40 + 2 x 232 per lane of
-//              the 3 x 168 the block is launched with.
-// Measured and left: CTA pairs (256 x 256 tiles, paired MMAs) load a third less
-// from L2, but their accumulator hand-shake crosses CTAs once per block
-// (8192 x 14336 x 4096 forward: 954 us against 551); sixteen epilogue warps of
-// 64 columns hide no more latency than eight (598 us).
+//   warp 1     TMEM owner, MMA issuer (the pair's leader)
+//   warp 2     scheduler: decodes the CTA's tiles ahead of their use (the
+//              divisions and the search for a tile's group take some 2000
+//              cycles) into a ring of records
+//   warps 4-7  scale builders: a slot holds four k blocks' exponents, one
+//              32-bit word per row in the order tcgen05.cp spreads over TMEM;
+//              warp 4 + j writes byte j
+//   warps 8-15 epilogue: lane quarter warp & 3, column half (warp - 8) >> 2
+// TMEM: two accumulators of 256 columns that overlap by the 24 columns the
+// scales take, so the next tile's MMAs wait for the chunk of 32 columns in the
+// overlap to be read (the first thing the epilogue does) and run beside the
+// rest of the epilogue.
 // Operands whose contraction runs along the stored rows (the weights of the
 // data gradient, both operands of the weight gradient) are read MN-major
 // through the shared-memory descriptor; nothing is transposed in memory.
 #include <algorithm>
+#include <cstdlib>
 
 #include "blockops.cuh"
 #include "fp8.cuh"
@@ -45,33 +50,47 @@ constexpr int BM = 128;
 constexpr int BN = 256;
 constexpr int BK = kFp8Block;
 constexpr int kEpiWarps = 8;
-constexpr int kEpiWarp0 = 4;
+constexpr int kBuildWarp0 = 4;
+constexpr int kEpiWarp0 = 8;
 constexpr int kCols = 128;  // columns of an epilogue warp
 constexpr int kThreads = 32 * (kEpiWarp0 + kEpiWarps);
 constexpr int kBand = 16;  // tile rows walked together (their A stays in L2 while the columns pass)
-constexpr uint32_t kTmemCols = 2 * BN;
 constexpr uint32_t A_BYTES = BM * BK;
-constexpr uint32_t B_BYTES = BN * BK;
 constexpr uint32_t kBoxBytes = 128 * 128;
-constexpr int STAGES = 3;
-constexpr int kStageRow = 128;                    // bytes of a row staged for the output stores
-constexpr int kStageBytes = 32 * kStageRow;        // per epilogue warp
 
-// A scale slot holds kSlotBlocks k blocks' scales, for each the 128 row scales
-// and then its two column-half scales, or 256 column scales (weight gradient).
-// One barrier wait per k block costs the epilogue about 150 cycles of the 800
-// it has; a slot of four shares it.
-constexpr int kScaleSlots = 3;
+// TMEM columns: accumulator 0 at 0, accumulator 1 at kAcc1, two scale slots of
+// 4 columns for A's 128 rows and 8 for B's 256.
+constexpr uint32_t kTmemCols = 512;
+constexpr uint32_t kScaleCols = 12;
+constexpr uint32_t kScaleTmem = kTmemCols - 2 * kScaleCols;
+constexpr uint32_t kAcc1 = kScaleTmem - BN;
+static_assert(BN - kAcc1 <= 32, "the overlap lies in one chunk of 32 columns of either accumulator");
+
+// CG = 1: a CTA computes 128 x 256 tiles. CG = 2: a pair of CTAs computes 256 x
+// 256 tiles with paired MMAs; each stages its 128 rows of A and 128 of B's 256.
+template <int CG>
+struct Cfg {
+    static constexpr int STAGES = CG == 1 ? 3 : 5;
+    static constexpr int BNH = BN / CG;  // rows of B a CTA stages
+    static constexpr uint32_t B_BYTES = BNH * BK;
+    static constexpr int TM = BM * CG;
+};
+
+// A scale slot in shared memory: 512 bytes for A's 128 rows and 1024 for B's
+// 256. Row r of 128 is the word at 16 (r mod 32) + 4 (r / 32); its byte j is the
+// exponent of the slot's j-th k block.
+constexpr int kScaleSlots = 2;
 constexpr int kSlotBlocks = 4;
-template <bool WGRAD>
-constexpr int kScaleFloats = WGRAD ? BM + BN : BM + 4;
-template <bool WGRAD>
-constexpr int kSlotFloats = kSlotBlocks * kScaleFloats<WGRAD>;
+constexpr uint32_t kSlotBytes = 512 + 1024;
+constexpr int kSegment = 16;  // k blocks of a segment of an fp32 result
+static_assert(kSegment % kSlotBlocks == 0, "a scale slot lies in one segment");
+constexpr int kStageRow = 128;               // bytes of a row staged for the output stores
+constexpr int kStageBytes = 32 * kStageRow;  // per epilogue warp
 
 constexpr int kTileSlots = 4;
-constexpr int kTileReaders = 3 + kEpiWarps;  // producer, MMA issuer, scale producer, epilogue warps
+constexpr int kTileReaders = 2 + kSlotBlocks + kEpiWarps;  // producer, MMA issuer, scale builder, epilogue warps
 
-constexpr int kNumBars = 2 * STAGES + 5 + 2 * kScaleSlots + 2 * kTileSlots;
+__host__ __device__ constexpr int num_bars(int stages) { return 2 * stages + 6 + 2 * kScaleSlots + 2 * kTileSlots; }
 
 // A tile as the roles see it.
 struct Tile {
@@ -89,31 +108,66 @@ struct Groups {
     int pre[kMaxExperts + 2];   // tile rows (weight gradient: token blocks) of the groups before
 };
 
-constexpr int kSmemBytes = 1024 + STAGES * static_cast<int>(A_BYTES + B_BYTES) + kScaleSlots * kSlotFloats<true> * 4 +
-                           kEpiWarps * kStageBytes + kTileSlots * static_cast<int>(sizeof(Tile)) + kNumBars * 8 + 16 + static_cast<int>(sizeof(Groups));
-static_assert(kSmemBytes <= 232448, "shared memory budget");
+template <int CG>
+constexpr int smem_bytes() {
+    return 1024 + Cfg<CG>::STAGES * static_cast<int>(A_BYTES + Cfg<CG>::B_BYTES) + kScaleSlots * static_cast<int>(kSlotBytes) +
+           kEpiWarps * kStageBytes + kTileSlots * static_cast<int>(sizeof(Tile)) + num_bars(Cfg<CG>::STAGES) * 8 + 16 +
+           static_cast<int>(sizeof(Groups));
+}
+static_assert(smem_bytes<1>() <= 232448 && smem_bytes<2>() <= 232448, "shared memory budget");
 
-__device__ __forceinline__ void tc_mma_f8(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
-                                          uint32_t accumulate) {
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "setp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
-        "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
-        : "memory");
+// D(tmem) (+)= A(smem) * B(smem)^T with the exponents of the rows of A and B
+// at the TMEM addresses sfa and sfb (the byte idesc names).
+template <int CG>
+__device__ __forceinline__ void tc_mma_mx(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc, uint32_t sfa,
+                                          uint32_t sfb, uint32_t accumulate) {
+    if constexpr (CG == 1)
+        asm volatile(
+            "{\n\t.reg .pred p;\n\t"
+            "setp.ne.b32 p, %4, 0;\n\t"
+            "tcgen05.mma.cta_group::1.kind::mxf8f6f4.block_scale.scale_vec::1X [%0], %1, %2, %3, [%5], [%6], p;\n\t}" ::"r"(
+                d_tmem),
+            "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate), "r"(sfa), "r"(sfb)
+            : "memory");
+    else
+        asm volatile(
+            "{\n\t.reg .pred p;\n\t"
+            "setp.ne.b32 p, %4, 0;\n\t"
+            "tcgen05.mma.cta_group::2.kind::mxf8f6f4.block_scale.scale_vec::1X [%0], %1, %2, %3, [%5], [%6], p;\n\t}" ::"r"(
+                d_tmem),
+            "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate), "r"(sfa), "r"(sfb)
+            : "memory");
 }
 
-// Instruction descriptor of kind::f8f6f4, fp32 accumulator.
-__device__ __forceinline__ uint32_t idesc_f8(int M, int N, int fmt_a, int fmt_b, uint32_t a_mn, uint32_t b_mn) {
-    return (1u << 4)                                  // D format: f32
-           | (static_cast<uint32_t>(fmt_a) << 7)      // 0: e4m3, 1: e5m2
-           | (static_cast<uint32_t>(fmt_b) << 10)
-           | (a_mn << 15) | (b_mn << 16)
-           | (static_cast<uint32_t>(N >> 3) << 17) | (static_cast<uint32_t>(M >> 4) << 24);
+// Instruction descriptor of kind::mxf8f6f4 with 8-bit exponents as scales; the
+// byte of the scale words is added per k block (scale_id).
+__device__ __forceinline__ uint32_t idesc_mx(int M, int N, int fmt_a, int fmt_b, uint32_t a_mn, uint32_t b_mn) {
+    return (static_cast<uint32_t>(fmt_a) << 7)  // 0: e4m3, 1: e5m2
+           | (static_cast<uint32_t>(fmt_b) << 10) | (a_mn << 15) | (b_mn << 16) | (static_cast<uint32_t>(N >> 3) << 17) |
+           (1u << 23)  // scale type: 8-bit exponent
+           | (static_cast<uint32_t>(M >> 7) << 27);
+}
+__device__ __forceinline__ uint32_t scale_id(uint32_t byte) { return (byte << 4) | (byte << 29); }
+
+__device__ __forceinline__ void st_shared_u8(uint32_t addr, uint32_t v) {
+    asm volatile("st.shared.u8 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
 }
 
-// mbar_wait with its bounded spin inline: a call in the epilogue's loop would
-// have the 128 accumulators saved around it.
+// 512 bytes of scale words (32 rows of 16 bytes, contiguous) from shared memory
+// to four TMEM columns of each lane quarter.
+template <int CG>
+__device__ __forceinline__ void tc_copy_scales(uint32_t tmem, uint32_t smem_addr) {
+    uint64_t d = 0;
+    d |= static_cast<uint64_t>((smem_addr & 0x3FFFFu) >> 4);  // start address
+    d |= static_cast<uint64_t>(128 >> 4) << 32;               // stride byte offset: 8 rows of 16 bytes
+    d |= static_cast<uint64_t>(1) << 46;                       // descriptor version; no swizzle
+    if constexpr (CG == 1)
+        asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(tmem), "l"(d) : "memory");
+    else
+        asm volatile("tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;" ::"r"(tmem), "l"(d) : "memory");
+}
+
+// mbar_wait with its bounded spin inline.
 __device__ __forceinline__ bool mbar_wait_here(uint32_t bar, uint32_t parity, const DevStatus& st) {
     if (mbar_try_wait(bar, parity)) return true;
     const uint64_t t0 = globaltimer();
@@ -127,17 +181,10 @@ __device__ __forceinline__ bool mbar_wait_here(uint32_t bar, uint32_t parity, co
     return true;
 }
 
-// Whether the phase is complete, without waiting.
-__device__ __forceinline__ bool mbar_test(uint32_t bar, uint32_t parity) {
-    uint32_t ok;
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
-        "selp.u32 %0, 1, 0, p;\n\t}"
-        : "=r"(ok)
-        : "r"(bar), "r"(parity)
-        : "memory");
-    return ok != 0;
+__device__ __forceinline__ float ld_shared_f32(uint32_t addr) {
+    float v;
+    asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
+    return v;
 }
 
 // tcgen05.wait::ld that the uses of v depend on.
@@ -152,30 +199,13 @@ __device__ __forceinline__ void tmem_ld_wait_for(uint32_t (&v)[32]) {
         : "memory");
 }
 
-// BYTES from global to shared memory, zeros where `in` is false (then `safe`,
-// which is not read, stands for the address).
-template <int BYTES>
-__device__ __forceinline__ void copy_async(uint32_t dst, const float* src, bool in, const float* safe) {
-    const int n = in ? BYTES : 0;
-    const float* p = in ? src : safe;
-    if constexpr (BYTES == 16)
-        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(p), "r"(n) : "memory");
-    else
-        asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(p), "r"(n) : "memory");
-}
-
-__device__ __forceinline__ float ld_shared_f32(uint32_t addr) {
-    float v;
-    asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
-    return v;
-}
-
 // What the scheduler needs to decode tiles.
 struct Walk {
     int G, M, ntn, mtn, split, wgrad, total_kb;
     const Groups* gr;
 };
 
+template <int CG>
 __device__ __forceinline__ Tile decode(const Walk& w, int t) {
     Tile tl;
     tl.split = 0;
@@ -207,7 +237,7 @@ __device__ __forceinline__ Tile decode(const Walk& w, int t) {
     const int h = min(kBand, rows - band * kBand);
     const int nt = rem / h;
     tl.n0 = nt * BN;
-    tl.m0 = (band * kBand + rem - nt * h) * BM;
+    tl.m0 = (band * kBand + rem - nt * h) * Cfg<CG>::TM;
     if (w.wgrad) {
         tl.kb0 = w.gr->pre[tl.g];
         tl.kb1 = w.gr->pre[tl.g + 1];
@@ -238,102 +268,120 @@ __device__ __forceinline__ uint32_t pack_pair(float lo, float hi, bool bf16) {
     return pack_half2(lo, hi);
 }
 
-// The warp's 32 rows x kCols columns (a thread holds one row), clipped to
-// rows x ncol, to d (row stride ldd elements of ES bytes). Rows go through
-// shared memory, 128 bytes of each at a time (16-byte pieces, piece index XOR
-// row mod 8), so that a store instruction writes four whole 128-byte lines
-// where rows start on 16-byte boundaries, and runs of neighbouring elements
-// where they do not. Straight from the registers a store would touch 32 rows:
-// a 128 x 256 tile took 4000 cycles that way.
-template <int ES>
-__device__ __forceinline__ void store_tile(uint32_t stage, uint8_t* d, long long ldd, int rows, int ncol,
-                                           const float (&acc)[kCols], bool bf16, bool aligned, int lane) {
-    constexpr int PASS = kStageRow / ES;  // columns per pass
-    constexpr int PIECE = 16 / ES;        // elements of a 16-byte piece
-#pragma unroll
-    for (int p = 0; p < kCols / PASS; ++p) {
-        const int left = ncol - p * PASS;  // columns from here on
-        if (left <= 0) break;
-#pragma unroll
-        for (int k = 0; k < 8; ++k) {
-            uint32_t w[4];
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                if constexpr (ES == 2)
-                    w[e] = pack_pair(acc[p * PASS + 8 * k + 2 * e], acc[p * PASS + 8 * k + 2 * e + 1], bf16);
-                else
-                    w[e] = __float_as_uint(acc[p * PASS + 4 * k + e]);
-            }
-            st_shared_v4(stage + lane * kStageRow + ((k ^ (lane & 7)) << 4), w[0], w[1], w[2], w[3]);
-        }
-        __syncwarp();
-        uint8_t* dp = d + static_cast<long long>(p) * kStageRow;
-        if (aligned) {
-            const int k = lane & 7, r0 = lane >> 3;
-            uint4 piece[8];  // all reads first: each takes some 200 cycles beside the MMAs
-#pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                const int r = 4 * j + r0;
-                piece[j] = ld_shared_v4(stage + r * kStageRow + ((k ^ (r & 7)) << 4));
-            }
-#pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                const int r = 4 * j + r0;
-                const uint4 v = piece[j];
-                uint8_t* a = dp + r * ldd * ES + 16 * k;
-                if (r < rows) {
-                    if ((k + 1) * PIECE <= left) {
-                        *reinterpret_cast<uint4*>(a) = v;
-                    } else {
-                        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-                        for (int e = 0; e < PIECE; ++e) {
-                            if (k * PIECE + e >= left) continue;
-                            if constexpr (ES == 2)
-                                reinterpret_cast<uint16_t*>(a)[e] = static_cast<uint16_t>(w[e / 2] >> (16 * (e & 1)));
-                            else
-                                reinterpret_cast<uint32_t*>(a)[e] = w[e];
-                        }
-                    }
-                }
-            }
-        } else {
-            for (int r = 0; r < min(rows, 32); ++r) {
-#pragma unroll
-                for (int c = lane; c < PASS; c += 32) {
-                    const uint32_t at = stage + r * kStageRow + (((c / PIECE) ^ (r & 7)) << 4) + (c % PIECE) * ES;
-                    if (c < left) {
-                        if constexpr (ES == 2)
-                            *reinterpret_cast<uint16_t*>(dp + r * ldd * ES + c * ES) = ld_shared_u16(at);
-                        else
-                            *reinterpret_cast<float*>(dp + r * ldd * ES + c * ES) = ld_shared_f32(at);
-                    }
-                }
-            }
-        }
-        __syncwarp();  // read before the next pass overwrites
-    }
+__device__ __forceinline__ uint32_t add_bits(uint32_t a, uint32_t b) {
+    return __float_as_uint(__uint_as_float(a) + __uint_as_float(b));
 }
 
-template <bool WGRAD>
+// 128 / ES columns of the warp's 32 rows (a thread holds one row), clipped to
+// rows x left, to d (row stride ldd elements of ES bytes). The rows
+// go through shared memory (16-byte pieces, piece index XOR row mod 8), so that
+// a store instruction writes four whole 128-byte lines where rows start on
+// 16-byte boundaries, and runs of neighbouring elements where they do not. With
+// `add` (fp32) the stored values are added to; a lane meets its own stores.
+template <int ES>
+__device__ __forceinline__ void store_pass(uint32_t stage, uint8_t* d, long long ldd, int rows, int left,
+                                           const uint32_t (&w)[32], bool aligned, bool add, int lane) {
+    constexpr int PASS = kStageRow / ES;  // columns
+    constexpr int PIECE = 16 / ES;        // elements of a 16-byte piece
+#pragma unroll
+    for (int k = 0; k < 8; ++k)
+        st_shared_v4(stage + lane * kStageRow + ((k ^ (lane & 7)) << 4), w[4 * k], w[4 * k + 1], w[4 * k + 2], w[4 * k + 3]);
+    __syncwarp();
+    if (aligned) {
+        const int k = lane & 7, r0 = lane >> 3;
+        uint4 piece[8];  // all reads first
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const int r = 4 * j + r0;
+            piece[j] = ld_shared_v4(stage + r * kStageRow + ((k ^ (r & 7)) << 4));
+        }
+        if (ES == 4 && add && (k + 1) * PIECE <= left) {
+            uint4 old[8];
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                const int r = 4 * j + r0;
+                old[j] = r < rows ? *reinterpret_cast<const uint4*>(d + r * ldd * ES + 16 * k) : make_uint4(0, 0, 0, 0);
+            }
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                piece[j].x = add_bits(old[j].x, piece[j].x);
+                piece[j].y = add_bits(old[j].y, piece[j].y);
+                piece[j].z = add_bits(old[j].z, piece[j].z);
+                piece[j].w = add_bits(old[j].w, piece[j].w);
+            }
+        }
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const int r = 4 * j + r0;
+            uint8_t* a = d + r * ldd * ES + 16 * k;
+            if (r >= rows) continue;
+            if ((k + 1) * PIECE <= left) {
+                *reinterpret_cast<uint4*>(a) = piece[j];
+            } else {
+                const uint32_t x[4] = {piece[j].x, piece[j].y, piece[j].z, piece[j].w};
+#pragma unroll
+                for (int e = 0; e < PIECE; ++e) {
+                    if (k * PIECE + e >= left) continue;
+                    if constexpr (ES == 2)
+                        reinterpret_cast<uint16_t*>(a)[e] = static_cast<uint16_t>(x[e / 2] >> (16 * (e & 1)));
+                    else
+                        reinterpret_cast<uint32_t*>(a)[e] = add ? add_bits(reinterpret_cast<uint32_t*>(a)[e], x[e]) : x[e];
+                }
+            }
+        }
+    } else {
+        for (int r = 0; r < min(rows, 32); ++r) {
+#pragma unroll
+            for (int c = lane; c < PASS; c += 32) {
+                const uint32_t at = stage + r * kStageRow + (((c / PIECE) ^ (r & 7)) << 4) + (c % PIECE) * ES;
+                if (c < left) {
+                    if constexpr (ES == 2)
+                        *reinterpret_cast<uint16_t*>(d + r * ldd * ES + c * ES) = ld_shared_u16(at);
+                    else {
+                        float* a = reinterpret_cast<float*>(d + r * ldd * ES + c * ES);
+                        const float v = ld_shared_f32(at);
+                        *a = add ? *a + v : v;
+                    }
+                }
+            }
+        }
+    }
+    __syncwarp();  // read before the next pass overwrites
+}
+
+// Hands accumulator columns back to the MMA issuer of the pair's leader. The
+// tcgen05.wait::ld before it has put their values into registers, so no memory
+// operation has to be ordered and the arrive is relaxed (one with
+// cluster-scope release would wait for the warp's global stores).
+__device__ __forceinline__ void mbar_arrive_relaxed(uint32_t cluster_addr) {
+    asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
+}
+
+template <int CG>
 __global__ void __launch_bounds__(kThreads, 1) fp8_gemm_kernel(const __grid_constant__ Fp8GemmJob P) {
+    constexpr int STAGES = Cfg<CG>::STAGES;
+    constexpr int TM = Cfg<CG>::TM;
+    constexpr int BNH = Cfg<CG>::BNH;
+    constexpr uint32_t B_BYTES = Cfg<CG>::B_BYTES;
+
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     uint8_t* sA = smem;
     uint8_t* sB = sA + STAGES * A_BYTES;
-    float* scales = reinterpret_cast<float*>(sB + STAGES * B_BYTES);
-    uint8_t* staging = reinterpret_cast<uint8_t*>(scales + kScaleSlots * kSlotFloats<true>);
+    uint8_t* scales = sB + STAGES * B_BYTES;
+    uint8_t* staging = scales + kScaleSlots * kSlotBytes;
     Tile* tiles = reinterpret_cast<Tile*>(staging + kEpiWarps * kStageBytes);
     uint64_t* bars = reinterpret_cast<uint64_t*>(tiles + kTileSlots);
-    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + kNumBars);
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + num_bars(STAGES));
     Groups* gr = reinterpret_cast<Groups*>(tmem_slot + 4);
 
     const uint32_t full0 = smem_u32(bars);
-    const uint32_t empty0 = smem_u32(bars + STAGES);
-    const uint32_t accf0 = smem_u32(bars + 2 * STAGES);
-    const uint32_t acce0 = smem_u32(bars + 2 * STAGES + 2);
-    const uint32_t drain_bar = smem_u32(bars + 2 * STAGES + 4);
-    const uint32_t sfull0 = smem_u32(bars + 2 * STAGES + 5);
+    const uint32_t empty0 = full0 + 8 * STAGES;
+    const uint32_t accf0 = empty0 + 8 * STAGES;   // accumulator complete
+    const uint32_t acce0 = accf0 + 16;            // accumulator read
+    const uint32_t overlap_bar = acce0 + 16;      // the overlap's chunk of the last accumulator read
+    const uint32_t drain_bar = overlap_bar + 8;
+    const uint32_t sfull0 = drain_bar + 8;
     const uint32_t sempty0 = sfull0 + 8 * kScaleSlots;
     const uint32_t tfull0 = sempty0 + 8 * kScaleSlots;
     const uint32_t tempty0 = tfull0 + 8 * kTileSlots;
@@ -341,6 +389,10 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_gemm_kernel(const __grid_cons
     const int warp = threadIdx.x >> 5;
     const int lane = threadIdx.x & 31;
     const DevStatus& err = P.st;
+    const int rank = CG > 1 ? static_cast<int>(cluster_ctarank()) : 0;  // 0: the pair's leader
+    const bool wgrad = P.wgrad;
+    // k blocks summed in TMEM before the result is stored or added to.
+    const int segment = P.out_dtype == GNS_FP32 || P.split > 1 ? kSegment : 1 << 30;
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < STAGES; ++s) {
@@ -349,24 +401,25 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_gemm_kernel(const __grid_cons
         }
         for (int b = 0; b < 2; ++b) {
             mbar_init(accf0 + 8 * b, 1);
-            mbar_init(acce0 + 8 * b, kEpiWarps);
+            mbar_init(acce0 + 8 * b, kEpiWarps * CG);
         }
+        mbar_init(overlap_bar, kEpiWarps / 2 * CG);
         mbar_init(drain_bar, 1);
         for (int b = 0; b < kScaleSlots; ++b) {
-            mbar_init(sfull0 + 8 * b, 32);
-            mbar_init(sempty0 + 8 * b, kEpiWarps);
+            mbar_init(sfull0 + 8 * b, kSlotBlocks * CG);
+            mbar_init(sempty0 + 8 * b, 1);
         }
         for (int b = 0; b < kTileSlots; ++b) {
             mbar_init(tfull0 + 8 * b, 1);
-            mbar_init(tempty0 + 8 * b, kTileReaders);
+            mbar_init(tempty0 + 8 * b, kTileReaders - (rank != 0));  // no MMA issuer on the peer
         }
         fence_mbar_init();
         prefetch_tmap(&P.mapA);
         prefetch_tmap(&P.mapB);
     }
     if (warp == 1) {
-        tmem_alloc<1>(smem_u32(tmem_slot), kTmemCols);
-        tmem_relinquish<1>();
+        tmem_alloc<CG>(smem_u32(tmem_slot), kTmemCols);
+        tmem_relinquish<CG>();
     }
     grid_dependency_wait();
     grid_launch_dependents();
@@ -383,7 +436,7 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_gemm_kernel(const __grid_cons
         const int g0 = threadIdx.x * per;
         auto units = [&](int g) {
             const int c = gr->offs[g + 1] - gr->offs[g];
-            return WGRAD ? (c + BK - 1) / BK : (c + BM - 1) / BM;
+            return wgrad ? (c + BK - 1) / BK : (c + TM - 1) / TM;
         };
         int mine = 0;
         for (int i = 0; i < per && g0 + i < n; ++i) mine += units(g0 + i);
@@ -403,14 +456,14 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_gemm_kernel(const __grid_cons
             if (g0 + i == G) gr->pre[n] = start;
         }
     } else if (threadIdx.x == 0) {
-        const int u = WGRAD ? (P.rows + BK - 1) / BK : (P.rows + BM - 1) / BM;
         gr->offs[0] = 0;
         gr->offs[1] = gr->offs[2] = P.rows;
         gr->pre[0] = 0;
-        gr->pre[1] = gr->pre[2] = u;
+        gr->pre[1] = gr->pre[2] = wgrad ? (P.rows + BK - 1) / BK : (P.rows + TM - 1) / TM;
     }
     tc_fence_before();
     __syncthreads();
+    if constexpr (CG > 1) cluster_sync();  // the pair's barriers exist before any remote use
     tc_fence_after();
     const uint32_t tmem_base = *tmem_slot;
 
@@ -430,155 +483,221 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_gemm_kernel(const __grid_cons
         if (!whole_warp || lane == 0) mbar_arrive(tempty0 + 8 * slot);
         return tl.g >= 0;
     };
-    const bool a_mn = WGRAD, b_mn = WGRAD || P.b_mn;
+    const bool a_mn = wgrad, b_mn = wgrad || P.b_mn;
 
-    if (warp < kEpiWarp0) {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 40;");
-        if (warp == 0) {
-            // ------------------------------------------------------ TMA producer
-            if (lane == 0) {
-                uint32_t stage = 0, phase = 0;
-                int issued = 0;
-                bool ok = true;
-                Tile tl;
-                for (int i = 0; ok && take(i, tl, false); ++i) {
-                    const int arow = tl.row0 + tl.m0;
-                    const int gb = WGRAD ? 0 : tl.g;
-                    for (int kb = tl.kb0; kb < tl.kb1; ++kb) {
-                        if (!mbar_wait(empty0 + 8 * stage, phase ^ 1, err)) {
-                            ok = false;
-                            break;
-                        }
-                        const uint32_t fb = full0 + 8 * stage;
-                        const uint32_t da = smem_u32(sA + stage * A_BYTES), db = smem_u32(sB + stage * B_BYTES);
-                        mbar_arrive_expect_tx(fb, A_BYTES + B_BYTES);
-                        if (a_mn)
-                            tma_load_3d(da, &P.mapA, fb, arow, kb * BK, 0);
-                        else
-                            tma_load_3d(da, &P.mapA, fb, kb * BK, arow, 0);
-                        if (b_mn) {
-                            for (int h = 0; h < BN / 128; ++h)
-                                tma_load_3d(db + h * kBoxBytes, &P.mapB, fb, tl.n0 + 128 * h, kb * BK, gb);
-                        } else {
-                            tma_load_3d(db, &P.mapB, fb, kb * BK, tl.n0, gb);
-                        }
-                        ++issued;
-                        if (++stage == STAGES) {
-                            stage = 0;
-                            phase ^= 1;
-                        }
+    if (warp == 0) {
+        // ------------------------------------------------------ TMA producer
+        if (lane == 0) {
+            uint32_t stage = 0, phase = 0;
+            int issued = 0;
+            bool ok = true;
+            Tile tl;
+            for (int i = 0; ok && take(i, tl, false); ++i) {
+                const int arow = tl.row0 + tl.m0 + BM * rank;
+                const int brow = tl.n0 + BNH * rank;
+                const int gb = wgrad ? 0 : tl.g;
+                for (int kb = tl.kb0; kb < tl.kb1; ++kb) {
+                    if (!mbar_wait(empty0 + 8 * stage, phase ^ 1, err)) {
+                        ok = false;
+                        break;
                     }
-                }
-                // Loads still in flight land before the CTA ends.
-                const int pending = issued < STAGES ? issued : STAGES;
-                for (int i = 0; i < pending; ++i) {
-                    if (stage == 0) {
-                        stage = STAGES;
+                    const uint32_t fb = full0 + 8 * stage;
+                    const uint32_t da = smem_u32(sA + stage * A_BYTES), db = smem_u32(sB + stage * B_BYTES);
+                    const int ka = a_mn ? arow : kb * BK, ra = a_mn ? kb * BK : arow;
+                    if constexpr (CG == 1) {
+                        mbar_arrive_expect_tx(fb, A_BYTES + B_BYTES);
+                        tma_load_3d(da, &P.mapA, fb, ka, ra, 0);
+                        if (b_mn) {
+                            for (int h = 0; h < BNH / 128; ++h)
+                                tma_load_3d(db + h * kBoxBytes, &P.mapB, fb, brow + 128 * h, kb * BK, gb);
+                        } else {
+                            tma_load_3d(db, &P.mapB, fb, kb * BK, brow, gb);
+                        }
+                    } else {  // both halves complete on the leader's barrier
+                        if (rank == 0) mbar_arrive_expect_tx(fb, 2 * (A_BYTES + B_BYTES));
+                        const uint32_t lead_fb = map_to_rank(fb, 0);
+                        tma_load_3d_pair(da, &P.mapA, lead_fb, ka, ra, 0);
+                        tma_load_3d_pair(db, &P.mapB, lead_fb, b_mn ? brow : kb * BK, b_mn ? kb * BK : brow, gb);
+                    }
+                    ++issued;
+                    if (++stage == STAGES) {
+                        stage = 0;
                         phase ^= 1;
                     }
-                    --stage;
-                    drain_wait(full0 + 8 * stage, phase, err.limit_ns);
                 }
             }
-            __syncwarp();
-        } else if (warp == 1) {
-            // ------------------------------------------- MMA issuer
-            if (lane == 0) {
-                uint32_t stage = 0, phase = 0;
-                int it = 0;  // k blocks issued; the accumulator buffer is it & 1
-                bool ok = true;
-                const uint32_t idesc = idesc_f8(BM, BN, P.fmt_a, P.fmt_b, a_mn, b_mn);
-                const uint64_t a0 = a_mn ? sw128_mnmajor_desc(smem_u32(sA), kBoxBytes) : sw128_kmajor_desc(smem_u32(sA));
-                const uint64_t b0 = b_mn ? sw128_mnmajor_desc(smem_u32(sB), kBoxBytes) : sw128_kmajor_desc(smem_u32(sB));
-                // A 32-wide k step: 32 bytes along a K-major row, or 32 rows of an MN-major tile.
-                const uint32_t a_step = a_mn ? (4096 >> 4) : (32 >> 4);
-                const uint32_t b_step = b_mn ? (4096 >> 4) : (32 >> 4);
-                Tile tl;
-                for (int i = 0; ok && take(i, tl, false); ++i) {
-                    for (int kb = tl.kb0; kb < tl.kb1; ++kb, ++it) {
-                        const int buf = it & 1;
-                        if (!mbar_wait(acce0 + 8 * buf, ((it >> 1) & 1) ^ 1, err) ||
-                            !mbar_wait(full0 + 8 * stage, phase, err)) {
+            // Loads still in flight land before the CTA ends.
+            const int pending = rank != 0 ? 0 : issued < STAGES ? issued : STAGES;
+            for (int i = 0; i < pending; ++i) {
+                if (stage == 0) {
+                    stage = STAGES;
+                    phase ^= 1;
+                }
+                --stage;
+                drain_wait(full0 + 8 * stage, phase, err.limit_ns);
+            }
+        }
+        __syncwarp();
+    } else if (warp == 1) {
+        // ------------------------------------------- MMA issuer (pair leader)
+        if (lane == 0 && rank == 0) {
+            // This thread's own instructions bound the kernel when they take
+            // longer than a block's MMAs (512 cycles), so the loop runs over
+            // scale slots with their four k blocks unrolled, and counts
+            // instead of dividing.
+            uint32_t stage = 0, phase = 0;
+            int it = 0;       // segments done; the accumulator is it & 1
+            uint32_t sn = 0;  // scale slots used
+            bool ok = true;
+            const uint32_t idesc = idesc_mx(TM, BN, P.fmt_a, P.fmt_b, a_mn, b_mn);
+            const uint64_t a0 = a_mn ? sw128_mnmajor_desc(smem_u32(sA), kBoxBytes) : sw128_kmajor_desc(smem_u32(sA));
+            const uint64_t b0 = b_mn ? sw128_mnmajor_desc(smem_u32(sB), kBoxBytes) : sw128_kmajor_desc(smem_u32(sB));
+            // A 32-wide k step: 32 bytes along a K-major row, or 32 rows of an MN-major tile.
+            const uint32_t a_step = a_mn ? (4096 >> 4) : (32 >> 4);
+            const uint32_t b_step = b_mn ? (4096 >> 4) : (32 >> 4);
+            auto commit = [&](uint32_t bar) {
+                if constexpr (CG == 1)
+                    tc_commit<1>(bar);
+                else
+                    tc_commit_pair(bar);
+            };
+            Tile tl;
+            for (int i = 0; ok && take(i, tl, false); ++i) {
+                int left = tl.kb1 - tl.kb0;  // k blocks
+                int in_segment = 0;          // scale slots of this segment so far
+                while (left > 0) {
+                    const uint32_t buf = it & 1, slot = sn & 1;
+                    static_assert(kScaleSlots == 2, "slot and phase come from sn's bits");
+                    const uint32_t d_tmem = tmem_base + buf * kAcc1;
+                    if (in_segment == 0 && (!mbar_wait(acce0 + 8 * buf, ((it >> 1) & 1) ^ 1, err) ||
+                                            (it > 0 && !mbar_wait(overlap_bar, (it - 1) & 1, err)))) {
+                        ok = false;
+                        break;
+                    }
+                    // A full slot also says that the MMAs that read its TMEM
+                    // columns before are done (see the builders).
+                    if (!mbar_wait_cluster(sfull0 + 8 * slot, (sn >> 1) & 1, err)) {
+                        ok = false;
+                        break;
+                    }
+                    tc_fence_after();
+                    const uint32_t sf = tmem_base + kScaleTmem + slot * kScaleCols;
+                    const uint32_t src = smem_u32(scales) + slot * kSlotBytes;
+                    tc_copy_scales<CG>(sf, src);
+                    tc_copy_scales<CG>(sf + 4, src + 512);
+                    tc_copy_scales<CG>(sf + 8, src + 1024);
+#pragma unroll
+                    for (int j = 0; j < kSlotBlocks; ++j) {
+                        if (j >= left) break;
+                        if (!mbar_wait(full0 + 8 * stage, phase, err)) {
                             ok = false;
                             break;
                         }
                         tc_fence_after();
-                        const uint64_t adesc = a0 + ((stage * A_BYTES) >> 4);
-                        const uint64_t bdesc = b0 + ((stage * B_BYTES) >> 4);
+                        const uint64_t adesc = a0 + stage * (A_BYTES >> 4);
+                        const uint64_t bdesc = b0 + stage * (B_BYTES >> 4);
 #pragma unroll
                         for (int kk = 0; kk < BK / 32; ++kk)
-                            tc_mma_f8(tmem_base + buf * BN, adesc + a_step * kk, bdesc + b_step * kk, idesc, kk != 0);
-                        tc_commit<1>(empty0 + 8 * stage);
-                        tc_commit<1>(accf0 + 8 * buf);
+                            tc_mma_mx<CG>(d_tmem, adesc + a_step * kk, bdesc + b_step * kk, idesc | scale_id(j), sf, sf + 4,
+                                          (j | kk) != 0 || in_segment != 0);
+                        commit(empty0 + 8 * stage);
                         if (++stage == STAGES) {
                             stage = 0;
                             phase ^= 1;
                         }
                     }
-                }
-                // All MMAs issued by this thread must finish before TMEM is freed.
-                tc_commit<1>(drain_bar);
-                drain_wait(drain_bar, 0, err.limit_ns);
-            }
-            __syncwarp();
-        } else if (warp == 2) {
-            // ----------------------------------------------- scale producer
-            const uint32_t ring = smem_u32(scales);
-            int slot = 0;
-            uint32_t phase = 0;
-            bool ok = true;
-            Tile tl;
-            for (int i = 0; ok && take(i, tl, true); ++i) {
-                const int local = tl.m0 + lane;
-                const float* pa = P.sA + tl.row0 + local;
-                const float* pb = P.sB + (WGRAD ? tl.n0 + 4 * lane
-                                                : tl.g * P.sB_g + static_cast<long long>(tl.n0 / kFp8Block + lane) * P.sB_n);
-                for (int kb0 = tl.kb0; kb0 < tl.kb1; kb0 += kSlotBlocks) {
-                    if (!__all_sync(0xffffffffu, mbar_wait(sempty0 + 8 * slot, phase ^ 1, err))) {
-                        ok = false;
-                        break;
-                    }
-                    const int end = min(kb0 + kSlotBlocks, tl.kb1);
-                    for (int kb = kb0; kb < end; ++kb) {
-                        const uint32_t dst = ring + 4 * (slot * kSlotFloats<WGRAD> + (kb - kb0) * kScaleFloats<WGRAD>);
-#pragma unroll
-                        for (int i = 0; i < 4; ++i)
-                            copy_async<4>(dst + 4 * (lane + 32 * i), pa + kb * P.ldsA + 32 * i, local + 32 * i < tl.rows, P.sA);
-                        if constexpr (WGRAD) {
-#pragma unroll
-                            for (int i = 0; i < 2; ++i)
-                                copy_async<16>(dst + 4 * (BM + 4 * lane + 128 * i), pb + kb * P.sB_k + 128 * i,
-                                               tl.n0 + 4 * lane + 128 * i < P.sB_k, P.sB);
-                        } else if (lane < 2) {
-                            copy_async<4>(dst + 4 * (BM + lane), pb + kb * P.sB_k, tl.n0 + 128 * lane < P.N, P.sB);
-                        }
-                    }
-                    asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(sfull0 + 8 * slot) : "memory");
-                    if (++slot == kScaleSlots) {
-                        slot = 0;
-                        phase ^= 1;
+                    if (!ok) break;
+                    commit(sempty0 + 8 * slot);
+                    ++sn;
+                    left -= kSlotBlocks;
+                    if (++in_segment == segment / kSlotBlocks || left <= 0) {
+                        commit(accf0 + 8 * buf);
+                        ++it;
+                        in_segment = 0;
                     }
                 }
             }
-            asm volatile("cp.async.wait_all;" ::: "memory");
-            __syncwarp();
-        } else if (lane == 0) {
-            // ---------------------------------------------------- scheduler
+            // All MMAs issued by this thread must finish before TMEM is freed.
+            tc_commit<CG>(drain_bar);
+            drain_wait(drain_bar, 0, err.limit_ns);
+        }
+        __syncwarp();
+    } else if (warp >= kBuildWarp0 && warp < kEpiWarp0) {
+        // --------------------------------------------------- scale builders
+        // This warp's k block of each slot; lane l holds rows l, l + 32, l +
+        // 64, l + 96 of A's (and of each half of B's) 128. The exponents
+        // are read before the wait for the slot, which ends when the MMAs
+        // that used it are done and so frees its TMEM columns too.
+        const uint32_t ring = smem_u32(scales);
+        const uint32_t sfull_lead = CG == 2 ? map_to_rank(sfull0, 0) : sfull0;
+        const int j = warp - kBuildWarp0;
+        int groups = 0;
+        bool ok = true;
+        Tile tl;
+        for (int i = 0; ok && take(i, tl, true); ++i) {
+            const int arow = tl.m0 + BM * rank + lane;
+            const float* pa = P.sA + tl.row0 + arow;
+            const float* pb = P.sB + (wgrad ? tl.n0 + lane
+                                            : tl.g * P.sB_g + static_cast<long long>(tl.n0 / kFp8Block) * P.sB_n);
+            for (int kb0 = tl.kb0; kb0 < tl.kb1; kb0 += kSlotBlocks, ++groups) {
+                const int kb = kb0 + j;
+                const bool in = kb < tl.kb1;
+                // Rows outside have some valid element's scale: nothing of theirs is stored.
+                float va[4], vb[8];
+#pragma unroll
+                for (int r = 0; r < 4; ++r)
+                    va[r] = __ldg(in && arow + 32 * r < tl.rows ? pa + kb * P.ldsA + 32 * r : P.sA);
+                if (wgrad) {
+#pragma unroll
+                    for (int r = 0; r < 8; ++r)
+                        vb[r] = __ldg(in && tl.n0 + lane + 32 * r < P.N ? pb + kb * P.sB_k + 32 * r : P.sB);
+                } else {
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        const float v = __ldg(in && tl.n0 + 128 * h < P.N ? pb + kb * P.sB_k + h * P.sB_n : P.sB);
+#pragma unroll
+                        for (int r = 0; r < 4; ++r) vb[4 * h + r] = v;
+                    }
+                }
+                const int slot = groups % kScaleSlots;
+                if (!__all_sync(0xffffffffu, mbar_wait(sempty0 + 8 * slot, ((groups / kScaleSlots) & 1) ^ 1, err))) {
+                    ok = false;
+                    break;
+                }
+                const uint32_t at = ring + slot * kSlotBytes + 16 * lane + j;
+#pragma unroll
+                for (int r = 0; r < 4; ++r) st_shared_u8(at + 4 * r, __float_as_uint(va[r]) >> 23);
+#pragma unroll
+                for (int r = 0; r < 8; ++r) st_shared_u8(at + 512 + 128 * (r & ~3) + 4 * (r & 3), __float_as_uint(vb[r]) >> 23);
+                asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // tcgen05.cp reads through the async proxy
+                __syncwarp();
+                if (lane == 0) {
+                    if constexpr (CG == 1)
+                        mbar_arrive(sfull0 + 8 * slot);
+                    else
+                        mbar_arrive_cluster(sfull_lead + 8 * slot);
+                }
+            }
+        }
+        __syncwarp();
+    } else if (warp == 2) {
+        // -------------------------------------------------------- scheduler
+        if (lane == 0) {
             Walk w;
             w.G = G;
             w.M = P.M;
             w.ntn = (P.N + BN - 1) / BN;
-            w.mtn = WGRAD ? (P.M + BM - 1) / BM : 0;
+            w.mtn = wgrad ? (P.M + TM - 1) / TM : 0;
             w.split = P.split;
-            w.wgrad = WGRAD;
-            w.total_kb = WGRAD ? 0 : (P.K + BK - 1) / BK;
+            w.wgrad = wgrad;
+            w.total_kb = wgrad ? 0 : (P.K + BK - 1) / BK;
             w.gr = gr;
-            const int total = WGRAD ? G * w.mtn * w.ntn : gr->pre[G + 1] * w.ntn * P.split;
-            int t = static_cast<int>(blockIdx.x);
-            for (int i = 0;; ++i, t += static_cast<int>(gridDim.x)) {
+            const int total = wgrad ? G * w.mtn * w.ntn : gr->pre[G + 1] * w.ntn * P.split;
+            int t = static_cast<int>(blockIdx.x) / CG;
+            for (int i = 0;; ++i, t += static_cast<int>(gridDim.x) / CG) {
                 Tile tl{};
                 tl.g = -1;
-                if (t < total) tl = decode(w, t);
+                if (t < total) tl = decode<CG>(w, t);
                 const int slot = i % kTileSlots;
                 if (!mbar_wait(tempty0 + 8 * slot, ((i / kTileSlots) & 1) ^ 1, err)) break;
                 const uint32_t at = tiles_u32 + slot * static_cast<uint32_t>(sizeof(Tile));
@@ -589,120 +708,110 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_gemm_kernel(const __grid_cons
             }
         }
         __syncwarp();
-    } else {
+    } else if (warp >= kEpiWarp0) {
         // ---------------------------------------------------------- epilogue
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 232;");
-        const int q = warp & 3;           // TMEM lane quarter this warp may read
+        const int q = warp & 3;  // TMEM lane quarter this warp may read
         const int ew = warp - kEpiWarp0;
-        const int cq = (ew >> 2) * kCols;  // its first column within the tile
-        const uint32_t ring = smem_u32(scales);
-        const uint32_t tmem_warp = tmem_base + (static_cast<uint32_t>(q * 32) << 16) + cq;
-        int it = 0;    // k blocks added
-        int slot = 0;  // scale slot and its phase
-        uint32_t sphase = 0;
+        const int half = ew >> 2;  // columns 128 half .. + 127 of the tile
+        const uint32_t stage = smem_u32(staging + ew * kStageBytes);
+        const uint32_t acce_lead = CG == 2 ? map_to_rank(acce0, 0) : acce0;
+        const uint32_t overlap_lead = CG == 2 ? map_to_rank(overlap_bar, 0) : overlap_bar;
+        auto hand_back = [&](uint32_t bar) {
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) {
+                if constexpr (CG == 1)
+                    mbar_arrive(bar);
+                else
+                    mbar_arrive_relaxed(bar);
+            }
+        };
+        int it = 0;  // segments read; the accumulator is it & 1
         bool ok = true;
         Tile tl;
         for (int i = 0; ok && take(i, tl, true); ++i) {
-            const int col = tl.n0 + cq;
-            float acc[kCols];
-#pragma unroll
-            for (int i = 0; i < kCols; ++i) acc[i] = 0.0f;
-            // A chunk of 32 columns is loaded from TMEM while the one before it
-            // is added; the next k block's barrier is polled ahead of its use
-            // (a poll, like every shared-memory access, takes some 150 cycles
-            // beside the MMAs' operand reads).
-            bool ready = false;
-            float s = 0.0f;
-#pragma unroll 1
-            for (int kb = tl.kb0; kb < tl.kb1; ++kb, ++it) {
-                const int in_slot = (kb - tl.kb0) % kSlotBlocks;
-                const uint32_t acc_tmem = tmem_warp + (it & 1) * BN;
-                const uint32_t sc = ring + 4 * (slot * kSlotFloats<WGRAD> + in_slot * kScaleFloats<WGRAD>);
-                if (!__all_sync(0xffffffffu, ready)) {
-                    ok = (in_slot != 0 || mbar_wait_here(sfull0 + 8 * slot, sphase, err)) &&
-                         mbar_wait_here(accf0 + 8 * (it & 1), (it >> 1) & 1, err);
-                    if (!__all_sync(0xffffffffu, ok)) {
+            const int col = tl.n0 + kCols * half;
+            const int row = tl.m0 + BM * rank + 32 * q;
+            // Rows of this warp inside the group (of D) and columns inside D.
+            const int rows = tl.rows - row, ncol = P.N - col;
+            const bool live = rows > 0 && ncol > 0;
+            const bool split = P.split > 1;
+            const int es = P.out_dtype == GNS_FP32 || split ? 4 : 2;
+            const long long row0 = static_cast<long long>(tl.row0) + row;
+            const long long ldd = split ? P.N : P.ldd;
+            uint8_t* d = split ? reinterpret_cast<uint8_t*>(P.partial + (static_cast<long long>(tl.split) * P.rows + row0) * P.N + col)
+                               : static_cast<uint8_t*>(P.D) + ((wgrad ? tl.g * P.strideD : 0LL) + row0 * P.ldd + col) * es;
+            const bool aligned = split ? P.N % 4 == 0
+                                       : ((reinterpret_cast<uintptr_t>(P.D) | static_cast<uintptr_t>(P.ldd * es) |
+                                           static_cast<uintptr_t>(P.strideD * es)) & 15) == 0;
+            const int passes = es == 2 ? 2 : 4;
+            const bool bf16 = P.out_dtype == GNS_BF16;
+            int kb = tl.kb0;
+            do {  // segments; once, with zeros, for a group without rows to sum over
+                const bool filled = kb < tl.kb1;
+                const int buf = it & 1;
+                const uint32_t acc = tmem_base + (static_cast<uint32_t>(32 * q) << 16) + buf * kAcc1 + kCols * half;
+                if (filled) {
+                    if (!__all_sync(0xffffffffu, mbar_wait_here(accf0 + 8 * buf, (it >> 1) & 1, err))) {
                         ok = false;
                         break;
                     }
+                    tc_fence_after();
                 }
-                tc_fence_after();
-                uint32_t v[2][32];
-                tmem_ld_32x32b_x32(acc_tmem, v[0]);
-                s = ld_shared_f32(sc + 4 * (q * 32 + lane));
-                if (!WGRAD) s *= ld_shared_f32(sc + 4 * (BM + cq / kFp8Block));
+                // The chunk in the overlap comes first: accumulator 0's last
+                // columns (the second half's warps), accumulator 1's first.
+                const bool mine = half == (buf == 0);
+#pragma unroll 1
+                for (int n = 0; n < passes; ++n) {
+                    const int p = buf == 0 ? passes - 1 - n : n;
+                    uint32_t w[32];
+                    if (filled && live) {
+                        if (es == 2) {
+                            uint32_t x[32], y[32];
+                            tmem_ld_32x32b_x32(acc + 64 * p, x);
+                            tmem_ld_32x32b_x32(acc + 64 * p + 32, y);
+                            tmem_ld_wait_for(x);
+                            tmem_ld_wait_for(y);
 #pragma unroll
-                for (int c = 0; c < kCols / 32; ++c) {
-                    const uint32_t(&x)[32] = v[c & 1];
-                    tmem_ld_wait_for(v[c & 1]);
-                    if (c + 1 < kCols / 32) {
-                        tmem_ld_32x32b_x32(acc_tmem + 32 * (c + 1), v[(c + 1) & 1]);
-                    } else {  // all in registers: the next MMAs may overwrite the accumulator
-                        tc_fence_before();
-                        __syncwarp();
-                        if (lane == 0) mbar_arrive(acce0 + 8 * (it & 1));
-                        ready = in_slot != kSlotBlocks - 1 && kb + 1 < tl.kb1 &&
-                                mbar_test(accf0 + 8 * ((it + 1) & 1), ((it + 1) >> 1) & 1);
-                    }
-                    if constexpr (WGRAD) {
-#pragma unroll
-                        for (int i = 0; i < 8; ++i) {
-                            const uint4 f = ld_shared_v4(sc + 4 * (BM + cq + 32 * c + 4 * i));
-                            const uint32_t g[4] = {f.x, f.y, f.z, f.w};
-#pragma unroll
-                            for (int e = 0; e < 4; ++e) {
-                                const int j = 4 * i + e;
-                                acc[32 * c + j] = fmaf(__uint_as_float(x[j]), s * __uint_as_float(g[e]), acc[32 * c + j]);
+                            for (int j = 0; j < 16; ++j) {
+                                w[j] = pack_pair(__uint_as_float(x[2 * j]), __uint_as_float(x[2 * j + 1]), bf16);
+                                w[16 + j] = pack_pair(__uint_as_float(y[2 * j]), __uint_as_float(y[2 * j + 1]), bf16);
                             }
+                        } else {
+                            tmem_ld_32x32b_x32(acc + 32 * p, w);
+                            tmem_ld_wait_for(w);
                         }
                     } else {
 #pragma unroll
-                        for (int j = 0; j < 32; ++j)
-                            acc[32 * c + j] = fmaf(__uint_as_float(x[j]), s, acc[32 * c + j]);
+                        for (int j = 0; j < 32; ++j) w[j] = 0;
+                    }
+                    if (filled) {
+                        if (n == 0 && mine) hand_back(overlap_lead);
+                        if (n == passes - 1) hand_back(acce_lead + 8 * buf);
+                    }
+                    const int c0 = p * (kStageRow / es);
+                    if (live && c0 < ncol) {
+                        if (es == 2)
+                            store_pass<2>(stage, d + c0 * 2, ldd, rows, ncol - c0, w, aligned, false, lane);
+                        else
+                            store_pass<4>(stage, d + c0 * 4, ldd, rows, ncol - c0, w, aligned, kb > tl.kb0, lane);
                     }
                 }
-                if (in_slot == kSlotBlocks - 1 || kb + 1 == tl.kb1) {
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(sempty0 + 8 * slot);
-                    if (++slot == kScaleSlots) {
-                        slot = 0;
-                        sphase ^= 1;
-                    }
-                }
-            }
-            if (!ok) break;
-            // Rows of this warp inside the group (of D) and columns inside D.
-            const int wrows = tl.rows - tl.m0 - q * 32, ncol = P.N - col;
-            if (wrows <= 0 || ncol <= 0) continue;
-            const int es = P.out_dtype == GNS_FP32 || P.split > 1 ? 4 : 2;
-            const uint32_t stage = smem_u32(staging + ew * kStageBytes);
-            const long long row0 = tl.row0 + tl.m0 + q * 32;
-            uint8_t* d;
-            long long ldd;
-            bool aligned;
-            if (P.split > 1) {
-                d = reinterpret_cast<uint8_t*>(P.partial + (static_cast<long long>(tl.split) * P.rows + row0) * P.N + col);
-                ldd = P.N;
-                aligned = P.N % 4 == 0;
-            } else {
-                d = static_cast<uint8_t*>(P.D) + ((WGRAD ? tl.g * P.strideD : 0LL) + row0 * P.ldd + col) * es;
-                ldd = P.ldd;
-                aligned = ((reinterpret_cast<uintptr_t>(P.D) | static_cast<uintptr_t>(P.ldd * es) |
-                            static_cast<uintptr_t>(P.strideD * es)) & 15) == 0;
-            }
-            if (es == 2)
-                store_tile<2>(stage, d, ldd, wrows, ncol, acc, P.out_dtype == GNS_BF16, aligned, lane);
-            else
-                store_tile<4>(stage, d, ldd, wrows, ncol, acc, false, aligned, lane);
+                it += filled;
+                kb = segment < tl.kb1 - kb ? kb + segment : tl.kb1;
+            } while (kb < tl.kb1);
         }
         __syncwarp();
     }
 
     tc_fence_before();
     __syncthreads();
+    // The leader's MMAs read the peer's shared memory and the peer's loads and
+    // epilogues arrive on the leader's barriers: neither leaves before the other.
+    if constexpr (CG > 1) cluster_sync();
     if (warp == 1) {
         tc_fence_after();
-        tmem_dealloc<1>(tmem_base, kTmemCols);
+        tmem_dealloc<CG>(tmem_base, kTmemCols);
     }
 }
 
@@ -723,20 +832,45 @@ __global__ void __launch_bounds__(256) fp8_reduce_kernel(const float* partial, i
 
 constexpr int kMaxDevices = 64;
 
-template <bool WGRAD>
+template <int CG>
 int launch_variant(const Fp8GemmJob& job, long long max_tiles, int num_sms, cudaStream_t s) {
-    static bool configured[kMaxDevices];  // the shared-memory opt-in is per device
+    // Per device: the shared-memory opt-in, and the clusters that fit at once
+    // (tiles go to them with a static stride).
+    static int clusters[kMaxDevices];
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
     if (dev < 0 || dev >= kMaxDevices) return cudaErrorInvalidDevice;
-    if (!configured[dev]) {
-        e = cudaFuncSetAttribute(fp8_gemm_kernel<WGRAD>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
+    const auto kernel = fp8_gemm_kernel<CG>;
+    cudaLaunchConfig_t cfg = {};
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = smem_bytes<CG>();
+    cfg.stream = s;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = CG;
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    if (clusters[dev] == 0) {
+        e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem_bytes<CG>());
         if (e != cudaSuccess) return e;
-        configured[dev] = true;
+        int n = 0;
+        if (CG > 1) {
+            cfg.attrs = attr + 1;
+            cfg.numAttrs = 1;
+            cfg.gridDim = dim3(static_cast<unsigned>(std::max(num_sms / CG, 1) * CG));
+            if (cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) != cudaSuccess) cudaGetLastError();
+            cfg.attrs = attr;
+        }
+        clusters[dev] = n > 0 ? n : std::max(num_sms / CG, 1);
     }
-    const unsigned grid = static_cast<unsigned>(std::min<long long>(num_sms, max_tiles));
-    return launch_after(fp8_gemm_kernel<WGRAD>, dim3(grid), dim3(kThreads), kSmemBytes, s, job);
+    const int fit = std::max(1, std::min(clusters[dev], num_sms / CG));
+    cfg.gridDim = dim3(static_cast<unsigned>(CG * std::min<long long>(fit, max_tiles)));
+    cfg.numAttrs = CG > 1 ? 2 : 1;
+    return cudaLaunchKernelEx(&cfg, kernel, job);
 }
 
 }  // namespace
@@ -749,18 +883,25 @@ int fp8_gemm_split(int rows, int N, int K, int num_sms) {
     return static_cast<int>(std::max<long long>(1, std::min<long long>(num_sms / tiles, kb / 4)));
 }
 
-int launch_fp8_gemm(const Fp8GemmJob& job, int num_sms, cudaStream_t s) {
+int fp8_gemm_cg(int M, int N, int G, bool grouped, int num_sms) {
+    static const char* f = std::getenv("GNS_FP8_CG");
+    if (f) return std::atoi(f);
+    return 1;
+}
+
+int launch_fp8_gemm(const Fp8GemmJob& job, int cg, int num_sms, cudaStream_t s) {
+    const int tile = BM * cg;
     const long long tn = (job.N + BN - 1) / BN;
     long long tm;  // tile rows, an upper bound where the groups are on the device
     if (job.wgrad)
-        tm = static_cast<long long>(job.G) * ((job.M + BM - 1) / BM);
+        tm = static_cast<long long>(job.G) * ((job.M + tile - 1) / tile);
     else if (job.offsets)
-        tm = (job.rows + static_cast<long long>(BM - 1) * (std::min(job.rows, job.G) + 1)) / BM;
+        tm = (job.rows + static_cast<long long>(tile - 1) * (std::min(job.rows, job.G) + 1)) / tile;
     else
-        tm = (job.rows + BM - 1) / BM;
+        tm = (job.rows + tile - 1) / tile;
     const long long tiles = tm * tn * job.split;
     if (tiles <= 0) return cudaSuccess;
-    const int e = job.wgrad ? launch_variant<true>(job, tiles, num_sms, s) : launch_variant<false>(job, tiles, num_sms, s);
+    const int e = cg == 2 ? launch_variant<2>(job, tiles, num_sms, s) : launch_variant<1>(job, tiles, num_sms, s);
     if (e != cudaSuccess || job.split <= 1) return e;
     const long long elems = static_cast<long long>(job.rows) * job.N;
     return by_dtype(job.out_dtype, [&](auto t) {
