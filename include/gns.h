@@ -335,6 +335,7 @@ int gns_moe_combine_backward(const void* dout, int64_t lddo, const void* y, int6
  * each block of 128 values: s = the smallest power of two (at least 2^-126)
  * with amax / s <= the format's largest value, amax over the block's finite
  * values; q = x / s rounded to nearest even; NaN and infinities become NaN.
+ * Scales are stored as 8-bit exponents: b stands for 2^(b - 127).
  *   slots, topk    row r is read from x[slots[r] / topk] (slots NULL: x[r]):
  *                  the gather of gns_moe_gather on the way.
  *   q_rows         row form (or NULL): [rows][ld_rows], blocks along the row;
@@ -352,11 +353,10 @@ int gns_moe_combine_backward(const void* dout, int64_t lddo, const void* y, int6
  *                  offsets[groups] of the row form are not written.
  * 8-bit rows are 16-byte aligned (ld a multiple of 16 that covers the
  * columns; the columns up to the next multiple of 16 are written as zero).
- * Column scales have 16-byte aligned rows.
  */
 int gns_fp8_quantize(const void* x, int64_t ldx, int dtype, int rows, int cols, const int32_t* slots, int topk,
-                     const int32_t* offsets, int groups, int format, void* q_rows, int64_t ld_rows, float* scale_rows,
-                     int64_t ld_scale_rows, void* q_cols, int64_t ld_cols, float* scale_cols, int64_t ld_scale_cols,
+                     const int32_t* offsets, int groups, int format, void* q_rows, int64_t ld_rows, uint8_t* scale_rows,
+                     int64_t ld_scale_rows, void* q_cols, int64_t ld_cols, uint8_t* scale_cols, int64_t ld_scale_cols,
                      void* stream);
 
 /*
@@ -365,28 +365,29 @@ int gns_fp8_quantize(const void* x, int64_t ldx, int dtype, int rows, int cols, 
  * [groups][ceil(N / 128)][ceil(K / 128)], scaled as by gns_fp8_quantize.
  */
 int gns_fp8_quantize_weight(const void* w, int64_t ldw, int64_t stride_w, int dtype, int groups, int N, int K,
-                            int format, void* q, int64_t ldq, float* scale, void* stream);
+                            int format, void* q, int64_t ldq, uint8_t* scale, void* stream);
 
 /*
  * gns_fp8_matmul: y[r] = a[r] . w[g]^T for the rows r of each group g, [rows][N],
  * from the row form of a ([rows][K]) and 8-bit weights:
  *   y[r][n] = sum over the blocks b of 128 along K of
- *             scale_a[b][r] scale_w[g][n / 128][b] sum_{k in b} a[r][k] w[g][n][k].
- * Any fp32 scales are taken; the product of two must stay in fp32's range.
+ *             scale_a[b][r] scale_w[g][n / 128][b] sum_{k in b} a[r][k] w[g][n][k],
+ * summed in the tensor core's fp32 accumulator (which truncates); fp32 results
+ * in segments of 2048 terms, added with one rounding each.
  *   offsets  [groups + 1] as written by gns_moe_sort; rows past
  *            offsets[groups] of y are set to zero. NULL with groups = 1: all
  *            rows are one group's.
  */
-int gns_fp8_matmul(const void* a, int64_t lda, const float* scale_a, int64_t ld_scale_a, int format_a, int rows,
-                   const void* w, int64_t ldw, const float* scale_w, int format_w, int groups, int N, int K,
+int gns_fp8_matmul(const void* a, int64_t lda, const uint8_t* scale_a, int64_t ld_scale_a, int format_a, int rows,
+                   const void* w, int64_t ldw, const uint8_t* scale_w, int format_w, int groups, int N, int K,
                    const int32_t* offsets, void* y, int64_t ldy, int out_dtype, void* stream);
 
 /*
  * gns_fp8_matmul_dgrad: the data gradient dx[r] = dy[r] . w[g], [rows][K], from
  * the row form of dy ([rows][N]) and the same 8-bit weights.
  */
-int gns_fp8_matmul_dgrad(const void* dy, int64_t lddy, const float* scale_dy, int64_t ld_scale_dy, int format_dy,
-                         int rows, const void* w, int64_t ldw, const float* scale_w, int format_w, int groups, int N,
+int gns_fp8_matmul_dgrad(const void* dy, int64_t lddy, const uint8_t* scale_dy, int64_t ld_scale_dy, int format_dy,
+                         int rows, const void* w, int64_t ldw, const uint8_t* scale_w, int format_w, int groups, int N,
                          int K, const int32_t* offsets, void* dx, int64_t lddx, int out_dtype, void* stream);
 
 /*
@@ -394,8 +395,8 @@ int gns_fp8_matmul_dgrad(const void* dy, int64_t lddy, const float* scale_dy, in
  * the rows of group g (zero for a group without rows), from the column forms
  * of dy and x made with the same offsets. The dw[g] are stride_dw elements apart.
  */
-int gns_fp8_matmul_wgrad(const void* dy, int64_t lddy, const float* scale_dy, int64_t ld_scale_dy, int format_dy,
-                         const void* x, int64_t ldx, const float* scale_x, int64_t ld_scale_x, int format_x, int rows,
+int gns_fp8_matmul_wgrad(const void* dy, int64_t lddy, const uint8_t* scale_dy, int64_t ld_scale_dy, int format_dy,
+                         const void* x, int64_t ldx, const uint8_t* scale_x, int64_t ld_scale_x, int format_x, int rows,
                          int groups, int N, int K, const int32_t* offsets, void* dw, int64_t lddw, int64_t stride_dw,
                          int out_dtype, void* stream);
 
@@ -405,7 +406,7 @@ int gns_fp8_matmul_wgrad(const void* dy, int64_t lddy, const float* scale_dy, in
  * gns_fp8_matmul. Up to eight rows run as one kernel that casts on the way.
  */
 int gns_fp8_linear(const void* x, int64_t ldx, int dtype, int rows, const int32_t* slots, int topk,
-                   const int32_t* offsets, const void* w, int64_t ldw, const float* scale_w, int format_w, int groups,
+                   const int32_t* offsets, const void* w, int64_t ldw, const uint8_t* scale_w, int format_w, int groups,
                    int N, int K, void* y, int64_t ldy, int out_dtype, void* stream);
 
 /* Synchronizes `stream`, returns the device status word of the current device

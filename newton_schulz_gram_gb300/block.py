@@ -32,14 +32,15 @@ class MoeRoute(NamedTuple):
 
 
 class Fp8Rows(NamedTuple):
-    """Row form of a matrix: q [rows, cols rounded up to 16], scale [ceil(cols / 128), rows]."""
+    """Row form of a matrix: q [rows, cols rounded up to 16], scale [ceil(cols /
+    128), rows], 8-bit exponents as in all three forms."""
     q: torch.Tensor
     scale: torch.Tensor
     cols: int
 
 
 class Fp8Cols(NamedTuple):
-    """Column form: q [128 * blocks, cols rounded up to 16], scale [blocks, cols rounded up to 4]."""
+    """Column form: q [128 * blocks, cols rounded up to 16], scale [blocks, cols]."""
     q: torch.Tensor
     scale: torch.Tensor
     rows: int
@@ -295,12 +296,12 @@ def gns_fp8_quantize(x, fmt="e4m3", route=None, gather=False, rows=True, cols=Tr
     q_r = s_r = q_c = s_c = None
     if rows:
         q_r = _new((n, ld), _FP8[fmt], x, stream)
-        s_r = _new((-(-c // BLOCK), n), torch.float32, x, stream)
+        s_r = _new((-(-c // BLOCK), n), torch.float8_e8m0fnu, x, stream)
     if cols:
         q_c = _new((blocks * BLOCK, ld), _FP8[fmt], x, stream)
-        s_c = _new((blocks, _up(c, 4)), torch.float32, x, stream)
+        s_c = _new((blocks, c), torch.float8_e8m0fnu, x, stream)
     check(load().gns_fp8_quantize(x.data_ptr(), ldx, DTYPES[x.dtype], n, c, _ptr(slots), topk, _ptr(offsets), groups, f,
-                                  _ptr(q_r), ld, _ptr(s_r), n, _ptr(q_c), ld, _ptr(s_c), _up(c, 4), _on(x, stream)),
+                                  _ptr(q_r), ld, _ptr(s_r), n, _ptr(q_c), ld, _ptr(s_c), c, _on(x, stream)),
           "gns_fp8_quantize")
     return (Fp8Rows(q_r, s_r, c) if rows else None), (Fp8Cols(q_c, s_c, n, c) if cols else None)
 
@@ -321,7 +322,7 @@ def gns_fp8_quantize_weight(w, fmt="e4m3", stream=None):
         ldw, stride = k, n * k
     ld = _up(k, 16)
     q = _new((groups, n, ld), _FP8[fmt], w, stream)
-    scale = _new((groups, -(-n // BLOCK), -(-k // BLOCK)), torch.float32, w, stream)
+    scale = _new((groups, -(-n // BLOCK), -(-k // BLOCK)), torch.float8_e8m0fnu, w, stream)
     check(load().gns_fp8_quantize_weight(w.data_ptr(), ldw, stride, DTYPES[w.dtype], groups, n, k, f, q.data_ptr(), ld,
                                          scale.data_ptr(), _on(w, stream)), "gns_fp8_quantize_weight")
     return Fp8Weight(q, scale, k, grouped)

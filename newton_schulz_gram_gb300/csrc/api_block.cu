@@ -4,7 +4,6 @@
 #include <algorithm>
 #include <cmath>
 #include <string>
-#include <tuple>
 
 #include "blockops.cuh"
 #include "dropout.cuh"
@@ -42,6 +41,30 @@ int map_u8(CUtensorMap* m, const void* p, int64_t inner, int64_t outer, int64_t 
     return GNS_OK;
 }
 
+// The map that whole rows of the product's output are stored through, where it
+// can be described (16-byte rows).
+int map_output(Fp8GemmJob& j) {
+    const bool split = j.split > 1;
+    const int es = split ? 4 : elem_bytes(j.out_dtype);
+    void* p = split ? static_cast<void*>(j.partial) : j.D;
+    const int64_t rows = j.wgrad ? j.M : j.rows, ld = split ? j.N : j.ldd;
+    const int64_t G = split ? j.split : j.wgrad ? j.G : 1;
+    const int64_t stride = split ? ld * rows : j.wgrad && j.G > 1 ? j.strideD : ld * rows;
+    j.bulk_store = !misaligned(p, 16) && ld * es % 16 == 0 && stride * es % 16 == 0;
+    if (!j.bulk_store) return GNS_OK;
+    const auto fn = encode_fn();
+    if (!fn) return fail(GNS_ERR_CUDA, "cuTensorMapEncodeTiled is unavailable");
+    cuuint64_t dims[3] = {static_cast<cuuint64_t>(j.N), static_cast<cuuint64_t>(rows), static_cast<cuuint64_t>(G)};
+    cuuint64_t strides[2] = {static_cast<cuuint64_t>(ld * es), static_cast<cuuint64_t>(stride * es)};
+    cuuint32_t box[3] = {static_cast<cuuint32_t>(128 / es), 32, 1};
+    cuuint32_t estr[3] = {1, 1, 1};
+    const CUresult r = fn(&j.mapD, es == 2 ? CU_TENSOR_MAP_DATA_TYPE_UINT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 3, p, dims,
+                          strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                          CU_TENSOR_MAP_L2_PROMOTION_NONE, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    if (r != CUDA_SUCCESS) return fail(GNS_ERR_INVALID, "cuTensorMapEncodeTiled failed for the output");
+    return GNS_OK;
+}
+
 int64_t up(int64_t v, int64_t a) { return (v + a - 1) / a * a; }
 
 // An 8-bit operand [outer][ld] with `inner` values per row.
@@ -68,8 +91,8 @@ int check_moves(int tokens, int topk, int num_experts, int cols, int dtype, cons
 }
 
 // The forward and the data-gradient product: A [rows][inner_a], D [rows][n_out].
-int product(const void* a, int64_t lda, const float* sa, int64_t ld_sa, int fmt_a, int rows, const void* w, int64_t ldw,
-            const float* sw, int fmt_w, int groups, int N, int K, bool dgrad, const int32_t* offsets, void* D,
+int product(const void* a, int64_t lda, const uint8_t* sa, int64_t ld_sa, int fmt_a, int rows, const void* w, int64_t ldw,
+            const uint8_t* sw, int fmt_w, int groups, int N, int K, bool dgrad, const int32_t* offsets, void* D,
             int64_t ldd, int out_dtype, DeviceState* st, size_t ws_used, cudaStream_t s) {
     const int inner = dgrad ? N : K, out = dgrad ? K : N;
     RET(check_q(a, inner, lda));
@@ -78,7 +101,7 @@ int product(const void* a, int64_t lda, const float* sa, int64_t ld_sa, int fmt_
     if (ld_sa < rows) return invalid("a scale's row stride must cover the rows");
     if (ldd < out) return invalid("the output's row stride must cover its columns");
     Fp8GemmJob j{};
-    const int cg = fp8_gemm_cg(rows, out, groups, offsets != nullptr, st->num_sms);
+    const int cg = fp8_gemm_cg(rows, out, offsets != nullptr, st->num_sms);
     j.split = offsets ? 1 : fp8_gemm_split(rows, out, inner, st->num_sms);
     RET(map_u8(&j.mapA, a, inner, rows, 1, lda, lda * rows, 128));
     RET(map_u8(&j.mapB, w, K, N, groups, ldw, ldw * N, fp8_gemm_b_box(cg, dgrad)));
@@ -104,6 +127,7 @@ int product(const void* a, int64_t lda, const float* sa, int64_t ld_sa, int fmt_
         RET(ensure_workspace(*st, ws_used + sizeof(float) * static_cast<size_t>(j.split) * rows * out));
         j.partial = reinterpret_cast<float*>(st->ws + ws_used);
     }
+    RET(map_output(j));
     begin_call(*st);
     j.st = st->status;
     LAUNCH(kClsFp8Gemm, launch_fp8_gemm(j, cg, st->num_sms, s));
@@ -221,8 +245,8 @@ int gns_moe_combine_backward(const void* dout, int64_t lddo, const void* y, int6
 }
 
 int gns_fp8_quantize(const void* x, int64_t ldx, int dtype, int rows, int cols, const int32_t* slots, int topk,
-                     const int32_t* offsets, int groups, int format, void* q_rows, int64_t ld_rows, float* scale_rows,
-                     int64_t ld_scale_rows, void* q_cols, int64_t ld_cols, float* scale_cols, int64_t ld_scale_cols,
+                     const int32_t* offsets, int groups, int format, void* q_rows, int64_t ld_rows, uint8_t* scale_rows,
+                     int64_t ld_scale_rows, void* q_cols, int64_t ld_cols, uint8_t* scale_cols, int64_t ld_scale_cols,
                      void* stream) {
     if (rows < 0 || rows > kMaxRows || cols < 1) return invalid("rows must be in 0..8388480 and cols >= 1");
     if (bad_dtype(dtype)) return invalid("unknown dtype");
@@ -239,8 +263,7 @@ int gns_fp8_quantize(const void* x, int64_t ldx, int dtype, int rows, int cols, 
     if (q_cols) {
         RET(check_q(q_cols, cols, ld_cols));
         if (!scale_cols) return invalid("null pointer");
-        if (misaligned(scale_cols, 16) || ld_scale_cols % 4 || ld_scale_cols < cols)
-            return invalid("column scales need 16-byte aligned rows that cover the columns");
+        if (ld_scale_cols < cols) return invalid("a scale's row stride must cover the columns");
     }
     if (!x) return invalid("null pointer");
     if (ldx < cols) return invalid("a row stride must cover the columns");
@@ -272,7 +295,7 @@ int gns_fp8_quantize(const void* x, int64_t ldx, int dtype, int rows, int cols, 
 }
 
 int gns_fp8_quantize_weight(const void* w, int64_t ldw, int64_t stride_w, int dtype, int groups, int N, int K,
-                            int format, void* q, int64_t ldq, float* scale, void* stream) {
+                            int format, void* q, int64_t ldq, uint8_t* scale, void* stream) {
     if (groups < 0 || N < 1 || N > kMaxRows || K < 1) return invalid("groups >= 0, N in 1..8388480 and K >= 1 required");
     if (bad_dtype(dtype)) return invalid("unknown dtype");
     if (bad_format(format)) return invalid("unknown 8-bit format");
@@ -288,8 +311,8 @@ int gns_fp8_quantize_weight(const void* w, int64_t ldw, int64_t stride_w, int dt
     return GNS_OK;
 }
 
-int gns_fp8_matmul(const void* a, int64_t lda, const float* scale_a, int64_t ld_scale_a, int format_a, int rows,
-                   const void* w, int64_t ldw, const float* scale_w, int format_w, int groups, int N, int K,
+int gns_fp8_matmul(const void* a, int64_t lda, const uint8_t* scale_a, int64_t ld_scale_a, int format_a, int rows,
+                   const void* w, int64_t ldw, const uint8_t* scale_w, int format_w, int groups, int N, int K,
                    const int32_t* offsets, void* y, int64_t ldy, int out_dtype, void* stream) {
     RET(check_product(format_a, format_w, groups, rows, N, K, offsets, out_dtype));
     if (rows == 0) return GNS_OK;
@@ -299,8 +322,8 @@ int gns_fp8_matmul(const void* a, int64_t lda, const float* scale_a, int64_t ld_
                    y, ldy, out_dtype, st, 0, static_cast<cudaStream_t>(stream));
 }
 
-int gns_fp8_matmul_dgrad(const void* dy, int64_t lddy, const float* scale_dy, int64_t ld_scale_dy, int format_dy,
-                         int rows, const void* w, int64_t ldw, const float* scale_w, int format_w, int groups, int N,
+int gns_fp8_matmul_dgrad(const void* dy, int64_t lddy, const uint8_t* scale_dy, int64_t ld_scale_dy, int format_dy,
+                         int rows, const void* w, int64_t ldw, const uint8_t* scale_w, int format_w, int groups, int N,
                          int K, const int32_t* offsets, void* dx, int64_t lddx, int out_dtype, void* stream) {
     RET(check_product(format_dy, format_w, groups, rows, N, K, offsets, out_dtype));
     if (rows == 0) return GNS_OK;
@@ -310,13 +333,19 @@ int gns_fp8_matmul_dgrad(const void* dy, int64_t lddy, const float* scale_dy, in
                    offsets, dx, lddx, out_dtype, st, 0, static_cast<cudaStream_t>(stream));
 }
 
-int gns_fp8_matmul_wgrad(const void* dy, int64_t lddy, const float* scale_dy, int64_t ld_scale_dy, int format_dy,
-                         const void* x, int64_t ldx, const float* scale_x, int64_t ld_scale_x, int format_x, int rows,
+int gns_fp8_matmul_wgrad(const void* dy, int64_t lddy, const uint8_t* scale_dy, int64_t ld_scale_dy, int format_dy,
+                         const void* x, int64_t ldx, const uint8_t* scale_x, int64_t ld_scale_x, int format_x, int rows,
                          int groups, int N, int K, const int32_t* offsets, void* dw, int64_t lddw, int64_t stride_dw,
                          int out_dtype, void* stream) {
     RET(check_product(format_dy, format_x, groups, rows, N, K, offsets, out_dtype));
     if (!dw) return invalid("null pointer");
     if (lddw < K || stride_dw < 0) return invalid("a row stride must cover the columns");
+    if (rows > 0) {
+        RET(check_q(dy, N, lddy));
+        RET(check_q(x, K, ldx));
+        if (!scale_dy || !scale_x) return invalid("null pointer");
+        if (ld_scale_dy < N || ld_scale_x < K) return invalid("a scale's row stride must cover the columns");
+    }
     DeviceState* st = nullptr;
     RET(get_state(&st));
     cudaStream_t s = static_cast<cudaStream_t>(stream);
@@ -326,15 +355,9 @@ int gns_fp8_matmul_wgrad(const void* dy, int64_t lddy, const float* scale_dy, in
             CK(cudaMemset2DAsync(static_cast<char*>(dw) + es * g * stride_dw, es * lddw, 0, es * K, N, s));
         return GNS_OK;
     }
-    RET(check_q(dy, N, lddy));
-    RET(check_q(x, K, ldx));
-    if (!scale_dy || !scale_x) return invalid("null pointer");
-    for (const auto& [p, ld, cols] : {std::tuple{scale_dy, ld_scale_dy, N}, std::tuple{scale_x, ld_scale_x, K}})
-        if (misaligned(p, 16) || ld % 4 || ld < cols)
-            return invalid("column scales need 16-byte aligned rows that cover the columns");
     Fp8GemmJob j{};
     const int64_t qrows = offsets ? static_cast<int64_t>(fp8_max_blocks(rows, groups)) * kFp8Block : up(rows, kFp8Block);
-    const int cg = fp8_gemm_cg(N, K, groups, false, st->num_sms);
+    const int cg = fp8_gemm_cg(N, K, groups > 1, st->num_sms);
     RET(map_u8(&j.mapA, dy, N, qrows, 1, lddy, lddy * qrows, 128));
     RET(map_u8(&j.mapB, x, K, qrows, 1, ldx, ldx * qrows, 128));
     j.wgrad = 1;
@@ -355,6 +378,7 @@ int gns_fp8_matmul_wgrad(const void* dy, int64_t lddy, const float* scale_dy, in
     j.strideD = stride_dw;
     j.out_dtype = out_dtype;
     j.split = 1;
+    RET(map_output(j));
     begin_call(*st);
     j.st = st->status;
     LAUNCH(kClsFp8Gemm, launch_fp8_gemm(j, cg, st->num_sms, s));
@@ -362,7 +386,7 @@ int gns_fp8_matmul_wgrad(const void* dy, int64_t lddy, const float* scale_dy, in
 }
 
 int gns_fp8_linear(const void* x, int64_t ldx, int dtype, int rows, const int32_t* slots, int topk,
-                   const int32_t* offsets, const void* w, int64_t ldw, const float* scale_w, int format_w, int groups,
+                   const int32_t* offsets, const void* w, int64_t ldw, const uint8_t* scale_w, int format_w, int groups,
                    int N, int K, void* y, int64_t ldy, int out_dtype, void* stream) {
     RET(check_product(GNS_E4M3, format_w, groups, rows, N, K, offsets, out_dtype));
     if (bad_dtype(dtype)) return invalid("unknown dtype");
@@ -382,11 +406,11 @@ int gns_fp8_linear(const void* x, int64_t ldx, int dtype, int rows, const int32_
     }
     const int64_t ldq = up(K, 16);
     const size_t q_bytes = static_cast<size_t>(up(ldq * rows, 256));
-    const size_t s_bytes = static_cast<size_t>(up(sizeof(float) * (up(K, kFp8Block) / kFp8Block) * rows, 256));
+    const size_t s_bytes = static_cast<size_t>(up(up(K, kFp8Block) / kFp8Block * rows, 256));
     const int split = offsets ? 1 : fp8_gemm_split(rows, N, K, st->num_sms);
     const size_t partial = split > 1 ? sizeof(float) * static_cast<size_t>(split) * rows * N : 0;
     RET(ensure_workspace(*st, q_bytes + s_bytes + partial));
-    float* scale = reinterpret_cast<float*>(st->ws + q_bytes);
+    uint8_t* scale = reinterpret_cast<uint8_t*>(st->ws + q_bytes);
     RET(gns_fp8_quantize(x, ldx, dtype, rows, K, slots, topk, nullptr, 1, GNS_E4M3, st->ws, ldq, scale, rows, nullptr, 0,
                          nullptr, 0, stream));
     return product(st->ws, ldq, scale, rows, GNS_E4M3, rows, w, ldw, scale_w, format_w, groups, N, K, false, offsets, y,

@@ -26,10 +26,10 @@ struct CastJob {
     int G;
     int fmt;
     uint8_t* q_rows;
-    float* s_rows;
+    uint8_t* s_rows;  // scales are 8-bit exponents: b stands for 2^(b - 127)
     long long ld_rows, lds_rows;
     uint8_t* q_cols;
-    float* s_cols;
+    uint8_t* s_cols;
     long long ld_cols, lds_cols;
 };
 
@@ -42,7 +42,7 @@ struct CastWeightJob {
     int dtype, G, rows, cols, fmt;
     uint8_t* q;
     long long ldq;  // matrices are rows * ldq apart
-    float* scale;   // [G][ceil(rows / 128)][ceil(cols / 128)]
+    uint8_t* scale;  // [G][ceil(rows / 128)][ceil(cols / 128)]
 };
 
 int launch_fp8_cast_weight(const CastWeightJob& job, cudaStream_t s);
@@ -62,16 +62,17 @@ __device__ __forceinline__ int blocks_of(int count) { return (count + kFp8Block 
 //   weight gradient (wgrad = 1): D[g][m][n], contraction the group's rows; A
 //     and B are column forms, [blocks * 128][M] and [blocks * 128][N].
 struct Fp8GemmJob {
-    CUtensorMap mapA, mapB;
+    CUtensorMap mapA, mapB, mapD;  // mapD: boxes of 32 rows of 128 bytes of the output (partial when split > 1)
+    int bulk_store;                // mapD holds (the output has 16-byte rows)
     int wgrad, b_mn;
     int fmt_a, fmt_b;
     int G;
     const int* offsets;  // or null: one group of all rows
     int rows;            // rows of all groups (capacity when offsets is given)
     int M, N, K;         // M: wgrad only; K: not for wgrad
-    const float* sA;     // [k block or token block][row or m], row stride ldsA
+    const uint8_t* sA;   // [k block or token block][row or m], row stride ldsA
     long long ldsA;
-    const float* sB;     // weights: scale of (g, n block, k block) at g * sB_g + nb * sB_n + kb * sB_k
+    const uint8_t* sB;   // weights: scale of (g, n block, k block) at g * sB_g + nb * sB_n + kb * sB_k
     long long sB_g, sB_n, sB_k;  // wgrad: [token block][n], row stride sB_k
     void* D;
     long long ldd, strideD;
@@ -83,7 +84,7 @@ struct Fp8GemmJob {
 
 // CTAs per tile (1: 128 x 256 tiles, 2: a pair, 256 x 256) for a product with M
 // rows (of all groups; the weight gradient: of each D) and N columns.
-int fp8_gemm_cg(int M, int N, int G, bool grouped, int num_sms);
+int fp8_gemm_cg(int M, int N, bool grouped, int num_sms);
 // Rows of the boxes of B's tensor map.
 inline int fp8_gemm_b_box(int cg, bool b_mn) { return b_mn || cg == 2 ? 128 : 256; }
 
@@ -105,7 +106,7 @@ struct Fp8RowsJob {
     int fmt_w;
     const uint8_t* w;
     long long ldw, stride_w;
-    const float* sw;  // [G][ceil(N / 128)][ceil(K / 128)]
+    const uint8_t* sw;  // [G][ceil(N / 128)][ceil(K / 128)]
     void* D;
     long long ldd;
     int out_dtype;

@@ -5,7 +5,7 @@
 //
 //   s = the smallest power of two with amax / s <= 1.75 * 2^e  (448 = 1.75 * 2^8
 //       for e4m3, 57344 = 1.75 * 2^15 for e5m2), at least 2^-126,
-//   q = x / s rounded to nearest even.
+//   q = x / s rounded to nearest even; s is kept as its 8-bit exponent.
 //
 // The scale is a power of two so that x / s and s q are exact: the only
 // rounding is the one to 8 bits, and a value's 8-bit form does not depend on
@@ -48,10 +48,225 @@ struct Tile {
     int sc_row;        // its row of column scales
 };
 
+// Two 16-bit values at a time: magnitudes and their maximum as packed words.
+// The maximum passes over a NaN and shows an infinity, whose block then takes
+// the finite maximum the slow way.
+template <typename T>
+struct Pair;
+template <>
+struct Pair<__nv_bfloat16> {
+    static constexpr uint32_t kInf = 0x7F80u;
+    static __device__ __forceinline__ uint32_t max(uint32_t a, uint32_t b) {
+        uint32_t r;
+        asm("max.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+        return r;
+    }
+    static __device__ __forceinline__ float lo(uint32_t w) { return __uint_as_float(w << 16); }
+    static __device__ __forceinline__ float hi(uint32_t w) { return __uint_as_float(w & 0xFFFF0000u); }
+};
+template <>
+struct Pair<__half> {
+    static constexpr uint32_t kInf = 0x7C00u;
+    static __device__ __forceinline__ uint32_t max(uint32_t a, uint32_t b) {
+        uint32_t r;
+        asm("max.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+        return r;
+    }
+    static __device__ __forceinline__ float lo(uint32_t w) {
+        return __half2float(__ushort_as_half(static_cast<unsigned short>(w)));
+    }
+    static __device__ __forceinline__ float hi(uint32_t w) {
+        return __half2float(__ushort_as_half(static_cast<unsigned short>(w >> 16)));
+    }
+};
+
+__device__ __forceinline__ uint32_t magnitudes(uint32_t w) { return w & 0x7FFF7FFFu; }
+
+// The same with infinities (and NaN) as zero.
+template <typename T>
+__device__ __forceinline__ uint32_t finite_magnitudes(uint32_t w) {
+    const uint32_t m = magnitudes(w);
+    return ((m & 0xFFFFu) < Pair<T>::kInf ? m & 0xFFFFu : 0u) | ((m >> 16) < Pair<T>::kInf ? m & 0xFFFF0000u : 0u);
+}
+
+// An infinity, or NaN alone, among the values behind these maxima.
+template <typename T>
+__device__ __forceinline__ bool has_infinity(uint32_t maxima) {
+    return (maxima & 0xFFFFu) >= Pair<T>::kInf || (maxima >> 16) >= Pair<T>::kInf;
+}
+
+// Eight values (four words) with their inverse scales to 8 bits.
+template <typename T, bool E5M2, bool INF>
+__device__ __forceinline__ uint2 cast_words(const uint4& p, const float (&inv)[8]) {
+    const uint32_t w[4] = {p.x, p.y, p.z, p.w};
+    float v[8];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        v[2 * i] = Pair<T>::lo(w[i]);
+        v[2 * i + 1] = Pair<T>::hi(w[i]);
+    }
+    if (INF) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] = no_infinity(v[i]);
+    }
+    return cast8<E5M2>(v, inv);
+}
+
+// The tile of 16-bit values: the general tile below with the maxima taken over
+// packed pairs (two rows' maxima travel through the shuffles in one word) and
+// the infinities out of the way. 8 instructions per value for both forms where
+// the general one takes about 20, which is what bounded it: 8192 x 14336 in
+// both forms ZZ us against 208.
+template <typename T, int MODE, bool E5M2>
+__device__ __forceinline__ void cast_tile16(const Tile& tl, const T* x, long long ldx, const int* slots, int topk,
+                                            int cols, bool vec, uint8_t* q_rows, long long ld_rows, uint8_t* s_rows,
+                                            long long lds_rows, uint8_t* q_cols, long long ld_cols, uint8_t* s_cols,
+                                            long long lds_cols, float (&part)[kWarps][128], float (&inv_col)[128]) {
+    constexpr int kTop = E5M2 ? 15 : 8;
+    using P2 = Pair<T>;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int cl = (threadIdx.x & 15) * 8;  // this thread's columns within the tile
+    const int rl = threadIdx.x >> 4;        // its row within a pass
+    const int c = tl.c0 + cl;
+    uint4 raw[kPasses];
+#pragma unroll
+    for (int p = 0; p < kPasses; ++p) {
+        const int r = 16 * p + rl;
+        raw[p] = make_uint4(0, 0, 0, 0);
+        if (r < tl.nrows && c < cols) {
+            const int row = tl.r0 + r;
+            const T* a = x + static_cast<long long>(slots ? slots[row] / topk : row) * ldx + c;
+            if (vec && c + 8 <= cols) {
+                raw[p] = *reinterpret_cast<const uint4*>(a);
+            } else {
+                uint32_t w[4] = {0, 0, 0, 0};
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                    if (c + i < cols)
+                        w[i >> 1] |= static_cast<uint32_t>(reinterpret_cast<const uint16_t*>(a)[i]) << (16 * (i & 1));
+                raw[p] = make_uint4(w[0], w[1], w[2], w[3]);
+            }
+        }
+    }
+    auto mag = [&](int p, int i) {
+        const uint32_t w[4] = {raw[p].x, raw[p].y, raw[p].z, raw[p].w};
+        return magnitudes(w[i]);
+    };
+    auto fin = [&](int p, int i) {
+        const uint32_t w[4] = {raw[p].x, raw[p].y, raw[p].z, raw[p].w};
+        return finite_magnitudes<T>(w[i]);
+    };
+    if (MODE & kRowForm) {
+        // Row maxima, passes p and p + 4 in the halves of one word.
+        uint32_t m[kPasses / 2];
+        auto row_maxima = [&](auto value) {
+#pragma unroll
+            for (int p = 0; p < kPasses / 2; ++p) {
+                const uint32_t a = P2::max(P2::max(value(p, 0), value(p, 1)), P2::max(value(p, 2), value(p, 3)));
+                const uint32_t b =
+                    P2::max(P2::max(value(p + 4, 0), value(p + 4, 1)), P2::max(value(p + 4, 2), value(p + 4, 3)));
+                m[p] = P2::max(__byte_perm(a, b, 0x5410), __byte_perm(a, b, 0x7632));
+            }
+#pragma unroll
+            for (int d = 8; d > 0; d >>= 1) {
+#pragma unroll
+                for (int p = 0; p < kPasses / 2; ++p) m[p] = P2::max(m[p], __shfl_xor_sync(0xffffffffu, m[p], d));
+            }
+        };
+        row_maxima(mag);
+        bool inf = false;
+#pragma unroll
+        for (int p = 0; p < kPasses / 2; ++p) inf |= has_infinity<T>(m[p]);
+        const bool slow = __any_sync(0xffffffffu, inf);
+        if (slow) row_maxima(fin);
+#pragma unroll
+        for (int p = 0; p < kPasses; ++p) {
+            const uint32_t e = scale_exponent(p < 4 ? P2::lo(m[p & 3]) : P2::hi(m[p & 3]), kTop);
+            const float s = exp_inverse(e);
+            const float inv[8] = {s, s, s, s, s, s, s, s};
+            const int r = 16 * p + rl;
+            if (r < tl.nrows) {
+                if (c < ld_rows)
+                    *reinterpret_cast<uint2*>(q_rows + static_cast<long long>(tl.r0 + r) * ld_rows + c) =
+                        slow ? cast_words<T, E5M2, true>(raw[p], inv) : cast_words<T, E5M2, false>(raw[p], inv);
+                if (cl == 0) s_rows[static_cast<long long>(tl.c0 / 128) * lds_rows + tl.r0 + r] = static_cast<uint8_t>(e);
+            }
+        }
+    }
+    if (MODE & (kColForm | kBlockForm)) {
+        uint32_t m[4];  // maxima of columns 2 i, 2 i + 1 over this thread's rows
+        auto col_maxima = [&](auto value) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                m[i] = value(0, i);
+#pragma unroll
+                for (int p = 1; p < kPasses; ++p) m[i] = P2::max(m[i], value(p, i));
+            }
+        };
+        col_maxima(mag);
+        const bool slow =
+            __syncthreads_or(has_infinity<T>(m[0]) || has_infinity<T>(m[1]) || has_infinity<T>(m[2]) || has_infinity<T>(m[3]));
+        if (slow) col_maxima(fin);
+        float iv[8];
+        if (MODE & kBlockForm) {  // one maximum for the tile
+            uint32_t a = P2::max(P2::max(m[0], m[1]), P2::max(m[2], m[3]));
+            a = P2::max(a, __byte_perm(a, a, 0x1032));
+#pragma unroll
+            for (int d = 16; d > 0; d >>= 1) a = P2::max(a, __shfl_xor_sync(0xffffffffu, a, d));
+            if (lane == 0) part[warp][0] = P2::lo(a);
+            __syncthreads();
+            float t = part[0][0];
+#pragma unroll
+            for (int w = 1; w < kWarps; ++w) t = fmaxf(t, part[w][0]);
+            const uint32_t e = scale_exponent(t, kTop);
+            if (threadIdx.x == 0) *s_cols = static_cast<uint8_t>(e);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) iv[i] = exp_inverse(e);
+        } else {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) m[i] = P2::max(m[i], __shfl_xor_sync(0xffffffffu, m[i], 16));
+            if (lane < 16) {
+#pragma unroll
+                for (int i = 0; i < 4; i += 2)
+                    *reinterpret_cast<float4*>(&part[warp][cl + 2 * i]) =
+                        make_float4(P2::lo(m[i]), P2::hi(m[i]), P2::lo(m[i + 1]), P2::hi(m[i + 1]));
+            }
+            __syncthreads();
+            if (threadIdx.x < 128) {
+                float t = part[0][threadIdx.x];
+#pragma unroll
+                for (int w = 1; w < kWarps; ++w) t = fmaxf(t, part[w][threadIdx.x]);
+                const uint32_t e = scale_exponent(t, kTop);
+                inv_col[threadIdx.x] = exp_inverse(e);
+                if (tl.c0 + static_cast<int>(threadIdx.x) < cols)
+                    s_cols[static_cast<long long>(tl.sc_row) * lds_cols + tl.c0 + threadIdx.x] = static_cast<uint8_t>(e);
+            }
+            __syncthreads();
+#pragma unroll
+            for (int i = 0; i < 8; i += 4) {
+                const float4 f = *reinterpret_cast<const float4*>(&inv_col[cl + i]);
+                iv[i] = f.x, iv[i + 1] = f.y, iv[i + 2] = f.z, iv[i + 3] = f.w;
+            }
+        }
+#pragma unroll
+        for (int p = 0; p < kPasses; ++p) {
+            const int r = 16 * p + rl;
+            // The column form is zero to the end of its last block of 128
+            // rows (the rows past nrows were loaded as zero).
+            if (c < ld_cols && (!(MODE & kBlockForm) || r < tl.nrows))
+                *reinterpret_cast<uint2*>(q_cols + (tl.qc_row + r) * ld_cols + c) =
+                    slow ? cast_words<T, E5M2, true>(raw[p], iv) : cast_words<T, E5M2, false>(raw[p], iv);
+        }
+        // part is written again only after the next tile's barrier; its readers
+        // of inv_col and part are past theirs by then.
+    }
+}
+
+// The tile of any type, value by value.
 template <typename T, int MODE, bool E5M2>
 __device__ __forceinline__ void cast_tile(const Tile& tl, const T* x, long long ldx, const int* slots, int topk,
-                                          int cols, bool vec, uint8_t* q_rows, long long ld_rows, float* s_rows,
-                                          long long lds_rows, uint8_t* q_cols, long long ld_cols, float* s_cols,
+                                          int cols, bool vec, uint8_t* q_rows, long long ld_rows, uint8_t* s_rows,
+                                          long long lds_rows, uint8_t* q_cols, long long ld_cols, uint8_t* s_cols,
                                           long long lds_cols, float (&part)[kWarps][128], float (&inv_col)[128]) {
     constexpr int kTop = E5M2 ? 15 : 8;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -107,7 +322,7 @@ __device__ __forceinline__ void cast_tile(const Tile& tl, const T* x, long long 
                     *reinterpret_cast<uint2*>(q_rows + static_cast<long long>(tl.r0 + r) * ld_rows + c) =
                         cast8<E5M2>(w, iv);
                 }
-                if (cl == 0) s_rows[static_cast<long long>(tl.c0 / 128) * lds_rows + tl.r0 + r] = exp_value(e);
+                if (cl == 0) s_rows[static_cast<long long>(tl.c0 / 128) * lds_rows + tl.r0 + r] = static_cast<uint8_t>(e);
             }
         }
     }
@@ -138,7 +353,7 @@ __device__ __forceinline__ void cast_tile(const Tile& tl, const T* x, long long 
                 const uint32_t e = scale_exponent(m, kTop);
                 inv_col[threadIdx.x] = exp_inverse(e);
                 if (tl.c0 + static_cast<int>(threadIdx.x) < cols)
-                    s_cols[static_cast<long long>(tl.sc_row) * lds_cols + tl.c0 + threadIdx.x] = exp_value(e);
+                    s_cols[static_cast<long long>(tl.sc_row) * lds_cols + tl.c0 + threadIdx.x] = static_cast<uint8_t>(e);
             }
             __syncthreads();
         }
@@ -148,7 +363,7 @@ __device__ __forceinline__ void cast_tile(const Tile& tl, const T* x, long long 
 #pragma unroll
             for (int w = 1; w < kWarps; ++w) m = fmaxf(m, part[w][0]);
             const uint32_t e = scale_exponent(m, kTop);
-            if (threadIdx.x == 0) *s_cols = exp_value(e);
+            if (threadIdx.x == 0) *s_cols = static_cast<uint8_t>(e);
 #pragma unroll
             for (int i = 0; i < 8; ++i) iv[i] = exp_inverse(e);
         } else {
@@ -177,7 +392,7 @@ __device__ __forceinline__ void cast_tile(const Tile& tl, const T* x, long long 
 
 // blockIdx.y: token block; blockIdx.x: the first of the `span` column blocks.
 template <typename T, int MODE, bool E5M2>
-__global__ void __launch_bounds__(kThreads) fp8_cast_kernel(CastJob j, bool vec, int span) {
+__global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 4 : 2) fp8_cast_kernel(CastJob j, bool vec, int span) {
     __shared__ float part[kWarps][128];
     __shared__ __align__(16) float inv_col[128];
     __shared__ int found[3];
@@ -230,13 +445,19 @@ __global__ void __launch_bounds__(kThreads) fp8_cast_kernel(CastJob j, bool vec,
     const int nblk = (j.cols + kFp8Block - 1) / kFp8Block;
     for (int cb = blockIdx.x * span; cb < min(nblk, static_cast<int>(blockIdx.x + 1) * span); ++cb) {
         tl.c0 = cb * kFp8Block;
-        cast_tile<T, MODE, E5M2>(tl, static_cast<const T*>(j.x), j.ldx, j.slots, j.topk, j.cols, vec, j.q_rows, j.ld_rows,
-                                 j.s_rows, j.lds_rows, j.q_cols, j.ld_cols, j.s_cols, j.lds_cols, part, inv_col);
+        if constexpr (sizeof(T) == 2)
+            cast_tile16<T, MODE, E5M2>(tl, static_cast<const T*>(j.x), j.ldx, j.slots, j.topk, j.cols, vec, j.q_rows,
+                                       j.ld_rows, j.s_rows, j.lds_rows, j.q_cols, j.ld_cols, j.s_cols, j.lds_cols, part,
+                                       inv_col);
+        else
+            cast_tile<T, MODE, E5M2>(tl, static_cast<const T*>(j.x), j.ldx, j.slots, j.topk, j.cols, vec, j.q_rows,
+                                     j.ld_rows, j.s_rows, j.lds_rows, j.q_cols, j.ld_cols, j.s_cols, j.lds_cols, part,
+                                     inv_col);
     }
 }
 
 template <typename T, bool E5M2>
-__global__ void __launch_bounds__(kThreads) fp8_cast_weight_kernel(CastWeightJob j, bool vec) {
+__global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 4 : 2) fp8_cast_weight_kernel(CastWeightJob j, bool vec) {
     __shared__ float part[kWarps][128];
     __shared__ __align__(16) float inv_col[128];
     grid_dependency_wait();
@@ -249,9 +470,14 @@ __global__ void __launch_bounds__(kThreads) fp8_cast_weight_kernel(CastWeightJob
         tl.c0 = blockIdx.x * kFp8Block;
         tl.qc_row = static_cast<long long>(g) * j.rows + tl.r0;
         tl.sc_row = 0;
-        float* scale = j.scale + (static_cast<long long>(g) * nb + blockIdx.y) * kb + blockIdx.x;
-        cast_tile<T, kBlockForm, E5M2>(tl, static_cast<const T*>(j.w) + g * j.stride_w, j.ldw, nullptr, 1, j.cols, vec,
-                                       nullptr, 0, nullptr, 0, j.q, j.ldq, scale, 0, part, inv_col);
+        uint8_t* scale = j.scale + (static_cast<long long>(g) * nb + blockIdx.y) * kb + blockIdx.x;
+        const T* w = static_cast<const T*>(j.w) + g * j.stride_w;
+        if constexpr (sizeof(T) == 2)
+            cast_tile16<T, kBlockForm, E5M2>(tl, w, j.ldw, nullptr, 1, j.cols, vec, nullptr, 0, nullptr, 0, j.q, j.ldq,
+                                             scale, 0, part, inv_col);
+        else
+            cast_tile<T, kBlockForm, E5M2>(tl, w, j.ldw, nullptr, 1, j.cols, vec, nullptr, 0, nullptr, 0, j.q, j.ldq,
+                                           scale, 0, part, inv_col);
     }
 }
 

@@ -36,7 +36,6 @@
 // data gradient, both operands of the weight gradient) are read MN-major
 // through the shared-memory descriptor; nothing is transposed in memory.
 #include <algorithm>
-#include <cstdlib>
 
 #include "blockops.cuh"
 #include "fp8.cuh"
@@ -70,7 +69,7 @@ static_assert(BN - kAcc1 <= 32, "the overlap lies in one chunk of 32 columns of 
 // 256 tiles with paired MMAs; each stages its 128 rows of A and 128 of B's 256.
 template <int CG>
 struct Cfg {
-    static constexpr int STAGES = CG == 1 ? 3 : 5;
+    static constexpr int STAGES = CG == 1 ? 3 : 4;
     static constexpr int BNH = BN / CG;  // rows of B a CTA stages
     static constexpr uint32_t B_BYTES = BNH * BK;
     static constexpr int TM = BM * CG;
@@ -85,7 +84,7 @@ constexpr uint32_t kSlotBytes = 512 + 1024;
 constexpr int kSegment = 16;  // k blocks of a segment of an fp32 result
 static_assert(kSegment % kSlotBlocks == 0, "a scale slot lies in one segment");
 constexpr int kStageRow = 128;               // bytes of a row staged for the output stores
-constexpr int kStageBytes = 32 * kStageRow;  // per epilogue warp
+constexpr int kStageBytes = 32 * kStageRow;  // a buffer of an epilogue warp, which has two
 
 constexpr int kTileSlots = 4;
 constexpr int kTileReaders = 2 + kSlotBlocks + kEpiWarps;  // producer, MMA issuer, scale builder, epilogue warps
@@ -111,7 +110,7 @@ struct Groups {
 template <int CG>
 constexpr int smem_bytes() {
     return 1024 + Cfg<CG>::STAGES * static_cast<int>(A_BYTES + Cfg<CG>::B_BYTES) + kScaleSlots * static_cast<int>(kSlotBytes) +
-           kEpiWarps * kStageBytes + kTileSlots * static_cast<int>(sizeof(Tile)) + num_bars(Cfg<CG>::STAGES) * 8 + 16 +
+           kEpiWarps * 2 * kStageBytes + kTileSlots * static_cast<int>(sizeof(Tile)) + num_bars(Cfg<CG>::STAGES) * 8 + 16 +
            static_cast<int>(sizeof(Groups));
 }
 static_assert(smem_bytes<1>() <= 232448 && smem_bytes<2>() <= 232448, "shared memory budget");
@@ -272,21 +271,32 @@ __device__ __forceinline__ uint32_t add_bits(uint32_t a, uint32_t b) {
     return __float_as_uint(__uint_as_float(a) + __uint_as_float(b));
 }
 
-// 128 / ES columns of the warp's 32 rows (a thread holds one row), clipped to
-// rows x left, to d (row stride ldd elements of ES bytes). The rows
-// go through shared memory (16-byte pieces, piece index XOR row mod 8), so that
-// a store instruction writes four whole 128-byte lines where rows start on
+// Stores (or, with `add`, adds, fp32) a staged block of 32 rows of 128 bytes,
+// asynchronously, clipped to the map's extents.
+__device__ __forceinline__ void bulk_store(const CUtensorMap* m, uint32_t src, int c0, int c1, int c2, bool add) {
+    if (add)
+        asm volatile("cp.reduce.async.bulk.tensor.3d.global.shared::cta.add.tile.bulk_group [%0, {%2, %3, %4}], [%1];" ::"l"(
+                         reinterpret_cast<uint64_t>(m)),
+                     "r"(src), "r"(c0), "r"(c1), "r"(c2)
+                     : "memory");
+    else
+        asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.tile.bulk_group [%0, {%2, %3, %4}], [%1];" ::"l"(
+                         reinterpret_cast<uint64_t>(m)),
+                     "r"(src), "r"(c0), "r"(c1), "r"(c2)
+                     : "memory");
+    asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+}
+
+// Writes a staged block (32 rows of 128 bytes, 16-byte piece index XOR row mod
+// 8), clipped to rows x left, to d (row stride ldd elements of ES bytes): a
+// store instruction covers four whole 128-byte lines where rows start on
 // 16-byte boundaries, and runs of neighbouring elements where they do not. With
 // `add` (fp32) the stored values are added to; a lane meets its own stores.
 template <int ES>
-__device__ __forceinline__ void store_pass(uint32_t stage, uint8_t* d, long long ldd, int rows, int left,
-                                           const uint32_t (&w)[32], bool aligned, bool add, int lane) {
+__device__ __forceinline__ void store_rows(uint32_t stage, uint8_t* d, long long ldd, int rows, int left, bool aligned,
+                                           bool add, int lane) {
     constexpr int PASS = kStageRow / ES;  // columns
     constexpr int PIECE = 16 / ES;        // elements of a 16-byte piece
-#pragma unroll
-    for (int k = 0; k < 8; ++k)
-        st_shared_v4(stage + lane * kStageRow + ((k ^ (lane & 7)) << 4), w[4 * k], w[4 * k + 1], w[4 * k + 2], w[4 * k + 3]);
-    __syncwarp();
     if (aligned) {
         const int k = lane & 7, r0 = lane >> 3;
         uint4 piece[8];  // all reads first
@@ -368,9 +378,9 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_gemm_kernel(const __grid_cons
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     uint8_t* sA = smem;
     uint8_t* sB = sA + STAGES * A_BYTES;
-    uint8_t* scales = sB + STAGES * B_BYTES;
-    uint8_t* staging = scales + kScaleSlots * kSlotBytes;
-    Tile* tiles = reinterpret_cast<Tile*>(staging + kEpiWarps * kStageBytes);
+    uint8_t* staging = sB + STAGES * B_BYTES;  // 1024-byte aligned, as the swizzle wants
+    uint8_t* scales = staging + kEpiWarps * 2 * kStageBytes;
+    Tile* tiles = reinterpret_cast<Tile*>(scales + kScaleSlots * kSlotBytes);
     uint64_t* bars = reinterpret_cast<uint64_t*>(tiles + kTileSlots);
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + num_bars(STAGES));
     Groups* gr = reinterpret_cast<Groups*>(tmem_slot + 4);
@@ -416,6 +426,7 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_gemm_kernel(const __grid_cons
         fence_mbar_init();
         prefetch_tmap(&P.mapA);
         prefetch_tmap(&P.mapB);
+        if (P.bulk_store) prefetch_tmap(&P.mapD);
     }
     if (warp == 1) {
         tmem_alloc<CG>(smem_u32(tmem_slot), kTmemCols);
@@ -636,14 +647,13 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_gemm_kernel(const __grid_cons
         Tile tl;
         for (int i = 0; ok && take(i, tl, true); ++i) {
             const int arow = tl.m0 + BM * rank + lane;
-            const float* pa = P.sA + tl.row0 + arow;
-            const float* pb = P.sB + (wgrad ? tl.n0 + lane
+            const uint8_t* pa = P.sA + tl.row0 + arow;
+            const uint8_t* pb = P.sB + (wgrad ? tl.n0 + lane
                                             : tl.g * P.sB_g + static_cast<long long>(tl.n0 / kFp8Block) * P.sB_n);
-            for (int kb0 = tl.kb0; kb0 < tl.kb1; kb0 += kSlotBlocks, ++groups) {
-                const int kb = kb0 + j;
+            // Rows outside have some valid element's scale: nothing of theirs is stored.
+            uint8_t va[4], vb[8];
+            auto load = [&](int kb) {
                 const bool in = kb < tl.kb1;
-                // Rows outside have some valid element's scale: nothing of theirs is stored.
-                float va[4], vb[8];
 #pragma unroll
                 for (int r = 0; r < 4; ++r)
                     va[r] = __ldg(in && arow + 32 * r < tl.rows ? pa + kb * P.ldsA + 32 * r : P.sA);
@@ -653,12 +663,19 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_gemm_kernel(const __grid_cons
                         vb[r] = __ldg(in && tl.n0 + lane + 32 * r < P.N ? pb + kb * P.sB_k + 32 * r : P.sB);
                 } else {
 #pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        const float v = __ldg(in && tl.n0 + 128 * h < P.N ? pb + kb * P.sB_k + h * P.sB_n : P.sB);
-#pragma unroll
-                        for (int r = 0; r < 4; ++r) vb[4 * h + r] = v;
-                    }
+                    for (int h = 0; h < 2; ++h)
+                        vb[h] = __ldg(in && tl.n0 + 128 * h < P.N ? pb + kb * P.sB_k + h * P.sB_n : P.sB);
                 }
+            };
+            load(tl.kb0 + j);
+            for (int kb0 = tl.kb0; kb0 < tl.kb1; kb0 += kSlotBlocks, ++groups) {
+                // This slot's exponents, then the loads for the next one.
+                uint32_t ea[4], eb[8];
+#pragma unroll
+                for (int r = 0; r < 4; ++r) ea[r] = va[r];
+#pragma unroll
+                for (int r = 0; r < 8; ++r) eb[r] = wgrad ? vb[r] : vb[r >> 2];
+                load(kb0 + kSlotBlocks + j);
                 const int slot = groups % kScaleSlots;
                 if (!__all_sync(0xffffffffu, mbar_wait(sempty0 + 8 * slot, ((groups / kScaleSlots) & 1) ^ 1, err))) {
                     ok = false;
@@ -666,9 +683,9 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_gemm_kernel(const __grid_cons
                 }
                 const uint32_t at = ring + slot * kSlotBytes + 16 * lane + j;
 #pragma unroll
-                for (int r = 0; r < 4; ++r) st_shared_u8(at + 4 * r, __float_as_uint(va[r]) >> 23);
+                for (int r = 0; r < 4; ++r) st_shared_u8(at + 4 * r, ea[r]);
 #pragma unroll
-                for (int r = 0; r < 8; ++r) st_shared_u8(at + 512 + 128 * (r & ~3) + 4 * (r & 3), __float_as_uint(vb[r]) >> 23);
+                for (int r = 0; r < 8; ++r) st_shared_u8(at + 512 + 128 * (r & ~3) + 4 * (r & 3), eb[r]);
                 asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // tcgen05.cp reads through the async proxy
                 __syncwarp();
                 if (lane == 0) {
@@ -713,7 +730,7 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_gemm_kernel(const __grid_cons
         const int q = warp & 3;  // TMEM lane quarter this warp may read
         const int ew = warp - kEpiWarp0;
         const int half = ew >> 2;  // columns 128 half .. + 127 of the tile
-        const uint32_t stage = smem_u32(staging + ew * kStageBytes);
+        const uint32_t stage0 = smem_u32(staging + ew * 2 * kStageBytes);
         const uint32_t acce_lead = CG == 2 ? map_to_rank(acce0, 0) : acce0;
         const uint32_t overlap_lead = CG == 2 ? map_to_rank(overlap_bar, 0) : overlap_bar;
         auto hand_back = [&](uint32_t bar) {
@@ -726,7 +743,8 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_gemm_kernel(const __grid_cons
                     mbar_arrive_relaxed(bar);
             }
         };
-        int it = 0;  // segments read; the accumulator is it & 1
+        int it = 0;         // segments read; the accumulator is it & 1
+        uint32_t turn = 0;  // staging buffer of the next pass
         bool ok = true;
         Tile tl;
         for (int i = 0; ok && take(i, tl, true); ++i) {
@@ -747,6 +765,9 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_gemm_kernel(const __grid_cons
             const int passes = es == 2 ? 2 : 4;
             const bool bf16 = P.out_dtype == GNS_BF16;
             int kb = tl.kb0;
+            // 32 whole rows leave by a bulk store; the ragged end of a group,
+            // and outputs without 16-byte rows, by the warp's own stores.
+            const bool bulk = P.bulk_store && live && rows >= 32;
             do {  // segments; once, with zeros, for a group without rows to sum over
                 const bool filled = kb < tl.kb1;
                 const int buf = it & 1;
@@ -761,6 +782,7 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_gemm_kernel(const __grid_cons
                 // The chunk in the overlap comes first: accumulator 0's last
                 // columns (the second half's warps), accumulator 1's first.
                 const bool mine = half == (buf == 0);
+                bool fresh = true;  // no pass of this segment has been stored
 #pragma unroll 1
                 for (int n = 0; n < passes; ++n) {
                     const int p = buf == 0 ? passes - 1 - n : n;
@@ -790,17 +812,46 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_gemm_kernel(const __grid_cons
                         if (n == passes - 1) hand_back(acce_lead + 8 * buf);
                     }
                     const int c0 = p * (kStageRow / es);
-                    if (live && c0 < ncol) {
-                        if (es == 2)
-                            store_pass<2>(stage, d + c0 * 2, ldd, rows, ncol - c0, w, aligned, false, lane);
+                    if (!live || c0 >= ncol) continue;
+                    // The two buffers take turns: all bulk stores but the last
+                    // have read theirs (all, before one that the warp's own
+                    // stores use, which no group counts). Before a segment is
+                    // added, the stores it adds to are complete.
+                    const uint32_t stage = stage0 + turn * kStageBytes;
+                    const bool add = kb > tl.kb0;
+                    turn ^= 1;
+                    if (lane == 0) {
+                        if (add && fresh)
+                            asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
+                        else if (bulk)
+                            asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");
                         else
-                            store_pass<4>(stage, d + c0 * 4, ldd, rows, ncol - c0, w, aligned, kb > tl.kb0, lane);
+                            asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+                    }
+                    fresh = false;
+                    __syncwarp();
+#pragma unroll
+                    for (int k = 0; k < 8; ++k)
+                        st_shared_v4(stage + lane * kStageRow + ((k ^ (lane & 7)) << 4), w[4 * k], w[4 * k + 1], w[4 * k + 2],
+                                     w[4 * k + 3]);
+                    if (bulk) {
+                        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                        __syncwarp();
+                        if (lane == 0)
+                            bulk_store(&P.mapD, stage, col + c0, static_cast<int>(row0), split ? tl.split : wgrad ? tl.g : 0, add);
+                    } else {
+                        __syncwarp();
+                        if (es == 2)
+                            store_rows<2>(stage, d + c0 * 2, ldd, rows, ncol - c0, aligned, false, lane);
+                        else
+                            store_rows<4>(stage, d + c0 * 4, ldd, rows, ncol - c0, aligned, add, lane);
                     }
                 }
                 it += filled;
                 kb = segment < tl.kb1 - kb ? kb + segment : tl.kb1;
             } while (kb < tl.kb1);
         }
+        if (lane == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");  // the stores are complete
         __syncwarp();
     }
 
@@ -883,10 +934,15 @@ int fp8_gemm_split(int rows, int N, int K, int num_sms) {
     return static_cast<int>(std::max<long long>(1, std::min<long long>(num_sms / tiles, kb / 4)));
 }
 
-int fp8_gemm_cg(int M, int N, int G, bool grouped, int num_sms) {
-    static const char* f = std::getenv("GNS_FP8_CG");
-    if (f) return std::atoi(f);
-    return 1;
+int fp8_gemm_cg(int M, int N, bool grouped, int num_sms) {
+    // A pair loads and reads from shared memory 32 KB per k block and SM where a
+    // single CTA takes 48 KB (8192 x 14336 x 4096, the three products: 317, 349
+    // and 356 us with pairs, 358, 379 and 387 us without), but its tile of 256
+    // rows wastes more of a ragged group (256 experts of 512 x 2048, 65536
+    // rows: 97, 140 and 170 us with pairs, 92, 139 and 156 us without) and needs
+    // enough tiles for all pairs (1021 x 712 x 4093: 18, 12, 18 against 17, 11, 16).
+    const long long tiles = static_cast<long long>((M + 255) / 256) * ((N + BN - 1) / BN);
+    return !grouped && tiles >= num_sms / 2 ? 2 : 1;
 }
 
 int launch_fp8_gemm(const Fp8GemmJob& job, int cg, int num_sms, cudaStream_t s) {

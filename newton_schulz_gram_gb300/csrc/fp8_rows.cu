@@ -112,7 +112,7 @@ __global__ void __launch_bounds__(kThreads) fp8_rows_kernel(Fp8RowsJob j, bool v
     const int gq = lane >> 2, t = lane & 3;
     const uint8_t* wg = j.w + g * j.stride_w;
     const int nkb = (j.K + kFp8Block - 1) / kFp8Block;
-    const float* sw = j.sw + (static_cast<long long>(g) * ((j.N + kFp8Block - 1) / kFp8Block) + n0 / kFp8Block) * nkb;
+    const uint8_t* sw = j.sw + (static_cast<long long>(g) * ((j.N + kFp8Block - 1) / kFp8Block) + n0 / kFp8Block) * nkb;
     const T* xrow = nullptr;  // the row of x of this lane's column
     if (gq < count) {
         const int r = r0 + gq;
@@ -160,7 +160,7 @@ __global__ void __launch_bounds__(kThreads) fp8_rows_kernel(Fp8RowsJob j, bool v
             amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
             const uint32_t e = scale_exponent(amax, 8);
             const float inv = exp_inverse(e);
-            const float s = sw[kb] * exp_value(e);  // of this lane's column
+            const float s = exp_value(sw[kb]) * exp_value(e);  // of this lane's column
             uint32_t b[2][4];
 #pragma unroll
             for (int c = 0; c < 2; ++c)

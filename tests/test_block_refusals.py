@@ -52,11 +52,11 @@ BAD = {
     "gns_moe_combine": [(3, -1), (4, 0), (5, 1025), (6, -1), (7, 9), (8, None), (9, None)],
     "gns_moe_combine_backward": [(4, None), (5, -1), (6, 0), (7, 1025), (8, -1), (9, 9), (10, None)],
     "gns_fp8_quantize": [(2, 5), (3, -1), (3, 1 << 30), (4, 0), (9, 2), (11, 8), (11, 24), (12, None), (13, 3), (15, 24),
-                         (16, None), (16, P + 4), (17, 6), (17, 4), (10, P + 8)],
+                         (16, None), (17, 7), (17, 4), (10, P + 8)],
     "gns_fp8_quantize_weight": [(3, 4), (4, -1), (5, 0), (6, 0), (7, 7), (8, None), (8, P + 1), (9, 20)],
     "gns_fp8_matmul": [(4, 2), (5, -1), (9, 3), (10, 0), (10, 1025), (10, 2), (11, 0), (12, 0), (16, 8)],
     "gns_fp8_matmul_dgrad": [(4, 2), (5, -1), (9, 3), (10, 0), (10, 1025), (10, 2), (11, 0), (12, 0), (16, 8)],
-    "gns_fp8_matmul_wgrad": [(4, 2), (9, 2), (10, -1), (11, 0), (11, 2), (12, 0), (13, 0), (15, None), (16, 7), (18, 4)],
+    "gns_fp8_matmul_wgrad": [(4, 2), (9, 2), (10, -1), (11, 0), (11, 2), (12, 0), (13, 0), (15, None), (16, 7), (18, 4), (3, 7), (8, 7)],
     "gns_fp8_linear": [(2, 3), (3, -1), (8, 24), (9, None), (10, 2), (11, 0), (11, 2), (12, 0), (13, 0), (14, None), (15, 4),
                        (16, 3), (1, 7)],
 }

@@ -21,19 +21,24 @@ def gns():
     assert m.gns_get_status() == 0
 
 
+def scales(t):
+    """The powers of two that 8-bit exponents stand for."""
+    return np.ldexp(1.0, t.view(torch.uint8).cpu().numpy().astype(np.int64) - 127)
+
+
 def values_rows(a):
-    s = f64(a.scale).repeat(128, 0)[:a.cols].T
+    s = scales(a.scale).repeat(128, 0)[:a.cols].T
     return f64(a.q.float())[:, :a.cols] * s
 
 
 def values_weight(w):
     n, k = w.q.shape[1], w.cols
-    return f64(w.q.float())[:, :, :k] * f64(w.scale).repeat(128, 1)[:, :n].repeat(128, 2)[:, :, :k]
+    return f64(w.q.float())[:, :, :k] * scales(w.scale).repeat(128, 1)[:, :n].repeat(128, 2)[:, :, :k]
 
 
 def values_cols(c, offsets=None):
     """[rows, cols] in sorted order; zero past the last group."""
-    v = f64(c.q.float())[:, :c.cols] * f64(c.scale).repeat(128, 0)[:, :c.cols]
+    v = f64(c.q.float())[:, :c.cols] * scales(c.scale).repeat(128, 0)[:, :c.cols]
     if offsets is None:
         return v[:c.rows]
     out, block = np.zeros((c.rows, c.cols)), 0
@@ -78,9 +83,9 @@ def test_cast_matches_the_oracle(gns, fmt, dtype, rows, cols, pad):
     r, c = gns.gns_fp8_quantize(x, fmt=fmt)
     w = gns.gns_fp8_quantize_weight(x, fmt=fmt)
     for (scale, v), got_scale, got in ((B.fp8_rows(f64(x), fmt), r.scale, values_rows(r)),
-                                       (B.fp8_cols(f64(x), fmt), c.scale[:, :cols], values_cols(c)),
+                                       (B.fp8_cols(f64(x), fmt), c.scale, values_cols(c)),
                                        (B.fp8_blocks(f64(x), fmt), w.scale[0], values_weight(w)[0])):
-        assert np.array_equal(f64(got_scale), scale) and np.array_equal(got, v)
+        assert np.array_equal(scales(got_scale), scale) and np.array_equal(got, v)
     assert torch.all(r.q[:, cols:].float() == 0) and torch.all(w.q[:, :, cols:].float() == 0)
     assert torch.all(c.q[rows:].float() == 0) and torch.all(c.q[:, cols:].float() == 0)
     only_r, none = gns.gns_fp8_quantize(x, fmt=fmt, cols=False)
@@ -89,22 +94,30 @@ def test_cast_matches_the_oracle(gns, fmt, dtype, rows, cols, pad):
     assert none is None and torch.equal(only_c.q.view(torch.uint8), c.q.view(torch.uint8))
 
 
+@pytest.mark.parametrize("dtype", sorted(DTYPES))
 @pytest.mark.parametrize("fmt", ["e4m3", "e5m2"])
-def test_cast_of_extremes(gns, fmt):
-    x = torch.zeros(4, 512, device="cuda")
+def test_cast_of_extremes(gns, fmt, dtype):
+    x = torch.zeros(300, 640, device="cuda")
     x[0, 0], x[0, 1], x[0, 2] = float("nan"), float("inf"), 1.0
     x[0, 128], x[0, 129] = torch.finfo(torch.float32).max, 1.0
     x[0, 256], x[0, 257] = 2.0 ** -149, -(2.0 ** -140)
-    x[1, 384:] = torch.linspace(-448, 448, 128)
+    x[1, 384:512] = torch.linspace(-448, 448, 128)
     x[2, :128] = float("-inf")
+    x[3, 128:256] = float("nan")
+    x[140:268, 7] = float("nan")
+    x[128:256, 200], x[200, 200] = 3.0, float("inf")
+    x[256:, 512:], x[270, 600] = 0.7, float("nan")
+    x[290, 256:512] = torch.finfo(DTYPES[dtype]).max
+    x[291, 256:512] = torch.finfo(DTYPES[dtype]).smallest_normal
+    x = x.to(DTYPES[dtype])
     r, c = gns.gns_fp8_quantize(x, fmt=fmt)
     scale, v = B.fp8_rows(f64(x), fmt)
-    assert np.array_equal(f64(r.scale), scale) and np.array_equal(values_rows(r), v, equal_nan=True)
+    assert np.array_equal(scales(r.scale), scale) and np.array_equal(values_rows(r), v, equal_nan=True)
     scale, v = B.fp8_cols(f64(x), fmt)
-    assert np.array_equal(f64(c.scale), scale) and np.array_equal(values_cols(c), v, equal_nan=True)
+    assert np.array_equal(scales(c.scale), scale) and np.array_equal(values_cols(c), v, equal_nan=True)
     scale, v = B.fp8_blocks(f64(x), fmt)
     w = gns.gns_fp8_quantize_weight(x, fmt=fmt)
-    assert np.array_equal(f64(w.scale[0]), scale) and np.array_equal(values_weight(w)[0], v, equal_nan=True)
+    assert np.array_equal(scales(w.scale[0]), scale) and np.array_equal(values_weight(w)[0], v, equal_nan=True)
 
 
 @pytest.mark.parametrize("tokens,topk,experts,cols,drop", [
@@ -166,13 +179,13 @@ def test_long_contractions_of_few_rows_are_split(gns, tokens, n, k):
                 loud(tokens, n, 0, torch.float16, rng), torch.float32)
 
 
-def test_any_scale(gns):
-    """Scales that are no powers of two (a caller's own), and padding that holds NaN."""
+def test_other_scales(gns):
+    """A caller's own powers of two, and padding that holds NaN."""
     rng = np.random.default_rng(2)
     x, w = loud(70, 200, 0, torch.float32, rng), loud(150, 200, 0, torch.float32, rng)
     a, wq = gns.gns_fp8_quantize(x, cols=False)[0], gns.gns_fp8_quantize_weight(w)
-    a.scale.mul_(torch.rand(a.scale.shape, device="cuda") + 0.5)
-    wq.scale.mul_(torch.rand(wq.scale.shape, device="cuda") + 0.5)
+    for t in (a.scale, wq.scale):
+        t.view(torch.uint8).add_(torch.randint(0, 9, t.shape, dtype=torch.uint8, device="cuda"))
     av, wv = values_rows(a), values_weight(wq)[0]
     a.q.view(torch.uint8)[:, 200:] = 127  # NaN
     wq.q.view(torch.uint8)[:, :, 200:] = 127
