@@ -17,6 +17,7 @@
 // read of x. Bound: HBM, 2 bytes read and 1 (2 for both forms) written per
 // value of 16 bits.
 #include <algorithm>
+#include <initializer_list>
 
 #include "blockops.cuh"
 #include "fp8.cuh"
@@ -82,11 +83,20 @@ struct Pair<__half> {
 
 __device__ __forceinline__ uint32_t magnitudes(uint32_t w) { return w & 0x7FFF7FFFu; }
 
-// The same with infinities (and NaN) as zero.
+// Maxima that are no finite value (of nothing but NaN) as zero.
 template <typename T>
-__device__ __forceinline__ uint32_t finite_magnitudes(uint32_t w) {
-    const uint32_t m = magnitudes(w);
+__device__ __forceinline__ uint32_t finite_maxima(uint32_t m) {
     return ((m & 0xFFFFu) < Pair<T>::kInf ? m & 0xFFFFu : 0u) | ((m >> 16) < Pair<T>::kInf ? m & 0xFFFF0000u : 0u);
+}
+
+// Infinities become NaN: the maximum then passes over them, and the conversion,
+// which would saturate them, keeps them.
+template <typename T>
+__device__ __forceinline__ void nan_for_infinity(uint4& p) {
+    for (uint32_t* w : {&p.x, &p.y, &p.z, &p.w}) {
+        const uint32_t m = magnitudes(*w);
+        *w |= ((m & 0xFFFFu) == Pair<T>::kInf ? 0x7FFFu : 0u) | ((m >> 16) == Pair<T>::kInf ? 0x7FFF0000u : 0u);
+    }
 }
 
 // An infinity, or NaN alone, among the values behind these maxima.
@@ -96,7 +106,7 @@ __device__ __forceinline__ bool has_infinity(uint32_t maxima) {
 }
 
 // Eight values (four words) with their inverse scales to 8 bits.
-template <typename T, bool E5M2, bool INF>
+template <typename T, bool E5M2>
 __device__ __forceinline__ uint2 cast_words(const uint4& p, const float (&inv)[8]) {
     const uint32_t w[4] = {p.x, p.y, p.z, p.w};
     float v[8];
@@ -105,10 +115,6 @@ __device__ __forceinline__ uint2 cast_words(const uint4& p, const float (&inv)[8
         v[2 * i] = Pair<T>::lo(w[i]);
         v[2 * i + 1] = Pair<T>::hi(w[i]);
     }
-    if (INF) {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] = no_infinity(v[i]);
-    }
     return cast8<E5M2>(v, inv);
 }
 
@@ -116,8 +122,8 @@ __device__ __forceinline__ uint2 cast_words(const uint4& p, const float (&inv)[8
 // packed pairs (two rows' maxima travel through the shuffles in one word) and
 // the infinities out of the way. 8 instructions per value for both forms where
 // the general one takes about 20, which is what bounded it: 8192 x 14336 in
-// both forms ZZ us against 208.
-template <typename T, int MODE, bool E5M2>
+// both forms 73 us against 208.
+template <typename T, int MODE, bool E5M2, bool FULL>
 __device__ __forceinline__ void cast_tile16(const Tile& tl, const T* x, long long ldx, const int* slots, int topk,
                                             int cols, bool vec, uint8_t* q_rows, long long ld_rows, uint8_t* s_rows,
                                             long long lds_rows, uint8_t* q_cols, long long ld_cols, uint8_t* s_cols,
@@ -129,14 +135,14 @@ __device__ __forceinline__ void cast_tile16(const Tile& tl, const T* x, long lon
     const int rl = threadIdx.x >> 4;        // its row within a pass
     const int c = tl.c0 + cl;
     uint4 raw[kPasses];
+    const T* base = x + (slots ? c : static_cast<long long>(tl.r0 + rl) * ldx + c);
 #pragma unroll
     for (int p = 0; p < kPasses; ++p) {
         const int r = 16 * p + rl;
-        raw[p] = make_uint4(0, 0, 0, 0);
-        if (r < tl.nrows && c < cols) {
-            const int row = tl.r0 + r;
-            const T* a = x + static_cast<long long>(slots ? slots[row] / topk : row) * ldx + c;
-            if (vec && c + 8 <= cols) {
+        if (!FULL) raw[p] = make_uint4(0, 0, 0, 0);
+        if (FULL || (r < tl.nrows && c < cols)) {
+            const T* a = slots ? base + static_cast<long long>(slots[tl.r0 + r] / topk) * ldx : base + 16LL * p * ldx;
+            if (FULL || (vec && c + 8 <= cols)) {
                 raw[p] = *reinterpret_cast<const uint4*>(a);
             } else {
                 uint32_t w[4] = {0, 0, 0, 0};
@@ -152,19 +158,15 @@ __device__ __forceinline__ void cast_tile16(const Tile& tl, const T* x, long lon
         const uint32_t w[4] = {raw[p].x, raw[p].y, raw[p].z, raw[p].w};
         return magnitudes(w[i]);
     };
-    auto fin = [&](int p, int i) {
-        const uint32_t w[4] = {raw[p].x, raw[p].y, raw[p].z, raw[p].w};
-        return finite_magnitudes<T>(w[i]);
-    };
     if (MODE & kRowForm) {
         // Row maxima, passes p and p + 4 in the halves of one word.
         uint32_t m[kPasses / 2];
-        auto row_maxima = [&](auto value) {
+        auto row_maxima = [&]() {
 #pragma unroll
             for (int p = 0; p < kPasses / 2; ++p) {
-                const uint32_t a = P2::max(P2::max(value(p, 0), value(p, 1)), P2::max(value(p, 2), value(p, 3)));
+                const uint32_t a = P2::max(P2::max(mag(p, 0), mag(p, 1)), P2::max(mag(p, 2), mag(p, 3)));
                 const uint32_t b =
-                    P2::max(P2::max(value(p + 4, 0), value(p + 4, 1)), P2::max(value(p + 4, 2), value(p + 4, 3)));
+                    P2::max(P2::max(mag(p + 4, 0), mag(p + 4, 1)), P2::max(mag(p + 4, 2), mag(p + 4, 3)));
                 m[p] = P2::max(__byte_perm(a, b, 0x5410), __byte_perm(a, b, 0x7632));
             }
 #pragma unroll
@@ -173,40 +175,54 @@ __device__ __forceinline__ void cast_tile16(const Tile& tl, const T* x, long lon
                 for (int p = 0; p < kPasses / 2; ++p) m[p] = P2::max(m[p], __shfl_xor_sync(0xffffffffu, m[p], d));
             }
         };
-        row_maxima(mag);
+        row_maxima();
         bool inf = false;
 #pragma unroll
         for (int p = 0; p < kPasses / 2; ++p) inf |= has_infinity<T>(m[p]);
-        const bool slow = __any_sync(0xffffffffu, inf);
-        if (slow) row_maxima(fin);
+        if (__any_sync(0xffffffffu, inf)) {
+#pragma unroll
+            for (int p = 0; p < kPasses; ++p) nan_for_infinity<T>(raw[p]);
+            row_maxima();
+#pragma unroll
+            for (int p = 0; p < kPasses / 2; ++p) m[p] = finite_maxima<T>(m[p]);
+        }
+        uint8_t* out = q_rows + static_cast<long long>(tl.r0 + rl) * ld_rows + c;
+        uint32_t bytes[2] = {0, 0};  // the passes' exponents
 #pragma unroll
         for (int p = 0; p < kPasses; ++p) {
             const uint32_t e = scale_exponent(p < 4 ? P2::lo(m[p & 3]) : P2::hi(m[p & 3]), kTop);
+            bytes[p >> 2] |= e << (8 * (p & 3));
             const float s = exp_inverse(e);
             const float inv[8] = {s, s, s, s, s, s, s, s};
-            const int r = 16 * p + rl;
-            if (r < tl.nrows) {
-                if (c < ld_rows)
-                    *reinterpret_cast<uint2*>(q_rows + static_cast<long long>(tl.r0 + r) * ld_rows + c) =
-                        slow ? cast_words<T, E5M2, true>(raw[p], inv) : cast_words<T, E5M2, false>(raw[p], inv);
-                if (cl == 0) s_rows[static_cast<long long>(tl.c0 / 128) * lds_rows + tl.r0 + r] = static_cast<uint8_t>(e);
-            }
+            if (FULL || (16 * p + rl < tl.nrows && c < ld_rows))
+                *reinterpret_cast<uint2*>(out + 16LL * p * ld_rows) =
+                    cast_words<T, E5M2>(raw[p], inv);
         }
+        // Lane k of a row's sixteen stores the exponent of pass k.
+        const int k = threadIdx.x & 15;
+        if (k < kPasses && (FULL || 16 * k + rl < tl.nrows))
+            s_rows[static_cast<long long>(tl.c0 / 128) * lds_rows + tl.r0 + 16 * k + rl] =
+                static_cast<uint8_t>((k & 4 ? bytes[1] : bytes[0]) >> (8 * (k & 3)));
     }
     if (MODE & (kColForm | kBlockForm)) {
         uint32_t m[4];  // maxima of columns 2 i, 2 i + 1 over this thread's rows
-        auto col_maxima = [&](auto value) {
+        auto col_maxima = [&]() {
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                m[i] = value(0, i);
+                m[i] = mag(0, i);
 #pragma unroll
-                for (int p = 1; p < kPasses; ++p) m[i] = P2::max(m[i], value(p, i));
+                for (int p = 1; p < kPasses; ++p) m[i] = P2::max(m[i], mag(p, i));
             }
         };
-        col_maxima(mag);
-        const bool slow =
-            __syncthreads_or(has_infinity<T>(m[0]) || has_infinity<T>(m[1]) || has_infinity<T>(m[2]) || has_infinity<T>(m[3]));
-        if (slow) col_maxima(fin);
+        col_maxima();
+        if (__syncthreads_or(has_infinity<T>(m[0]) || has_infinity<T>(m[1]) || has_infinity<T>(m[2]) ||
+                             has_infinity<T>(m[3]))) {
+#pragma unroll
+            for (int p = 0; p < kPasses; ++p) nan_for_infinity<T>(raw[p]);
+            col_maxima();
+#pragma unroll
+            for (int i = 0; i < 4; ++i) m[i] = finite_maxima<T>(m[i]);
+        }
         float iv[8];
         if (MODE & kBlockForm) {  // one maximum for the tile
             uint32_t a = P2::max(P2::max(m[0], m[1]), P2::max(m[2], m[3]));
@@ -238,7 +254,7 @@ __device__ __forceinline__ void cast_tile16(const Tile& tl, const T* x, long lon
                 for (int w = 1; w < kWarps; ++w) t = fmaxf(t, part[w][threadIdx.x]);
                 const uint32_t e = scale_exponent(t, kTop);
                 inv_col[threadIdx.x] = exp_inverse(e);
-                if (tl.c0 + static_cast<int>(threadIdx.x) < cols)
+                if (FULL || tl.c0 + static_cast<int>(threadIdx.x) < cols)
                     s_cols[static_cast<long long>(tl.sc_row) * lds_cols + tl.c0 + threadIdx.x] = static_cast<uint8_t>(e);
             }
             __syncthreads();
@@ -248,14 +264,14 @@ __device__ __forceinline__ void cast_tile16(const Tile& tl, const T* x, long lon
                 iv[i] = f.x, iv[i + 1] = f.y, iv[i + 2] = f.z, iv[i + 3] = f.w;
             }
         }
+        uint8_t* out = q_cols + (tl.qc_row + rl) * ld_cols + c;
 #pragma unroll
         for (int p = 0; p < kPasses; ++p) {
-            const int r = 16 * p + rl;
             // The column form is zero to the end of its last block of 128
             // rows (the rows past nrows were loaded as zero).
-            if (c < ld_cols && (!(MODE & kBlockForm) || r < tl.nrows))
-                *reinterpret_cast<uint2*>(q_cols + (tl.qc_row + r) * ld_cols + c) =
-                    slow ? cast_words<T, E5M2, true>(raw[p], iv) : cast_words<T, E5M2, false>(raw[p], iv);
+            if (FULL || (c < ld_cols && (!(MODE & kBlockForm) || 16 * p + rl < tl.nrows)))
+                *reinterpret_cast<uint2*>(out + 16LL * p * ld_cols) =
+                    cast_words<T, E5M2>(raw[p], iv);
         }
         // part is written again only after the next tile's barrier; its readers
         // of inv_col and part are past theirs by then.
@@ -390,6 +406,19 @@ __device__ __forceinline__ void cast_tile(const Tile& tl, const T* x, long long 
     }
 }
 
+template <typename T, int MODE, bool E5M2, typename... Args>
+__device__ __forceinline__ void cast_tile_of(const Tile& tl, const T* x, long long ldx, const int* slots, int topk, int cols,
+                                             bool vec, Args&&... args) {
+    if constexpr (sizeof(T) == 2) {
+        if (vec && tl.nrows == kFp8Block && tl.c0 + kFp8Block <= cols)  // the common case without its edge tests
+            cast_tile16<T, MODE, E5M2, true>(tl, x, ldx, slots, topk, cols, vec, args...);
+        else
+            cast_tile16<T, MODE, E5M2, false>(tl, x, ldx, slots, topk, cols, vec, args...);
+    } else {
+        cast_tile<T, MODE, E5M2>(tl, x, ldx, slots, topk, cols, vec, args...);
+    }
+}
+
 // blockIdx.y: token block; blockIdx.x: the first of the `span` column blocks.
 template <typename T, int MODE, bool E5M2>
 __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 4 : 2) fp8_cast_kernel(CastJob j, bool vec, int span) {
@@ -445,14 +474,8 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 4 : 2) fp8_cast_ker
     const int nblk = (j.cols + kFp8Block - 1) / kFp8Block;
     for (int cb = blockIdx.x * span; cb < min(nblk, static_cast<int>(blockIdx.x + 1) * span); ++cb) {
         tl.c0 = cb * kFp8Block;
-        if constexpr (sizeof(T) == 2)
-            cast_tile16<T, MODE, E5M2>(tl, static_cast<const T*>(j.x), j.ldx, j.slots, j.topk, j.cols, vec, j.q_rows,
-                                       j.ld_rows, j.s_rows, j.lds_rows, j.q_cols, j.ld_cols, j.s_cols, j.lds_cols, part,
-                                       inv_col);
-        else
-            cast_tile<T, MODE, E5M2>(tl, static_cast<const T*>(j.x), j.ldx, j.slots, j.topk, j.cols, vec, j.q_rows,
-                                     j.ld_rows, j.s_rows, j.lds_rows, j.q_cols, j.ld_cols, j.s_cols, j.lds_cols, part,
-                                     inv_col);
+        cast_tile_of<T, MODE, E5M2>(tl, static_cast<const T*>(j.x), j.ldx, j.slots, j.topk, j.cols, vec, j.q_rows, j.ld_rows,
+                                    j.s_rows, j.lds_rows, j.q_cols, j.ld_cols, j.s_cols, j.lds_cols, part, inv_col);
     }
 }
 
@@ -471,13 +494,9 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 4 : 2) fp8_cast_wei
         tl.qc_row = static_cast<long long>(g) * j.rows + tl.r0;
         tl.sc_row = 0;
         uint8_t* scale = j.scale + (static_cast<long long>(g) * nb + blockIdx.y) * kb + blockIdx.x;
-        const T* w = static_cast<const T*>(j.w) + g * j.stride_w;
-        if constexpr (sizeof(T) == 2)
-            cast_tile16<T, kBlockForm, E5M2>(tl, w, j.ldw, nullptr, 1, j.cols, vec, nullptr, 0, nullptr, 0, j.q, j.ldq,
-                                             scale, 0, part, inv_col);
-        else
-            cast_tile<T, kBlockForm, E5M2>(tl, w, j.ldw, nullptr, 1, j.cols, vec, nullptr, 0, nullptr, 0, j.q, j.ldq,
-                                           scale, 0, part, inv_col);
+        cast_tile_of<T, kBlockForm, E5M2>(tl, static_cast<const T*>(j.w) + g * j.stride_w, j.ldw, nullptr, 1, j.cols, vec,
+                                          static_cast<uint8_t*>(nullptr), 0LL, static_cast<uint8_t*>(nullptr), 0LL, j.q,
+                                          j.ldq, scale, 0LL, part, inv_col);
     }
 }
 
@@ -487,10 +506,10 @@ int cast_typed(const CastJob& j, int num_sms, cudaStream_t s) {
     const int nblk = (j.cols + kFp8Block - 1) / kFp8Block;
     const int tblk = j.offsets ? fp8_max_blocks(j.rows, j.G) : (j.rows + kFp8Block - 1) / kFp8Block;
     // With groups a block looks its token block up first, so it takes several
-    // column blocks then, as long as that leaves about eight blocks per SM.
+    // column blocks then, as long as that leaves about sixteen blocks per SM.
     int span = 1;
     if (j.offsets)
-        while (span < 8 && static_cast<long long>(tblk) * ((nblk + 2 * span - 1) / (2 * span)) >= 8LL * num_sms) span *= 2;
+        while (span < 8 && static_cast<long long>(tblk) * ((nblk + 2 * span - 1) / (2 * span)) >= 16LL * num_sms) span *= 2;
     const dim3 grid((nblk + span - 1) / span, tblk);
     auto run = [&](auto k) { return static_cast<int>(launch_after(k, grid, dim3(kThreads), 0, s, j, vec, span)); };
     if (j.q_rows && j.q_cols) return run(fp8_cast_kernel<T, kBothForms, E5M2>);
