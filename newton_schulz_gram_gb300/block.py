@@ -21,14 +21,29 @@ _FP8_FORMAT = {torch.float8_e4m3fn: 0, torch.float8_e5m2: 1}
 BLOCK = 128
 
 
-class MoeRoute(NamedTuple):
+class MoeRoute:
     """A sorted routing (gns_moe_sort): expert e owns the sorted rows
     offsets[e] .. offsets[e + 1] - 1; rows[t, j] is the sorted row of token t's
     j-th choice and slots its inverse. Rows from offsets[-1] on belong to no
-    expert."""
-    offsets: torch.Tensor  # int32 [num_experts + 1]
-    rows: torch.Tensor     # int32 [tokens, topk]
-    slots: torch.Tensor    # int32 [tokens * topk]
+    expert. int32: offsets [num_experts + 1], rows [tokens, topk], slots
+    [tokens * topk]; checked here once, not by every call that takes a route."""
+    __slots__ = ("offsets", "rows", "slots", "tokens", "topk", "experts", "device")
+
+    def __init__(self, offsets, rows, slots):
+        for name, t, dims in (("offsets", offsets, 1), ("rows", rows, 2), ("slots", slots, 1)):
+            _contiguous(t, torch.int32, name)
+            if t.dim() != dims:
+                raise ValueError(f"{name} must have {dims} dimension(s)")
+            _same_device(offsets, name, t)
+        self.offsets, self.rows, self.slots = offsets, rows, slots
+        self.tokens, self.topk = rows.shape
+        self.experts = offsets.shape[0] - 1
+        self.device = offsets.get_device()
+        if slots.shape[0] != self.tokens * self.topk or self.experts < 1:
+            raise ValueError("offsets, rows and slots do not belong together")
+
+    def __iter__(self):
+        return iter((self.offsets, self.rows, self.slots))
 
 
 class Fp8Rows(NamedTuple):
@@ -139,14 +154,14 @@ def gns_dropout(x, p, seed, step, residual=None, base_index=0, out=None, stream=
     with contiguous rows. out may be x or residual."""
     rows, cols, ldx = _rows_of(x, "x")
     one_row = rows == 1
+    for t in (residual, out):
+        if t is not None:
+            if t.dtype != x.dtype or t.shape != x.shape:
+                raise ValueError("residual and out must have the type and shape of x")
+            _same_device(x, "residual or out", t)
+            one_row = one_row and t.is_contiguous()
     if out is None:
         out = _new(x.shape, x.dtype, x, stream)
-    others = [out] if residual is None else [out, residual]
-    for t in others:
-        if t.dtype != x.dtype or t.shape != x.shape:
-            raise ValueError("residual and out must have the type and shape of x")
-        _same_device(x, "residual or out", t)
-        one_row = one_row and t.is_contiguous()
     if one_row:
         ldr = ldy = ldx
     else:  # some tensor has gaps between its rows: all are walked row by row
@@ -188,16 +203,11 @@ def gns_moe_sort(experts, num_experts, stream=None):
 
 
 def _route_sizes(route, like):
-    offsets, rows, slots = route
-    i32 = torch.int32
-    if not (offsets.dtype is i32 and rows.dtype is i32 and slots.dtype is i32 and offsets.is_contiguous()
-            and rows.is_contiguous() and slots.is_contiguous() and rows.dim() == 2):
-        for name, t in route._asdict().items():
-            _contiguous(t, i32, f"route.{name}")
-        raise ValueError("route.rows must be [tokens, topk]")
-    _same_device(like, "the route", rows)
-    tokens, topk = rows.shape
-    return tokens, topk, offsets.shape[0] - 1
+    if not isinstance(route, MoeRoute):
+        raise TypeError("route must be a MoeRoute")
+    if route.device != like.get_device():
+        raise ValueError(f"the route is on cuda:{route.device}, not on {like.device}")
+    return route.tokens, route.topk, route.experts
 
 
 def gns_moe_gather(x, route, stream=None):
@@ -332,9 +342,11 @@ def _weight_args(w, route):
     if not isinstance(w, Fp8Weight):
         raise TypeError("w must be an Fp8Weight")
     groups, n, _ = w.q.shape
+    if route is not None and not isinstance(route, MoeRoute):
+        raise TypeError("route must be a MoeRoute")
     if w.grouped != (route is not None):
         raise ValueError("weights of several experts go with a route, a single matrix without one")
-    if route is not None and route.offsets.shape[0] != groups + 1:
+    if route is not None and route.experts != groups:
         raise ValueError("the route and the weights differ in the number of experts")
     return groups, n, w.cols
 
@@ -346,12 +358,13 @@ def _row_product(entry, a, w, route, contraction, out_cols, out_dtype, stream):
     rows = a.q.shape[0]
     if a.cols != contraction:
         raise ValueError(f"the operands' inner sizes differ: {a.cols} and {contraction}")
-    if route is not None and route.slots.shape[0] != rows:
+    if route is not None and route.tokens * route.topk != rows:
         raise ValueError("the operand must have one row per slot of the route")
     if out_dtype not in DTYPES:
         raise TypeError(f"out_dtype must be one of {sorted(str(d) for d in DTYPES)}")
     _same_device(a.q, "w", w.q)
-    _same_device(a.q, "the route", None if route is None else route.offsets)
+    if route is not None:
+        _route_sizes(route, a.q)
     y = _new((rows, out_cols), out_dtype, a.q, stream)
     check(getattr(load(), entry)(a.q.data_ptr(), a.q.shape[1], a.scale.data_ptr(), a.scale.shape[1], _FP8_FORMAT[a.q.dtype],
                                  rows, w.q.data_ptr(), w.q.shape[2], w.scale.data_ptr(), _FP8_FORMAT[w.q.dtype], groups,

@@ -113,6 +113,7 @@ struct Fp8RowsJob {
 };
 
 constexpr int kFp8FewRows = 8;
-int launch_fp8_rows(const Fp8RowsJob& job, cudaStream_t s);
+bool fp8_rows_fit(int rows, int K);  // up to eight rows, whose 8-bit form fits in shared memory
+int launch_fp8_rows(const Fp8RowsJob& job, int num_sms, cudaStream_t s);
 
 }  // namespace gns

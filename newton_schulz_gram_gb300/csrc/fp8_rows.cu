@@ -1,17 +1,25 @@
 // The block-scaled 8-bit linear layer for up to eight rows (a decode step), in
 // one launch: D[r][n] = x_r . w[g(r)][n] with x cast to 8 bits on the way.
 //
-// Bound: HBM, the weights once, N K bytes per group that has rows. A block of
-// threads takes 32 weight rows; its eight warps split the contraction (k block
-// b belongs to warp b mod 8), so even a 512 x 2048 expert puts every byte in
-// flight at once. The rows of x are the 8 columns of mma.sync m16n8k32: a
-// lane's 16-byte loads of two weight rows are two A fragments as they are,
-// because the order of k within a block is free as long as x uses the same
-// one, and x's fragment is cast in the registers that hold it (the block's
-// maximum is shared by four lanes). Tensor throughput does not matter at 8
-// columns; tcgen05 would add a TMA ring, TMEM and their set-up to a kernel
-// that lives for a few microseconds. The warps' sums are joined in a fixed
-// order.
+// Bound: HBM, the weights once, N K bytes per group that has rows. Two blocks
+// of threads per SM cast their group's rows of x once and then walk strips of
+// 16 weight rows; the sixteen warps split the contraction (k block b belongs to
+// warp b mod 16). Each warp streams its own pieces of the weights, across
+// strips, through a ring of cp.async slots that only its own lanes read back,
+// so nothing but the sum over the warps at the end of a strip synchronizes, and
+// 128 KB per SM are in flight all the time. The products run as mma.sync
+// m16n8k16 with the rows of x as the 8 columns: 8-bit values are exact in fp16
+// and so are their fp32 products, x is kept in shared memory as the fp16 form
+// of its 8-bit values, and a lane's 16-byte loads of two weight rows convert to
+// A fragments as they are, because the order of k within a block is free as
+// long as x uses the same one. Tensor throughput does not matter at 8 columns;
+// tcgen05 would add TMEM and descriptors to a kernel that lives for a few
+// microseconds. The warps' sums are joined in a fixed order.
+// One row, 14336 x 4096: 15.1 us (3.9 TB/s); without conversions and products,
+// the loads alone, 11.9. The 8-bit mma.sync took 19.4 us, a block of threads
+// per strip without the ring 15.6, and more of them, of eight warps, 17.0.
+#include <algorithm>
+
 #include "blockops.cuh"
 #include "fp8.cuh"
 #include "fp8_convert.cuh"
@@ -20,32 +28,50 @@
 namespace gns {
 namespace {
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 512;
 constexpr int kWarps = kThreads / 32;
-constexpr int kRowsPerBlock = 32;
-constexpr int kUnroll = 2;  // k blocks whose loads are issued together
+constexpr int kStrip = 16;               // weight rows
+constexpr int kSlotBytes = 4 * 32 * 16;  // a warp's k block: four 16-byte pieces per lane
+constexpr int kMaxSlots = 4;
+constexpr size_t kMaxSmem = 200 * 1024;
 
-template <bool E5M2>
-__device__ __forceinline__ void mma_16832(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
-                                          uint32_t b0, uint32_t b1) {
-    if constexpr (E5M2)
-        asm volatile("mma.sync.aligned.m16n8k32.row.col.f32.e5m2.e4m3.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
-                     "{%0,%1,%2,%3};"
-                     : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-                     : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
-    else
-        asm volatile("mma.sync.aligned.m16n8k32.row.col.f32.e4m3.e4m3.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
-                     "{%0,%1,%2,%3};"
-                     : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-                     : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+__device__ __forceinline__ void mma_16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                          uint32_t b1) {
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+                 : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+                 : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-__device__ __forceinline__ uint4 load_once(const uint8_t* p) {
-    uint4 v;
-    asm volatile("ld.global.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
-                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-                 : "l"(p));
-    return v;
+// The four 8-bit values of a word as two pairs of fp16.
+template <bool E5M2>
+__device__ __forceinline__ uint2 to_half4(uint32_t four) {
+    uint2 r;
+    if constexpr (E5M2)
+        asm("{\n\t.reg .b16 lo, hi;\n\tmov.b32 {lo, hi}, %2;\n\tcvt.rn.f16x2.e5m2x2 %0, lo;\n\tcvt.rn.f16x2.e5m2x2 %1, hi;\n\t}"
+            : "=r"(r.x), "=r"(r.y)
+            : "r"(four));
+    else
+        asm("{\n\t.reg .b16 lo, hi;\n\tmov.b32 {lo, hi}, %2;\n\tcvt.rn.f16x2.e4m3x2 %0, lo;\n\tcvt.rn.f16x2.e4m3x2 %1, hi;\n\t}"
+            : "=r"(r.x), "=r"(r.y)
+            : "r"(four));
+    return r;
+}
+
+// Sixteen k of two weight rows (lo, hi) and of x (b, sixteen fp16).
+template <bool E5M2>
+__device__ __forceinline__ void product(float (&c)[4], const uint4& lo, const uint4& hi, const uint4 (&b)[2]) {
+    const uint32_t l[4] = {lo.x, lo.y, lo.z, lo.w}, h[4] = {hi.x, hi.y, hi.z, hi.w};
+    const uint32_t x[8] = {b[0].x, b[0].y, b[0].z, b[0].w, b[1].x, b[1].y, b[1].z, b[1].w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const uint2 p = to_half4<E5M2>(l[i]), q = to_half4<E5M2>(h[i]);
+        mma_16816(c, p.x, q.x, p.y, q.y, x[2 * i], x[2 * i + 1]);
+    }
+}
+
+// 16 bytes to shared memory, zeros where `in` is false.
+__device__ __forceinline__ void copy16(uint32_t dst, const uint8_t* src, bool in) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(in ? 16 : 0) : "memory");
 }
 
 // The bytes of a 16-byte piece that lie inside the row (left of them).
@@ -59,26 +85,28 @@ __device__ __forceinline__ uint4 clip(uint4 v, int left) {
     return v;
 }
 
-// 16 values of a row of x from column k (K columns in all) as fp32.
+// 8 values of a row of x from column k (K columns in all) as fp32.
 template <typename T>
-__device__ __forceinline__ void load_x(const T* row, int k, int K, bool vec, float (&v)[16]) {
-    if (vec && k + 16 <= K) {
-        Pack<T, 16> p;
+__device__ __forceinline__ void load_x(const T* row, int k, int K, bool vec, float (&v)[8]) {
+    if (vec && k + 8 <= K) {
+        Pack<T, 8> p;
         p.load(row + k);
         p.get(v);
     } else {
 #pragma unroll
-        for (int i = 0; i < 16; ++i) v[i] = k + i < K ? to_f32<T>(row[k + i]) : 0.0f;
+        for (int i = 0; i < 8; ++i) v[i] = k + i < K ? to_f32<T>(row[k + i]) : 0.0f;
     }
 }
 
 template <typename T>
-__global__ void __launch_bounds__(kThreads) fp8_rows_kernel(Fp8RowsJob j, bool vec) {
-    __shared__ float sums[kWarps][kRowsPerBlock][kFp8FewRows + 1];
+__global__ void __launch_bounds__(kThreads, 2) fp8_rows_kernel(Fp8RowsJob j, bool vec, int slots) {
+    // [kWarps][slots] ring slots, then x in fp16: [rows + 1][K rounded up to 128, + 8], the last row zero, then its
+    // scales [rows][k blocks].
+    extern __shared__ __align__(16) uint8_t smem[];
+    __shared__ float sums[2][kWarps][kStrip][kFp8FewRows + 1];
     __shared__ int found[3];  // group, its first row, its row count
     grid_dependency_wait();
     grid_launch_dependents();
-    const int n0 = blockIdx.x * kRowsPerBlock;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     int g = 0, r0 = 0, count = j.rows;
     if (j.offsets) {
@@ -99,8 +127,7 @@ __global__ void __launch_bounds__(kThreads) fp8_rows_kernel(Fp8RowsJob j, bool v
         r0 = found[1];
         count = found[2];
         if (g < 0) {  // a row of no group: zero
-            const int n = n0 + static_cast<int>(threadIdx.x);
-            if (threadIdx.x < kRowsPerBlock && n < j.N)
+            for (int n = blockIdx.x * kThreads + threadIdx.x; n < j.N; n += gridDim.x * kThreads)
                 by_dtype_device(j.out_dtype, [&](auto t) {
                     using O = decltype(t);
                     static_cast<O*>(j.D)[static_cast<long long>(r) * j.ldd + n] = from_f32<O>(0.0f);
@@ -112,116 +139,176 @@ __global__ void __launch_bounds__(kThreads) fp8_rows_kernel(Fp8RowsJob j, bool v
     const int gq = lane >> 2, t = lane & 3;
     const uint8_t* wg = j.w + g * j.stride_w;
     const int nkb = (j.K + kFp8Block - 1) / kFp8Block;
-    const uint8_t* sw = j.sw + (static_cast<long long>(g) * ((j.N + kFp8Block - 1) / kFp8Block) + n0 / kFp8Block) * nkb;
-    const T* xrow = nullptr;  // the row of x of this lane's column
-    if (gq < count) {
-        const int r = r0 + gq;
-        xrow = static_cast<const T*>(j.x) + static_cast<long long>(j.slots ? j.slots[r] / j.topk : r) * j.ldx;
-    }
-    float acc[2][4] = {};
-    for (int kb0 = warp; kb0 < nkb; kb0 += kWarps * kUnroll) {
-        uint4 a[kUnroll][2][2][2];  // [k block][16-row tile][row g, g + 8][64-byte half]
-#pragma unroll
-        for (int u = 0; u < kUnroll; ++u) {
-#pragma unroll
-            for (int m = 0; m < 2; ++m) {
-#pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    const int n = n0 + 16 * m + 8 * h + gq;
-#pragma unroll
-                    for (int c = 0; c < 2; ++c) {
-                        const int k = (kb0 + u * kWarps) * kFp8Block + 64 * c + 16 * t;
-                        a[u][m][h][c] = n < j.N && k < j.K ? load_once(wg + n * j.ldw + k) : make_uint4(0, 0, 0, 0);
-                        if (k + 16 > j.K) a[u][m][h][c] = clip(a[u][m][h][c], j.K - k);
-                    }
-                }
+    const uint8_t* sw = j.sw + static_cast<long long>(g) * ((j.N + kFp8Block - 1) / kFp8Block) * nkb;
+    const int strips = (j.N + kStrip - 1) / kStrip;
+    const int per_strip = (nkb - warp + kWarps - 1) / kWarps;  // k blocks of this warp (0 when there are fewer than warps)
+    const int my_strips = (strips - static_cast<int>(blockIdx.x) + static_cast<int>(gridDim.x) - 1) / static_cast<int>(gridDim.x);
+    const int total = my_strips * per_strip;
+    const uint32_t ring = smem_u32(smem) + (warp * slots) * kSlotBytes + lane * 16;
+
+    // The next k block of the walk into its slot; one group per call, empty
+    // past the end, so that the wait below counts alike everywhere.
+    int strip_at = blockIdx.x, kb_at = warp, slot_at = 0, issued = 0;
+    const uint8_t* src = nullptr;   // this lane's first piece of row gq
+    bool in0 = false, in1 = false;  // rows gq and gq + 8 of the strip exist
+    auto enter_strip = [&]() {
+        const int n = strip_at * kStrip + gq;
+        in0 = n < j.N;
+        in1 = n + 8 < j.N;
+        src = wg + static_cast<long long>(n) * j.ldw + warp * kFp8Block + 16 * t;
+        kb_at = warp;
+    };
+    enter_strip();
+    auto issue = [&]() {
+        if (issued < total) {
+            const uint32_t dst = ring + slot_at * kSlotBytes;
+            const int left = j.K - (kb_at * kFp8Block + 16 * t);  // columns from this lane's first piece on
+            const uint8_t* row8 = src + 8 * j.ldw;
+            copy16(dst, in0 && left > 0 ? src : wg, in0 && left > 0);
+            copy16(dst + 512, in0 && left > 64 ? src + 64 : wg, in0 && left > 64);
+            copy16(dst + 1024, in1 && left > 0 ? row8 : wg, in1 && left > 0);
+            copy16(dst + 1536, in1 && left > 64 ? row8 + 64 : wg, in1 && left > 64);
+            ++issued;
+            kb_at += kWarps;
+            src += kWarps * kFp8Block;
+            if (kb_at >= nkb) {
+                strip_at += gridDim.x;
+                enter_strip();
             }
+            if (++slot_at == slots) slot_at = 0;
         }
+        asm volatile("cp.async.commit_group;" ::: "memory");
+    };
+    for (int i = 0; i < slots; ++i) issue();
+
+    // x to 8 bits: sixteen threads per block of 128.
+    const int stride = nkb * kFp8Block + 8;
+    __half* xq = reinterpret_cast<__half*>(smem + kWarps * slots * kSlotBytes);
+    float* xs = reinterpret_cast<float*>(xq + (count + 1) * stride);
+    for (int i = threadIdx.x; i < stride / 8; i += kThreads)
+        *reinterpret_cast<uint4*>(xq + count * stride + 8 * i) = make_uint4(0, 0, 0, 0);
+    for (int i = threadIdx.x >> 4; i < count * nkb; i += kThreads / 16) {
+        const int r = i / nkb, b = i - r * nkb, l = threadIdx.x & 15;
+        const int row = j.slots ? j.slots[r0 + r] / j.topk : r0 + r;
+        float v[8];
+        load_x(static_cast<const T*>(j.x) + row * j.ldx, b * kFp8Block + 8 * l, j.K, vec, v);
+        float amax = 0.0f;
 #pragma unroll
-        for (int u = 0; u < kUnroll; ++u) {
-            const int kb = kb0 + u * kWarps;
-            if (kb >= nkb) break;  // the same for the whole warp
-            float v[2][16];
+        for (int e = 0; e < 8; ++e) amax = fmaxf(amax, finite_abs(v[e]));
+        const unsigned half = 0xFFFFu << (lane & 16);
 #pragma unroll
-            for (int c = 0; c < 2; ++c) {
-                if (xrow) {
-                    load_x(xrow, kb * kFp8Block + 64 * c + 16 * t, j.K, vec, v[c]);
-                } else {
+        for (int m = 8; m > 0; m >>= 1) amax = fmaxf(amax, __shfl_xor_sync(half, amax, m));
+        const uint32_t e = scale_exponent(amax, 8);
+        const float inv = exp_inverse(e);
+        uint32_t w[2];
 #pragma unroll
-                    for (int i = 0; i < 16; ++i) v[c][i] = 0.0f;
-                }
-            }
-            float amax = 0.0f;
-#pragma unroll
-            for (int c = 0; c < 2; ++c)
-#pragma unroll
-                for (int i = 0; i < 16; ++i) amax = fmaxf(amax, finite_abs(v[c][i]));
-            amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
-            amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
-            const uint32_t e = scale_exponent(amax, 8);
-            const float inv = exp_inverse(e);
-            const float s = exp_value(sw[kb]) * exp_value(e);  // of this lane's column
-            uint32_t b[2][4];
-#pragma unroll
-            for (int c = 0; c < 2; ++c)
-#pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    b[c][i] = cast_pair<false>(no_infinity(v[c][4 * i]) * inv, no_infinity(v[c][4 * i + 1]) * inv) |
-                              (cast_pair<false>(no_infinity(v[c][4 * i + 2]) * inv, no_infinity(v[c][4 * i + 3]) * inv)
-                               << 16);
-            const float s0 = __shfl_sync(0xffffffffu, s, 8 * t);      // column 2 t
-            const float s1 = __shfl_sync(0xffffffffu, s, 8 * t + 4);  // column 2 t + 1
-#pragma unroll
-            for (int m = 0; m < 2; ++m) {
-                float part[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-                for (int c = 0; c < 2; ++c) {
-                    const uint4 lo = a[u][m][0][c], hi = a[u][m][1][c];
-                    if (j.fmt_w == GNS_E5M2) {
-                        mma_16832<true>(part, lo.x, hi.x, lo.y, hi.y, b[c][0], b[c][1]);
-                        mma_16832<true>(part, lo.z, hi.z, lo.w, hi.w, b[c][2], b[c][3]);
-                    } else {
-                        mma_16832<false>(part, lo.x, hi.x, lo.y, hi.y, b[c][0], b[c][1]);
-                        mma_16832<false>(part, lo.z, hi.z, lo.w, hi.w, b[c][2], b[c][3]);
-                    }
-                }
-                acc[m][0] = fmaf(part[0], s0, acc[m][0]);
-                acc[m][1] = fmaf(part[1], s1, acc[m][1]);
-                acc[m][2] = fmaf(part[2], s0, acc[m][2]);
-                acc[m][3] = fmaf(part[3], s1, acc[m][3]);
-            }
-        }
-    }
-#pragma unroll
-    for (int m = 0; m < 2; ++m) {
-        sums[warp][16 * m + gq][2 * t] = acc[m][0];
-        sums[warp][16 * m + gq][2 * t + 1] = acc[m][1];
-        sums[warp][16 * m + 8 + gq][2 * t] = acc[m][2];
-        sums[warp][16 * m + 8 + gq][2 * t + 1] = acc[m][3];
+        for (int h = 0; h < 2; ++h)
+            w[h] = cast_pair<false>(no_infinity(v[4 * h]) * inv, no_infinity(v[4 * h + 1]) * inv) |
+                   (cast_pair<false>(no_infinity(v[4 * h + 2]) * inv, no_infinity(v[4 * h + 3]) * inv) << 16);
+        const uint2 lo = to_half4<false>(w[0]), hi = to_half4<false>(w[1]);
+        *reinterpret_cast<uint4*>(xq + r * stride + b * kFp8Block + 8 * l) = make_uint4(lo.x, lo.y, hi.x, hi.y);
+        if (l == 0) xs[r * nkb + b] = exp_value(e);
     }
     __syncthreads();
-    const int r = warp, n = n0 + lane;  // one warp per row of D
-    if (r < count && n < j.N) {
-        float v = 0.0f;
+
+    const __half* xrow = xq + (gq < count ? gq : count) * stride + 16 * t;
+    int slot = 0, buf = 0;
+    for (int strip = blockIdx.x; strip < strips; strip += gridDim.x, buf ^= 1) {
+        const uint8_t* ws = sw + strip * kStrip / kFp8Block * nkb;
+        float acc[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+        for (int b = warp; b < nkb; b += kWarps) {
+            const float wsc = exp_value(__ldg(ws + b));
+            // All but the slots - 1 youngest groups have landed: this block's among them.
+            if (slots == 1)
+                asm volatile("cp.async.wait_group 0;" ::: "memory");
+            else if (slots == 2)
+                asm volatile("cp.async.wait_group 1;" ::: "memory");
+            else
+                asm volatile("cp.async.wait_group 3;" ::: "memory");
+            const uint32_t at = ring + slot * kSlotBytes;
+            uint4 a[2][2];
 #pragma unroll
-        for (int k = 0; k < kWarps; ++k) v += sums[k][lane][r];
-        by_dtype_device(j.out_dtype, [&](auto o) {
-            using O = decltype(o);
-            static_cast<O*>(j.D)[static_cast<long long>(r0 + r) * j.ldd + n] = from_f32<O>(v);
-        });
+            for (int h = 0; h < 2; ++h)
+#pragma unroll
+                for (int c = 0; c < 2; ++c) a[h][c] = ld_shared_v4(at + (2 * h + c) * 512);
+            if (++slot == slots) slot = 0;
+            const int k = b * kFp8Block + 16 * t;
+            float part[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+                if (k + 64 * c + 16 > j.K) {
+                    a[0][c] = clip(a[0][c], j.K - k - 64 * c);
+                    a[1][c] = clip(a[1][c], j.K - k - 64 * c);
+                }
+                const uint4* xp = reinterpret_cast<const uint4*>(xrow + b * kFp8Block + 64 * c);
+                const uint4 x[2] = {xp[0], xp[1]};
+                if (j.fmt_w == GNS_E5M2)
+                    product<true>(part, a[0][c], a[1][c], x);
+                else
+                    product<false>(part, a[0][c], a[1][c], x);
+            }
+            issue();  // into the slot just read: a lane meets only its own pieces
+            const float s0 = 2 * t < count ? wsc * xs[2 * t * nkb + b] : 0.0f;
+            const float s1 = 2 * t + 1 < count ? wsc * xs[(2 * t + 1) * nkb + b] : 0.0f;
+            acc[0] = fmaf(part[0], s0, acc[0]);
+            acc[1] = fmaf(part[1], s1, acc[1]);
+            acc[2] = fmaf(part[2], s0, acc[2]);
+            acc[3] = fmaf(part[3], s1, acc[3]);
+        }
+        sums[buf][warp][gq][2 * t] = acc[0];
+        sums[buf][warp][gq][2 * t + 1] = acc[1];
+        sums[buf][warp][8 + gq][2 * t] = acc[2];
+        sums[buf][warp][8 + gq][2 * t + 1] = acc[3];
+        __syncthreads();  // one per strip: the other buffer's readers are a barrier behind
+        const int r = threadIdx.x / kStrip, c = threadIdx.x % kStrip, n = strip * kStrip + c;
+        if (r < count && n < j.N) {
+            float v = 0.0f;
+#pragma unroll
+            for (int k = 0; k < kWarps; ++k) v += sums[buf][k][c][r];
+            by_dtype_device(j.out_dtype, [&](auto o) {
+                using O = decltype(o);
+                static_cast<O*>(j.D)[static_cast<long long>(r0 + r) * j.ldd + n] = from_f32<O>(v);
+            });
+        }
     }
+    asm volatile("cp.async.wait_all;" ::: "memory");
 }
 
-static_assert(kWarps == kFp8FewRows, "one warp stores each row");
+static_assert(kThreads / kStrip >= kFp8FewRows, "a thread per result");
+
+size_t rows_smem(int rows, int K, int slots) {
+    const size_t nkb = (static_cast<size_t>(K) + kFp8Block - 1) / kFp8Block;
+    return static_cast<size_t>(kWarps) * slots * kSlotBytes + (rows + 1) * (nkb * kFp8Block + 8) * 2 + rows * nkb * 4;
+}
 
 }  // namespace
 
-int launch_fp8_rows(const Fp8RowsJob& j, cudaStream_t s) {
+bool fp8_rows_fit(int rows, int K) { return rows <= kFp8FewRows && rows_smem(rows, K, 2) <= kMaxSmem; }
+
+int launch_fp8_rows(const Fp8RowsJob& j, int num_sms, cudaStream_t s) {
+    const int strips = (j.N + kStrip - 1) / kStrip, nkb = (j.K + kFp8Block - 1) / kFp8Block;
+    // Two blocks per SM when there is one group; with several, a block per strip
+    // of each row that may start a group (most of them end at once).
+    const int blocks = j.offsets ? strips : std::min(strips, 2 * num_sms);
+    const int walk = (strips + blocks - 1) / blocks * ((nkb + kWarps - 1) / kWarps);  // k blocks of a warp
+    int slots = 1;
+    while (slots < kMaxSlots && slots < walk && rows_smem(j.rows, j.K, 2 * slots) <= kMaxSmem / 2) slots *= 2;
+    const size_t smem = rows_smem(j.rows, j.K, slots);
     return by_dtype(j.dtype, [&](auto t) {
         using T = decltype(t);
         const bool vec = (reinterpret_cast<uintptr_t>(j.x) & 15) == 0 && j.ldx * static_cast<int>(sizeof(T)) % 16 == 0;
-        const dim3 grid((j.N + kRowsPerBlock - 1) / kRowsPerBlock, j.offsets ? j.rows : 1);
-        return static_cast<int>(launch_after(fp8_rows_kernel<T>, grid, dim3(kThreads), 0, s, j, vec));
+        static bool configured[64];  // the shared-memory opt-in is per device
+        int dev = 0;
+        cudaError_t e = cudaGetDevice(&dev);
+        if (e == cudaSuccess && (dev < 0 || dev >= 64)) e = cudaErrorInvalidDevice;
+        if (e == cudaSuccess && !configured[dev]) {
+            e = cudaFuncSetAttribute(fp8_rows_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                     static_cast<int>(kMaxSmem));
+            configured[dev] = e == cudaSuccess;
+        }
+        if (e != cudaSuccess) return static_cast<int>(e);
+        return static_cast<int>(launch_after(fp8_rows_kernel<T>, dim3(blocks, j.offsets ? j.rows : 1), dim3(kThreads), smem,
+                                             s, j, vec, slots));
     });
 }
 
