@@ -42,6 +42,14 @@ class MoeRoute:
         if slots.shape[0] != self.tokens * self.topk or self.experts < 1:
             raise ValueError("offsets, rows and slots do not belong together")
 
+    @classmethod
+    def _made(cls, offsets, rows, slots, tokens, topk, experts):
+        """A route of the library's own making, without the checks."""
+        self = cls.__new__(cls)
+        self.offsets, self.rows, self.slots = offsets, rows, slots
+        self.tokens, self.topk, self.experts, self.device = tokens, topk, experts, offsets.get_device()
+        return self
+
     def __iter__(self):
         return iter((self.offsets, self.rows, self.slots))
 
@@ -199,7 +207,7 @@ def gns_moe_sort(experts, num_experts, stream=None):
     check(load().gns_moe_sort(experts.data_ptr(), experts.element_size(), tokens, topk, num_experts,
                               offsets.data_ptr(), rows.data_ptr(), slots.data_ptr(), _on(experts, stream)),
           "gns_moe_sort")
-    return MoeRoute(offsets, rows, slots)
+    return MoeRoute._made(offsets, rows, slots, tokens, topk, num_experts)
 
 
 def _route_sizes(route, like):

@@ -200,16 +200,67 @@ int sort_typed(const SortJob& j, cudaStream_t s) {
 // All three walk the tokens, not the sorted rows: a token's own row is read
 // (or written) once and stays in registers while its topk places are visited,
 // so HBM sees each byte once. A thread owns one 16-byte piece of a token's
-// row (single elements where rows are not 16-byte aligned) and issues the
-// loads of up to kJ places before it uses the first.
+// row and issues the loads of up to kJ places before it uses the first. Where
+// rows are not 16-byte aligned a piece is kLoose elements 32 apart, the
+// neighbouring lanes' next to them: single accesses, but whole lines per warp
+// and the piece's bookkeeping shared (4093 tokens of 1021 fp32 values, 3
+// places each: single elements took 18, 31, 33 and 27 us for gather, combine, its gradient and
+// the gather's, pieces 9, 12, 22 and 10).
 
 constexpr int kThreads = 256;
 constexpr int kJ = 8;  // places handled together
+constexpr int kLoose = 4;
+
+// Piece v of a row of H elements.
+template <typename T, int N>
+struct Wide {
+    static constexpr int kSize = N;
+    Pack<T, N> p;
+    __device__ __forceinline__ void load(const T* row, unsigned v, int) { p.load(row + static_cast<long long>(v) * N); }
+    __device__ __forceinline__ void load_stream(const T* row, unsigned v, int) {
+        p.load_stream(row + static_cast<long long>(v) * N);
+    }
+    __device__ __forceinline__ void store(T* row, unsigned v, int) const { p.store(row + static_cast<long long>(v) * N); }
+    __device__ __forceinline__ void clear() { p.clear(); }
+    __device__ __forceinline__ void get(float (&f)[N]) const { p.get(f); }
+    __device__ __forceinline__ void set(const float (&f)[N]) { p.set(f); }
+};
+
+template <typename T>
+struct Loose {
+    static constexpr int kSize = kLoose;
+    T e[kLoose];
+    static __device__ __forceinline__ int column(unsigned v, int i) {
+        return static_cast<int>((v >> 5) * (32 * kLoose) + (v & 31) + 32 * i);
+    }
+    __device__ __forceinline__ void load(const T* row, unsigned v, int H) {
+#pragma unroll
+        for (int i = 0; i < kLoose; ++i) e[i] = column(v, i) < H ? row[column(v, i)] : from_f32<T>(0.0f);
+    }
+    __device__ __forceinline__ void load_stream(const T* row, unsigned v, int H) { load(row, v, H); }
+    __device__ __forceinline__ void store(T* row, unsigned v, int H) const {
+#pragma unroll
+        for (int i = 0; i < kLoose; ++i)
+            if (column(v, i) < H) row[column(v, i)] = e[i];
+    }
+    __device__ __forceinline__ void clear() {
+#pragma unroll
+        for (int i = 0; i < kLoose; ++i) e[i] = from_f32<T>(0.0f);
+    }
+    __device__ __forceinline__ void get(float (&f)[kLoose]) const {
+#pragma unroll
+        for (int i = 0; i < kLoose; ++i) f[i] = to_f32<T>(e[i]);
+    }
+    __device__ __forceinline__ void set(const float (&f)[kLoose]) {
+#pragma unroll
+        for (int i = 0; i < kLoose; ++i) e[i] = from_f32<T>(f[i]);
+    }
+};
 
 struct Walk {
     unsigned long long pieces;  // tokens * per_row
     unsigned per_row;           // pieces of a row
-    int topk;
+    int topk, H;
     const int* offsets_end;     // &offsets[G]
     const int* rows;
 };
@@ -226,7 +277,7 @@ __device__ __forceinline__ void token_piece(const Walk& w, unsigned long long i,
     }
 }
 
-template <typename T, int N>
+template <typename T, typename Piece>
 __global__ void __launch_bounds__(kThreads) moe_gather_kernel(Walk w, const T* x, long long ldx, T* y, long long ldy) {
     grid_dependency_wait();
     grid_launch_dependents();
@@ -237,20 +288,21 @@ __global__ void __launch_bounds__(kThreads) moe_gather_kernel(Walk w, const T* x
         int t;
         unsigned v;
         token_piece(w, i, t, v);
-        Pack<T, N> p, zero;
-        p.load(x + t * ldx + static_cast<long long>(v) * N);
+        Piece p, zero;
+        p.load(x + t * ldx, v, w.H);
         zero.clear();
         const int* at = w.rows + static_cast<long long>(t) * w.topk;
         for (int j = 0; j < w.topk; ++j) {
             const int r = at[j];
-            (r < live ? p : zero).store(y + r * ldy + static_cast<long long>(v) * N);
+            (r < live ? p : zero).store(y + r * ldy, v, w.H);
         }
     }
 }
 
-template <typename T, int N, bool WEIGHTS>
+template <typename T, typename Piece, bool WEIGHTS>
 __global__ void __launch_bounds__(kThreads) moe_combine_kernel(Walk w, const T* y, long long ldy, const float* weights,
                                                                T* out, long long ldo) {
+    constexpr int N = Piece::kSize;
     grid_dependency_wait();
     grid_launch_dependents();
     const int live = *w.offsets_end;
@@ -266,12 +318,12 @@ __global__ void __launch_bounds__(kThreads) moe_combine_kernel(Walk w, const T* 
         for (int e = 0; e < N; ++e) acc[e] = 0.0f;
         for (int j0 = 0; j0 < w.topk; j0 += kJ) {
             int r[kJ];
-            Pack<T, N> p[kJ];
+            Piece p[kJ];
 #pragma unroll
             for (int j = 0; j < kJ; ++j) r[j] = j0 + j < w.topk ? w.rows[s0 + j0 + j] : 0x7fffffff;
 #pragma unroll
             for (int j = 0; j < kJ; ++j)
-                if (r[j] < live) p[j].load_stream(y + r[j] * ldy + static_cast<long long>(v) * N);
+                if (r[j] < live) p[j].load_stream(y + r[j] * ldy, v, w.H);
 #pragma unroll
             for (int j = 0; j < kJ; ++j) {
                 if (r[j] < live) {
@@ -283,20 +335,21 @@ __global__ void __launch_bounds__(kThreads) moe_combine_kernel(Walk w, const T* 
                 }
             }
         }
-        Pack<T, N> o;
+        Piece o;
         o.set(acc);
-        o.store(out + t * ldo + static_cast<long long>(v) * N);
+        o.store(out + t * ldo, v, w.H);
     }
 }
 
 // WPT warps share a token: one when there are tokens enough to fill the
 // machine, a whole block otherwise.
-template <typename T, int N, int WPT, bool DOTS>
+template <typename T, typename Piece, int WPT, bool DOTS>
 __global__ void __launch_bounds__(kThreads) moe_combine_backward_kernel(Walk w, int tokens, const T* dout,
                                                                         long long lddo, const T* y, long long ldy,
                                                                         const float* weights, T* dy, long long lddy,
                                                                         float* dweights) {
     constexpr int kWarps = kThreads / 32;
+    constexpr int N = Piece::kSize;
     __shared__ float part[kJ][kWarps];
     grid_dependency_wait();
     grid_launch_dependents();
@@ -316,20 +369,19 @@ __global__ void __launch_bounds__(kThreads) moe_combine_backward_kernel(Walk w, 
             dot[j] = 0.0f;
         }
         for (unsigned v = WPT == 1 ? lane : threadIdx.x; v < w.per_row; v += 32 * WPT) {
-            const long long c = static_cast<long long>(v) * N;
-            Pack<T, N> pd, py[kJ];
-            pd.load(dout + t * lddo + c);
+            Piece pd, py[kJ];
+            pd.load(dout + t * lddo, v, w.H);
             if (DOTS) {
 #pragma unroll
                 for (int j = 0; j < kJ; ++j)
-                    if (r[j] >= 0 && r[j] < live) py[j].load_stream(y + r[j] * ldy + c);
+                    if (r[j] >= 0 && r[j] < live) py[j].load_stream(y + r[j] * ldy, v, w.H);
             }
             float d[N];
             pd.get(d);
 #pragma unroll
             for (int j = 0; j < kJ; ++j) {
                 if (r[j] < 0) continue;
-                Pack<T, N> o;
+                Piece o;
                 if (r[j] < live) {
                     float f[N];
 #pragma unroll
@@ -343,7 +395,7 @@ __global__ void __launch_bounds__(kThreads) moe_combine_backward_kernel(Walk w, 
                 } else {
                     o.clear();
                 }
-                o.store(dy + r[j] * lddy + c);
+                o.store(dy + r[j] * lddy, v, w.H);
             }
         }
         if (DOTS) {
@@ -376,9 +428,11 @@ bool rows_aligned(const void* p, long long ld, long long rows, int es) {
     return (reinterpret_cast<uintptr_t>(p) & 15) == 0 && (rows <= 1 || ld * es % 16 == 0);
 }
 
-Walk make_walk(const RouteJob& j, int n) {
+Walk make_walk(const RouteJob& j, bool vec) {
     Walk w;
-    w.per_row = static_cast<unsigned>(j.H / n);
+    const int n = 16 / elem_bytes(j.dtype), loose = 32 * kLoose;
+    w.per_row = static_cast<unsigned>(vec ? j.H / n : (j.H + loose - 1) / loose * 32);
+    w.H = j.H;
     w.pieces = static_cast<unsigned long long>(j.tokens) * w.per_row;
     w.topk = j.topk;
     w.offsets_end = j.offsets + j.G;
@@ -406,10 +460,10 @@ int launch_moe_gather(const RouteJob& j, const void* x, long long ldx, void* y, 
     const int es = elem_bytes(j.dtype), n = 16 / es;
     const bool vec = j.H % n == 0 && rows_aligned(x, ldx, j.tokens, es) &&
                      rows_aligned(y, ldy, static_cast<long long>(j.tokens) * j.topk, es);
-    const Walk w = make_walk(j, vec ? n : 1);
+    const Walk w = make_walk(j, vec);
     return by_dtype(j.dtype, [&](auto t) {
         using T = decltype(t);
-        auto k = vec ? moe_gather_kernel<T, 16 / sizeof(T)> : moe_gather_kernel<T, 1>;
+        auto k = vec ? moe_gather_kernel<T, Wide<T, 16 / sizeof(T)>> : moe_gather_kernel<T, Loose<T>>;
         return static_cast<int>(launch_after(k, walk_grid(w), dim3(kThreads), 0, s, w, static_cast<const T*>(x), ldx,
                                              static_cast<T*>(y), ldy));
     });
@@ -420,12 +474,13 @@ int launch_moe_combine(const RouteJob& j, const void* y, long long ldy, const fl
     const int es = elem_bytes(j.dtype), n = 16 / es;
     const bool vec = j.H % n == 0 && rows_aligned(y, ldy, static_cast<long long>(j.tokens) * j.topk, es) &&
                      rows_aligned(out, ldo, j.tokens, es);
-    const Walk w = make_walk(j, vec ? n : 1);
+    const Walk w = make_walk(j, vec);
     return by_dtype(j.dtype, [&](auto t) {
         using T = decltype(t);
-        constexpr int N = 16 / sizeof(T);
-        auto k = weights ? (vec ? moe_combine_kernel<T, N, true> : moe_combine_kernel<T, 1, true>)
-                         : (vec ? moe_combine_kernel<T, N, false> : moe_combine_kernel<T, 1, false>);
+        using W = Wide<T, 16 / sizeof(T)>;
+        using L = Loose<T>;
+        auto k = weights ? (vec ? moe_combine_kernel<T, W, true> : moe_combine_kernel<T, L, true>)
+                         : (vec ? moe_combine_kernel<T, W, false> : moe_combine_kernel<T, L, false>);
         return static_cast<int>(launch_after(k, walk_grid(w), dim3(kThreads), 0, s, w, static_cast<const T*>(y), ldy,
                                              weights, static_cast<T*>(out), ldo));
     });
@@ -437,23 +492,24 @@ int launch_moe_combine_backward(const RouteJob& j, const void* dout, long long l
     const long long slots = static_cast<long long>(j.tokens) * j.topk;
     const bool vec = j.H % n == 0 && rows_aligned(dout, lddo, j.tokens, es) && rows_aligned(dy, lddy, slots, es) &&
                      (!dweights || rows_aligned(y, ldy, slots, es));
-    const Walk w = make_walk(j, vec ? n : 1);
+    const Walk w = make_walk(j, vec);
     constexpr int kWarps = kThreads / 32;
     const bool wide = j.tokens < 152 * kWarps;  // fewer tokens than one round of warps: a block per token
     return by_dtype(j.dtype, [&](auto t) {
         using T = decltype(t);
-        constexpr int N = 16 / sizeof(T);
         auto run = [&](auto kernel) {
             const unsigned blocks = static_cast<unsigned>(wide ? j.tokens : (j.tokens + kWarps - 1) / kWarps);
             return static_cast<int>(launch_after(kernel, dim3(blocks), dim3(kThreads), 0, s, w, j.tokens,
                                                  static_cast<const T*>(dout), lddo, static_cast<const T*>(y), ldy,
                                                  weights, static_cast<T*>(dy), lddy, dweights));
         };
+        using W = Wide<T, 16 / sizeof(T)>;
+        using L = Loose<T>;
         if (dweights)
-            return vec ? run(wide ? moe_combine_backward_kernel<T, N, kWarps, true> : moe_combine_backward_kernel<T, N, 1, true>)
-                       : run(wide ? moe_combine_backward_kernel<T, 1, kWarps, true> : moe_combine_backward_kernel<T, 1, 1, true>);
-        return vec ? run(wide ? moe_combine_backward_kernel<T, N, kWarps, false> : moe_combine_backward_kernel<T, N, 1, false>)
-                   : run(wide ? moe_combine_backward_kernel<T, 1, kWarps, false> : moe_combine_backward_kernel<T, 1, 1, false>);
+            return vec ? run(wide ? moe_combine_backward_kernel<T, W, kWarps, true> : moe_combine_backward_kernel<T, W, 1, true>)
+                       : run(wide ? moe_combine_backward_kernel<T, L, kWarps, true> : moe_combine_backward_kernel<T, L, 1, true>);
+        return vec ? run(wide ? moe_combine_backward_kernel<T, W, kWarps, false> : moe_combine_backward_kernel<T, W, 1, false>)
+                   : run(wide ? moe_combine_backward_kernel<T, L, kWarps, false> : moe_combine_backward_kernel<T, L, 1, false>);
     });
 }
 
