@@ -8,15 +8,13 @@ optimizer steps: nothing here records an autograd graph.
 """
 from __future__ import annotations
 
-from typing import NamedTuple
-
 import torch
 
 from ._lib import check, load
 
 DTYPES = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
 FORMATS = {"e4m3": 0, "e5m2": 1}
-_FP8 = {"e4m3": torch.float8_e4m3fn, "e5m2": torch.float8_e5m2}
+_FP8 = (torch.float8_e4m3fn, torch.float8_e5m2)  # by format
 _FP8_FORMAT = {torch.float8_e4m3fn: 0, torch.float8_e5m2: 1}
 BLOCK = 128
 
@@ -26,8 +24,13 @@ class MoeRoute:
     offsets[e] .. offsets[e + 1] - 1; rows[t, j] is the sorted row of token t's
     j-th choice and slots its inverse. Rows from offsets[-1] on belong to no
     expert. int32: offsets [num_experts + 1], rows [tokens, topk], slots
-    [tokens * topk]; checked here once, not by every call that takes a route."""
-    __slots__ = ("offsets", "rows", "slots", "tokens", "topk", "experts", "device")
+    [tokens * topk]; checked here once, not by every call that takes a route.
+
+    What the library makes is one allocation (rows, slots, offsets); the
+    tensors are views made when they are asked for, since a launch costs a call
+    less than the four tensor objects would. The 8-bit forms below do the same."""
+    __slots__ = ("_buf", "_offsets", "_rows", "_slots", "p_offsets", "p_rows", "p_slots", "tokens", "topk", "experts",
+                 "device")
 
     def __init__(self, offsets, rows, slots):
         for name, t, dims in (("offsets", offsets, 1), ("rows", rows, 2), ("slots", slots, 1)):
@@ -35,47 +38,138 @@ class MoeRoute:
             if t.dim() != dims:
                 raise ValueError(f"{name} must have {dims} dimension(s)")
             _same_device(offsets, name, t)
-        self.offsets, self.rows, self.slots = offsets, rows, slots
         self.tokens, self.topk = rows.shape
         self.experts = offsets.shape[0] - 1
         self.device = offsets.get_device()
         if slots.shape[0] != self.tokens * self.topk or self.experts < 1:
             raise ValueError("offsets, rows and slots do not belong together")
+        self._buf, self._offsets, self._rows, self._slots = None, offsets, rows, slots
+        self.p_offsets, self.p_rows, self.p_slots = offsets.data_ptr(), rows.data_ptr(), slots.data_ptr()
 
     @classmethod
-    def _made(cls, offsets, rows, slots, tokens, topk, experts):
-        """A route of the library's own making, without the checks."""
+    def _made(cls, buf, tokens, topk, experts):
         self = cls.__new__(cls)
-        self.offsets, self.rows, self.slots = offsets, rows, slots
-        self.tokens, self.topk, self.experts, self.device = tokens, topk, experts, offsets.get_device()
+        n, p = tokens * topk, buf.data_ptr()
+        self._buf, self._offsets, self._rows, self._slots = buf, None, None, None
+        self.p_rows, self.p_slots, self.p_offsets = p, p + 4 * n, p + 8 * n
+        self.tokens, self.topk, self.experts, self.device = tokens, topk, experts, buf.get_device()
         return self
+
+    @property
+    def offsets(self):
+        if self._offsets is None:
+            self._offsets = self._buf[2 * self.tokens * self.topk:]
+        return self._offsets
+
+    @property
+    def rows(self):
+        if self._rows is None:
+            self._rows = self._buf[:self.tokens * self.topk].view(self.tokens, self.topk)
+        return self._rows
+
+    @property
+    def slots(self):
+        if self._slots is None:
+            n = self.tokens * self.topk
+            self._slots = self._buf[n:2 * n]
+        return self._slots
 
     def __iter__(self):
         return iter((self.offsets, self.rows, self.slots))
 
 
-class Fp8Rows(NamedTuple):
+class _Fp8:
+    """An 8-bit operand: values q and the 8-bit exponents of its scales."""
+    __slots__ = ("_buf", "_q", "_scale", "_q_shape", "_scale_shape", "p_q", "p_scale", "ld", "ld_scale", "fmt", "cols",
+                 "device")
+
+    def _from(self, q, scale, cols, q_dims):
+        for name, t, dtypes in (("q", q, _FP8_FORMAT), ("scale", scale, {torch.float8_e8m0fnu})):
+            _typed(t, name, dtypes)
+            if t.dim() != q_dims or not t.is_contiguous():
+                raise ValueError(f"{name} must be contiguous with {q_dims} dimensions")
+        _same_device(q, "scale", scale)
+        if not 0 < cols <= q.shape[-1]:
+            raise ValueError("cols must be in 1 .. the columns of q")
+        self._buf, self._q, self._scale = None, q, scale
+        self._q_shape, self._scale_shape = tuple(q.shape), tuple(scale.shape)
+        self.p_q, self.p_scale, self.ld, self.ld_scale = q.data_ptr(), scale.data_ptr(), q.shape[-1], scale.shape[-1]
+        self.fmt, self.cols, self.device = _FP8_FORMAT[q.dtype], cols, q.get_device()
+
+    @classmethod
+    def _made(cls, q_shape, scale_shape, cols, fmt, like, stream):
+        self = cls.__new__(cls)
+        n = m = 1
+        for v in q_shape:
+            n *= v
+        for v in scale_shape:
+            m *= v
+        buf = _new((n + m,), torch.uint8, like, stream)
+        self._buf, self._q, self._scale, self._q_shape, self._scale_shape = buf, None, None, q_shape, scale_shape
+        self.p_q = buf.data_ptr()
+        self.p_scale = self.p_q + n
+        self.ld, self.ld_scale, self.fmt, self.cols, self.device = q_shape[-1], scale_shape[-1], fmt, cols, buf.get_device()
+        return self
+
+    @property
+    def q(self):
+        if self._q is None:
+            n = self._buf.shape[0] - _numel(self._scale_shape)
+            self._q = self._buf[:n].view(_FP8[self.fmt]).view(self._q_shape)
+        return self._q
+
+    @property
+    def scale(self):
+        if self._scale is None:
+            n = self._buf.shape[0] - _numel(self._scale_shape)
+            self._scale = self._buf[n:].view(torch.float8_e8m0fnu).view(self._scale_shape)
+        return self._scale
+
+
+class Fp8Rows(_Fp8):
     """Row form of a matrix: q [rows, cols rounded up to 16], scale [ceil(cols /
-    128), rows], 8-bit exponents as in all three forms."""
-    q: torch.Tensor
-    scale: torch.Tensor
-    cols: int
+    128), rows]."""
+    __slots__ = ()
+
+    def __init__(self, q, scale, cols):
+        self._from(q, scale, cols, 2)
+        if self._scale_shape != (-(-cols // BLOCK), q.shape[0]):
+            raise ValueError("scale must be [ceil(cols / 128), rows]")
+
+    rows = property(lambda self: self._q_shape[0])
 
 
-class Fp8Cols(NamedTuple):
+class Fp8Cols(_Fp8):
     """Column form: q [128 * blocks, cols rounded up to 16], scale [blocks, cols]."""
-    q: torch.Tensor
-    scale: torch.Tensor
-    rows: int
-    cols: int
+    __slots__ = ("rows",)
+
+    def __init__(self, q, scale, rows, cols):
+        self._from(q, scale, cols, 2)
+        if q.shape[0] != BLOCK * scale.shape[0] or scale.shape[1] != cols or rows > q.shape[0]:
+            raise ValueError("q must be [128 * blocks, ...] and scale [blocks, cols]")
+        self.rows = rows
+
+    blocks = property(lambda self: self._scale_shape[0])
 
 
-class Fp8Weight(NamedTuple):
+class Fp8Weight(_Fp8):
     """8-bit weights: q [groups, N, K rounded up to 16], scale [groups, ceil(N / 128), ceil(K / 128)]."""
-    q: torch.Tensor
-    scale: torch.Tensor
-    cols: int
-    grouped: bool  # made from a [groups, N, K] tensor
+    __slots__ = ("grouped",)  # made from a [groups, N, K] tensor
+
+    def __init__(self, q, scale, cols, grouped):
+        self._from(q, scale, cols, 3)
+        if self._scale_shape != (q.shape[0], -(-q.shape[1] // BLOCK), -(-cols // BLOCK)):
+            raise ValueError("scale must be [groups, ceil(N / 128), ceil(K / 128)]")
+        if not grouped and q.shape[0] != 1:
+            raise ValueError("more than one matrix is a group")
+        self.grouped = grouped
+
+
+def _numel(shape):
+    n = 1
+    for v in shape:
+        n *= v
+    return n
 
 
 # The helpers below run on every call of operators that take a few microseconds
@@ -201,13 +295,11 @@ def gns_moe_sort(experts, num_experts, stream=None):
     tokens, topk = experts.shape
     if num_experts < 1:
         raise ValueError("num_experts must be at least 1")
-    rows = _new((tokens, topk), torch.int32, experts, stream)
-    slots = _new((tokens * topk,), torch.int32, experts, stream)
-    offsets = _new((num_experts + 1,), torch.int32, experts, stream)
-    check(load().gns_moe_sort(experts.data_ptr(), experts.element_size(), tokens, topk, num_experts,
-                              offsets.data_ptr(), rows.data_ptr(), slots.data_ptr(), _on(experts, stream)),
-          "gns_moe_sort")
-    return MoeRoute._made(offsets, rows, slots, tokens, topk, num_experts)
+    n = tokens * topk
+    route = MoeRoute._made(_new((2 * n + num_experts + 1,), torch.int32, experts, stream), tokens, topk, num_experts)
+    check(load().gns_moe_sort(experts.data_ptr(), experts.element_size(), tokens, topk, num_experts, route.p_offsets,
+                              route.p_rows, route.p_slots, _on(experts, stream)), "gns_moe_sort")
+    return route
 
 
 def _route_sizes(route, like):
@@ -227,14 +319,14 @@ def gns_moe_gather(x, route, stream=None):
         raise ValueError("x must have one row per token of the route")
     y = _new((tokens * topk, cols), x.dtype, x, stream)
     check(load().gns_moe_gather(x.data_ptr(), ldx, tokens, topk, experts, cols, DTYPES[x.dtype],
-                                route.offsets.data_ptr(), route.rows.data_ptr(), y.data_ptr(), cols, _on(x, stream)),
+                                route.p_offsets, route.p_rows, y.data_ptr(), cols, _on(x, stream)),
           "gns_moe_gather")
     return y
 
 
 def _route_weights(weights, route, like):
     _contiguous(weights, torch.float32, "weights")
-    if weights.shape != route.rows.shape:
+    if weights.dim() != 2 or weights.shape[0] != route.tokens or weights.shape[1] != route.topk:
         raise ValueError("weights must be [tokens, topk]")
     _same_device(like, "weights", weights)
 
@@ -250,7 +342,7 @@ def gns_moe_combine(y, weights, route, stream=None):
         _route_weights(weights, route, y)
     out = _new((tokens, cols), y.dtype, y, stream)
     check(load().gns_moe_combine(y.data_ptr(), ldy, _ptr(weights), tokens, topk, experts, cols, DTYPES[y.dtype],
-                                 route.offsets.data_ptr(), route.rows.data_ptr(), out.data_ptr(), cols, _on(y, stream)),
+                                 route.p_offsets, route.p_rows, out.data_ptr(), cols, _on(y, stream)),
           "gns_moe_combine")
     return out
 
@@ -276,7 +368,7 @@ def gns_moe_combine_backward(dout, y, weights, route, stream=None):
         dweights = _new((tokens, topk), torch.float32, dout, stream)
     dy = _new((tokens * topk, cols), dout.dtype, dout, stream)
     check(load().gns_moe_combine_backward(dout.data_ptr(), lddo, _ptr(y), ldy, weights.data_ptr(), tokens, topk, experts,
-                                          cols, DTYPES[dout.dtype], route.offsets.data_ptr(), route.rows.data_ptr(),
+                                          cols, DTYPES[dout.dtype], route.p_offsets, route.p_rows,
                                           dy.data_ptr(), cols, _ptr(dweights), _on(dout, stream)),
           "gns_moe_combine_backward")
     return dy, dweights
@@ -304,24 +396,25 @@ def gns_fp8_quantize(x, fmt="e4m3", route=None, gather=False, rows=True, cols=Tr
         if n != (tokens if gather else tokens * topk):
             raise ValueError("x must have one row per token (gather) or per slot of the route")
         n = tokens * topk
-        slots, offsets = (route.slots if gather else None), route.offsets
+        slots, offsets = (route.p_slots if gather else None), route.p_offsets
         blocks = (n + (BLOCK - 1) * min(n, groups)) // BLOCK
     elif gather:
         raise ValueError("gather needs a route")
     else:
         blocks = -(-n // BLOCK)
     ld = _up(c, 16)
+    r = k = None
     q_r = s_r = q_c = s_c = None
     if rows:
-        q_r = _new((n, ld), _FP8[fmt], x, stream)
-        s_r = _new((-(-c // BLOCK), n), torch.float8_e8m0fnu, x, stream)
+        r = Fp8Rows._made((n, ld), (-(-c // BLOCK), n), c, f, x, stream)
+        q_r, s_r = r.p_q, r.p_scale
     if cols:
-        q_c = _new((blocks * BLOCK, ld), _FP8[fmt], x, stream)
-        s_c = _new((blocks, c), torch.float8_e8m0fnu, x, stream)
-    check(load().gns_fp8_quantize(x.data_ptr(), ldx, DTYPES[x.dtype], n, c, _ptr(slots), topk, _ptr(offsets), groups, f,
-                                  _ptr(q_r), ld, _ptr(s_r), n, _ptr(q_c), ld, _ptr(s_c), c, _on(x, stream)),
-          "gns_fp8_quantize")
-    return (Fp8Rows(q_r, s_r, c) if rows else None), (Fp8Cols(q_c, s_c, n, c) if cols else None)
+        k = Fp8Cols._made((blocks * BLOCK, ld), (blocks, c), c, f, x, stream)
+        k.rows = n
+        q_c, s_c = k.p_q, k.p_scale
+    check(load().gns_fp8_quantize(x.data_ptr(), ldx, DTYPES[x.dtype], n, c, slots, topk, offsets, groups, f, q_r, ld, s_r, n,
+                                  q_c, ld, s_c, c, _on(x, stream)), "gns_fp8_quantize")
+    return r, k
 
 
 def gns_fp8_quantize_weight(w, fmt="e4m3", stream=None):
@@ -339,17 +432,17 @@ def gns_fp8_quantize_weight(w, fmt="e4m3", stream=None):
         groups, n, k = w.shape
         ldw, stride = k, n * k
     ld = _up(k, 16)
-    q = _new((groups, n, ld), _FP8[fmt], w, stream)
-    scale = _new((groups, -(-n // BLOCK), -(-k // BLOCK)), torch.float8_e8m0fnu, w, stream)
-    check(load().gns_fp8_quantize_weight(w.data_ptr(), ldw, stride, DTYPES[w.dtype], groups, n, k, f, q.data_ptr(), ld,
-                                         scale.data_ptr(), _on(w, stream)), "gns_fp8_quantize_weight")
-    return Fp8Weight(q, scale, k, grouped)
+    out = Fp8Weight._made((groups, n, ld), (groups, -(-n // BLOCK), -(-k // BLOCK)), k, f, w, stream)
+    out.grouped = grouped
+    check(load().gns_fp8_quantize_weight(w.data_ptr(), ldw, stride, DTYPES[w.dtype], groups, n, k, f, out.p_q, ld,
+                                         out.p_scale, _on(w, stream)), "gns_fp8_quantize_weight")
+    return out
 
 
 def _weight_args(w, route):
     if not isinstance(w, Fp8Weight):
         raise TypeError("w must be an Fp8Weight")
-    groups, n, _ = w.q.shape
+    groups, n, _ = w._q_shape
     if route is not None and not isinstance(route, MoeRoute):
         raise TypeError("route must be a MoeRoute")
     if w.grouped != (route is not None):
@@ -359,62 +452,77 @@ def _weight_args(w, route):
     return groups, n, w.cols
 
 
-def _row_product(entry, a, w, route, contraction, out_cols, out_dtype, stream):
+def _out_type(out_dtype):
+    if out_dtype not in DTYPES:
+        raise TypeError(f"out_dtype must be one of {sorted(str(d) for d in DTYPES)}")
+    return DTYPES[out_dtype]
+
+
+def _output(shape, dtype, device, stream):
+    if stream is None:
+        return _empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        return _empty(shape, dtype=dtype, device=device)
+
+
+def _one_device(a, *others):
+    for b in others:
+        if b is not None and b.device != a.device:
+            raise ValueError(f"operands on cuda:{a.device} and cuda:{b.device}")
+
+
+def _row_product(entry, a, w, route, dgrad, out_dtype, stream):
     if not isinstance(a, Fp8Rows):
         raise TypeError("the first operand must be an Fp8Rows")
     groups, n, k = _weight_args(w, route)
-    rows = a.q.shape[0]
-    if a.cols != contraction:
-        raise ValueError(f"the operands' inner sizes differ: {a.cols} and {contraction}")
+    rows = a._q_shape[0]
+    inner, out_cols = (n, k) if dgrad else (k, n)
+    if a.cols != inner:
+        raise ValueError(f"the operands' inner sizes differ: {a.cols} and {inner}")
     if route is not None and route.tokens * route.topk != rows:
         raise ValueError("the operand must have one row per slot of the route")
-    if out_dtype not in DTYPES:
-        raise TypeError(f"out_dtype must be one of {sorted(str(d) for d in DTYPES)}")
-    _same_device(a.q, "w", w.q)
-    if route is not None:
-        _route_sizes(route, a.q)
-    y = _new((rows, out_cols), out_dtype, a.q, stream)
-    check(getattr(load(), entry)(a.q.data_ptr(), a.q.shape[1], a.scale.data_ptr(), a.scale.shape[1], _FP8_FORMAT[a.q.dtype],
-                                 rows, w.q.data_ptr(), w.q.shape[2], w.scale.data_ptr(), _FP8_FORMAT[w.q.dtype], groups,
-                                 n, k, None if route is None else route.offsets.data_ptr(), y.data_ptr(), out_cols,
-                                 DTYPES[out_dtype], _on(a.q, stream)), entry)
+    out = _out_type(out_dtype)
+    _one_device(a, w, route)
+    y = _output((rows, out_cols), out_dtype, a.device, stream)
+    check(getattr(load(), entry)(a.p_q, a.ld, a.p_scale, a.ld_scale, a.fmt, rows, w.p_q, w.ld, w.p_scale, w.fmt, groups, n, k,
+                                 None if route is None else route.p_offsets, y.data_ptr(), out_cols, out,
+                                 _raw_stream(a.device) if stream is None else stream.cuda_stream), entry)
     return y
 
 
 def gns_fp8_matmul(a, w, route=None, out_dtype=torch.bfloat16, stream=None):
     """a w^T, [rows, N]: a Fp8Rows [rows, K] (in sorted order with a route), w Fp8Weight."""
-    return _row_product("gns_fp8_matmul", a, w, route, w.cols, w.q.shape[1], out_dtype, stream)
+    return _row_product("gns_fp8_matmul", a, w, route, False, out_dtype, stream)
 
 
 def gns_fp8_matmul_dgrad(dy, w, route=None, out_dtype=torch.bfloat16, stream=None):
     """The data gradient dy w, [rows, K]: dy Fp8Rows [rows, N]."""
-    return _row_product("gns_fp8_matmul_dgrad", dy, w, route, w.q.shape[1], w.cols, out_dtype, stream)
+    return _row_product("gns_fp8_matmul_dgrad", dy, w, route, True, out_dtype, stream)
 
 
 def gns_fp8_matmul_wgrad(dy, x, route=None, out_dtype=torch.bfloat16, stream=None):
     """The weight gradient dy^T x, [N, K] ([experts, N, K] with a route): dy and x Fp8Cols."""
     if not isinstance(dy, Fp8Cols) or not isinstance(x, Fp8Cols):
         raise TypeError("dy and x must be Fp8Cols")
-    if dy.rows != x.rows or dy.q.shape[0] != x.q.shape[0]:
+    rows, blocks = x.rows, x._scale_shape[0]
+    if dy.rows != rows or dy._scale_shape[0] != blocks:
         raise ValueError("dy and x differ in their rows")
-    if out_dtype not in DTYPES:
-        raise TypeError(f"out_dtype must be one of {sorted(str(d) for d in DTYPES)}")
-    groups = 1
+    out = _out_type(out_dtype)
+    groups, n, k = 1, dy.cols, x.cols
     if route is not None:
-        tokens, topk, groups = _route_sizes(route, x.q)
-        blocks = (tokens * topk + (BLOCK - 1) * min(tokens * topk, groups)) // BLOCK
-        if tokens * topk != x.rows or x.scale.shape[0] != blocks:
+        if not isinstance(route, MoeRoute):
+            raise TypeError("route must be a MoeRoute")
+        groups = route.experts
+        if route.tokens * route.topk != rows or blocks != (rows + (BLOCK - 1) * min(rows, groups)) // BLOCK:
             raise ValueError("the operands were not cast with this route")
-    elif x.scale.shape[0] != -(-x.rows // BLOCK):
+    elif blocks != -(-rows // BLOCK):
         raise ValueError("operands cast with a route need it here too")
-    _same_device(x.q, "dy", dy.q)
-    n, k = dy.cols, x.cols
-    dw = _new((n, k) if route is None else (groups, n, k), out_dtype, x.q, stream)
-    check(load().gns_fp8_matmul_wgrad(dy.q.data_ptr(), dy.q.shape[1], dy.scale.data_ptr(), dy.scale.shape[1],
-                                      _FP8_FORMAT[dy.q.dtype], x.q.data_ptr(), x.q.shape[1], x.scale.data_ptr(),
-                                      x.scale.shape[1], _FP8_FORMAT[x.q.dtype], x.rows, groups, n, k,
-                                      None if route is None else route.offsets.data_ptr(), dw.data_ptr(), k, n * k,
-                                      DTYPES[out_dtype], _on(x.q, stream)), "gns_fp8_matmul_wgrad")
+    _one_device(x, dy, route)
+    dw = _output((n, k) if route is None else (groups, n, k), out_dtype, x.device, stream)
+    check(load().gns_fp8_matmul_wgrad(dy.p_q, dy.ld, dy.p_scale, dy.ld_scale, dy.fmt, x.p_q, x.ld, x.p_scale, x.ld_scale,
+                                      x.fmt, rows, groups, n, k, None if route is None else route.p_offsets, dw.data_ptr(),
+                                      k, n * k, out, _raw_stream(x.device) if stream is None else stream.cuda_stream),
+          "gns_fp8_matmul_wgrad")
     return dw
 
 
@@ -426,17 +534,16 @@ def gns_fp8_linear(x, w, route=None, out_dtype=torch.bfloat16, stream=None):
     groups, n, k = _weight_args(w, route)
     if inner != k:
         raise ValueError(f"the operands' inner sizes differ: {inner} and {k}")
-    if out_dtype not in DTYPES:
-        raise TypeError(f"out_dtype must be one of {sorted(str(d) for d in DTYPES)}")
+    out = _out_type(out_dtype)
     topk, slots, offsets = 1, None, None
     if route is not None:
         tokens, topk, _ = _route_sizes(route, x)
         if tokens != rows:
             raise ValueError("x must have one row per token of the route")
-        rows, slots, offsets = tokens * topk, route.slots, route.offsets
-    _same_device(x, "w", w.q)
+        rows, slots, offsets = tokens * topk, route.p_slots, route.p_offsets
+    if w.device != x.get_device():
+        raise ValueError(f"x is on {x.device}, the weights on cuda:{w.device}")
     y = _new((rows, n), out_dtype, x, stream)
-    check(load().gns_fp8_linear(x.data_ptr(), ldx, DTYPES[x.dtype], rows, _ptr(slots), topk, _ptr(offsets),
-                                w.q.data_ptr(), w.q.shape[2], w.scale.data_ptr(), _FP8_FORMAT[w.q.dtype], groups, n, k,
-                                y.data_ptr(), n, DTYPES[out_dtype], _on(x, stream)), "gns_fp8_linear")
+    check(load().gns_fp8_linear(x.data_ptr(), ldx, DTYPES[x.dtype], rows, slots, topk, offsets, w.p_q, w.ld, w.p_scale,
+                                w.fmt, groups, n, k, y.data_ptr(), n, out, _on(x, stream)), "gns_fp8_linear")
     return y

@@ -97,7 +97,13 @@ def test_binding_refuses():
     with pytest.raises(ValueError, match="CUDA"):
         gns.gns_fp8_quantize(x)
     with pytest.raises(TypeError, match="Fp8Rows"):
-        gns.gns_fp8_matmul(x, gns.Fp8Weight(x.view(1, 4, 8), x, 8, False))
+        gns.gns_fp8_matmul(x, x)
+    with pytest.raises(TypeError, match="Fp8Weight"):
+        gns.gns_fp8_linear(x, x) if x.is_cuda else gns.block._weight_args(x, None)
+    with pytest.raises(TypeError, match="one of"):
+        gns.Fp8Rows(x, x, 8)
+    with pytest.raises(ValueError, match="CUDA"):
+        gns.MoeRoute(*(torch.zeros(2, dtype=torch.int32),) * 3)
     with pytest.raises(TypeError, match="Fp8Cols"):
         gns.gns_fp8_matmul_wgrad(x, x)
 
@@ -130,5 +136,16 @@ def test_binding_refuses_mismatches():
             call()
     with pytest.raises(TypeError):
         gns.gns_fp8_matmul(r, w, out_dtype=torch.float64)
+    for make in (lambda: gns.Fp8Rows(r.q, r.scale, 17), lambda: gns.Fp8Rows(r.q, r.scale[:, :3], 8),
+                 lambda: gns.Fp8Cols(r.q, c.scale, 4, 8), lambda: gns.Fp8Weight(we.q, we.scale, 8, False),
+                 lambda: gns.MoeRoute(route.offsets, route.rows[:3], route.slots),
+                 lambda: gns.MoeRoute(route.offsets, route.slots, route.slots)):
+        with pytest.raises(ValueError):
+            make()
+    # Operands and routes of one's own making are taken like the library's.
+    assert torch.equal(gns.gns_fp8_matmul(gns.Fp8Rows(r.q, r.scale, 8), gns.Fp8Weight(w.q, w.scale, 8, False)),
+                       gns.gns_fp8_matmul(r, w))
+    again = gns.MoeRoute(*(t.clone() for t in route))
+    assert torch.equal(gns.gns_moe_gather(x, again), gns.gns_moe_gather(x, route))
     with pytest.raises(gns.GnsError, match="GNS_ERR_INVALID"):
         gns.gns_dropout(x, 2.0, 0, 0)
