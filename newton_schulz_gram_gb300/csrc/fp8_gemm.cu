@@ -166,20 +166,6 @@ __device__ __forceinline__ void tc_copy_scales(uint32_t tmem, uint32_t smem_addr
         asm volatile("tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;" ::"r"(tmem), "l"(d) : "memory");
 }
 
-// mbar_wait with its bounded spin inline.
-__device__ __forceinline__ bool mbar_wait_here(uint32_t bar, uint32_t parity, const DevStatus& st) {
-    if (mbar_try_wait(bar, parity)) return true;
-    const uint64_t t0 = globaltimer();
-    while (!mbar_try_wait(bar, parity)) {
-        if (call_aborted(st)) return false;
-        if (globaltimer() - t0 > st.limit_ns) {
-            raise_timeout(st);
-            return false;
-        }
-    }
-    return true;
-}
-
 __device__ __forceinline__ float ld_shared_f32(uint32_t addr) {
     float v;
     asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
@@ -260,13 +246,15 @@ __device__ __forceinline__ void drain_wait(uint32_t bar, uint32_t parity, uint64
     }
 }
 
-// One 32-bit word of two 16-bit results, or of one 32-bit result.
-__device__ __forceinline__ uint32_t pack_pair(float lo, float hi, bool bf16) {
-    if (bf16) {
+// One 32-bit word of two 16-bit results.
+template <typename T>
+__device__ __forceinline__ uint32_t pack_pair(float lo, float hi) {
+    if constexpr (std::is_same_v<T, __nv_bfloat16>) {
         const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
         return *reinterpret_cast<const uint32_t*>(&h);
+    } else {
+        return pack_half2(lo, hi);
     }
-    return pack_half2(lo, hi);
 }
 
 __device__ __forceinline__ uint32_t add_bits(uint32_t a, uint32_t b) {
@@ -295,7 +283,7 @@ __device__ __forceinline__ void bulk_store(const CUtensorMap* m, uint32_t src, i
 // 16-byte boundaries, and runs of neighbouring elements where they do not. With
 // `add` (fp32) the stored values are added to; a lane meets its own stores.
 template <int ES>
-__device__ __forceinline__ void store_rows(uint32_t stage, uint8_t* d, long long ldd, int rows, int left, bool aligned,
+__device__ __noinline__ void store_rows(uint32_t stage, uint8_t* d, long long ldd, int rows, int left, bool aligned,
                                            bool add, int lane) {
     constexpr int PASS = kStageRow / ES;  // columns
     constexpr int PIECE = 16 / ES;        // elements of a 16-byte piece
@@ -369,7 +357,14 @@ __device__ __forceinline__ void mbar_arrive_relaxed(uint32_t cluster_addr) {
     asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
 }
 
-template <int CG>
+// T is the type that is stored: D's, or float for the partial sums of a split.
+// One kernel per type and direction rather than branches: the warps' roles run
+// at the same time and share the instruction cache, which short tiles feel most
+// (256 experts of 512 x 2048, 65536 rows, one kernel for all: data gradient 137
+// us, weight gradient 155, against 112 and 138; one for all directions 119 and
+// 138). Rare paths, the plain stores and the waits' spins, are out of line for
+// the same reason.
+template <int CG, typename T, bool wgrad>
 __global__ void __launch_bounds__(kThreads, 1) fp8_gemm_kernel(const __grid_constant__ Fp8GemmJob P) {
     constexpr int STAGES = Cfg<CG>::STAGES;
     constexpr int TM = Cfg<CG>::TM;
@@ -402,9 +397,9 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_gemm_kernel(const __grid_cons
     const int lane = threadIdx.x & 31;
     const DevStatus& err = P.st;
     const int rank = CG > 1 ? static_cast<int>(cluster_ctarank()) : 0;  // 0: the pair's leader
-    const bool wgrad = P.wgrad;
     // k blocks summed in TMEM before the result is stored or added to.
-    const int segment = P.out_dtype == GNS_FP32 || P.split > 1 ? kSegment : 1 << 30;
+    constexpr int ES = sizeof(T);
+    constexpr int segment = ES == 4 ? kSegment : 1 << 30;
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < STAGES; ++s) {
@@ -485,7 +480,7 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_gemm_kernel(const __grid_cons
     const uint32_t tiles_u32 = smem_u32(tiles);
     auto take = [&](int i, Tile& tl, bool whole_warp) -> bool {
         const int slot = i % kTileSlots;
-        bool got = mbar_wait_here(tfull0 + 8 * slot, (i / kTileSlots) & 1, err);
+        bool got = mbar_wait(tfull0 + 8 * slot, (i / kTileSlots) & 1, err);
         if (whole_warp) got = __all_sync(0xffffffffu, got);
         if (!got) return false;
         const uint32_t at = tiles_u32 + slot * static_cast<uint32_t>(sizeof(Tile));
@@ -496,7 +491,8 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_gemm_kernel(const __grid_cons
         if (!whole_warp || lane == 0) mbar_arrive(tempty0 + 8 * slot);
         return tl.g >= 0;
     };
-    const bool a_mn = wgrad, b_mn = wgrad || P.b_mn;
+    constexpr bool a_mn = wgrad;
+    const bool b_mn = wgrad || P.b_mn;
 
     if (warp == 0) {
         // ------------------------------------------------------ TMA producer
@@ -755,17 +751,15 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_gemm_kernel(const __grid_cons
             // Rows of this warp inside the group (of D) and columns inside D.
             const int rows = tl.rows - row, ncol = P.N - col;
             const bool live = rows > 0 && ncol > 0;
-            const bool split = P.split > 1;
-            const int es = P.out_dtype == GNS_FP32 || split ? 4 : 2;
+            const bool split = ES == 4 && P.split > 1;
             const long long row0 = static_cast<long long>(tl.row0) + row;
             const long long ldd = split ? P.N : P.ldd;
             uint8_t* d = split ? reinterpret_cast<uint8_t*>(P.partial + (static_cast<long long>(tl.split) * P.rows + row0) * P.N + col)
-                               : static_cast<uint8_t*>(P.D) + ((wgrad ? tl.g * P.strideD : 0LL) + row0 * P.ldd + col) * es;
+                               : static_cast<uint8_t*>(P.D) + ((wgrad ? tl.g * P.strideD : 0LL) + row0 * P.ldd + col) * ES;
             const bool aligned = split ? P.N % 4 == 0
-                                       : ((reinterpret_cast<uintptr_t>(P.D) | static_cast<uintptr_t>(P.ldd * es) |
-                                           static_cast<uintptr_t>(P.strideD * es)) & 15) == 0;
-            const int passes = es == 2 ? 2 : 4;
-            const bool bf16 = P.out_dtype == GNS_BF16;
+                                       : ((reinterpret_cast<uintptr_t>(P.D) | static_cast<uintptr_t>(P.ldd * ES) |
+                                           static_cast<uintptr_t>(P.strideD * ES)) & 15) == 0;
+            constexpr int passes = ES == 2 ? 2 : 4;
             int kb = tl.kb0;
             // 32 whole rows leave by a bulk store; the ragged end of a group,
             // and outputs without 16-byte rows, by the warp's own stores.
@@ -775,7 +769,7 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_gemm_kernel(const __grid_cons
                 const int buf = it & 1;
                 const uint32_t acc = tmem_base + (static_cast<uint32_t>(32 * q) << 16) + buf * kAcc1 + kCols * half;
                 if (filled) {
-                    if (!__all_sync(0xffffffffu, mbar_wait_here(accf0 + 8 * buf, (it >> 1) & 1, err))) {
+                    if (!__all_sync(0xffffffffu, mbar_wait(accf0 + 8 * buf, (it >> 1) & 1, err))) {
                         ok = false;
                         break;
                     }
@@ -790,7 +784,7 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_gemm_kernel(const __grid_cons
                     const int p = buf == 0 ? passes - 1 - n : n;
                     uint32_t w[32];
                     if (filled && live) {
-                        if (es == 2) {
+                        if constexpr (ES == 2) {
                             uint32_t x[32], y[32];
                             tmem_ld_32x32b_x32(acc + 64 * p, x);
                             tmem_ld_32x32b_x32(acc + 64 * p + 32, y);
@@ -798,8 +792,8 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_gemm_kernel(const __grid_cons
                             tmem_ld_wait_for(y);
 #pragma unroll
                             for (int j = 0; j < 16; ++j) {
-                                w[j] = pack_pair(__uint_as_float(x[2 * j]), __uint_as_float(x[2 * j + 1]), bf16);
-                                w[16 + j] = pack_pair(__uint_as_float(y[2 * j]), __uint_as_float(y[2 * j + 1]), bf16);
+                                w[j] = pack_pair<T>(__uint_as_float(x[2 * j]), __uint_as_float(x[2 * j + 1]));
+                                w[16 + j] = pack_pair<T>(__uint_as_float(y[2 * j]), __uint_as_float(y[2 * j + 1]));
                             }
                         } else {
                             tmem_ld_32x32b_x32(acc + 32 * p, w);
@@ -813,14 +807,14 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_gemm_kernel(const __grid_cons
                         if (n == 0 && mine) hand_back(overlap_lead);
                         if (n == passes - 1) hand_back(acce_lead + 8 * buf);
                     }
-                    const int c0 = p * (kStageRow / es);
+                    const int c0 = p * (kStageRow / ES);
                     if (!live || c0 >= ncol) continue;
                     // The two buffers take turns: all bulk stores but the last
                     // have read theirs (all, before one that the warp's own
                     // stores use, which no group counts). Before a segment is
                     // added, the stores it adds to are complete.
                     const uint32_t stage = stage0 + turn * kStageBytes;
-                    const bool add = kb > tl.kb0;
+                    const bool add = ES == 4 && kb > tl.kb0;
                     turn ^= 1;
                     if (lane == 0) {
                         if (add && fresh)
@@ -843,10 +837,7 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_gemm_kernel(const __grid_cons
                             bulk_store(&P.mapD, stage, col + c0, static_cast<int>(row0), split ? tl.split : wgrad ? tl.g : 0, add);
                     } else {
                         __syncwarp();
-                        if (es == 2)
-                            store_rows<2>(stage, d + c0 * 2, ldd, rows, ncol - c0, aligned, false, lane);
-                        else
-                            store_rows<4>(stage, d + c0 * 4, ldd, rows, ncol - c0, aligned, add, lane);
+                        store_rows<ES>(stage, d + c0 * ES, ldd, rows, ncol - c0, aligned, add, lane);
                     }
                 }
                 it += filled;
@@ -897,7 +888,7 @@ __global__ void __launch_bounds__(128) fp8_reduce_kernel(const float* partial, i
 
 constexpr int kMaxDevices = 64;
 
-template <int CG>
+template <int CG, typename T, bool wgrad>
 int launch_variant(const Fp8GemmJob& job, long long max_tiles, int num_sms, cudaStream_t s) {
     // Per device: the shared-memory opt-in, and the clusters that fit at once
     // (tiles go to them with a static stride).
@@ -906,7 +897,7 @@ int launch_variant(const Fp8GemmJob& job, long long max_tiles, int num_sms, cuda
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
     if (dev < 0 || dev >= kMaxDevices) return cudaErrorInvalidDevice;
-    const auto kernel = fp8_gemm_kernel<CG>;
+    const auto kernel = fp8_gemm_kernel<CG, T, wgrad>;
     cudaLaunchConfig_t cfg = {};
     cfg.blockDim = dim3(kThreads);
     cfg.dynamicSmemBytes = smem_bytes<CG>();
@@ -963,11 +954,11 @@ int fp8_gemm_split(int rows, int N, int K, int num_sms) {
 
 int fp8_gemm_cg(int M, int N, bool grouped, int num_sms) {
     // A pair loads and reads from shared memory 32 KB per k block and SM where a
-    // single CTA takes 48 KB (8192 x 14336 x 4096, the three products: 317, 349
-    // and 356 us with pairs, 358, 379 and 387 us without), but its tile of 256
+    // single CTA takes 48 KB (8192 x 14336 x 4096, the three products: 314, 356
+    // and 353 us with pairs, 354, 383 and 385 us without), but its tile of 256
     // rows wastes more of a ragged group (256 experts of 512 x 2048, 65536
-    // rows: 97, 140 and 170 us with pairs, 92, 139 and 156 us without) and needs
-    // enough tiles for all pairs (1021 x 712 x 4093: 18, 12, 18 against 17, 11, 16).
+    // rows: 94, 113 and 159 us with pairs, 91, 113 and 138 us without) and needs
+    // enough tiles for all pairs (1021 x 712 x 4093: 15, 10, 17 against 14, 9, 15).
     const long long tiles = static_cast<long long>((M + 255) / 256) * ((N + BN - 1) / BN);
     return !grouped && tiles >= num_sms / 2 ? 2 : 1;
 }
@@ -984,7 +975,12 @@ int launch_fp8_gemm(const Fp8GemmJob& job, int cg, int num_sms, cudaStream_t s) 
         tm = (job.rows + tile - 1) / tile;
     const long long tiles = tm * tn * job.split;
     if (tiles <= 0) return cudaSuccess;
-    const int e = cg == 2 ? launch_variant<2>(job, tiles, num_sms, s) : launch_variant<1>(job, tiles, num_sms, s);
+    const int e = by_dtype(job.split > 1 ? static_cast<int>(GNS_FP32) : job.out_dtype, [&](auto t) {
+        using T = decltype(t);
+        if (job.wgrad)
+            return cg == 2 ? launch_variant<2, T, true>(job, tiles, num_sms, s) : launch_variant<1, T, true>(job, tiles, num_sms, s);
+        return cg == 2 ? launch_variant<2, T, false>(job, tiles, num_sms, s) : launch_variant<1, T, false>(job, tiles, num_sms, s);
+    });
     if (e != cudaSuccess || job.split <= 1) return e;
     const int v = job.N % 4 == 0 ? 4 : 1;
     const dim3 grid((job.N + 128 * v - 1) / (128 * v), std::min(job.rows, 65535));
