@@ -41,26 +41,38 @@ __device__ __forceinline__ uint2 cast8(const float (&v)[8], const float (&inv)[8
     return o;
 }
 
-// One tile: rows r0 .. r0 + nrows - 1 of the matrix (source rows through
-// `src`), columns c0 .. c0 + 127.
+// One tile: rows r0 .. r0 + nrows - 1 of the matrix (their rows of x from
+// `source` if there is one), columns c0 .. c0 + 127.
 struct Tile {
     int r0, nrows, c0;
     long long qc_row;  // first row of the tile in the column form
     int sc_row;        // its row of column scales
 };
 
-// Two 16-bit values at a time: magnitudes and their maximum as packed words.
-// The maximum passes over a NaN and shows an infinity, whose block then takes
-// the finite maximum the slow way.
+// Two 16-bit values at a time. max_abs has the larger magnitudes (and signs of
+// no meaning); it passes over a NaN and shows an infinity, whose block then
+// takes the finite maximum the slow way. scaled is a pair times a power of two
+// as two floats: exact, except that a bf16 product too small to be a normal
+// number may lose bits, hundreds of binades below the smallest 8-bit value.
+// fp16 has no room for the inverse scales and is multiplied in fp32.
 template <typename T>
 struct Pair;
 template <>
 struct Pair<__nv_bfloat16> {
     static constexpr uint32_t kInf = 0x7F80u;
-    static __device__ __forceinline__ uint32_t max(uint32_t a, uint32_t b) {
+    static __device__ __forceinline__ uint32_t max_abs(uint32_t a, uint32_t b) {
         uint32_t r;
-        asm("max.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+        asm("max.xorsign.abs.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
         return r;
+    }
+    using Scale = uint32_t;  // of both values
+    static __device__ __forceinline__ Scale scale(float lo, float hi) {
+        return __byte_perm(__float_as_uint(lo), __float_as_uint(hi), 0x7632);
+    }
+    static __device__ __forceinline__ float2 scaled(uint32_t w, Scale s) {
+        uint32_t r;
+        asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(w), "r"(s));
+        return make_float2(lo(r), hi(r));
     }
     static __device__ __forceinline__ float lo(uint32_t w) { return __uint_as_float(w << 16); }
     static __device__ __forceinline__ float hi(uint32_t w) { return __uint_as_float(w & 0xFFFF0000u); }
@@ -68,10 +80,15 @@ struct Pair<__nv_bfloat16> {
 template <>
 struct Pair<__half> {
     static constexpr uint32_t kInf = 0x7C00u;
-    static __device__ __forceinline__ uint32_t max(uint32_t a, uint32_t b) {
+    static __device__ __forceinline__ uint32_t max_abs(uint32_t a, uint32_t b) {
         uint32_t r;
-        asm("max.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+        asm("max.xorsign.abs.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
         return r;
+    }
+    using Scale = float2;
+    static __device__ __forceinline__ Scale scale(float lo, float hi) { return make_float2(lo, hi); }
+    static __device__ __forceinline__ float2 scaled(uint32_t w, Scale s) {
+        return make_float2(lo(w) * s.x, hi(w) * s.y);
     }
     static __device__ __forceinline__ float lo(uint32_t w) {
         return __half2float(__ushort_as_half(static_cast<unsigned short>(w)));
@@ -107,15 +124,15 @@ __device__ __forceinline__ bool has_infinity(uint32_t maxima) {
 
 // Eight values (four words) with their inverse scales to 8 bits.
 template <typename T, bool E5M2>
-__device__ __forceinline__ uint2 cast_words(const uint4& p, const float (&inv)[8]) {
+__device__ __forceinline__ uint2 cast_words(const uint4& p, const typename Pair<T>::Scale (&inv)[4]) {
     const uint32_t w[4] = {p.x, p.y, p.z, p.w};
-    float v[8];
+    uint32_t q[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-        v[2 * i] = Pair<T>::lo(w[i]);
-        v[2 * i + 1] = Pair<T>::hi(w[i]);
+        const float2 v = Pair<T>::scaled(w[i], inv[i]);
+        q[i] = cast_pair<E5M2>(v.x, v.y);
     }
-    return cast8<E5M2>(v, inv);
+    return make_uint2(q[0] | (q[1] << 16), q[2] | (q[3] << 16));
 }
 
 // The tile of 16-bit values: the general tile below with the maxima taken over
@@ -124,7 +141,7 @@ __device__ __forceinline__ uint2 cast_words(const uint4& p, const float (&inv)[8
 // the general one takes about 20, which is what bounded it: 8192 x 14336 in
 // both forms 73 us against 208.
 template <typename T, int MODE, bool E5M2, bool FULL>
-__device__ __forceinline__ void cast_tile16(const Tile& tl, const T* x, long long ldx, const int* slots, int topk,
+__device__ __forceinline__ void cast_tile16(const Tile& tl, const T* x, long long ldx, const int* source,
                                             int cols, bool vec, uint8_t* q_rows, long long ld_rows, uint8_t* s_rows,
                                             long long lds_rows, uint8_t* q_cols, long long ld_cols, uint8_t* s_cols,
                                             long long lds_cols, float (&part)[kWarps][128], float (&inv_col)[128]) {
@@ -135,13 +152,13 @@ __device__ __forceinline__ void cast_tile16(const Tile& tl, const T* x, long lon
     const int rl = threadIdx.x >> 4;        // its row within a pass
     const int c = tl.c0 + cl;
     uint4 raw[kPasses];
-    const T* base = x + (slots ? c : static_cast<long long>(tl.r0 + rl) * ldx + c);
+    const T* base = x + (source ? c : static_cast<long long>(tl.r0 + rl) * ldx + c);
 #pragma unroll
     for (int p = 0; p < kPasses; ++p) {
         const int r = 16 * p + rl;
         if (!FULL) raw[p] = make_uint4(0, 0, 0, 0);
         if (FULL || (r < tl.nrows && c < cols)) {
-            const T* a = slots ? base + static_cast<long long>(slots[tl.r0 + r] / topk) * ldx : base + 16LL * p * ldx;
+            const T* a = source ? base + static_cast<long long>(source[r]) * ldx : base + 16LL * p * ldx;
             if (FULL || (vec && c + 8 <= cols)) {
                 raw[p] = *reinterpret_cast<const uint4*>(a);
             } else {
@@ -154,9 +171,9 @@ __device__ __forceinline__ void cast_tile16(const Tile& tl, const T* x, long lon
             }
         }
     }
-    auto mag = [&](int p, int i) {
+    auto word = [&](int p, int i) {
         const uint32_t w[4] = {raw[p].x, raw[p].y, raw[p].z, raw[p].w};
-        return magnitudes(w[i]);
+        return w[i];
     };
     if (MODE & kRowForm) {
         // Row maxima, passes p and p + 4 in the halves of one word.
@@ -164,16 +181,18 @@ __device__ __forceinline__ void cast_tile16(const Tile& tl, const T* x, long lon
         auto row_maxima = [&]() {
 #pragma unroll
             for (int p = 0; p < kPasses / 2; ++p) {
-                const uint32_t a = P2::max(P2::max(mag(p, 0), mag(p, 1)), P2::max(mag(p, 2), mag(p, 3)));
-                const uint32_t b =
-                    P2::max(P2::max(mag(p + 4, 0), mag(p + 4, 1)), P2::max(mag(p + 4, 2), mag(p + 4, 3)));
-                m[p] = P2::max(__byte_perm(a, b, 0x5410), __byte_perm(a, b, 0x7632));
+                const uint32_t a = P2::max_abs(P2::max_abs(word(p, 0), word(p, 1)), P2::max_abs(word(p, 2), word(p, 3)));
+                const uint32_t b = P2::max_abs(P2::max_abs(word(p + 4, 0), word(p + 4, 1)),
+                                               P2::max_abs(word(p + 4, 2), word(p + 4, 3)));
+                m[p] = P2::max_abs(__byte_perm(a, b, 0x5410), __byte_perm(a, b, 0x7632));
             }
 #pragma unroll
             for (int d = 8; d > 0; d >>= 1) {
 #pragma unroll
-                for (int p = 0; p < kPasses / 2; ++p) m[p] = P2::max(m[p], __shfl_xor_sync(0xffffffffu, m[p], d));
+                for (int p = 0; p < kPasses / 2; ++p) m[p] = P2::max_abs(m[p], __shfl_xor_sync(0xffffffffu, m[p], d));
             }
+#pragma unroll
+            for (int p = 0; p < kPasses / 2; ++p) m[p] = magnitudes(m[p]);
         };
         row_maxima();
         bool inf = false;
@@ -192,8 +211,8 @@ __device__ __forceinline__ void cast_tile16(const Tile& tl, const T* x, long lon
         for (int p = 0; p < kPasses; ++p) {
             const uint32_t e = scale_exponent(p < 4 ? P2::lo(m[p & 3]) : P2::hi(m[p & 3]), kTop);
             bytes[p >> 2] |= e << (8 * (p & 3));
-            const float s = exp_inverse(e);
-            const float inv[8] = {s, s, s, s, s, s, s, s};
+            if (!FULL && 16 * p >= tl.nrows) continue;  // no row of this pass is there
+            const typename P2::Scale s = P2::scale(exp_inverse(e), exp_inverse(e)), inv[4] = {s, s, s, s};
             if (FULL || (16 * p + rl < tl.nrows && c < ld_rows))
                 *reinterpret_cast<uint2*>(out + 16LL * p * ld_rows) =
                     cast_words<T, E5M2>(raw[p], inv);
@@ -209,9 +228,10 @@ __device__ __forceinline__ void cast_tile16(const Tile& tl, const T* x, long lon
         auto col_maxima = [&]() {
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                m[i] = mag(0, i);
+                m[i] = word(0, i);
 #pragma unroll
-                for (int p = 1; p < kPasses; ++p) m[i] = P2::max(m[i], mag(p, i));
+                for (int p = 1; p < kPasses; ++p) m[i] = P2::max_abs(m[i], word(p, i));
+                m[i] = magnitudes(m[i]);
             }
         };
         col_maxima();
@@ -223,12 +243,12 @@ __device__ __forceinline__ void cast_tile16(const Tile& tl, const T* x, long lon
 #pragma unroll
             for (int i = 0; i < 4; ++i) m[i] = finite_maxima<T>(m[i]);
         }
-        float iv[8];
+        typename P2::Scale iv[4];
         if (MODE & kBlockForm) {  // one maximum for the tile
-            uint32_t a = P2::max(P2::max(m[0], m[1]), P2::max(m[2], m[3]));
-            a = P2::max(a, __byte_perm(a, a, 0x1032));
+            uint32_t a = P2::max_abs(P2::max_abs(m[0], m[1]), P2::max_abs(m[2], m[3]));
+            a = magnitudes(P2::max_abs(a, __byte_perm(a, a, 0x1032)));
 #pragma unroll
-            for (int d = 16; d > 0; d >>= 1) a = P2::max(a, __shfl_xor_sync(0xffffffffu, a, d));
+            for (int d = 16; d > 0; d >>= 1) a = magnitudes(P2::max_abs(a, __shfl_xor_sync(0xffffffffu, a, d)));
             if (lane == 0) part[warp][0] = P2::lo(a);
             __syncthreads();
             float t = part[0][0];
@@ -237,10 +257,10 @@ __device__ __forceinline__ void cast_tile16(const Tile& tl, const T* x, long lon
             const uint32_t e = scale_exponent(t, kTop);
             if (threadIdx.x == 0) *s_cols = static_cast<uint8_t>(e);
 #pragma unroll
-            for (int i = 0; i < 8; ++i) iv[i] = exp_inverse(e);
+            for (int i = 0; i < 4; ++i) iv[i] = P2::scale(exp_inverse(e), exp_inverse(e));
         } else {
 #pragma unroll
-            for (int i = 0; i < 4; ++i) m[i] = P2::max(m[i], __shfl_xor_sync(0xffffffffu, m[i], 16));
+            for (int i = 0; i < 4; ++i) m[i] = magnitudes(P2::max_abs(m[i], __shfl_xor_sync(0xffffffffu, m[i], 16)));
             if (lane < 16) {
 #pragma unroll
                 for (int i = 0; i < 4; i += 2)
@@ -261,7 +281,8 @@ __device__ __forceinline__ void cast_tile16(const Tile& tl, const T* x, long lon
 #pragma unroll
             for (int i = 0; i < 8; i += 4) {
                 const float4 f = *reinterpret_cast<const float4*>(&inv_col[cl + i]);
-                iv[i] = f.x, iv[i + 1] = f.y, iv[i + 2] = f.z, iv[i + 3] = f.w;
+                iv[i / 2] = P2::scale(f.x, f.y);
+                iv[i / 2 + 1] = P2::scale(f.z, f.w);
             }
         }
         uint8_t* out = q_cols + (tl.qc_row + rl) * ld_cols + c;
@@ -271,7 +292,7 @@ __device__ __forceinline__ void cast_tile16(const Tile& tl, const T* x, long lon
             // rows (the rows past nrows were loaded as zero).
             if (FULL || (c < ld_cols && (!(MODE & kBlockForm) || 16 * p + rl < tl.nrows)))
                 *reinterpret_cast<uint2*>(out + 16LL * p * ld_cols) =
-                    cast_words<T, E5M2>(raw[p], iv);
+                    !FULL && 16 * p >= tl.nrows ? make_uint2(0, 0) : cast_words<T, E5M2>(raw[p], iv);
         }
         // part is written again only after the next tile's barrier; its readers
         // of inv_col and part are past theirs by then.
@@ -280,7 +301,7 @@ __device__ __forceinline__ void cast_tile16(const Tile& tl, const T* x, long lon
 
 // The tile of any type, value by value.
 template <typename T, int MODE, bool E5M2>
-__device__ __forceinline__ void cast_tile(const Tile& tl, const T* x, long long ldx, const int* slots, int topk,
+__device__ __forceinline__ void cast_tile(const Tile& tl, const T* x, long long ldx, const int* source,
                                           int cols, bool vec, uint8_t* q_rows, long long ld_rows, uint8_t* s_rows,
                                           long long lds_rows, uint8_t* q_cols, long long ld_cols, uint8_t* s_cols,
                                           long long lds_cols, float (&part)[kWarps][128], float (&inv_col)[128]) {
@@ -296,7 +317,7 @@ __device__ __forceinline__ void cast_tile(const Tile& tl, const T* x, long long 
         raw[p].clear();
         if (r < tl.nrows && c < cols) {
             const int row = tl.r0 + r;
-            const T* a = x + static_cast<long long>(slots ? slots[row] / topk : row) * ldx + c;
+            const T* a = x + static_cast<long long>(source ? source[r] : row) * ldx + c;
             if (vec && c + 8 <= cols) {
                 raw[p].load(a);
             } else {
@@ -407,15 +428,15 @@ __device__ __forceinline__ void cast_tile(const Tile& tl, const T* x, long long 
 }
 
 template <typename T, int MODE, bool E5M2, typename... Args>
-__device__ __forceinline__ void cast_tile_of(const Tile& tl, const T* x, long long ldx, const int* slots, int topk, int cols,
+__device__ __forceinline__ void cast_tile_of(const Tile& tl, const T* x, long long ldx, const int* source, int cols,
                                              bool vec, Args&&... args) {
     if constexpr (sizeof(T) == 2) {
         if (vec && tl.nrows == kFp8Block && tl.c0 + kFp8Block <= cols)  // the common case without its edge tests
-            cast_tile16<T, MODE, E5M2, true>(tl, x, ldx, slots, topk, cols, vec, args...);
+            cast_tile16<T, MODE, E5M2, true>(tl, x, ldx, source, cols, vec, args...);
         else
-            cast_tile16<T, MODE, E5M2, false>(tl, x, ldx, slots, topk, cols, vec, args...);
+            cast_tile16<T, MODE, E5M2, false>(tl, x, ldx, source, cols, vec, args...);
     } else {
-        cast_tile<T, MODE, E5M2>(tl, x, ldx, slots, topk, cols, vec, args...);
+        cast_tile<T, MODE, E5M2>(tl, x, ldx, source, cols, vec, args...);
     }
 }
 
@@ -425,6 +446,7 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 4 : 2) fp8_cast_ker
     __shared__ float part[kWarps][128];
     __shared__ __align__(16) float inv_col[128];
     __shared__ int found[3];
+    __shared__ int source[kFp8Block];  // with a route, the row of x behind each row of the tile
     grid_dependency_wait();
     grid_launch_dependents();
     Tile tl;
@@ -469,12 +491,16 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 4 : 2) fp8_cast_ker
         tl.r0 = blockIdx.y * kFp8Block;
         tl.nrows = min(j.rows - tl.r0, kFp8Block);
     }
+    if (j.slots) {  // once for all column blocks: a division per row
+        if (static_cast<int>(threadIdx.x) < tl.nrows) source[threadIdx.x] = j.slots[tl.r0 + threadIdx.x] / j.topk;
+        __syncthreads();
+    }
     tl.qc_row = static_cast<long long>(blockIdx.y) * kFp8Block;
     tl.sc_row = blockIdx.y;
     const int nblk = (j.cols + kFp8Block - 1) / kFp8Block;
     for (int cb = blockIdx.x * span; cb < min(nblk, static_cast<int>(blockIdx.x + 1) * span); ++cb) {
         tl.c0 = cb * kFp8Block;
-        cast_tile_of<T, MODE, E5M2>(tl, static_cast<const T*>(j.x), j.ldx, j.slots, j.topk, j.cols, vec, j.q_rows, j.ld_rows,
+        cast_tile_of<T, MODE, E5M2>(tl, static_cast<const T*>(j.x), j.ldx, j.slots ? source : nullptr, j.cols, vec, j.q_rows, j.ld_rows,
                                     j.s_rows, j.lds_rows, j.q_cols, j.ld_cols, j.s_cols, j.lds_cols, part, inv_col);
     }
 }
@@ -494,7 +520,7 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 4 : 2) fp8_cast_wei
         tl.qc_row = static_cast<long long>(g) * j.rows + tl.r0;
         tl.sc_row = 0;
         uint8_t* scale = j.scale + (static_cast<long long>(g) * nb + blockIdx.y) * kb + blockIdx.x;
-        cast_tile_of<T, kBlockForm, E5M2>(tl, static_cast<const T*>(j.w) + g * j.stride_w, j.ldw, nullptr, 1, j.cols, vec,
+        cast_tile_of<T, kBlockForm, E5M2>(tl, static_cast<const T*>(j.w) + g * j.stride_w, j.ldw, nullptr, j.cols, vec,
                                           static_cast<uint8_t*>(nullptr), 0LL, static_cast<uint8_t*>(nullptr), 0LL, j.q,
                                           j.ldq, scale, 0LL, part, inv_col);
     }
