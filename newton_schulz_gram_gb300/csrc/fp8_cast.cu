@@ -506,7 +506,7 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 4 : 2) fp8_cast_ker
 }
 
 template <typename T, bool E5M2>
-__global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 4 : 2) fp8_cast_weight_kernel(CastWeightJob j, bool vec) {
+__global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 3 : 2) fp8_cast_weight_kernel(CastWeightJob j, bool vec) {
     __shared__ float part[kWarps][128];
     __shared__ __align__(16) float inv_col[128];
     grid_dependency_wait();
