@@ -80,8 +80,8 @@ class MoeRoute:
 
 class _Fp8:
     """An 8-bit operand: values q and the 8-bit exponents of its scales."""
-    __slots__ = ("_buf", "_q", "_scale", "_q_shape", "_scale_shape", "p_q", "p_scale", "ld", "ld_scale", "fmt", "cols",
-                 "device")
+    __slots__ = ("_buf", "_at", "_q", "_scale", "_q_shape", "_scale_shape", "p_q", "p_scale", "ld", "ld_scale", "fmt",
+                 "cols", "device")
 
     def _from(self, q, scale, cols, q_dims):
         for name, t, dtypes in (("q", q, _FP8_FORMAT), ("scale", scale, {torch.float8_e8m0fnu})):
@@ -91,38 +91,33 @@ class _Fp8:
         _same_device(q, "scale", scale)
         if not 0 < cols <= q.shape[-1]:
             raise ValueError("cols must be in 1 .. the columns of q")
-        self._buf, self._q, self._scale = None, q, scale
+        self._buf, self._at, self._q, self._scale = None, 0, q, scale
         self._q_shape, self._scale_shape = tuple(q.shape), tuple(scale.shape)
         self.p_q, self.p_scale, self.ld, self.ld_scale = q.data_ptr(), scale.data_ptr(), q.shape[-1], scale.shape[-1]
         self.fmt, self.cols, self.device = _FP8_FORMAT[q.dtype], cols, q.get_device()
 
     @classmethod
-    def _made(cls, q_shape, scale_shape, cols, fmt, like, stream):
+    def _made(cls, q_shape, scale_shape, cols, fmt, buf, at=0):
+        """On bytes of buf from byte `at` on: q, then the exponents."""
         self = cls.__new__(cls)
-        n = m = 1
-        for v in q_shape:
-            n *= v
-        for v in scale_shape:
-            m *= v
-        buf = _new((n + m,), torch.uint8, like, stream)
-        self._buf, self._q, self._scale, self._q_shape, self._scale_shape = buf, None, None, q_shape, scale_shape
-        self.p_q = buf.data_ptr()
-        self.p_scale = self.p_q + n
+        self._buf, self._at, self._q, self._scale, self._q_shape, self._scale_shape = buf, at, None, None, q_shape, scale_shape
+        self.p_q = buf.data_ptr() + at
+        self.p_scale = self.p_q + _numel(q_shape)
         self.ld, self.ld_scale, self.fmt, self.cols, self.device = q_shape[-1], scale_shape[-1], fmt, cols, buf.get_device()
         return self
 
     @property
     def q(self):
         if self._q is None:
-            n = self._buf.shape[0] - _numel(self._scale_shape)
-            self._q = self._buf[:n].view(_FP8[self.fmt]).view(self._q_shape)
+            at = self._at
+            self._q = self._buf[at:at + _numel(self._q_shape)].view(_FP8[self.fmt]).view(self._q_shape)
         return self._q
 
     @property
     def scale(self):
         if self._scale is None:
-            n = self._buf.shape[0] - _numel(self._scale_shape)
-            self._scale = self._buf[n:].view(torch.float8_e8m0fnu).view(self._scale_shape)
+            at = self._at + _numel(self._q_shape)
+            self._scale = self._buf[at:at + _numel(self._scale_shape)].view(torch.float8_e8m0fnu).view(self._scale_shape)
         return self._scale
 
 
@@ -376,6 +371,13 @@ def gns_moe_combine_backward(dout, y, weights, route, stream=None):
 
 # --------------------------------------------------------- 8-bit operands
 
+# Both forms of an operand of up to this many bytes share one allocation (the
+# second costs the host 3 us of the call's 14, as much as a small cast takes on
+# the GPU). Larger forms have their own: whichever lives longer, the column
+# form until the backward pass, would hold the memory of both.
+_SHARED = 16 << 20
+
+
 def _format(fmt):
     if fmt not in FORMATS:
         raise ValueError(f"fmt must be one of {sorted(FORMATS)}")
@@ -403,13 +405,18 @@ def gns_fp8_quantize(x, fmt="e4m3", route=None, gather=False, rows=True, cols=Tr
     else:
         blocks = -(-n // BLOCK)
     ld = _up(c, 16)
-    r = k = None
+    r = k = buf = None
     q_r = s_r = q_c = s_c = None
+    kb, at = -(-c // BLOCK), 0
+    r_bytes, k_bytes = _up(n * (ld + kb), 256), blocks * (BLOCK * ld + c)
+    if rows and cols and r_bytes + k_bytes <= _SHARED:
+        buf, at = _new((r_bytes + k_bytes,), torch.uint8, x, stream), r_bytes
     if rows:
-        r = Fp8Rows._made((n, ld), (-(-c // BLOCK), n), c, f, x, stream)
+        r = Fp8Rows._made((n, ld), (kb, n), c, f, _new((r_bytes,), torch.uint8, x, stream) if buf is None else buf)
         q_r, s_r = r.p_q, r.p_scale
     if cols:
-        k = Fp8Cols._made((blocks * BLOCK, ld), (blocks, c), c, f, x, stream)
+        k = Fp8Cols._made((blocks * BLOCK, ld), (blocks, c), c, f,
+                          _new((k_bytes,), torch.uint8, x, stream) if buf is None else buf, at)
         k.rows = n
         q_c, s_c = k.p_q, k.p_scale
     check(load().gns_fp8_quantize(x.data_ptr(), ldx, DTYPES[x.dtype], n, c, slots, topk, offsets, groups, f, q_r, ld, s_r, n,
@@ -432,7 +439,9 @@ def gns_fp8_quantize_weight(w, fmt="e4m3", stream=None):
         groups, n, k = w.shape
         ldw, stride = k, n * k
     ld = _up(k, 16)
-    out = Fp8Weight._made((groups, n, ld), (groups, -(-n // BLOCK), -(-k // BLOCK)), k, f, w, stream)
+    nb, kb = -(-n // BLOCK), -(-k // BLOCK)
+    buf = _new((groups * (n * ld + nb * kb),), torch.uint8, w, stream)
+    out = Fp8Weight._made((groups, n, ld), (groups, nb, kb), k, f, buf)
     out.grouped = grouped
     check(load().gns_fp8_quantize_weight(w.data_ptr(), ldw, stride, DTYPES[w.dtype], groups, n, k, f, out.p_q, ld,
                                          out.p_scale, _on(w, stream)), "gns_fp8_quantize_weight")

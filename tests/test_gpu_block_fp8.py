@@ -306,6 +306,37 @@ def test_empty_inputs(gns):
     assert torch.equal(gns.gns_fp8_matmul_wgrad(d, c, out_dtype=torch.float32), torch.zeros(5, 7, device="cuda"))
 
 
+def test_both_forms_with_and_without_a_shared_allocation(gns, monkeypatch):
+    from newton_schulz_gram_gb300 import block
+    x = torch.randn(333, 261, device="cuda", dtype=torch.bfloat16)
+    r, c = gns.gns_fp8_quantize(x)
+    monkeypatch.setattr(block, "_SHARED", 0)
+    r2, c2 = gns.gns_fp8_quantize(x)
+    assert r._buf is c._buf and r2._buf is not c2._buf
+    for a, b in ((r, r2), (c, c2)):
+        assert a.q.shape == b.q.shape and a.scale.shape == b.scale.shape
+        assert torch.equal(a.q.view(torch.uint8), b.q.view(torch.uint8))
+        assert torch.equal(a.scale.view(torch.uint8), b.scale.view(torch.uint8))
+
+
+def test_every_16_bit_value(gns):
+    """All bit patterns of the 16-bit types (subnormals, infinities and NaN among
+    them), in blocks of one binade and of mixed ones."""
+    bits = np.arange(65536, dtype=np.uint32).astype(np.uint16).view(np.int16)
+    mixed = np.random.default_rng(12).permutation(bits)
+    for dtype in (torch.bfloat16, torch.float16):
+        for b in (bits, mixed):
+            x = torch.from_numpy(b.copy()).view(dtype).reshape(256, 256).cuda()
+            for fmt in ("e4m3", "e5m2"):
+                r, c = gns.gns_fp8_quantize(x, fmt=fmt)
+                w = gns.gns_fp8_quantize_weight(x, fmt=fmt)
+                for (scale, v), got_scale, got in ((B.fp8_rows(f64(x), fmt), r.scale, values_rows(r)),
+                                                   (B.fp8_cols(f64(x), fmt), c.scale, values_cols(c)),
+                                                   (B.fp8_blocks(f64(x), fmt), w.scale[0], values_weight(w)[0])):
+                    assert np.array_equal(scales(got_scale), scale)
+                    assert np.array_equal(got, v, equal_nan=True)
+
+
 def test_runs_repeat_and_on_another_stream(gns):
     rng = np.random.default_rng(11)
     x, w = loud(500, 640, 0, torch.bfloat16, rng), loud(700, 640, 0, torch.bfloat16, rng)
