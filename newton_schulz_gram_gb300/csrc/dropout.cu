@@ -13,7 +13,9 @@
 // value (a NaN in x is dropped too).
 //
 // Bound: HBM, 2 (3 with the residual) elements moved per element; about nine
-// integer instructions of Philox per element stay below that at 2 bytes.
+// integer instructions of Philox per element stay below that at 2 bytes. 2^26
+// bf16 elements: 59 us with the residual (6.8 TB/s), 48 without (5.6); 1021 x
+// 4093 unaligned fp32 ones 7.8 (4.3 TB/s, from L2).
 #include "blockops.cuh"
 #include "dropout.cuh"
 #include "philox.cuh"
@@ -23,7 +25,9 @@ namespace gns {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kUnroll = 2;  // blocks of eight elements per thread on the vector path
+// Blocks of eight elements per thread on the vector path. With and without the
+// residual, as above: one 70 and 58 us, two 67 and 47, four 59 and 48, eight 68 and 46.
+constexpr int kUnroll = 4;
 
 struct Draw {
     uint32_t k0, k1, step_lo, step_hi, threshold;
