@@ -43,7 +43,7 @@ int map_u8(CUtensorMap* m, const void* p, int64_t inner, int64_t outer, int64_t 
 
 // The map that whole rows of the product's output are stored through, where it
 // can be described (16-byte rows).
-int map_output(Fp8GemmJob& j) {
+int map_output(Fp8GemmJob& j, int cg) {
     const bool split = j.split > 1;
     const int es = split ? 4 : elem_bytes(j.out_dtype);
     void* p = split ? static_cast<void*>(j.partial) : j.D;
@@ -56,10 +56,11 @@ int map_output(Fp8GemmJob& j) {
     if (!fn) return fail(GNS_ERR_CUDA, "cuTensorMapEncodeTiled is unavailable");
     cuuint64_t dims[3] = {static_cast<cuuint64_t>(j.N), static_cast<cuuint64_t>(rows), static_cast<cuuint64_t>(G)};
     cuuint64_t strides[2] = {static_cast<cuuint64_t>(ld * es), static_cast<cuuint64_t>(stride * es)};
-    cuuint32_t box[3] = {static_cast<cuuint32_t>(128 / es), 32, 1};
+    cuuint32_t box[3] = {static_cast<cuuint32_t>(fp8_store_row(cg) / es), 32, 1};
     cuuint32_t estr[3] = {1, 1, 1};
     const CUresult r = fn(&j.mapD, es == 2 ? CU_TENSOR_MAP_DATA_TYPE_UINT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 3, p, dims,
-                          strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                          strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                          fp8_store_row(cg) == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B,
                           CU_TENSOR_MAP_L2_PROMOTION_NONE, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
     if (r != CUDA_SUCCESS) return fail(GNS_ERR_INVALID, "cuTensorMapEncodeTiled failed for the output");
     return GNS_OK;
@@ -127,7 +128,7 @@ int product(const void* a, int64_t lda, const uint8_t* sa, int64_t ld_sa, int fm
         RET(ensure_workspace(*st, ws_used + sizeof(float) * static_cast<size_t>(j.split) * rows * out));
         j.partial = reinterpret_cast<float*>(st->ws + ws_used);
     }
-    RET(map_output(j));
+    RET(map_output(j, cg));
     begin_call(*st);
     j.st = st->status;
     LAUNCH(kClsFp8Gemm, launch_fp8_gemm(j, cg, st->num_sms, s));
@@ -378,7 +379,7 @@ int gns_fp8_matmul_wgrad(const void* dy, int64_t lddy, const uint8_t* scale_dy, 
     j.strideD = stride_dw;
     j.out_dtype = out_dtype;
     j.split = 1;
-    RET(map_output(j));
+    RET(map_output(j, cg));
     begin_call(*st);
     j.st = st->status;
     LAUNCH(kClsFp8Gemm, launch_fp8_gemm(j, cg, st->num_sms, s));

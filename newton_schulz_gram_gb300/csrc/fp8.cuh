@@ -12,6 +12,13 @@ namespace gns {
 
 constexpr int kFp8Block = 128;
 
+// Bytes of a row of the product's output that one bulk store takes (and its
+// swizzle), for single CTAs and pairs. A single CTA's tile needs 48 KB per k
+// block, and with 64-byte rows there is room for a fourth (data and weight
+// gradient of 256 experts of 512 x 2048, 65536 rows: 103 and 129 us, 113 and 138
+// with 128-byte rows and three); a pair's needs 32 KB and has five with 128.
+constexpr int fp8_store_row(int cg) { return cg == 1 ? 64 : 128; }
+
 // The cast of a rows x cols matrix; see gns_fp8_quantize. Either output may
 // be null. With offsets the token blocks of the column form are those of the
 // G groups of rows, and rows past offsets[G] are not written.

@@ -69,7 +69,9 @@ static_assert(BN - kAcc1 <= 32, "the overlap lies in one chunk of 32 columns of 
 // 256 tiles with paired MMAs; each stages its 128 rows of A and 128 of B's 256.
 template <int CG>
 struct Cfg {
-    static constexpr int STAGES = CG == 1 ? 3 : 4;
+    static constexpr int STAGES = CG == 1 ? 4 : 5;
+    static constexpr int STORE_ROW = fp8_store_row(CG);          // bytes of a row staged for an output store
+    static constexpr uint32_t STORE_BYTES = 32 * STORE_ROW;      // an epilogue warp's buffer
     static constexpr int BNH = BN / CG;  // rows of B a CTA stages
     static constexpr uint32_t B_BYTES = BNH * BK;
     static constexpr int TM = BM * CG;
@@ -83,8 +85,6 @@ constexpr int kSlotBlocks = 4;
 constexpr uint32_t kSlotBytes = 512 + 1024;
 constexpr int kSegment = 16;  // k blocks of a segment of an fp32 result
 static_assert(kSegment % kSlotBlocks == 0, "a scale slot lies in one segment");
-constexpr int kStageRow = 128;               // bytes of a row staged for the output stores
-constexpr int kStageBytes = 32 * kStageRow;  // a buffer of an epilogue warp, which has two
 
 constexpr int kTileSlots = 4;
 constexpr int kTileReaders = 2 + kSlotBlocks + kEpiWarps;  // producer, MMA issuer, scale builder, epilogue warps
@@ -110,7 +110,7 @@ struct Groups {
 template <int CG>
 constexpr int smem_bytes() {
     return 1024 + Cfg<CG>::STAGES * static_cast<int>(A_BYTES + Cfg<CG>::B_BYTES) + kScaleSlots * static_cast<int>(kSlotBytes) +
-           kEpiWarps * 2 * kStageBytes + kTileSlots * static_cast<int>(sizeof(Tile)) + num_bars(Cfg<CG>::STAGES) * 8 + 16 +
+           kEpiWarps * static_cast<int>(Cfg<CG>::STORE_BYTES) + kTileSlots * static_cast<int>(sizeof(Tile)) + num_bars(Cfg<CG>::STAGES) * 8 + 16 +
            static_cast<int>(sizeof(Groups));
 }
 static_assert(smem_bytes<1>() <= 232448 && smem_bytes<2>() <= 232448, "shared memory budget");
@@ -257,6 +257,13 @@ __device__ __forceinline__ uint32_t pack_pair(float lo, float hi) {
     }
 }
 
+// Offset of a staged row's 16-byte piece: the 64- or 128-byte swizzle.
+template <int ROW>
+__device__ __forceinline__ uint32_t stage_piece(int row, int piece) {
+    static_assert(ROW == 64 || ROW == 128, "a swizzle's row");
+    return row * ROW + ((piece ^ (ROW == 64 ? (row >> 1) & 3 : row & 7)) << 4);
+}
+
 __device__ __forceinline__ uint32_t add_bits(uint32_t a, uint32_t b) {
     return __float_as_uint(__uint_as_float(a) + __uint_as_float(b));
 }
@@ -282,28 +289,29 @@ __device__ __forceinline__ void bulk_store(const CUtensorMap* m, uint32_t src, i
 // store instruction covers four whole 128-byte lines where rows start on
 // 16-byte boundaries, and runs of neighbouring elements where they do not. With
 // `add` (fp32) the stored values are added to; a lane meets its own stores.
-template <int ES>
+template <int ES, int ROW>
 __device__ __noinline__ void store_rows(uint32_t stage, uint8_t* d, long long ldd, int rows, int left, bool aligned,
                                            bool add, int lane) {
-    constexpr int PASS = kStageRow / ES;  // columns
+    constexpr int PASS = ROW / ES;  // columns
     constexpr int PIECE = 16 / ES;        // elements of a 16-byte piece
+    constexpr int PR = ROW / 16;    // pieces of a row
     if (aligned) {
-        const int k = lane & 7, r0 = lane >> 3;
-        uint4 piece[8];  // all reads first
+        const int k = lane % PR, r0 = lane / PR;
+        uint4 piece[PR];  // all reads first
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            const int r = 4 * j + r0;
-            piece[j] = ld_shared_v4(stage + r * kStageRow + ((k ^ (r & 7)) << 4));
+        for (int j = 0; j < PR; ++j) {
+            const int r = 32 / PR * j + r0;
+            piece[j] = ld_shared_v4(stage + stage_piece<ROW>(r, k));
         }
         if (ES == 4 && add && (k + 1) * PIECE <= left) {
-            uint4 old[8];
+            uint4 old[PR];
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                const int r = 4 * j + r0;
+            for (int j = 0; j < PR; ++j) {
+                const int r = 32 / PR * j + r0;
                 old[j] = r < rows ? *reinterpret_cast<const uint4*>(d + r * ldd * ES + 16 * k) : make_uint4(0, 0, 0, 0);
             }
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
+            for (int j = 0; j < PR; ++j) {
                 piece[j].x = add_bits(old[j].x, piece[j].x);
                 piece[j].y = add_bits(old[j].y, piece[j].y);
                 piece[j].z = add_bits(old[j].z, piece[j].z);
@@ -311,8 +319,8 @@ __device__ __noinline__ void store_rows(uint32_t stage, uint8_t* d, long long ld
             }
         }
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            const int r = 4 * j + r0;
+        for (int j = 0; j < PR; ++j) {
+            const int r = 32 / PR * j + r0;
             uint8_t* a = d + r * ldd * ES + 16 * k;
             if (r >= rows) continue;
             if ((k + 1) * PIECE <= left) {
@@ -330,10 +338,11 @@ __device__ __noinline__ void store_rows(uint32_t stage, uint8_t* d, long long ld
             }
         }
     } else {
-        for (int r = 0; r < min(rows, 32); ++r) {
+        constexpr int LANES = PASS < 32 ? PASS : 32;  // lanes on a row
+        for (int r = lane / LANES; r < min(rows, 32); r += 32 / LANES) {
 #pragma unroll
-            for (int c = lane; c < PASS; c += 32) {
-                const uint32_t at = stage + r * kStageRow + (((c / PIECE) ^ (r & 7)) << 4) + (c % PIECE) * ES;
+            for (int c = lane % LANES; c < PASS; c += LANES) {
+                const uint32_t at = stage + stage_piece<ROW>(r, c / PIECE) + (c % PIECE) * ES;
                 if (c < left) {
                     if constexpr (ES == 2)
                         *reinterpret_cast<uint16_t*>(d + r * ldd * ES + c * ES) = ld_shared_u16(at);
@@ -376,7 +385,7 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_gemm_kernel(const __grid_cons
     uint8_t* sA = smem;
     uint8_t* sB = sA + STAGES * A_BYTES;
     uint8_t* staging = sB + STAGES * B_BYTES;  // 1024-byte aligned, as the swizzle wants
-    uint8_t* scales = staging + kEpiWarps * 2 * kStageBytes;
+    uint8_t* scales = staging + kEpiWarps * Cfg<CG>::STORE_BYTES;
     Tile* tiles = reinterpret_cast<Tile*>(scales + kScaleSlots * kSlotBytes);
     uint64_t* bars = reinterpret_cast<uint64_t*>(tiles + kTileSlots);
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + num_bars(STAGES));
@@ -728,7 +737,7 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_gemm_kernel(const __grid_cons
         const int q = warp & 3;  // TMEM lane quarter this warp may read
         const int ew = warp - kEpiWarp0;
         const int half = ew >> 2;  // columns 128 half .. + 127 of the tile
-        const uint32_t stage0 = smem_u32(staging + ew * 2 * kStageBytes);
+        const uint32_t stage = smem_u32(staging + ew * Cfg<CG>::STORE_BYTES);
         const uint32_t acce_lead = CG == 2 ? map_to_rank(acce0, 0) : acce0;
         const uint32_t overlap_lead = CG == 2 ? map_to_rank(overlap_bar, 0) : overlap_bar;
         auto hand_back = [&](uint32_t bar) {
@@ -742,7 +751,6 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_gemm_kernel(const __grid_cons
             }
         };
         int it = 0;         // segments read; the accumulator is it & 1
-        uint32_t turn = 0;  // staging buffer of the next pass
         bool ok = true;
         Tile tl;
         for (int i = 0; ok && take(i, tl, true); ++i) {
@@ -759,7 +767,6 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_gemm_kernel(const __grid_cons
             const bool aligned = split ? P.N % 4 == 0
                                        : ((reinterpret_cast<uintptr_t>(P.D) | static_cast<uintptr_t>(P.ldd * ES) |
                                            static_cast<uintptr_t>(P.strideD * ES)) & 15) == 0;
-            constexpr int passes = ES == 2 ? 2 : 4;
             int kb = tl.kb0;
             // 32 whole rows leave by a bulk store; the ragged end of a group,
             // and outputs without 16-byte rows, by the warp's own stores.
@@ -778,66 +785,67 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_gemm_kernel(const __grid_cons
                 // The chunk in the overlap comes first: accumulator 0's last
                 // columns (the second half's warps), accumulator 1's first.
                 const bool mine = half == (buf == 0);
-                bool fresh = true;  // no pass of this segment has been stored
+                const bool add = ES == 4 && kb > tl.kb0;
+                bool fresh = true;  // nothing of this segment has been stored
+                // Chunks of 32 columns, each staged and stored in kRounds
+                // pieces, or kJoin chunks in one.
+                constexpr int ROW = Cfg<CG>::STORE_ROW;
+                constexpr int kRounds = 32 * ES > ROW ? 32 * ES / ROW : 1, kJoin = ROW > 32 * ES ? ROW / (32 * ES) : 1;
 #pragma unroll 1
-                for (int n = 0; n < passes; ++n) {
-                    const int p = buf == 0 ? passes - 1 - n : n;
-                    uint32_t w[32];
+                for (int n = 0; n < kCols / 32; ++n) {
+                    const int p = buf == 0 ? kCols / 32 - 1 - n : n;
+                    uint32_t x[32];
                     if (filled && live) {
-                        if constexpr (ES == 2) {
-                            uint32_t x[32], y[32];
-                            tmem_ld_32x32b_x32(acc + 64 * p, x);
-                            tmem_ld_32x32b_x32(acc + 64 * p + 32, y);
-                            tmem_ld_wait_for(x);
-                            tmem_ld_wait_for(y);
-#pragma unroll
-                            for (int j = 0; j < 16; ++j) {
-                                w[j] = pack_pair<T>(__uint_as_float(x[2 * j]), __uint_as_float(x[2 * j + 1]));
-                                w[16 + j] = pack_pair<T>(__uint_as_float(y[2 * j]), __uint_as_float(y[2 * j + 1]));
-                            }
-                        } else {
-                            tmem_ld_32x32b_x32(acc + 32 * p, w);
-                            tmem_ld_wait_for(w);
-                        }
+                        tmem_ld_32x32b_x32(acc + 32 * p, x);
+                        tmem_ld_wait_for(x);
                     } else {
 #pragma unroll
-                        for (int j = 0; j < 32; ++j) w[j] = 0;
+                        for (int j = 0; j < 32; ++j) x[j] = 0;
                     }
                     if (filled) {
                         if (n == 0 && mine) hand_back(overlap_lead);
-                        if (n == passes - 1) hand_back(acce_lead + 8 * buf);
+                        if (n == kCols / 32 - 1) hand_back(acce_lead + 8 * buf);
                     }
-                    const int c0 = p * (kStageRow / ES);
-                    if (!live || c0 >= ncol) continue;
-                    // The two buffers take turns: all bulk stores but the last
-                    // have read theirs (all, before one that the warp's own
-                    // stores use, which no group counts). Before a segment is
-                    // added, the stores it adds to are complete.
-                    const uint32_t stage = stage0 + turn * kStageBytes;
-                    const bool add = ES == 4 && kb > tl.kb0;
-                    turn ^= 1;
-                    if (lane == 0) {
-                        if (add && fresh)
-                            asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
-                        else if (bulk)
-                            asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");
-                        else
-                            asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
-                    }
-                    fresh = false;
-                    __syncwarp();
 #pragma unroll
-                    for (int k = 0; k < 8; ++k)
-                        st_shared_v4(stage + lane * kStageRow + ((k ^ (lane & 7)) << 4), w[4 * k], w[4 * k + 1], w[4 * k + 2],
-                                     w[4 * k + 3]);
-                    if (bulk) {
-                        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-                        __syncwarp();
-                        if (lane == 0)
-                            bulk_store(&P.mapD, stage, col + c0, static_cast<int>(row0), split ? tl.split : wgrad ? tl.g : 0, add);
-                    } else {
-                        __syncwarp();
-                        store_rows<ES>(stage, d + c0 * ES, ldd, rows, ncol - c0, aligned, add, lane);
+                    for (int h = 0; h < kRounds; ++h) {
+                        const int c0 = 32 * (kJoin == 2 ? p & ~1 : p) + h * (ROW / ES);
+                        if (!live || c0 >= ncol) continue;
+                        if (kJoin == 1 || n % 2 == 0) {
+                            // The last bulk store has read the buffer. Before a
+                            // segment is added, the stores it adds to are complete.
+                            if (lane == 0) {
+                                if (add && fresh)
+                                    asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
+                                else
+                                    asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+                            }
+                            fresh = false;
+                            __syncwarp();
+                        }
+                        constexpr int PIECES = ROW / 16 / kJoin;
+#pragma unroll
+                        for (int k = 0; k < PIECES; ++k) {
+                            uint32_t w[4];
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) {
+                                if constexpr (ES == 2)
+                                    w[i] = pack_pair<T>(__uint_as_float(x[8 * k + 2 * i]), __uint_as_float(x[8 * k + 2 * i + 1]));
+                                else
+                                    w[i] = x[4 * PIECES * h + 4 * k + i];
+                            }
+                            st_shared_v4(stage + stage_piece<ROW>(lane, k + (kJoin == 2 ? PIECES * (p & 1) : 0)), w[0], w[1],
+                                         w[2], w[3]);
+                        }
+                        if (kJoin == 2 && n % 2 == 0) continue;
+                        if (bulk) {
+                            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                            __syncwarp();
+                            if (lane == 0)
+                                bulk_store(&P.mapD, stage, col + c0, static_cast<int>(row0), split ? tl.split : wgrad ? tl.g : 0, add);
+                        } else {
+                            __syncwarp();
+                            store_rows<ES, ROW>(stage, d + c0 * ES, ldd, rows, ncol - c0, aligned, add, lane);
+                        }
                     }
                 }
                 it += filled;
