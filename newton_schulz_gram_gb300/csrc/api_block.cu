@@ -102,7 +102,7 @@ int product(const void* a, int64_t lda, const uint8_t* sa, int64_t ld_sa, int fm
     if (ld_sa < rows) return invalid("a scale's row stride must cover the rows");
     if (ldd < out) return invalid("the output's row stride must cover its columns");
     Fp8GemmJob j{};
-    const int cg = fp8_gemm_cg(rows, out, offsets != nullptr, st->num_sms);
+    const int cg = fp8_gemm_cg(rows, out, offsets != nullptr, !dgrad, out_dtype, st->num_sms);
     j.split = offsets ? 1 : fp8_gemm_split(rows, out, inner, st->num_sms);
     RET(map_u8(&j.mapA, a, inner, rows, 1, lda, lda * rows, 128));
     RET(map_u8(&j.mapB, w, K, N, groups, ldw, ldw * N, fp8_gemm_b_box(cg, dgrad)));
@@ -358,7 +358,7 @@ int gns_fp8_matmul_wgrad(const void* dy, int64_t lddy, const uint8_t* scale_dy, 
     }
     Fp8GemmJob j{};
     const int64_t qrows = offsets ? static_cast<int64_t>(fp8_max_blocks(rows, groups)) * kFp8Block : up(rows, kFp8Block);
-    const int cg = fp8_gemm_cg(N, K, groups > 1, st->num_sms);
+    const int cg = fp8_gemm_cg(N, K, groups > 1, false, out_dtype, st->num_sms);
     RET(map_u8(&j.mapA, dy, N, qrows, 1, lddy, lddy * qrows, 128));
     RET(map_u8(&j.mapB, x, K, qrows, 1, ldx, ldx * qrows, 128));
     j.wgrad = 1;

@@ -91,7 +91,7 @@ struct Fp8GemmJob {
 
 // CTAs per tile (1: 128 x 256 tiles, 2: a pair, 256 x 256) for a product with M
 // rows (of all groups; the weight gradient: of each D) and N columns.
-int fp8_gemm_cg(int M, int N, bool grouped, int num_sms);
+int fp8_gemm_cg(int M, int N, bool grouped, bool forward, int out_dtype, int num_sms);
 // Rows of the boxes of B's tensor map.
 inline int fp8_gemm_b_box(int cg, bool b_mn) { return b_mn || cg == 2 ? 128 : 256; }
 

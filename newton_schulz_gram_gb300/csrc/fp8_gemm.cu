@@ -35,6 +35,13 @@
 // Operands whose contraction runs along the stored rows (the weights of the
 // data gradient, both operands of the weight gradient) are read MN-major
 // through the shared-memory descriptor; nothing is transposed in memory.
+//
+// Bound: the tensor cores for large matrices, HBM for many experts of few rows,
+// the latency of one tile for small ones. 8192 x 14336 x 4096: forward 302 us
+// (3.2 PFLOP/s, 0.85 of twice the measured bf16 rate), data gradient 331 (2.9),
+// weight gradient 347 (2.8). 256 experts of 512 x 2048, 65536 rows: 86, 100 and
+// 126 us (5.5 TB/s of operands and results, each once). One tile of one k block:
+// 4.7 us.
 #include <algorithm>
 
 #include "blockops.cuh"
@@ -369,9 +376,9 @@ __device__ __forceinline__ void mbar_arrive_relaxed(uint32_t cluster_addr) {
 // T is the type that is stored: D's, or float for the partial sums of a split.
 // One kernel per type and direction rather than branches: the warps' roles run
 // at the same time and share the instruction cache, which short tiles feel most
-// (256 experts of 512 x 2048, 65536 rows, one kernel for all: data gradient 137
-// us, weight gradient 155, against 112 and 138; one for all directions 119 and
-// 138). Rare paths, the plain stores and the waits' spins, are out of line for
+// (256 experts of 512 x 2048, 65536 rows, with three operand stages: one kernel
+// for all, data gradient 137 us, weight gradient 155; one per type 119 and 138;
+// one per type and direction 112 and 138). Rare paths, the plain stores and the waits' spins, are out of line for
 // the same reason.
 template <int CG, typename T, bool wgrad>
 __global__ void __launch_bounds__(kThreads, 1) fp8_gemm_kernel(const __grid_constant__ Fp8GemmJob P) {
@@ -941,7 +948,7 @@ int launch_variant(const Fp8GemmJob& job, long long max_tiles, int num_sms, cuda
 
 int fp8_gemm_split(int rows, int N, int K, int num_sms) {
     // Fewer tiles than SMs: the contraction is split where that pays. Measured: a
-    // k block takes 0.37 us (three stages in flight at the latency of L2), the
+    // k block takes 0.33 us (four stages in flight at the latency of L2), the
     // second kernel 3 us, and its fp32 partial sums, written and read, 8 bytes
     // per result and split at 7.5 TB/s. (1024 x 768 x 4096, 24 tiles: 17.1 us
     // whole, 15.6 in six parts; 48 x 4096 x 14336, 16 tiles, in nine: 16.4 us.)
@@ -949,9 +956,9 @@ int fp8_gemm_split(int rows, int N, int K, int num_sms) {
     const int kb = (K + BK - 1) / BK;
     const int most = static_cast<int>(std::min<long long>(num_sms / tiles, kb / 4));  // the pipeline fills with four
     int best = 1;
-    double least = 0.37 * kb;
+    double least = 0.33 * kb;
     for (int s = 2; s <= most; ++s) {
-        const double us = 0.37 * ((kb + s - 1) / s) + 3.0 + s * (8.0 / 7.5e6) * rows * N;
+        const double us = 0.33 * ((kb + s - 1) / s) + 3.0 + s * (8.0 / 7.5e6) * rows * N;
         if (us < least) {
             least = us;
             best = s;
@@ -960,15 +967,21 @@ int fp8_gemm_split(int rows, int N, int K, int num_sms) {
     return best;
 }
 
-int fp8_gemm_cg(int M, int N, bool grouped, int num_sms) {
+int fp8_gemm_cg(int M, int N, bool grouped, bool forward, int out_dtype, int num_sms) {
     // A pair loads and reads from shared memory 32 KB per k block and SM where a
-    // single CTA takes 48 KB (8192 x 14336 x 4096, the three products: 314, 356
-    // and 353 us with pairs, 354, 383 and 385 us without), but its tile of 256
-    // rows wastes more of a ragged group (256 experts of 512 x 2048, 65536
-    // rows: 94, 113 and 159 us with pairs, 91, 113 and 138 us without) and needs
-    // enough tiles for all pairs (1021 x 712 x 4093: 15, 10, 17 against 14, 9, 15).
+    // single CTA takes 48 KB, has larger output stores and a stage more; a single
+    // CTA's loads come from one place and its epilogue hands back to itself.
+    // Measured, pairs against singles: forward, 16-bit results, 8192 x 14336 x
+    // 4096 298 and 310 us, 16384 x 8192 x 8192 683 and 689, 8192 x 4096 x 4096 95
+    // and 91, 8192 x 2048 x 8192 115 and 108; data and weight gradient of the
+    // first 338 and 347, 323 and 337; fp32 results of 8192 x 4096 x 14336 386 and
+    // 421, its weight gradient 392 and 426.
+    // Pairs need enough tiles for all of them (1021 x 712 x 4093: 15, 11, 17
+    // against 13, 11, 16), and their 256 rows waste more of ragged groups (256
+    // experts of 512 x 2048, 65536 rows: 94, 112, 160 against 85, 97, 126).
     const long long tiles = static_cast<long long>((M + 255) / 256) * ((N + BN - 1) / BN);
-    return !grouped && tiles >= num_sms / 2 ? 2 : 1;
+    if (grouped || tiles < num_sms / 2) return 1;
+    return out_dtype == GNS_FP32 || (forward && N >= 8192) ? 2 : 1;
 }
 
 int launch_fp8_gemm(const Fp8GemmJob& job, int cg, int num_sms, cudaStream_t s) {
@@ -985,8 +998,11 @@ int launch_fp8_gemm(const Fp8GemmJob& job, int cg, int num_sms, cudaStream_t s) 
     if (tiles <= 0) return cudaSuccess;
     const int e = by_dtype(job.split > 1 ? static_cast<int>(GNS_FP32) : job.out_dtype, [&](auto t) {
         using T = decltype(t);
-        if (job.wgrad)
-            return cg == 2 ? launch_variant<2, T, true>(job, tiles, num_sms, s) : launch_variant<1, T, true>(job, tiles, num_sms, s);
+        if (job.wgrad) {
+            if constexpr (sizeof(T) == 4)
+                if (cg == 2) return launch_variant<2, T, true>(job, tiles, num_sms, s);
+            return launch_variant<1, T, true>(job, tiles, num_sms, s);
+        }
         return cg == 2 ? launch_variant<2, T, false>(job, tiles, num_sms, s) : launch_variant<1, T, false>(job, tiles, num_sms, s);
     });
     if (e != cudaSuccess || job.split <= 1) return e;

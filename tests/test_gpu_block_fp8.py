@@ -172,6 +172,16 @@ def test_products_of_many_tiles(gns):
                 loud(2300, 2420, 0, torch.bfloat16, rng), torch.float32)
 
 
+@pytest.mark.parametrize("out", ["bf16", "fp16"])
+@pytest.mark.parametrize("tokens,n,k", [(2300, 2420, 2190), (700, 8202, 200), (520, 8192, 136)])
+def test_products_of_many_tiles_in_16_bits(gns, out, tokens, n, k):
+    """Single CTAs and, from 8192 columns of a forward product, pairs; rows of
+    the output that are and are not 16-byte aligned."""
+    rng = np.random.default_rng(n)
+    check_dense(gns, loud(tokens, k, 0, torch.bfloat16, rng), loud(n, k, 0, torch.bfloat16, rng),
+                loud(tokens, n, 0, torch.float32, rng) * 0.01, DTYPES[out], "e5m2")
+
+
 @pytest.mark.parametrize("tokens,n,k", [(9, 300, 5000), (100, 256, 2048), (33, 77, 14336)])
 def test_long_contractions_of_few_rows_are_split(gns, tokens, n, k):
     rng = np.random.default_rng(n)
