@@ -16,13 +16,18 @@ __device__ __forceinline__ float exp_value(uint32_t biased) { return __uint_as_f
 // 1 / 2^(biased - 127); biased <= 247, so the inverse is a normal number.
 __device__ __forceinline__ float exp_inverse(uint32_t biased) { return __uint_as_float((254u - biased) << 23); }
 
+// Four values as the bytes of a word, the first lowest.
 template <bool E5M2>
-__device__ __forceinline__ uint32_t cast_pair(float lo, float hi) {
-    uint16_t r;
+__device__ __forceinline__ uint32_t cast_quad(float a, float b, float c, float d) {
+    uint32_t r;
     if constexpr (E5M2)
-        asm("cvt.rn.satfinite.e5m2x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
+        asm("{\n\t.reg .b16 lo, hi;\n\tcvt.rn.satfinite.e5m2x2.f32 lo, %2, %1;\n\tcvt.rn.satfinite.e5m2x2.f32 hi, %4, %3;\n\tmov.b32 %0, {lo, hi};\n\t}"
+            : "=r"(r)
+            : "f"(a), "f"(b), "f"(c), "f"(d));
     else
-        asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
+        asm("{\n\t.reg .b16 lo, hi;\n\tcvt.rn.satfinite.e4m3x2.f32 lo, %2, %1;\n\tcvt.rn.satfinite.e4m3x2.f32 hi, %4, %3;\n\tmov.b32 %0, {lo, hi};\n\t}"
+            : "=r"(r)
+            : "f"(a), "f"(b), "f"(c), "f"(d));
     return r;
 }
 

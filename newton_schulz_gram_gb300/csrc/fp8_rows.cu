@@ -200,11 +200,9 @@ __global__ void __launch_bounds__(kThreads, 2) fp8_rows_kernel(Fp8RowsJob j, boo
         for (int m = 8; m > 0; m >>= 1) amax = fmaxf(amax, __shfl_xor_sync(half, amax, m));
         const uint32_t e = scale_exponent(amax, 8);
         const float inv = exp_inverse(e);
-        uint32_t w[2];
 #pragma unroll
-        for (int h = 0; h < 2; ++h)
-            w[h] = cast_pair<false>(no_infinity(v[4 * h]) * inv, no_infinity(v[4 * h + 1]) * inv) |
-                   (cast_pair<false>(no_infinity(v[4 * h + 2]) * inv, no_infinity(v[4 * h + 3]) * inv) << 16);
+        for (int c = 0; c < 8; ++c) v[c] = no_infinity(v[c]) * inv;
+        const uint32_t w[2] = {cast_quad<false>(v[0], v[1], v[2], v[3]), cast_quad<false>(v[4], v[5], v[6], v[7])};
         const uint2 lo = to_half4<false>(w[0]), hi = to_half4<false>(w[1]);
         *reinterpret_cast<uint4*>(xq + r * stride + b * kFp8Block + 8 * l) = make_uint4(lo.x, lo.y, hi.x, hi.y);
         if (l == 0) xs[r * nkb + b] = exp_value(e);
