@@ -2,7 +2,7 @@
 // one launch: D[r][n] = x_r . w[g(r)][n] with x cast to 8 bits on the way.
 //
 // Bound: HBM, the weights once, N K bytes per group that has rows. Two blocks
-// of threads per SM cast their group's rows of x once and then walk strips of
+// of threads per SM (one where shared memory has no room for two) cast their group's rows of x once and then walk strips of
 // 16 weight rows; the sixteen warps split the contraction (k block b belongs to
 // warp b mod 16). Each warp streams its own pieces of the weights, across
 // strips, through a ring of cp.async slots that only its own lanes read back,
@@ -16,7 +16,8 @@
 // tcgen05 would add TMEM and descriptors to a kernel that lives for a few
 // microseconds. The warps' sums are joined in a fixed order.
 // One row, 14336 x 4096: 15.1 us (3.9 TB/s); without conversions and products,
-// the loads alone, 11.9. The 8-bit mma.sync took 19.4 us, a block of threads
+// the loads alone, 11.9. Eight rows, whose fp16 forms leave room for one block of
+// threads per SM: 22 (28 with a grid for two). The 8-bit mma.sync took 19.4 us, a block of threads
 // per strip without the ring 15.6, and more of them, of eight warps, 17.0.
 #include <algorithm>
 
@@ -32,8 +33,10 @@ constexpr int kThreads = 512;
 constexpr int kWarps = kThreads / 32;
 constexpr int kStrip = 16;               // weight rows
 constexpr int kSlotBytes = 4 * 32 * 16;  // a warp's k block: four 16-byte pieces per lane
-constexpr int kMaxSlots = 4;
+// Dynamic shared memory of a block: the limit, and what lets two share an SM
+// (228 KB, of which each takes 1 KB and the 18.1 KB of its static arrays).
 constexpr size_t kMaxSmem = 200 * 1024;
+constexpr size_t kSmemOfTwo = 94 * 1024;
 
 __device__ __forceinline__ void mma_16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                           uint32_t b1) {
@@ -219,10 +222,8 @@ __global__ void __launch_bounds__(kThreads, 2) fp8_rows_kernel(Fp8RowsJob j, boo
             // All but the slots - 1 youngest groups have landed: this block's among them.
             if (slots == 1)
                 asm volatile("cp.async.wait_group 0;" ::: "memory");
-            else if (slots == 2)
-                asm volatile("cp.async.wait_group 1;" ::: "memory");
             else
-                asm volatile("cp.async.wait_group 3;" ::: "memory");
+                asm volatile("cp.async.wait_group 1;" ::: "memory");
             const uint32_t at = ring + slot * kSlotBytes;
             uint4 a[2][2];
 #pragma unroll
@@ -285,12 +286,17 @@ bool fp8_rows_fit(int rows, int K) { return rows <= kFp8FewRows && rows_smem(row
 
 int launch_fp8_rows(const Fp8RowsJob& j, int num_sms, cudaStream_t s) {
     const int strips = (j.N + kStrip - 1) / kStrip, nkb = (j.K + kFp8Block - 1) / kFp8Block;
-    // Two blocks per SM when there is one group; with several, a block per strip
-    // of each row that may start a group (most of them end at once).
-    const int blocks = j.offsets ? strips : std::min(strips, 2 * num_sms);
-    const int walk = (strips + blocks - 1) / blocks * ((nkb + kWarps - 1) / kWarps);  // k blocks of a warp
+    // Two blocks per SM where two fit, whose products hide each other's waits
+    // (one row of 14336 x 4096: 15.8 us, one block per SM 19.9), with two slots if
+    // there is room and the walk is that long, else one.
+    const bool two = rows_smem(j.rows, j.K, 1) <= kSmemOfTwo;
     int slots = 1;
-    while (slots < kMaxSlots && slots < walk && rows_smem(j.rows, j.K, 2 * slots) <= kMaxSmem / 2) slots *= 2;
+    if ((nkb + kWarps - 1) / kWarps * ((strips + 2 * num_sms - 1) / (2 * num_sms)) > 1 &&
+        rows_smem(j.rows, j.K, 2) <= (two ? kSmemOfTwo : kMaxSmem))
+        slots = 2;
+    // With several groups a block per strip of each row that may start a group
+    // (most of them end at once).
+    const int blocks = j.offsets ? strips : std::min(strips, (two ? 2 : 1) * num_sms);
     const size_t smem = rows_smem(j.rows, j.K, slots);
     return by_dtype(j.dtype, [&](auto t) {
         using T = decltype(t);
