@@ -2,9 +2,9 @@
 // one launch: D[r][n] = x_r . w[g(r)][n] with x cast to 8 bits on the way.
 //
 // Bound: HBM, the weights once, N K bytes per group that has rows. Two blocks
-// of threads per SM (one where shared memory has no room for two) cast their group's rows of x once and then walk strips of
-// 16 weight rows; the sixteen warps split the contraction (k block b belongs to
-// warp b mod 16). Each warp streams its own pieces of the weights, across
+// of threads per SM (one where shared memory has no room for two) cast their
+// group's rows of x once and then walk strips of 16 weight rows; the sixteen
+// warps split the contraction (k block b belongs to warp b mod 16). Each warp streams its own pieces of the weights, across
 // strips, through a ring of cp.async slots that only its own lanes read back,
 // so nothing but the sum over the warps at the end of a strip synchronizes, and
 // 128 KB per SM are in flight all the time. The products run as mma.sync
@@ -15,10 +15,11 @@
 // long as x uses the same one. Tensor throughput does not matter at 8 columns;
 // tcgen05 would add TMEM and descriptors to a kernel that lives for a few
 // microseconds. The warps' sums are joined in a fixed order.
-// One row, 14336 x 4096: 15.1 us (3.9 TB/s); without conversions and products,
-// the loads alone, 11.9. Eight rows, whose fp16 forms leave room for one block of
-// threads per SM: 22 (28 with a grid for two). The 8-bit mma.sync took 19.4 us, a block of threads
-// per strip without the ring 15.6, and more of them, of eight warps, 17.0.
+// One row, 14336 x 4096: 15.0 us (3.9 TB/s; 28672 x 8192 47.6, 4.9); without
+// conversions and products, the loads alone, 11.9. Eight rows, whose fp16 forms
+// leave room for one block of threads per SM: 20 (28 with a grid for two). The
+// 8-bit mma.sync took 19.4 us for one row, a block of threads per strip without
+// the ring 15.6, and more of them, of eight warps, 17.0.
 #include <algorithm>
 
 #include "blockops.cuh"
@@ -214,11 +215,18 @@ __global__ void __launch_bounds__(kThreads, 2) fp8_rows_kernel(Fp8RowsJob j, boo
 
     const __half* xrow = xq + (gq < count ? gq : count) * stride + 16 * t;
     int slot = 0, buf = 0;
+    // The weights' exponent of the walk's next k block, loaded a block ahead.
+    uint32_t scale = 0;
+    if (warp < nkb && static_cast<int>(blockIdx.x) < strips) scale = __ldg(sw + blockIdx.x * kStrip / kFp8Block * nkb + warp);
     for (int strip = blockIdx.x; strip < strips; strip += gridDim.x, buf ^= 1) {
-        const uint8_t* ws = sw + strip * kStrip / kFp8Block * nkb;
         float acc[4] = {0.0f, 0.0f, 0.0f, 0.0f};
         for (int b = warp; b < nkb; b += kWarps) {
-            const float wsc = exp_value(__ldg(ws + b));
+            const float wsc = exp_value(scale);
+            {
+                int next = b + kWarps, at = strip;
+                if (next >= nkb) next = warp, at += gridDim.x;
+                if (at < strips) scale = __ldg(sw + at * kStrip / kFp8Block * nkb + next);
+            }
             // All but the slots - 1 youngest groups have landed: this block's among them.
             if (slots == 1)
                 asm volatile("cp.async.wait_group 0;" ::: "memory");
