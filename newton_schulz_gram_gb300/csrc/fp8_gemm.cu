@@ -775,9 +775,10 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_gemm_kernel(const __grid_cons
                                        : ((reinterpret_cast<uintptr_t>(P.D) | static_cast<uintptr_t>(P.ldd * ES) |
                                            static_cast<uintptr_t>(P.strideD * ES)) & 15) == 0;
             int kb = tl.kb0;
-            // 32 whole rows leave by a bulk store; the ragged end of a group,
-            // and outputs without 16-byte rows, by the warp's own stores.
-            const bool bulk = P.bulk_store && live && rows >= 32;
+            // Rows leave by bulk stores, which the map clips at D's end. Where a
+            // group ends inside the 32 rows, the next one's follow, and the
+            // warp stores the rows itself; so it does without 16-byte rows.
+            const bool bulk = P.bulk_store && live && (rows >= 32 || wgrad || !P.offsets);
             do {  // segments; once, with zeros, for a group without rows to sum over
                 const bool filled = kb < tl.kb1;
                 const int buf = it & 1;
