@@ -273,6 +273,20 @@ def test_linear_casts_on_the_way(gns, dtype, tokens, topk, experts, n, k, drop):
             assert_close(got[at], a[at] @ b[g].T, np.abs(a[at]) @ np.abs(b[g]).T, adds(k), f"expert {g}")
 
 
+@pytest.mark.parametrize("tokens,n,k", [(1, 10001, 1100), (2, 9800, 2048), (8, 5008, 4096), (8, 5001, 3970), (3, 2500, 14336),
+                                        (8, 300, 14336), (31, 2049, 2048)])
+def test_linear_of_few_rows_and_many_columns(gns, tokens, n, k):
+    """More strips of weight rows than blocks of threads, one or two blocks per
+    SM, and rows that do not fit shared memory."""
+    rng = np.random.default_rng(n)
+    x = loud(tokens, k, 0, torch.bfloat16, rng)
+    wq = gns.gns_fp8_quantize_weight(loud(n, k, 0, torch.bfloat16, rng))
+    a, b = values_rows(gns.gns_fp8_quantize(x, cols=False)[0]), values_weight(wq)[0]
+    want, size = a @ b.T, np.abs(a) @ np.abs(b).T
+    for out in (torch.float32, torch.bfloat16):
+        assert_close(gns.gns_fp8_linear(x, wq, out_dtype=out), want, size, adds(k), "linear")
+
+
 def test_gradients_against_differences(gns):
     """Small whole numbers are their own 8-bit forms and every sum of them is
     exact, so the layer is bilinear there and differences are exact too."""
