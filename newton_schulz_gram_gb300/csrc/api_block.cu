@@ -399,7 +399,7 @@ int gns_fp8_linear(const void* x, int64_t ldx, int dtype, int rows, const int32_
     DeviceState* st = nullptr;
     RET(get_state(&st));
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-    if (fp8_rows_fit(rows, K)) {
+    if (fp8_rows_fit(rows, N, K, groups, offsets != nullptr, st->num_sms)) {
         Fp8RowsJob j{x,       ldx, dtype, slots, slots ? topk : 1, offsets, groups, rows, N, K, format_w,
                      static_cast<const uint8_t*>(w), ldw, ldw * N, scale_w, y, ldy, out_dtype};
         LAUNCH(kClsFp8Gemm, launch_fp8_rows(j, st->num_sms, s));

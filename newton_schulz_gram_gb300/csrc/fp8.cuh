@@ -119,8 +119,10 @@ struct Fp8RowsJob {
     int out_dtype;
 };
 
-constexpr int kFp8FewRows = 8;
-bool fp8_rows_fit(int rows, int K);  // up to eight rows, whose 8-bit form fits in shared memory
+constexpr int kFp8FewRows = 8;     // rows of one matrix (and of a block of threads)
+constexpr int kFp8FewRouted = 32;  // rows of a routed batch
+// Whether launch_fp8_rows takes this product.
+bool fp8_rows_fit(int rows, int N, int K, int groups, bool grouped, int num_sms);
 int launch_fp8_rows(const Fp8RowsJob& job, int num_sms, cudaStream_t s);
 
 }  // namespace gns

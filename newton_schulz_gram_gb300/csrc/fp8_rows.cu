@@ -1,4 +1,4 @@
-// The block-scaled 8-bit linear layer for up to eight rows (a decode step), in
+// The block-scaled 8-bit linear layer for few rows (a decode step), in
 // one launch: D[r][n] = x_r . w[g(r)][n] with x cast to 8 bits on the way.
 //
 // Bound: HBM, the weights once, N K bytes per group that has rows. Two blocks
@@ -103,7 +103,7 @@ __device__ __forceinline__ void load_x(const T* row, int k, int K, bool vec, flo
 }
 
 template <typename T>
-__global__ void __launch_bounds__(kThreads, 2) fp8_rows_kernel(Fp8RowsJob j, bool vec, int slots) {
+__global__ void __launch_bounds__(kThreads, 2) fp8_rows_kernel(Fp8RowsJob j, bool vec, int slots, int chunk) {
     // [kWarps][slots] ring slots, then x in fp16: [rows + 1][K rounded up to 128, + 8], the last row zero, then its
     // scales [rows][k blocks].
     extern __shared__ __align__(16) uint8_t smem[];
@@ -114,7 +114,7 @@ __global__ void __launch_bounds__(kThreads, 2) fp8_rows_kernel(Fp8RowsJob j, boo
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     int g = 0, r0 = 0, count = j.rows;
     if (j.offsets) {
-        // Row blockIdx.y stands for its group if it is the group's first.
+        // Row blockIdx.y stands for `chunk` rows of its group if it is the first of them.
         const int r = blockIdx.y;
         if (threadIdx.x == 0) found[0] = -1;
         __syncthreads();
@@ -138,7 +138,9 @@ __global__ void __launch_bounds__(kThreads, 2) fp8_rows_kernel(Fp8RowsJob j, boo
                 });
             return;
         }
-        if (r != r0) return;
+        if ((r - r0) % chunk != 0) return;
+        count = min(count - (r - r0), chunk);
+        r0 = r;
     }
     const int gq = lane >> 2, t = lane & 3;
     const uint8_t* wg = j.w + g * j.stride_w;
@@ -288,24 +290,48 @@ size_t rows_smem(int rows, int K, int slots) {
     return static_cast<size_t>(kWarps) * slots * kSlotBytes + (rows + 1) * (nkb * kFp8Block + 8) * 2 + rows * nkb * 4;
 }
 
+// Rows of one group that a block of threads takes: as many as let two blocks
+// share an SM with two slots each (most groups of few rows have one or two).
+int rows_of_chunk(int rows, int K) {
+    int chunk = std::min(rows, kFp8FewRows);
+    while (chunk > 1 && rows_smem(chunk, K, 2) > kSmemOfTwo) --chunk;
+    return chunk;
+}
+
 }  // namespace
 
-bool fp8_rows_fit(int rows, int K) { return rows <= kFp8FewRows && rows_smem(rows, K, 2) <= kMaxSmem; }
+bool fp8_rows_fit(int rows, int N, int K, int groups, bool grouped, int num_sms) {
+    if (!grouped) return rows <= kFp8FewRows && rows_smem(rows, K, 2) <= kMaxSmem;
+    if (rows > kFp8FewRouted || rows_smem(1, K, 1) > kSmemOfTwo) return false;
+    // This kernel starts at once but streams the weights of one group per row at
+    // 2 to 5 TB/s (least where the warps are more than the k blocks, most where a
+    // block walks over several strips); the tensor cores' kernel takes the cast
+    // before it and a tile's k blocks one after another, and then streams
+    // faster. Measured, us, this and that: 256 experts of 512 x 2048, 8 rows 5.6
+    // and 13.0, 16 rows 9.8 and 13.1, 32 rows 14.8 and 13.4; of 2048 x 512, 8 rows
+    // 8.7 and 9.3, 16 rows 11.5 and 9.7; 16 of 4096 x 4096, 1 row 8.0 and 17.6, 4
+    // rows 21.8 and 17.9; 8 of 14336 x 4096, 2 rows 29.6 and 27.5, 8 rows 75 and 69.
+    const int strips = (N + kStrip - 1) / kStrip, nkb = (K + kFp8Block - 1) / kFp8Block;
+    const int parts = std::min(rows, groups + (rows - 1) / rows_of_chunk(rows, K));
+    const double megabytes = 1e-6 * parts * N * K;
+    return 3 + megabytes * (nkb < kWarps ? 0.5 : strips < 2 * num_sms ? 0.35 : 0.2) <= 8 + 0.3 * nkb;
+}
 
 int launch_fp8_rows(const Fp8RowsJob& j, int num_sms, cudaStream_t s) {
     const int strips = (j.N + kStrip - 1) / kStrip, nkb = (j.K + kFp8Block - 1) / kFp8Block;
+    const int chunk = j.offsets ? rows_of_chunk(j.rows, j.K) : j.rows;
     // Two blocks per SM where two fit, whose products hide each other's waits
     // (one row of 14336 x 4096: 15.8 us, one block per SM 19.9), with two slots if
-    // there is room and the walk is that long, else one.
-    const bool two = rows_smem(j.rows, j.K, 1) <= kSmemOfTwo;
+    // there is room and the walk is that long, else one. With groups, whose
+    // number that have rows is on the device, enough blocks for two rounds if
+    // all rows are of different groups.
+    const bool two = rows_smem(chunk, j.K, 1) <= kSmemOfTwo;
+    const int blocks = j.offsets ? std::min(strips, std::max(1, 4 * num_sms / j.rows)) : std::min(strips, (two ? 2 : 1) * num_sms);
     int slots = 1;
-    if ((nkb + kWarps - 1) / kWarps * ((strips + 2 * num_sms - 1) / (2 * num_sms)) > 1 &&
-        rows_smem(j.rows, j.K, 2) <= (two ? kSmemOfTwo : kMaxSmem))
+    if ((nkb + kWarps - 1) / kWarps * ((strips + blocks - 1) / blocks) > 1 &&
+        rows_smem(chunk, j.K, 2) <= (two ? kSmemOfTwo : kMaxSmem))
         slots = 2;
-    // With several groups a block per strip of each row that may start a group
-    // (most of them end at once).
-    const int blocks = j.offsets ? strips : std::min(strips, (two ? 2 : 1) * num_sms);
-    const size_t smem = rows_smem(j.rows, j.K, slots);
+    const size_t smem = rows_smem(chunk, j.K, slots);
     return by_dtype(j.dtype, [&](auto t) {
         using T = decltype(t);
         const bool vec = (reinterpret_cast<uintptr_t>(j.x) & 15) == 0 && j.ldx * static_cast<int>(sizeof(T)) % 16 == 0;
@@ -320,7 +346,7 @@ int launch_fp8_rows(const Fp8RowsJob& j, int num_sms, cudaStream_t s) {
         }
         if (e != cudaSuccess) return static_cast<int>(e);
         return static_cast<int>(launch_after(fp8_rows_kernel<T>, dim3(blocks, j.offsets ? j.rows : 1), dim3(kThreads), smem,
-                                             s, j, vec, slots));
+                                             s, j, vec, slots, chunk));
     });
 }
 

@@ -273,6 +273,25 @@ def test_linear_casts_on_the_way(gns, dtype, tokens, topk, experts, n, k, drop):
             assert_close(got[at], a[at] @ b[g].T, np.abs(a[at]) @ np.abs(b[g]).T, adds(k), f"expert {g}")
 
 
+@pytest.mark.parametrize("tokens,topk,experts,n,k,drop", [
+    (4, 2, 64, 3003, 520, 0), (16, 2, 40, 200, 140, 0.3), (31, 1, 16, 129, 264, 0), (32, 1, 200, 64, 2051, 0.1),
+    (8, 1, 1, 300, 4096, 0), (8, 4, 16, 40, 7000, 0), (2, 4, 4, 2600, 1030, 0), (9, 1, 9, 64, 14336, 0)])
+def test_linear_of_few_routed_rows(gns, tokens, topk, experts, n, k, drop):
+    """Experts with more rows than a block of threads takes, experts without any, and blocks
+    that walk over several strips of weight rows."""
+    rng = np.random.default_rng(n + k)
+    x = loud(tokens, k, 0, torch.bfloat16, rng)
+    route, (offsets, rows, slots) = route_of(gns, tokens, topk, experts, drop, n, skew=False)
+    wq = gns.gns_fp8_quantize_weight(loud(experts * n, k, 0, torch.bfloat16, rng).view(experts, n, k))
+    got = gns.gns_fp8_linear(x, wq, route=route, out_dtype=torch.float32)
+    a, b = values_rows(gns.gns_fp8_quantize(x, cols=False)[0])[slots // topk], values_weight(wq)
+    assert torch.all(got[offsets[-1]:] == 0)
+    for g in range(experts):
+        at = slice(offsets[g], offsets[g + 1])
+        if at.start < at.stop:
+            assert_close(got[at], a[at] @ b[g].T, np.abs(a[at]) @ np.abs(b[g]).T, adds(k), f"expert {g}")
+
+
 @pytest.mark.parametrize("tokens,n,k", [(1, 10001, 1100), (2, 9800, 2048), (8, 5008, 4096), (8, 5001, 3970), (3, 2500, 14336),
                                         (8, 300, 14336), (31, 2049, 2048)])
 def test_linear_of_few_rows_and_many_columns(gns, tokens, n, k):
