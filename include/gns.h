@@ -260,9 +260,11 @@ int gns_symm_gemm(const void* A, const void* B, const void* C, void* D, int G, i
  *
  * Matrices are row-major with a row stride (ld..., in elements) of at least
  * their columns. Sums are fp32 and each result is rounded once to its type.
- * Calls are asynchronous and write only what they name; those that need a
- * workspace (gns_moe_sort beyond 4096 slots, gns_fp8_linear, products of few
- * rows) use the library's, under the rule stated at the top of this file.
+ * Calls are asynchronous and write only what they name. gns_fp8_linear and
+ * products of few rows use the library's workspace, under the rule stated at
+ * the top of this file. gns_moe_sort beyond 4096 slots takes its intermediate
+ * memory in the order of its stream (a memory pool of the library, or the
+ * graph's own memory in a stream capture), so it may overlap other calls.
  */
 typedef enum { GNS_BF16 = 0, GNS_FP16 = 1, GNS_FP32 = 2 } gns_dtype;
 
@@ -460,10 +462,12 @@ void gns_profile_enable(int on);
  * number of classes (8), or a negative gns_status. */
 int gns_profile_read(int64_t* counts, double* ms, int max_classes);
 
-/* Workspace bytes currently held on the current device. */
+/* Workspace bytes currently held on the current device, and those its pool of
+ * stream-ordered memory has reserved. */
 int64_t gns_workspace_bytes(void);
 
-/* Frees the cached workspace of the current device (synchronizes it first). */
+/* Frees the cached workspace of the current device and what its pool holds
+ * unused (synchronizes it first). */
 void gns_release(void);
 
 #ifdef __cplusplus

@@ -115,6 +115,44 @@ int ensure_workspace(DeviceState& st, size_t bytes) {
     return GNS_OK;
 }
 
+int Scratch::take(DeviceState& st, size_t bytes, cudaStream_t s) {
+    cudaMemPool_t pool;
+    {
+        std::lock_guard<std::mutex> lk(g_mu);
+        if (!st.scratch) {
+            cudaMemPoolProps props = {};
+            props.allocType = cudaMemAllocationTypePinned;
+            props.location.type = cudaMemLocationTypeDevice;
+            props.location.id = st.device;
+            cudaMemPool_t made = nullptr;
+            CK(cudaMemPoolCreate(&made, &props));
+            // Freed memory stays with the pool until gns_release().
+            uint64_t keep = ~uint64_t(0);
+            const cudaError_t e = cudaMemPoolSetAttribute(made, cudaMemPoolAttrReleaseThreshold, &keep);
+            if (e != cudaSuccess) {
+                cudaMemPoolDestroy(made);
+                return cuda_fail(e, "cudaMemPoolSetAttribute");
+            }
+            st.scratch = made;
+        }
+        pool = st.scratch;
+    }
+    void* p = nullptr;
+    const cudaError_t e = cudaMallocFromPoolAsync(&p, bytes, pool, s);
+    if (e == cudaErrorMemoryAllocation) {
+        cudaGetLastError();
+        return fail(GNS_ERR_NOMEM, "scratch allocation of " + std::to_string(bytes) + " bytes failed");
+    }
+    if (e != cudaSuccess) return cuda_fail(e, "cudaMallocFromPoolAsync");
+    p_ = static_cast<char*>(p);
+    s_ = s;
+    return GNS_OK;
+}
+
+Scratch::~Scratch() {
+    if (p_) cudaFreeAsync(p_, s_);
+}
+
 namespace {
 
 // ---------------------------------------------------------------------------
@@ -1548,7 +1586,14 @@ int64_t gns_workspace_bytes(void) {
     }
     std::lock_guard<std::mutex> lk(g_mu);
     auto it = g_dev.find(dev);
-    return it == g_dev.end() ? 0 : static_cast<int64_t>(it->second.ws_bytes);
+    if (it == g_dev.end()) return 0;
+    uint64_t scratch = 0;
+    if (it->second.scratch &&
+        cudaMemPoolGetAttribute(it->second.scratch, cudaMemPoolAttrReservedMemCurrent, &scratch) != cudaSuccess) {
+        cudaGetLastError();
+        scratch = 0;
+    }
+    return static_cast<int64_t>(it->second.ws_bytes + scratch);
 }
 
 void gns_release(void) {
@@ -1562,6 +1607,7 @@ void gns_release(void) {
     if (it == g_dev.end()) return;
     cudaDeviceSynchronize();
     if (it->second.ws) cudaFree(it->second.ws);
+    if (it->second.scratch) cudaMemPoolTrimTo(it->second.scratch, 0);
     if (it->second.stage) cudaFree(it->second.stage);
     it->second.ws = nullptr;
     it->second.ws_bytes = 0;

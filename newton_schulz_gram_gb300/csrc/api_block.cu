@@ -193,11 +193,12 @@ int gns_moe_sort(const void* experts, int id_bytes, int tokens, int topk, int nu
     DeviceState* st = nullptr;
     RET(get_state(&st));
     SortJob j{experts, id_bytes, static_cast<long long>(tokens) * topk, num_experts, offsets, rows, slots, nullptr};
-    if (const size_t bytes = moe_sort_workspace(j.n, num_experts)) {
-        RET(ensure_workspace(*st, bytes));
-        j.hist = reinterpret_cast<int*>(st->ws);
-    }
     cudaStream_t s = static_cast<cudaStream_t>(stream);
+    Scratch scratch;
+    if (const size_t bytes = moe_sort_scratch(j.n, num_experts)) {
+        RET(scratch.take(*st, bytes, s));
+        j.hist = reinterpret_cast<int*>(scratch.data());
+    }
     LAUNCH(kClsMoe, launch_moe_sort(j, s));
     return GNS_OK;
 }

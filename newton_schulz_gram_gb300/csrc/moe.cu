@@ -452,7 +452,7 @@ dim3 walk_grid(const Walk& w) {
 
 }  // namespace
 
-size_t moe_sort_workspace(long long n, int G) {
+size_t moe_sort_scratch(long long n, int G) {
     const long long b = sort_blocks(n);
     return b > 1 ? sizeof(int) * static_cast<size_t>(b) * (G + 1) : 0;
 }

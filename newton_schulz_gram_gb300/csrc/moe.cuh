@@ -23,10 +23,10 @@ struct SortJob {
     int* offsets;
     int* rows;
     int* slots;
-    int* hist;  // moe_sort_workspace() bytes, or null where that is 0
+    int* hist;  // moe_sort_scratch() bytes, or null where that is 0
 };
 
-size_t moe_sort_workspace(long long n, int G);
+size_t moe_sort_scratch(long long n, int G);
 int launch_moe_sort(const SortJob& job, cudaStream_t s);
 
 struct RouteJob {

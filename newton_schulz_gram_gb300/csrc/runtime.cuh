@@ -42,6 +42,7 @@ struct DeviceState {
     float* stage = nullptr;  // device staging for the host-buffer entry point
     size_t stage_bytes = 0;
     cudaStream_t h2d = nullptr, d2h = nullptr;  // copy streams of the host-buffer entry point
+    cudaMemPool_t scratch = nullptr;            // pool of Scratch
 };
 
 // State of the current device, created on first use.
@@ -51,6 +52,25 @@ int get_state(DeviceState** out);
 void begin_call(DeviceState& st);
 
 int ensure_workspace(DeviceState& st, size_t bytes);
+
+// Intermediate memory of one call, taken and given back in the order of the
+// call's stream: calls on other streams have their own, and a stream capture
+// makes it part of the graph, so no later call can free or overwrite it. (The
+// workspace above is one buffer per device that a larger call replaces.) From
+// the pool a call's two steps take the host 0.6 us.
+class Scratch {
+public:
+    Scratch() = default;
+    Scratch(const Scratch&) = delete;
+    Scratch& operator=(const Scratch&) = delete;
+    ~Scratch();
+    int take(DeviceState& st, size_t bytes, cudaStream_t s);
+    char* data() const { return p_; }
+
+private:
+    char* p_ = nullptr;
+    cudaStream_t s_ = nullptr;
+};
 
 // Kernel classes of gns_profile_read().
 enum KernelClass {

@@ -1,0 +1,75 @@
+"""Intermediate memory of the training-block operators: calls that overlap on
+several streams do not meet in it, and a captured graph keeps its own whatever
+the library does between the capture and a replay."""
+import numpy as np
+import pytest
+
+from oracle import block as B
+
+torch = pytest.importorskip("torch")
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def gns():
+    import newton_schulz_gram_gb300 as m
+    from newton_schulz_gram_gb300 import build
+    build.build()
+    m.load()
+    yield m
+    assert m.gns_get_status() == 0
+
+
+def ids_of(tokens, topk, experts, seed):
+    ids = np.random.default_rng(seed).integers(-1, experts, (tokens, topk))
+    return torch.from_numpy(ids).cuda(), B.moe_sort(ids, experts)
+
+
+def same_route(route, want):
+    return all(np.array_equal(a.cpu().numpy().reshape(-1), b.reshape(-1)) for a, b in zip(route, want))
+
+
+def use_memory(gns):
+    """Makes the library replace its workspace and overwrite what it held, and
+    other allocations take what that freed."""
+    gns.gns_release()
+    g = torch.randn(2, 512, 1024, device="cuda")
+    gns.gns_orthogonalize_batched(g)
+    big = torch.randn(4, 2048, 4096, device="cuda")
+    gns.gns_orthogonalize_batched(big)
+    filler = [torch.full((1 << 22,), -1, dtype=torch.int32, device="cuda") for _ in range(8)]
+    torch.cuda.synchronize()
+    return filler
+
+
+def test_sorts_on_several_streams(gns):
+    """Sorts whose counts lie in intermediate memory, each stream with its own
+    ids, queued behind one another so that they run side by side."""
+    streams = [torch.cuda.Stream() for _ in range(4)]
+    jobs = [ids_of(20000 + 977 * i, 3, 5 + 200 * i, i) for i in range(4)]
+    torch.cuda.synchronize()
+    for _ in range(5):
+        for s in streams:
+            with torch.cuda.stream(s):
+                torch.cuda._sleep(200000)
+        routes = [gns.gns_moe_sort(ids, 5 + 200 * i, stream=s) for i, ((ids, _), s) in enumerate(zip(jobs, streams))]
+        torch.cuda.synchronize()
+        for route, (_, want) in zip(routes, jobs):
+            assert same_route(route, want)
+
+
+def test_a_captured_sort_outlives_later_calls(gns):
+    ids, want = ids_of(30000, 2, 64, 9)
+    other, want_other = ids_of(30000, 2, 64, 10)
+    gns.gns_moe_sort(ids, 64)
+    torch.cuda.synchronize()
+    graph, static = torch.cuda.CUDAGraph(), ids.clone()
+    with torch.cuda.graph(graph):
+        route = gns.gns_moe_sort(static, 64)
+    for now, expected in ((ids, want), (other, want_other)):
+        filler = use_memory(gns)
+        static.copy_(now)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert same_route(route, expected)
+        assert all((f == -1).all() for f in filler)
