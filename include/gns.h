@@ -10,7 +10,9 @@
  * cached workspace per device (Gram state, fp16 copies of the inputs, norm
  * partials, a status word). It grows on demand and is freed by
  * gns_release(). Calls on different streams of one device must not overlap
- * in time, because they share that workspace.
+ * in time, because they share that workspace, and a captured call is valid
+ * only until a larger one replaces it. (The operators of a training block
+ * have neither rule; see there.)
  *
  * Errors: argument and shape errors, and failures of CUDA runtime calls, are
  * returned at once as a negative gns_status. Conditions found on the device
@@ -260,11 +262,12 @@ int gns_symm_gemm(const void* A, const void* B, const void* C, void* D, int G, i
  *
  * Matrices are row-major with a row stride (ld..., in elements) of at least
  * their columns. Sums are fp32 and each result is rounded once to its type.
- * Calls are asynchronous and write only what they name. gns_fp8_linear and
- * products of few rows use the library's workspace, under the rule stated at
- * the top of this file. gns_moe_sort beyond 4096 slots takes its intermediate
- * memory in the order of its stream (a memory pool of the library, or the
- * graph's own memory in a stream capture), so it may overlap other calls.
+ * Calls are asynchronous and write only what they name. Those that need
+ * intermediate memory (gns_moe_sort beyond 4096 slots, gns_fp8_linear, products
+ * of few rows) take it in the order of their stream, from a memory pool of the
+ * library or, in a stream capture, as the graph's own: none of these operators
+ * uses the workspace of the entry points above, so they may overlap each other
+ * and anything else on other streams, and a captured one stays valid.
  */
 typedef enum { GNS_BF16 = 0, GNS_FP16 = 1, GNS_FP32 = 2 } gns_dtype;
 

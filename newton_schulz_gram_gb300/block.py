@@ -3,8 +3,9 @@ routing of tokens to experts, and linear layers on block-scaled 8-bit operands.
 
 Each function marshals tensors and calls the C entry point of the same name
 (include/gns.h states what it computes); outputs are new tensors on the
-stream of the call. Gradients are functions of their own, as for the
-optimizer steps: nothing here records an autograd graph.
+stream of the call. Calls may overlap on several streams and may be captured in
+a graph. Gradients are functions of their own, as for the optimizer steps:
+nothing here records an autograd graph.
 """
 from __future__ import annotations
 

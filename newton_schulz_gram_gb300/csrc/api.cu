@@ -92,10 +92,13 @@ static unsigned long long wait_limit_ns() {
     return kDefaultWaitLimitNs;
 }
 
-void begin_call(DeviceState& st) {
+DevStatus new_call(DeviceState& st) {
+    std::lock_guard<std::mutex> lk(g_mu);
     st.epoch = st.epoch == 0x7fffffff ? 1 : st.epoch + 1;
-    st.status = DevStatus{st.err, st.epoch, 0, wait_limit_ns()};
+    return DevStatus{st.err, st.epoch, 0, wait_limit_ns()};
 }
+
+void begin_call(DeviceState& st) { st.status = new_call(st); }
 
 int ensure_workspace(DeviceState& st, size_t bytes) {
     if (st.ws_bytes >= bytes) return GNS_OK;

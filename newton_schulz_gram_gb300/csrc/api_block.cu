@@ -1,6 +1,6 @@
 // C ABI of the training-block operators: counter-based dropout, expert
 // routing, block-scaled 8-bit casts and products. Argument checks, tensor maps
-// and workspaces; the kernels are in dropout.cu, moe.cu and fp8_*.cu.
+// and intermediate memory; the kernels are in dropout.cu, moe.cu and fp8_*.cu.
 #include <algorithm>
 #include <cmath>
 #include <string>
@@ -94,7 +94,7 @@ int check_moves(int tokens, int topk, int num_experts, int cols, int dtype, cons
 // The forward and the data-gradient product: A [rows][inner_a], D [rows][n_out].
 int product(const void* a, int64_t lda, const uint8_t* sa, int64_t ld_sa, int fmt_a, int rows, const void* w, int64_t ldw,
             const uint8_t* sw, int fmt_w, int groups, int N, int K, bool dgrad, const int32_t* offsets, void* D,
-            int64_t ldd, int out_dtype, DeviceState* st, size_t ws_used, cudaStream_t s) {
+            int64_t ldd, int out_dtype, DeviceState* st, cudaStream_t s) {
     const int inner = dgrad ? N : K, out = dgrad ? K : N;
     RET(check_q(a, inner, lda));
     RET(check_q(w, K, ldw));
@@ -124,13 +124,13 @@ int product(const void* a, int64_t lda, const uint8_t* sa, int64_t ld_sa, int fm
     j.D = D;
     j.ldd = ldd;
     j.out_dtype = out_dtype;
+    Scratch partial;
     if (j.split > 1) {
-        RET(ensure_workspace(*st, ws_used + sizeof(float) * static_cast<size_t>(j.split) * rows * out));
-        j.partial = reinterpret_cast<float*>(st->ws + ws_used);
+        RET(partial.take(*st, sizeof(float) * static_cast<size_t>(j.split) * rows * out, s));
+        j.partial = reinterpret_cast<float*>(partial.data());
     }
     RET(map_output(j, cg));
-    begin_call(*st);
-    j.st = st->status;
+    j.st = new_call(*st);
     LAUNCH(kClsFp8Gemm, launch_fp8_gemm(j, cg, st->num_sms, s));
     return GNS_OK;
 }
@@ -321,7 +321,7 @@ int gns_fp8_matmul(const void* a, int64_t lda, const uint8_t* scale_a, int64_t l
     DeviceState* st = nullptr;
     RET(get_state(&st));
     return product(a, lda, scale_a, ld_scale_a, format_a, rows, w, ldw, scale_w, format_w, groups, N, K, false, offsets,
-                   y, ldy, out_dtype, st, 0, static_cast<cudaStream_t>(stream));
+                   y, ldy, out_dtype, st, static_cast<cudaStream_t>(stream));
 }
 
 int gns_fp8_matmul_dgrad(const void* dy, int64_t lddy, const uint8_t* scale_dy, int64_t ld_scale_dy, int format_dy,
@@ -332,7 +332,7 @@ int gns_fp8_matmul_dgrad(const void* dy, int64_t lddy, const uint8_t* scale_dy, 
     DeviceState* st = nullptr;
     RET(get_state(&st));
     return product(dy, lddy, scale_dy, ld_scale_dy, format_dy, rows, w, ldw, scale_w, format_w, groups, N, K, true,
-                   offsets, dx, lddx, out_dtype, st, 0, static_cast<cudaStream_t>(stream));
+                   offsets, dx, lddx, out_dtype, st, static_cast<cudaStream_t>(stream));
 }
 
 int gns_fp8_matmul_wgrad(const void* dy, int64_t lddy, const uint8_t* scale_dy, int64_t ld_scale_dy, int format_dy,
@@ -381,8 +381,7 @@ int gns_fp8_matmul_wgrad(const void* dy, int64_t lddy, const uint8_t* scale_dy, 
     j.out_dtype = out_dtype;
     j.split = 1;
     RET(map_output(j, cg));
-    begin_call(*st);
-    j.st = st->status;
+    j.st = new_call(*st);
     LAUNCH(kClsFp8Gemm, launch_fp8_gemm(j, cg, st->num_sms, s));
     return GNS_OK;
 }
@@ -412,14 +411,13 @@ int gns_fp8_linear(const void* x, int64_t ldx, int dtype, int rows, const int32_
     const int64_t ldq = std::max(up(K, 16), up((256 << 10) / rows, 128));
     const size_t q_bytes = static_cast<size_t>(up(ldq * rows, 256));
     const size_t s_bytes = static_cast<size_t>(up(up(K, kFp8Block) / kFp8Block * rows, 256));
-    const int split = offsets ? 1 : fp8_gemm_split(rows, N, K, st->num_sms);
-    const size_t partial = split > 1 ? sizeof(float) * static_cast<size_t>(split) * rows * N : 0;
-    RET(ensure_workspace(*st, q_bytes + s_bytes + partial));
-    uint8_t* scale = reinterpret_cast<uint8_t*>(st->ws + q_bytes);
-    RET(gns_fp8_quantize(x, ldx, dtype, rows, K, slots, topk, nullptr, 1, GNS_E4M3, st->ws, ldq, scale, rows, nullptr, 0,
-                         nullptr, 0, stream));
-    return product(st->ws, ldq, scale, rows, GNS_E4M3, rows, w, ldw, scale_w, format_w, groups, N, K, false, offsets, y,
-                   ldy, out_dtype, st, q_bytes + s_bytes, s);
+    Scratch cast;
+    RET(cast.take(*st, q_bytes + s_bytes, s));
+    uint8_t* scale = reinterpret_cast<uint8_t*>(cast.data() + q_bytes);
+    RET(gns_fp8_quantize(x, ldx, dtype, rows, K, slots, topk, nullptr, 1, GNS_E4M3, cast.data(), ldq, scale, rows, nullptr,
+                         0, nullptr, 0, stream));
+    return product(cast.data(), ldq, scale, rows, GNS_E4M3, rows, w, ldw, scale_w, format_w, groups, N, K, false, offsets,
+                   y, ldy, out_dtype, st, s);
 }
 
 }  // extern "C"

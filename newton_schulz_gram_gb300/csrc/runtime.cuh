@@ -48,8 +48,10 @@ struct DeviceState {
 // State of the current device, created on first use.
 int get_state(DeviceState** out);
 
-// Starts a call on a device: a new epoch for its kernels' abort mark.
+// Starts a call on a device: a new epoch for its kernels' abort mark. The
+// second form hands it to the caller, for calls that may run beside others.
 void begin_call(DeviceState& st);
+DevStatus new_call(DeviceState& st);
 
 int ensure_workspace(DeviceState& st, size_t bytes);
 

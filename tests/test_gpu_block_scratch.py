@@ -73,3 +73,55 @@ def test_a_captured_sort_outlives_later_calls(gns):
         torch.cuda.synchronize()
         assert same_route(route, expected)
         assert all((f == -1).all() for f in filler)
+
+
+def layers(gns, seed):
+    """Products with intermediate memory, as functions of (x, stream): the fused
+    layer of many rows, the split product and both split gradients."""
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    n, k = 700 + 128 * seed, 4096
+    w = gns.gns_fp8_quantize_weight(torch.randn(n, k, generator=g, device="cuda"))
+    wt = gns.gns_fp8_quantize_weight(torch.randn(k, n, generator=g, device="cuda"))
+    rows = lambda x, s: gns.gns_fp8_quantize(x, cols=False, stream=s)[0]  # noqa: E731
+    x = torch.randn(40 + 8 * seed, k, generator=g, device="cuda").bfloat16()
+    return x, (lambda x, s: gns.gns_fp8_linear(x, w, out_dtype=torch.float32, stream=s),
+               lambda x, s: gns.gns_fp8_matmul(rows(x, s), w, stream=s),
+               lambda x, s: gns.gns_fp8_matmul_dgrad(rows(x, s), wt, out_dtype=torch.float32, stream=s))
+
+
+def test_products_on_several_streams(gns):
+    streams = [torch.cuda.Stream() for _ in range(4)]
+    jobs = [layers(gns, i) for i in range(4)]
+    ids, want_route = ids_of(20000, 3, 70, 4)
+    want = [[f(x, None) for f in fs] for x, fs in jobs]
+    torch.cuda.synchronize()
+    for _ in range(5):
+        for s in streams:
+            with torch.cuda.stream(s):
+                torch.cuda._sleep(400000)
+        got = [[] for _ in jobs]
+        for k in range(3):
+            for out, (x, fs), s in zip(got, jobs, streams):
+                out.append(fs[k](x, s))
+        route = gns.gns_moe_sort(ids, 70, stream=streams[0])
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for out, exact in zip(got, want) for a, b in zip(out, exact))
+        assert same_route(route, want_route)
+
+
+def test_captured_products_outlive_later_calls(gns):
+    x, fs = layers(gns, 2)
+    other = torch.randn_like(x)
+    want = {id(t): [f(t, None) for f in fs] for t in (x, other)}
+    torch.cuda.synchronize()
+    graph, static = torch.cuda.CUDAGraph(), x.clone()
+    with torch.cuda.graph(graph):
+        outs = [f(static, None) for f in fs]
+    for t in (other, x):
+        filler = use_memory(gns)
+        fs[0](torch.randn(4000, 4096, device="cuda"), None)
+        static.copy_(t)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(outs, want[id(t)]))
+        assert all((f == -1).all() for f in filler)
