@@ -60,6 +60,35 @@ long long round_up_ll(long long v, long long a) { return (v + a - 1) / a * a; }
 std::mutex g_mu;
 std::map<int, DeviceState> g_dev;
 
+// While one lives, this thread may allocate although a stream is capturing:
+// what a first call sets up is no part of the graph and touches no stream of
+// the caller's.
+struct OutsideCapture {
+    cudaStreamCaptureMode mode = cudaStreamCaptureModeRelaxed;
+    OutsideCapture() { cudaThreadExchangeStreamCaptureMode(&mode); }
+    ~OutsideCapture() { cudaThreadExchangeStreamCaptureMode(&mode); }
+};
+
+// The zeroed status block, cleared on a stream of its own.
+int make_status_block(int** out) {
+    OutsideCapture relaxed;
+    int* p = nullptr;
+    CK(cudaMalloc(&p, 256));
+    cudaStream_t s = nullptr;
+    cudaError_t e = cudaStreamCreateWithFlags(&s, cudaStreamNonBlocking);
+    if (e == cudaSuccess) {
+        e = cudaMemsetAsync(p, 0, 256, s);
+        if (e == cudaSuccess) e = cudaStreamSynchronize(s);
+        cudaStreamDestroy(s);
+    }
+    if (e != cudaSuccess) {
+        cudaFree(p);
+        return cuda_fail(e, "status block");
+    }
+    *out = p;
+    return GNS_OK;
+}
+
 }  // namespace
 
 int get_state(DeviceState** out) {
@@ -75,10 +104,7 @@ int get_state(DeviceState** out) {
     }
     if (!(st.cc_major == 10 && st.cc_minor == 3))
         return fail(GNS_ERR_UNSUPPORTED, "this library is built for sm_103a (GB300) only");
-    if (!st.err) {
-        CK(cudaMalloc(&st.err, 256));
-        CK(cudaMemset(st.err, 0, 256));
-    }
+    if (!st.err) RET(make_status_block(&st.err));
     const char* cap = std::getenv("GNS_NUM_SMS");
     if (cap && std::atoi(cap) > 0) st.num_sms = std::min(st.num_sms, std::atoi(cap));
     *out = &st;
@@ -123,6 +149,7 @@ int Scratch::take(DeviceState& st, size_t bytes, cudaStream_t s) {
     {
         std::lock_guard<std::mutex> lk(g_mu);
         if (!st.scratch) {
+            OutsideCapture relaxed;
             cudaMemPoolProps props = {};
             props.allocType = cudaMemAllocationTypePinned;
             props.location.type = cudaMemLocationTypeDevice;

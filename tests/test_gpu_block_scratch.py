@@ -1,6 +1,10 @@
 """Intermediate memory of the training-block operators: calls that overlap on
 several streams do not meet in it, and a captured graph keeps its own whatever
 the library does between the capture and a replay."""
+import os
+import subprocess
+import sys
+
 import numpy as np
 import pytest
 
@@ -125,3 +129,40 @@ def test_captured_products_outlive_later_calls(gns):
         torch.cuda.synchronize()
         assert all(torch.equal(a, b) for a, b in zip(outs, want[id(t)]))
         assert all((f == -1).all() for f in filler)
+
+
+FIRST_CALLS = """
+import sys
+import torch
+sys.path.insert(0, {root!r})
+import newton_schulz_gram_gb300 as gns
+gns.load()
+x = torch.randn(300, 4096, device="cuda")
+ids = torch.randint(0, 6, (5000, 2), device="cuda")
+w = torch.randn(200, 4096, device="cuda")
+
+def calls():
+    d = gns.gns_dropout(x, 0.3, 1, 2)
+    route = gns.gns_moe_sort(ids, 6)
+    w8 = gns.gns_fp8_quantize_weight(w)
+    return [d, *route, *(gns.gns_fp8_linear(x[:n], w8, out_dtype=torch.float32) for n in (3, 40, 300))]
+
+torch.cuda.synchronize()
+graph = torch.cuda.CUDAGraph()
+with torch.cuda.graph(graph):
+    captured = calls()
+graph.replay()
+torch.cuda.synchronize()
+for a, b in zip(captured, calls()):
+    assert torch.equal(a, b)
+assert gns.gns_get_status() == 0
+print("same")
+"""
+
+
+def test_the_first_calls_of_a_process_can_be_captured(gns):
+    """What the library sets up on first use (status block, memory pool, kernel
+    attributes) does not break a capture."""
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", FIRST_CALLS.format(root=root)], capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0 and r.stdout.strip() == "same", r.stdout + r.stderr
