@@ -5,6 +5,8 @@ import ctypes
 import os
 import platform
 
+import torch
+
 HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(HERE, "_build", platform.machine(), "libgns.so")
 
@@ -97,3 +99,19 @@ def check(status, where):
         detail = lib.gns_last_error().decode(errors="replace")
         raise GnsError(status, where, detail)
     return status
+
+
+_current_device = torch._C._cuda_getDevice
+
+
+def call(entry, device, *args):
+    """A C entry on tensors of cuda:<device>. The library works on the current
+    device, so another one is made current for the call."""
+    fn = getattr(_LIB or load(), entry)
+    if _current_device() == device:
+        status = fn(*args)
+    else:
+        with torch.cuda.device(device):
+            status = fn(*args)
+    if status != 0:
+        check(status, entry)

@@ -11,7 +11,7 @@ from __future__ import annotations
 
 import torch
 
-from ._lib import check, load
+from ._lib import call
 
 DTYPES = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
 FORMATS = {"e4m3": 0, "e5m2": 1}
@@ -268,8 +268,8 @@ def gns_dropout(x, p, seed, step, residual=None, base_index=0, out=None, stream=
         rows, cols, ldx = _matrix(x, "x")
         ldy = _matrix(out, "out")[2]
         ldr = 0 if residual is None else _matrix(residual, "residual")[2]
-    check(load().gns_dropout(x.data_ptr(), _ptr(residual), out.data_ptr(), rows, cols, ldx, ldr, ldy, DTYPES[x.dtype],
-                             p, seed, step, base_index, _on(x, stream)), "gns_dropout")
+    call("gns_dropout", x.get_device(), x.data_ptr(), _ptr(residual), out.data_ptr(), rows, cols, ldx, ldr, ldy,
+         DTYPES[x.dtype], p, seed, step, base_index, _on(x, stream))
     return out
 
 
@@ -293,8 +293,8 @@ def gns_moe_sort(experts, num_experts, stream=None):
         raise ValueError("num_experts must be at least 1")
     n = tokens * topk
     route = MoeRoute._made(_new((2 * n + num_experts + 1,), torch.int32, experts, stream), tokens, topk, num_experts)
-    check(load().gns_moe_sort(experts.data_ptr(), experts.element_size(), tokens, topk, num_experts, route.p_offsets,
-                              route.p_rows, route.p_slots, _on(experts, stream)), "gns_moe_sort")
+    call("gns_moe_sort", route.device, experts.data_ptr(), experts.element_size(), tokens, topk, num_experts,
+         route.p_offsets, route.p_rows, route.p_slots, _on(experts, stream))
     return route
 
 
@@ -314,9 +314,8 @@ def gns_moe_gather(x, route, stream=None):
     if n != tokens:
         raise ValueError("x must have one row per token of the route")
     y = _new((tokens * topk, cols), x.dtype, x, stream)
-    check(load().gns_moe_gather(x.data_ptr(), ldx, tokens, topk, experts, cols, DTYPES[x.dtype],
-                                route.p_offsets, route.p_rows, y.data_ptr(), cols, _on(x, stream)),
-          "gns_moe_gather")
+    call("gns_moe_gather", route.device, x.data_ptr(), ldx, tokens, topk, experts, cols, DTYPES[x.dtype], route.p_offsets,
+         route.p_rows, y.data_ptr(), cols, _on(x, stream))
     return y
 
 
@@ -337,9 +336,8 @@ def gns_moe_combine(y, weights, route, stream=None):
     if weights is not None:
         _route_weights(weights, route, y)
     out = _new((tokens, cols), y.dtype, y, stream)
-    check(load().gns_moe_combine(y.data_ptr(), ldy, _ptr(weights), tokens, topk, experts, cols, DTYPES[y.dtype],
-                                 route.p_offsets, route.p_rows, out.data_ptr(), cols, _on(y, stream)),
-          "gns_moe_combine")
+    call("gns_moe_combine", route.device, y.data_ptr(), ldy, _ptr(weights), tokens, topk, experts, cols, DTYPES[y.dtype],
+         route.p_offsets, route.p_rows, out.data_ptr(), cols, _on(y, stream))
     return out
 
 
@@ -363,10 +361,9 @@ def gns_moe_combine_backward(dout, y, weights, route, stream=None):
         _same_device(dout, "y", y)
         dweights = _new((tokens, topk), torch.float32, dout, stream)
     dy = _new((tokens * topk, cols), dout.dtype, dout, stream)
-    check(load().gns_moe_combine_backward(dout.data_ptr(), lddo, _ptr(y), ldy, weights.data_ptr(), tokens, topk, experts,
-                                          cols, DTYPES[dout.dtype], route.p_offsets, route.p_rows,
-                                          dy.data_ptr(), cols, _ptr(dweights), _on(dout, stream)),
-          "gns_moe_combine_backward")
+    call("gns_moe_combine_backward", route.device, dout.data_ptr(), lddo, _ptr(y), ldy, weights.data_ptr(), tokens, topk,
+         experts, cols, DTYPES[dout.dtype], route.p_offsets, route.p_rows, dy.data_ptr(), cols, _ptr(dweights),
+         _on(dout, stream))
     return dy, dweights
 
 
@@ -420,8 +417,8 @@ def gns_fp8_quantize(x, fmt="e4m3", route=None, gather=False, rows=True, cols=Tr
                           _new((k_bytes,), torch.uint8, x, stream) if buf is None else buf, at)
         k.rows = n
         q_c, s_c = k.p_q, k.p_scale
-    check(load().gns_fp8_quantize(x.data_ptr(), ldx, DTYPES[x.dtype], n, c, slots, topk, offsets, groups, f, q_r, ld, s_r, n,
-                                  q_c, ld, s_c, c, _on(x, stream)), "gns_fp8_quantize")
+    call("gns_fp8_quantize", x.get_device(), x.data_ptr(), ldx, DTYPES[x.dtype], n, c, slots, topk, offsets, groups, f, q_r,
+         ld, s_r, n, q_c, ld, s_c, c, _on(x, stream))
     return r, k
 
 
@@ -444,8 +441,8 @@ def gns_fp8_quantize_weight(w, fmt="e4m3", stream=None):
     buf = _new((groups * (n * ld + nb * kb),), torch.uint8, w, stream)
     out = Fp8Weight._made((groups, n, ld), (groups, nb, kb), k, f, buf)
     out.grouped = grouped
-    check(load().gns_fp8_quantize_weight(w.data_ptr(), ldw, stride, DTYPES[w.dtype], groups, n, k, f, out.p_q, ld,
-                                         out.p_scale, _on(w, stream)), "gns_fp8_quantize_weight")
+    call("gns_fp8_quantize_weight", out.device, w.data_ptr(), ldw, stride, DTYPES[w.dtype], groups, n, k, f, out.p_q, ld,
+         out.p_scale, _on(w, stream))
     return out
 
 
@@ -494,9 +491,9 @@ def _row_product(entry, a, w, route, dgrad, out_dtype, stream):
     out = _out_type(out_dtype)
     _one_device(a, w, route)
     y = _output((rows, out_cols), out_dtype, a.device, stream)
-    check(getattr(load(), entry)(a.p_q, a.ld, a.p_scale, a.ld_scale, a.fmt, rows, w.p_q, w.ld, w.p_scale, w.fmt, groups, n, k,
-                                 None if route is None else route.p_offsets, y.data_ptr(), out_cols, out,
-                                 _raw_stream(a.device) if stream is None else stream.cuda_stream), entry)
+    call(entry, a.device, a.p_q, a.ld, a.p_scale, a.ld_scale, a.fmt, rows, w.p_q, w.ld, w.p_scale, w.fmt, groups, n, k,
+         None if route is None else route.p_offsets, y.data_ptr(), out_cols, out,
+         _raw_stream(a.device) if stream is None else stream.cuda_stream)
     return y
 
 
@@ -529,10 +526,9 @@ def gns_fp8_matmul_wgrad(dy, x, route=None, out_dtype=torch.bfloat16, stream=Non
         raise ValueError("operands cast with a route need it here too")
     _one_device(x, dy, route)
     dw = _output((n, k) if route is None else (groups, n, k), out_dtype, x.device, stream)
-    check(load().gns_fp8_matmul_wgrad(dy.p_q, dy.ld, dy.p_scale, dy.ld_scale, dy.fmt, x.p_q, x.ld, x.p_scale, x.ld_scale,
-                                      x.fmt, rows, groups, n, k, None if route is None else route.p_offsets, dw.data_ptr(),
-                                      k, n * k, out, _raw_stream(x.device) if stream is None else stream.cuda_stream),
-          "gns_fp8_matmul_wgrad")
+    call("gns_fp8_matmul_wgrad", x.device, dy.p_q, dy.ld, dy.p_scale, dy.ld_scale, dy.fmt, x.p_q, x.ld, x.p_scale,
+         x.ld_scale, x.fmt, rows, groups, n, k, None if route is None else route.p_offsets, dw.data_ptr(), k, n * k, out,
+         _raw_stream(x.device) if stream is None else stream.cuda_stream)
     return dw
 
 
@@ -554,6 +550,6 @@ def gns_fp8_linear(x, w, route=None, out_dtype=torch.bfloat16, stream=None):
     if w.device != x.get_device():
         raise ValueError(f"x is on {x.device}, the weights on cuda:{w.device}")
     y = _new((rows, n), out_dtype, x, stream)
-    check(load().gns_fp8_linear(x.data_ptr(), ldx, DTYPES[x.dtype], rows, slots, topk, offsets, w.p_q, w.ld, w.p_scale,
-                                w.fmt, groups, n, k, y.data_ptr(), n, out, _on(x, stream)), "gns_fp8_linear")
+    call("gns_fp8_linear", w.device, x.data_ptr(), ldx, DTYPES[x.dtype], rows, slots, topk, offsets, w.p_q, w.ld, w.p_scale,
+         w.fmt, groups, n, k, y.data_ptr(), n, out, _on(x, stream))
     return y
