@@ -11,7 +11,7 @@ import ctypes
 
 import torch
 
-from ._lib import GnsError, GnsTensor, check, load
+from ._lib import GnsError, GnsTensor, call, check, load
 from .block import (Fp8Cols, Fp8Rows, Fp8Weight, MoeRoute, gns_dropout, gns_dropout_backward, gns_fp8_linear,
                     gns_fp8_matmul, gns_fp8_matmul_dgrad, gns_fp8_matmul_wgrad, gns_fp8_quantize,
                     gns_fp8_quantize_weight, gns_moe_combine, gns_moe_combine_backward, gns_moe_gather,
@@ -59,14 +59,19 @@ def _require(t, dtype, cuda=True, name="tensor"):
         raise ValueError(f"{name} must be contiguous")
 
 
+def _same_device(first, *others):
+    for t in others:
+        if t is not None and t.get_device() != first.get_device():
+            raise ValueError(f"tensors on {first.device} and {t.device}")
+
+
 def gns_orthogonalize_batched(x, steps=5, restart_at=2, coeffs=None, stream=None):
     """Orthogonalize x in place: fp32 CUDA tensor [R, C] or [G, R, C]."""
     _require(x, torch.float32, name="x")
     G, R, C = (1, *x.shape) if x.dim() == 2 else tuple(x.shape)
     keep, cptr = _coeff_array(coeffs, steps)
-    lib = load()
-    check(lib.gns_orthogonalize_batched(ctypes.c_void_p(x.data_ptr()), G, R, C, steps, restart_at,
-                                        cptr, _stream(stream, x.device)), "gns_orthogonalize_batched")
+    call("gns_orthogonalize_batched", x.get_device(), ctypes.c_void_p(x.data_ptr()), G, R, C, steps, restart_at,
+         cptr, _stream(stream, x.device))
     del keep
     return x
 
@@ -80,9 +85,8 @@ def gns_orthogonalize_batched_schedule(x, steps=5, restarts=(2,), coeffs=None, s
     mask = 0
     for t in restarts:
         mask |= 1 << int(t)
-    lib = load()
-    check(lib.gns_orthogonalize_batched_schedule(ctypes.c_void_p(x.data_ptr()), G, R, C, steps, mask, cptr,
-                                                 _stream(stream, x.device)), "gns_orthogonalize_batched_schedule")
+    call("gns_orthogonalize_batched_schedule", x.get_device(), ctypes.c_void_p(x.data_ptr()), G, R, C, steps,
+         mask, cptr, _stream(stream, x.device))
     del keep
     return x
 
@@ -101,10 +105,9 @@ def gns_gram_ns_state(x, steps=5, restarts=(2,), stream=None):
     mask = 0
     for t in restarts:
         mask |= 1 << int(t)
-    lib = load()
-    check(lib.gns_gram_ns_state(ctypes.c_void_p(x.data_ptr()), G, R, C, steps, mask,
-                                ctypes.c_void_p(r_state.data_ptr()), ctypes.c_void_p(q_state.data_ptr()),
-                                ctypes.byref(scale), _stream(stream, x.device)), "gns_gram_ns_state")
+    call("gns_gram_ns_state", x.get_device(), ctypes.c_void_p(x.data_ptr()), G, R, C, steps, mask,
+         ctypes.c_void_p(r_state.data_ptr()), ctypes.c_void_p(q_state.data_ptr()), ctypes.byref(scale),
+         _stream(stream, x.device))
     return r_state, q_state, float(scale.value)
 
 
@@ -127,10 +130,8 @@ def gns_orthogonalize_batched_noalloc(x, steps=5, restart_at=2, coeffs=None, str
     _require(x, torch.float32, name="x")
     G, R, C = (1, *x.shape) if x.dim() == 2 else tuple(x.shape)
     keep, cptr = _coeff_array(coeffs, steps)
-    lib = load()
-    check(lib.gns_orthogonalize_batched_noalloc(ctypes.c_void_p(x.data_ptr()), G, R, C, steps, restart_at,
-                                                cptr, _stream(stream, x.device)),
-          "gns_orthogonalize_batched_noalloc")
+    call("gns_orthogonalize_batched_noalloc", x.get_device(), ctypes.c_void_p(x.data_ptr()), G, R, C, steps,
+         restart_at, cptr, _stream(stream, x.device))
     del keep
     return x
 
@@ -164,8 +165,9 @@ def muon_step(params, grads, momenta, lr, wd, mu, seed, step, base_indices=None,
     P = _tensors(params, torch.bfloat16, "params", base_indices)
     Gr = _tensors(grads, torch.bfloat16, "grads")
     M = _tensors(momenta, torch.float32, "momenta")
-    lib = load()
-    check(lib.muon_step(P, Gr, M, n, lr, wd, mu, seed, step, _stream(stream, params[0].device)), "muon_step")
+    _same_device(*params, *grads, *momenta)
+    call("muon_step", params[0].get_device(), P, Gr, M, n, lr, wd, mu, seed, step,
+         _stream(stream, params[0].device))
 
 
 def dion3_step(params, grads, momenta, fraction, lr, wd, mu, seed=0, step=0, base_indices=None, stream=None):
@@ -184,9 +186,9 @@ def dion3_step(params, grads, momenta, fraction, lr, wd, mu, seed=0, step=0, bas
     P = _tensors(params, torch.bfloat16, "params", base_indices)
     Gr = _tensors(grads, torch.bfloat16, "grads")
     M = _tensors(momenta, torch.float32, "momenta")
-    lib = load()
-    check(lib.dion3_step(P, Gr, M, n, fraction, lr, wd, mu, seed, step, _stream(stream, params[0].device)),
-          "dion3_step")
+    _same_device(*params, *grads, *momenta)
+    call("dion3_step", params[0].get_device(), P, Gr, M, n, fraction, lr, wd, mu, seed, step,
+         _stream(stream, params[0].device))
 
 
 def normuon_step(params, grads, momenta, second_moments, lr, wd, mu, beta2=0.95, eps=1e-8, seed=0, step=0,
@@ -207,9 +209,9 @@ def normuon_step(params, grads, momenta, second_moments, lr, wd, mu, beta2=0.95,
     Gr = _tensors(grads, torch.bfloat16, "grads")
     M = _tensors(momenta, torch.float32, "momenta")
     V = _tensors([v.view(-1, 1) for v in second_moments], torch.float32, "second_moments")
-    lib = load()
-    check(lib.normuon_step(P, Gr, M, V, n, lr, wd, mu, beta2, eps, seed, step, _stream(stream, params[0].device)),
-          "normuon_step")
+    _same_device(*params, *grads, *momenta, *second_moments)
+    call("normuon_step", params[0].get_device(), P, Gr, M, V, n, lr, wd, mu, beta2, eps, seed, step,
+         _stream(stream, params[0].device))
 
 
 def gns_muon_momentum(M, G, mu, stream=None):
@@ -218,9 +220,9 @@ def gns_muon_momentum(M, G, mu, stream=None):
     _require(G, torch.bfloat16, name="G")
     if M.numel() != G.numel():
         raise ValueError("M and G differ in size")
-    lib = load()
-    check(lib.gns_muon_momentum(ctypes.c_void_p(M.data_ptr()), ctypes.c_void_p(G.data_ptr()), M.numel(),
-                                mu, _stream(stream, M.device)), "gns_muon_momentum")
+    _same_device(M, G)
+    call("gns_muon_momentum", M.get_device(), ctypes.c_void_p(M.data_ptr()), ctypes.c_void_p(G.data_ptr()),
+         M.numel(), mu, _stream(stream, M.device))
 
 
 def gns_muon_update(W, O, lr, wd, scale, seed, step, base_index=0, stream=None):
@@ -229,10 +231,9 @@ def gns_muon_update(W, O, lr, wd, scale, seed, step, base_index=0, stream=None):
     _require(O, torch.float16, name="O")
     if W.shape != O.shape or W.dim() != 2:
         raise ValueError("W and O must be equal-shaped 2D tensors")
-    lib = load()
-    check(lib.gns_muon_update(ctypes.c_void_p(W.data_ptr()), ctypes.c_void_p(O.data_ptr()), W.shape[0],
-                              W.shape[1], lr, wd, scale, seed, step, base_index, _stream(stream, W.device)),
-          "gns_muon_update")
+    _same_device(W, O)
+    call("gns_muon_update", W.get_device(), ctypes.c_void_p(W.data_ptr()), ctypes.c_void_p(O.data_ptr()),
+         W.shape[0], W.shape[1], lr, wd, scale, seed, step, base_index, _stream(stream, W.device))
 
 
 def gns_symm_gemm(A, B, C, D, alpha=1.0, beta=0.0, stream=None):
@@ -242,11 +243,10 @@ def gns_symm_gemm(A, B, C, D, alpha=1.0, beta=0.0, stream=None):
     if C is not None:
         _require(C, torch.float16, name="C")
     G, n, k = A.shape
-    lib = load()
-    check(lib.gns_symm_gemm(ctypes.c_void_p(A.data_ptr()), ctypes.c_void_p(B.data_ptr()),
-                            ctypes.c_void_p(C.data_ptr() if C is not None else 0),
-                            ctypes.c_void_p(D.data_ptr()), G, n, k, alpha, beta, _stream(stream, A.device)),
-          "gns_symm_gemm")
+    _same_device(A, B, C, D)
+    call("gns_symm_gemm", A.get_device(), ctypes.c_void_p(A.data_ptr()), ctypes.c_void_p(B.data_ptr()),
+         ctypes.c_void_p(C.data_ptr() if C is not None else 0), ctypes.c_void_p(D.data_ptr()), G, n, k, alpha,
+         beta, _stream(stream, A.device))
     return D
 
 
