@@ -5,11 +5,14 @@ Each function marshals tensors and calls the C entry point of the same name
 (include/gns.h states what it computes); outputs are new tensors on the
 stream of the call. Calls may overlap on several streams and may be captured in
 a graph. Gradients are functions of their own, as for the optimizer steps:
-nothing here records an autograd graph.
+nothing here records an autograd graph, and a tensor whose gradient would be
+lost without a word (it requires grad while gradients are enabled, or carries a
+forward-mode tangent) is refused.
 """
 from __future__ import annotations
 
 import torch
+from torch.autograd import forward_ad as _forward_ad
 
 from ._lib import call
 
@@ -191,8 +194,19 @@ def _new(shape, dtype, like, stream):
         return _empty(shape, dtype=dtype, device=like.device)
 
 
+def _no_graph(t, name):
+    """Refuses a tensor that a derivative is wanted through."""
+    if t.requires_grad and torch.is_grad_enabled():
+        raise ValueError(f"{name} requires grad, but no graph is recorded here: call under torch.no_grad() or with "
+                         f"{name}.detach(), and the gradient's function in the backward pass")
+    if _forward_ad._current_level >= 0 and _forward_ad.unpack_dual(t).tangent is not None:
+        raise ValueError(f"{name} carries a forward-mode tangent, which would be lost here")
+
+
 def _typed(t, name, dtypes=DTYPES):
     if isinstance(t, torch.Tensor) and t.dtype in dtypes and t.is_cuda:
+        if t.requires_grad or _forward_ad._current_level >= 0:
+            _no_graph(t, name)
         return
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
@@ -257,6 +271,8 @@ def gns_dropout(x, p, seed, step, residual=None, base_index=0, out=None, stream=
             if t.dtype != x.dtype or t.shape != x.shape:
                 raise ValueError("residual and out must have the type and shape of x")
             _same_device(x, "residual or out", t)
+            if t.requires_grad or _forward_ad._current_level >= 0:
+                _no_graph(t, "residual or out")
             one_row = one_row and t.is_contiguous()
     if out is None:
         out = _new(x.shape, x.dtype, x, stream)
