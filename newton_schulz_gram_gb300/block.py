@@ -44,6 +44,7 @@ class MoeRoute:
             _same_device(offsets, name, t)
         self.tokens, self.topk = rows.shape
         self.experts = offsets.shape[0] - 1
+        _counts("a size", self.tokens, self.topk, self.experts)
         self.device = offsets.get_device()
         if slots.shape[0] != self.tokens * self.topk or self.experts < 1:
             raise ValueError("offsets, rows and slots do not belong together")
@@ -93,6 +94,7 @@ class _Fp8:
             if t.dim() != q_dims or not t.is_contiguous():
                 raise ValueError(f"{name} must be contiguous with {q_dims} dimensions")
         _same_device(q, "scale", scale)
+        _counts("a size", *q.shape)
         if not 0 < cols <= q.shape[-1]:
             raise ValueError("cols must be in 1 .. the columns of q")
         self._buf, self._at, self._q, self._scale = None, 0, q, scale
@@ -248,6 +250,16 @@ def _up(v, a):
     return -(-v // a) * a
 
 
+_MOST = 0x7fffffff
+
+
+def _counts(what, *sizes):
+    """Sizes that the C entries take as int, to which ctypes would cut them without a word."""
+    for v in sizes:
+        if v > _MOST:
+            raise ValueError(f"{what} of {v} is beyond 2^31 - 1")
+
+
 # ------------------------------------------------------------------ dropout
 
 def _rows_of(t, name):
@@ -307,6 +319,7 @@ def gns_moe_sort(experts, num_experts, stream=None):
     tokens, topk = experts.shape
     if num_experts < 1:
         raise ValueError("num_experts must be at least 1")
+    _counts("a size", tokens, topk, num_experts)
     n = tokens * topk
     route = MoeRoute._made(_new((2 * n + num_experts + 1,), torch.int32, experts, stream), tokens, topk, num_experts)
     call("gns_moe_sort", route.device, experts.data_ptr(), experts.element_size(), tokens, topk, num_experts,
@@ -329,6 +342,7 @@ def gns_moe_gather(x, route, stream=None):
     tokens, topk, experts = _route_sizes(route, x)
     if n != tokens:
         raise ValueError("x must have one row per token of the route")
+    _counts("a row", cols)
     y = _new((tokens * topk, cols), x.dtype, x, stream)
     call("gns_moe_gather", route.device, x.data_ptr(), ldx, tokens, topk, experts, cols, DTYPES[x.dtype], route.p_offsets,
          route.p_rows, y.data_ptr(), cols, _on(x, stream))
@@ -349,6 +363,7 @@ def gns_moe_combine(y, weights, route, stream=None):
     tokens, topk, experts = _route_sizes(route, y)
     if n != tokens * topk:
         raise ValueError("y must have one row per slot of the route")
+    _counts("a row", cols)
     if weights is not None:
         _route_weights(weights, route, y)
     out = _new((tokens, cols), y.dtype, y, stream)
@@ -368,6 +383,7 @@ def gns_moe_combine_backward(dout, y, weights, route, stream=None):
     tokens, topk, experts = _route_sizes(route, dout)
     if n != tokens:
         raise ValueError("dout must have one row per token of the route")
+    _counts("a row", cols)
     _route_weights(weights, route, dout)
     ldy, dweights = 0, None
     if y is not None:
@@ -406,6 +422,7 @@ def gns_fp8_quantize(x, fmt="e4m3", route=None, gather=False, rows=True, cols=Tr
     f = _format(fmt)
     if not rows and not cols:
         raise ValueError("rows or cols must be asked for")
+    _counts("a size", n, c)
     groups, topk, slots, offsets = 1, 1, None, None
     if route is not None:
         tokens, topk, groups = _route_sizes(route, x)
@@ -452,6 +469,7 @@ def gns_fp8_quantize_weight(w, fmt="e4m3", stream=None):
             raise ValueError("grouped weights must be contiguous")
         groups, n, k = w.shape
         ldw, stride = k, n * k
+    _counts("a size", groups, n, k)
     ld = _up(k, 16)
     nb, kb = -(-n // BLOCK), -(-k // BLOCK)
     buf = _new((groups * (n * ld + nb * kb),), torch.uint8, w, stream)
@@ -556,6 +574,7 @@ def gns_fp8_linear(x, w, route=None, out_dtype=torch.bfloat16, stream=None):
     groups, n, k = _weight_args(w, route)
     if inner != k:
         raise ValueError(f"the operands' inner sizes differ: {inner} and {k}")
+    _counts("a number of rows", rows)
     out = _out_type(out_dtype)
     topk, slots, offsets = 1, None, None
     if route is not None:
