@@ -14,7 +14,7 @@
 namespace gns {
 namespace {
 
-constexpr int64_t kMaxRows = 65535LL * kFp8Block;  // token blocks are a grid dimension
+constexpr int64_t kMaxRows = 65535LL * kFp8Block;  // blocks of rows are a grid dimension
 
 bool bad_dtype(int d) { return d != GNS_BF16 && d != GNS_FP16 && d != GNS_FP32; }
 bool bad_format(int f) { return f != GNS_E4M3 && f != GNS_E5M2; }

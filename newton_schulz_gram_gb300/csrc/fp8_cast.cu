@@ -437,7 +437,8 @@ __device__ __forceinline__ void cast_tile_of(const Tile& tl, const T* x, long lo
     }
 }
 
-// blockIdx.y: token block; blockIdx.x: the first of the `span` column blocks.
+// blockIdx.z * gridDim.y + blockIdx.y: token block; blockIdx.x: the first of the
+// `span` column blocks.
 template <typename T, int MODE, bool E5M2>
 __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 4 : 2) fp8_cast_kernel(CastJob j, bool vec, int span) {
     __shared__ float part[kWarps][128];
@@ -447,6 +448,7 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 4 : 2) fp8_cast_ker
     grid_dependency_wait();
     grid_launch_dependents();
     Tile tl;
+    const int tb = static_cast<int>(blockIdx.z * gridDim.y + blockIdx.y);
     if (j.offsets) {
         // The group that owns this token block: thread t sums the blocks of
         // groups t * per .. t * per + per - 1.
@@ -466,14 +468,13 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 4 : 2) fp8_cast_ker
         __syncthreads();
         int start = scan - mine;
         for (int w = 0; w < warp; ++w) start += __float_as_int(part[0][w]);
-        const int b = blockIdx.y;
-        if (b >= start && b < start + mine) {
+        if (tb >= start && tb < start + mine) {
             for (int i = 0; i < per && g0 + i < j.G; ++i) {
                 const int beg = j.offsets[g0 + i], n = j.offsets[g0 + i + 1] - beg;
                 const int nb = blocks_of(n);
-                if (b < start + nb) {
-                    found[1] = beg + (b - start) * kFp8Block;
-                    found[2] = min(n - (b - start) * kFp8Block, kFp8Block);
+                if (tb < start + nb) {
+                    found[1] = beg + (tb - start) * kFp8Block;
+                    found[2] = min(n - (tb - start) * kFp8Block, kFp8Block);
                     found[0] = 1;
                     break;
                 }
@@ -485,15 +486,15 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 4 : 2) fp8_cast_ker
         tl.r0 = found[1];
         tl.nrows = found[2];
     } else {
-        tl.r0 = blockIdx.y * kFp8Block;
+        tl.r0 = tb * kFp8Block;
         tl.nrows = min(j.rows - tl.r0, kFp8Block);
     }
     if (j.slots) {  // once for all column blocks: a division per row
         if (static_cast<int>(threadIdx.x) < tl.nrows) source[threadIdx.x] = j.slots[tl.r0 + threadIdx.x] / j.topk;
         __syncthreads();
     }
-    tl.qc_row = static_cast<long long>(blockIdx.y) * kFp8Block;
-    tl.sc_row = blockIdx.y;
+    tl.qc_row = static_cast<long long>(tb) * kFp8Block;
+    tl.sc_row = tb;
     const int nblk = (j.cols + kFp8Block - 1) / kFp8Block;
     for (int cb = blockIdx.x * span; cb < min(nblk, static_cast<int>(blockIdx.x + 1) * span); ++cb) {
         tl.c0 = cb * kFp8Block;
@@ -533,7 +534,10 @@ int cast_typed(const CastJob& j, int num_sms, cudaStream_t s) {
     int span = 1;
     if (j.offsets)
         while (span < 8 && static_cast<long long>(tblk) * ((nblk + 2 * span - 1) / (2 * span)) >= 16LL * num_sms) span *= 2;
-    const dim3 grid((nblk + span - 1) / span, tblk);
+    // Without groups at most 65535 token blocks; groups may add one each, and a
+    // second layer of the grid takes those (its last blocks find no group).
+    const int layers = (tblk + 65534) / 65535;
+    const dim3 grid((nblk + span - 1) / span, (tblk + layers - 1) / layers, layers);
     auto run = [&](auto k) { return static_cast<int>(launch_after(k, grid, dim3(kThreads), 0, s, j, vec, span)); };
     if (j.q_rows && j.q_cols) return run(fp8_cast_kernel<T, kBothForms, E5M2>);
     if (j.q_rows) return run(fp8_cast_kernel<T, kRowForm, E5M2>);

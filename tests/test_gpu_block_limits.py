@@ -1,0 +1,45 @@
+"""The training-block operators at the largest sizes that their entries accept."""
+import pytest
+
+torch = pytest.importorskip("torch")
+pytestmark = pytest.mark.gpu
+
+MOST_ROWS = 65535 * 128
+
+
+@pytest.fixture(scope="module")
+def gns():
+    import newton_schulz_gram_gb300 as m
+    from newton_schulz_gram_gb300 import build
+    build.build()
+    m.load()
+    yield m
+    torch.cuda.empty_cache()
+    assert m.gns_get_status() == 0
+
+
+def same(a, b):
+    return torch.equal(a.contiguous().view(torch.uint8), b.contiguous().view(torch.uint8))
+
+
+@pytest.mark.parametrize("experts", [2, 300])
+def test_routed_cast_of_the_most_rows(gns, experts):
+    """Each group starts a token block of its own, so there are more of them than
+    rows / 128: every group's forms are those of its rows alone, and whole
+    numbers make the weight gradient over them exact."""
+    g = torch.Generator(device="cuda").manual_seed(experts)
+    x = torch.randint(-1, 2, (MOST_ROWS, 16), generator=g, device="cuda").bfloat16()
+    ids = torch.randint(0, experts, (MOST_ROWS, 1), generator=g, device="cuda")
+    route = gns.gns_moe_sort(ids, experts)
+    offsets = route.offsets.tolist()
+    assert sum(-(-(b - a) // 128) for a, b in zip(offsets, offsets[1:])) > 65535
+    rows, cols = gns.gns_fp8_quantize(x, route=route)
+    dw = gns.gns_fp8_matmul_wgrad(cols, cols, route=route, out_dtype=torch.float32)
+    block = 0
+    for e, (a, b) in enumerate(zip(offsets, offsets[1:])):
+        r, c = gns.gns_fp8_quantize(x[a:b])
+        assert same(rows.q[a:b], r.q) and same(rows.scale[:, a:b], r.scale)
+        assert same(cols.q[128 * block:128 * block + c.q.shape[0]], c.q)
+        assert same(cols.scale[block:block + c.blocks], c.scale)
+        block += c.blocks
+        assert torch.equal(dw[e], (x[a:b].double().t() @ x[a:b].double()).float())
