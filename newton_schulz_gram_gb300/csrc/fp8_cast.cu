@@ -49,6 +49,10 @@ struct Tile {
     int sc_row;        // its row of column scales
 };
 
+// Columns of an 8-bit row that are written: what lies beyond, in a row stride
+// that is larger, is the caller's.
+__device__ __forceinline__ int written(int cols) { return (cols + 15) & ~15; }
+
 // Two 16-bit values at a time. max_abs has the larger magnitudes (and signs of
 // no meaning); it passes over a NaN and shows an infinity, whose block then
 // takes the finite maximum the slow way. scaled is a pair times a power of two
@@ -210,7 +214,7 @@ __device__ __forceinline__ void cast_tile16(const Tile& tl, const T* x, long lon
             bytes[p >> 2] |= e << (8 * (p & 3));
             if (!FULL && 16 * p >= tl.nrows) continue;  // no row of this pass is there
             const typename P2::Scale s = P2::scale(exp_inverse(e), exp_inverse(e)), inv[4] = {s, s, s, s};
-            if (FULL || (16 * p + rl < tl.nrows && c < ld_rows))
+            if (FULL || (16 * p + rl < tl.nrows && c < written(cols)))
                 *reinterpret_cast<uint2*>(out + 16LL * p * ld_rows) =
                     cast_words<T, E5M2>(raw[p], inv);
         }
@@ -287,7 +291,7 @@ __device__ __forceinline__ void cast_tile16(const Tile& tl, const T* x, long lon
         for (int p = 0; p < kPasses; ++p) {
             // The column form is zero to the end of its last block of 128
             // rows (the rows past nrows were loaded as zero).
-            if (FULL || (c < ld_cols && (!(MODE & kBlockForm) || 16 * p + rl < tl.nrows)))
+            if (FULL || (c < written(cols) && (!(MODE & kBlockForm) || 16 * p + rl < tl.nrows)))
                 *reinterpret_cast<uint2*>(out + 16LL * p * ld_cols) =
                     !FULL && 16 * p >= tl.nrows ? make_uint2(0, 0) : cast_words<T, E5M2>(raw[p], iv);
         }
@@ -346,7 +350,7 @@ __device__ __forceinline__ void cast_tile(const Tile& tl, const T* x, long long 
             const float inv = exp_inverse(e);
             const int r = 16 * p + rl;
             if (r < tl.nrows) {
-                if (c < ld_rows) {
+                if (c < written(cols)) {
                     float w[8], iv[8];
 #pragma unroll
                     for (int i = 0; i < 8; ++i) {
@@ -412,7 +416,7 @@ __device__ __forceinline__ void cast_tile(const Tile& tl, const T* x, long long 
             const int r = 16 * p + rl;
             // The column form is zero to the end of its last block of 128
             // rows (the rows past nrows were loaded as zero).
-            if (c < ld_cols && (!(MODE & kBlockForm) || r < tl.nrows)) {
+            if (c < written(cols) && (!(MODE & kBlockForm) || r < tl.nrows)) {
                 float v[8];
                 raw[p].get(v);
 #pragma unroll
