@@ -38,6 +38,7 @@ struct CastJob {
     uint8_t* q_cols;
     uint8_t* s_cols;
     long long ld_cols, lds_cols;
+    int block0;  // first token block of a launch (set by the launcher)
 };
 
 int launch_fp8_cast(const CastJob& job, int num_sms, cudaStream_t s);

@@ -32,6 +32,7 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kPasses = 8;   // 16 rows each; a thread owns 8 columns of one row per pass
 constexpr int kWarps = kThreads / 32;
+constexpr int kMaxGrid = 65535;  // blocks in the grid's second dimension
 
 enum CastMode { kRowForm = 1, kColForm = 2, kBothForms = 3, kBlockForm = 4 };
 
@@ -49,9 +50,9 @@ struct Tile {
     int sc_row;        // its row of column scales
 };
 
-// Columns of an 8-bit row that are written: what lies beyond, in a row stride
-// that is larger, is the caller's.
-__device__ __forceinline__ int written(int cols) { return (cols + 15) & ~15; }
+// Whether column c (a multiple of 8) of an 8-bit row is written: those up to the
+// next multiple of 16 are, what lies beyond in a larger row stride is the caller's.
+__device__ __forceinline__ bool written(int c, int cols) { return (c & ~15) < cols; }
 
 // Two 16-bit values at a time. max_abs has the larger magnitudes (and signs of
 // no meaning); it passes over a NaN and shows an infinity, whose block then
@@ -214,7 +215,7 @@ __device__ __forceinline__ void cast_tile16(const Tile& tl, const T* x, long lon
             bytes[p >> 2] |= e << (8 * (p & 3));
             if (!FULL && 16 * p >= tl.nrows) continue;  // no row of this pass is there
             const typename P2::Scale s = P2::scale(exp_inverse(e), exp_inverse(e)), inv[4] = {s, s, s, s};
-            if (FULL || (16 * p + rl < tl.nrows && c < written(cols)))
+            if (FULL || (16 * p + rl < tl.nrows && written(c, cols)))
                 *reinterpret_cast<uint2*>(out + 16LL * p * ld_rows) =
                     cast_words<T, E5M2>(raw[p], inv);
         }
@@ -291,7 +292,7 @@ __device__ __forceinline__ void cast_tile16(const Tile& tl, const T* x, long lon
         for (int p = 0; p < kPasses; ++p) {
             // The column form is zero to the end of its last block of 128
             // rows (the rows past nrows were loaded as zero).
-            if (FULL || (c < written(cols) && (!(MODE & kBlockForm) || 16 * p + rl < tl.nrows)))
+            if (FULL || (written(c, cols) && (!(MODE & kBlockForm) || 16 * p + rl < tl.nrows)))
                 *reinterpret_cast<uint2*>(out + 16LL * p * ld_cols) =
                     !FULL && 16 * p >= tl.nrows ? make_uint2(0, 0) : cast_words<T, E5M2>(raw[p], iv);
         }
@@ -350,7 +351,7 @@ __device__ __forceinline__ void cast_tile(const Tile& tl, const T* x, long long 
             const float inv = exp_inverse(e);
             const int r = 16 * p + rl;
             if (r < tl.nrows) {
-                if (c < written(cols)) {
+                if (written(c, cols)) {
                     float w[8], iv[8];
 #pragma unroll
                     for (int i = 0; i < 8; ++i) {
@@ -416,7 +417,7 @@ __device__ __forceinline__ void cast_tile(const Tile& tl, const T* x, long long 
             const int r = 16 * p + rl;
             // The column form is zero to the end of its last block of 128
             // rows (the rows past nrows were loaded as zero).
-            if (c < written(cols) && (!(MODE & kBlockForm) || r < tl.nrows)) {
+            if (written(c, cols) && (!(MODE & kBlockForm) || r < tl.nrows)) {
                 float v[8];
                 raw[p].get(v);
 #pragma unroll
@@ -441,8 +442,8 @@ __device__ __forceinline__ void cast_tile_of(const Tile& tl, const T* x, long lo
     }
 }
 
-// blockIdx.z * gridDim.y + blockIdx.y: token block; blockIdx.x: the first of the
-// `span` column blocks.
+// blockIdx.y: token block, after those of earlier launches (j.block0; the column
+// form's pointers are this launch's); blockIdx.x: the first of the `span` column blocks.
 template <typename T, int MODE, bool E5M2>
 __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 4 : 2) fp8_cast_kernel(CastJob j, bool vec, int span) {
     __shared__ float part[kWarps][128];
@@ -452,7 +453,6 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 4 : 2) fp8_cast_ker
     grid_dependency_wait();
     grid_launch_dependents();
     Tile tl;
-    const int tb = static_cast<int>(blockIdx.z * gridDim.y + blockIdx.y);
     if (j.offsets) {
         // The group that owns this token block: thread t sums the blocks of
         // groups t * per .. t * per + per - 1.
@@ -472,13 +472,14 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 4 : 2) fp8_cast_ker
         __syncthreads();
         int start = scan - mine;
         for (int w = 0; w < warp; ++w) start += __float_as_int(part[0][w]);
-        if (tb >= start && tb < start + mine) {
+        const int b = j.block0 + static_cast<int>(blockIdx.y);
+        if (b >= start && b < start + mine) {
             for (int i = 0; i < per && g0 + i < j.G; ++i) {
                 const int beg = j.offsets[g0 + i], n = j.offsets[g0 + i + 1] - beg;
                 const int nb = blocks_of(n);
-                if (tb < start + nb) {
-                    found[1] = beg + (tb - start) * kFp8Block;
-                    found[2] = min(n - (tb - start) * kFp8Block, kFp8Block);
+                if (b < start + nb) {
+                    found[1] = beg + (b - start) * kFp8Block;
+                    found[2] = min(n - (b - start) * kFp8Block, kFp8Block);
                     found[0] = 1;
                     break;
                 }
@@ -490,15 +491,15 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 4 : 2) fp8_cast_ker
         tl.r0 = found[1];
         tl.nrows = found[2];
     } else {
-        tl.r0 = tb * kFp8Block;
+        tl.r0 = blockIdx.y * kFp8Block;
         tl.nrows = min(j.rows - tl.r0, kFp8Block);
     }
     if (j.slots) {  // once for all column blocks: a division per row
         if (static_cast<int>(threadIdx.x) < tl.nrows) source[threadIdx.x] = j.slots[tl.r0 + threadIdx.x] / j.topk;
         __syncthreads();
     }
-    tl.qc_row = static_cast<long long>(tb) * kFp8Block;
-    tl.sc_row = tb;
+    tl.qc_row = static_cast<long long>(blockIdx.y) * kFp8Block;
+    tl.sc_row = blockIdx.y;
     const int nblk = (j.cols + kFp8Block - 1) / kFp8Block;
     for (int cb = blockIdx.x * span; cb < min(nblk, static_cast<int>(blockIdx.x + 1) * span); ++cb) {
         tl.c0 = cb * kFp8Block;
@@ -538,11 +539,23 @@ int cast_typed(const CastJob& j, int num_sms, cudaStream_t s) {
     int span = 1;
     if (j.offsets)
         while (span < 8 && static_cast<long long>(tblk) * ((nblk + 2 * span - 1) / (2 * span)) >= 16LL * num_sms) span *= 2;
-    // Without groups at most 65535 token blocks; groups may add one each, and a
-    // second layer of the grid takes those (its last blocks find no group).
-    const int layers = (tblk + 65534) / 65535;
-    const dim3 grid((nblk + span - 1) / span, (tblk + layers - 1) / layers, layers);
-    auto run = [&](auto k) { return static_cast<int>(launch_after(k, grid, dim3(kThreads), 0, s, j, vec, span)); };
+    // Without groups there are at most 65535 token blocks, the grid's limit; groups
+    // may add one each, and a second launch takes those beyond. (A third grid
+    // dimension instead costs the kernel of both forms the registers it has not:
+    // spills, 92 us instead of 88 for the gathered cast above.)
+    auto run = [&](auto k) {
+        CastJob part = j;
+        for (part.block0 = 0; part.block0 < tblk; part.block0 += kMaxGrid) {
+            const dim3 grid((nblk + span - 1) / span, std::min(tblk - part.block0, kMaxGrid));
+            const cudaError_t e = launch_after(k, grid, dim3(kThreads), 0, s, part, vec, span);
+            if (e != cudaSuccess) return static_cast<int>(e);
+            if (part.q_cols) {
+                part.q_cols += static_cast<long long>(kMaxGrid) * kFp8Block * j.ld_cols;
+                part.s_cols += static_cast<long long>(kMaxGrid) * j.lds_cols;
+            }
+        }
+        return static_cast<int>(cudaSuccess);
+    };
     if (j.q_rows && j.q_cols) return run(fp8_cast_kernel<T, kBothForms, E5M2>);
     if (j.q_rows) return run(fp8_cast_kernel<T, kRowForm, E5M2>);
     return run(fp8_cast_kernel<T, kColForm, E5M2>);
