@@ -377,8 +377,9 @@ int gns_fp8_quantize_weight(const void* w, int64_t ldw, int64_t stride_w, int dt
  * from the row form of a ([rows][K]) and 8-bit weights:
  *   y[r][n] = sum over the blocks b of 128 along K of
  *             scale_a[b][r] scale_w[g][n / 128][b] sum_{k in b} a[r][k] w[g][n][k],
- * summed in the tensor core's fp32 accumulator (which truncates); fp32 results
- * in segments of 2048 terms, added with one rounding each.
+ * summed in the tensor core's fp32 accumulator (which truncates), in segments of
+ * 2048 terms for fp32 results and 32768 for 16-bit ones, added with one rounding
+ * each (so in the two gradients).
  *   offsets  [groups + 1] as written by gns_moe_sort; rows past
  *            offsets[groups] of y are set to zero. NULL with groups = 1: all
  *            rows are one group's.

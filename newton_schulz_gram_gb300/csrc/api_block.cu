@@ -124,10 +124,14 @@ int product(const void* a, int64_t lda, const uint8_t* sa, int64_t ld_sa, int fm
     j.D = D;
     j.ldd = ldd;
     j.out_dtype = out_dtype;
-    Scratch partial;
+    Scratch partial, carry;
     if (j.split > 1) {
         RET(partial.take(*st, sizeof(float) * static_cast<size_t>(j.split) * rows * out, s));
         j.partial = reinterpret_cast<float*>(partial.data());
+    }
+    if (const size_t bytes = fp8_carry_bytes(inner, out_dtype, j.split, st->num_sms)) {
+        RET(carry.take(*st, bytes, s));
+        j.carry = reinterpret_cast<float*>(carry.data());
     }
     RET(map_output(j, cg));
     j.st = new_call(*st);
@@ -380,6 +384,11 @@ int gns_fp8_matmul_wgrad(const void* dy, int64_t lddy, const uint8_t* scale_dy, 
     j.strideD = stride_dw;
     j.out_dtype = out_dtype;
     j.split = 1;
+    Scratch carry;
+    if (const size_t bytes = fp8_carry_bytes(rows, out_dtype, 1, st->num_sms)) {
+        RET(carry.take(*st, bytes, s));
+        j.carry = reinterpret_cast<float*>(carry.data());
+    }
     RET(map_output(j, cg));
     j.st = new_call(*st);
     LAUNCH(kClsFp8Gemm, launch_fp8_gemm(j, cg, st->num_sms, s));

@@ -6,6 +6,7 @@
 #include <cuda.h>
 #include <cuda_runtime.h>
 
+#include "blockops.cuh"
 #include "ptx.cuh"
 
 namespace gns {
@@ -86,6 +87,7 @@ struct Fp8GemmJob {
     long long ldd, strideD;
     int out_dtype;
     float* partial;      // split > 1: fp32 [split][rows][N]
+    float* carry;        // fp8_carry_bytes() bytes, or null where that is 0
     int split;           // forward / data gradient of one group only
     DevStatus st;
 };
@@ -97,6 +99,15 @@ int fp8_gemm_cg(int M, int N, bool grouped, bool forward, int out_dtype, int num
 inline int fp8_gemm_b_box(int cg, bool b_mn) { return b_mn || cg == 2 ? 128 : 256; }
 
 int launch_fp8_gemm(const Fp8GemmJob& job, int cg, int num_sms, cudaStream_t s);
+
+// Bytes of intermediate memory for a 16-bit result whose contraction (an upper
+// bound of it) is longer than the tensor core's accumulator sums alone: a tile's
+// fp32 sums so far, for each CTA.
+constexpr int kFp8LongBlocks = 256;  // blocks of 128 along the contraction (see fp8_gemm.cu)
+inline size_t fp8_carry_bytes(long long contraction, int out_dtype, int split, int num_sms) {
+    const bool carries = elem_bytes(out_dtype) == 2 && split <= 1 && contraction > kFp8LongBlocks * kFp8Block;
+    return carries ? sizeof(float) * 128 * 256 * num_sms : 0;
+}
 
 // The split of the contraction that fills the machine, 1 for none.
 int fp8_gemm_split(int rows, int N, int K, int num_sms);

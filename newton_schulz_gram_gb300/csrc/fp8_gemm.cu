@@ -8,10 +8,16 @@
 // core applies the scales itself (kind::mxf8f6f4, block_scale): it takes one
 // 8-bit exponent per row of A and of B and 32-wide k step, so a block of 128 is
 // four steps with the same exponent, and the sum stays in TMEM in fp32. That
-// accumulator truncates, an error that grows with the steps (at a contraction
-// of 4096 up to 2.9e-6 of the result, far below a 16-bit result's rounding), so
-// fp32 results are summed in segments of kSegment blocks, each segment added to
-// the stored result with one rounding (6e-7 at any length).
+// accumulator truncates, an error that grows with the steps: up to about 2^-23 of
+// the sum per step of 32 terms where all have one sign (3.7e-2 of a sum of 8.4
+// million), 2.9e-6 of a result at 4096 terms of mixed signs. So fp32 results are
+// summed in segments of kSegment blocks, each segment added to the stored result
+// with one rounding (6e-7 at any length), and 16-bit results in segments of
+// kFp8LongBlocks blocks (32768 terms, 1.5e-4 at most: a third of fp16's
+// rounding), whose fp32 sums a tile's CTA carries on in its own part of an
+// intermediate buffer. (Weight gradients over 65536 rows, two segments: N x K =
+// 1024 x 4096 204 us without and 206 to 217 with it, 4096 x 4096 798 to 814 and
+// 804 to 837; segments of 128 blocks cost up to twice that.)
 // Applying the scales in registers instead, which any fp32 scale would need,
 // reads the accumulator once per block: 1220 cycles per block beside the 512 of
 // its MMAs (8192 x 14336 x 4096 forward: 470 us, with scaled MMAs 378).
@@ -91,7 +97,7 @@ constexpr int kScaleSlots = 2;
 constexpr int kSlotBlocks = 4;
 constexpr uint32_t kSlotBytes = 512 + 1024;
 constexpr int kSegment = 16;  // k blocks of a segment of an fp32 result
-static_assert(kSegment % kSlotBlocks == 0, "a scale slot lies in one segment");
+static_assert(kSegment % kSlotBlocks == 0 && kFp8LongBlocks % kSlotBlocks == 0, "a scale slot lies in one segment");
 
 constexpr int kTileSlots = 4;
 constexpr int kTileReaders = 2 + kSlotBlocks + kEpiWarps;  // producer, MMA issuer, scale builder, epilogue warps
@@ -413,9 +419,10 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_gemm_kernel(const __grid_cons
     const int lane = threadIdx.x & 31;
     const DevStatus& err = P.st;
     const int rank = CG > 1 ? static_cast<int>(cluster_ctarank()) : 0;  // 0: the pair's leader
-    // k blocks summed in TMEM before the result is stored or added to.
+    // k blocks summed in TMEM before the result is stored or added to (fp32) or
+    // added to the sums that are carried on to the tile's last segment (16 bits).
     constexpr int ES = sizeof(T);
-    constexpr int segment = ES == 4 ? kSegment : 1 << 30;
+    constexpr int segment = ES == 4 ? kSegment : kFp8LongBlocks;
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < STAGES; ++s) {
@@ -814,6 +821,22 @@ __global__ void __launch_bounds__(kThreads, 1) fp8_gemm_kernel(const __grid_cons
                         if (n == 0 && mine) hand_back(overlap_lead);
                         if (n == kCols / 32 - 1) hand_back(acce_lead + 8 * buf);
                     }
+                    if constexpr (ES == 2) {
+                        if (live && tl.kb1 - tl.kb0 > segment) {
+                            // A lane's sums are 32 words apart, a warp's neighbouring.
+                            float* sums = P.carry + (static_cast<size_t>(blockIdx.x) * kEpiWarps + ew) * (32 * kCols) +
+                                          1024 * p + lane;
+                            if (kb > tl.kb0) {
+#pragma unroll
+                                for (int j = 0; j < 32; ++j) x[j] = add_bits(__float_as_uint(sums[32 * j]), x[j]);
+                            }
+                            if (tl.kb1 - kb > segment) {
+#pragma unroll
+                                for (int j = 0; j < 32; ++j) sums[32 * j] = __uint_as_float(x[j]);
+                                continue;
+                            }
+                        }
+                    }
 #pragma unroll
                     for (int h = 0; h < kRounds; ++h) {
                         const int c0 = 32 * (kJoin == 2 ? p & ~1 : p) + h * (ROW / ES);
@@ -997,6 +1020,8 @@ int launch_fp8_gemm(const Fp8GemmJob& job, int cg, int num_sms, cudaStream_t s) 
         tm = (job.rows + tile - 1) / tile;
     const long long tiles = tm * tn * job.split;
     if (tiles <= 0) return cudaSuccess;
+    if (!job.carry && fp8_carry_bytes(job.wgrad ? job.rows : job.K, job.out_dtype, job.split, num_sms))
+        return cudaErrorInvalidValue;
     const int e = by_dtype(job.split > 1 ? static_cast<int>(GNS_FP32) : job.out_dtype, [&](auto t) {
         using T = decltype(t);
         if (job.wgrad) {

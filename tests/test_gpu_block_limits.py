@@ -43,3 +43,30 @@ def test_routed_cast_of_the_most_rows(gns, experts):
         assert same(cols.scale[block:block + c.blocks], c.scale)
         block += c.blocks
         assert torch.equal(dw[e], (x[a:b].double().t() @ x[a:b].double()).float())
+
+
+@pytest.mark.parametrize("dtype", [torch.float16, torch.bfloat16])
+@pytest.mark.parametrize("experts", [0, 2])
+def test_16_bit_results_of_the_longest_contraction(gns, dtype, experts):
+    """Values of one sign, the worst case of an accumulator that truncates. Each of
+    its steps, of 32 terms, loses less than one unit in the last place of the sum
+    so far (2^-23 of it at most); a result is at most 65536 terms of that away
+    from its sum before it is rounded to its type, however many terms there are."""
+    g = torch.Generator(device="cuda").manual_seed(3)
+    x = (0.5 + 0.5 * torch.rand(MOST_ROWS, 24, generator=g, device="cuda")) / 32
+    dy = (0.5 + 0.5 * torch.rand(MOST_ROWS, 40, generator=g, device="cuda")) / 32
+    route = None
+    if experts:
+        route = gns.gns_moe_sort((torch.rand(MOST_ROWS, 1, generator=g, device="cuda") < 0.3).int(), experts)
+    (_, xc), (_, dc) = (gns.gns_fp8_quantize(t, route=route, rows=False) for t in (x, dy))
+    offsets = route.offsets.tolist() if experts else [0, MOST_ROWS]
+    dw = gns.gns_fp8_matmul_wgrad(dc, xc, route=route, out_dtype=dtype).view(-1, 40, 24)
+    block = 0
+    for e, (a, b) in enumerate(zip(offsets, offsets[1:])):
+        n = -(-(b - a) // 128)
+        xv, dv = (c.q[128 * block:128 * (block + n), :c.cols].float().double()
+                  .mul_(c.scale[block:block + n].float().double().repeat_interleave(128, 0)) for c in (xc, dc))
+        exact = dv.t() @ xv
+        error = ((dw[e].double() - exact).abs() / exact).max().item()
+        assert error <= torch.finfo(dtype).eps / 2 + 2048 * 2.0 ** -23, (e, error)
+        block += n
