@@ -12,7 +12,6 @@ __device__ __forceinline__ uint32_t scale_exponent(float amax, int top) {
     const int b = static_cast<int>((__float_as_uint(amax) + 0x1FFFFFu) >> 23) - top;
     return static_cast<uint32_t>(b < 1 ? 1 : b);
 }
-__device__ __forceinline__ float exp_value(uint32_t biased) { return __uint_as_float(biased << 23); }
 // 1 / 2^(biased - 127); biased <= 247, so the inverse is a normal number.
 __device__ __forceinline__ float exp_inverse(uint32_t biased) { return __uint_as_float((254u - biased) << 23); }
 

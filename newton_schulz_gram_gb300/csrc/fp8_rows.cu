@@ -15,9 +15,9 @@
 // long as x uses the same one. Tensor throughput does not matter at 8 columns;
 // tcgen05 would add TMEM and descriptors to a kernel that lives for a few
 // microseconds. The warps' sums are joined in a fixed order.
-// One row, 14336 x 4096: 15.0 us (3.9 TB/s; 28672 x 8192 47.6, 4.9); without
+// One row, 14336 x 4096: 15.2 us (3.9 TB/s; 28672 x 8192 46.7, 5.0); without
 // conversions and products, the loads alone, 11.9. Eight rows, whose fp16 forms
-// leave room for one block of threads per SM: 20 (28 with a grid for two). The
+// leave room for one block of threads per SM: 20.2. The
 // 8-bit mma.sync took 19.4 us for one row, a block of threads per strip without
 // the ring 15.6, and more of them, of eight warps, 17.0.
 #include <algorithm>
@@ -71,6 +71,16 @@ __device__ __forceinline__ void product(float (&c)[4], const uint4& lo, const ui
         const uint2 p = to_half4<E5M2>(l[i]), q = to_half4<E5M2>(h[i]);
         mma_16816(c, p.x, q.x, p.y, q.y, x[2 * i], x[2 * i + 1]);
     }
+}
+
+// acc + part 2^(a + b - 254) for two 8-bit exponents a, b, given as (a + b) << 22:
+// half of it in each of two factors, since the whole may be no fp32 number where
+// the result is (a block whose scale is 2^100 may meet nothing but zeros). `nan`
+// is a NaN's bits where an exponent is the one that stands for NaN.
+__device__ __forceinline__ float scaled(float part, uint32_t exps, uint32_t nan, float acc) {
+    const float lo = __uint_as_float((exps & 0x7F800000u) | nan);
+    const float hi = __uint_as_float((exps + 0x400000u) & 0x7F800000u);
+    return fmaf(part * lo, hi, acc);
 }
 
 // 16 bytes to shared memory, zeros where `in` is false.
@@ -190,7 +200,7 @@ __global__ void __launch_bounds__(kThreads, 2) fp8_rows_kernel(Fp8RowsJob j, boo
     // x to 8 bits: sixteen threads per block of 128.
     const int stride = nkb * kFp8Block + 8;
     __half* xq = reinterpret_cast<__half*>(smem + kWarps * slots * kSlotBytes);
-    float* xs = reinterpret_cast<float*>(xq + (count + 1) * stride);
+    uint32_t* xs = reinterpret_cast<uint32_t*>(xq + (count + 1) * stride);  // exponents, as `scaled` wants them
     for (int i = threadIdx.x; i < stride / 8; i += kThreads)
         *reinterpret_cast<uint4*>(xq + count * stride + 8 * i) = make_uint4(0, 0, 0, 0);
     for (int i = threadIdx.x >> 4; i < count * nkb; i += kThreads / 16) {
@@ -211,7 +221,7 @@ __global__ void __launch_bounds__(kThreads, 2) fp8_rows_kernel(Fp8RowsJob j, boo
         const uint32_t w[2] = {cast_quad<false>(v[0], v[1], v[2], v[3]), cast_quad<false>(v[4], v[5], v[6], v[7])};
         const uint2 lo = to_half4<false>(w[0]), hi = to_half4<false>(w[1]);
         *reinterpret_cast<uint4*>(xq + r * stride + b * kFp8Block + 8 * l) = make_uint4(lo.x, lo.y, hi.x, hi.y);
-        if (l == 0) xs[r * nkb + b] = exp_value(e);
+        if (l == 0) xs[r * nkb + b] = e << 22;
     }
     __syncthreads();
 
@@ -223,7 +233,7 @@ __global__ void __launch_bounds__(kThreads, 2) fp8_rows_kernel(Fp8RowsJob j, boo
     for (int strip = blockIdx.x; strip < strips; strip += gridDim.x, buf ^= 1) {
         float acc[4] = {0.0f, 0.0f, 0.0f, 0.0f};
         for (int b = warp; b < nkb; b += kWarps) {
-            const float wsc = exp_value(scale);
+            const uint32_t wexp = scale << 22, nan = scale == 255 ? 0x7FC00000u : 0u;
             {
                 int next = b + kWarps, at = strip;
                 if (next >= nkb) next = warp, at += gridDim.x;
@@ -257,12 +267,12 @@ __global__ void __launch_bounds__(kThreads, 2) fp8_rows_kernel(Fp8RowsJob j, boo
                     product<false>(part, a[0][c], a[1][c], x);
             }
             issue();  // into the slot just read: a lane meets only its own pieces
-            const float s0 = 2 * t < count ? wsc * xs[2 * t * nkb + b] : 0.0f;
-            const float s1 = 2 * t + 1 < count ? wsc * xs[(2 * t + 1) * nkb + b] : 0.0f;
-            acc[0] = fmaf(part[0], s0, acc[0]);
-            acc[1] = fmaf(part[1], s1, acc[1]);
-            acc[2] = fmaf(part[2], s0, acc[2]);
-            acc[3] = fmaf(part[3], s1, acc[3]);
+            const uint32_t s0 = wexp + (2 * t < count ? xs[2 * t * nkb + b] : 0);
+            const uint32_t s1 = wexp + (2 * t + 1 < count ? xs[(2 * t + 1) * nkb + b] : 0);
+            acc[0] = scaled(part[0], s0, nan, acc[0]);
+            acc[1] = scaled(part[1], s1, nan, acc[1]);
+            acc[2] = scaled(part[2], s0, nan, acc[2]);
+            acc[3] = scaled(part[3], s1, nan, acc[3]);
         }
         sums[buf][warp][gq][2 * t] = acc[0];
         sums[buf][warp][gq][2 * t + 1] = acc[1];
