@@ -28,7 +28,11 @@ class MoeRoute:
     offsets[e] .. offsets[e + 1] - 1; rows[t, j] is the sorted row of token t's
     j-th choice and slots its inverse. Rows from offsets[-1] on belong to no
     expert. int32: offsets [num_experts + 1], rows [tokens, topk], slots
-    [tokens * topk]; checked here once, not by every call that takes a route.
+    [tokens * topk]. The operators read and write where these say, so a route
+    that is made of one's own tensors is checked, once, here: offsets that
+    begin at 0, do not fall and end within the slots, and rows and slots that
+    are inverse permutations. That waits for the tensors, so such a route is
+    made before a stream capture, not in it.
 
     What the library makes is one allocation (rows, slots, offsets); the
     tensors are views made when they are asked for, since a launch costs a call
@@ -48,6 +52,7 @@ class MoeRoute:
         self.device = offsets.get_device()
         if slots.shape[0] != self.tokens * self.topk or self.experts < 1:
             raise ValueError("offsets, rows and slots do not belong together")
+        _checked_route(offsets, rows.view(-1), slots)
         self._buf, self._offsets, self._rows, self._slots = None, offsets, rows, slots
         self.p_offsets, self.p_rows, self.p_slots = offsets.data_ptr(), rows.data_ptr(), slots.data_ptr()
 
@@ -81,6 +86,19 @@ class MoeRoute:
 
     def __iter__(self):
         return iter((self.offsets, self.rows, self.slots))
+
+
+def _checked_route(offsets, rows, slots):
+    if torch.cuda.is_current_stream_capturing():
+        raise ValueError("a route of one's own tensors is checked, which a stream capture does not allow: make it before")
+    n = rows.shape[0]
+    ok = (offsets[0] == 0) & (offsets[1:] >= offsets[:-1]).all() & (offsets[-1] <= n)
+    if n:
+        inside = ((rows >= 0) & (rows < n) & (slots >= 0) & (slots < n)).all()
+        back = slots[rows.clamp(0, n - 1).long()] == torch.arange(n, dtype=torch.int32, device=rows.device)
+        ok = ok & inside & back.all()
+    if not ok.item():
+        raise ValueError("offsets must rise from 0 to at most the number of slots, rows and slots be inverse permutations")
 
 
 class _Fp8:

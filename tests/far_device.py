@@ -55,6 +55,7 @@ def install(monkeypatch):
 
     monkeypatch.setattr(_lib, "_LIB", m)
     monkeypatch.setattr(_lib, "_current_device", lambda: m.current, raising=False)
+    monkeypatch.setattr(torch.cuda, "is_current_stream_capturing", lambda: False)
     monkeypatch.setattr(torch.cuda, "current_device", lambda: m.current)
     monkeypatch.setattr(torch.cuda, "device", device)
     monkeypatch.setattr(torch.cuda, "current_stream", lambda device=None: Stream)
