@@ -136,6 +136,7 @@ int product(const void* a, int64_t lda, const uint8_t* sa, int64_t ld_sa, int fm
     RET(map_output(j, cg));
     j.st = new_call(*st);
     LAUNCH(kClsFp8Gemm, launch_fp8_gemm(j, cg, st->num_sms, s));
+    if (j.split > 1) LAUNCH(kClsFp8Gemm, launch_fp8_reduce(j, s));
     return GNS_OK;
 }
 
@@ -202,8 +203,9 @@ int gns_moe_sort(const void* experts, int id_bytes, int tokens, int topk, int nu
     if (const size_t bytes = moe_sort_scratch(j.n, num_experts)) {
         RET(scratch.take(*st, bytes, s));
         j.hist = reinterpret_cast<int*>(scratch.data());
+        LAUNCH(kClsMoe, launch_moe_count(j, s));
     }
-    LAUNCH(kClsMoe, launch_moe_sort(j, s));
+    LAUNCH(kClsMoe, launch_moe_place(j, s));
     return GNS_OK;
 }
 
@@ -296,7 +298,10 @@ int gns_fp8_quantize(const void* x, int64_t ldx, int dtype, int rows, int cols, 
     j.ld_cols = ld_cols;
     j.lds_cols = ld_scale_cols;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-    LAUNCH(kClsFp8Cast, launch_fp8_cast(j, st->num_sms, s));
+    // Without groups there are at most 65535 token blocks, the limit of a launch;
+    // groups may add one each.
+    const int blocks = fp8_cast_blocks(j);
+    for (; j.block0 < blocks; j.block0 += kFp8CastBlocks) LAUNCH(kClsFp8Cast, launch_fp8_cast(j, st->num_sms, s));
     return GNS_OK;
 }
 

@@ -39,9 +39,12 @@ struct CastJob {
     uint8_t* q_cols;
     uint8_t* s_cols;
     long long ld_cols, lds_cols;
-    int block0;  // first token block of a launch (set by the launcher)
+    int block0;  // first token block of the launch
 };
 
+// Token blocks of the cast (with offsets, an upper bound), and those that one launch takes.
+int fp8_cast_blocks(const CastJob& job);
+constexpr int kFp8CastBlocks = 65535;
 int launch_fp8_cast(const CastJob& job, int num_sms, cudaStream_t s);
 
 // The cast of G matrices of rows x cols in blocks of 128 x 128.
@@ -99,6 +102,8 @@ int fp8_gemm_cg(int M, int N, bool grouped, bool forward, int out_dtype, int num
 inline int fp8_gemm_b_box(int cg, bool b_mn) { return b_mn || cg == 2 ? 128 : 256; }
 
 int launch_fp8_gemm(const Fp8GemmJob& job, int cg, int num_sms, cudaStream_t s);
+// The sum over the parts of a split contraction, after launch_fp8_gemm.
+int launch_fp8_reduce(const Fp8GemmJob& job, cudaStream_t s);
 
 // Bytes of intermediate memory for a 16-bit result whose contraction (an upper
 // bound of it) is longer than the tensor core's accumulator sums alone: a tile's

@@ -32,7 +32,6 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kPasses = 8;   // 16 rows each; a thread owns 8 columns of one row per pass
 constexpr int kWarps = kThreads / 32;
-constexpr int kMaxGrid = 65535;  // blocks in the grid's second dimension
 
 enum CastMode { kRowForm = 1, kColForm = 2, kBothForms = 3, kBlockForm = 4 };
 
@@ -533,35 +532,32 @@ template <typename T, bool E5M2>
 int cast_typed(const CastJob& j, int num_sms, cudaStream_t s) {
     const bool vec = (reinterpret_cast<uintptr_t>(j.x) & 15) == 0 && j.ldx * static_cast<int>(sizeof(T)) % 16 == 0;
     const int nblk = (j.cols + kFp8Block - 1) / kFp8Block;
-    const int tblk = j.offsets ? fp8_max_blocks(j.rows, j.G) : (j.rows + kFp8Block - 1) / kFp8Block;
+    const int tblk = fp8_cast_blocks(j);
     // With groups a block looks its token block up first, so it takes several
     // column blocks then, as long as that leaves about sixteen blocks per SM.
     int span = 1;
     if (j.offsets)
         while (span < 8 && static_cast<long long>(tblk) * ((nblk + 2 * span - 1) / (2 * span)) >= 16LL * num_sms) span *= 2;
-    // Without groups there are at most 65535 token blocks, the grid's limit; groups
-    // may add one each, and a second launch takes those beyond. (A third grid
-    // dimension instead costs the kernel of both forms the registers it has not:
-    // spills, 92 us instead of 88 for the gathered cast above.)
-    auto run = [&](auto k) {
-        CastJob part = j;
-        for (part.block0 = 0; part.block0 < tblk; part.block0 += kMaxGrid) {
-            const dim3 grid((nblk + span - 1) / span, std::min(tblk - part.block0, kMaxGrid));
-            const cudaError_t e = launch_after(k, grid, dim3(kThreads), 0, s, part, vec, span);
-            if (e != cudaSuccess) return static_cast<int>(e);
-            if (part.q_cols) {
-                part.q_cols += static_cast<long long>(kMaxGrid) * kFp8Block * j.ld_cols;
-                part.s_cols += static_cast<long long>(kMaxGrid) * j.lds_cols;
-            }
-        }
-        return static_cast<int>(cudaSuccess);
-    };
+    // Later token blocks than a launch takes: the column form begins there. (A
+    // third grid dimension instead costs the kernel of both forms registers that
+    // it has not: spills, 92 us instead of 88 for the gathered cast above.)
+    CastJob part = j;
+    if (part.q_cols) {
+        part.q_cols += static_cast<long long>(j.block0) * kFp8Block * j.ld_cols;
+        part.s_cols += static_cast<long long>(j.block0) * j.lds_cols;
+    }
+    const dim3 grid((nblk + span - 1) / span, std::min(tblk - j.block0, kFp8CastBlocks));
+    auto run = [&](auto k) { return static_cast<int>(launch_after(k, grid, dim3(kThreads), 0, s, part, vec, span)); };
     if (j.q_rows && j.q_cols) return run(fp8_cast_kernel<T, kBothForms, E5M2>);
     if (j.q_rows) return run(fp8_cast_kernel<T, kRowForm, E5M2>);
     return run(fp8_cast_kernel<T, kColForm, E5M2>);
 }
 
 }  // namespace
+
+int fp8_cast_blocks(const CastJob& j) {
+    return j.offsets ? fp8_max_blocks(j.rows, j.G) : (j.rows + kFp8Block - 1) / kFp8Block;
+}
 
 int launch_fp8_cast(const CastJob& j, int num_sms, cudaStream_t s) {
     return by_dtype(j.dtype, [&](auto t) {

@@ -1022,7 +1022,7 @@ int launch_fp8_gemm(const Fp8GemmJob& job, int cg, int num_sms, cudaStream_t s) 
     if (tiles <= 0) return cudaSuccess;
     if (!job.carry && fp8_carry_bytes(job.wgrad ? job.rows : job.K, job.out_dtype, job.split, num_sms))
         return cudaErrorInvalidValue;
-    const int e = by_dtype(job.split > 1 ? static_cast<int>(GNS_FP32) : job.out_dtype, [&](auto t) {
+    return by_dtype(job.split > 1 ? static_cast<int>(GNS_FP32) : job.out_dtype, [&](auto t) {
         using T = decltype(t);
         if (job.wgrad) {
             if constexpr (sizeof(T) == 4)
@@ -1031,7 +1031,9 @@ int launch_fp8_gemm(const Fp8GemmJob& job, int cg, int num_sms, cudaStream_t s) 
         }
         return cg == 2 ? launch_variant<2, T, false>(job, tiles, num_sms, s) : launch_variant<1, T, false>(job, tiles, num_sms, s);
     });
-    if (e != cudaSuccess || job.split <= 1) return e;
+}
+
+int launch_fp8_reduce(const Fp8GemmJob& job, cudaStream_t s) {
     const int v = job.N % 4 == 0 ? 4 : 1;
     const dim3 grid((job.N + 128 * v - 1) / (128 * v), std::min(job.rows, 65535));
     return by_dtype(job.out_dtype, [&](auto t) {

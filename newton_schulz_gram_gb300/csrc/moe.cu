@@ -176,28 +176,26 @@ __global__ void __launch_bounds__(kSortThreads) moe_place_kernel(const I* ids, l
     }
 }
 
-template <typename I>
-int sort_typed(const SortJob& j, cudaStream_t s) {
+template <typename... KArgs, typename... Args>
+int sort_step(void (*kernel)(KArgs...), const SortJob& j, cudaStream_t s, Args... args) {
     const size_t smem = sort_smem(j.G);
-    const long long blocks = sort_blocks(j.n), span = sort_span(j.n);
-    const I* ids = static_cast<const I*>(j.ids);
     if (smem > 48 * 1024) {
-        for (const void* k : {reinterpret_cast<const void*>(moe_count_kernel<I>),
-                              reinterpret_cast<const void*>(moe_place_kernel<I>)}) {
-            const cudaError_t e =
-                cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
-            if (e != cudaSuccess) return e;
-        }
-    }
-    const int* hist = nullptr;
-    if (blocks > 1) {
-        const cudaError_t e = launch_after(moe_count_kernel<I>, dim3(static_cast<unsigned>(blocks)),
-                                           dim3(kSortThreads), smem, s, ids, j.n, j.G, span, j.hist);
+        const cudaError_t e =
+            cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
         if (e != cudaSuccess) return e;
-        hist = j.hist;
     }
-    return launch_after(moe_place_kernel<I>, dim3(static_cast<unsigned>(blocks)), dim3(kSortThreads), smem, s, ids, j.n,
-                        j.G, span, hist, j.offsets, j.rows, j.slots);
+    return launch_after(kernel, dim3(static_cast<unsigned>(sort_blocks(j.n))), dim3(kSortThreads), smem, s, args...);
+}
+
+template <typename I>
+int count_typed(const SortJob& j, cudaStream_t s) {
+    return sort_step(moe_count_kernel<I>, j, s, static_cast<const I*>(j.ids), j.n, j.G, sort_span(j.n), j.hist);
+}
+
+template <typename I>
+int place_typed(const SortJob& j, cudaStream_t s) {
+    return sort_step(moe_place_kernel<I>, j, s, static_cast<const I*>(j.ids), j.n, j.G, sort_span(j.n),
+                     static_cast<const int*>(j.hist), j.offsets, j.rows, j.slots);
 }
 
 // --------------------------------------------------------- moves over tokens
@@ -457,8 +455,12 @@ size_t moe_sort_scratch(long long n, int G) {
     return b > 1 ? sizeof(int) * static_cast<size_t>(b) * (G + 1) : 0;
 }
 
-int launch_moe_sort(const SortJob& j, cudaStream_t s) {
-    return j.id_bytes == 8 ? sort_typed<long long>(j, s) : sort_typed<int>(j, s);
+int launch_moe_count(const SortJob& j, cudaStream_t s) {
+    return j.id_bytes == 8 ? count_typed<long long>(j, s) : count_typed<int>(j, s);
+}
+
+int launch_moe_place(const SortJob& j, cudaStream_t s) {
+    return j.id_bytes == 8 ? place_typed<long long>(j, s) : place_typed<int>(j, s);
 }
 
 int launch_moe_gather(const RouteJob& j, const void* x, long long ldx, void* y, long long ldy, cudaStream_t s) {

@@ -27,7 +27,9 @@ struct SortJob {
 };
 
 size_t moe_sort_scratch(long long n, int G);
-int launch_moe_sort(const SortJob& job, cudaStream_t s);
+// Two kernels where there is scratch, the counts and the places, else the latter alone.
+int launch_moe_count(const SortJob& job, cudaStream_t s);
+int launch_moe_place(const SortJob& job, cudaStream_t s);
 
 struct RouteJob {
     int tokens, topk, G, H;
