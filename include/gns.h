@@ -264,8 +264,9 @@ int gns_symm_gemm(const void* A, const void* B, const void* C, void* D, int G, i
  * their columns. Sums are fp32 and each result is rounded once to its type.
  * Calls are asynchronous and write only what they name. Those that need
  * intermediate memory (gns_moe_sort beyond 4096 slots, gns_fp8_linear, products
- * of few rows) take it in the order of their stream, from a memory pool of the
- * library or, in a stream capture, as the graph's own: none of these operators
+ * of few rows or with a long contraction) take it in the order of their stream,
+ * from a memory pool of the library, which keeps a buffer for each of 16
+ * streams, or, in a stream capture, as the graph's own: none of these operators
  * uses the workspace of the entry points above, so they may overlap each other
  * and anything else on other streams, and a captured one stays valid.
  */

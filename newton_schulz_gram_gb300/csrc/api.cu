@@ -144,29 +144,44 @@ int ensure_workspace(DeviceState& st, size_t bytes) {
     return GNS_OK;
 }
 
-int Scratch::take(DeviceState& st, size_t bytes, cudaStream_t s) {
-    cudaMemPool_t pool;
-    {
-        std::lock_guard<std::mutex> lk(g_mu);
-        if (!st.scratch) {
-            OutsideCapture relaxed;
-            cudaMemPoolProps props = {};
-            props.allocType = cudaMemAllocationTypePinned;
-            props.location.type = cudaMemLocationTypeDevice;
-            props.location.id = st.device;
-            cudaMemPool_t made = nullptr;
-            CK(cudaMemPoolCreate(&made, &props));
-            // Freed memory stays with the pool until gns_release().
-            uint64_t keep = ~uint64_t(0);
-            const cudaError_t e = cudaMemPoolSetAttribute(made, cudaMemPoolAttrReleaseThreshold, &keep);
-            if (e != cudaSuccess) {
-                cudaMemPoolDestroy(made);
-                return cuda_fail(e, "cudaMemPoolSetAttribute");
-            }
-            st.scratch = made;
-        }
-        pool = st.scratch;
+struct ScratchSlot {
+    std::mutex mu;
+    char* p = nullptr;
+    size_t bytes = 0;
+};
+
+namespace {
+
+struct ScratchPool {
+    cudaMemPool_t pool = nullptr;
+    std::map<unsigned long long, ScratchSlot> slots;  // by stream id, which no later stream gets again
+};
+std::map<int, ScratchPool> g_scratch;  // by device, under g_mu
+
+// Streams whose buffers are kept; a program that uses more of them pays for an
+// allocation per call on the others.
+constexpr size_t kMaxScratchSlots = 16;
+
+int make_pool(int device, cudaMemPool_t* out) {
+    OutsideCapture relaxed;
+    cudaMemPoolProps props = {};
+    props.allocType = cudaMemAllocationTypePinned;
+    props.location.type = cudaMemLocationTypeDevice;
+    props.location.id = device;
+    cudaMemPool_t made = nullptr;
+    CK(cudaMemPoolCreate(&made, &props));
+    // Freed memory stays with the pool until gns_release().
+    uint64_t keep = ~uint64_t(0);
+    const cudaError_t e = cudaMemPoolSetAttribute(made, cudaMemPoolAttrReleaseThreshold, &keep);
+    if (e != cudaSuccess) {
+        cudaMemPoolDestroy(made);
+        return cuda_fail(e, "cudaMemPoolSetAttribute");
     }
+    *out = made;
+    return GNS_OK;
+}
+
+int pool_alloc(cudaMemPool_t pool, size_t bytes, cudaStream_t s, char** out) {
     void* p = nullptr;
     const cudaError_t e = cudaMallocFromPoolAsync(&p, bytes, pool, s);
     if (e == cudaErrorMemoryAllocation) {
@@ -174,13 +189,79 @@ int Scratch::take(DeviceState& st, size_t bytes, cudaStream_t s) {
         return fail(GNS_ERR_NOMEM, "scratch allocation of " + std::to_string(bytes) + " bytes failed");
     }
     if (e != cudaSuccess) return cuda_fail(e, "cudaMallocFromPoolAsync");
-    p_ = static_cast<char*>(p);
-    s_ = s;
+    *out = static_cast<char*>(p);
     return GNS_OK;
 }
 
+}  // namespace
+
+int Scratch::take(DeviceState& st, size_t bytes, cudaStream_t s) {
+    cudaStreamCaptureStatus capture = cudaStreamCaptureStatusNone;
+    CK(cudaStreamIsCapturing(s, &capture));
+    const bool captured = capture != cudaStreamCaptureStatusNone;
+    unsigned long long id = 0;
+    if (!captured) CK(cudaStreamGetId(s, &id));
+    cudaMemPool_t pool;
+    ScratchSlot* slot = nullptr;
+    {
+        std::lock_guard<std::mutex> lk(g_mu);
+        ScratchPool& sp = g_scratch[st.device];
+        if (!sp.pool) RET(make_pool(st.device, &sp.pool));
+        pool = sp.pool;
+        if (!captured) {
+            const auto it = sp.slots.find(id);
+            if (it != sp.slots.end())
+                slot = &it->second;
+            else if (sp.slots.size() < kMaxScratchSlots)
+                slot = &sp.slots[id];
+        }
+    }
+    s_ = s;
+    if (!slot) return pool_alloc(pool, bytes, s, &p_);
+    slot->mu.lock();
+    slot_ = slot;
+    if (slot->bytes < bytes) {
+        if (slot->p) {
+            const cudaError_t e = cudaFreeAsync(slot->p, s);
+            slot->p = nullptr;
+            slot->bytes = 0;
+            if (e != cudaSuccess) return cuda_fail(e, "cudaFreeAsync");
+        }
+        const size_t want = align_up(bytes, size_t(1) << 20);
+        RET(pool_alloc(pool, want, s, &slot->p));
+        slot->bytes = want;
+    }
+    p_ = slot->p;
+    return GNS_OK;
+}
+
+// Frees the streams' buffers of a device whose work is done. The slots stay, so
+// that none vanishes under a call that waits for it.
+static void release_scratch(int device) {
+    cudaMemPool_t pool = nullptr;
+    std::vector<ScratchSlot*> slots;
+    {
+        std::lock_guard<std::mutex> lk(g_mu);
+        const auto it = g_scratch.find(device);
+        if (it == g_scratch.end() || !it->second.pool) return;
+        pool = it->second.pool;
+        for (auto& s : it->second.slots) slots.push_back(&s.second);
+    }
+    for (ScratchSlot* s : slots) {
+        std::lock_guard<std::mutex> lk(s->mu);
+        if (s->p) cudaFreeAsync(s->p, cudaStreamLegacy);
+        s->p = nullptr;
+        s->bytes = 0;
+    }
+    cudaStreamSynchronize(cudaStreamLegacy);
+    cudaMemPoolTrimTo(pool, 0);
+}
+
 Scratch::~Scratch() {
-    if (p_) cudaFreeAsync(p_, s_);
+    if (slot_)
+        slot_->mu.unlock();
+    else if (p_)
+        cudaFreeAsync(p_, s_);
 }
 
 namespace {
@@ -1618,8 +1699,9 @@ int64_t gns_workspace_bytes(void) {
     auto it = g_dev.find(dev);
     if (it == g_dev.end()) return 0;
     uint64_t scratch = 0;
-    if (it->second.scratch &&
-        cudaMemPoolGetAttribute(it->second.scratch, cudaMemPoolAttrReservedMemCurrent, &scratch) != cudaSuccess) {
+    const auto sp = g_scratch.find(dev);
+    if (sp != g_scratch.end() && sp->second.pool &&
+        cudaMemPoolGetAttribute(sp->second.pool, cudaMemPoolAttrReservedMemCurrent, &scratch) != cudaSuccess) {
         cudaGetLastError();
         scratch = 0;
     }
@@ -1632,12 +1714,12 @@ void gns_release(void) {
         cudaGetLastError();
         return;
     }
+    cudaDeviceSynchronize();
+    release_scratch(dev);
     std::lock_guard<std::mutex> lk(g_mu);
     auto it = g_dev.find(dev);
     if (it == g_dev.end()) return;
-    cudaDeviceSynchronize();
     if (it->second.ws) cudaFree(it->second.ws);
-    if (it->second.scratch) cudaMemPoolTrimTo(it->second.scratch, 0);
     if (it->second.stage) cudaFree(it->second.stage);
     it->second.ws = nullptr;
     it->second.ws_bytes = 0;

@@ -91,10 +91,18 @@ int check_moves(int tokens, int topk, int num_experts, int cols, int dtype, cons
     return GNS_OK;
 }
 
+// Intermediate memory of such a product: the parts of a split contraction or the carried sums of a long one.
+size_t product_scratch(int rows, int inner, int out, bool grouped, int out_dtype, int num_sms) {
+    const int split = grouped ? 1 : fp8_gemm_split(rows, out, inner, num_sms);
+    return split > 1 ? sizeof(float) * static_cast<size_t>(split) * rows * out
+                     : fp8_carry_bytes(inner, out_dtype, split, num_sms);
+}
+
 // The forward and the data-gradient product: A [rows][inner_a], D [rows][n_out].
+// scratch: product_scratch() bytes.
 int product(const void* a, int64_t lda, const uint8_t* sa, int64_t ld_sa, int fmt_a, int rows, const void* w, int64_t ldw,
             const uint8_t* sw, int fmt_w, int groups, int N, int K, bool dgrad, const int32_t* offsets, void* D,
-            int64_t ldd, int out_dtype, DeviceState* st, cudaStream_t s) {
+            int64_t ldd, int out_dtype, DeviceState* st, char* scratch, cudaStream_t s) {
     const int inner = dgrad ? N : K, out = dgrad ? K : N;
     RET(check_q(a, inner, lda));
     RET(check_q(w, K, ldw));
@@ -124,15 +132,8 @@ int product(const void* a, int64_t lda, const uint8_t* sa, int64_t ld_sa, int fm
     j.D = D;
     j.ldd = ldd;
     j.out_dtype = out_dtype;
-    Scratch partial, carry;
-    if (j.split > 1) {
-        RET(partial.take(*st, sizeof(float) * static_cast<size_t>(j.split) * rows * out, s));
-        j.partial = reinterpret_cast<float*>(partial.data());
-    }
-    if (const size_t bytes = fp8_carry_bytes(inner, out_dtype, j.split, st->num_sms)) {
-        RET(carry.take(*st, bytes, s));
-        j.carry = reinterpret_cast<float*>(carry.data());
-    }
+    // One of the two at most, in product_scratch() bytes.
+    (j.split > 1 ? j.partial : j.carry) = reinterpret_cast<float*>(scratch);
     RET(map_output(j, cg));
     j.st = new_call(*st);
     LAUNCH(kClsFp8Gemm, launch_fp8_gemm(j, cg, st->num_sms, s));
@@ -329,8 +330,12 @@ int gns_fp8_matmul(const void* a, int64_t lda, const uint8_t* scale_a, int64_t l
     if (rows == 0) return GNS_OK;
     DeviceState* st = nullptr;
     RET(get_state(&st));
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    Scratch scratch;
+    if (const size_t bytes = product_scratch(rows, K, N, offsets != nullptr, out_dtype, st->num_sms))
+        RET(scratch.take(*st, bytes, s));
     return product(a, lda, scale_a, ld_scale_a, format_a, rows, w, ldw, scale_w, format_w, groups, N, K, false, offsets,
-                   y, ldy, out_dtype, st, static_cast<cudaStream_t>(stream));
+                   y, ldy, out_dtype, st, scratch.data(), s);
 }
 
 int gns_fp8_matmul_dgrad(const void* dy, int64_t lddy, const uint8_t* scale_dy, int64_t ld_scale_dy, int format_dy,
@@ -340,8 +345,12 @@ int gns_fp8_matmul_dgrad(const void* dy, int64_t lddy, const uint8_t* scale_dy, 
     if (rows == 0) return GNS_OK;
     DeviceState* st = nullptr;
     RET(get_state(&st));
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    Scratch scratch;
+    if (const size_t bytes = product_scratch(rows, N, K, offsets != nullptr, out_dtype, st->num_sms))
+        RET(scratch.take(*st, bytes, s));
     return product(dy, lddy, scale_dy, ld_scale_dy, format_dy, rows, w, ldw, scale_w, format_w, groups, N, K, true,
-                   offsets, dx, lddx, out_dtype, st, static_cast<cudaStream_t>(stream));
+                   offsets, dx, lddx, out_dtype, st, scratch.data(), s);
 }
 
 int gns_fp8_matmul_wgrad(const void* dy, int64_t lddy, const uint8_t* scale_dy, int64_t ld_scale_dy, int format_dy,
@@ -425,13 +434,13 @@ int gns_fp8_linear(const void* x, int64_t ldx, int dtype, int rows, const int32_
     const int64_t ldq = std::max(up(K, 16), up((256 << 10) / rows, 128));
     const size_t q_bytes = static_cast<size_t>(up(ldq * rows, 256));
     const size_t s_bytes = static_cast<size_t>(up(up(K, kFp8Block) / kFp8Block * rows, 256));
-    Scratch cast;
-    RET(cast.take(*st, q_bytes + s_bytes, s));
-    uint8_t* scale = reinterpret_cast<uint8_t*>(cast.data() + q_bytes);
-    RET(gns_fp8_quantize(x, ldx, dtype, rows, K, slots, topk, nullptr, 1, GNS_E4M3, cast.data(), ldq, scale, rows, nullptr,
-                         0, nullptr, 0, stream));
-    return product(cast.data(), ldq, scale, rows, GNS_E4M3, rows, w, ldw, scale_w, format_w, groups, N, K, false, offsets,
-                   y, ldy, out_dtype, st, s);
+    Scratch scratch;
+    RET(scratch.take(*st, q_bytes + s_bytes + product_scratch(rows, K, N, offsets != nullptr, out_dtype, st->num_sms), s));
+    uint8_t* scale = reinterpret_cast<uint8_t*>(scratch.data() + q_bytes);
+    RET(gns_fp8_quantize(x, ldx, dtype, rows, K, slots, topk, nullptr, 1, GNS_E4M3, scratch.data(), ldq, scale, rows,
+                         nullptr, 0, nullptr, 0, stream));
+    return product(scratch.data(), ldq, scale, rows, GNS_E4M3, rows, w, ldw, scale_w, format_w, groups, N, K, false,
+                   offsets, y, ldy, out_dtype, st, scratch.data() + q_bytes + s_bytes, s);
 }
 
 }  // extern "C"

@@ -42,7 +42,6 @@ struct DeviceState {
     float* stage = nullptr;  // device staging for the host-buffer entry point
     size_t stage_bytes = 0;
     cudaStream_t h2d = nullptr, d2h = nullptr;  // copy streams of the host-buffer entry point
-    cudaMemPool_t scratch = nullptr;            // pool of Scratch
 };
 
 // State of the current device, created on first use.
@@ -55,11 +54,16 @@ DevStatus new_call(DeviceState& st);
 
 int ensure_workspace(DeviceState& st, size_t bytes);
 
-// Intermediate memory of one call, taken and given back in the order of the
-// call's stream: calls on other streams have their own, and a stream capture
-// makes it part of the graph, so no later call can free or overwrite it. (The
-// workspace above is one buffer per device that a larger call replaces.) From
-// the pool a call's two steps take the host 0.6 us.
+// Intermediate memory of one call, in the order of its stream; one per call.
+// Calls on other streams have their own, and in a stream capture it is part of
+// the graph, so no later call can free or overwrite it. (The workspace above is
+// one buffer per device that a larger call replaces.)
+// A stream's buffer stays for its next call, which cannot begin before this one
+// is done with it, and is locked from take() on, so that two threads that
+// launch on one stream do not mix their kernels. Allocating for every call
+// instead took the host 2 us of the 15 to 20 (48 rows through the fused layer,
+// alone: 44 us, 50 with two allocations).
+struct ScratchSlot;
 class Scratch {
 public:
     Scratch() = default;
@@ -71,6 +75,7 @@ public:
 
 private:
     char* p_ = nullptr;
+    ScratchSlot* slot_ = nullptr;  // locked; null for memory of this call alone
     cudaStream_t s_ = nullptr;
 };
 

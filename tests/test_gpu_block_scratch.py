@@ -4,6 +4,7 @@ the library does between the capture and a replay."""
 import os
 import subprocess
 import sys
+import threading
 
 import numpy as np
 import pytest
@@ -133,6 +134,7 @@ def test_captured_products_outlive_later_calls(gns):
 
 FIRST_CALLS = """
 import sys
+import threading
 import torch
 sys.path.insert(0, {root!r})
 import newton_schulz_gram_gb300 as gns
@@ -166,3 +168,43 @@ def test_the_first_calls_of_a_process_can_be_captured(gns):
     root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
     r = subprocess.run([sys.executable, "-c", FIRST_CALLS.format(root=root)], capture_output=True, text=True, timeout=300)
     assert r.returncode == 0 and r.stdout.strip() == "same", r.stdout + r.stderr
+
+
+def test_more_streams_than_kept_buffers(gns):
+    """Each stream with rows of its own through the same layer, and the buffers
+    released in between."""
+    gns.gns_release()
+    x, fs = layers(gns, 1)
+    streams = [torch.cuda.Stream() for _ in range(24)]
+    jobs = [x * (1 + i) for i in range(24)]
+    want = [fs[0](j, None) for j in jobs]
+    for _ in range(3):
+        torch.cuda.synchronize()
+        got = [fs[0](j, s) for j, s in zip(jobs, streams)]
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
+        assert gns.gns_workspace_bytes() > 0
+        gns.gns_release()
+        assert gns.gns_workspace_bytes() == 0
+
+
+def test_threads_that_share_a_stream(gns):
+    """The kernels of one call stay together although ctypes lets other threads run."""
+    stream = torch.cuda.Stream()
+    jobs = [layers(gns, i) for i in range(3)]
+    want = [fs[0](x, None) for x, fs in jobs]
+    torch.cuda.synchronize()
+    bad = []
+
+    def work(i):
+        x, fs = jobs[i]
+        outs = [fs[0](x, stream) for _ in range(60)]
+        stream.synchronize()
+        bad.extend(i for o in outs if not torch.equal(o, want[i]))
+
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(3)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert bad == []
