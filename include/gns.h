@@ -412,7 +412,9 @@ int gns_fp8_matmul_wgrad(const void* dy, int64_t lddy, const uint8_t* scale_dy, 
  * gns_fp8_quantize (e4m3, row form, row r read from x[slots[r] / topk]), then
  * gns_fp8_matmul. Up to eight rows of one matrix, as long as they fit shared
  * memory ((rows + 1) * K up to about 68,000), and up to 32 routed rows, as long
- * as their experts' weights are small, run as one kernel that casts on the way.
+ * as their experts' weights are small, run as one kernel that casts on the way
+ * and sums in another order than gns_fp8_matmul: a row's last bits depend on how
+ * many rows it comes with, as those of split contractions do.
  */
 int gns_fp8_linear(const void* x, int64_t ldx, int dtype, int rows, const int32_t* slots, int topk,
                    const int32_t* offsets, const void* w, int64_t ldw, const uint8_t* scale_w, int format_w, int groups,

@@ -42,8 +42,8 @@ __device__ __forceinline__ __nv_bfloat16 from_f32<__nv_bfloat16>(float v) {
     return __float2bfloat16_rn(v);
 }
 
-// N consecutive elements as they lie in memory, in 16-byte pieces. N
-// elements start on a 16-byte boundary (or on their own, for N == 1).
+// N consecutive elements as they lie in memory, in 16-byte pieces; they start on
+// a 16-byte boundary.
 template <typename T, int N>
 struct Pack {
     static constexpr int kPieces = N * static_cast<int>(sizeof(T)) / 16;
@@ -75,17 +75,6 @@ struct Pack {
 #pragma unroll
         for (int i = 0; i < N; ++i) e[i] = from_f32<T>(f[i]);
     }
-};
-
-template <typename T>
-struct Pack<T, 1> {
-    T v;
-    __device__ __forceinline__ void load(const T* a) { v = *a; }
-    __device__ __forceinline__ void load_stream(const T* a) { v = *a; }
-    __device__ __forceinline__ void store(T* a) const { *a = v; }
-    __device__ __forceinline__ void clear() { v = from_f32<T>(0.0f); }
-    __device__ __forceinline__ void get(float (&f)[1]) const { f[0] = to_f32<T>(v); }
-    __device__ __forceinline__ void set(const float (&f)[1]) { v = from_f32<T>(f[0]); }
 };
 
 // Launch with the programmatic-dependent-launch attribute: the kernel calls

@@ -15,7 +15,7 @@
 // Bound: HBM, 2 (3 with the residual) elements moved per element; about nine
 // integer instructions of Philox per element stay below that at 2 bytes. 2^26
 // bf16 elements: 59 us with the residual (6.8 TB/s), 48 without (5.6); 1021 x
-// 4093 unaligned fp32 ones 7.8 (4.3 TB/s, from L2).
+// 4093 unaligned fp32 ones 8.0 (4.2 TB/s, from L2).
 #include "blockops.cuh"
 #include "dropout.cuh"
 #include "philox.cuh"

@@ -74,7 +74,7 @@ __device__ __forceinline__ int blocks_of(int count) { return (count + kFp8Block 
 //   weight gradient (wgrad = 1): D[g][m][n], contraction the group's rows; A
 //     and B are column forms, [blocks * 128][M] and [blocks * 128][N].
 struct Fp8GemmJob {
-    CUtensorMap mapA, mapB, mapD;  // mapD: boxes of 32 rows of 128 bytes of the output (partial when split > 1)
+    CUtensorMap mapA, mapB, mapD;  // mapD: boxes of 32 rows of fp8_store_row() bytes of the output (partial when split > 1)
     int bulk_store;                // mapD holds (the output has 16-byte rows)
     int wgrad, b_mn;
     int fmt_a, fmt_b;

@@ -43,11 +43,11 @@
 // through the shared-memory descriptor; nothing is transposed in memory.
 //
 // Bound: the tensor cores for large matrices, HBM for many experts of few rows,
-// the latency of one tile for small ones. 8192 x 14336 x 4096: forward 302 us
-// (3.2 PFLOP/s, 0.85 of twice the measured bf16 rate), data gradient 331 (2.9),
-// weight gradient 347 (2.8). 256 experts of 512 x 2048, 65536 rows: 86, 100 and
-// 126 us (5.5 TB/s of operands and results, each once). One tile of one k block:
-// 4.7 us.
+// the latency of one tile for small ones. 8192 x 14336 x 4096: forward 295 us
+// (3.3 PFLOP/s, 0.87 of twice the measured bf16 rate), data gradient 327 (2.9),
+// weight gradient 331 (2.9). 256 experts of 512 x 2048, 65536 rows: 85, 96 and
+// 126 us (5.5 to 5.8 TB/s of operands and results, each once). One tile of one k
+// block: 4.7 us.
 #include <algorithm>
 
 #include "blockops.cuh"
@@ -281,7 +281,7 @@ __device__ __forceinline__ uint32_t add_bits(uint32_t a, uint32_t b) {
     return __float_as_uint(__uint_as_float(a) + __uint_as_float(b));
 }
 
-// Stores (or, with `add`, adds, fp32) a staged block of 32 rows of 128 bytes,
+// Stores (or, with `add`, adds, fp32) a staged block of 32 rows of 64 or 128 bytes,
 // asynchronously, clipped to the map's extents.
 __device__ __forceinline__ void bulk_store(const CUtensorMap* m, uint32_t src, int c0, int c1, int c2, bool add) {
     if (add)
@@ -297,11 +297,11 @@ __device__ __forceinline__ void bulk_store(const CUtensorMap* m, uint32_t src, i
     asm volatile("cp.async.bulk.commit_group;" ::: "memory");
 }
 
-// Writes a staged block (32 rows of 128 bytes, 16-byte piece index XOR row mod
-// 8), clipped to rows x left, to d (row stride ldd elements of ES bytes): a
-// store instruction covers four whole 128-byte lines where rows start on
-// 16-byte boundaries, and runs of neighbouring elements where they do not. With
-// `add` (fp32) the stored values are added to; a lane meets its own stores.
+// Writes a staged block (32 rows of ROW bytes, swizzled), clipped to rows x left,
+// to d (row stride ldd elements of ES bytes): a store instruction covers whole
+// 16-byte pieces of neighbouring rows where rows start on 16-byte boundaries, and
+// runs of neighbouring elements where they do not. With `add` (fp32) the stored
+// values are added to; a lane meets its own stores.
 template <int ES, int ROW>
 __device__ __noinline__ void store_rows(uint32_t stage, uint8_t* d, long long ldd, int rows, int left, bool aligned,
                                            bool add, int lane) {

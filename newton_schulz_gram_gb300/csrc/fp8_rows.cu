@@ -17,9 +17,9 @@
 // microseconds. The warps' sums are joined in a fixed order.
 // One row, 14336 x 4096: 15.2 us (3.9 TB/s; 28672 x 8192 46.7, 5.0); without
 // conversions and products, the loads alone, 11.9. Eight rows, whose fp16 forms
-// leave room for one block of threads per SM: 20.2. The
-// 8-bit mma.sync took 19.4 us for one row, a block of threads per strip without
-// the ring 15.6, and more of them, of eight warps, 17.0.
+// leave room for one block of threads per SM: 20.2. The 8-bit mma.sync took
+// 19.4 us for one row, a block of threads per strip without the ring 15.6, and
+// more of them, of eight warps, 17.0.
 #include <algorithm>
 
 #include "blockops.cuh"
@@ -317,10 +317,12 @@ bool fp8_rows_fit(int rows, int N, int K, int groups, bool grouped, int num_sms)
     // 2 to 5 TB/s (least where the warps are more than the k blocks, most where a
     // block walks over several strips); the tensor cores' kernel takes the cast
     // before it and a tile's k blocks one after another, and then streams
-    // faster. Measured, us, this and that: 256 experts of 512 x 2048, 8 rows 5.6
-    // and 13.0, 16 rows 9.8 and 13.1, 32 rows 14.8 and 13.4; of 2048 x 512, 8 rows
-    // 8.7 and 9.3, 16 rows 11.5 and 9.7; 16 of 4096 x 4096, 1 row 8.0 and 17.6, 4
-    // rows 21.8 and 17.9; 8 of 14336 x 4096, 2 rows 29.6 and 27.5, 8 rows 75 and 69.
+    // faster. Measured, us, this and that, weights from HBM: 256 experts of 512 x
+    // 2048, 8 rows 5.7 and 13.4, 16 rows 10.1 and 14.3, 32 rows 15.3 and 15.2; of
+    // 2048 x 512, 8 rows 8.7 and 9.7, 16 rows 11.7 and 10.2, 32 rows 17.1 and 14.0;
+    // 16 of 4096 x 4096, 1 row 8.1 and 18.1, 4 rows 22.3 and 22.4; 8 of 14336 x
+    // 4096, 2 rows 30.4 and 29.2, 8 rows 76.5 and 54.8. How many experts have rows
+    // is on the device: the rule takes one per row.
     const int strips = (N + kStrip - 1) / kStrip, nkb = (K + kFp8Block - 1) / kFp8Block;
     const int parts = std::min(rows, groups + (rows - 1) / rows_of_chunk(rows, K));
     const double megabytes = 1e-6 * parts * N * K;
@@ -331,7 +333,7 @@ int launch_fp8_rows(const Fp8RowsJob& j, int num_sms, cudaStream_t s) {
     const int strips = (j.N + kStrip - 1) / kStrip, nkb = (j.K + kFp8Block - 1) / kFp8Block;
     const int chunk = j.offsets ? rows_of_chunk(j.rows, j.K) : j.rows;
     // Two blocks per SM where two fit, whose products hide each other's waits
-    // (one row of 14336 x 4096: 15.8 us, one block per SM 19.9), with two slots if
+    // (one row of 14336 x 4096: 15.2 us, one block per SM 16.6), with two slots if
     // there is room and the walk is that long, else one. With groups, whose
     // number that have rows is on the device, enough blocks for two rounds if
     // all rows are of different groups.
