@@ -435,7 +435,10 @@ def _format(fmt):
 def gns_fp8_quantize(x, fmt="e4m3", route=None, gather=False, rows=True, cols=True, stream=None):
     """The 8-bit forms (Fp8Rows, Fp8Cols) of x, None for one not asked for. With
     a route the blocks of the column form start at each expert's first row: x
-    is in sorted order, or, with gather, in token order and sorted on the way."""
+    is in sorted order, or, with gather, in token order and sorted on the way;
+    blocks past the last expert's and, where both forms are made, rows of slots
+    without an expert are not written, and products with the same route do not
+    read them."""
     n, c, ldx = _matrix(x, "x")
     f = _format(fmt)
     if not rows and not cols:
@@ -587,7 +590,8 @@ def gns_fp8_matmul_wgrad(dy, x, route=None, out_dtype=torch.bfloat16, stream=Non
 def gns_fp8_linear(x, w, route=None, out_dtype=torch.bfloat16, stream=None):
     """x w^T as a serving program calls it: x ([tokens, K], bf16, fp16 or fp32) is
     cast on the way (and, with a route, gathered to its sorted rows: the result
-    is [tokens * topk, N] in sorted order)."""
+    is [tokens * topk, N] in sorted order). Few rows are summed in another order
+    than many."""
     rows, inner, ldx = _matrix(x, "x")
     groups, n, k = _weight_args(w, route)
     if inner != k:
