@@ -111,7 +111,7 @@ int launch_fp8_reduce(const Fp8GemmJob& job, cudaStream_t s);
 constexpr int kFp8LongBlocks = 256;  // blocks of 128 along the contraction (see fp8_gemm.cu)
 inline size_t fp8_carry_bytes(long long contraction, int out_dtype, int split, int num_sms) {
     const bool carries = elem_bytes(out_dtype) == 2 && split <= 1 && contraction > kFp8LongBlocks * kFp8Block;
-    return carries ? sizeof(float) * 128 * 256 * num_sms : 0;
+    return carries ? sizeof(float) * 128 * 256 * (num_sms > 1 ? num_sms : 2) : 0;  // a pair is launched whole
 }
 
 // The split of the contraction that fills the machine, 1 for none.

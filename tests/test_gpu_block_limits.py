@@ -1,4 +1,8 @@
 """The training-block operators at the largest sizes that their entries accept."""
+import os
+import subprocess
+import sys
+
 import pytest
 
 torch = pytest.importorskip("torch")
@@ -70,3 +74,26 @@ def test_16_bit_results_of_the_longest_contraction(gns, dtype, experts):
         error = ((dw[e].double() - exact).abs() / exact).max().item()
         assert error <= torch.finfo(dtype).eps / 2 + 2048 * 2.0 ** -23, (e, error)
         block += n
+
+
+ONE_SM = """
+import sys
+import torch
+sys.path.insert(0, {root!r})
+import newton_schulz_gram_gb300 as gns
+x, w = torch.rand(300, 33000, device="cuda"), torch.rand(8200, 33000, device="cuda")
+a, b = gns.gns_fp8_quantize(x, cols=False)[0], gns.gns_fp8_quantize_weight(w)
+exact = gns.gns_fp8_matmul(a, b, out_dtype=torch.float32)
+got = gns.gns_fp8_matmul(a, b).float()
+assert ((got - exact).abs() <= (2.0 ** -8 + 2048 * 2.0 ** -23) * exact).all()
+assert gns.gns_get_status() == 0
+print("near")
+"""
+
+
+def test_long_contraction_on_a_share_of_one_sm(gns):
+    """A pair of CTAs is launched whole, and each has its own part of the carried sums."""
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", ONE_SM.format(root=root)], capture_output=True, text=True, timeout=300,
+                       env=dict(os.environ, GNS_NUM_SMS="1"))
+    assert r.returncode == 0 and r.stdout.strip() == "near", r.stdout + r.stderr
