@@ -420,6 +420,34 @@ int gns_fp8_linear(const void* x, int64_t ldx, int dtype, int rows, const int32_
                    const int32_t* offsets, const void* w, int64_t ldw, const uint8_t* scale_w, int format_w, int groups,
                    int N, int K, void* y, int64_t ldy, int out_dtype, void* stream);
 
+/* ---------------------------------------------------------------------------
+ * Operators around such a block, in the same manner: layer norm.
+ */
+
+/*
+ * gns_layer_norm: each of `rows` rows of cols elements (up to 2^24),
+ *   y = (x - mean) * rstd * weight + bias, rstd = 1 / sqrt(var + eps),
+ * var the mean of (x - mean)^2; with rms != 0 the mean is taken as 0 (the
+ * root-mean-square form). The squares are fp32: deviations beyond 1e19 overflow.
+ *   weight, bias  [cols], fp32 or of x's type (weight_dtype), NULL for 1 and 0.
+ *   stats         fp32 [rows][2], written: mean and rstd, for the backward pass.
+ */
+int gns_layer_norm(const void* x, int64_t ldx, int64_t rows, int cols, int dtype, const void* weight, const void* bias,
+                   int weight_dtype, double eps, int rms, void* y, int64_t ldy, float* stats, void* stream);
+
+/*
+ * gns_layer_norm_backward: with h = (x - mean) rstd and g = weight dy,
+ *   dx = residual + rstd (g - mean(g) - h mean(g h)), without mean(g) where rms,
+ *   dweight = sum over the rows of dy h, dbias = sum over the rows of dy.
+ *   residual        the gradient that reaches x past the norm, NULL for 0.
+ *   dweight, dbias  [cols] of weight_dtype, NULL where not wanted; fp32 sums in an
+ *                   order that the sizes and the number of SMs give, rounded once.
+ *                   They take intermediate memory.
+ */
+int gns_layer_norm_backward(const void* dy, int64_t lddy, const void* x, int64_t ldx, const float* stats, int64_t rows,
+                            int cols, int dtype, const void* weight, int weight_dtype, int rms, const void* residual,
+                            int64_t ldr, void* dx, int64_t lddx, void* dweight, void* dbias, void* stream);
+
 /* Synchronizes `stream`, returns the device status word of the current device
  * as a gns_status (GNS_OK, GNS_ERR_NONFINITE or GNS_ERR_TIMEOUT) and clears it.
  * It reads both the allocating entry points' word and, once the
@@ -464,9 +492,10 @@ void gns_profile_enable(int on);
  * (ms[k]) since the previous read; then forgets them. Classes: 0 tcgen05
  * GEMM, 1 norm + scale + cast to fp16 (with the momentum update inside
  * muon_step), 2 Muon elementwise (update / write-back, standalone momentum),
- * 3 output copy, 4 8-bit products, 5 8-bit casts, 6 expert routing, 7 dropout.
- * Writes min(max_classes, 8) entries of each non-null array and returns the
- * number of classes (8), or a negative gns_status. */
+ * 3 output copy, 4 8-bit products, 5 8-bit casts, 6 expert routing, 7 dropout,
+ * 8 layer norm, 9 embedding.
+ * Writes min(max_classes, 10) entries of each non-null array and returns the
+ * number of classes (10), or a negative gns_status. */
 int gns_profile_read(int64_t* counts, double* ms, int max_classes);
 
 /* Workspace bytes currently held on the current device, and those its pool of

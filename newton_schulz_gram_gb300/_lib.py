@@ -54,6 +54,9 @@ PROTOTYPES = {
     "gns_fp8_matmul_wgrad": (_i, [_vp, _i64, _vp, _i64, _i, _vp, _i64, _vp, _i64, _i, _i, _i, _i, _i, _vp, _vp, _i64,
                                   _i64, _i, _vp]),
     "gns_fp8_linear": (_i, [_vp, _i64, _i, _i, _vp, _i, _vp, _vp, _i64, _vp, _i, _i, _i, _i, _vp, _i64, _i, _vp]),
+    "gns_layer_norm": (_i, [_vp, _i64, _i64, _i, _i, _vp, _vp, _i, _d, _i, _vp, _i64, _vp, _vp]),
+    "gns_layer_norm_backward": (_i, [_vp, _i64, _vp, _i64, _vp, _i64, _i, _i, _vp, _i, _i, _vp, _i64, _vp, _i64, _vp, _vp,
+                                     _vp]),
     "gns_get_status": (_i, [_vp]),
     "gns_test_bounded_wait": (_i, [_i, _i64, _vp]),
     "gns_status_string": (ctypes.c_char_p, [_i]),

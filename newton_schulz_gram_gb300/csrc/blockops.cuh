@@ -77,6 +77,58 @@ struct Pack {
     }
 };
 
+// Pieces: what a thread owns of a row of H elements, 16 bytes of it where rows are
+// 16-byte aligned. Where they are not a piece is kLoose elements 32 apart, the
+// neighbouring lanes' next to them: single accesses, but whole lines per warp and
+// the piece's bookkeeping shared.
+constexpr int kLoose = 4;
+
+// Piece v of a row of H elements.
+template <typename T, int N>
+struct Wide {
+    static constexpr int kSize = N;
+    Pack<T, N> p;
+    __device__ __forceinline__ void load(const T* row, unsigned v, int) { p.load(row + static_cast<long long>(v) * N); }
+    __device__ __forceinline__ void load_stream(const T* row, unsigned v, int) {
+        p.load_stream(row + static_cast<long long>(v) * N);
+    }
+    __device__ __forceinline__ void store(T* row, unsigned v, int) const { p.store(row + static_cast<long long>(v) * N); }
+    __device__ __forceinline__ void clear() { p.clear(); }
+    __device__ __forceinline__ void get(float (&f)[N]) const { p.get(f); }
+    __device__ __forceinline__ void set(const float (&f)[N]) { p.set(f); }
+};
+
+template <typename T>
+struct Loose {
+    static constexpr int kSize = kLoose;
+    T e[kLoose];
+    static __device__ __forceinline__ int column(unsigned v, int i) {
+        return static_cast<int>((v >> 5) * (32 * kLoose) + (v & 31) + 32 * i);
+    }
+    __device__ __forceinline__ void load(const T* row, unsigned v, int H) {
+#pragma unroll
+        for (int i = 0; i < kLoose; ++i) e[i] = column(v, i) < H ? row[column(v, i)] : from_f32<T>(0.0f);
+    }
+    __device__ __forceinline__ void load_stream(const T* row, unsigned v, int H) { load(row, v, H); }
+    __device__ __forceinline__ void store(T* row, unsigned v, int H) const {
+#pragma unroll
+        for (int i = 0; i < kLoose; ++i)
+            if (column(v, i) < H) row[column(v, i)] = e[i];
+    }
+    __device__ __forceinline__ void clear() {
+#pragma unroll
+        for (int i = 0; i < kLoose; ++i) e[i] = from_f32<T>(0.0f);
+    }
+    __device__ __forceinline__ void get(float (&f)[kLoose]) const {
+#pragma unroll
+        for (int i = 0; i < kLoose; ++i) f[i] = to_f32<T>(e[i]);
+    }
+    __device__ __forceinline__ void set(const float (&f)[kLoose]) {
+#pragma unroll
+        for (int i = 0; i < kLoose; ++i) e[i] = from_f32<T>(f[i]);
+    }
+};
+
 // Launch with the programmatic-dependent-launch attribute: the kernel calls
 // grid_dependency_wait() before it reads what an earlier grid wrote or
 // writes what an earlier grid may still read.
@@ -93,6 +145,10 @@ cudaError_t launch_after(void (*kernel)(KArgs...), dim3 grid, dim3 block, size_t
     cfg.attrs = attr;
     cfg.numAttrs = 1;
     return cudaLaunchKernelEx(&cfg, kernel, static_cast<KArgs>(args)...);
+}
+
+inline bool rows_aligned(const void* p, long long ld, long long rows, int es) {
+    return (reinterpret_cast<uintptr_t>(p) & 15) == 0 && (rows <= 1 || ld * es % 16 == 0);
 }
 
 inline int elem_bytes(int dtype) { return dtype == GNS_FP32 ? 4 : 2; }

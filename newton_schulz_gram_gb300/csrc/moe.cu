@@ -212,53 +212,6 @@ int place_typed(const SortJob& j, cudaStream_t s) {
 
 constexpr int kThreads = 256;
 constexpr int kJ = 8;  // places handled together
-constexpr int kLoose = 4;
-
-// Piece v of a row of H elements.
-template <typename T, int N>
-struct Wide {
-    static constexpr int kSize = N;
-    Pack<T, N> p;
-    __device__ __forceinline__ void load(const T* row, unsigned v, int) { p.load(row + static_cast<long long>(v) * N); }
-    __device__ __forceinline__ void load_stream(const T* row, unsigned v, int) {
-        p.load_stream(row + static_cast<long long>(v) * N);
-    }
-    __device__ __forceinline__ void store(T* row, unsigned v, int) const { p.store(row + static_cast<long long>(v) * N); }
-    __device__ __forceinline__ void clear() { p.clear(); }
-    __device__ __forceinline__ void get(float (&f)[N]) const { p.get(f); }
-    __device__ __forceinline__ void set(const float (&f)[N]) { p.set(f); }
-};
-
-template <typename T>
-struct Loose {
-    static constexpr int kSize = kLoose;
-    T e[kLoose];
-    static __device__ __forceinline__ int column(unsigned v, int i) {
-        return static_cast<int>((v >> 5) * (32 * kLoose) + (v & 31) + 32 * i);
-    }
-    __device__ __forceinline__ void load(const T* row, unsigned v, int H) {
-#pragma unroll
-        for (int i = 0; i < kLoose; ++i) e[i] = column(v, i) < H ? row[column(v, i)] : from_f32<T>(0.0f);
-    }
-    __device__ __forceinline__ void load_stream(const T* row, unsigned v, int H) { load(row, v, H); }
-    __device__ __forceinline__ void store(T* row, unsigned v, int H) const {
-#pragma unroll
-        for (int i = 0; i < kLoose; ++i)
-            if (column(v, i) < H) row[column(v, i)] = e[i];
-    }
-    __device__ __forceinline__ void clear() {
-#pragma unroll
-        for (int i = 0; i < kLoose; ++i) e[i] = from_f32<T>(0.0f);
-    }
-    __device__ __forceinline__ void get(float (&f)[kLoose]) const {
-#pragma unroll
-        for (int i = 0; i < kLoose; ++i) f[i] = to_f32<T>(e[i]);
-    }
-    __device__ __forceinline__ void set(const float (&f)[kLoose]) {
-#pragma unroll
-        for (int i = 0; i < kLoose; ++i) e[i] = from_f32<T>(f[i]);
-    }
-};
 
 struct Walk {
     unsigned long long pieces;  // tokens * per_row
@@ -425,10 +378,6 @@ __global__ void __launch_bounds__(kThreads) moe_combine_backward_kernel(Walk w, 
             }
         }
     }
-}
-
-bool rows_aligned(const void* p, long long ld, long long rows, int es) {
-    return (reinterpret_cast<uintptr_t>(p) & 15) == 0 && (rows <= 1 || ld * es % 16 == 0);
 }
 
 Walk make_walk(const RouteJob& j, bool vec) {

@@ -89,7 +89,9 @@ enum KernelClass {
     kClsFp8Cast = 5,
     kClsMoe = 6,
     kClsDropout = 7,
-    kNumCls = 8
+    kClsLayerNorm = 8,
+    kClsEmbedding = 9,
+    kNumCls = 10
 };
 
 // Accounting around one launch (see gns_launch_count, gns_profile_enable).

@@ -1,0 +1,173 @@
+"""Layer norm and its gradients on the GPU against the fp64 oracle: types,
+widths on every path, strides, both forms, rows that go wrong."""
+import numpy as np
+import pytest
+
+from oracle import layers as L
+
+torch = pytest.importorskip("torch")
+from block_helpers import DTYPES, assert_close, f64, strided  # noqa: E402
+
+pytestmark = pytest.mark.gpu
+
+# Roundings on the way to a row's statistics: a thread's elements one after the
+# other (at most 16 in registers, 32 of rows beyond them), five steps among
+# the lanes, up to 32 warps; the squares once more, and a few single operations.
+DEPTH = 80
+
+
+@pytest.fixture(scope="module")
+def gns():
+    import newton_schulz_gram_gb300 as m
+    from newton_schulz_gram_gb300 import build
+    build.build()
+    m.load()
+    yield m
+    assert m.gns_get_status() == 0
+
+
+def inputs(rows, cols, dtype, wdtype, bias, pad, seed):
+    rng = np.random.default_rng(seed)
+    x = strided(rows, cols, pad, dtype, rng, 2.0)
+    x += torch.from_numpy(rng.normal(size=(rows, 1))).to(dtype).cuda()
+    dy, res = strided(rows, cols, pad, dtype, rng), strided(rows, cols, 0, dtype, rng)
+    w = None if wdtype is None else torch.from_numpy(1 + 0.3 * rng.normal(size=cols)).to(wdtype).cuda()
+    b = torch.from_numpy(rng.normal(size=cols)).to(wdtype or torch.float32).cuda() if bias else None
+    return x, dy, res, w, b
+
+
+def check(gns, x, dy, res, w, b, rms, eps=1e-5):
+    rows, cols = x.shape
+    X, D = f64(x), f64(dy)
+    W = np.ones(cols) if w is None else f64(w)
+    want, h, mean, rstd = L.layer_norm(X, W, None if b is None else f64(b), eps, rms)
+    y, stats = gns.gns_layer_norm(x, w, b, eps=eps, rms=rms)
+    assert_close(y, want, (np.abs(h) + 1) * np.abs(W) + (0 if b is None else np.abs(f64(b))), DEPTH, "y")
+    assert_close(stats[:, 0], mean, np.abs(mean) / DEPTH + 1 / rstd, DEPTH, "mean")
+    assert_close(stats[:, 1], rstd, rstd, DEPTH, "rstd")
+    dx, dw, db = gns.gns_layer_norm_backward(dy, x, stats, w, bias=b is not None, rms=rms, residual=res)
+    ex, ew, eb = L.layer_norm_backward(D, X, W, eps, rms, None if res is None else f64(res))
+    # The backward pass takes h from the rounded mean: half a step of it is that much of a deviation.
+    herr = np.abs(h) + 1 + (np.abs(mean) * rstd)[:, None] / DEPTH
+    g = np.abs(D * W)
+    mag = rstd[:, None] * (g + g.mean(1, keepdims=True) + np.abs(h) * (g * herr).mean(1, keepdims=True)
+                           + herr * (g * np.abs(h)).mean(1, keepdims=True))
+    assert_close(dx, ex, mag + (0 if res is None else np.abs(f64(res)) / DEPTH), 2 * DEPTH, "dx")
+    # A thread's rows one after the other, at least 152 blocks of rows where there are as many; the blocks' sums.
+    sums = -(-rows // 152) + 60
+    if w is None:
+        assert dw is None
+    else:
+        assert dw.dtype == w.dtype
+        assert_close(dw, ew, (np.abs(D) * herr).sum(0), DEPTH + sums, "dweight")
+    if b is None:
+        assert db is None
+    else:
+        assert_close(db, eb, np.abs(D).sum(0), sums, "dbias")
+    return y, stats, dx, dw, db
+
+
+# One lane a row to a whole block; widths that are no whole pieces; beyond the registers.
+SHAPES = [(1, 1), (3, 1), (5, 7), (2, 8), (300, 16), (33, 24), (1, 4096), (257, 128), (70, 33), (513, 256), (300, 1024),
+          (130, 712), (40, 1021), (9, 14336), (4, 14343), (700, 2048)]
+LONG = [(3, 16392), (2, 40001), (5, 20000)]
+
+
+@pytest.mark.parametrize("dtype", list(DTYPES))
+@pytest.mark.parametrize("rows,cols", SHAPES + LONG)
+def test_types_and_widths(gns, rows, cols, dtype):
+    for k, (rms, wdtype, bias, pad, with_res) in enumerate([(False, DTYPES[dtype], True, 0, True), (True, torch.float32, False, 0, False),
+                                                            (False, torch.float32, True, 3, False), (True, None, True, 8, True)]):
+        x, dy, res, w, b = inputs(rows, cols, DTYPES[dtype], wdtype, bias, pad, 100 * k + rows)
+        check(gns, x, dy, res if with_res else None, w, b, rms)
+
+
+@pytest.mark.parametrize("rows", [0, 1, 151, 4099, 30011])
+def test_many_rows(gns, rows):
+    x, dy, _, w, b = inputs(rows, 72, torch.bfloat16, torch.float32, True, 0, rows)
+    if rows == 0:
+        y, stats = gns.gns_layer_norm(x, w, b)
+        dx, dw, db = gns.gns_layer_norm_backward(dy, x, stats, w, bias=True)
+        assert y.shape == dx.shape == (0, 72) and stats.shape == (0, 2)
+        assert not dw.any() and not db.any()
+    else:
+        check(gns, x, dy, None, w, b, False)
+
+
+def test_weights_that_are_not_aligned(gns):
+    x, dy, res, w, b = inputs(20, 64, torch.bfloat16, torch.bfloat16, True, 0, 5)
+    w, b = (torch.cat([t[:1], t])[1:] for t in (w, b))
+    assert w.data_ptr() % 16 and w.is_contiguous()
+    check(gns, x, dy, res, w, b, False)
+
+
+@pytest.mark.parametrize("cols", [8, 100, 4096, 20000])
+def test_rows_without_spread(gns, cols):
+    """Constant rows of any size have h = 0: dx = rstd (g - mean(g)), y = bias."""
+    values = torch.tensor([0.0, 1.0, -1000.0, 1e-20, 65536.0 * 3, 0.1], device="cuda")
+    x = values[:, None].expand(6, cols).contiguous()
+    bias = torch.randn(cols, device="cuda")
+    y, stats = gns.gns_layer_norm(x, None, bias)
+    assert_close(y, np.broadcast_to(f64(bias), y.shape), np.ones((6, cols)), 8, "y")
+    assert torch.equal(stats[:, 0], values)
+    assert torch.allclose(stats[:, 1], torch.full((6,), 1e5 ** 0.5, device="cuda"))
+
+
+def test_a_large_mean_costs_no_spread(gns):
+    """Values 4096 +- 1 in fp32: the first mean is off by up to some hundred units
+    of its last place, which the second sum takes back."""
+    x = torch.randn(7, 5000, device="cuda", dtype=torch.float64) + 4096
+    x = x.float()
+    y, _ = gns.gns_layer_norm(x)
+    want, h, _, _ = L.layer_norm(f64(x))
+    assert_close(y, want, np.abs(h) + 1, DEPTH, "y")
+
+
+def test_a_row_with_nan_or_infinity_is_its_own_matter(gns):
+    x, dy, res, w, b = inputs(12, 512, torch.bfloat16, torch.float32, True, 0, 8)
+    clean, clean_stats = gns.gns_layer_norm(x, w, b)
+    clean_dx = gns.gns_layer_norm_backward(dy, x, clean_stats, w)[0]
+    bad = x.clone()
+    bad[3, 17], bad[7, 400] = float("nan"), float("inf")
+    y, stats = gns.gns_layer_norm(bad, w, b)
+    dx = gns.gns_layer_norm_backward(dy, bad, stats, w)[0]
+    keep = torch.ones(12, dtype=torch.bool, device="cuda")
+    keep[[3, 7]] = False
+    assert torch.equal(y[keep], clean[keep]) and torch.equal(dx[keep], clean_dx[keep])
+    assert y[3].isnan().all() and y[7].isnan().all() and dx[3].isnan().all()
+
+
+def test_rows_of_a_padded_buffer_stay(gns):
+    """What is asked for is written, and nothing behind it."""
+    full = torch.randn(10, 256, device="cuda").bfloat16()
+    y, stats = gns.gns_layer_norm(full[:7])
+    assert y.shape == (7, 256) and stats.shape == (7, 2)
+    again, _ = gns.gns_layer_norm(full)
+    assert torch.equal(again[:7], y)
+
+
+def test_repeats_bit_for_bit(gns):
+    x, dy, res, w, b = inputs(5000, 640, torch.bfloat16, torch.float32, True, 0, 3)
+    first = gns.gns_layer_norm_backward(dy, x, gns.gns_layer_norm(x, w, b)[1], w, bias=True, residual=res)
+    for _ in range(3):
+        again = gns.gns_layer_norm_backward(dy, x, gns.gns_layer_norm(x, w, b)[1], w, bias=True, residual=res)
+        assert all(torch.equal(a, c) for a, c in zip(first, again))
+
+
+def test_gradients_against_differences(gns):
+    """The GPU's own forward pass in fp32, central differences along random directions."""
+    x, dy, _, w, b = inputs(40, 96, torch.float32, torch.float32, True, 0, 11)
+    dx, dw, db = gns.gns_layer_norm_backward(dy, x, gns.gns_layer_norm(x, w, b)[1], w, bias=True)
+    g = torch.Generator(device="cuda").manual_seed(1)
+    loss = lambda x, w, b: (gns.gns_layer_norm(x, w, b)[0].double() * dy.double()).sum().item()  # noqa: E731
+    for at, grad in enumerate((dx, dw, db)):
+        args = [x, w, b]
+        d = torch.randn(args[at].shape, generator=g, device="cuda")
+        ends = []
+        for step in (1e-2, -1e-2):
+            args[at] = (x, w, b)[at] + step * d
+            ends.append(loss(*args))
+        want = (grad.double() * d.double()).sum().item()
+        # Third derivatives give about step^2 = 1e-4 of the value, fp32 outputs 2^-23 / step per summand.
+        scale = (grad.double() * d.double()).abs().sum().item()
+        assert abs((ends[0] - ends[1]) / 2e-2 - want) < 2e-3 * scale + 1e-3, at
