@@ -276,6 +276,7 @@ typedef enum { GNS_BF16 = 0, GNS_FP16 = 1, GNS_FP32 = 2 } gns_dtype;
 typedef enum { GNS_E4M3 = 0, GNS_E5M2 = 1 } gns_fp8_format;
 
 #define GNS_MAX_EXPERTS 1024
+#define GNS_MAX_TOPK 32
 
 /*
  * gns_dropout: y = residual + (u >= t ? x * 65536 / (65536 - t) : 0) over rows
@@ -421,7 +422,8 @@ int gns_fp8_linear(const void* x, int64_t ldx, int dtype, int rows, const int32_
                    int N, int K, void* y, int64_t ldy, int out_dtype, void* stream);
 
 /* ---------------------------------------------------------------------------
- * Operators around such a block, in the same manner: layer norm.
+ * Operators around such a block, in the same manner: layer norm, the router's
+ * gates with the loss that keeps the experts' loads level, and the embedding.
  */
 
 /*
@@ -447,6 +449,75 @@ int gns_layer_norm(const void* x, int64_t ldx, int64_t rows, int cols, int dtype
 int gns_layer_norm_backward(const void* dy, int64_t lddy, const void* x, int64_t ldx, const float* stats, int64_t rows,
                             int cols, int dtype, const void* weight, int weight_dtype, int rms, const void* residual,
                             int64_t ldr, void* dx, int64_t lddx, void* dweight, void* dbias, void* stream);
+
+/*
+ * gns_moe_gate: the topk experts of each token and their weights, from the
+ * router's logits [tokens][ld].
+ *   ids      device int64 [tokens][topk], written: the experts of the largest
+ *            logits, largest first, of equal ones the lowest first. NaN is larger
+ *            than all else. A logit of -inf is an expert that the token must not
+ *            have: it is never chosen, and where fewer than topk are left the last
+ *            ids are -1 (slots without an expert, as gns_moe_sort takes them).
+ *   weights  fp32 [tokens][topk], written: exp(logit) over the sum of it, over the
+ *            chosen experts (normalize != 0) or over all of them; 0 where the id is
+ *            -1. NaN in a row that holds NaN or +inf.
+ *   lse      fp32 [tokens], written: log of the sum of exp(logit) over all experts,
+ *            -inf for a row of -inf alone: a row without a token.
+ * 1 <= topk <= num_experts <= GNS_MAX_EXPERTS, topk <= GNS_MAX_TOPK.
+ */
+int gns_moe_gate(const void* logits, int64_t ld, int tokens, int num_experts, int topk, int dtype, int normalize,
+                 int64_t* ids, float* weights, float* lse, void* stream);
+
+/*
+ * gns_moe_balance: with N the rows whose lse is not -inf, c_e the slots of
+ * expert e, p = exp(logit - lse) and P_e the mean of p_e over the N rows,
+ *   loss = balance * num_experts / (N topk) * sum_e c_e P_e + z / N * sum lse^2
+ * (balance alone where all loads and probabilities are level; z keeps the logits
+ * small). 0 where N is 0.
+ *   ids, lse  as gns_moe_gate writes them; an id outside 0 .. num_experts - 1
+ *             counts for no expert.
+ *   loss      device fp32 [1], counts int32 [num_experts + 1] (the c_e, then N),
+ *             probs fp32 [num_experts] (the P_e), written.
+ * Takes intermediate memory. Its gradient is part of gns_moe_gate_backward.
+ */
+int gns_moe_balance(const void* logits, int64_t ld, int tokens, int num_experts, int topk, int dtype, const int64_t* ids,
+                    const float* lse, double balance, double z, float* loss, int32_t* counts, float* probs, void* stream);
+
+/*
+ * gns_moe_gate_backward: the gradient of the logits, [tokens][ldd] of their type,
+ * from the gradients of the weights and of the loss. With w, dw a token's weights
+ * and their gradients over its chosen experts, in the place of the j-th of them
+ *   w_j (dw_j - sum_i w_i dw_i)            where normalize, else w_j dw_j, and
+ *   - p_e sum_i w_i dw_i                   for every expert; and where counts is given
+ *   dloss p_e (balance num_experts / (N^2 topk) (c_e - sum_i p_i c_i) + 2 z / N lse)
+ * (the counts have no gradient). Slots without an expert add nothing, whatever dw
+ * holds there; the rows without a token are 0.
+ *   counts  as gns_moe_balance writes them, NULL without the loss.
+ *   dloss   device fp32 [1], NULL for 1.
+ */
+int gns_moe_gate_backward(const float* dweights, const void* logits, int64_t ld, int tokens, int num_experts, int topk,
+                          int dtype, int normalize, const int64_t* ids, const float* weights, const float* lse,
+                          const int32_t* counts, double balance, double z, const float* dloss, void* dlogits, int64_t ldd,
+                          void* stream);
+
+/*
+ * gns_embedding: y[t] = scale * table[ids[t]] (cols elements), 0 for an id outside
+ * 0 .. vocab - 1. ids int32 or int64 (id_bytes 4 or 8); vocab up to 2^30, cols up
+ * to 2^24.
+ */
+int gns_embedding(const void* ids, int id_bytes, int64_t tokens, const void* table, int64_t ldt, int64_t vocab, int64_t cols,
+                  int dtype, double scale, void* y, int64_t ldy, void* stream);
+
+/*
+ * gns_embedding_backward: the table's gradient, every row written:
+ *   dtable[v] = scale * sum over the tokens t with ids[t] = v of dy[t],
+ * 0 for a row without a token. dy is of dtype, dtable of out_dtype; fp32 sums in
+ * token order, joined over runs of sorted tokens, rounded once. Takes intermediate
+ * memory: 16 bytes per token and 4 per row of the table, and up to 8 cols bytes per
+ * 32 tokens (at most 2048 such runs).
+ */
+int gns_embedding_backward(const void* dy, int64_t lddy, const void* ids, int id_bytes, int64_t tokens, int64_t vocab,
+                           int64_t cols, int dtype, double scale, void* dtable, int64_t lddt, int out_dtype, void* stream);
 
 /* Synchronizes `stream`, returns the device status word of the current device
  * as a gns_status (GNS_OK, GNS_ERR_NONFINITE or GNS_ERR_TIMEOUT) and clears it.

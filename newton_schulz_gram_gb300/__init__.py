@@ -16,7 +16,8 @@ from .block import (Fp8Cols, Fp8Rows, Fp8Weight, MoeRoute, gns_dropout, gns_drop
                     gns_fp8_matmul, gns_fp8_matmul_dgrad, gns_fp8_matmul_wgrad, gns_fp8_quantize,
                     gns_fp8_quantize_weight, gns_moe_combine, gns_moe_combine_backward, gns_moe_gather,
                     gns_moe_gather_backward, gns_moe_sort)
-from .layers import gns_layer_norm, gns_layer_norm_backward
+from .layers import (MoeGate, gns_embedding, gns_embedding_backward, gns_layer_norm, gns_layer_norm_backward,
+                     gns_moe_balance, gns_moe_gate, gns_moe_gate_backward)
 
 __all__ = ["gns_orthogonalize_batched", "gns_orthogonalize_batched_host",
            "gns_orthogonalize_batched_noalloc", "gns_orthogonalize_batched_schedule", "muon_step", "normuon_step", "dion3_step",
@@ -26,7 +27,8 @@ __all__ = ["gns_orthogonalize_batched", "gns_orthogonalize_batched_host",
            "gns_dropout", "gns_dropout_backward", "gns_moe_sort", "gns_moe_gather", "gns_moe_gather_backward",
            "gns_moe_combine", "gns_moe_combine_backward", "gns_fp8_quantize", "gns_fp8_quantize_weight",
            "gns_fp8_matmul", "gns_fp8_matmul_dgrad", "gns_fp8_matmul_wgrad", "gns_fp8_linear", "MoeRoute", "Fp8Rows",
-           "Fp8Cols", "Fp8Weight", "gns_layer_norm", "gns_layer_norm_backward", "GnsError", "QUINTIC", "load"]
+           "Fp8Cols", "Fp8Weight", "gns_layer_norm", "gns_layer_norm_backward", "gns_moe_gate", "gns_moe_balance",
+           "gns_moe_gate_backward", "MoeGate", "gns_embedding", "gns_embedding_backward", "GnsError", "QUINTIC", "load"]
 
 QUINTIC = (3.4445, -4.7750, 2.0315)
 

@@ -57,6 +57,11 @@ PROTOTYPES = {
     "gns_layer_norm": (_i, [_vp, _i64, _i64, _i, _i, _vp, _vp, _i, _d, _i, _vp, _i64, _vp, _vp]),
     "gns_layer_norm_backward": (_i, [_vp, _i64, _vp, _i64, _vp, _i64, _i, _i, _vp, _i, _i, _vp, _i64, _vp, _i64, _vp, _vp,
                                      _vp]),
+    "gns_moe_gate": (_i, [_vp, _i64, _i, _i, _i, _i, _i, _vp, _vp, _vp, _vp]),
+    "gns_moe_balance": (_i, [_vp, _i64, _i, _i, _i, _i, _vp, _vp, _d, _d, _vp, _vp, _vp, _vp]),
+    "gns_moe_gate_backward": (_i, [_vp, _vp, _i64, _i, _i, _i, _i, _i, _vp, _vp, _vp, _vp, _d, _d, _vp, _vp, _i64, _vp]),
+    "gns_embedding": (_i, [_vp, _i, _i64, _vp, _i64, _i64, _i64, _i, _d, _vp, _i64, _vp]),
+    "gns_embedding_backward": (_i, [_vp, _i64, _vp, _i, _i64, _i64, _i64, _i, _d, _vp, _i64, _i, _vp]),
     "gns_get_status": (_i, [_vp]),
     "gns_test_bounded_wait": (_i, [_i, _i64, _vp]),
     "gns_status_string": (ctypes.c_char_p, [_i]),

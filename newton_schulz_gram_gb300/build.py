@@ -21,7 +21,8 @@ INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(HERE, "_build", platform.machine())
 LIB = os.path.join(BUILD, "libgns.so")
 SOURCES = ["gemm_tc.cu", "elementwise.cu", "dion3.cu", "fp8_gemm.cu", "fp8_cast.cu", "fp8_rows.cu", "moe.cu",
-           "dropout.cu", "layer_norm.cu", "layer_norm_backward.cu", "api.cu", "api_block.cu", "api_layers.cu"]
+           "dropout.cu", "layer_norm.cu", "layer_norm_backward.cu", "moe_gate.cu", "embedding.cu",
+           "api.cu", "api_block.cu", "api_layers.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

@@ -2,8 +2,8 @@
 // by expert, the copy of each token's row to its places, the weighted sum of
 // a token's rows, and the gradients of both.
 //
-// Everything is a function of the inputs alone: the sort ranks slots by
-// counting (no atomics), a token's rows are summed in slot order in fp32 and
+// Everything is a function of the inputs alone: the sort (counting_sort.cuh) ranks
+// slots by counting (no atomics), a token's rows are summed in slot order in fp32 and
 // rounded once, and the weights' gradients are summed in a fixed order.
 //
 // Bound: HBM for the moves, a token's row once and its topk rows once each way.
@@ -13,6 +13,7 @@
 #include <algorithm>
 
 #include "blockops.cuh"
+#include "counting_sort.cuh"
 #include "moe.cuh"
 #include "ptx.cuh"
 
@@ -20,182 +21,27 @@ namespace gns {
 namespace {
 
 // ------------------------------------------------------------------ the sort
-//
-// A warp owns a run of consecutive slots and walks it 32 at a time:
-// __match_any_sync groups the lanes of one expert, a lane's rank in its group
-// is the popcount of the lanes before it, and the warp's running count of
-// the expert (its own column of shared memory, so no atomics) gives the rest.
-// Up to kOneBlock slots a single block does it all. Beyond, a first kernel
-// stores each block's counts and the second one's blocks sum, each for
-// itself, the counts of all blocks and of those before it: nblocks * (G + 1)
-// loads that stay in L2, which is less than the round trip of a third launch
-// for up to kMaxBlocks blocks.
 
-constexpr int kSortWarps = 16;
-constexpr int kSortThreads = 32 * kSortWarps;
-constexpr int kOneBlock = 4096;
-constexpr int kMaxBlocks = 152;
-
-size_t sort_smem(int G) { return sizeof(int) * static_cast<size_t>(G + 1) * (kSortWarps + 1); }
-
-long long sort_blocks(long long n) {
-    if (n <= kOneBlock) return 1;
-    return std::min<long long>(kMaxBlocks, (n + 2047) / 2048);
-}
-
-// Slots per block, a multiple of 32 per warp.
-long long sort_span(long long n) {
-    const long long per = (n + sort_blocks(n) - 1) / sort_blocks(n);
-    return (per + kSortThreads - 1) / kSortThreads * kSortThreads;
-}
+// The slots by expert; ids outside 0 .. G - 1 have digit G.
+template <typename I>
+struct ExpertSlots {
+    const I* ids;
+    int G;
+    int *offsets, *rows, *slots;
+    __device__ __forceinline__ int digit(long long s) const {
+        const I v = ids[s];
+        return v >= 0 && v < static_cast<I>(G) ? static_cast<int>(v) : G;
+    }
+    __device__ __forceinline__ void place(long long s, int at) const {
+        rows[s] = at;
+        slots[at] = static_cast<int>(s);
+    }
+    __device__ __forceinline__ void start(int e, int at) const { offsets[e] = at; }  // offsets[G]: the slots with an expert
+};
 
 template <typename I>
-__device__ __forceinline__ int expert_of(const I* ids, long long s, int G) {
-    const I v = ids[s];
-    return v >= 0 && v < static_cast<I>(G) ? static_cast<int>(v) : G;
-}
-
-// Counts of this warp's run of slots into its column cnt[0 .. G].
-template <typename I>
-__device__ __forceinline__ void count_run(const I* ids, long long beg, long long end, int G, int* cnt, int lane) {
-    for (long long s0 = beg; s0 < end; s0 += 32) {
-        const long long s = s0 + lane;
-        const int e = s < end ? expert_of(ids, s, G) : -1;
-        const unsigned peers = __match_any_sync(0xffffffffu, e);
-        if (e >= 0 && (peers & ((1u << lane) - 1)) == 0) cnt[e] += __popc(peers);
-        __syncwarp();
-    }
-}
-
-template <typename I>
-__global__ void __launch_bounds__(kSortThreads) moe_count_kernel(const I* ids, long long n, int G, long long span,
-                                                                 int* hist) {
-    extern __shared__ int smem[];
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    for (int i = threadIdx.x; i < (G + 1) * kSortWarps; i += kSortThreads) smem[i] = 0;
-    grid_dependency_wait();
-    grid_launch_dependents();
-    __syncthreads();
-    const long long run = span / kSortWarps;
-    const long long beg = blockIdx.x * span + warp * run;
-    count_run(ids, beg, min(beg + run, n), G, smem + warp * (G + 1), lane);
-    __syncthreads();
-    for (int e = threadIdx.x; e <= G; e += kSortThreads) {
-        int c = 0;
-        for (int w = 0; w < kSortWarps; ++w) c += smem[w * (G + 1) + e];
-        hist[static_cast<long long>(blockIdx.x) * (G + 1) + e] = c;
-    }
-}
-
-// hist null: the grid is one block and its own counts are all there are.
-template <typename I>
-__global__ void __launch_bounds__(kSortThreads) moe_place_kernel(const I* ids, long long n, int G, long long span,
-                                                                 const int* hist, int* offsets, int* rows,
-                                                                 int* slots) {
-    extern __shared__ int smem[];
-    __shared__ int warp_sum[kSortWarps];
-    int* first = smem + (G + 1) * kSortWarps;  // first place of this block's slots of each expert
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    for (int i = threadIdx.x; i < (G + 1) * kSortWarps; i += kSortThreads) smem[i] = 0;
-    grid_dependency_wait();
-    grid_launch_dependents();
-    __syncthreads();
-    const long long run = span / kSortWarps;
-    const long long beg = blockIdx.x * span + warp * run;
-    const long long end = min(beg + run, n);
-    int* cnt = smem + warp * (G + 1);
-    count_run(ids, beg, end, G, cnt, lane);
-    __syncthreads();
-
-    // Totals of all blocks, scanned over the experts: thread t owns experts
-    // t * per .. t * per + per - 1.
-    constexpr int kPer = (kMaxExperts + 1 + kSortThreads - 1) / kSortThreads;
-    const int per = (G + kSortThreads) / kSortThreads;  // ceil((G + 1) / threads)
-    int total[kPer], before[kPer];
-    int mine = 0;
-#pragma unroll
-    for (int i = 0; i < kPer; ++i) {
-        const int e = threadIdx.x * per + i;
-        total[i] = before[i] = 0;
-        if (i >= per || e > G) continue;
-        if (hist) {
-#pragma unroll 8
-            for (int b = 0; b < static_cast<int>(gridDim.x); ++b) {
-                const int c = hist[static_cast<long long>(b) * (G + 1) + e];
-                total[i] += c;
-                if (b < static_cast<int>(blockIdx.x)) before[i] += c;
-            }
-        } else {
-            for (int w = 0; w < kSortWarps; ++w) total[i] += smem[w * (G + 1) + e];
-        }
-        mine += total[i];
-    }
-    int scan = mine;
-#pragma unroll
-    for (int d = 1; d < 32; d <<= 1) {
-        const int v = __shfl_up_sync(0xffffffffu, scan, d);
-        if (lane >= d) scan += v;
-    }
-    if (lane == 31) warp_sum[warp] = scan;
-    __syncthreads();
-    int start = scan - mine;
-    for (int w = 0; w < warp; ++w) start += warp_sum[w];
-#pragma unroll
-    for (int i = 0; i < kPer; ++i) {
-        const int e = threadIdx.x * per + i;
-        if (i >= per || e > G) continue;
-        first[e] = start + before[i];
-        if (blockIdx.x == 0) offsets[e] = start;  // offsets[G]: the slots with an expert
-        start += total[i];
-    }
-    __syncthreads();
-    // Each warp's first place per expert: the block's, plus the warps before it.
-    for (int e = threadIdx.x; e <= G; e += kSortThreads) {
-        int at = first[e];
-        for (int w = 0; w < kSortWarps; ++w) {
-            const int c = smem[w * (G + 1) + e];
-            smem[w * (G + 1) + e] = at;
-            at += c;
-        }
-    }
-    __syncthreads();
-    for (long long s0 = beg; s0 < end; s0 += 32) {
-        const long long s = s0 + lane;
-        const int e = s < end ? expert_of(ids, s, G) : -1;
-        const unsigned peers = __match_any_sync(0xffffffffu, e);
-        const int rank = __popc(peers & ((1u << lane) - 1));
-        int at = 0;
-        if (e >= 0) {
-            at = cnt[e] + rank;
-            rows[s] = at;
-            slots[at] = static_cast<int>(s);
-        }
-        __syncwarp();
-        if (e >= 0 && rank == 0) cnt[e] += __popc(peers);
-        __syncwarp();
-    }
-}
-
-template <typename... KArgs, typename... Args>
-int sort_step(void (*kernel)(KArgs...), const SortJob& j, cudaStream_t s, Args... args) {
-    const size_t smem = sort_smem(j.G);
-    if (smem > 48 * 1024) {
-        const cudaError_t e =
-            cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
-        if (e != cudaSuccess) return e;
-    }
-    return launch_after(kernel, dim3(static_cast<unsigned>(sort_blocks(j.n))), dim3(kSortThreads), smem, s, args...);
-}
-
-template <typename I>
-int count_typed(const SortJob& j, cudaStream_t s) {
-    return sort_step(moe_count_kernel<I>, j, s, static_cast<const I*>(j.ids), j.n, j.G, sort_span(j.n), j.hist);
-}
-
-template <typename I>
-int place_typed(const SortJob& j, cudaStream_t s) {
-    return sort_step(moe_place_kernel<I>, j, s, static_cast<const I*>(j.ids), j.n, j.G, sort_span(j.n),
-                     static_cast<const int*>(j.hist), j.offsets, j.rows, j.slots);
+ExpertSlots<I> slots_of(const SortJob& j) {
+    return {static_cast<const I*>(j.ids), j.G, j.offsets, j.rows, j.slots};
 }
 
 // --------------------------------------------------------- moves over tokens
@@ -399,17 +245,16 @@ dim3 walk_grid(const Walk& w) {
 
 }  // namespace
 
-size_t moe_sort_scratch(long long n, int G) {
-    const long long b = sort_blocks(n);
-    return b > 1 ? sizeof(int) * static_cast<size_t>(b) * (G + 1) : 0;
-}
+size_t moe_sort_scratch(long long n, int G) { return sort_scratch(n, G); }
 
 int launch_moe_count(const SortJob& j, cudaStream_t s) {
-    return j.id_bytes == 8 ? count_typed<long long>(j, s) : count_typed<int>(j, s);
+    return j.id_bytes == 8 ? launch_sort_count(slots_of<long long>(j), j.n, j.G, j.hist, s)
+                           : launch_sort_count(slots_of<int>(j), j.n, j.G, j.hist, s);
 }
 
 int launch_moe_place(const SortJob& j, cudaStream_t s) {
-    return j.id_bytes == 8 ? place_typed<long long>(j, s) : place_typed<int>(j, s);
+    return j.id_bytes == 8 ? launch_sort_place(slots_of<long long>(j), j.n, j.G, j.hist, s)
+                           : launch_sort_place(slots_of<int>(j), j.n, j.G, j.hist, s);
 }
 
 int launch_moe_gather(const RouteJob& j, const void* x, long long ldx, void* y, long long ldy, cudaStream_t s) {
