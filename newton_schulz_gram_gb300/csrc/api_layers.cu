@@ -80,6 +80,7 @@ int gns_layer_norm(const void* x, int64_t ldx, int64_t rows, int cols, int dtype
     j.y = y;
     j.ldy = ldy;
     j.stats = stats;
+    j.st = new_call(*st);
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     LAUNCH(kClsLayerNorm, launch_layer_norm(j, st->num_sms, s));
     return GNS_OK;
@@ -121,6 +122,7 @@ int gns_layer_norm_backward(const void* dy, int64_t lddy, const void* x, int64_t
     j.lddx = lddx;
     j.dweight = dweight;
     j.dbias = dbias;
+    j.st = new_call(*st);
     Scratch scratch;
     if (const size_t bytes = norm_backward_scratch(j, st->num_sms)) {
         RET(scratch.take(*st, bytes, s));

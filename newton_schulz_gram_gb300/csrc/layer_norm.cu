@@ -16,11 +16,18 @@
 namespace gns {
 namespace {
 
-// Pieces a thread keeps: four of a warp's row in blocks of 256, two of a block's.
-constexpr int kWarpPieces = 4, kBlockPieces = 2;
+// From the mean of the squared deviations and of the deviations. fmaxf drops a NaN;
+// the squares carry it.
+__device__ __forceinline__ float norm_rstd(float squares, float dev, float eps) {
+    const float var = fmaxf(squares - dev * dev, 0.0f);
+    return rsqrtf((squares == squares ? var : squares) + eps);
+}
+
+// Most threads a row, of up to kMostPieces pieces each.
+constexpr int kMostPieces = 16, kMostThreads = 512;
 
 template <typename T, typename Piece, int V>
-__global__ void __launch_bounds__(V == kBlockPieces ? 1024 : 256) layer_norm_kernel(NormJob j) {
+__global__ void __launch_bounds__(kMostThreads) layer_norm_kernel(NormJob j) {
     constexpr int N = Piece::kSize;
     __shared__ float2 red[2][32];
     int phase = 0;
@@ -56,6 +63,8 @@ __global__ void __launch_bounds__(V == kBlockPieces ? 1024 : 256) layer_norm_ker
             row_sum2(mean, none, j.tpr, red[phase ^= 1]);
             mean /= n;
         }
+#pragma unroll
+        for (int i = 0; i < V; ++i) p[i].forget();
         float dev = 0.0f, squares = 0.0f;
 #pragma unroll
         for (int i = 0; i < V; ++i) {
@@ -71,13 +80,13 @@ __global__ void __launch_bounds__(V == kBlockPieces ? 1024 : 256) layer_norm_ker
         }
         row_sum2(dev, squares, j.tpr, red[phase ^= 1]);
         dev = j.rms ? 0.0f : dev / n;
-        const float var = fmaxf(squares / n - dev * dev, 0.0f);
-        // fmaxf drops a NaN; the sum of squares carries it.
-        const float rstd = 1.0f / sqrtf((squares == squares ? var : squares) + j.eps);
+        const float rstd = norm_rstd(squares / n, dev, j.eps);
         if (live && at == 0) {
             j.stats[2 * r] = mean + dev;
             j.stats[2 * r + 1] = rstd;
         }
+#pragma unroll
+        for (int i = 0; i < V; ++i) p[i].forget();
 #pragma unroll
         for (int i = 0; i < V; ++i) {
             const unsigned v = at + i * j.tpr;
@@ -103,6 +112,158 @@ __global__ void __launch_bounds__(V == kBlockPieces ? 1024 : 256) layer_norm_ker
             o.store(y + r * j.ldy, v, j.cols);
         }
     }
+}
+
+// ------------------------------------------------------------- aligned rows
+//
+// A thread keeps its columns, and their weights, from row to row. It copies its
+// pieces of rows to come to shared memory (cp.async) while it works on R rows in
+// registers, so a copy needs no barrier, and the R rows' sums share a reduction.
+// FULL: every thread has all its pieces.
+//
+// CLUSTER: rows of more columns than a CTA's registers have weights for are shared by the
+// CTAs of a cluster, which exchange the sums.
+
+template <typename T, int V, bool FULL, bool CLUSTER>
+__global__ void __launch_bounds__(kRingThreads) layer_norm_ring_kernel(NormJob j) {
+    constexpr int N = 16 / sizeof(T), P = N / 2, R = 2;
+    extern __shared__ __align__(128) uint4 ring[];  // [stage][row][piece][thread]
+    __shared__ __align__(128) RowSums<2 * R> red;
+    int use = 0;
+    bool dead = false;
+    if (CLUSTER) {
+        if (threadIdx.x < 2) mbar_init(smem_u32(&red.full[threadIdx.x]), 1);
+        fence_mbar_init();
+        cluster_sync();
+    }
+    grid_dependency_wait();
+    grid_launch_dependents();
+    const int at = j.tpr <= 32 ? threadIdx.x & (j.tpr - 1) : threadIdx.x;
+    const int group = j.tpr <= 32 ? threadIdx.x / j.tpr : 0;
+    const int groups = blockDim.x / j.tpr, threads = blockDim.x;
+    const int rank = CLUSTER ? cluster_ctarank() : 0;
+    const int piece = rank * j.per_cta + at, pieces = min(j.per_row, (rank + 1) * j.per_cta);  // this thread's first, the CTA's end
+    const unsigned cluster = CLUSTER ? blockIdx.x / j.ctas : blockIdx.x, clusters = CLUSTER ? gridDim.x / j.ctas : gridDim.x;
+    const float inv = 1.0f / static_cast<float>(j.cols);
+    const unsigned rows = static_cast<unsigned>(j.rows), batch = groups * R, step = clusters * batch;
+    const unsigned first = cluster * batch + group;
+    const T* x = static_cast<const T*>(j.x) + first * j.ldx + piece * N;  // of the rows fetched next
+    T* y = static_cast<T*>(j.y) + first * j.ldy + piece * N;
+    const long long x_step = step * j.ldx, y_step = step * j.ldy, x_row = groups * j.ldx, y_row = groups * j.ldy;
+    const int apart = j.tpr * N;  // from one piece to the next
+    const uint4* mine = ring + threadIdx.x;
+    const uint32_t slots = smem_u32(mine);
+    auto has = [&](int i) { return FULL || piece + i * j.tpr < pieces; };
+    unsigned ahead = first;
+    auto fetch = [&](int stage) {
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+            if (ahead + r * groups >= rows) break;
+#pragma unroll
+            for (int i = 0; i < V; ++i)
+                if (has(i)) copy16(slots + 16 * ((stage * R + r) * V + i) * threads, x + r * x_row + i * apart);
+        }
+        copies_commit();
+        x += x_step;
+        ahead += step;
+    };
+    float2 w[V][P], b[V][P];
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+        float f[N];
+        const Wide<T, N> p{};
+#pragma unroll
+        for (int e = 0; e < P; ++e) w[i][e] = both(1.0f), b[i][e] = both(0.0f);
+        if (j.weight && has(i)) {
+            piece_weights(p, j.weight, j.wf32, piece + i * j.tpr, j.cols, f);
+#pragma unroll
+            for (int e = 0; e < P; ++e) w[i][e] = make_float2(f[2 * e], f[2 * e + 1]);
+        }
+        if (j.bias && has(i)) {
+            piece_weights(p, j.bias, j.wf32, piece + i * j.tpr, j.cols, f);
+#pragma unroll
+            for (int e = 0; e < P; ++e) b[i][e] = make_float2(f[2 * e], f[2 * e + 1]);
+        }
+    }
+#pragma unroll
+    for (int k = 0; k < kStages - 1; ++k) fetch(k);
+    int stage = 0;
+    for (unsigned row = first; row - group < rows; row += step, y += y_step) {
+        fetch(stage == 0 ? kStages - 1 : stage - 1);
+        copies_wait<kStages - 1>();
+        float2 f[R][V][P];
+#pragma unroll
+        for (int r = 0; r < R; ++r)
+#pragma unroll
+            for (int i = 0; i < V; ++i) {
+                uint4 v = make_uint4(0, 0, 0, 0);
+                if (has(i) && row + r * groups < rows) v = mine[((stage * R + r) * V + i) * threads];
+                unpack<T, N>(v, f[r][i]);
+            }
+        float mean[R];
+#pragma unroll
+        for (int r = 0; r < R; ++r) mean[r] = 0.0f;
+        if (!j.rms) {
+#pragma unroll
+            for (int r = 0; r < R; ++r) {
+                float2 sum = both(0.0f);
+#pragma unroll
+                for (int i = 0; i < V; ++i)
+#pragma unroll
+                    for (int e = 0; e < P; ++e) sum = add2(sum, f[r][i][e]);
+                mean[r] = sum.x + sum.y;
+            }
+            row_sums<R, CLUSTER>(mean, j, red, use, dead);
+        }
+        float c[2 * R];  // sums of the deviations and of their squares
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+            mean[r] *= inv;
+            float2 dev = both(0.0f), squares = both(0.0f);
+#pragma unroll
+            for (int i = 0; i < V; ++i) {
+                if (!has(i)) continue;
+#pragma unroll
+                for (int e = 0; e < P; ++e) {
+                    f[r][i][e] = add2(f[r][i][e], both(-mean[r]));
+                    dev = add2(dev, f[r][i][e]);
+                    squares = fma2(f[r][i][e], f[r][i][e], squares);
+                }
+            }
+            c[2 * r] = dev.x + dev.y;
+            c[2 * r + 1] = squares.x + squares.y;
+        }
+        row_sums<2 * R, CLUSTER>(c, j, red, use, dead);
+        float dev[R], rstd[R];
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+            dev[r] = j.rms ? 0.0f : c[2 * r] * inv;
+            rstd[r] = norm_rstd(c[2 * r + 1] * inv, dev[r], j.eps);
+            const unsigned o = row + r * groups;
+            if (piece == 0 && o < rows) {
+                j.stats[2LL * o] = mean[r] + dev[r];
+                j.stats[2LL * o + 1] = rstd[r];
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            if (!has(i)) continue;
+#pragma unroll
+            for (int r = 0; r < R; ++r) {
+                if (row + r * groups >= rows) break;
+                float2 o[P];
+#pragma unroll
+                for (int e = 0; e < P; ++e) {
+                    o[e] = fma2(f[r][i][e], both(rstd[r]), both(-dev[r] * rstd[r]));
+                    o[e] = fma2(o[e], w[i][e], b[i][e]);
+                }
+                *reinterpret_cast<uint4*>(y + r * y_row + i * apart) = pack<T>(o);
+            }
+        }
+        stage = stage == kStages - 1 ? 0 : stage + 1;
+    }
+    copies_wait<0>();
+    if (CLUSTER) cluster_sync();  // no CTA ends while another may send to it
 }
 
 // Rows beyond the registers of a block: read three times, the later ones from L2.
@@ -147,8 +308,7 @@ __global__ void __launch_bounds__(kLongThreads) layer_norm_long_kernel(NormJob j
         }
         row_sum2(dev, squares, kLongThreads, red[phase ^= 1]);
         dev = j.rms ? 0.0f : dev / n;
-        const float var = fmaxf(squares / n - dev * dev, 0.0f);
-        const float rstd = 1.0f / sqrtf((squares == squares ? var : squares) + j.eps);
+        const float rstd = norm_rstd(squares / n, dev, j.eps);
         if (threadIdx.x == 0) {
             j.stats[2 * r] = mean + dev;
             j.stats[2 * r + 1] = rstd;
@@ -182,31 +342,56 @@ __global__ void __launch_bounds__(kLongThreads) layer_norm_long_kernel(NormJob j
 
 int launch_layer_norm(NormJob j, int num_sms, cudaStream_t s) {
     const bool vec = norm_vec(j, false);
-    j.per_row = norm_pieces(j, vec);
-    const int p = j.per_row;
-    const bool fits = p <= kBlockPieces * 1024;
-    const int V = p <= 32 ? 1 : p <= 64 || p > 32 * kWarpPieces ? kBlockPieces : kWarpPieces;
-    int threads = 256;
-    if (p <= 32 * kWarpPieces) {
-        j.tpr = std::min(32, next_pow2(p));
+    const int p = j.per_row = norm_pieces(j, vec);
+    const bool fits = p <= kMostPieces * kMostThreads;
+    int V = 1, threads = 128;
+    if (p <= 4) {
+        j.tpr = next_pow2(p);
+    } else if (j.rows <= 2 * num_sms && p > 32) {
+        while (V < kMostPieces && p > V * kMostThreads) V *= 2;
+        threads = j.tpr = (p + 32 * V - 1) / (32 * V) * 32;
+    } else if (p <= 32 * kMostPieces) {
+        while (V < kMostPieces && (V < 4 ? p > 4 * V : p > 32 * V)) V *= 2;
+        j.tpr = std::max(4, next_pow2((p + V - 1) / V));
     } else {
+        const auto idle = [&](int v) { return (p + 32 * v - 1) / (32 * v) * 32 * v - p; };
+        V = idle(8) < idle(16) && p <= 8 * kMostThreads ? 8 : 16;
         threads = j.tpr = (p + 32 * V - 1) / (32 * V) * 32;
     }
-    const long long groups = threads / (fits ? j.tpr : threads);
-    const long long most = (j.rows + groups - 1) / groups;
-    const unsigned blocks = static_cast<unsigned>(std::min<long long>(most, static_cast<long long>(num_sms) * std::max(1, 2048 / threads)));
     return by_dtype(j.dtype, [&](auto t) {
         using T = decltype(t);
         using W = Wide<T, 16 / sizeof(T)>;
         using L = Loose<T>;
+        constexpr int n = 16 / sizeof(T), few = 16 / n;
+        RingShape c;
+        if (vec && j.rows > 2 * num_sms && ring_shape(p, n, 2 * kStages, &c)) {
+            j.tpr = c.tpr;
+            j.ctas = c.ctas;
+            j.per_cta = c.per_cta;
+            const size_t smem = sizeof(uint4) * kStages * 2 * c.V * c.threads;
+            const long long batch = static_cast<long long>(c.threads / c.tpr) * 2;
+            const unsigned clusters = ring_clusters(c, (j.rows + batch - 1) / batch, num_sms, smem);
+            const bool full = p == c.V * c.tpr * c.ctas;
+            const auto run = [&](auto k) { return launch_ring(k, c, clusters, smem, s, j); };
+            if (c.ctas > 1) return run(full ? layer_norm_ring_kernel<T, few, true, true> : layer_norm_ring_kernel<T, few, false, true>);
+            if (c.V == 1) return run(full ? layer_norm_ring_kernel<T, 1, true, false> : layer_norm_ring_kernel<T, 1, false, false>);
+            return run(full ? layer_norm_ring_kernel<T, few, true, false> : layer_norm_ring_kernel<T, few, false, false>);
+        }
         if (!fits) {
             const unsigned b = static_cast<unsigned>(std::min<long long>(j.rows, 2LL * num_sms));
             return static_cast<int>(launch_after(vec ? layer_norm_long_kernel<T, W> : layer_norm_long_kernel<T, L>, dim3(b),
                                                  dim3(kLongThreads), 0, s, j));
         }
-        auto k = vec ? (V == 1 ? layer_norm_kernel<T, W, 1> : V == 2 ? layer_norm_kernel<T, W, 2> : layer_norm_kernel<T, W, 4>)
-                     : (V == 1 ? layer_norm_kernel<T, L, 1> : V == 2 ? layer_norm_kernel<T, L, 2> : layer_norm_kernel<T, L, 4>);
-        return static_cast<int>(launch_after(k, dim3(blocks), dim3(threads), 0, s, j));
+        const long long groups = threads / j.tpr;
+        const dim3 blocks(static_cast<unsigned>((j.rows + groups - 1) / groups));
+        const auto run = [&](auto k) { return static_cast<int>(launch_after(k, blocks, dim3(threads), 0, s, j)); };
+        switch (V) {
+            case 1: return run(vec ? layer_norm_kernel<T, W, 1> : layer_norm_kernel<T, L, 1>);
+            case 2: return run(vec ? layer_norm_kernel<T, W, 2> : layer_norm_kernel<T, L, 2>);
+            case 4: return run(vec ? layer_norm_kernel<T, W, 4> : layer_norm_kernel<T, L, 4>);
+            case 8: return run(vec ? layer_norm_kernel<T, W, 8> : layer_norm_kernel<T, L, 8>);
+            default: return run(vec ? layer_norm_kernel<T, W, 16> : layer_norm_kernel<T, L, 16>);
+        }
     });
 }
 

@@ -7,9 +7,11 @@
 
 #include <cstddef>
 #include <cstdint>
+#include <algorithm>
 #include <cuda_runtime.h>
 
 #include "blockops.cuh"
+#include "ptx.cuh"
 
 namespace gns {
 
@@ -35,7 +37,9 @@ struct NormJob {
     void* dweight;  // typed as weight; either may be null
     void* dbias;
     float* part;    // norm_backward_scratch() bytes
+    DevStatus st;   // of waits among the CTAs of a row
     int tpr, per_row;  // set by the launchers
+    int ctas, per_cta;  // of the ring kernels: CTAs that share a row, and pieces of each
 };
 
 int launch_layer_norm(NormJob job, int num_sms, cudaStream_t s);
@@ -113,6 +117,156 @@ __device__ __forceinline__ void row_sum2(float& a, float& b, int tpr, float2* re
     }
 }
 
+// Copies to shared memory that the thread waits for itself.
+__device__ __forceinline__ void copy16(uint32_t to, const void* from) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to), "l"(from) : "memory");
+}
+__device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int LEFT>
+__device__ __forceinline__ void copies_wait() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(LEFT) : "memory");
+}
+
+// Pairs of fp32 values, which one instruction adds, multiplies or accumulates.
+__device__ __forceinline__ unsigned long long pair_bits(float2 a) {
+    return static_cast<unsigned long long>(__float_as_uint(a.y)) << 32 | __float_as_uint(a.x);
+}
+__device__ __forceinline__ float2 pair_of(unsigned long long b) {
+    return make_float2(__uint_as_float(static_cast<unsigned>(b)), __uint_as_float(static_cast<unsigned>(b >> 32)));
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+    unsigned long long d;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(pair_bits(a)), "l"(pair_bits(b)));
+    return pair_of(d);
+}
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+    unsigned long long d;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(pair_bits(a)), "l"(pair_bits(b)));
+    return pair_of(d);
+}
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+    unsigned long long d;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(pair_bits(a)), "l"(pair_bits(b)), "l"(pair_bits(c)));
+    return pair_of(d);
+}
+__device__ __forceinline__ float2 both(float a) { return make_float2(a, a); }
+
+// The 16 bytes of a piece as pairs and back.
+template <typename T, int N>
+__device__ __forceinline__ void unpack(const uint4& u, float2 (&f)[N / 2]) {
+    const T* e = reinterpret_cast<const T*>(&u);
+#pragma unroll
+    for (int i = 0; i < N / 2; ++i) f[i] = make_float2(to_f32<T>(e[2 * i]), to_f32<T>(e[2 * i + 1]));
+}
+__device__ __forceinline__ unsigned pack2(float2 a, __nv_bfloat16) {
+    const __nv_bfloat162 v = __floats2bfloat162_rn(a.x, a.y);
+    return *reinterpret_cast<const unsigned*>(&v);
+}
+__device__ __forceinline__ unsigned pack2(float2 a, __half) {
+    const __half2 v = __floats2half2_rn(a.x, a.y);
+    return *reinterpret_cast<const unsigned*>(&v);
+}
+template <typename T>
+__device__ __forceinline__ uint4 pack(const float2 (&f)[4]) {
+    return make_uint4(pack2(f[0], T{}), pack2(f[1], T{}), pack2(f[2], T{}), pack2(f[3], T{}));
+}
+template <typename T>
+__device__ __forceinline__ uint4 pack(const float2 (&f)[2]) {
+    return make_uint4(__float_as_uint(f[0].x), __float_as_uint(f[0].y), __float_as_uint(f[1].x), __float_as_uint(f[1].y));
+}
+
+// What the CTAs of a cluster that share a row exchange their sums through: every warp
+// writes its sums into all of them (st.async), where they count on a barrier. A CTA can
+// be one reduction ahead of another at most, so two buffers in turn are enough, and a
+// count that comes before the barrier is armed for it is not lost.
+constexpr int kMaxCtas = 8, kMostWarps = 16;  // of a row
+template <int K>
+struct __align__(128) RowSums {
+    float4 sums[2][kMaxCtas * kMostWarps * K / 4 + 1];
+    uint64_t full[2];
+};
+
+template <int K>
+__device__ __forceinline__ void send_sums(uint32_t to, uint32_t bar, const float (&a)[K]) {
+    static_assert(K == 2 || K == 4, "8 or 16 bytes");
+    if (K == 2)
+        asm volatile("st.async.shared::cluster.mbarrier::complete_tx::bytes.v2.b32 [%0], {%2, %3}, [%1];" ::"r"(to), "r"(bar),
+                     "r"(__float_as_uint(a[0])), "r"(__float_as_uint(a[1]))
+                     : "memory");
+    else
+        asm volatile("st.async.shared::cluster.mbarrier::complete_tx::bytes.v4.b32 [%0], {%2, %3, %4, %5}, [%1];" ::"r"(to), "r"(bar),
+                     "r"(__float_as_uint(a[0])), "r"(__float_as_uint(a[1])), "r"(__float_as_uint(a[2 % K])), "r"(__float_as_uint(a[3 % K]))
+                     : "memory");
+}
+
+// Sums of K = 2 or 4 values over the threads of a row: `tpr` neighbouring lanes, the
+// block (one barrier; its next call takes the other buffer of two), or, CLUSTER, the
+// CTAs of the cluster. Across a whole warp the values part on the way: half the lanes go
+// on with half of them, so that four cost 12 shuffles' and adds' worth instead of 40.
+// use: reductions done so far.
+template <int K, bool CLUSTER, int KS>
+__device__ __forceinline__ void row_sums(float (&a)[K], const NormJob& j, RowSums<KS>& red, int& use, bool& dead) {
+    const int tpr = j.tpr;
+    if (tpr < 32) {
+        for (int m = tpr >> 1; m > 0; m >>= 1) {
+#pragma unroll
+            for (int k = 0; k < K; ++k) a[k] += __shfl_xor_sync(0xffffffffu, a[k], m);
+        }
+        return;
+    }
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    float v;
+    if (K == 4) {
+        const bool up = lane & 16;
+        const float p = (up ? a[2 % K] : a[0]) + __shfl_xor_sync(0xffffffffu, up ? a[0] : a[2 % K], 16);
+        const float q = (up ? a[3 % K] : a[1]) + __shfl_xor_sync(0xffffffffu, up ? a[1] : a[3 % K], 16);
+        const bool odd = lane & 8;
+        v = (odd ? q : p) + __shfl_xor_sync(0xffffffffu, odd ? p : q, 8);
+    } else {
+        const bool up = lane & 16;
+        v = (up ? a[1] : a[0]) + __shfl_xor_sync(0xffffffffu, up ? a[0] : a[1], 16);
+        v += __shfl_xor_sync(0xffffffffu, v, 8);
+    }
+    v += __shfl_xor_sync(0xffffffffu, v, 4);
+    v += __shfl_xor_sync(0xffffffffu, v, 2);
+    v += __shfl_xor_sync(0xffffffffu, v, 1);
+    constexpr int kSpan = 32 / K;  // lanes that hold the same sum
+    const int buf = use & 1, warps = tpr >> 5;
+    float* sums = reinterpret_cast<float*>(red.sums[buf]);
+    if (tpr == 32 || CLUSTER) {
+#pragma unroll
+        for (int k = 0; k < K; ++k) a[k] = __shfl_sync(0xffffffffu, v, k * kSpan);
+        if (!CLUSTER) return;
+        const uint32_t bar = smem_u32(&red.full[buf]);
+        if (threadIdx.x == 0) mbar_arrive_expect_tx(bar, static_cast<uint32_t>(j.ctas * warps * K * sizeof(float)));
+        if (lane < j.ctas) {  // lane l sends to CTA l
+            const uint32_t to = smem_u32(sums + (cluster_ctarank() * warps + warp) * K);
+            send_sums(map_to_rank(to, lane), map_to_rank(bar, lane), a);
+        }
+        if (!dead && !mbar_wait_cluster(bar, (use >> 1) & 1, j.st)) dead = true;
+    } else {
+        if (lane % kSpan == 0) sums[warp * K + lane / kSpan] = v;
+        __syncthreads();
+    }
+    ++use;
+    const int parts = CLUSTER ? warps * j.ctas : warps;
+    if (K == 4) {
+        float2 p = both(0.0f), q = both(0.0f);
+#pragma unroll 4
+        for (int w = 0; w < parts; ++w) {
+            const float4 t = reinterpret_cast<const float4*>(sums)[w];
+            p = add2(p, make_float2(t.x, t.y));
+            q = add2(q, make_float2(t.z, t.w));
+        }
+        a[0] = p.x, a[1] = p.y, a[2 % K] = q.x, a[3 % K] = q.y;
+    } else {
+        float2 p = both(0.0f);
+#pragma unroll 4
+        for (int w = 0; w < parts; ++w) p = add2(p, reinterpret_cast<const float2*>(sums)[w]);
+        a[0] = p.x, a[1] = p.y;
+    }
+}
+
 // Pieces of a row, and whether they are 16 bytes wide.
 inline bool norm_vec(const NormJob& j, bool backward) {
     const int es = elem_bytes(j.dtype);
@@ -128,10 +282,67 @@ inline int norm_pieces(const NormJob& j, bool vec) {
     return vec ? j.cols / n : static_cast<int>((static_cast<long long>(j.cols) + loose - 1) / loose * 32);
 }
 
+// How the ring kernels share out rows of p pieces: V pieces, 16 elements (one piece of
+// very short rows), for each of tpr threads of each of `ctas` CTAs.
+constexpr int kRingThreads = 32 * kMostWarps;
+constexpr int kStages = 3;                // batches of rows in flight, with the one that is worked on
+constexpr size_t kRingBytes = 204 << 10;  // of shared memory, at most
+struct RingShape {
+    int V, threads, tpr, ctas, per_cta;
+};
 inline int next_pow2(int v) {
     int p = 1;
     while (p < v) p <<= 1;
     return p;
+}
+// n: elements of a piece; copies: pieces in flight for each of a row.
+inline bool ring_shape(int p, int n, int copies, RingShape* s) {
+    const int few = 16 / n;
+    const int most = std::min(kRingThreads, static_cast<int>(kRingBytes / (sizeof(uint4) * copies * few)) / 32 * 32);
+    s->threads = 256;
+    s->V = p <= 4 ? 1 : few;
+    s->ctas = 1;
+    while (s->ctas < kMaxCtas && p > s->ctas * few * most) s->ctas *= 2;
+    // Five to six warps' worth of a processor left idle by one block cost more than the exchange.
+    if (s->ctas == 1 && p > 256 * few && p < 384 * few) s->ctas = 2;
+    s->per_cta = (p + s->ctas - 1) / s->ctas;
+    if (p <= 32 * few)
+        s->tpr = next_pow2((p + s->V - 1) / s->V);
+    else
+        s->threads = s->tpr = (s->per_cta + 32 * few - 1) / (32 * few) * 32;
+    return s->tpr <= most;
+}
+
+// Clusters (or blocks) that walk the rows, `resident` CTAs a processor. Not every
+// processor has its place in a cluster of four or eight (74 of 76 fours fitted), and one
+// that has to wait for the others to end would double the time.
+inline unsigned ring_clusters(const RingShape& c, long long batches, int num_sms, size_t smem) {
+    const int resident = std::max(1, std::min(512 / c.threads, static_cast<int>(kRingBytes / smem)));
+    long long fit = static_cast<long long>(num_sms) * resident / c.ctas;
+    if (c.ctas > 2) fit = fit * 15 / 16;
+    return static_cast<unsigned>(std::min(batches, std::max(1LL, fit)));
+}
+
+// Launches a ring kernel on the clusters that share its rows.
+template <typename... KArgs>
+int launch_ring(void (*kernel)(KArgs...), const RingShape& c, unsigned clusters, size_t smem, cudaStream_t s, const NormJob& j) {
+    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+    if (e != cudaSuccess) return e;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(clusters * c.ctas);
+    cfg.blockDim = dim3(c.threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = c.ctas;
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = c.ctas > 1 ? 2 : 1;
+    return cudaLaunchKernelEx(&cfg, kernel, j);
 }
 
 }  // namespace gns

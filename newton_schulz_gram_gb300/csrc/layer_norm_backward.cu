@@ -9,6 +9,7 @@
 //
 // Bound: HBM, x, dy (and the residual) read and dx written once.
 #include <algorithm>
+#include <type_traits>
 
 #include "layer_norm.cuh"
 #include "ptx.cuh"
@@ -19,8 +20,8 @@ namespace {
 // A block's sums of one piece's columns: the groups of a warp, then the warps, in
 // shared memory where several rows share the block.
 template <typename Piece, int N>
-__device__ __forceinline__ void store_sums(float (&acc)[N], const Piece& p, const NormJob& j, unsigned v, int at, float* part,
-                                           float* smem) {
+__device__ __forceinline__ void store_sums(float (&acc)[N], const Piece& p, const NormJob& j, unsigned v, unsigned end,
+                                           float* part, float* smem) {
     if (j.tpr <= 32) {
         const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
         for (int m = j.tpr; m < 32; m <<= 1) {
@@ -41,15 +42,14 @@ __device__ __forceinline__ void store_sums(float (&acc)[N], const Piece& p, cons
             acc[e] = sum;
         }
     }
-    if (v >= j.per_row) return;
+    if (v >= end) return;
 #pragma unroll
     for (int e = 0; e < N; ++e)
         if (piece_has(p, v, e, j.cols)) part[piece_column(p, v, e)] = acc[e];
 }
 
 // A row that a block's registers hold: up to kMostPieces pieces of each of
-// kMostThreads threads. (Four pieces of 16-bit values with their sums spill 40
-// registers: rows of 8193 to 16384 such columns.)
+// kMostThreads threads.
 constexpr int kMostPieces = 4, kMostThreads = 512;
 
 template <typename T, typename Piece, int V, bool SUMS>
@@ -149,10 +149,158 @@ __global__ void __launch_bounds__(kMostThreads) layer_norm_backward_kernel(NormJ
         const Piece p{};
 #pragma unroll
         for (int i = 0; i < V; ++i) {
-            store_sums(dw[i], p, j, at + i * j.tpr, at, part, smem);
-            if (j.dbias) store_sums(db[i], p, j, at + i * j.tpr, at, part + all, smem);
+            store_sums(dw[i], p, j, at + i * j.tpr, j.per_row, part, smem);
+            if (j.dbias) store_sums(db[i], p, j, at + i * j.tpr, j.per_row, part + all, smem);
         }
     }
+}
+
+// ------------------------------------------------------------- aligned rows
+//
+// The same with the rows copied to shared memory ahead of their use (cp.async): a
+// thread copies, and later reads, the pieces of its own columns alone, so the copies
+// need no barrier and hold no registers. FULL: every thread has all its pieces.
+// CLUSTER: rows of more columns than a CTA's registers have sums for are shared by the CTAs
+// of a cluster, which exchange the row's sums.
+
+template <typename T, int V, bool SUMS, bool FULL, bool CLUSTER>
+__global__ void __launch_bounds__(kRingThreads) layer_norm_backward_ring_kernel(NormJob j) {
+    constexpr int N = 16 / sizeof(T), P = N / 2;
+    extern __shared__ __align__(128) uint4 ring[];  // [stage][x, dy, residual][piece][thread]
+    __shared__ __align__(128) RowSums<2> red;
+    __shared__ float smem[SUMS ? 8 * 32 * N : 1];
+    int use = 0;
+    bool dead = false;
+    if (CLUSTER) {
+        if (threadIdx.x < 2) mbar_init(smem_u32(&red.full[threadIdx.x]), 1);
+        fence_mbar_init();
+        cluster_sync();
+    }
+    grid_dependency_wait();
+    grid_launch_dependents();
+    const int at = j.tpr <= 32 ? threadIdx.x & (j.tpr - 1) : threadIdx.x;
+    const int group = j.tpr <= 32 ? threadIdx.x / j.tpr : 0;
+    const int groups = blockDim.x / j.tpr, threads = blockDim.x;
+    const int rank = CLUSTER ? cluster_ctarank() : 0;
+    const int piece = rank * j.per_cta + at, pieces = min(j.per_row, (rank + 1) * j.per_cta);  // this thread's first, the CTA's end
+    const unsigned cluster = CLUSTER ? blockIdx.x / j.ctas : blockIdx.x, clusters = CLUSTER ? gridDim.x / j.ctas : gridDim.x;
+    const float inv = 1.0f / static_cast<float>(j.cols);
+    const unsigned rows = static_cast<unsigned>(j.rows), step = clusters * groups, first = cluster * groups + group;
+    const T* x = static_cast<const T*>(j.x) + first * j.ldx + piece * N;  // of the row fetched next
+    const T* dy = static_cast<const T*>(j.dy) + first * j.lddy + piece * N;
+    const T* res = static_cast<const T*>(j.residual) + (j.residual ? first * j.ldr + piece * N : 0);
+    T* dx = static_cast<T*>(j.dx) + first * j.lddx + piece * N;
+    const float* stats = j.stats + 2LL * first;
+    const long long x_step = step * j.ldx, dy_step = step * j.lddy, res_step = step * j.ldr, dx_step = step * j.lddx;
+    const int apart = j.tpr * N, kinds = j.residual ? 3 : 2;
+    const uint4* mine = ring + threadIdx.x;
+    const uint32_t slots = smem_u32(mine);
+    auto has = [&](int i) { return FULL || piece + i * j.tpr < pieces; };
+    unsigned ahead = first;
+    auto fetch = [&](int stage) {
+        float2 st = both(0.0f);
+        if (ahead < rows) {
+            st = make_float2(stats[0], stats[1]);
+#pragma unroll
+            for (int i = 0; i < V; ++i) {
+                if (!has(i)) continue;
+                const uint32_t to = slots + 16 * (stage * kinds * V + i) * threads;
+                copy16(to, x + i * apart);
+                copy16(to + 16 * V * threads, dy + i * apart);
+                if (kinds == 3) copy16(to + 32 * V * threads, res + i * apart);
+            }
+        }
+        copies_commit();
+        x += x_step, dy += dy_step, res += res_step, stats += 2LL * step, ahead += step;
+        return st;
+    };
+    float2 dw[V][P], db[V][P], w[V][P];
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+#pragma unroll
+        for (int e = 0; e < P; ++e) w[i][e] = both(1.0f), dw[i][e] = db[i][e] = both(0.0f);
+        if (j.weight && has(i)) {
+            float f[N];
+            const Wide<T, N> p{};
+            piece_weights(p, j.weight, j.wf32, piece + i * j.tpr, j.cols, f);
+#pragma unroll
+            for (int e = 0; e < P; ++e) w[i][e] = make_float2(f[2 * e], f[2 * e + 1]);
+        }
+    }
+    float2 st[kStages];  // mean and rstd of the rows in flight, the next one's first
+#pragma unroll
+    for (int k = 0; k < kStages - 1; ++k) st[k] = fetch(k);
+    int stage = 0;
+    for (unsigned row = first; row - group < rows; row += step, dx += dx_step) {
+        st[kStages - 1] = fetch(stage == 0 ? kStages - 1 : stage - 1);
+        copies_wait<kStages - 1>();
+        const bool live = row < rows;
+        const float rstd = st[0].y;
+        float2 h[V][P], g[V][P], c1 = both(0.0f), c2 = both(0.0f);
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            uint4 u = make_uint4(0, 0, 0, 0), d = u;
+            if (has(i) && live) {
+                u = mine[(stage * kinds * V + i) * threads];
+                d = mine[((stage * kinds + 1) * V + i) * threads];
+            }
+            unpack<T, N>(u, h[i]);
+            unpack<T, N>(d, g[i]);
+#pragma unroll
+            for (int e = 0; e < P; ++e) {
+                h[i][e] = mul2(add2(h[i][e], both(-st[0].x)), both(rstd));
+                if (SUMS) {
+                    dw[i][e] = fma2(g[i][e], h[i][e], dw[i][e]);
+                    db[i][e] = add2(db[i][e], g[i][e]);
+                }
+                g[i][e] = mul2(g[i][e], w[i][e]);
+                c1 = add2(c1, g[i][e]);
+                c2 = fma2(g[i][e], h[i][e], c2);
+            }
+        }
+        float c[2] = {c1.x + c1.y, c2.x + c2.y};
+        row_sums<2, CLUSTER>(c, j, red, use, dead);
+        if (live) {
+            const float2 minus = both(j.rms ? 0.0f : -c[0] * inv * rstd), by = both(-c[1] * inv);
+#pragma unroll
+            for (int i = 0; i < V; ++i) {
+                if (!has(i)) continue;
+                float2 r[P];
+                if (j.residual) {
+                    unpack<T, N>(mine[((stage * kinds + 2) * V + i) * threads], r);
+#pragma unroll
+                    for (int e = 0; e < P; ++e) r[e] = add2(r[e], minus);
+                } else {
+#pragma unroll
+                    for (int e = 0; e < P; ++e) r[e] = minus;
+                }
+#pragma unroll
+                for (int e = 0; e < P; ++e) r[e] = fma2(fma2(h[i][e], by, g[i][e]), both(rstd), r[e]);
+                *reinterpret_cast<uint4*>(dx + i * apart) = pack<T>(r);
+            }
+        }
+        stage = stage == kStages - 1 ? 0 : stage + 1;
+#pragma unroll
+        for (int k = 0; k < kStages - 1; ++k) st[k] = st[k + 1];
+    }
+    copies_wait<0>();
+    if (SUMS) {
+        float* part = j.part + static_cast<long long>(cluster) * j.cols;
+        const long long all = static_cast<long long>(clusters) * j.cols;
+        const Wide<T, N> p{};
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            float sum[N];
+#pragma unroll
+            for (int e = 0; e < P; ++e) sum[2 * e] = dw[i][e].x, sum[2 * e + 1] = dw[i][e].y;
+            store_sums(sum, p, j, piece + i * j.tpr, pieces, part, smem);
+            if (!j.dbias) continue;
+#pragma unroll
+            for (int e = 0; e < P; ++e) sum[2 * e] = db[i][e].x, sum[2 * e + 1] = db[i][e].y;
+            store_sums(sum, p, j, piece + i * j.tpr, pieces, part + all, smem);
+        }
+    }
+    if (CLUSTER) cluster_sync();  // no CTA ends while another may send to it
 }
 
 // Rows beyond a block's registers: the same in two passes over the row, the second
@@ -282,7 +430,9 @@ __global__ void __launch_bounds__(1024) layer_norm_join_kernel(const float* part
 
 struct Shape {
     bool vec, fits;
+    RingShape ring;
     int V, threads, tpr, per_row;
+    size_t smem;  // of the ring, 0 where the rows go through registers
     unsigned blocks, strips;  // strips: the column kernel's
     int parts;
 };
@@ -291,26 +441,26 @@ Shape shape_of(const NormJob& j, int num_sms) {
     Shape c{};
     c.vec = norm_vec(j, true);
     const int p = c.per_row = norm_pieces(j, c.vec);
-    c.V = p <= 32 ? 1 : p <= 1024 ? 2 : kMostPieces;
-    c.fits = p <= kMostPieces * kMostThreads;
+    c.fits = c.vec ? ring_shape(p, 16 / elem_bytes(j.dtype), kStages * (j.residual ? 3 : 2), &c.ring) : p <= kMostPieces * kMostThreads;
     if (!c.fits) {
         c.blocks = static_cast<unsigned>(std::min<long long>(j.rows, 4LL * num_sms));
         c.strips = static_cast<unsigned>((p + 255) / 256);
         c.parts = static_cast<int>(std::min<long long>(j.rows, std::max(1u, 8u * num_sms / c.strips)));
         return c;
     }
-    if (p <= 32) {
-        c.threads = 256;
-        c.tpr = next_pow2(p);
-    } else if (p <= 64) {
-        c.threads = 256;
-        c.tpr = 32;
+    if (c.vec) {
+        c.threads = c.ring.threads;
+        c.tpr = c.ring.tpr;
+        c.smem = sizeof(uint4) * kStages * (j.residual ? 3 : 2) * c.ring.V * c.threads;
+        const long long groups = c.threads / c.tpr;
+        c.blocks = ring_clusters(c.ring, (j.rows + groups - 1) / groups, num_sms, c.smem);
     } else {
+        c.V = p <= 32 ? 1 : p <= 1024 ? 2 : kMostPieces;
         c.threads = c.tpr = (p + 32 * c.V - 1) / (32 * c.V) * 32;
+        if (c.tpr == 32) c.threads = 256;
+        const long long groups = c.threads / c.tpr;
+        c.blocks = static_cast<unsigned>(std::min<long long>((j.rows + groups - 1) / groups, static_cast<long long>(num_sms) * std::max(1, 768 / c.threads)));
     }
-    const long long groups = c.threads / c.tpr;
-    c.blocks = static_cast<unsigned>(std::min<long long>((j.rows + groups - 1) / groups,
-                                                         static_cast<long long>(num_sms) * std::max(1, 768 / c.threads)));
     c.parts = static_cast<int>(c.blocks);
     return c;
 }
@@ -334,12 +484,25 @@ int launch_layer_norm_backward(NormJob j, int num_sms, cudaStream_t s) {
         if (!c.fits)
             return static_cast<int>(launch_after(c.vec ? layer_norm_backward_long_kernel<T, W> : layer_norm_backward_long_kernel<T, L>,
                                                  dim3(c.blocks), dim3(kLongThreads), 0, s, j));
+        if (c.vec) {
+            constexpr int few = 16 / (16 / sizeof(T));
+            const bool full = c.per_row == c.ring.V * c.tpr * c.ring.ctas;
+            j.ctas = c.ring.ctas;
+            j.per_cta = c.ring.per_cta;
+            const auto pick = [&](auto v, auto shared) {
+                constexpr int V = decltype(v)::value;
+                constexpr bool CLUSTER = decltype(shared)::value;
+                const auto run = [&](auto k) { return launch_ring(k, c.ring, c.blocks, c.smem, s, j); };
+                if (sums) return run(full ? layer_norm_backward_ring_kernel<T, V, true, true, CLUSTER> : layer_norm_backward_ring_kernel<T, V, true, false, CLUSTER>);
+                return run(full ? layer_norm_backward_ring_kernel<T, V, false, true, CLUSTER> : layer_norm_backward_ring_kernel<T, V, false, false, CLUSTER>);
+            };
+            if (c.ring.ctas > 1) return pick(std::integral_constant<int, few>{}, std::true_type{});
+            return c.ring.V == 1 ? pick(std::integral_constant<int, 1>{}, std::false_type{}) : pick(std::integral_constant<int, few>{}, std::false_type{});
+        }
         auto run = [&](auto k) { return static_cast<int>(launch_after(k, dim3(c.blocks), dim3(c.threads), 0, s, j)); };
         if (sums)
-            return c.vec ? run(c.V == 1 ? layer_norm_backward_kernel<T, W, 1, true> : c.V == 2 ? layer_norm_backward_kernel<T, W, 2, true> : layer_norm_backward_kernel<T, W, 4, true>)
-                         : run(c.V == 1 ? layer_norm_backward_kernel<T, L, 1, true> : c.V == 2 ? layer_norm_backward_kernel<T, L, 2, true> : layer_norm_backward_kernel<T, L, 4, true>);
-        return c.vec ? run(c.V == 1 ? layer_norm_backward_kernel<T, W, 1, false> : c.V == 2 ? layer_norm_backward_kernel<T, W, 2, false> : layer_norm_backward_kernel<T, W, 4, false>)
-                     : run(c.V == 1 ? layer_norm_backward_kernel<T, L, 1, false> : c.V == 2 ? layer_norm_backward_kernel<T, L, 2, false> : layer_norm_backward_kernel<T, L, 4, false>);
+            return run(c.V == 1 ? layer_norm_backward_kernel<T, L, 1, true> : c.V == 2 ? layer_norm_backward_kernel<T, L, 2, true> : layer_norm_backward_kernel<T, L, 4, true>);
+        return run(c.V == 1 ? layer_norm_backward_kernel<T, L, 1, false> : c.V == 2 ? layer_norm_backward_kernel<T, L, 2, false> : layer_norm_backward_kernel<T, L, 4, false>);
     });
 }
 

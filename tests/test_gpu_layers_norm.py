@@ -71,10 +71,13 @@ def check(gns, x, dy, res, w, b, rms, eps=1e-5):
 SHAPES = [(1, 1), (3, 1), (5, 7), (2, 8), (300, 16), (33, 24), (1, 4096), (257, 128), (70, 33), (513, 256), (300, 1024),
           (130, 712), (40, 1021), (9, 14336), (4, 14343), (700, 2048)]
 LONG = [(3, 16392), (2, 40001), (5, 20000)]
+# More rows than two a processor, which go through shared memory, and of those rows
+# that two, four and eight blocks share, whole and with a remainder.
+RING = [(305, 8), (400, 4096), (310, 4104), (307, 14336), (306, 8200), (308, 33000), (305, 60000), (310, 70008)]
 
 
 @pytest.mark.parametrize("dtype", list(DTYPES))
-@pytest.mark.parametrize("rows,cols", SHAPES + LONG)
+@pytest.mark.parametrize("rows,cols", SHAPES + LONG + RING)
 def test_types_and_widths(gns, rows, cols, dtype):
     for k, (rms, wdtype, bias, pad, with_res) in enumerate([(False, DTYPES[dtype], True, 0, True), (True, torch.float32, False, 0, False),
                                                             (False, torch.float32, True, 3, False), (True, None, True, 8, True)]):
