@@ -239,12 +239,13 @@ int gns_embedding_backward(const void* dy, int64_t lddy, const void* ids, int id
     Scratch scratch;
     RET(scratch.take(*st, embedding_plan(j, nullptr).bytes, s));
     const EmbeddingPlan p = embedding_plan(j, scratch.data());
+    CK(cudaMemsetAsync(p.ready, 0, p.cleared, s));
     for (int pass = 0; pass < p.passes; ++pass) {
         if (p.counts) LAUNCH(kClsEmbedding, launch_embedding_count(j, p, pass, s));
         LAUNCH(kClsEmbedding, launch_embedding_place(j, p, pass, s));
     }
     LAUNCH(kClsEmbedding, launch_embedding_runs(j, p, s));
-    LAUNCH(kClsEmbedding, launch_embedding_rows(j, p, s));
+    if (p.chunks > 1) LAUNCH(kClsEmbedding, launch_embedding_joins(j, p, s));
     return GNS_OK;
 }
 

@@ -42,6 +42,30 @@ __device__ __forceinline__ __nv_bfloat16 from_f32<__nv_bfloat16>(float v) {
     return __float2bfloat16_rn(v);
 }
 
+// Pairs of fp32 values, which one instruction adds, multiplies or accumulates.
+__device__ __forceinline__ unsigned long long pair_bits(float2 a) {
+    return static_cast<unsigned long long>(__float_as_uint(a.y)) << 32 | __float_as_uint(a.x);
+}
+__device__ __forceinline__ float2 pair_of(unsigned long long b) {
+    return make_float2(__uint_as_float(static_cast<unsigned>(b)), __uint_as_float(static_cast<unsigned>(b >> 32)));
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+    unsigned long long d;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(pair_bits(a)), "l"(pair_bits(b)));
+    return pair_of(d);
+}
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+    unsigned long long d;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(pair_bits(a)), "l"(pair_bits(b)));
+    return pair_of(d);
+}
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+    unsigned long long d;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(pair_bits(a)), "l"(pair_bits(b)), "l"(pair_bits(c)));
+    return pair_of(d);
+}
+__device__ __forceinline__ float2 both(float a) { return make_float2(a, a); }
+
 // N consecutive elements as they lie in memory, in 16-byte pieces; they start on
 // a 16-byte boundary.
 template <typename T, int N>
@@ -135,6 +159,16 @@ struct Loose {
     }
     __device__ __forceinline__ void forget() {}
 };
+
+// Copies to shared memory that the thread waits for itself.
+__device__ __forceinline__ void copy16(uint32_t to, const void* from) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to), "l"(from) : "memory");
+}
+__device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int LEFT>
+__device__ __forceinline__ void copies_wait() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(LEFT) : "memory");
+}
 
 // Launch with the programmatic-dependent-launch attribute: the kernel calls
 // grid_dependency_wait() before it reads what an earlier grid wrote or

@@ -5,15 +5,17 @@
 // __match_any_sync groups the lanes of one digit, a lane's rank in its group
 // is the popcount of the lanes before it, and the warp's running count of
 // the digit (its own column of shared memory, so no atomics) gives the rest.
-// Up to kOneBlock slots a single block does it all. Beyond, a first kernel
+// Up to `alone` slots a single block does it all. Beyond, a first kernel
 // stores each block's counts and the second one's blocks sum, each for
 // itself, the counts of all blocks and of those before it: nblocks * (G + 1)
 // loads that stay in L2, which is less than the round trip of a third launch
 // for up to kMaxBlocks blocks.
 //
-// A source says what is sorted: digit(s), the digit of slot s; place(s, at), called
-// once for every slot with its place; start(d, at), called once for every digit with
-// the place of its first slot.
+// A source says what is sorted: digit(s), the digit of slot s; note(s), called for every
+// slot by each kernel; place(s, at), called once for every slot with its place; start(d,
+// at), called once for every digit with the place of its first slot; extra(b), called by
+// the b-th of the blocks that a launch has beside the sort's, which is bound by latency
+// and leaves most of the GPU free for them.
 #pragma once
 
 #include <algorithm>
@@ -25,27 +27,33 @@ namespace gns {
 
 constexpr int kSortWarps = 16;
 constexpr int kSortThreads = 32 * kSortWarps;
-constexpr int kOneBlock = 4096;
 constexpr int kMaxBlocks = 152;
 constexpr int kMaxDigit = 1024;
 
+// How n slots are shared out: one block up to `alone` of them, else blocks of at least `tile`.
+struct SortPlan {
+    long long n;
+    int G;
+    long long alone, tile;
+};
+
 inline size_t sort_smem(int G) { return sizeof(int) * static_cast<size_t>(G + 1) * (kSortWarps + 1); }
 
-inline long long sort_blocks(long long n) {
-    if (n <= kOneBlock) return 1;
-    return std::min<long long>(kMaxBlocks, (n + 2047) / 2048);
+inline long long sort_blocks(const SortPlan& p) {
+    if (p.n <= p.alone) return 1;
+    return std::min<long long>(kMaxBlocks, (p.n + p.tile - 1) / p.tile);
 }
 
 // Slots per block, a multiple of 32 per warp.
-inline long long sort_span(long long n) {
-    const long long per = (n + sort_blocks(n) - 1) / sort_blocks(n);
+inline long long sort_span(const SortPlan& p) {
+    const long long per = (p.n + sort_blocks(p) - 1) / sort_blocks(p);
     return (per + kSortThreads - 1) / kSortThreads * kSortThreads;
 }
 
 // Bytes of the blocks' counts, 0 where one block does it all.
-inline size_t sort_scratch(long long n, int G) {
-    const long long b = sort_blocks(n);
-    return b > 1 ? sizeof(int) * static_cast<size_t>(b) * (G + 1) : 0;
+inline size_t sort_scratch(const SortPlan& p) {
+    const long long b = sort_blocks(p);
+    return b > 1 ? sizeof(int) * static_cast<size_t>(b) * (p.G + 1) : 0;
 }
 
 // Counts of this warp's run of slots into its column cnt[0 .. G].
@@ -56,19 +64,24 @@ __device__ __forceinline__ void count_run(const Source& src, long long beg, long
         const int e = s < end ? src.digit(s) : -1;
         const unsigned peers = __match_any_sync(0xffffffffu, e);
         if (e >= 0 && (peers & ((1u << lane) - 1)) == 0) cnt[e] += __popc(peers);
+        src.note(s, e >= 0);
         __syncwarp();
     }
 }
 
 template <typename Source>
 __global__ void __launch_bounds__(kSortThreads) sort_count_kernel(Source src, long long n, int G, long long span,
-                                                                  int* hist) {
+                                                                  int blocks, int* hist) {
     extern __shared__ int smem[];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     for (int i = threadIdx.x; i < (G + 1) * kSortWarps; i += kSortThreads) smem[i] = 0;
     grid_dependency_wait();
     grid_launch_dependents();
     __syncthreads();
+    if (static_cast<int>(blockIdx.x) >= blocks) {
+        src.extra(blockIdx.x - blocks);
+        return;
+    }
     const long long run = span / kSortWarps;
     const long long beg = blockIdx.x * span + warp * run;
     count_run(src, beg, min(beg + run, n), smem + warp * (G + 1), lane);
@@ -83,15 +96,19 @@ __global__ void __launch_bounds__(kSortThreads) sort_count_kernel(Source src, lo
 // hist null: the grid is one block and its own counts are all there are.
 template <typename Source>
 __global__ void __launch_bounds__(kSortThreads) sort_place_kernel(Source src, long long n, int G, long long span,
-                                                                  const int* hist) {
+                                                                  int blocks, const int* hist) {
     extern __shared__ int smem[];
     __shared__ int warp_sum[kSortWarps];
-    int* first = smem + (G + 1) * kSortWarps;  // first place of this block's slots of each expert
+    int* first = smem + (G + 1) * kSortWarps;  // first place of this block's slots of each digit
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     for (int i = threadIdx.x; i < (G + 1) * kSortWarps; i += kSortThreads) smem[i] = 0;
     grid_dependency_wait();
     grid_launch_dependents();
     __syncthreads();
+    if (static_cast<int>(blockIdx.x) >= blocks) {
+        src.extra(blockIdx.x - blocks);
+        return;
+    }
     const long long run = span / kSortWarps;
     const long long beg = blockIdx.x * span + warp * run;
     const long long end = min(beg + run, n);
@@ -99,7 +116,7 @@ __global__ void __launch_bounds__(kSortThreads) sort_place_kernel(Source src, lo
     count_run(src, beg, end, cnt, lane);
     __syncthreads();
 
-    // Totals of all blocks, scanned over the experts: thread t owns experts
+    // Totals of all blocks, scanned over the digits: thread t owns digits
     // t * per .. t * per + per - 1.
     constexpr int kPer = (kMaxDigit + 1 + kSortThreads - 1) / kSortThreads;
     const int per = (G + kSortThreads) / kSortThreads;  // ceil((G + 1) / threads)
@@ -112,7 +129,7 @@ __global__ void __launch_bounds__(kSortThreads) sort_place_kernel(Source src, lo
         if (i >= per || e > G) continue;
         if (hist) {
 #pragma unroll 8
-            for (int b = 0; b < static_cast<int>(gridDim.x); ++b) {
+            for (int b = 0; b < blocks; ++b) {
                 const int c = hist[static_cast<long long>(b) * (G + 1) + e];
                 total[i] += c;
                 if (b < static_cast<int>(blockIdx.x)) before[i] += c;
@@ -141,7 +158,7 @@ __global__ void __launch_bounds__(kSortThreads) sort_place_kernel(Source src, lo
         start += total[i];
     }
     __syncthreads();
-    // Each warp's first place per expert: the block's, plus the warps before it.
+    // Each warp's first place per digit: the block's, plus the warps before it.
     for (int e = threadIdx.x; e <= G; e += kSortThreads) {
         int at = first[e];
         for (int w = 0; w < kSortWarps; ++w) {
@@ -168,25 +185,25 @@ __global__ void __launch_bounds__(kSortThreads) sort_place_kernel(Source src, lo
 }
 
 template <typename... KArgs, typename... Args>
-int sort_step(void (*kernel)(KArgs...), long long n, int G, cudaStream_t s, Args... args) {
-    const size_t smem = sort_smem(G);
+int sort_step(void (*kernel)(KArgs...), const SortPlan& p, unsigned extra, cudaStream_t s, Args... args) {
+    const size_t smem = sort_smem(p.G);
     if (smem > 48 * 1024) {
         const cudaError_t e =
             cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
         if (e != cudaSuccess) return e;
     }
-    return launch_after(kernel, dim3(static_cast<unsigned>(sort_blocks(n))), dim3(kSortThreads), smem, s, args...);
+    return launch_after(kernel, dim3(static_cast<unsigned>(sort_blocks(p)) + extra), dim3(kSortThreads), smem, s, args...);
 }
 
 // The two kernels; the first is left out where sort_scratch() is 0 (hist null).
 template <typename Source>
-int launch_sort_count(const Source& src, long long n, int G, int* hist, cudaStream_t s) {
-    return sort_step(sort_count_kernel<Source>, n, G, s, src, n, G, sort_span(n), hist);
+int launch_sort_count(const Source& src, const SortPlan& p, int* hist, cudaStream_t s, unsigned extra = 0) {
+    return sort_step(sort_count_kernel<Source>, p, extra, s, src, p.n, p.G, sort_span(p), static_cast<int>(sort_blocks(p)), hist);
 }
 
 template <typename Source>
-int launch_sort_place(const Source& src, long long n, int G, const int* hist, cudaStream_t s) {
-    return sort_step(sort_place_kernel<Source>, n, G, s, src, n, G, sort_span(n), hist);
+int launch_sort_place(const Source& src, const SortPlan& p, const int* hist, cudaStream_t s, unsigned extra = 0) {
+    return sort_step(sort_place_kernel<Source>, p, extra, s, src, p.n, p.G, sort_span(p), static_cast<int>(sort_blocks(p)), hist);
 }
 
 }  // namespace gns

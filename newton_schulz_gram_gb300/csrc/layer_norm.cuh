@@ -117,40 +117,6 @@ __device__ __forceinline__ void row_sum2(float& a, float& b, int tpr, float2* re
     }
 }
 
-// Copies to shared memory that the thread waits for itself.
-__device__ __forceinline__ void copy16(uint32_t to, const void* from) {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to), "l"(from) : "memory");
-}
-__device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int LEFT>
-__device__ __forceinline__ void copies_wait() {
-    asm volatile("cp.async.wait_group %0;" ::"n"(LEFT) : "memory");
-}
-
-// Pairs of fp32 values, which one instruction adds, multiplies or accumulates.
-__device__ __forceinline__ unsigned long long pair_bits(float2 a) {
-    return static_cast<unsigned long long>(__float_as_uint(a.y)) << 32 | __float_as_uint(a.x);
-}
-__device__ __forceinline__ float2 pair_of(unsigned long long b) {
-    return make_float2(__uint_as_float(static_cast<unsigned>(b)), __uint_as_float(static_cast<unsigned>(b >> 32)));
-}
-__device__ __forceinline__ float2 add2(float2 a, float2 b) {
-    unsigned long long d;
-    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(pair_bits(a)), "l"(pair_bits(b)));
-    return pair_of(d);
-}
-__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
-    unsigned long long d;
-    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(pair_bits(a)), "l"(pair_bits(b)));
-    return pair_of(d);
-}
-__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
-    unsigned long long d;
-    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(pair_bits(a)), "l"(pair_bits(b)), "l"(pair_bits(c)));
-    return pair_of(d);
-}
-__device__ __forceinline__ float2 both(float a) { return make_float2(a, a); }
-
 // The 16 bytes of a piece as pairs and back.
 template <typename T, int N>
 __device__ __forceinline__ void unpack(const uint4& u, float2 (&f)[N / 2]) {

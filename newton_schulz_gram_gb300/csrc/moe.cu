@@ -32,12 +32,16 @@ struct ExpertSlots {
         const I v = ids[s];
         return v >= 0 && v < static_cast<I>(G) ? static_cast<int>(v) : G;
     }
+    __device__ __forceinline__ void note(long long, bool) const {}
+    __device__ __forceinline__ void extra(unsigned) const {}
     __device__ __forceinline__ void place(long long s, int at) const {
         rows[s] = at;
         slots[at] = static_cast<int>(s);
     }
     __device__ __forceinline__ void start(int e, int at) const { offsets[e] = at; }  // offsets[G]: the slots with an expert
 };
+
+SortPlan plan_of(long long n, int G) { return {n, G, 4096, 2048}; }
 
 template <typename I>
 ExpertSlots<I> slots_of(const SortJob& j) {
@@ -245,16 +249,16 @@ dim3 walk_grid(const Walk& w) {
 
 }  // namespace
 
-size_t moe_sort_scratch(long long n, int G) { return sort_scratch(n, G); }
+size_t moe_sort_scratch(long long n, int G) { return sort_scratch(plan_of(n, G)); }
 
 int launch_moe_count(const SortJob& j, cudaStream_t s) {
-    return j.id_bytes == 8 ? launch_sort_count(slots_of<long long>(j), j.n, j.G, j.hist, s)
-                           : launch_sort_count(slots_of<int>(j), j.n, j.G, j.hist, s);
+    return j.id_bytes == 8 ? launch_sort_count(slots_of<long long>(j), plan_of(j.n, j.G), j.hist, s)
+                           : launch_sort_count(slots_of<int>(j), plan_of(j.n, j.G), j.hist, s);
 }
 
 int launch_moe_place(const SortJob& j, cudaStream_t s) {
-    return j.id_bytes == 8 ? launch_sort_place(slots_of<long long>(j), j.n, j.G, j.hist, s)
-                           : launch_sort_place(slots_of<int>(j), j.n, j.G, j.hist, s);
+    return j.id_bytes == 8 ? launch_sort_place(slots_of<long long>(j), plan_of(j.n, j.G), j.hist, s)
+                           : launch_sort_place(slots_of<int>(j), plan_of(j.n, j.G), j.hist, s);
 }
 
 int launch_moe_gather(const RouteJob& j, const void* x, long long ldx, void* y, long long ldy, cudaStream_t s) {
