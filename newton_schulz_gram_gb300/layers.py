@@ -223,9 +223,9 @@ def gns_embedding_backward(dy, ids, vocab, scale=1.0, out_dtype=None, stream=Non
     cols], 2D with contiguous rows or contiguous) summed by id in token order, times
     scale, zero for the others; out_dtype None for dy's."""
     _typed(dy, "dy")
+    tokens = _token_ids(ids, dy)
     if dy.dim() < 1 or dy.shape[:-1] != ids.shape:
         raise ValueError("dy must be [*ids.shape, cols]")
-    tokens = _token_ids(ids, dy)
     if dy.dim() == 2:
         _, cols, lddy = _matrix(dy, "dy")
     else:
