@@ -266,6 +266,122 @@ __global__ void __launch_bounds__(kRingThreads) layer_norm_ring_kernel(NormJob j
     if (CLUSTER) cluster_sync();  // no CTA ends while another may send to it
 }
 
+// ----------------------------------------------------------- unaligned rows
+//
+// The same with the row's words in shared memory and a thread's columns tpr apart, so
+// that neighbouring lanes read and write neighbouring elements.
+
+template <typename T>
+__global__ void __launch_bounds__(kRingThreads) layer_norm_loose_kernel(NormJob j) {
+    constexpr int R = 2, P = kLoosePairs;
+    extern __shared__ __align__(128) uint4 ring[];  // [stage][row][group][window]
+    __shared__ __align__(128) RowSums<2 * R> red;
+    int use = 0;
+    bool dead = false;
+    grid_dependency_wait();
+    grid_launch_dependents();
+    const int at = j.tpr <= 32 ? threadIdx.x & (j.tpr - 1) : threadIdx.x;
+    const int group = j.tpr <= 32 ? threadIdx.x / j.tpr : 0;
+    const int groups = blockDim.x / j.tpr, tpr = j.tpr, window = window_bytes(j.cols * static_cast<int>(sizeof(T)));
+    const float inv = 1.0f / static_cast<float>(j.cols);
+    const unsigned rows = static_cast<unsigned>(j.rows), batch = groups * R, step = gridDim.x * batch;
+    const unsigned first = blockIdx.x * batch + group;
+    const T* x = static_cast<const T*>(j.x) + first * j.ldx;  // of the rows worked on
+    const T* x_ahead = x;                                     // of those fetched next
+    T* y = static_cast<T*>(j.y) + first * j.ldy;
+    const long long x_step = step * j.ldx, y_step = step * j.ldy, x_row = groups * j.ldx, y_row = groups * j.ldy;
+    const char* slots = reinterpret_cast<const char*>(ring) + group * window;
+    auto slot = [&](int stage, int r) { return slots + (stage * R + r) * groups * window; };
+    unsigned ahead = first;
+    auto fetch = [&](int stage) {
+#pragma unroll
+        for (int r = 0; r < R; ++r)
+            if (ahead + r * groups < rows) copy_window(smem_u32(slot(stage, r)), x_ahead + r * x_row, j.cols, at, tpr);
+        copies_commit();
+        x_ahead += x_step;
+        ahead += step;
+    };
+    const int whole = whole_pairs(j), last = at + 2 * whole * tpr;  // the last pair's first column
+    const bool lo = last < j.cols, hi = last + tpr < j.cols;
+    // Calls fn with each pair of the thread, its first column and which of the two there are.
+    auto pairs = [&](auto&& fn) {
+#pragma unroll
+        for (int q = 0; q < P - 1; ++q)
+            if (q < whole) fn(q, at + 2 * q * tpr, true, true);
+        fn(P - 1, last, lo, hi);
+    };
+    auto weight = [&](const void* v, int c) { return j.wf32 ? static_cast<const float*>(v)[c] : to_f32<T>(static_cast<const T*>(v)[c]); };
+    float2 w[P], b[P];
+    pairs([&](int q, int c, bool has0, bool has1) {
+        w[q] = both(1.0f), b[q] = both(0.0f);
+        if (j.weight && has0) w[q].x = weight(j.weight, c);
+        if (j.weight && has1) w[q].y = weight(j.weight, c + tpr);
+        if (j.bias && has0) b[q].x = weight(j.bias, c);
+        if (j.bias && has1) b[q].y = weight(j.bias, c + tpr);
+    });
+#pragma unroll
+    for (int k = 0; k < kStages - 1; ++k) fetch(k);
+    int stage = 0;
+    for (unsigned row = first; row - group < rows; row += step, x += x_step, y += y_step) {
+        copies_wait<kStages - 2>();
+        row_barrier(tpr);
+        fetch(stage == 0 ? kStages - 1 : stage - 1);
+        float2 f[R][P];
+        float mean[R];
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+            // Behind the last row its slot's bytes are whatever they are, and not used.
+            const T* in = in_window(slot(stage, r), x + r * x_row);
+            float2 sum = both(0.0f);
+            pairs([&](int q, int c, bool has0, bool has1) {
+                f[r][q] = make_float2(has0 ? to_f32<T>(in[c]) : 0.0f, has1 ? to_f32<T>(in[c + tpr]) : 0.0f);
+                sum = add2(sum, f[r][q]);
+            });
+            mean[r] = sum.x + sum.y;
+        }
+        if (j.rms) {
+#pragma unroll
+            for (int r = 0; r < R; ++r) mean[r] = 0.0f;
+        } else {
+            row_sums<R, false>(mean, j, red, use, dead);
+        }
+        float c[2 * R];  // sums of the deviations and of their squares
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+            mean[r] *= inv;
+            float2 dev = both(0.0f), squares = both(0.0f);
+            pairs([&](int q, int, bool has0, bool has1) {
+                f[r][q] = add2(f[r][q], both(-mean[r]));
+                if (!has0) f[r][q].x = 0.0f;
+                if (!has1) f[r][q].y = 0.0f;
+                dev = add2(dev, f[r][q]);
+                squares = fma2(f[r][q], f[r][q], squares);
+            });
+            c[2 * r] = dev.x + dev.y;
+            c[2 * r + 1] = squares.x + squares.y;
+        }
+        row_sums<2 * R, false>(c, j, red, use, dead);
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+            const unsigned o = row + r * groups;
+            if (o >= rows) break;
+            const float dev = j.rms ? 0.0f : c[2 * r] * inv, rstd = norm_rstd(c[2 * r + 1] * inv, dev, j.eps);
+            if (at == 0) {
+                j.stats[2LL * o] = mean[r] + dev;
+                j.stats[2LL * o + 1] = rstd;
+            }
+            T* to = y + r * y_row;
+            pairs([&](int q, int c, bool has0, bool has1) {
+                const float2 v = fma2(fma2(f[r][q], both(rstd), both(-dev * rstd)), w[q], b[q]);
+                if (has0) to[c] = from_f32<T>(v.x);
+                if (has1) to[c + tpr] = from_f32<T>(v.y);
+            });
+        }
+        stage = stage == kStages - 1 ? 0 : stage + 1;
+    }
+    copies_wait<0>();
+}
+
 // Rows beyond the registers of a block: read three times, the later ones from L2.
 constexpr int kLongThreads = 1024;
 
@@ -376,6 +492,14 @@ int launch_layer_norm(NormJob j, int num_sms, cudaStream_t s) {
             if (c.ctas > 1) return run(full ? layer_norm_ring_kernel<T, few, true, true> : layer_norm_ring_kernel<T, few, false, true>);
             if (c.V == 1) return run(full ? layer_norm_ring_kernel<T, 1, true, false> : layer_norm_ring_kernel<T, 1, false, false>);
             return run(full ? layer_norm_ring_kernel<T, few, true, false> : layer_norm_ring_kernel<T, few, false, false>);
+        }
+        if (!vec && j.rows > 2 * num_sms && loose_shape(j.cols, &c)) {
+            const long long groups = c.threads / c.tpr, batch = 2 * groups;
+            const size_t smem = static_cast<size_t>(kStages) * batch * window_bytes(j.cols * static_cast<int>(sizeof(T)));
+            if (smem <= kRingBytes) {
+                j.tpr = c.tpr;
+                return launch_ring(layer_norm_loose_kernel<T>, c, ring_clusters(c, (j.rows + batch - 1) / batch, num_sms, smem), smem, s, j);
+            }
         }
         if (!fits) {
             const unsigned b = static_cast<unsigned>(std::min<long long>(j.rows, 2LL * num_sms));

@@ -40,6 +40,7 @@ struct NormJob {
     DevStatus st;   // of waits among the CTAs of a row
     int tpr, per_row;  // set by the launchers
     int ctas, per_cta;  // of the ring kernels: CTAs that share a row, and pieces of each
+    int stages;         // of unaligned rows, backward: rows in flight with the one that is worked on, 2 or 3
 };
 
 int launch_layer_norm(NormJob job, int num_sms, cudaStream_t s);
@@ -287,6 +288,53 @@ inline unsigned ring_clusters(const RingShape& c, long long batches, int num_sms
     long long fit = static_cast<long long>(num_sms) * resident / c.ctas;
     if (c.ctas > 2) fit = fit * 15 / 16;
     return static_cast<unsigned>(std::min(batches, std::max(1LL, fit)));
+}
+
+// Rows that are not 16-byte aligned are copied as the aligned 16-byte words that hold
+// them, by the threads of a row together, to a slot that has room for one word more.
+// Words are whole or not there: the bytes before and behind a row that come along are
+// never used.
+// A thread has pairs of columns: pair q is at + 2 q tpr and at + (2 q + 1) tpr. `whole`
+// pairs, alike for all threads, lie in the row, the next may in part.
+constexpr int kLoosePairs = 8;
+__device__ __forceinline__ int whole_pairs(const NormJob& j) { return (j.cols - 1) / (2 * j.tpr); }
+
+__host__ __device__ __forceinline__ int window_bytes(int row_bytes) { return (row_bytes + 15) / 16 * 16 + 16; }
+
+template <typename T>
+__device__ __forceinline__ void copy_window(uint32_t slot, const T* row, int cols, int at, int tpr) {
+    const uintptr_t a = reinterpret_cast<uintptr_t>(row);
+    const char* base = reinterpret_cast<const char*>(a & ~static_cast<uintptr_t>(15));
+    const int words = (static_cast<int>(a & 15) + cols * static_cast<int>(sizeof(T)) + 15) >> 4;
+    for (int w = at; w < words; w += tpr) copy16(slot + 16 * w, base + 16 * w);
+}
+
+// The row's first element in its slot.
+template <typename T>
+__device__ __forceinline__ const T* in_window(const char* slot, const T* row) {
+    return reinterpret_cast<const T*>(slot + (reinterpret_cast<uintptr_t>(row) & 15));
+}
+
+// After a thread's own copies have come: those of the others of its row, too, and the
+// others are done with the rows before.
+__device__ __forceinline__ void row_barrier(int tpr) {
+    if (tpr <= 32)
+        __syncwarp();
+    else
+        __syncthreads();
+}
+
+inline bool loose_shape(int cols, RingShape* s) {
+    constexpr int each = 2 * kLoosePairs;
+    s->V = 1;
+    s->ctas = 1;
+    s->per_cta = 0;
+    s->threads = 256;
+    if (cols <= 32 * each)
+        s->tpr = next_pow2((cols + each - 1) / each);
+    else
+        s->threads = s->tpr = (cols + 32 * each - 1) / (32 * each) * 32;
+    return s->tpr <= kRingThreads;
 }
 
 // Launches a ring kernel on the clusters that share its rows.

@@ -17,11 +17,10 @@
 namespace gns {
 namespace {
 
-// A block's sums of one piece's columns: the groups of a warp, then the warps, in
-// shared memory where several rows share the block.
-template <typename Piece, int N>
-__device__ __forceinline__ void store_sums(float (&acc)[N], const Piece& p, const NormJob& j, unsigned v, unsigned end,
-                                           float* part, float* smem) {
+// A block's sums of N of a thread's columns, col(e) or -1: the groups of a warp, then the
+// warps, in shared memory, where several rows share the block.
+template <int N, typename Col>
+__device__ __forceinline__ void store_sums(float (&acc)[N], const NormJob& j, float* part, float* smem, Col&& col) {
     if (j.tpr <= 32) {
         const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
         for (int m = j.tpr; m < 32; m <<= 1) {
@@ -42,116 +41,10 @@ __device__ __forceinline__ void store_sums(float (&acc)[N], const Piece& p, cons
             acc[e] = sum;
         }
     }
-    if (v >= end) return;
 #pragma unroll
-    for (int e = 0; e < N; ++e)
-        if (piece_has(p, v, e, j.cols)) part[piece_column(p, v, e)] = acc[e];
-}
-
-// A row that a block's registers hold: up to kMostPieces pieces of each of
-// kMostThreads threads.
-constexpr int kMostPieces = 4, kMostThreads = 512;
-
-template <typename T, typename Piece, int V, bool SUMS>
-__global__ void __launch_bounds__(kMostThreads) layer_norm_backward_kernel(NormJob j) {
-    constexpr int N = Piece::kSize;
-    __shared__ float2 red[2][32];
-    __shared__ float smem[SUMS ? 8 * 32 * N : 1];
-    int phase = 0;
-    grid_dependency_wait();
-    grid_launch_dependents();
-    const int at = j.tpr <= 32 ? threadIdx.x & (j.tpr - 1) : threadIdx.x;
-    const int group = j.tpr <= 32 ? threadIdx.x / j.tpr : 0;
-    const int groups = blockDim.x / j.tpr;
-    const float n = static_cast<float>(j.cols);
-    const T* x = static_cast<const T*>(j.x);
-    const T* dy = static_cast<const T*>(j.dy);
-    const T* res = static_cast<const T*>(j.residual);
-    T* dx = static_cast<T*>(j.dx);
-    float dw[V][N], db[V][N];
-#pragma unroll
-    for (int i = 0; i < V; ++i)
-#pragma unroll
-        for (int e = 0; e < N; ++e) dw[i][e] = db[i][e] = 0.0f;
-    for (long long r0 = static_cast<long long>(blockIdx.x) * groups; r0 < j.rows; r0 += static_cast<long long>(gridDim.x) * groups) {
-        const long long r = r0 + group;
-        const bool live = r < j.rows;
-        Piece px[V], pd[V];
-#pragma unroll
-        for (int i = 0; i < V; ++i) {
-            const unsigned v = at + i * j.tpr;
-            if (live && v < j.per_row) {
-                px[i].load_stream(x + r * j.ldx, v, j.cols);
-                pd[i].load_stream(dy + r * j.lddy, v, j.cols);
-            } else {
-                px[i].clear();
-                pd[i].clear();
-            }
-        }
-        const float mean = live ? j.stats[2 * r] : 0.0f, rstd = live ? j.stats[2 * r + 1] : 0.0f;
-        float c1 = 0.0f, c2 = 0.0f;
-#pragma unroll
-        for (int i = 0; i < V; ++i) {
-            const unsigned v = at + i * j.tpr;
-            float f[N], d[N], w[N];
-            px[i].get(f);
-            pd[i].get(d);
-            if (j.weight && v < j.per_row) {
-                piece_weights(px[i], j.weight, j.wf32, v, j.cols, w);
-            } else {
-#pragma unroll
-                for (int e = 0; e < N; ++e) w[e] = 1.0f;
-            }
-#pragma unroll
-            for (int e = 0; e < N; ++e) {
-                const float h = (f[e] - mean) * rstd, g = d[e] * w[e];
-                c1 += g;
-                c2 = fmaf(g, h, c2);
-                if (SUMS) {
-                    dw[i][e] = fmaf(d[e], h, dw[i][e]);
-                    db[i][e] += d[e];
-                }
-            }
-        }
-        row_sum2(c1, c2, j.tpr, red[phase ^= 1]);
-        c1 = j.rms ? 0.0f : c1 / n;
-        c2 /= n;
-#pragma unroll
-        for (int i = 0; i < V; ++i) {
-            const unsigned v = at + i * j.tpr;
-            if (!live || v >= j.per_row) continue;
-            float f[N], d[N], w[N];
-            px[i].get(f);
-            pd[i].get(d);
-            if (j.weight) {
-                piece_weights(px[i], j.weight, j.wf32, v, j.cols, w);
-            } else {
-#pragma unroll
-                for (int e = 0; e < N; ++e) w[e] = 1.0f;
-            }
-#pragma unroll
-            for (int e = 0; e < N; ++e) f[e] = (d[e] * w[e] - c1 - (f[e] - mean) * rstd * c2) * rstd;
-            if (res) {
-                Piece pr;
-                pr.load_stream(res + r * j.ldr, v, j.cols);
-                pr.get(d);
-#pragma unroll
-                for (int e = 0; e < N; ++e) f[e] += d[e];
-            }
-            Piece o;
-            o.set(f);
-            o.store(dx + r * j.lddx, v, j.cols);
-        }
-    }
-    if (SUMS) {
-        float* part = j.part + static_cast<long long>(blockIdx.x) * j.cols;
-        const long long all = static_cast<long long>(gridDim.x) * j.cols;
-        const Piece p{};
-#pragma unroll
-        for (int i = 0; i < V; ++i) {
-            store_sums(dw[i], p, j, at + i * j.tpr, j.per_row, part, smem);
-            if (j.dbias) store_sums(db[i], p, j, at + i * j.tpr, j.per_row, part + all, smem);
-        }
+    for (int e = 0; e < N; ++e) {
+        const int c = col(e);
+        if (c >= 0) part[c] = acc[e];
     }
 }
 
@@ -287,20 +180,153 @@ __global__ void __launch_bounds__(kRingThreads) layer_norm_backward_ring_kernel(
     if (SUMS) {
         float* part = j.part + static_cast<long long>(cluster) * j.cols;
         const long long all = static_cast<long long>(clusters) * j.cols;
-        const Wide<T, N> p{};
 #pragma unroll
         for (int i = 0; i < V; ++i) {
+            const int v = piece + i * j.tpr;
+            const auto col = [&](int e) { return v < pieces ? v * N + e : -1; };
             float sum[N];
 #pragma unroll
             for (int e = 0; e < P; ++e) sum[2 * e] = dw[i][e].x, sum[2 * e + 1] = dw[i][e].y;
-            store_sums(sum, p, j, piece + i * j.tpr, pieces, part, smem);
+            store_sums(sum, j, part, smem, col);
             if (!j.dbias) continue;
 #pragma unroll
             for (int e = 0; e < P; ++e) sum[2 * e] = db[i][e].x, sum[2 * e + 1] = db[i][e].y;
-            store_sums(sum, p, j, piece + i * j.tpr, pieces, part + all, smem);
+            store_sums(sum, j, part + all, smem, col);
         }
     }
     if (CLUSTER) cluster_sync();  // no CTA ends while another may send to it
+}
+
+// ----------------------------------------------------------- unaligned rows
+//
+// The same with the row's words in shared memory and a thread's columns tpr apart.
+
+template <typename T, bool SUMS>
+__global__ void __launch_bounds__(kRingThreads) layer_norm_backward_loose_kernel(NormJob j) {
+    constexpr int P = kLoosePairs;
+    extern __shared__ __align__(128) uint4 ring[];  // [stage][x, dy, residual][group][window]
+    __shared__ __align__(128) RowSums<2> red;
+    __shared__ float smem[SUMS ? 8 * 32 * P : 1];
+    int use = 0;
+    bool dead = false;
+    grid_dependency_wait();
+    grid_launch_dependents();
+    const int at = j.tpr <= 32 ? threadIdx.x & (j.tpr - 1) : threadIdx.x;
+    const int group = j.tpr <= 32 ? threadIdx.x / j.tpr : 0;
+    const int groups = blockDim.x / j.tpr, tpr = j.tpr, window = window_bytes(j.cols * static_cast<int>(sizeof(T)));
+    const float inv = 1.0f / static_cast<float>(j.cols);
+    const unsigned rows = static_cast<unsigned>(j.rows), step = gridDim.x * groups, first = blockIdx.x * groups + group;
+    const T* x = static_cast<const T*>(j.x) + first * j.ldx;  // of the row worked on
+    const T* dy = static_cast<const T*>(j.dy) + first * j.lddy;
+    const T* res = static_cast<const T*>(j.residual) + (j.residual ? first * j.ldr : 0);
+    const T *x_ahead = x, *dy_ahead = dy, *res_ahead = res;  // of the row fetched next
+    T* dx = static_cast<T*>(j.dx) + first * j.lddx;
+    const float* stats = j.stats + 2LL * first;
+    const long long x_step = step * j.ldx, dy_step = step * j.lddy, res_step = step * j.ldr, dx_step = step * j.lddx;
+    const int kinds = j.residual ? 3 : 2;
+    const char* slots = reinterpret_cast<const char*>(ring) + group * window;
+    auto slot = [&](int stage, int kind) { return slots + (stage * kinds + kind) * groups * window; };
+    unsigned ahead = first;
+    auto fetch = [&](int stage) {
+        float2 st = both(0.0f);
+        if (ahead < rows) {
+            st = make_float2(stats[0], stats[1]);
+            copy_window(smem_u32(slot(stage, 0)), x_ahead, j.cols, at, tpr);
+            copy_window(smem_u32(slot(stage, 1)), dy_ahead, j.cols, at, tpr);
+            if (kinds == 3) copy_window(smem_u32(slot(stage, 2)), res_ahead, j.cols, at, tpr);
+        }
+        copies_commit();
+        x_ahead += x_step, dy_ahead += dy_step, res_ahead += res_step, stats += 2LL * step, ahead += step;
+        return st;
+    };
+    const int whole = whole_pairs(j), last = at + 2 * whole * tpr;  // the last pair's first column
+    const bool lo = last < j.cols, hi = last + tpr < j.cols;
+    // Calls fn with each pair of the thread, its first column and which of the two there are.
+    auto pairs = [&](auto&& fn) {
+#pragma unroll
+        for (int q = 0; q < P - 1; ++q)
+            if (q < whole) fn(q, at + 2 * q * tpr, true, true);
+        fn(P - 1, last, lo, hi);
+    };
+    auto weight = [&](int c) { return j.wf32 ? static_cast<const float*>(j.weight)[c] : to_f32<T>(static_cast<const T*>(j.weight)[c]); };
+    float2 dw[P], db[P], w[P];
+#pragma unroll
+    for (int q = 0; q < P; ++q) w[q] = both(1.0f), dw[q] = db[q] = both(0.0f);
+    pairs([&](int q, int c, bool has0, bool has1) {
+        if (j.weight && has0) w[q].x = weight(c);
+        if (j.weight && has1) w[q].y = weight(c + tpr);
+    });
+    const bool deep = j.stages == 3;
+    float2 st[3];  // mean and rstd of the rows in flight, the next one's first
+    st[0] = fetch(0);
+    if (deep) st[1] = fetch(1);
+    int stage = 0;
+    for (unsigned row = first; row - group < rows; row += step, x += x_step, dy += dy_step, res += res_step, dx += dx_step) {
+        if (deep)
+            copies_wait<1>();
+        else
+            copies_wait<0>();
+        row_barrier(tpr);
+        if (deep)
+            st[2] = fetch(stage == 0 ? 2 : stage - 1);
+        else
+            st[1] = fetch(stage ^ 1);
+        const float mean = st[0].x, rstd = st[0].y;
+        float2 h[P], g[P], c1 = both(0.0f), c2 = both(0.0f);
+        const T* xs = in_window(slot(stage, 0), x);
+        const T* ds = in_window(slot(stage, 1), dy);
+        const bool live = row < rows;
+        if (live) {
+            pairs([&](int q, int c, bool has0, bool has1) {
+                // A column that is not there has dy = 0 and x = mean.
+                h[q] = make_float2(has0 ? to_f32<T>(xs[c]) : mean, has1 ? to_f32<T>(xs[c + tpr]) : mean);
+                g[q] = make_float2(has0 ? to_f32<T>(ds[c]) : 0.0f, has1 ? to_f32<T>(ds[c + tpr]) : 0.0f);
+                h[q] = mul2(add2(h[q], both(-mean)), both(rstd));
+                if (SUMS) {
+                    dw[q] = fma2(g[q], h[q], dw[q]);
+                    db[q] = add2(db[q], g[q]);
+                }
+                g[q] = mul2(g[q], w[q]);
+                c1 = add2(c1, g[q]);
+                c2 = fma2(g[q], h[q], c2);
+            });
+        }
+        float c[2] = {c1.x + c1.y, c2.x + c2.y};
+        row_sums<2, false>(c, j, red, use, dead);
+        if (live) {
+            const float2 minus = both(j.rms ? 0.0f : -c[0] * inv * rstd), by = both(-c[1] * inv);
+            const T* rs = in_window(slot(stage, kinds - 1), res);
+            pairs([&](int q, int c, bool has0, bool has1) {
+                float2 r = minus;
+                if (kinds == 3) r = add2(r, make_float2(has0 ? to_f32<T>(rs[c]) : 0.0f, has1 ? to_f32<T>(rs[c + tpr]) : 0.0f));
+                r = fma2(fma2(h[q], by, g[q]), both(rstd), r);
+                if (has0) dx[c] = from_f32<T>(r.x);
+                if (has1) dx[c + tpr] = from_f32<T>(r.y);
+            });
+        }
+        stage = stage == j.stages - 1 ? 0 : stage + 1;
+        st[0] = st[1], st[1] = st[2];
+    }
+    copies_wait<0>();
+    if (SUMS) {
+        float* part = j.part + static_cast<long long>(blockIdx.x) * j.cols;
+        const long long all = static_cast<long long>(gridDim.x) * j.cols;
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+            const auto col = [&](int q) {
+                const int c = (q < P - 1 ? at + 2 * q * tpr : last) + half * tpr;
+                return (q < P - 1 && q >= whole) || c >= j.cols ? -1 : c;
+            };
+            float sum[P];
+#pragma unroll
+            for (int q = 0; q < P; ++q) sum[q] = half ? dw[q].y : dw[q].x;
+            store_sums(sum, j, part, smem, col);
+            if (!j.dbias) continue;
+#pragma unroll
+            for (int q = 0; q < P; ++q) sum[q] = half ? db[q].y : db[q].x;
+            store_sums(sum, j, part + all, smem, col);
+        }
+    }
 }
 
 // Rows beyond a block's registers: the same in two passes over the row, the second
@@ -431,37 +457,33 @@ __global__ void __launch_bounds__(1024) layer_norm_join_kernel(const float* part
 struct Shape {
     bool vec, fits;
     RingShape ring;
-    int V, threads, tpr, per_row;
-    size_t smem;  // of the ring, 0 where the rows go through registers
-    unsigned blocks, strips;  // strips: the column kernel's
-    int parts;
+    size_t smem;
+    unsigned blocks, strips;  // blocks: of clusters; strips: the column kernel's
+    int per_row, parts, stages;
 };
 
 Shape shape_of(const NormJob& j, int num_sms) {
     Shape c{};
+    const int es = elem_bytes(j.dtype), kinds = j.residual ? 3 : 2;
     c.vec = norm_vec(j, true);
-    const int p = c.per_row = norm_pieces(j, c.vec);
-    c.fits = c.vec ? ring_shape(p, 16 / elem_bytes(j.dtype), kStages * (j.residual ? 3 : 2), &c.ring) : p <= kMostPieces * kMostThreads;
+    c.per_row = norm_pieces(j, c.vec);
+    c.fits = c.vec ? ring_shape(c.per_row, 16 / es, kStages * kinds, &c.ring) : loose_shape(j.cols, &c.ring);
+    if (c.fits) {
+        const long long groups = c.ring.threads / c.ring.tpr;
+        const size_t stage = static_cast<size_t>(kinds) * (c.vec ? sizeof(uint4) * c.ring.V * c.ring.threads : groups * window_bytes(j.cols * es));
+        // Two unaligned rows in flight rather than three where that lets more blocks share a
+        // processor. (Aligned ones: the branch costs more, 100 us instead of 89 for 16384 x 4096.)
+        c.stages = !c.vec && kRingBytes / (kStages * stage) * c.ring.threads < 512 ? kStages - 1 : kStages;
+        c.smem = c.stages * stage;
+        c.blocks = ring_clusters(c.ring, (j.rows + groups - 1) / groups, num_sms, c.smem);
+        c.parts = static_cast<int>(c.blocks);
+        c.fits = c.smem <= kRingBytes;
+    }
     if (!c.fits) {
         c.blocks = static_cast<unsigned>(std::min<long long>(j.rows, 4LL * num_sms));
-        c.strips = static_cast<unsigned>((p + 255) / 256);
+        c.strips = static_cast<unsigned>((c.per_row + 255) / 256);
         c.parts = static_cast<int>(std::min<long long>(j.rows, std::max(1u, 8u * num_sms / c.strips)));
-        return c;
     }
-    if (c.vec) {
-        c.threads = c.ring.threads;
-        c.tpr = c.ring.tpr;
-        c.smem = sizeof(uint4) * kStages * (j.residual ? 3 : 2) * c.ring.V * c.threads;
-        const long long groups = c.threads / c.tpr;
-        c.blocks = ring_clusters(c.ring, (j.rows + groups - 1) / groups, num_sms, c.smem);
-    } else {
-        c.V = p <= 32 ? 1 : p <= 1024 ? 2 : kMostPieces;
-        c.threads = c.tpr = (p + 32 * c.V - 1) / (32 * c.V) * 32;
-        if (c.tpr == 32) c.threads = 256;
-        const long long groups = c.threads / c.tpr;
-        c.blocks = static_cast<unsigned>(std::min<long long>((j.rows + groups - 1) / groups, static_cast<long long>(num_sms) * std::max(1, 768 / c.threads)));
-    }
-    c.parts = static_cast<int>(c.blocks);
     return c;
 }
 
@@ -475,7 +497,10 @@ size_t norm_backward_scratch(const NormJob& j, int num_sms) {
 int launch_layer_norm_backward(NormJob j, int num_sms, cudaStream_t s) {
     const Shape c = shape_of(j, num_sms);
     j.per_row = c.per_row;
-    j.tpr = c.tpr;
+    j.tpr = c.ring.tpr;
+    j.ctas = c.ring.ctas;
+    j.per_cta = c.ring.per_cta;
+    j.stages = c.stages;
     const bool sums = j.dweight || j.dbias;
     return by_dtype(j.dtype, [&](auto t) {
         using T = decltype(t);
@@ -484,25 +509,18 @@ int launch_layer_norm_backward(NormJob j, int num_sms, cudaStream_t s) {
         if (!c.fits)
             return static_cast<int>(launch_after(c.vec ? layer_norm_backward_long_kernel<T, W> : layer_norm_backward_long_kernel<T, L>,
                                                  dim3(c.blocks), dim3(kLongThreads), 0, s, j));
-        if (c.vec) {
-            constexpr int few = 16 / (16 / sizeof(T));
-            const bool full = c.per_row == c.ring.V * c.tpr * c.ring.ctas;
-            j.ctas = c.ring.ctas;
-            j.per_cta = c.ring.per_cta;
-            const auto pick = [&](auto v, auto shared) {
-                constexpr int V = decltype(v)::value;
-                constexpr bool CLUSTER = decltype(shared)::value;
-                const auto run = [&](auto k) { return launch_ring(k, c.ring, c.blocks, c.smem, s, j); };
-                if (sums) return run(full ? layer_norm_backward_ring_kernel<T, V, true, true, CLUSTER> : layer_norm_backward_ring_kernel<T, V, true, false, CLUSTER>);
-                return run(full ? layer_norm_backward_ring_kernel<T, V, false, true, CLUSTER> : layer_norm_backward_ring_kernel<T, V, false, false, CLUSTER>);
-            };
-            if (c.ring.ctas > 1) return pick(std::integral_constant<int, few>{}, std::true_type{});
-            return c.ring.V == 1 ? pick(std::integral_constant<int, 1>{}, std::false_type{}) : pick(std::integral_constant<int, few>{}, std::false_type{});
-        }
-        auto run = [&](auto k) { return static_cast<int>(launch_after(k, dim3(c.blocks), dim3(c.threads), 0, s, j)); };
-        if (sums)
-            return run(c.V == 1 ? layer_norm_backward_kernel<T, L, 1, true> : c.V == 2 ? layer_norm_backward_kernel<T, L, 2, true> : layer_norm_backward_kernel<T, L, 4, true>);
-        return run(c.V == 1 ? layer_norm_backward_kernel<T, L, 1, false> : c.V == 2 ? layer_norm_backward_kernel<T, L, 2, false> : layer_norm_backward_kernel<T, L, 4, false>);
+        const auto run = [&](auto k) { return launch_ring(k, c.ring, c.blocks, c.smem, s, j); };
+        if (!c.vec) return sums ? run(layer_norm_backward_loose_kernel<T, true>) : run(layer_norm_backward_loose_kernel<T, false>);
+        constexpr int few = 16 / (16 / sizeof(T));
+        const bool full = c.per_row == c.ring.V * c.ring.tpr * c.ring.ctas;
+        const auto pick = [&](auto v, auto shared) {
+            constexpr int V = decltype(v)::value;
+            constexpr bool CLUSTER = decltype(shared)::value;
+            if (sums) return run(full ? layer_norm_backward_ring_kernel<T, V, true, true, CLUSTER> : layer_norm_backward_ring_kernel<T, V, true, false, CLUSTER>);
+            return run(full ? layer_norm_backward_ring_kernel<T, V, false, true, CLUSTER> : layer_norm_backward_ring_kernel<T, V, false, false, CLUSTER>);
+        };
+        if (c.ring.ctas > 1) return pick(std::integral_constant<int, few>{}, std::true_type{});
+        return c.ring.V == 1 ? pick(std::integral_constant<int, 1>{}, std::false_type{}) : pick(std::integral_constant<int, few>{}, std::false_type{});
     });
 }
 
