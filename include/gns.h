@@ -427,10 +427,12 @@ int gns_fp8_linear(const void* x, int64_t ldx, int dtype, int rows, const int32_
  */
 
 /*
- * gns_layer_norm: each of `rows` rows of cols elements (up to 2^24),
+ * gns_layer_norm: each of `rows` rows of cols elements (1 to 2^24),
  *   y = (x - mean) * rstd * weight + bias, rstd = 1 / sqrt(var + eps),
  * var the mean of (x - mean)^2; with rms != 0 the mean is taken as 0 (the
  * root-mean-square form). The squares are fp32: deviations beyond 1e19 overflow.
+ * Rows that are not 16-byte aligned are read in aligned 16-byte words, of which the
+ * first may begin before the row.
  *   weight, bias  [cols], fp32 or of x's type (weight_dtype), NULL for 1 and 0.
  *   stats         fp32 [rows][2], written: mean and rstd, for the backward pass.
  */

@@ -20,7 +20,7 @@ constexpr int kMaxNormCols = 1 << 24;  // as far as fp32 counts
 
 int check_norm(int64_t rows, int cols, int dtype, int weight_dtype) {
     if (rows < 0 || rows > 0x7fffffffLL) return invalid("rows must be in 0..2^31 - 1");
-    if (cols < 0 || cols > kMaxNormCols) return invalid("cols must be in 0..2^24");
+    if (cols < 1 || cols > kMaxNormCols) return invalid("cols must be in 1..2^24");
     if (bad_dtype(dtype)) return invalid("unknown dtype");
     if (weight_dtype != dtype && weight_dtype != GNS_FP32) return invalid("weight and bias must be fp32 or of x's type");
     return GNS_OK;
@@ -61,7 +61,7 @@ int gns_layer_norm(const void* x, int64_t ldx, int64_t rows, int cols, int dtype
                    int weight_dtype, double eps, int rms, void* y, int64_t ldy, float* stats, void* stream) {
     RET(check_norm(rows, cols, dtype, weight_dtype));
     if (!(eps >= 0.0 && std::isfinite(static_cast<float>(eps)))) return invalid("eps must be a finite fp32 value of at least 0");
-    if (rows == 0 || cols == 0) return GNS_OK;
+    if (rows == 0) return GNS_OK;
     if (!x || !y || !stats) return invalid("null pointer");
     if (ldx < cols || ldy < cols) return invalid("a row stride must cover the columns");
     DeviceState* st = nullptr;
@@ -90,7 +90,6 @@ int gns_layer_norm_backward(const void* dy, int64_t lddy, const void* x, int64_t
                             int cols, int dtype, const void* weight, int weight_dtype, int rms, const void* residual,
                             int64_t ldr, void* dx, int64_t lddx, void* dweight, void* dbias, void* stream) {
     RET(check_norm(rows, cols, dtype, weight_dtype));
-    if (cols == 0) return GNS_OK;
     if (rows > 0 && (!dy || !x || !stats || !dx)) return invalid("null pointer");
     if (rows > 0 && (lddy < cols || ldx < cols || lddx < cols || (residual && ldr < cols)))
         return invalid("a row stride must cover the columns");

@@ -292,8 +292,8 @@ inline unsigned ring_clusters(const RingShape& c, long long batches, int num_sms
 
 // Rows that are not 16-byte aligned are copied as the aligned 16-byte words that hold
 // them, by the threads of a row together, to a slot that has room for one word more.
-// Words are whole or not there: the bytes before and behind a row that come along are
-// never used.
+// The bytes of its first word before a row come along and are never used; those behind
+// its end are not read.
 // A thread has pairs of columns: pair q is at + 2 q tpr and at + (2 q + 1) tpr. `whole`
 // pairs, alike for all threads, lie in the row, the next may in part.
 constexpr int kLoosePairs = 8;
@@ -305,8 +305,8 @@ template <typename T>
 __device__ __forceinline__ void copy_window(uint32_t slot, const T* row, int cols, int at, int tpr) {
     const uintptr_t a = reinterpret_cast<uintptr_t>(row);
     const char* base = reinterpret_cast<const char*>(a & ~static_cast<uintptr_t>(15));
-    const int words = (static_cast<int>(a & 15) + cols * static_cast<int>(sizeof(T)) + 15) >> 4;
-    for (int w = at; w < words; w += tpr) copy16(slot + 16 * w, base + 16 * w);
+    const int bytes = static_cast<int>(a & 15) + cols * static_cast<int>(sizeof(T));
+    for (int w = at; 16 * w < bytes; w += tpr) copy16(slot + 16 * w, base + 16 * w, min(16, bytes - 16 * w));
 }
 
 // The row's first element in its slot.

@@ -71,11 +71,11 @@ def test_output_types(gns, dtype, out):
 def test_one_id_everywhere(gns, tokens):
     """Every run of the sorted tokens begins and ends inside one id; with padding, the last ones outside the table."""
     rng = np.random.default_rng(tokens)
-    dy = strided(tokens, 48, 0, torch.float32, rng)
-    for share in (0.0, 0.3):
-        ids = torch.full((tokens,), 5, device="cuda")
-        ids[torch.from_numpy(rng.random(tokens) < share).cuda()] = -1
-        gradient(gns, dy, ids, 9, 1.0)
+    for dy in (strided(tokens, 48, 0, torch.float32, rng), strided(tokens, 33, 0, torch.bfloat16, rng)):
+        for share in (0.0, 0.3):
+            ids = torch.full((tokens,), 5, device="cuda")
+            ids[torch.from_numpy(rng.random(tokens) < share).cuda()] = -1
+            gradient(gns, dy, ids, 9, 1.0)
 
 
 def test_runs_that_end_at_the_chunks(gns):

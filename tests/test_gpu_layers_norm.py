@@ -72,8 +72,10 @@ SHAPES = [(1, 1), (3, 1), (5, 7), (2, 8), (300, 16), (33, 24), (1, 4096), (257, 
           (130, 712), (40, 1021), (9, 14336), (4, 14343), (700, 2048)]
 LONG = [(3, 16392), (2, 40001), (5, 20000)]
 # More rows than two a processor, which go through shared memory, and of those rows
-# that two, four and eight blocks share, whole and with a remainder.
-RING = [(305, 8), (400, 4096), (310, 4104), (307, 14336), (306, 8200), (308, 33000), (305, 60000), (310, 70008)]
+# that two, four and eight blocks share, whole and with a remainder; unaligned ones up
+# to the last that fits and beyond.
+RING = [(305, 8), (400, 4096), (310, 4104), (307, 14336), (306, 8200), (308, 33000), (305, 60000), (310, 70008),
+        (1000, 7), (400, 33), (330, 257), (310, 1001), (311, 8191), (308, 8193)]
 
 
 @pytest.mark.parametrize("dtype", list(DTYPES))
@@ -174,3 +176,20 @@ def test_gradients_against_differences(gns):
         # Third derivatives give about step^2 = 1e-4 of the value, fp32 outputs 2^-23 / step per summand.
         scale = (grad.double() * d.double()).abs().sum().item()
         assert abs((ends[0] - ends[1]) / 2e-2 - want) < 2e-3 * scale + 1e-3, at
+
+
+@pytest.mark.parametrize("cols", [2056, 2049])
+def test_more_than_2_31_elements(gns, cols):
+    """Row offsets past 32 bits (4.3 GB a tensor), aligned and not: the rows at the
+    beginning, around 2^31 elements and at the end."""
+    rows = (1 << 20) + 5
+    x = torch.randn(rows, cols, dtype=torch.bfloat16, device="cuda")
+    w = torch.randn(cols, device="cuda")
+    y, stats = gns.gns_layer_norm(x, w)
+    dx = gns.gns_layer_norm_backward(y, x, stats, w)[0]
+    for at in (0, (1 << 31) // cols - 2, rows - 4):
+        part = slice(at, at + 4)
+        want = L.layer_norm(f64(x[part]), f64(w))
+        assert_close(y[part], want[0], (np.abs(want[1]) + 1) * np.abs(f64(w)), DEPTH, "y")
+        exact = L.layer_norm_backward(f64(y[part]), f64(x[part]), f64(w))[0]
+        assert np.linalg.norm(f64(dx[part]) - exact) < 2 * 2.0 ** -8 * np.linalg.norm(exact)
