@@ -9,16 +9,21 @@ tensors on the stream of the call, gradients are functions of their own.
 from __future__ import annotations
 
 import torch
+from torch.autograd import forward_ad as _forward_ad
 
 from ._lib import call
-from .block import DTYPES, _contiguous, _counts, _matrix, _new, _on, _out_type, _ptr, _same_device, _typed
+from .block import _MOST, DTYPES, _contiguous, _counts, _matrix, _new, _on, _out_type, _ptr, _same_device, _typed
 
 
 # --------------------------------------------------------------- layer norm
 
-def _norm_vector(t, name, x, cols, dtypes):
+def _norm_vector(t, name, x, cols):
     """A weight or bias: contiguous [cols], fp32 or of x's type."""
-    _typed(t, name, dtypes)
+    if (isinstance(t, torch.Tensor) and (t.dtype is torch.float32 or t.dtype is x.dtype) and t.get_device() == x.get_device()
+            and t.dim() == 1 and t.shape[0] == cols and t.is_contiguous() and t.is_cuda and not t.requires_grad
+            and _forward_ad._current_level < 0):
+        return
+    _typed(t, name, {torch.float32, x.dtype})
     if t.dim() != 1 or t.shape[0] != cols or not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous with one value per column")
     _same_device(x, name, t)
@@ -31,13 +36,14 @@ def gns_layer_norm(x, weight=None, bias=None, eps=1e-5, rms=False, stream=None):
     taken off. stats fp32 [rows, 2]: the mean (0 with rms) and 1 / sqrt(variance +
     eps), for the backward pass."""
     rows, cols, ldx = _matrix(x, "x")
-    _counts("a size", rows, cols)
+    if rows > _MOST or cols > _MOST:
+        _counts("a size", rows, cols)
     wdtype = x.dtype
     if weight is not None:
-        _norm_vector(weight, "weight", x, cols, {torch.float32, x.dtype})
+        _norm_vector(weight, "weight", x, cols)
         wdtype = weight.dtype
     if bias is not None:
-        _norm_vector(bias, "bias", x, cols, {torch.float32, x.dtype})
+        _norm_vector(bias, "bias", x, cols)
         if weight is not None and bias.dtype != wdtype:
             raise TypeError("weight and bias must have the same type")
         wdtype = bias.dtype
@@ -48,23 +54,24 @@ def gns_layer_norm(x, weight=None, bias=None, eps=1e-5, rms=False, stream=None):
     return y, stats
 
 
+def _like(t, name, dy):
+    """The row stride of a tensor of dy's type, shape and device."""
+    rows, cols, ld = _matrix(t, name, {dy.dtype})
+    if t.shape != dy.shape:
+        raise ValueError(f"{name} must have the shape of dy")
+    _same_device(dy, name, t)
+    return ld
+
+
 def gns_layer_norm_backward(dy, x, stats, weight=None, bias=False, rms=False, residual=None, stream=None):
     """The gradients (dx, dweight, dbias) of gns_layer_norm, from its x, stats,
     weight and rms. residual: the gradient that reaches x past the norm, added to
     dx. dweight (None without a weight) and, with bias, dbias (else None) have the
     weight's type, fp32 without a weight."""
     rows, cols, lddy = _matrix(dy, "dy")
-    _counts("a size", rows, cols)
-    ld = [lddy]
-    for name, t in (("x", x), ("residual", residual)):
-        if t is None:
-            ld.append(0)
-            continue
-        r, c, l = _matrix(t, name, {dy.dtype})
-        if r != rows or c != cols:
-            raise ValueError(f"{name} must have the shape of dy")
-        _same_device(dy, name, t)
-        ld.append(l)
+    if rows > _MOST or cols > _MOST:
+        _counts("a size", rows, cols)
+    ldx, ldr = _like(x, "x", dy), 0 if residual is None else _like(residual, "residual", dy)
     _contiguous(stats, torch.float32, "stats")
     if stats.dim() != 2 or stats.shape[0] != rows or stats.shape[1] != 2:
         raise ValueError("stats must be [rows, 2]")
@@ -72,14 +79,14 @@ def gns_layer_norm_backward(dy, x, stats, weight=None, bias=False, rms=False, re
     dweight = dbias = None
     wdtype = torch.float32
     if weight is not None:
-        _norm_vector(weight, "weight", dy, cols, {torch.float32, dy.dtype})
+        _norm_vector(weight, "weight", dy, cols)
         wdtype = weight.dtype
         dweight = _new((cols,), wdtype, dy, stream)
     if bias:
         dbias = _new((cols,), wdtype, dy, stream)
     dx = _new((rows, cols), dy.dtype, dy, stream)
-    call("gns_layer_norm_backward", dy.get_device(), dy.data_ptr(), lddy, x.data_ptr(), ld[1], stats.data_ptr(), rows, cols,
-         DTYPES[dy.dtype], _ptr(weight), DTYPES[wdtype], 1 if rms else 0, _ptr(residual), ld[2], dx.data_ptr(), cols,
+    call("gns_layer_norm_backward", dy.get_device(), dy.data_ptr(), lddy, x.data_ptr(), ldx, stats.data_ptr(), rows, cols,
+         DTYPES[dy.dtype], _ptr(weight), DTYPES[wdtype], 1 if rms else 0, _ptr(residual), ldr, dx.data_ptr(), cols,
          _ptr(dweight), _ptr(dbias), _on(dy, stream))
     return dx, dweight, dbias
 
@@ -127,7 +134,8 @@ def gns_moe_gate(logits, topk, normalize=True, stream=None):
     is never chosen, where too few are left the last ids are -1 with weight 0.
     Returns a MoeGate, whose ids gns_moe_sort takes."""
     tokens, experts, ld = _matrix(logits, "logits")
-    _counts("a size", tokens, experts, topk)
+    if tokens > _MOST or experts > _MOST or topk > _MOST:
+        _counts("a size", tokens, experts, topk)
     if not 0 < topk <= experts:
         raise ValueError("topk must be in 1 .. the number of experts")
     ids = _new((tokens, topk), torch.int64, logits, stream)
