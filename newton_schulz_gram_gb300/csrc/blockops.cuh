@@ -42,28 +42,12 @@ __device__ __forceinline__ __nv_bfloat16 from_f32<__nv_bfloat16>(float v) {
     return __float2bfloat16_rn(v);
 }
 
-// Pairs of fp32 values, which one instruction adds, multiplies or accumulates.
-__device__ __forceinline__ unsigned long long pair_bits(float2 a) {
-    return static_cast<unsigned long long>(__float_as_uint(a.y)) << 32 | __float_as_uint(a.x);
-}
-__device__ __forceinline__ float2 pair_of(unsigned long long b) {
-    return make_float2(__uint_as_float(static_cast<unsigned>(b)), __uint_as_float(static_cast<unsigned>(b >> 32)));
-}
-__device__ __forceinline__ float2 add2(float2 a, float2 b) {
-    unsigned long long d;
-    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(pair_bits(a)), "l"(pair_bits(b)));
-    return pair_of(d);
-}
-__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
-    unsigned long long d;
-    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(pair_bits(a)), "l"(pair_bits(b)));
-    return pair_of(d);
-}
-__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
-    unsigned long long d;
-    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(pair_bits(a)), "l"(pair_bits(b)), "l"(pair_bits(c)));
-    return pair_of(d);
-}
+// Pairs of fp32 values. (With the paired instructions, add.rn.f32x2 and the like, layer
+// norm took the same time: 16384 x 4096 52.2 us forward and 89.4 backward, 52.1 and 88.5
+// without.)
+__device__ __forceinline__ float2 add2(float2 a, float2 b) { return make_float2(a.x + b.x, a.y + b.y); }
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) { return make_float2(a.x * b.x, a.y * b.y); }
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) { return make_float2(fmaf(a.x, b.x, c.x), fmaf(a.y, b.y, c.y)); }
 __device__ __forceinline__ float2 both(float a) { return make_float2(a, a); }
 
 // N consecutive elements as they lie in memory, in 16-byte pieces; they start on
