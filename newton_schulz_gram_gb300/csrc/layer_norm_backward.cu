@@ -7,7 +7,11 @@
 // second kernel adds the blocks' in their order. Which rows a block takes follows
 // from the sizes and the number of SMs alone, so results repeat.
 //
-// Bound: HBM, x, dy (and the residual) read and dx written once.
+// Bound: HBM, x, dy (and the residual) read and dx written once. 16384 x 4096 bf16 with
+// fp32 weights: 73 us (5.5 TB/s), with the residual 89 (6.1), of which the second kernel
+// is 6; 262144 x 128: 37 (5.5); 4096 x 14336 by two CTAs a row: 106 (4.4); unaligned
+// 65536 x 257: 55, 16384 x 4093: 165, by instructions (single elements to and from
+// shared memory, 30 a value).
 #include <algorithm>
 #include <type_traits>
 
@@ -52,7 +56,8 @@ __device__ __forceinline__ void store_sums(float (&acc)[N], const NormJob& j, fl
 //
 // The same with the rows copied to shared memory ahead of their use (cp.async): a
 // thread copies, and later reads, the pieces of its own columns alone, so the copies
-// need no barrier and hold no registers. FULL: every thread has all its pieces.
+// need no barrier and hold no registers (loaded to registers instead, 160 us for
+// 16384 x 4096). FULL: every thread has all its pieces.
 // CLUSTER: rows of more columns than a CTA's registers have sums for are shared by the CTAs
 // of a cluster, which exchange the row's sums.
 

@@ -7,7 +7,10 @@
 // a lane each, in expert order, and their ranks among one another are their slots. Only
 // where more than 32 reach it (many equal logits) are they drawn one after the other.
 //
-// Bound: latency. 16384 tokens of 256 fp32 logits are 17 MB, 2.5 us of HBM.
+// Bound: instructions and latency; 16384 tokens of 256 fp32 logits are 17 MB, 2.5 us of
+// HBM. Those with their 8 experts take 12 us (drawn one after the other 15, by a maximum
+// over every lane's values each time 20), the balance loss 11, the gradient of both 8.5;
+// one token 2.3, 5.8 and 2.5.
 #include <algorithm>
 #include <type_traits>
 

@@ -98,6 +98,32 @@ def test_threads_that_share_a_stream(gns):
     assert bad == []
 
 
+def test_threads_whose_calls_differ_in_shared_memory(gns):
+    """One kernel with much and with little shared memory, and the sort with many and with
+    more digits, from two threads at once: neither call takes the other's limit away."""
+    wide, narrow = torch.randn(400, 7168, device="cuda").bfloat16(), torch.randn(400, 1024, device="cuda").bfloat16()
+    ids = torch.randint(0, 760, (3000, 2), device="cuda")
+    bad = []
+
+    def work(x, experts):
+        with torch.cuda.stream(torch.cuda.Stream()):
+            for _ in range(300):
+                try:
+                    gns.gns_layer_norm(x)
+                    gns.gns_moe_sort(ids, experts)
+                except gns.GnsError as e:
+                    bad.append(str(e))
+
+    threads = [threading.Thread(target=work, args=a) for a in ((wide, 1024), (narrow, 760), (wide, 800), (narrow, 1000))]
+    torch.cuda.synchronize()
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    torch.cuda.synchronize()
+    assert bad == []
+
+
 def test_two_captured_graphs_outlive_later_calls(gns):
     """Each graph has intermediate memory of its own: replayed in turn, between
     calls that use the library's and others' memory."""
