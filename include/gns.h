@@ -515,8 +515,8 @@ int gns_embedding(const void* ids, int id_bytes, int64_t tokens, const void* tab
  *   dtable[v] = scale * sum over the tokens t with ids[t] = v of dy[t],
  * 0 for a row without a token. dy is of dtype, dtable of out_dtype; fp32 sums in
  * token order, joined over runs of sorted tokens, rounded once. Takes intermediate
- * memory: 16 bytes per token, and 8 cols bytes for each run of 32 tokens, or for each
- * of at most 2048 longer runs.
+ * memory: 16 bytes per token, one per row of the table, and 8 cols bytes for each run:
+ * of 32 tokens, of fewer where there are few, or of as many as leave 2048 runs.
  */
 int gns_embedding_backward(const void* dy, int64_t lddy, const void* ids, int id_bytes, int64_t tokens, int64_t vocab,
                            int64_t cols, int dtype, double scale, void* dtable, int64_t lddt, int out_dtype, void* stream);

@@ -73,15 +73,17 @@ template <typename Source>
 __global__ void __launch_bounds__(kSortThreads) sort_count_kernel(Source src, long long n, int G, long long span,
                                                                   int blocks, int* hist) {
     extern __shared__ int smem[];
+    if (static_cast<int>(blockIdx.x) >= blocks) {
+        grid_dependency_wait();
+        grid_launch_dependents();
+        src.extra(blockIdx.x - blocks);
+        return;
+    }
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     for (int i = threadIdx.x; i < (G + 1) * kSortWarps; i += kSortThreads) smem[i] = 0;
     grid_dependency_wait();
     grid_launch_dependents();
     __syncthreads();
-    if (static_cast<int>(blockIdx.x) >= blocks) {
-        src.extra(blockIdx.x - blocks);
-        return;
-    }
     const long long run = span / kSortWarps;
     const long long beg = blockIdx.x * span + warp * run;
     count_run(src, beg, min(beg + run, n), smem + warp * (G + 1), lane);
@@ -99,16 +101,18 @@ __global__ void __launch_bounds__(kSortThreads) sort_place_kernel(Source src, lo
                                                                   int blocks, const int* hist) {
     extern __shared__ int smem[];
     __shared__ int warp_sum[kSortWarps];
+    if (static_cast<int>(blockIdx.x) >= blocks) {
+        grid_dependency_wait();
+        grid_launch_dependents();
+        src.extra(blockIdx.x - blocks);
+        return;
+    }
     int* first = smem + (G + 1) * kSortWarps;  // first place of this block's slots of each digit
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     for (int i = threadIdx.x; i < (G + 1) * kSortWarps; i += kSortThreads) smem[i] = 0;
     grid_dependency_wait();
     grid_launch_dependents();
     __syncthreads();
-    if (static_cast<int>(blockIdx.x) >= blocks) {
-        src.extra(blockIdx.x - blocks);
-        return;
-    }
     const long long run = span / kSortWarps;
     const long long beg = blockIdx.x * span + warp * run;
     const long long end = min(beg + run, n);

@@ -15,10 +15,10 @@
 // blocks for a share of the rows.
 //
 // Bound: HBM. Forward the rows and y; backward dy read and the table written once.
-// 16384 tokens of 4096 bf16 values: forward 42 us (6.5 TB/s); backward, of 32768 rows, 86
+// 16384 tokens of 4096 bf16 values: forward 42 us (6.5 TB/s); backward, of 32768 rows, 85
 // (4.7 TB/s of dy and the table): the sort with the empty rows about 45, the runs 30,
 // which is their share of HBM, the joins 5. 131072 tokens of 2048, a third of them one id,
-// to 131072 rows in fp32: 282 (5.7). A single token: the table, 43 (6.3).
+// to 131072 rows in fp32: 281 (5.7). A single token: the table, 43 (6.3).
 #include <algorithm>
 #include <type_traits>
 
@@ -447,7 +447,7 @@ Zeros zeros_of(const EmbeddingJob& j, const EmbeddingPlan& p, int h, unsigned* b
     z.row = j.cols * eo;
     z.element = eo;
     z.share = z.row <= 4096 ? 1 : z.row <= 8192 ? 2 : 4;
-    z.rows = std::max(kWarps / z.share, (64 << 10) / z.row);
+    z.rows = std::max(kWarps / z.share, (32 << 10) / z.row);
     *blocks = static_cast<unsigned>((z.end - z.begin + z.rows - 1) / z.rows);
     return z;
 }
@@ -479,6 +479,9 @@ int launch_embedding(const EmbeddingJob& j, cudaStream_t s) {
     });
 }
 
+// 27 warps a processor (4093 tokens of 1021 fp32 values: 60 us with runs of 32, 48 of 8).
+constexpr long long kLeastRuns = 4096;
+
 EmbeddingPlan embedding_plan(const EmbeddingJob& j, char* scratch) {
     EmbeddingPlan p{};
     int bits = 1;
@@ -487,11 +490,14 @@ EmbeddingPlan embedding_plan(const EmbeddingJob& j, char* scratch) {
     p.bits = (bits + p.passes - 1) / p.passes;
     const size_t hist = sort_scratch(sort_plan(j, p));
     p.counts = hist != 0;
-    p.chunk = 32;
-    while (static_cast<long long>(p.chunk) * 2048 < j.tokens) p.chunk *= 2;
-    p.chunks = (j.tokens + p.chunk - 1) / p.chunk;
     const bool vec = backward_vec(j);
     const int n = 16 / elem_bytes(j.dtype);
+    const long long strips = (pieces_of(j.cols, n, vec) + 31) / 32;
+    // Few tokens: short runs, so that there are warps for every processor.
+    p.chunk = 32;
+    while (p.chunk > 8 && strips * j.tokens < kLeastRuns * p.chunk) p.chunk /= 2;
+    while (static_cast<long long>(p.chunk) * 2048 < j.tokens) p.chunk *= 2;
+    p.chunks = (j.tokens + p.chunk - 1) / p.chunk;
     const size_t row = sizeof(float) * pieces_of(j.cols, n, vec) * (vec ? n : kLoose);
     auto take = [&](size_t bytes) {
         char* at = scratch + p.bytes;
@@ -505,7 +511,6 @@ EmbeddingPlan embedding_plan(const EmbeddingJob& j, char* scratch) {
     }
     p.hist = reinterpret_cast<int*>(take(hist));
     p.hosts = std::max(1, p.passes * (p.counts ? 2 : 1) - 1);
-    const size_t strips = (pieces_of(j.cols, n, vec) + 31) / 32;
     p.ready = reinterpret_cast<unsigned*>(take(sizeof(unsigned) * strips * (p.chunks / kMostParts + 1)));
     p.marks = reinterpret_cast<unsigned char*>(take(j.vocab));
     p.cleared = p.marks + j.vocab - reinterpret_cast<unsigned char*>(p.ready);
