@@ -159,21 +159,16 @@ __global__ void __launch_bounds__(kRingThreads) layer_norm_backward_ring_kernel(
         float c[2] = {c1.x + c1.y, c2.x + c2.y};
         row_sums<2, CLUSTER>(c, j, red, use, dead);
         if (live) {
-            const float2 minus = both(j.rms ? 0.0f : -c[0] * inv * rstd), by = both(-c[1] * inv);
+            const float2 minus = both(j.rms ? 0.0f : -c[0] * inv), by = both(-c[1] * inv);
 #pragma unroll
             for (int i = 0; i < V; ++i) {
                 if (!has(i)) continue;
                 float2 r[P];
-                if (j.residual) {
-                    unpack<T, N>(mine[((stage * kinds + 2) * V + i) * threads], r);
 #pragma unroll
-                    for (int e = 0; e < P; ++e) r[e] = add2(r[e], minus);
-                } else {
+                for (int e = 0; e < P; ++e) r[e] = both(0.0f);
+                if (j.residual) unpack<T, N>(mine[((stage * kinds + 2) * V + i) * threads], r);
 #pragma unroll
-                    for (int e = 0; e < P; ++e) r[e] = minus;
-                }
-#pragma unroll
-                for (int e = 0; e < P; ++e) r[e] = fma2(fma2(h[i][e], by, g[i][e]), both(rstd), r[e]);
+                for (int e = 0; e < P; ++e) r[e] = fma2(add2(fma2(h[i][e], by, g[i][e]), minus), both(rstd), r[e]);
                 *reinterpret_cast<uint4*>(dx + i * apart) = pack<T>(r);
             }
         }
@@ -299,12 +294,12 @@ __global__ void __launch_bounds__(kRingThreads) layer_norm_backward_loose_kernel
         float c[2] = {c1.x + c1.y, c2.x + c2.y};
         row_sums<2, false>(c, j, red, use, dead);
         if (live) {
-            const float2 minus = both(j.rms ? 0.0f : -c[0] * inv * rstd), by = both(-c[1] * inv);
+            const float2 minus = both(j.rms ? 0.0f : -c[0] * inv), by = both(-c[1] * inv);
             const T* rs = in_window(slot(stage, kinds - 1), res);
             pairs([&](int q, int c, bool has0, bool has1) {
-                float2 r = minus;
-                if (kinds == 3) r = add2(r, make_float2(has0 ? to_f32<T>(rs[c]) : 0.0f, has1 ? to_f32<T>(rs[c + tpr]) : 0.0f));
-                r = fma2(fma2(h[q], by, g[q]), both(rstd), r);
+                float2 r = both(0.0f);
+                if (kinds == 3) r = make_float2(has0 ? to_f32<T>(rs[c]) : 0.0f, has1 ? to_f32<T>(rs[c + tpr]) : 0.0f);
+                r = fma2(add2(fma2(h[q], by, g[q]), minus), both(rstd), r);
                 if (has0) dx[c] = from_f32<T>(r.x);
                 if (has1) dx[c + tpr] = from_f32<T>(r.y);
             });

@@ -9,8 +9,8 @@
 //
 // Bound: instructions and latency; 16384 tokens of 256 fp32 logits are 17 MB, 2.5 us of
 // HBM. Those with their 8 experts take 12 us (drawn one after the other 15, by a maximum
-// over every lane's values each time 20), the balance loss 11, the gradient of both 8.5;
-// one token 2.3, 5.8 and 2.5.
+// over every lane's values each time 20), the balance loss 13, the gradient of both 10;
+// one token 2.3, 5.8 and 2.6.
 #include <algorithm>
 #include <type_traits>
 
@@ -72,6 +72,25 @@ __device__ __forceinline__ void draw(const unsigned (&key)[NV], int topk, int la
         last_at = __reduce_min_sync(0xffffffffu, best == top ? at : 0x7fffffff);
         if (lane == r) mine = top, id = last_at;
     }
+}
+
+// A live row's probabilities, in place of its logits. From the row's maximum, not from
+// its lse, whose rounding would be that much of every probability (4e-6 of one at 100).
+template <int NV>
+__device__ __forceinline__ void probabilities(float (&l)[NV]) {
+    float best = l[0];
+#pragma unroll
+    for (int i = 1; i < NV; ++i) best = fmaxf(best, l[i]);
+    const float most = value_of(__reduce_max_sync(0xffffffffu, key_of(best)));
+    float total = 0.0f;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+        l[i] = expf(l[i] - most);
+        total += l[i];
+    }
+    const float inv = 1.0f / warp_sum(total);
+#pragma unroll
+    for (int i = 0; i < NV; ++i) l[i] *= inv;
 }
 
 template <typename T, int NV>
@@ -182,8 +201,9 @@ __global__ void __launch_bounds__(kBalanceThreads) moe_balance_kernel(GateJob j,
             if (z[a] == -kInf) continue;
             ++rows;
             squares = fmaf(z[a], z[a], squares);
+            probabilities(l[a]);
 #pragma unroll
-            for (int i = 0; i < NV; ++i) p[i] += expf(l[a][i] - z[a]);
+            for (int i = 0; i < NV; ++i) p[i] += l[a][i];
         }
     }
     for (int w = 0; w < kBalanceWarps; ++w) {  // one warp after the other: the order of the sums is fixed
@@ -306,21 +326,23 @@ __global__ void __launch_bounds__(kThreads) moe_gate_backward_kernel(GateJob j, 
         const float term = j.normalize ? w * (dw - inner) : w * dw;
         float d[NV];
 #pragma unroll
-        for (int i = 0; i < NV; ++i) d[i] = 0.0f;
+        for (int i = 0; i < NV; ++i) d[i] = row[lane + 32 * i] = 0.0f;
         if (PROBS) {
             const float z = j.lse[t];
             if (z != -kInf) {
                 float p[NV], level = 0.0f;
                 load_logits<T>(j, t, lane, p);
+                probabilities(p);
+#pragma unroll
+                for (int i = 0; i < NV; ++i) level = fmaf(p[i], c[i], level);
+                level = warp_sum(level);
+                // The weights' part and the loss' are added last: each cancels by itself.
+                const float all = by_lse * z, less = j.normalize ? 0.0f : inner;
 #pragma unroll
                 for (int i = 0; i < NV; ++i) {
-                    p[i] = expf(p[i] - z);
-                    level = fmaf(p[i], c[i], level);
+                    d[i] = p[i] * (by_count * (c[i] - level) + all);
+                    row[lane + 32 * i] = -p[i] * less;
                 }
-                level = warp_sum(level);
-                const float all = by_lse * z - (j.normalize ? 0.0f : inner);
-#pragma unroll
-                for (int i = 0; i < NV; ++i) d[i] = p[i] * (by_count * (c[i] - level) + all);
             }
         }
         // The chosen experts' terms, a lane each, through shared memory. A gate of one's own
@@ -334,14 +356,12 @@ __global__ void __launch_bounds__(kThreads) moe_gate_backward_kernel(GateJob j, 
                 if (same >> r & 1) v += o;
             }
         }
-#pragma unroll
-        for (int i = 0; i < NV; ++i) row[lane + 32 * i] = d[i];
         __syncwarp();
         if (id >= 0 && __ffs(same) - 1 == lane) row[id] += v;
         __syncwarp();
 #pragma unroll
         for (int i = 0; i < NV; ++i)
-            if (lane + 32 * i < j.experts) out[t * g.ldd + lane + 32 * i] = from_f32<T>(row[lane + 32 * i]);
+            if (lane + 32 * i < j.experts) out[t * g.ldd + lane + 32 * i] = from_f32<T>(d[i] + row[lane + 32 * i]);
         __syncwarp();
     }
 }

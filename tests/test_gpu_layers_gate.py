@@ -125,6 +125,29 @@ def test_values_at_the_border(gns):
     check(gns, rows[2:], 2, True, rng, z=0.0)
 
 
+def test_large_logits_cost_no_digits(gns):
+    """Logits around 1000, whose lse has steps of 2^-14: probabilities and their gradients
+    are those of the differences, which are exact."""
+    logits, rng = logits_of(64, 50, torch.float32, 12)
+    logits = torch.round(logits * 1024) / 1024
+    dw = torch.from_numpy(rng.normal(size=(64, 3))).float().cuda()
+    outs = []
+    for shift in (0.0, 1024.0):
+        gate = gns.gns_moe_gate(logits + shift, 3, normalize=False)
+        _, counts, probs = gns.gns_moe_balance(logits + shift, gate, 0.5)
+        outs.append((gate.ids, gate.weights, probs, gns.gns_moe_gate_backward(dw, logits + shift, gate, counts, 0.5)))
+    assert all(torch.equal(a, b) for a, b in zip(*outs))
+
+
+def test_one_expert_has_no_gradient(gns):
+    """Its probability is 1 whatever its logit."""
+    logits = torch.randn(40, 1, device="cuda") * 30
+    gate = gns.gns_moe_gate(logits, 1, normalize=False)
+    loss, counts, _ = gns.gns_moe_balance(logits, gate, 0.5)
+    assert loss == 0.5 and (gate.weights == 1).all()
+    assert not gns.gns_moe_gate_backward(torch.randn(40, 1, device="cuda"), logits, gate, counts, 0.5).any()
+
+
 def test_nan_and_infinity_stay_in_their_row(gns):
     logits, _ = logits_of(20, 40, torch.float32, 6)
     clean = gns.gns_moe_gate(logits, 4)

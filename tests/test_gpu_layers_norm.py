@@ -118,6 +118,16 @@ def test_rows_without_spread(gns, cols):
     assert torch.allclose(stats[:, 1], torch.full((6,), 1e5 ** 0.5, device="cuda"))
 
 
+@pytest.mark.parametrize("rows", [5, 400])
+def test_a_single_column_has_no_gradient(gns, rows):
+    """h = 0 and g = mean(g), whatever 1 / sqrt(eps) is: dx is the residual's gradient."""
+    x, dy, res = (torch.randn(rows, 1, device="cuda") for _ in range(3))
+    y, stats = gns.gns_layer_norm(x)
+    assert not y.any()
+    assert torch.equal(gns.gns_layer_norm_backward(dy, x, stats, residual=res)[0], res)
+    assert not gns.gns_layer_norm_backward(dy, x, stats)[0].any()
+
+
 def test_a_large_mean_costs_no_spread(gns):
     """Values 4096 +- 1 in fp32: the first mean is off by up to some hundred units
     of its last place, which the second sum takes back."""
