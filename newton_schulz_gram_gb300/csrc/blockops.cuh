@@ -83,11 +83,6 @@ struct Pack {
 #pragma unroll
         for (int i = 0; i < N; ++i) e[i] = from_f32<T>(f[i]);
     }
-    // Makes the next get() convert again instead of keeping the fp32 values in registers.
-    __device__ __forceinline__ void forget() {
-#pragma unroll
-        for (int i = 0; i < kPieces; ++i) asm volatile("" : "+r"(p[i].x), "+r"(p[i].y), "+r"(p[i].z), "+r"(p[i].w));
-    }
 };
 
 // Pieces: what a thread owns of a row of H elements, 16 bytes of it where rows are
@@ -109,7 +104,6 @@ struct Wide {
     __device__ __forceinline__ void clear() { p.clear(); }
     __device__ __forceinline__ void get(float (&f)[N]) const { p.get(f); }
     __device__ __forceinline__ void set(const float (&f)[N]) { p.set(f); }
-    __device__ __forceinline__ void forget() { p.forget(); }
 };
 
 template <typename T>
@@ -141,7 +135,6 @@ struct Loose {
 #pragma unroll
         for (int i = 0; i < kLoose; ++i) e[i] = from_f32<T>(f[i]);
     }
-    __device__ __forceinline__ void forget() {}
 };
 
 // Copies to shared memory that the thread waits for itself.

@@ -6,12 +6,12 @@
 // constant row of any size gives 0, and 4096 +- 1 in fp32 keeps its digits).
 //
 // Bound: HBM, x read and y written once; but the instructions of a row's 4096 values and
-// its two sums take about as long. Many rows go through shared memory (below); few,
-// which are latency, stay in the registers of one block each; rows beyond both are read
+// its two sums take about as long. Rows go through shared memory ahead of their use, as
+// 16-byte pieces or, unaligned, as the words that hold them; rows beyond that are read
 // three times. 16384 x 4096 bf16 with fp32 weights: 52 us (5.1 TB/s; issue slots 65%
 // busy with 16 warps a processor: 24, by one row at a time instead of two, took 53);
 // 262144 x 128: 20 (6.6); 4096 x 14336 by two CTAs a row: 69 (3.4); 65536 x 257: 26;
-// one row: 2.8.
+// one row: 2.4 (from registers alone 2.9; 304 rows 2.9 and 5.0).
 #include <algorithm>
 
 #include "layer_norm.cuh"
@@ -25,97 +25,6 @@ namespace {
 __device__ __forceinline__ float norm_rstd(float squares, float dev, float eps) {
     const float var = fmaxf(squares - dev * dev, 0.0f);
     return rsqrtf((squares == squares ? var : squares) + eps);
-}
-
-// Most threads a row, of up to kMostPieces pieces each.
-constexpr int kMostPieces = 16, kMostThreads = 512;
-
-template <typename T, typename Piece, int V>
-__global__ void __launch_bounds__(kMostThreads) layer_norm_kernel(NormJob j) {
-    constexpr int N = Piece::kSize;
-    __shared__ float2 red[2][32];
-    int phase = 0;
-    grid_dependency_wait();
-    grid_launch_dependents();
-    const int at = j.tpr <= 32 ? threadIdx.x & (j.tpr - 1) : threadIdx.x;
-    const int group = j.tpr <= 32 ? threadIdx.x / j.tpr : 0;
-    const int groups = blockDim.x / j.tpr;
-    const float n = static_cast<float>(j.cols);
-    const T* x = static_cast<const T*>(j.x);
-    T* y = static_cast<T*>(j.y);
-    for (long long r0 = static_cast<long long>(blockIdx.x) * groups; r0 < j.rows; r0 += static_cast<long long>(gridDim.x) * groups) {
-        const long long r = r0 + group;
-        const bool live = r < j.rows;
-        Piece p[V];
-#pragma unroll
-        for (int i = 0; i < V; ++i) {
-            const unsigned v = at + i * j.tpr;
-            if (live && v < j.per_row)
-                p[i].load_stream(x + r * j.ldx, v, j.cols);
-            else
-                p[i].clear();
-        }
-        float mean = 0.0f, none = 0.0f;
-        if (!j.rms) {
-#pragma unroll
-            for (int i = 0; i < V; ++i) {
-                float f[N];
-                p[i].get(f);
-#pragma unroll
-                for (int e = 0; e < N; ++e) mean += f[e];
-            }
-            row_sum2(mean, none, j.tpr, red[phase ^= 1]);
-            mean /= n;
-        }
-#pragma unroll
-        for (int i = 0; i < V; ++i) p[i].forget();
-        float dev = 0.0f, squares = 0.0f;
-#pragma unroll
-        for (int i = 0; i < V; ++i) {
-            const unsigned v = at + i * j.tpr;
-            float f[N];
-            p[i].get(f);
-#pragma unroll
-            for (int e = 0; e < N; ++e) {
-                const float d = v < j.per_row && piece_has(p[i], v, e, j.cols) ? f[e] - mean : 0.0f;
-                dev += d;
-                squares = fmaf(d, d, squares);
-            }
-        }
-        row_sum2(dev, squares, j.tpr, red[phase ^= 1]);
-        dev = j.rms ? 0.0f : dev / n;
-        const float rstd = norm_rstd(squares / n, dev, j.eps);
-        if (live && at == 0) {
-            j.stats[2 * r] = mean + dev;
-            j.stats[2 * r + 1] = rstd;
-        }
-#pragma unroll
-        for (int i = 0; i < V; ++i) p[i].forget();
-#pragma unroll
-        for (int i = 0; i < V; ++i) {
-            const unsigned v = at + i * j.tpr;
-            if (!live || v >= j.per_row) continue;
-            float f[N];
-            p[i].get(f);
-#pragma unroll
-            for (int e = 0; e < N; ++e) f[e] = ((f[e] - mean) - dev) * rstd;
-            if (j.weight) {
-                float w[N];
-                piece_weights(p[i], j.weight, j.wf32, v, j.cols, w);
-#pragma unroll
-                for (int e = 0; e < N; ++e) f[e] *= w[e];
-            }
-            if (j.bias) {
-                float b[N];
-                piece_weights(p[i], j.bias, j.wf32, v, j.cols, b);
-#pragma unroll
-                for (int e = 0; e < N; ++e) f[e] += b[e];
-            }
-            Piece o;
-            o.set(f);
-            o.store(y + r * j.ldy, v, j.cols);
-        }
-    }
 }
 
 // ------------------------------------------------------------- aligned rows
@@ -388,7 +297,7 @@ __global__ void __launch_bounds__(kRingThreads) layer_norm_loose_kernel(NormJob 
     copies_wait<0>();
 }
 
-// Rows beyond the registers of a block: read three times, the later ones from L2.
+// Rows that do not fit: read three times, the later ones from L2.
 constexpr int kLongThreads = 1024;
 
 template <typename T, typename Piece>
@@ -465,63 +374,29 @@ __global__ void __launch_bounds__(kLongThreads) layer_norm_long_kernel(NormJob j
 int launch_layer_norm(NormJob j, int num_sms, cudaStream_t s) {
     const bool vec = norm_vec(j, false);
     const int p = j.per_row = norm_pieces(j, vec);
-    const bool fits = p <= kMostPieces * kMostThreads;
-    int V = 1, threads = 128;
-    if (p <= 4) {
-        j.tpr = next_pow2(p);
-    } else if (j.rows <= 2 * num_sms && p > 32) {
-        while (V < kMostPieces && p > V * kMostThreads) V *= 2;
-        threads = j.tpr = (p + 32 * V - 1) / (32 * V) * 32;
-    } else if (p <= 32 * kMostPieces) {
-        while (V < kMostPieces && (V < 4 ? p > 4 * V : p > 32 * V)) V *= 2;
-        j.tpr = std::max(4, next_pow2((p + V - 1) / V));
-    } else {
-        const auto idle = [&](int v) { return (p + 32 * v - 1) / (32 * v) * 32 * v - p; };
-        V = idle(8) < idle(16) && p <= 8 * kMostThreads ? 8 : 16;
-        threads = j.tpr = (p + 32 * V - 1) / (32 * V) * 32;
-    }
     return by_dtype(j.dtype, [&](auto t) {
         using T = decltype(t);
-        using W = Wide<T, 16 / sizeof(T)>;
-        using L = Loose<T>;
         constexpr int n = 16 / sizeof(T), few = 16 / n;
         RingShape c;
-        if (vec && j.rows > 2 * num_sms && ring_shape(p, n, 2 * kStages, &c)) {
+        if (vec ? ring_shape(p, n, 2 * kStages, &c) : loose_shape(j.cols, &c)) {
             j.tpr = c.tpr;
             j.ctas = c.ctas;
             j.per_cta = c.per_cta;
-            const size_t smem = sizeof(uint4) * kStages * 2 * c.V * c.threads;
-            const long long batch = static_cast<long long>(c.threads / c.tpr) * 2;
-            const unsigned clusters = ring_clusters(c, (j.rows + batch - 1) / batch, num_sms, smem);
-            const bool full = p == c.V * c.tpr * c.ctas;
-            const auto run = [&](auto k) { return launch_ring(k, c, clusters, smem, s, j); };
-            if (c.ctas > 1) return run(full ? layer_norm_ring_kernel<T, few, true, true> : layer_norm_ring_kernel<T, few, false, true>);
-            if (c.V == 1) return run(full ? layer_norm_ring_kernel<T, 1, true, false> : layer_norm_ring_kernel<T, 1, false, false>);
-            return run(full ? layer_norm_ring_kernel<T, few, true, false> : layer_norm_ring_kernel<T, few, false, false>);
-        }
-        if (!vec && j.rows > 2 * num_sms && loose_shape(j.cols, &c)) {
-            const long long groups = c.threads / c.tpr, batch = 2 * groups;
-            const size_t smem = static_cast<size_t>(kStages) * batch * window_bytes(j.cols * static_cast<int>(sizeof(T)));
+            const long long batch = 2LL * (c.threads / c.tpr);  // rows
+            const size_t smem = kStages * (vec ? sizeof(uint4) * 2 * c.V * c.threads : static_cast<size_t>(batch) * window_bytes(j.cols * static_cast<int>(sizeof(T))));
             if (smem <= kRingBytes) {
-                j.tpr = c.tpr;
-                return launch_ring(layer_norm_loose_kernel<T>, c, ring_clusters(c, (j.rows + batch - 1) / batch, num_sms, smem), smem, s, j);
+                const unsigned clusters = ring_clusters(c, (j.rows + batch - 1) / batch, num_sms, smem);
+                const bool full = p == c.V * c.tpr * c.ctas;
+                const auto run = [&](auto k) { return launch_ring(k, c, clusters, smem, s, j); };
+                if (!vec) return run(layer_norm_loose_kernel<T>);
+                if (c.ctas > 1) return run(full ? layer_norm_ring_kernel<T, few, true, true> : layer_norm_ring_kernel<T, few, false, true>);
+                if (c.V == 1) return run(full ? layer_norm_ring_kernel<T, 1, true, false> : layer_norm_ring_kernel<T, 1, false, false>);
+                return run(full ? layer_norm_ring_kernel<T, few, true, false> : layer_norm_ring_kernel<T, few, false, false>);
             }
         }
-        if (!fits) {
-            const unsigned b = static_cast<unsigned>(std::min<long long>(j.rows, 2LL * num_sms));
-            return static_cast<int>(launch_after(vec ? layer_norm_long_kernel<T, W> : layer_norm_long_kernel<T, L>, dim3(b),
-                                                 dim3(kLongThreads), 0, s, j));
-        }
-        const long long groups = threads / j.tpr;
-        const dim3 blocks(static_cast<unsigned>((j.rows + groups - 1) / groups));
-        const auto run = [&](auto k) { return static_cast<int>(launch_after(k, blocks, dim3(threads), 0, s, j)); };
-        switch (V) {
-            case 1: return run(vec ? layer_norm_kernel<T, W, 1> : layer_norm_kernel<T, L, 1>);
-            case 2: return run(vec ? layer_norm_kernel<T, W, 2> : layer_norm_kernel<T, L, 2>);
-            case 4: return run(vec ? layer_norm_kernel<T, W, 4> : layer_norm_kernel<T, L, 4>);
-            case 8: return run(vec ? layer_norm_kernel<T, W, 8> : layer_norm_kernel<T, L, 8>);
-            default: return run(vec ? layer_norm_kernel<T, W, 16> : layer_norm_kernel<T, L, 16>);
-        }
+        const unsigned blocks = static_cast<unsigned>(std::min<long long>(j.rows, 2LL * num_sms));
+        return static_cast<int>(launch_after(vec ? layer_norm_long_kernel<T, Wide<T, n>> : layer_norm_long_kernel<T, Loose<T>>, dim3(blocks),
+                                             dim3(kLongThreads), 0, s, j));
     });
 }
 

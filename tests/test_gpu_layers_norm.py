@@ -10,9 +10,10 @@ from block_helpers import DTYPES, assert_close, f64, strided  # noqa: E402
 
 pytestmark = pytest.mark.gpu
 
-# Roundings on the way to a row's statistics: a thread's elements one after the
-# other (at most 16 in registers, 32 of rows beyond them), five steps among
-# the lanes, up to 32 warps; the squares once more, and a few single operations.
+# Roundings on the way to a row's statistics: a thread's elements one after the other
+# (at most 16, 72 of rows that do not fit), five steps among the lanes, up to 32 warps
+# or 8 times 16, and a few single operations: up to 160 half steps, 80 of the 2^-23 that
+# assert_close counts.
 DEPTH = 80
 
 
@@ -67,13 +68,13 @@ def check(gns, x, dy, res, w, b, rms, eps=1e-5):
     return y, stats, dx, dw, db
 
 
-# One lane a row to a whole block; widths that are no whole pieces; beyond the registers.
+# One lane a row to a whole block; widths that are no whole pieces; beyond a block.
 SHAPES = [(1, 1), (3, 1), (5, 7), (2, 8), (300, 16), (33, 24), (1, 4096), (257, 128), (70, 33), (513, 256), (300, 1024),
           (130, 712), (40, 1021), (9, 14336), (4, 14343), (700, 2048)]
 LONG = [(3, 16392), (2, 40001), (5, 20000)]
-# More rows than two a processor, which go through shared memory, and of those rows
-# that two, four and eight blocks share, whole and with a remainder; unaligned ones up
-# to the last that fits and beyond.
+# More rows than two a processor, so that blocks go from row to row; of those rows that
+# two, four and eight blocks share, whole and with a remainder; unaligned ones up to the
+# last that fits and beyond.
 RING = [(305, 8), (400, 4096), (310, 4104), (307, 14336), (306, 8200), (308, 33000), (305, 60000), (310, 70008),
         (1000, 7), (400, 33), (330, 257), (310, 1001), (311, 8191), (308, 8193)]
 
