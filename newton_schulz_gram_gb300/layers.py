@@ -11,8 +11,18 @@ from __future__ import annotations
 import torch
 from torch.autograd import forward_ad as _forward_ad
 
+from . import block as _block
 from ._lib import call
 from .block import _MOST, DTYPES, _contiguous, _counts, _matrix, _new, _on, _out_type, _ptr, _same_device, _typed
+
+
+def _new_each(like, stream, *specs):
+    """New tensors of the (shape, type) given, on the stream of the call."""
+    empty, device = _block._empty, like.device
+    if stream is None:
+        return [empty(shape, dtype=dtype, device=device) for shape, dtype in specs]
+    with torch.cuda.stream(stream):
+        return [empty(shape, dtype=dtype, device=device) for shape, dtype in specs]
 
 
 # --------------------------------------------------------------- layer norm
@@ -47,8 +57,7 @@ def gns_layer_norm(x, weight=None, bias=None, eps=1e-5, rms=False, stream=None):
         if weight is not None and bias.dtype != wdtype:
             raise TypeError("weight and bias must have the same type")
         wdtype = bias.dtype
-    y = _new((rows, cols), x.dtype, x, stream)
-    stats = _new((rows, 2), torch.float32, x, stream)
+    y, stats = _new_each(x, stream, ((rows, cols), x.dtype), ((rows, 2), torch.float32))
     call("gns_layer_norm", x.get_device(), x.data_ptr(), ldx, rows, cols, DTYPES[x.dtype], _ptr(weight), _ptr(bias),
          DTYPES[wdtype], eps, 1 if rms else 0, y.data_ptr(), cols, stats.data_ptr(), _on(x, stream))
     return y, stats
@@ -76,15 +85,14 @@ def gns_layer_norm_backward(dy, x, stats, weight=None, bias=False, rms=False, re
     if stats.dim() != 2 or stats.shape[0] != rows or stats.shape[1] != 2:
         raise ValueError("stats must be [rows, 2]")
     _same_device(dy, "stats", stats)
-    dweight = dbias = None
     wdtype = torch.float32
     if weight is not None:
         _norm_vector(weight, "weight", dy, cols)
         wdtype = weight.dtype
-        dweight = _new((cols,), wdtype, dy, stream)
-    if bias:
-        dbias = _new((cols,), wdtype, dy, stream)
-    dx = _new((rows, cols), dy.dtype, dy, stream)
+    wanted = [((rows, cols), dy.dtype)] + [((cols,), wdtype)] * ((weight is not None) + bool(bias))
+    dx, *sums = _new_each(dy, stream, *wanted)
+    dweight = sums[0] if weight is not None else None
+    dbias = sums[-1] if bias else None
     call("gns_layer_norm_backward", dy.get_device(), dy.data_ptr(), lddy, x.data_ptr(), ldx, stats.data_ptr(), rows, cols,
          DTYPES[dy.dtype], _ptr(weight), DTYPES[wdtype], 1 if rms else 0, _ptr(residual), ldr, dx.data_ptr(), cols,
          _ptr(dweight), _ptr(dbias), _on(dy, stream))
@@ -138,9 +146,8 @@ def gns_moe_gate(logits, topk, normalize=True, stream=None):
         _counts("a size", tokens, experts, topk)
     if not 0 < topk <= experts:
         raise ValueError("topk must be in 1 .. the number of experts")
-    ids = _new((tokens, topk), torch.int64, logits, stream)
-    weights = _new((tokens, topk), torch.float32, logits, stream)
-    lse = _new((tokens,), torch.float32, logits, stream)
+    ids, weights, lse = _new_each(logits, stream, ((tokens, topk), torch.int64), ((tokens, topk), torch.float32),
+                                  ((tokens,), torch.float32))
     call("gns_moe_gate", logits.get_device(), logits.data_ptr(), ld, tokens, experts, topk, DTYPES[logits.dtype],
          1 if normalize else 0, ids.data_ptr(), weights.data_ptr(), lse.data_ptr(), _on(logits, stream))
     return MoeGate._made(ids, weights, lse, experts, normalize)
@@ -164,9 +171,8 @@ def gns_moe_balance(logits, gate, balance, z=0.0, stream=None):
     over the rows that are tokens; counts int32 [num_experts + 1]: the slots of each
     expert, then the number of those rows."""
     tokens, experts, ld = _gate_sizes(logits, gate)
-    loss = _new((), torch.float32, logits, stream)
-    counts = _new((experts + 1,), torch.int32, logits, stream)
-    probs = _new((experts,), torch.float32, logits, stream)
+    loss, counts, probs = _new_each(logits, stream, ((), torch.float32), ((experts + 1,), torch.int32),
+                                    ((experts,), torch.float32))
     call("gns_moe_balance", gate.device, logits.data_ptr(), ld, tokens, experts, gate.topk, DTYPES[logits.dtype],
          gate.ids.data_ptr(), gate.lse.data_ptr(), balance, z, loss.data_ptr(), counts.data_ptr(), probs.data_ptr(),
          _on(logits, stream))
