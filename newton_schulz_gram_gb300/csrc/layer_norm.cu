@@ -183,10 +183,10 @@ __global__ void __launch_bounds__(kRingThreads) layer_norm_ring_kernel(NormJob j
 
 // ----------------------------------------------------------- unaligned rows
 //
-// The same with the row's words in shared memory and a thread's columns tpr apart, so
-// that neighbouring lanes read and write neighbouring elements.
+// The same with the row's words in shared memory and neighbouring lanes reading and
+// writing neighbouring elements. NARROW: rows of less than a warp.
 
-template <typename T>
+template <typename T, bool NARROW>
 __global__ void __launch_bounds__(kRingThreads) layer_norm_loose_kernel(NormJob j) {
     constexpr int R = 2, P = kLoosePairs;
     extern __shared__ __align__(128) uint4 ring[];  // [stage][row][group][window]
@@ -216,26 +216,20 @@ __global__ void __launch_bounds__(kRingThreads) layer_norm_loose_kernel(NormJob 
         x_ahead += x_step;
         ahead += step;
     };
-    const int whole = whole_pairs(j), last = at + 2 * whole * tpr;  // the last pair's first column
-    const bool lo = last < j.cols, hi = last + tpr < j.cols;
-    // Calls fn with each pair of the thread, its first column and which of the two there are.
-    auto pairs = [&](auto&& fn) {
-#pragma unroll
-        for (int q = 0; q < P - 1; ++q)
-            if (q < whole) fn(q, at + 2 * q * tpr, true, true);
-        fn(P - 1, last, lo, hi);
-    };
-    auto weight = [&](const void* v, int c) { return j.wf32 ? static_cast<const float*>(v)[c] : to_f32<T>(static_cast<const T*>(v)[c]); };
+    const LooseColumns k = loose_columns<NARROW>(j, at);
+    const int stride = NARROW ? tpr : 32;
+    auto pairs = [&](auto&& fn) { loose_pairs<NARROW>(k, tpr, fn); };
+    auto weight = [&](const void* v, int c) { return j.wf32 ? static_cast<const float*>(v)[k.first + c] : to_f32<T>(static_cast<const T*>(v)[k.first + c]); };
     float2 w[P], b[P];
     pairs([&](int q, int c, bool has0, bool has1) {
         w[q] = both(1.0f), b[q] = both(0.0f);
         if (j.weight && has0) w[q].x = weight(j.weight, c);
-        if (j.weight && has1) w[q].y = weight(j.weight, c + tpr);
+        if (j.weight && has1) w[q].y = weight(j.weight, c + stride);
         if (j.bias && has0) b[q].x = weight(j.bias, c);
-        if (j.bias && has1) b[q].y = weight(j.bias, c + tpr);
+        if (j.bias && has1) b[q].y = weight(j.bias, c + stride);
     });
 #pragma unroll
-    for (int k = 0; k < kStages - 1; ++k) fetch(k);
+    for (int i = 0; i < kStages - 1; ++i) fetch(i);
     int stage = 0;
     for (unsigned row = first; row - group < rows; row += step, x += x_step, y += y_step) {
         copies_wait<kStages - 2>();
@@ -246,10 +240,10 @@ __global__ void __launch_bounds__(kRingThreads) layer_norm_loose_kernel(NormJob 
 #pragma unroll
         for (int r = 0; r < R; ++r) {
             // Behind the last row its slot's bytes are whatever they are, and not used.
-            const T* in = in_window(slot(stage, r), x + r * x_row);
+            const T* in = in_window(slot(stage, r), x + r * x_row) + k.first;
             float2 sum = both(0.0f);
             pairs([&](int q, int c, bool has0, bool has1) {
-                f[r][q] = make_float2(has0 ? to_f32<T>(in[c]) : 0.0f, has1 ? to_f32<T>(in[c + tpr]) : 0.0f);
+                f[r][q] = make_float2(has0 ? to_f32<T>(in[c]) : 0.0f, has1 ? to_f32<T>(in[c + stride]) : 0.0f);
                 sum = add2(sum, f[r][q]);
             });
             mean[r] = sum.x + sum.y;
@@ -285,11 +279,11 @@ __global__ void __launch_bounds__(kRingThreads) layer_norm_loose_kernel(NormJob 
                 j.stats[2LL * o] = mean[r] + dev;
                 j.stats[2LL * o + 1] = rstd;
             }
-            T* to = y + r * y_row;
+            T* to = y + r * y_row + k.first;
             pairs([&](int q, int c, bool has0, bool has1) {
                 const float2 v = fma2(fma2(f[r][q], both(rstd), both(-dev * rstd)), w[q], b[q]);
                 if (has0) to[c] = from_f32<T>(v.x);
-                if (has1) to[c + tpr] = from_f32<T>(v.y);
+                if (has1) to[c + stride] = from_f32<T>(v.y);
             });
         }
         stage = stage == kStages - 1 ? 0 : stage + 1;
@@ -388,7 +382,7 @@ int launch_layer_norm(NormJob j, int num_sms, cudaStream_t s) {
                 const unsigned clusters = ring_clusters(c, (j.rows + batch - 1) / batch, num_sms, smem);
                 const bool full = p == c.V * c.tpr * c.ctas;
                 const auto run = [&](auto k) { return launch_ring(k, c, clusters, smem, s, j); };
-                if (!vec) return run(layer_norm_loose_kernel<T>);
+                if (!vec) return run(c.tpr < 32 ? layer_norm_loose_kernel<T, true> : layer_norm_loose_kernel<T, false>);
                 if (c.ctas > 1) return run(full ? layer_norm_ring_kernel<T, few, true, true> : layer_norm_ring_kernel<T, few, false, true>);
                 if (c.V == 1) return run(full ? layer_norm_ring_kernel<T, 1, true, false> : layer_norm_ring_kernel<T, 1, false, false>);
                 return run(full ? layer_norm_ring_kernel<T, few, true, false> : layer_norm_ring_kernel<T, few, false, false>);

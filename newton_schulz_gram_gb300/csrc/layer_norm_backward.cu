@@ -199,9 +199,10 @@ __global__ void __launch_bounds__(kRingThreads) layer_norm_backward_ring_kernel(
 
 // ----------------------------------------------------------- unaligned rows
 //
-// The same with the row's words in shared memory and a thread's columns tpr apart.
+// The same with the row's words in shared memory and neighbouring lanes reading and
+// writing neighbouring elements. NARROW: rows of less than a warp.
 
-template <typename T, bool SUMS>
+template <typename T, bool SUMS, bool NARROW>
 __global__ void __launch_bounds__(kRingThreads) layer_norm_backward_loose_kernel(NormJob j) {
     constexpr int P = kLoosePairs;
     extern __shared__ __align__(128) uint4 ring[];  // [stage][x, dy, residual][group][window]
@@ -239,22 +240,16 @@ __global__ void __launch_bounds__(kRingThreads) layer_norm_backward_loose_kernel
         x_ahead += x_step, dy_ahead += dy_step, res_ahead += res_step, stats += 2LL * step, ahead += step;
         return st;
     };
-    const int whole = whole_pairs(j), last = at + 2 * whole * tpr;  // the last pair's first column
-    const bool lo = last < j.cols, hi = last + tpr < j.cols;
-    // Calls fn with each pair of the thread, its first column and which of the two there are.
-    auto pairs = [&](auto&& fn) {
-#pragma unroll
-        for (int q = 0; q < P - 1; ++q)
-            if (q < whole) fn(q, at + 2 * q * tpr, true, true);
-        fn(P - 1, last, lo, hi);
-    };
-    auto weight = [&](int c) { return j.wf32 ? static_cast<const float*>(j.weight)[c] : to_f32<T>(static_cast<const T*>(j.weight)[c]); };
+    const LooseColumns k = loose_columns<NARROW>(j, at);
+    const int stride = NARROW ? tpr : 32;
+    auto pairs = [&](auto&& fn) { loose_pairs<NARROW>(k, tpr, fn); };
+    auto weight = [&](int c) { return j.wf32 ? static_cast<const float*>(j.weight)[k.first + c] : to_f32<T>(static_cast<const T*>(j.weight)[k.first + c]); };
     float2 dw[P], db[P], w[P];
 #pragma unroll
     for (int q = 0; q < P; ++q) w[q] = both(1.0f), dw[q] = db[q] = both(0.0f);
     pairs([&](int q, int c, bool has0, bool has1) {
         if (j.weight && has0) w[q].x = weight(c);
-        if (j.weight && has1) w[q].y = weight(c + tpr);
+        if (j.weight && has1) w[q].y = weight(c + stride);
     });
     const bool deep = j.stages == 3;
     float2 st[3];  // mean and rstd of the rows in flight, the next one's first
@@ -273,14 +268,14 @@ __global__ void __launch_bounds__(kRingThreads) layer_norm_backward_loose_kernel
             st[1] = fetch(stage ^ 1);
         const float mean = st[0].x, rstd = st[0].y;
         float2 h[P], g[P], c1 = both(0.0f), c2 = both(0.0f);
-        const T* xs = in_window(slot(stage, 0), x);
-        const T* ds = in_window(slot(stage, 1), dy);
+        const T* xs = in_window(slot(stage, 0), x) + k.first;
+        const T* ds = in_window(slot(stage, 1), dy) + k.first;
         const bool live = row < rows;
         if (live) {
             pairs([&](int q, int c, bool has0, bool has1) {
                 // A column that is not there has dy = 0 and x = mean.
-                h[q] = make_float2(has0 ? to_f32<T>(xs[c]) : mean, has1 ? to_f32<T>(xs[c + tpr]) : mean);
-                g[q] = make_float2(has0 ? to_f32<T>(ds[c]) : 0.0f, has1 ? to_f32<T>(ds[c + tpr]) : 0.0f);
+                h[q] = make_float2(has0 ? to_f32<T>(xs[c]) : mean, has1 ? to_f32<T>(xs[c + stride]) : mean);
+                g[q] = make_float2(has0 ? to_f32<T>(ds[c]) : 0.0f, has1 ? to_f32<T>(ds[c + stride]) : 0.0f);
                 h[q] = mul2(add2(h[q], both(-mean)), both(rstd));
                 if (SUMS) {
                     dw[q] = fma2(g[q], h[q], dw[q]);
@@ -295,13 +290,14 @@ __global__ void __launch_bounds__(kRingThreads) layer_norm_backward_loose_kernel
         row_sums<2, false>(c, j, red, use, dead);
         if (live) {
             const float2 minus = both(j.rms ? 0.0f : -c[0] * inv), by = both(-c[1] * inv);
-            const T* rs = in_window(slot(stage, kinds - 1), res);
+            const T* rs = in_window(slot(stage, kinds - 1), res) + k.first;
+            T* to = dx + k.first;
             pairs([&](int q, int c, bool has0, bool has1) {
                 float2 r = both(0.0f);
-                if (kinds == 3) r = make_float2(has0 ? to_f32<T>(rs[c]) : 0.0f, has1 ? to_f32<T>(rs[c + tpr]) : 0.0f);
+                if (kinds == 3) r = make_float2(has0 ? to_f32<T>(rs[c]) : 0.0f, has1 ? to_f32<T>(rs[c + stride]) : 0.0f);
                 r = fma2(add2(fma2(h[q], by, g[q]), minus), both(rstd), r);
-                if (has0) dx[c] = from_f32<T>(r.x);
-                if (has1) dx[c + tpr] = from_f32<T>(r.y);
+                if (has0) to[c] = from_f32<T>(r.x);
+                if (has1) to[c + stride] = from_f32<T>(r.y);
             });
         }
         stage = stage == j.stages - 1 ? 0 : stage + 1;
@@ -314,8 +310,8 @@ __global__ void __launch_bounds__(kRingThreads) layer_norm_backward_loose_kernel
 #pragma unroll
         for (int half = 0; half < 2; ++half) {
             const auto col = [&](int q) {
-                const int c = (q < P - 1 ? at + 2 * q * tpr : last) + half * tpr;
-                return (q < P - 1 && q >= whole) || c >= j.cols ? -1 : c;
+                if (q == P - 1) return (half ? k.hi : k.lo) ? k.first + k.last + half * stride : -1;
+                return q < k.whole ? k.first + (2 * q + half) * stride : -1;
             };
             float sum[P];
 #pragma unroll
@@ -514,7 +510,10 @@ int launch_layer_norm_backward(NormJob j, int num_sms, cudaStream_t s) {
             return static_cast<int>(launch_after(c.vec ? layer_norm_backward_long_kernel<T, W> : layer_norm_backward_long_kernel<T, L>,
                                                  dim3(c.blocks), dim3(kLongThreads), 0, s, j));
         const auto run = [&](auto k) { return launch_ring(k, c.ring, c.blocks, c.smem, s, j); };
-        if (!c.vec) return sums ? run(layer_norm_backward_loose_kernel<T, true>) : run(layer_norm_backward_loose_kernel<T, false>);
+        if (!c.vec) {
+            if (c.ring.tpr < 32) return sums ? run(layer_norm_backward_loose_kernel<T, true, true>) : run(layer_norm_backward_loose_kernel<T, false, true>);
+            return sums ? run(layer_norm_backward_loose_kernel<T, true, false>) : run(layer_norm_backward_loose_kernel<T, false, false>);
+        }
         constexpr int few = 16 / (16 / sizeof(T));
         const bool full = c.per_row == c.ring.V * c.ring.tpr * c.ring.ctas;
         const auto pick = [&](auto v, auto shared) {

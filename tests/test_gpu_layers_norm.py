@@ -88,6 +88,14 @@ def test_types_and_widths(gns, rows, cols, dtype):
         check(gns, x, dy, res if with_res else None, w, b, rms)
 
 
+@pytest.mark.parametrize("cols", [31, 481, 511, 512, 513, 543, 544, 545, 1025, 7680, 7681, 8192])
+def test_unaligned_rows_that_end_beside_a_warp(gns, cols):
+    """Rows one element apart: a last warp with one column, with all but one, and with all of them."""
+    x, dy, res, w, b = inputs(307, cols, torch.bfloat16, torch.float32, True, 1, cols)
+    check(gns, x, dy, res, w, b, False)
+    check(gns, x, dy, None, w, None, True)
+
+
 @pytest.mark.parametrize("rows", [0, 1, 151, 4099, 30011])
 def test_many_rows(gns, rows):
     x, dy, _, w, b = inputs(rows, 72, torch.bfloat16, torch.float32, True, 0, rows)
