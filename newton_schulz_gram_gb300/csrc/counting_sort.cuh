@@ -11,11 +11,12 @@
 // loads that stay in L2, which is less than the round trip of a third launch
 // for up to kMaxBlocks blocks.
 //
-// A source says what is sorted: digit(s), the digit of slot s; note(s), called for every
-// slot by each kernel; place(s, at), called once for every slot with its place; start(d,
-// at), called once for every digit with the place of its first slot; extra(b), called by
-// the b-th of the blocks that a launch has beside the sort's, which is bound by latency
-// and leaves most of the GPU free for them.
+// A source says what is sorted: key(s), read for slot s, and its digit(key); begin(),
+// called by a block's threads before its slots; note(key), called for every slot by each
+// kernel; value(s), read for slot s and handed with it to place(s, key, value, at), called
+// once for every slot with its place; start(d, at), called once for every digit with the
+// place of its first slot; extra(b), called by the b-th of the blocks that a launch has
+// beside the sort's, which is bound by latency and leaves most of the GPU free for them.
 #pragma once
 
 #include <algorithm>
@@ -56,16 +57,33 @@ inline size_t sort_scratch(const SortPlan& p) {
     return b > 1 ? sizeof(int) * static_cast<size_t>(b) * (p.G + 1) : 0;
 }
 
+constexpr int kSortTurns = 4;  // times 32 slots whose loads a warp issues together
+
+// The keys of slots s0 .., -1 from `end` on.
+template <typename Source>
+__device__ __forceinline__ void load_keys(const Source& src, long long s0, long long end, int lane, int (&key)[kSortTurns]) {
+#pragma unroll
+    for (int u = 0; u < kSortTurns; ++u) {
+        const long long s = s0 + 32 * u + lane;
+        key[u] = s < end ? src.key(s) : -1;
+    }
+}
+
 // Counts of this warp's run of slots into its column cnt[0 .. G].
 template <typename Source>
 __device__ __forceinline__ void count_run(const Source& src, long long beg, long long end, int* cnt, int lane) {
-    for (long long s0 = beg; s0 < end; s0 += 32) {
-        const long long s = s0 + lane;
-        const int e = s < end ? src.digit(s) : -1;
-        const unsigned peers = __match_any_sync(0xffffffffu, e);
-        if (e >= 0 && (peers & ((1u << lane) - 1)) == 0) cnt[e] += __popc(peers);
-        src.note(s, e >= 0);
-        __syncwarp();
+    for (long long s0 = beg; s0 < end; s0 += 32 * kSortTurns) {
+        int key[kSortTurns];
+        load_keys(src, s0, end, lane, key);
+#pragma unroll
+        for (int u = 0; u < kSortTurns; ++u) {
+            if (s0 + 32 * u >= end) break;
+            const int e = key[u] < 0 ? -1 : src.digit(key[u]);
+            const unsigned peers = __match_any_sync(0xffffffffu, e);
+            if (e >= 0 && (peers & ((1u << lane) - 1)) == 0) cnt[e] += __popc(peers);
+            if (e >= 0) src.note(key[u]);
+            __syncwarp();
+        }
     }
 }
 
@@ -81,6 +99,7 @@ __global__ void __launch_bounds__(kSortThreads) sort_count_kernel(Source src, lo
     }
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     for (int i = threadIdx.x; i < (G + 1) * kSortWarps; i += kSortThreads) smem[i] = 0;
+    src.begin();
     grid_dependency_wait();
     grid_launch_dependents();
     __syncthreads();
@@ -110,6 +129,7 @@ __global__ void __launch_bounds__(kSortThreads) sort_place_kernel(Source src, lo
     int* first = smem + (G + 1) * kSortWarps;  // first place of this block's slots of each digit
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     for (int i = threadIdx.x; i < (G + 1) * kSortWarps; i += kSortThreads) smem[i] = 0;
+    src.begin();
     grid_dependency_wait();
     grid_launch_dependents();
     __syncthreads();
@@ -172,19 +192,25 @@ __global__ void __launch_bounds__(kSortThreads) sort_place_kernel(Source src, lo
         }
     }
     __syncthreads();
-    for (long long s0 = beg; s0 < end; s0 += 32) {
-        const long long s = s0 + lane;
-        const int e = s < end ? src.digit(s) : -1;
-        const unsigned peers = __match_any_sync(0xffffffffu, e);
-        const int rank = __popc(peers & ((1u << lane) - 1));
-        int at = 0;
-        if (e >= 0) {
-            at = cnt[e] + rank;
-            src.place(s, at);
+    for (long long s0 = beg; s0 < end; s0 += 32 * kSortTurns) {
+        int key[kSortTurns], value[kSortTurns];
+        load_keys(src, s0, end, lane, key);
+#pragma unroll
+        for (int u = 0; u < kSortTurns; ++u) {
+            const long long s = s0 + 32 * u + lane;
+            value[u] = s < end ? src.value(s) : 0;
         }
-        __syncwarp();
-        if (e >= 0 && rank == 0) cnt[e] += __popc(peers);
-        __syncwarp();
+#pragma unroll
+        for (int u = 0; u < kSortTurns; ++u) {
+            if (s0 + 32 * u >= end) break;
+            const int e = key[u] < 0 ? -1 : src.digit(key[u]);
+            const unsigned peers = __match_any_sync(0xffffffffu, e);
+            const int rank = __popc(peers & ((1u << lane) - 1));
+            if (e >= 0) src.place(s0 + 32 * u + lane, key[u], value[u], cnt[e] + rank);
+            __syncwarp();
+            if (e >= 0 && rank == 0) cnt[e] += __popc(peers);
+            __syncwarp();
+        }
     }
 }
 

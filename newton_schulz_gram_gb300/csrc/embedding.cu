@@ -145,16 +145,30 @@ struct TokenDigits {
     unsigned char* marks;  // where the ids are to be marked, or null
     Zeros zeros;
     __device__ __forceinline__ int key(long long s) const { return keys_in ? keys_in[s] : row_of(ids, s, vocab); }
-    __device__ __forceinline__ int digit(long long s) const { return (key(s) >> shift) & mask; }
-    __device__ __forceinline__ void place(long long s, int at) const {
-        keys_out[at] = key(s);
-        order_out[at] = order_in ? order_in[s] : static_cast<int>(s);
+    __device__ __forceinline__ int digit(int key) const { return (key >> shift) & mask; }
+    __device__ __forceinline__ int value(long long s) const { return order_in ? order_in[s] : static_cast<int>(s); }
+    __device__ __forceinline__ void place(long long, int key, int value, int at) const {
+        keys_out[at] = key;
+        order_out[at] = value;
     }
     __device__ __forceinline__ void start(int, int) const {}
-    __device__ __forceinline__ void note(long long s, bool in) const {
-        if (!marks || !in) return;
-        const int k = key(s);
-        if (k < vocab) marks[k] = 1;
+    // Ids that a block has marked lately, so that frequent ones are not written over and
+    // over (262144 tokens of 32768 ids, log-uniform: 31 us, 22 so).
+    static constexpr int kSeen = 1024;
+    __device__ static __forceinline__ int* seen() {
+        __shared__ int ids[kSeen];
+        return ids;
+    }
+    __device__ __forceinline__ void begin() const {
+        if (!marks) return;
+        for (int i = threadIdx.x; i < kSeen; i += blockDim.x) seen()[i] = -1;
+    }
+    __device__ __forceinline__ void note(int key) const {
+        if (!marks || key >= vocab) return;
+        int* last = seen() + (key & (kSeen - 1));
+        if (*last == key) return;
+        *last = key;
+        marks[key] = 1;
     }
     __device__ __forceinline__ void extra(unsigned block) const { set_zero(zeros, block); }
 };

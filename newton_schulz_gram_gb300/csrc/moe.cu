@@ -28,13 +28,16 @@ struct ExpertSlots {
     const I* ids;
     int G;
     int *offsets, *rows, *slots;
-    __device__ __forceinline__ int digit(long long s) const {
+    __device__ __forceinline__ int key(long long s) const {
         const I v = ids[s];
         return v >= 0 && v < static_cast<I>(G) ? static_cast<int>(v) : G;
     }
-    __device__ __forceinline__ void note(long long, bool) const {}
+    __device__ __forceinline__ int digit(int key) const { return key; }
+    __device__ __forceinline__ int value(long long) const { return 0; }
+    __device__ __forceinline__ void begin() const {}
+    __device__ __forceinline__ void note(int) const {}
     __device__ __forceinline__ void extra(unsigned) const {}
-    __device__ __forceinline__ void place(long long s, int at) const {
+    __device__ __forceinline__ void place(long long s, int, int, int at) const {
         rows[s] = at;
         slots[at] = static_cast<int>(s);
     }
