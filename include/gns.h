@@ -430,7 +430,8 @@ int gns_fp8_linear(const void* x, int64_t ldx, int dtype, int rows, const int32_
  * gns_layer_norm: each of `rows` rows of cols elements (1 to 2^24),
  *   y = (x - mean) * rstd * weight + bias, rstd = 1 / sqrt(var + eps),
  * var the mean of (x - mean)^2; with rms != 0 the mean is taken as 0 (the
- * root-mean-square form). The squares are fp32: deviations beyond 1e19 overflow.
+ * root-mean-square form). The sums are fp32: a row whose sum, or whose sum of squared
+ * deviations, passes 3.4e38 overflows.
  * Rows that are not 16-byte aligned are read in aligned 16-byte words, of which the
  * first may begin before the row.
  *   weight, bias  [cols], fp32 or of x's type (weight_dtype), NULL for 1 and 0.
@@ -516,7 +517,7 @@ int gns_embedding(const void* ids, int id_bytes, int64_t tokens, const void* tab
  * 0 for a row without a token. dy is of dtype, dtable of out_dtype; fp32 sums in
  * token order, joined over runs of sorted tokens, rounded once. Takes intermediate
  * memory: 16 bytes per token, one per row of the table, and 8 cols bytes for each run:
- * of 32 tokens, of fewer where there are few, or of as many as leave 2048 runs.
+ * of 64 tokens, of fewer where there are few, or of as many as leave 2048 runs.
  */
 int gns_embedding_backward(const void* dy, int64_t lddy, const void* ids, int id_bytes, int64_t tokens, int64_t vocab,
                            int64_t cols, int dtype, double scale, void* dtable, int64_t lddt, int out_dtype, void* stream);

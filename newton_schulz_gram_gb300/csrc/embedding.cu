@@ -15,10 +15,10 @@
 // blocks for a share of the rows.
 //
 // Bound: HBM. Forward the rows and y; backward dy read and the table written once.
-// 16384 tokens of 4096 bf16 values: forward 42 us (6.5 TB/s); backward, of 32768 rows, 85
-// (4.7 TB/s of dy and the table): the sort with the empty rows about 45, the runs 30,
+// 16384 tokens of 4096 bf16 values: forward 42 us (6.5 TB/s); backward, of 32768 rows, 83
+// (4.8 TB/s of dy and the table): the sort with the empty rows about 45, the runs 30,
 // which is their share of HBM, the joins 5. 131072 tokens of 2048, a third of them one id,
-// to 131072 rows in fp32: 281 (5.7). A single token: the table, 43 (6.3).
+// to 131072 rows in fp32: 272 (5.9). A single token: the table, 43 (6.3).
 #include <algorithm>
 #include <type_traits>
 
@@ -524,8 +524,9 @@ EmbeddingPlan embedding_plan(const EmbeddingJob& j, char* scratch) {
     const bool vec = backward_vec(j);
     const int n = 16 / elem_bytes(j.dtype);
     const long long strips = (pieces_of(j.cols, n, vec) + 31) / 32;
-    // Few tokens: short runs, so that there are warps for every processor.
-    p.chunk = 32;
+    // Few tokens: short runs, so that there are warps for every processor. Else runs whose
+    // parts are few bytes beside dy (65536 tokens of 1024 x 2048 bf16: 95 us by 32, 87 by 64).
+    p.chunk = 64;
     while (p.chunk > 8 && strips * j.tokens < kLeastRuns * p.chunk) p.chunk /= 2;
     while (static_cast<long long>(p.chunk) * 2048 < j.tokens) p.chunk *= 2;
     p.chunks = (j.tokens + p.chunk - 1) / p.chunk;

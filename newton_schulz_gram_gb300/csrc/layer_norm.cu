@@ -10,7 +10,7 @@
 // 16-byte pieces or, unaligned, as the words that hold them; rows beyond that are read
 // three times. 16384 x 4096 bf16 with fp32 weights: 52 us (5.1 TB/s; issue slots 65%
 // busy with 16 warps a processor: 24, by one row at a time instead of two, took 53);
-// 262144 x 128: 20 (6.6); 4096 x 14336 by two CTAs a row: 69 (3.4); 65536 x 257: 26;
+// 262144 x 128: 20 (6.6); 4096 x 14336 by two CTAs a row: 69 (3.4); 65536 x 257: 24;
 // one row: 2.4 (from registers alone 2.9; 304 rows 2.9 and 5.0).
 #include <algorithm>
 

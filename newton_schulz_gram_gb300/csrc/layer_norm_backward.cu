@@ -10,7 +10,7 @@
 // Bound: HBM, x, dy (and the residual) read and dx written once. 16384 x 4096 bf16 with
 // fp32 weights: 73 us (5.5 TB/s), with the residual 89 (6.1), of which the second kernel
 // is 6; 262144 x 128: 37 (5.5); 4096 x 14336 by two CTAs a row: 106 (4.4); unaligned
-// 65536 x 257: 55, 16384 x 4093: 165, by instructions (single elements to and from
+// 65536 x 257: 56, 16384 x 4093: 162, by instructions (single elements to and from
 // shared memory, 30 a value).
 #include <algorithm>
 #include <type_traits>

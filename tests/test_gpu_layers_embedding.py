@@ -87,6 +87,15 @@ def test_runs_that_end_at_the_chunks(gns):
         gradient(gns, strided(ids.numel(), 264, 0, torch.bfloat16, rng), ids, 2 * len(lengths) + 1, 1.0, torch.float32)
 
 
+@pytest.mark.parametrize("lengths", [[64], [63, 65], [128, 64, 1, 63], [1, 127, 129, 191], [4096, 5, 2048]])
+def test_long_runs_that_end_at_the_chunks(gns, lengths):
+    """The same with tokens enough for the longest runs of 64."""
+    rng = np.random.default_rng(sum(lengths))
+    ids = np.repeat(np.arange(33000 // sum(lengths) * len(lengths)) * 2 + 1, lengths * (33000 // sum(lengths)))
+    ids = torch.from_numpy(rng.permutation(ids)).cuda()
+    gradient(gns, strided(ids.numel(), 1024, 0, torch.float32, rng), ids, int(ids.max()) + 2, 1.0)
+
+
 def test_wide_rows_and_shapes(gns):
     rng = np.random.default_rng(6)
     ids = torch.from_numpy(rng.integers(0, 40, (3, 4, 50))).int().cuda()
