@@ -96,6 +96,22 @@ def test_unaligned_rows_that_end_beside_a_warp(gns, cols):
     check(gns, x, dy, None, w, None, True)
 
 
+@pytest.mark.parametrize("dtype", list(DTYPES))
+@pytest.mark.parametrize("rows,cols", [(1, 5), (7, 3), (9, 1), (1001, 11), (700, 257), (33, 4093), (1300, 4093), (50, 14341), (11, 65001)])
+def test_what_lies_between_unaligned_rows_is_not_looked_at(gns, rows, cols, dtype):
+    """Rows a whole 16 bytes further apart, NaN in the gaps: the same as without them, bit for bit."""
+    dt = DTYPES[dtype]
+    x, dy, _, w, b = inputs(rows, cols, dt, torch.float32, True, 0, cols)
+    apart = 16 // x.element_size()
+    wide = [torch.full((rows + 1, cols + apart), float("nan"), dtype=dt, device="cuda")[:rows, :cols] for _ in range(2)]
+    wide[0].copy_(x), wide[1].copy_(dy)
+    y, stats = gns.gns_layer_norm(x, w, b)
+    y2, stats2 = gns.gns_layer_norm(wide[0], w, b)
+    assert torch.equal(y, y2) and torch.equal(stats, stats2) and bool(torch.isfinite(y).all())
+    for a, c in zip(gns.gns_layer_norm_backward(dy, x, stats, w, bias=True), gns.gns_layer_norm_backward(wide[1], wide[0], stats, w, bias=True)):
+        assert torch.equal(a, c) and bool(torch.isfinite(a).all())
+
+
 @pytest.mark.parametrize("rows", [0, 1, 151, 4099, 30011])
 def test_many_rows(gns, rows):
     x, dy, _, w, b = inputs(rows, 72, torch.bfloat16, torch.float32, True, 0, rows)
