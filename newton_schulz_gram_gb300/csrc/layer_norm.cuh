@@ -255,7 +255,7 @@ constexpr int kRingThreads = 32 * kMostWarps;
 constexpr int kStages = 3;                // batches of rows in flight, with the one that is worked on
 constexpr size_t kRingBytes = 204 << 10;  // of shared memory, at most
 struct RingShape {
-    int V, threads, tpr, ctas, per_cta;
+    int V, threads, tpr, ctas, per_cta, resident;  // resident: threads of a processor
 };
 
 inline int next_pow2(int v) {
@@ -276,10 +276,16 @@ inline bool ring_shape(int p, int n, int copies, RingShape* s) {
     // costs more than the exchange (8192 rows of 5120 bf16 values: 47 us, 39 by two CTAs).
     if (s->ctas == 1 && p > 256 * few && p < 384 * few) s->ctas = 2;
     s->per_cta = (p + s->ctas - 1) / s->ctas;
+    // fp32 rows that would leave a quarter or more of the pieces of 64 threads' sixteen
+    // elements empty: single pieces, which need half the registers (65536 x 640: 61 and 82
+    // us instead of 70 and 107, 768: 74 and 98 instead of 79 and 118; bf16 gains nothing).
+    const bool single = few == 4 && p > 128 && p <= 192;
+    s->resident = single ? 1024 : 512;
+    if (single) s->V = 1;
     if (p <= 32 * few)
         s->tpr = next_pow2((p + s->V - 1) / s->V);
     else
-        s->threads = s->tpr = (s->per_cta + 32 * few - 1) / (32 * few) * 32;
+        s->threads = s->tpr = (s->per_cta + 32 * s->V - 1) / (32 * s->V) * 32;
     return s->tpr <= most;
 }
 
@@ -287,7 +293,7 @@ inline bool ring_shape(int p, int n, int copies, RingShape* s) {
 // processor has its place in a cluster of four or eight (74 of 76 fours fitted), and one
 // that has to wait for the others to end would double the time.
 inline unsigned ring_clusters(const RingShape& c, long long batches, int num_sms, size_t smem) {
-    const int resident = std::max(1, std::min(512 / c.threads, static_cast<int>(kRingBytes / smem)));
+    const int resident = std::max(1, std::min(c.resident / c.threads, static_cast<int>(kRingBytes / smem)));
     long long fit = static_cast<long long>(num_sms) * resident / c.ctas;
     if (c.ctas > 2) fit = fit * 15 / 16;
     return static_cast<unsigned>(std::min(batches, std::max(1LL, fit)));
@@ -357,6 +363,7 @@ inline bool loose_shape(int cols, RingShape* s) {
     s->V = 1;
     s->ctas = 1;
     s->threads = 256;
+    s->resident = 512;
     if (cols <= 32 * each)
         s->tpr = next_pow2((cols + each - 1) / each);
     else

@@ -76,7 +76,7 @@ LONG = [(3, 16392), (2, 40001), (5, 20000)]
 # two, four and eight blocks share, whole and with a remainder; unaligned ones up to the
 # last that fits and beyond.
 RING = [(305, 8), (400, 4096), (310, 4104), (307, 14336), (306, 8200), (308, 33000), (305, 60000), (310, 70008),
-        (1000, 7), (400, 33), (330, 257), (310, 1001), (311, 8191), (308, 8193)]
+        (1000, 7), (400, 33), (330, 257), (310, 1001), (311, 8191), (308, 8193), (2500, 516), (2600, 640), (2500, 768), (300, 772)]
 
 
 @pytest.mark.parametrize("dtype", list(DTYPES))
