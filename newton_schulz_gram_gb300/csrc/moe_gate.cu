@@ -233,6 +233,7 @@ __global__ void __launch_bounds__(1024) moe_balance_join_kernel(const float* par
     __shared__ float terms[kJoinCtas];  // of the first CTA: the loss' sum over each CTA's experts
     __shared__ float rows;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, rank = static_cast<int>(blockIdx.x), cols = j.experts + 1;
+    cluster_sync();  // the first CTA has begun before any other writes to its shared memory
     grid_dependency_wait();
     grid_launch_dependents();
     float squares = 0.0f;

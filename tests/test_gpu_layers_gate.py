@@ -202,6 +202,16 @@ def test_repeats_bit_for_bit_and_feeds_the_sort(gns):
     assert torch.equal(route.offsets.diff(), first[1][:48])
 
 
+@pytest.mark.parametrize("experts", [1, 33, 256, 1024])
+def test_the_loss_repeats_with_any_number_of_strips(gns, experts):
+    """The loss' sum is made of what every CTA of a cluster sends, most of which have no
+    expert where there are few: the same every time, calls one behind the other."""
+    logits, rng = logits_of(300, experts, torch.float32, experts)
+    gate = check(gns, logits, 1, True, rng)
+    runs = [gns.gns_moe_balance(logits, gate, 0.02, 0.01) for _ in range(200)]
+    assert all(torch.equal(a, b) for r in runs[1:] for a, b in zip(r, runs[0]))
+
+
 @pytest.mark.parametrize("normalize", [False, True])
 def test_gradient_against_differences(gns, normalize):
     """The GPU's own forward pass; the choice stays while the step does not cross a tie."""
