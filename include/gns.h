@@ -431,7 +431,10 @@ int gns_fp8_linear(const void* x, int64_t ldx, int dtype, int rows, const int32_
  *   y = (x - mean) * rstd * weight + bias, rstd = 1 / sqrt(var + eps),
  * var the mean of (x - mean)^2; with rms != 0 the mean is taken as 0 (the
  * root-mean-square form). The sums are fp32: a row whose sum, or whose sum of squared
- * deviations, passes 3.4e38 overflows.
+ * deviations, passes 3.4e38 overflows. A row with next to no spread beside its mean (a
+ * constant one of 1e7) is read a second time, for sums of the differences to its first
+ * element; not where y shares memory with x: y may be x, such a row is then as good as
+ * the first sums make it.
  * Rows that are not 16-byte aligned are read in aligned 16-byte words, of which the
  * first may begin before the row.
  *   weight, bias  [cols], fp32 or of x's type (weight_dtype), NULL for 1 and 0.

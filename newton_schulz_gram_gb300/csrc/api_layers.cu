@@ -26,6 +26,12 @@ int check_norm(int64_t rows, int cols, int dtype, int weight_dtype) {
     return GNS_OK;
 }
 
+// Whether [rows][ld] rows of cols elements at a and b share memory.
+bool overlap(const void* a, int64_t lda, const void* b, int64_t ldb, int64_t rows, int cols, int es) {
+    const auto end = [&](const void* p, int64_t ld) { return static_cast<const char*>(p) + ((rows - 1) * ld + cols) * es; };
+    return a < end(b, ldb) && b < end(a, lda);
+}
+
 int check_gate(const void* logits, int64_t ld, int tokens, int experts, int topk, int dtype) {
     if (tokens < 0) return invalid("tokens >= 0 required");
     if (experts < 1 || experts > kMaxExperts) return invalid("num_experts must be in 1..GNS_MAX_EXPERTS");
@@ -79,6 +85,7 @@ int gns_layer_norm(const void* x, int64_t ldx, int64_t rows, int cols, int dtype
     j.eps = static_cast<float>(eps);
     j.y = y;
     j.ldy = ldy;
+    j.again = !overlap(x, ldx, y, ldy, rows, cols, elem_bytes(dtype));
     j.stats = stats;
     j.st = new_call(*st);
     cudaStream_t s = static_cast<cudaStream_t>(stream);

@@ -2,8 +2,10 @@
 //
 // The mean is found first, then the deviations from it and their squares in one sum:
 // the squares of the centred values lose nothing to cancellation, and the mean of the
-// deviations, which is what rounding left of the first mean, is taken off them (a
-// constant row of any size gives 0, and 4096 +- 1 in fp32 keeps its digits).
+// deviations, which is what rounding left of the first mean, is taken off them (4096 +- 1
+// in fp32 keeps its digits). Where a row has next to no spread beside its mean, its squares
+// are mostly those of that remainder, and their difference is what rounding leaves: such
+// rows are made anew at the block's end (a constant row of any size gives 0).
 //
 // Bound: HBM, x read and y written once; but the instructions of a row's 4096 values and
 // its two sums take about as long. Rows go through shared memory ahead of their use, as
@@ -20,11 +22,82 @@
 namespace gns {
 namespace {
 
-// From the mean of the squared deviations and of the deviations. fmaxf drops a NaN;
-// the squares carry it.
-__device__ __forceinline__ float norm_rstd(float squares, float dev, float eps) {
-    const float var = fmaxf(squares - dev * dev, 0.0f);
-    return rsqrtf((squares == squares ? var : squares) + eps);
+// Like fmaxf and fminf, but NaN where one of them is.
+__device__ __forceinline__ float max_nan(float a, float b) {
+    asm("max.NaN.f32 %0, %0, %1;" : "+f"(a) : "f"(b));
+    return a;
+}
+__device__ __forceinline__ float min_nan(float a, float b) {
+    asm("min.NaN.f32 %0, %0, %1;" : "+f"(a) : "f"(b));
+    return a;
+}
+
+// From the mean of the squared deviations and of the deviations.
+__device__ __forceinline__ float norm_rstd(float squares, float dev, float eps) { return rsqrtf(max_nan(squares - dev * dev, 0.0f) + eps); }
+
+// A row's rstd as the kernels below first write it: below 0 where the mean that was taken off
+// first lies more than a deviation (with eps) from the row's. Such rows are made anew at the
+// block's end, as are those whose rstd is 0, since their squares overflow, or NaN. (Of the
+// others, whose sums are off by up to 160 half steps, 2^-16.7 of themselves, the squares are no
+// more than twice the variance and eps: it is off by 2^-14 of them at worst, 2^-22 as measured.)
+__device__ __forceinline__ float rstd_or_again(float dev, float rstd) {
+    const float beyond = fmaf(fabsf(dev), rstd, -1.0f);
+    return __uint_as_float(__float_as_uint(rstd) ^ (~__float_as_uint(beyond) & 0x80000000u));
+}
+
+// Such a row by `threads` threads (a warp or the block), whose own sums row_sum2 joins: from the
+// differences to its first element, which lose nothing in a row of next to no spread.
+template <typename T>
+__device__ __noinline__ void norm_row_again(const NormJob& j, long long row, int threads, float2* red0, float2* red1) {
+    const T* x = static_cast<const T*>(j.x) + row * j.ldx;
+    T* y = static_cast<T*>(j.y) + row * j.ldy;
+    const int at = threads == 32 ? threadIdx.x & 31 : threadIdx.x;
+    const float n = static_cast<float>(j.cols), first = j.rms ? 0.0f : to_f32<T>(x[0]);
+    float mean = 0.0f, none = 0.0f, dev = 0.0f, squares = 0.0f;  // of the differences
+#pragma unroll 4
+    for (int c = at; c < j.cols; c += threads) mean += to_f32<T>(x[c]) - first;
+    row_sum2(mean, none, threads, red0);
+    mean = j.rms ? 0.0f : mean / n;
+#pragma unroll 4
+    for (int c = at; c < j.cols; c += threads) {
+        const float d = to_f32<T>(x[c]) - first - mean;
+        dev += d;
+        squares = fmaf(d, d, squares);
+    }
+    row_sum2(dev, squares, threads, red1);
+    dev = j.rms ? 0.0f : dev / n;
+    const float rstd = norm_rstd(squares / n, dev, j.eps);
+    const auto value = [&](const void* v, int c) { return j.wf32 ? static_cast<const float*>(v)[c] : to_f32<T>(static_cast<const T*>(v)[c]); };
+#pragma unroll 4
+    for (int c = at; c < j.cols; c += threads) {
+        float o = (to_f32<T>(x[c]) - first - mean - dev) * rstd;
+        if (j.weight) o *= value(j.weight, c);
+        if (j.bias) o += value(j.bias, c);
+        y[c] = from_f32<T>(o);
+    }
+    if (at == 0) {
+        j.stats[2 * row] = first + (mean + dev);
+        j.stats[2 * row + 1] = rstd;
+    }
+}
+
+// Those of a block's rows, which are base .. base + batch - 1, those `step` further, and so on,
+// a warp each or one after the other. After a barrier behind all that the block has written.
+template <typename T, typename Red>
+__device__ __forceinline__ void norm_rows_again(const NormJob& j, unsigned base, unsigned batch, unsigned step, Red& red) {
+    const int threads = j.tpr <= 32 ? 32 : blockDim.x, workers = blockDim.x / threads;
+    float2 *red0 = reinterpret_cast<float2*>(red.sums[0]), *red1 = reinterpret_cast<float2*>(red.sums[1]);
+    for (unsigned b = base; b < j.rows; b += step)
+        for (unsigned r = b + threadIdx.x / threads; r < b + batch && r < j.rows; r += workers) {
+            float* rstd = j.stats + 2LL * r + 1;
+            if (*rstd > 0.0f) continue;
+            if (j.again) {
+                norm_row_again<T>(j, r, threads, red0, red1);
+            } else {
+                row_barrier(threads);  // all have read it
+                if (threadIdx.x % threads == 0) *rstd = fabsf(*rstd);
+            }
+        }
 }
 
 // ------------------------------------------------------------- aligned rows
@@ -40,7 +113,7 @@ __device__ __forceinline__ float norm_rstd(float squares, float dev, float eps) 
 // CTAs of a cluster, which exchange the sums.
 
 template <typename T, int V, bool FULL, bool CLUSTER>
-__global__ void __launch_bounds__(kRingThreads) layer_norm_ring_kernel(NormJob j) {
+__global__ void __launch_bounds__(kRingThreads) layer_norm_ring_kernel(const __grid_constant__ NormJob j) {
     constexpr int N = 16 / sizeof(T), P = N / 2, R = 2;
     extern __shared__ __align__(128) uint4 ring[];  // [stage][row][piece][thread]
     __shared__ __align__(128) RowSums<2 * R> red;
@@ -103,6 +176,7 @@ __global__ void __launch_bounds__(kRingThreads) layer_norm_ring_kernel(NormJob j
 #pragma unroll
     for (int k = 0; k < kStages - 1; ++k) fetch(k);
     int stage = 0;
+    float least = 1.0f;  // rstd_or_again of the rows whose stats this thread writes
     for (unsigned row = first; row - group < rows; row += step, y += y_step) {
         fetch(stage == 0 ? kStages - 1 : stage - 1);
         copies_wait<kStages - 1>();
@@ -157,7 +231,9 @@ __global__ void __launch_bounds__(kRingThreads) layer_norm_ring_kernel(NormJob j
             const unsigned o = row + r * groups;
             if (piece == 0 && o < rows) {
                 j.stats[2LL * o] = mean[r] + dev[r];
-                j.stats[2LL * o + 1] = rstd[r];
+                const float kept = rstd_or_again(dev[r], rstd[r]);
+                j.stats[2LL * o + 1] = kept;
+                least = min_nan(least, kept);
             }
         }
 #pragma unroll
@@ -178,6 +254,7 @@ __global__ void __launch_bounds__(kRingThreads) layer_norm_ring_kernel(NormJob j
         stage = stage == kStages - 1 ? 0 : stage + 1;
     }
     copies_wait<0>();
+    if (rank == 0 && __syncthreads_or(!(least > 0.0f))) norm_rows_again<T>(j, cluster * batch, batch, step, red);
     if (CLUSTER) cluster_sync();  // no CTA ends while another may send to it
 }
 
@@ -187,7 +264,7 @@ __global__ void __launch_bounds__(kRingThreads) layer_norm_ring_kernel(NormJob j
 // writing neighbouring elements. NARROW: rows of less than a warp.
 
 template <typename T, bool NARROW>
-__global__ void __launch_bounds__(kRingThreads) layer_norm_loose_kernel(NormJob j) {
+__global__ void __launch_bounds__(kRingThreads) layer_norm_loose_kernel(const __grid_constant__ NormJob j) {
     constexpr int R = 2, P = kLoosePairs;
     extern __shared__ __align__(128) uint4 ring[];  // [stage][row][group][window]
     __shared__ __align__(128) RowSums<2 * R> red;
@@ -231,6 +308,7 @@ __global__ void __launch_bounds__(kRingThreads) layer_norm_loose_kernel(NormJob 
 #pragma unroll
     for (int i = 0; i < kStages - 1; ++i) fetch(i);
     int stage = 0;
+    float least = 1.0f;  // as above
     for (unsigned row = first; row - group < rows; row += step, x += x_step, y += y_step) {
         copies_wait<kStages - 2>();
         row_barrier(tpr);
@@ -275,9 +353,11 @@ __global__ void __launch_bounds__(kRingThreads) layer_norm_loose_kernel(NormJob 
             const unsigned o = row + r * groups;
             if (o >= rows) break;
             const float dev = j.rms ? 0.0f : c[2 * r] * inv, rstd = norm_rstd(c[2 * r + 1] * inv, dev, j.eps);
+            const float kept = rstd_or_again(dev, rstd);
+            least = min_nan(least, kept);
             if (at == 0) {
                 j.stats[2LL * o] = mean[r] + dev;
-                j.stats[2LL * o + 1] = rstd;
+                j.stats[2LL * o + 1] = kept;
             }
             T* to = y + r * y_row + k.first;
             pairs([&](int q, int c, bool has0, bool has1) {
@@ -289,9 +369,11 @@ __global__ void __launch_bounds__(kRingThreads) layer_norm_loose_kernel(NormJob 
         stage = stage == kStages - 1 ? 0 : stage + 1;
     }
     copies_wait<0>();
+    if (__builtin_expect(__syncthreads_or(!(least > 0.0f)), 0)) norm_rows_again<T>(j, blockIdx.x * batch, batch, step, red);
 }
 
-// Rows that do not fit: read three times, the later ones from L2.
+// Rows that do not fit: read three times, the later ones from L2. The mean is made of the
+// differences to the first element, which costs nothing here and leaves no row to make anew.
 constexpr int kLongThreads = 1024;
 
 template <typename T, typename Piece>
@@ -307,16 +389,17 @@ __global__ void __launch_bounds__(kLongThreads) layer_norm_long_kernel(NormJob j
         T* y = static_cast<T*>(j.y) + r * j.ldy;
         float mean = 0.0f, none = 0.0f;
         if (!j.rms) {
+            const float first = to_f32<T>(x[0]);
             for (unsigned v = threadIdx.x; v < j.per_row; v += kLongThreads) {
                 Piece p;
                 p.load(x, v, j.cols);
                 float f[N];
                 p.get(f);
 #pragma unroll
-                for (int e = 0; e < N; ++e) mean += f[e];
+                for (int e = 0; e < N; ++e) mean += piece_has(p, v, e, j.cols) ? f[e] - first : 0.0f;
             }
             row_sum2(mean, none, kLongThreads, red[phase ^= 1]);
-            mean /= n;
+            mean = first + mean / n;
         }
         float dev = 0.0f, squares = 0.0f;
         for (unsigned v = threadIdx.x; v < j.per_row; v += kLongThreads) {

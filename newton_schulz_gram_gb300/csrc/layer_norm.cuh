@@ -23,6 +23,7 @@ struct NormJob {
     const void* weight;  // fp32 where wf32, else of dtype; null for 1
     const void* bias;    // forward; null for 0
     int wf32, rms;
+    int again;  // forward: rows may be read again after y is written
     float eps;
     void* y;  // forward
     long long ldy;

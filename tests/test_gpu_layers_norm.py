@@ -143,6 +143,76 @@ def test_rows_without_spread(gns, cols):
     assert torch.allclose(stats[:, 1], torch.full((6,), 1e5 ** 0.5, device="cuda"))
 
 
+# A lane a row and several, a warp, a block, clusters of two and eight; unaligned; beyond a block.
+WIDTHS = [5, 24, 40, 100, 257, 512, 1021, 1500, 4093, 5172, 6020, 7868, 14336, 60000, 20001, 70008, 100001]
+
+
+@pytest.mark.parametrize("dtype", list(DTYPES))
+@pytest.mark.parametrize("cols", WIDTHS)
+def test_constant_rows_of_any_size(gns, cols, dtype):
+    """Rows whose sum rounding leaves off by several of the value's last places, whose
+    squares would be a spread that is not there. Among them rows that have one, which
+    are the same without them."""
+    values = torch.tensor([0.1, -3.0, 1000.3, 5.88e4, 0.0] + ([] if dtype == "fp16" else [5.88e6, -2.04e16, 9.66e29, 1.1e33]), device="cuda")
+    values = values.to(DTYPES[dtype]).repeat_interleave(67)  # more rows than two a processor
+    n = values.numel()
+    x, dy, _, w, b = inputs(2 * n, cols, DTYPES[dtype], torch.float32, True, 0, cols)
+    plain, plain_stats = gns.gns_layer_norm(x, w, b)
+    x[::2] = values[:, None]
+    y, stats = gns.gns_layer_norm(x, w, b)
+    assert torch.equal(y[1::2], plain[1::2]) and torch.equal(stats[1::2], plain_stats[1::2])
+    # Where the mean is off by less than a deviation, that comes off but for its rounding.
+    assert_close(y[::2], np.broadcast_to(f64(b), (n, cols)), np.broadcast_to(np.abs(f64(w)) + np.abs(f64(b)), (n, cols)), DEPTH, "y")
+    big = values.abs() > 1e6
+    assert torch.equal(y[::2][big], b.to(y.dtype).expand(int(big.sum()), cols))
+    assert torch.equal(stats[::2, 0], values.float())
+    rstd = 1 / np.sqrt(np.float64(np.float32(1e-5)))
+    assert np.abs(f64(stats[::2, 1]) - rstd).max() <= 4 * 2.0 ** -23 * rstd  # the root's two units, and roundings
+    dx = gns.gns_layer_norm_backward(dy, x, stats, w)[0]
+    g = f64(dy)[::2] * f64(w)
+    assert_close(dx[::2], rstd * (g - g.mean(1, keepdims=True)), rstd * (np.abs(g) + np.abs(g).mean(1, keepdims=True)), DEPTH, "dx")
+
+
+@pytest.mark.parametrize("at", [0, -1])
+@pytest.mark.parametrize("cols", WIDTHS)
+def test_rows_constant_but_for_one_element(gns, cols, at):
+    """One that is a last place larger, the first or the last of the row. (That of 1e30 is
+    7.6e22, whose square is beyond fp32: no such row is promised anything but that its
+    neighbours are as they are.)"""
+    values = torch.tensor([1.0, 3.1e3, 1e7, -7e7, 3e16, 1e30], device="cuda")
+    x = values[:, None].repeat(1, cols)
+    x[:, at] = torch.nextafter(values, torch.full_like(values, float("inf")))
+    y, stats = gns.gns_layer_norm(x)
+    x, y, stats = x[:5], y[:5], stats[:5]
+    want, h, mean, rstd = L.layer_norm(f64(x))
+    assert_close(stats[:, 0], mean, np.abs(mean) / DEPTH, DEPTH, "mean")
+    assert_close(stats[:, 1], rstd, rstd, DEPTH, "rstd")
+    assert_close(y, want, np.abs(h) + 1, DEPTH, "y")
+
+
+def test_squares_beyond_fp32_are_no_spread_of_zero(gns):
+    """Rows of which they overflow have rstd = 0, NaN or their own, not that of a constant row."""
+    for cols in (512, 511, 20000, 20001):
+        x = torch.randn(3, cols, device="cuda") * 1e25 + 1e30
+        rstd = gns.gns_layer_norm(x)[1][:, 1]
+        assert ((rstd < 1e-20) & (rstd >= 0) | rstd.isnan()).all()
+
+
+@pytest.mark.parametrize("cols", [40, 512, 4093, 14336, 20001])
+def test_y_may_be_x(gns, cols):
+    """Through the C entry: rows without spread are then not read again, and are what the first sums give."""
+    x, _, _, w, b = inputs(400, cols, torch.float32, torch.float32, True, 0, cols)
+    x[::7] = torch.linspace(-1e6, 1e6, x[::7].shape[0], device="cuda")[:, None]
+    want, _ = gns.gns_layer_norm(x, w, b)
+    stats = torch.empty(400, 2, device="cuda")
+    gns._lib.call("gns_layer_norm", 0, x.data_ptr(), cols, 400, cols, 2, w.data_ptr(), b.data_ptr(), 2, 1e-5, 0, x.data_ptr(), cols,
+                  stats.data_ptr(), torch.cuda.current_stream().cuda_stream)
+    near = torch.arange(400, device="cuda") % 7 != 0
+    assert torch.equal(x[near], want[near]) and (stats[:, 1] > 0).all()
+    # Their mean is off by up to 2^-16.7 of 1e6 = 9.4, of which half a step times 1 / sqrt(eps) stays: 9.4 * 2^-24 * 317 = 1.8e-4.
+    assert ((x - want).abs()[~near] <= 2e-4 * w.abs() + 2.0 ** -23 * (w.abs() + b.abs())).all()
+
+
 @pytest.mark.parametrize("rows", [5, 400])
 def test_a_single_column_has_no_gradient(gns, rows):
     """h = 0 and g = mean(g), whatever 1 / sqrt(eps) is: dx is the residual's gradient."""
