@@ -38,6 +38,10 @@ struct SortPlan {
     long long alone, tile;
 };
 
+// Dynamic shared memory that a launch gets without asking: 48 KB less what the kernels and
+// their sources have statically, 64 bytes and the embedding's 4096.
+constexpr size_t kSortShared = 40 << 10;
+
 inline size_t sort_smem(int G) { return sizeof(int) * static_cast<size_t>(G + 1) * (kSortWarps + 1); }
 
 inline long long sort_blocks(const SortPlan& p) {
@@ -217,7 +221,7 @@ __global__ void __launch_bounds__(kSortThreads) sort_place_kernel(Source src, lo
 template <typename... KArgs, typename... Args>
 int sort_step(void (*kernel)(KArgs...), const SortPlan& p, unsigned extra, cudaStream_t s, Args... args) {
     const size_t smem = sort_smem(p.G);
-    if (smem > 48 * 1024) {
+    if (smem > kSortShared) {
         // The same for every call: another thread's call must not lower it before this launch.
         const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                                    static_cast<int>(sort_smem(kMaxDigit)));

@@ -1,5 +1,9 @@
 """Expert routing on the GPU against the oracle: the sort exactly, the moves
 within their fp32 roundings, gradients, empty experts and dropped slots."""
+import os
+import subprocess
+import sys
+
 import numpy as np
 import pytest
 
@@ -8,6 +12,8 @@ from oracle import block as B
 torch = pytest.importorskip("torch")
 pytestmark = pytest.mark.gpu
 from block_helpers import DTYPES, assert_close, f64, strided  # noqa: E402
+
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 
 
 @pytest.fixture(scope="module")
@@ -43,6 +49,28 @@ def test_sort(gns, id_type, tokens, topk, experts, drop, kind):
     assert np.array_equal(route.offsets.cpu().numpy(), offsets)
     assert np.array_equal(route.rows.cpu().numpy(), rows)
     assert np.array_equal(route.slots.cpu().numpy(), slots)
+
+
+FIRST_CALL = r"""
+import sys
+import torch
+sys.path.insert(0, sys.argv[1])
+import newton_schulz_gram_gb300 as gns
+gns.load()
+for tokens in (40, 9000):
+    ids = torch.randint(0, int(sys.argv[2]), (tokens, 1), device="cuda")
+    route = gns.gns_moe_sort(ids, int(sys.argv[2]))
+    assert torch.equal(route.slots.long(), ids.view(-1).argsort(stable=True))
+print("sorted")
+"""
+
+
+@pytest.mark.parametrize("experts", [600, 660, 719, 720, 721, 722, 723])
+def test_the_first_sort_of_a_process(gns, experts):
+    """Around the number of experts whose counts leave the kernels' default share of
+    shared memory; no call before has asked for more."""
+    r = subprocess.run([sys.executable, "-c", FIRST_CALL, ROOT, str(experts)], capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0 and r.stdout.strip() == "sorted", r.stderr[-2000:]
 
 
 def test_ids_outside_the_range_have_no_expert(gns):
