@@ -529,7 +529,7 @@ EmbeddingPlan embedding_plan(const EmbeddingJob& j, char* scratch) {
     p.chunk = 64;
     while (p.chunk > 8 && strips * j.tokens < kLeastRuns * p.chunk) p.chunk /= 2;
     while (static_cast<long long>(p.chunk) * 2048 < j.tokens) p.chunk *= 2;
-    p.chunks = (j.tokens + p.chunk - 1) / p.chunk;
+    p.chunks = static_cast<int>((static_cast<long long>(j.tokens) + p.chunk - 1) / p.chunk);
     const size_t row = sizeof(float) * pieces_of(j.cols, n, vec) * (vec ? n : kLoose);
     auto take = [&](size_t bytes) {
         char* at = scratch + p.bytes;

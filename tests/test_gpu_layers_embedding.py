@@ -149,3 +149,17 @@ def test_a_table_beyond_2_31_elements(gns):
     assert torch.equal(grad[0], dy[0]) and torch.equal(grad[600000], dy[3])
     assert torch.equal(grad[vocab - 1], (dy[1].float() + dy[2].float()).bfloat16())
     assert int((grad != 0).any(1).sum()) == 3
+
+
+def test_the_most_tokens(gns):
+    """2^31 - 4097 tokens of one column (60 GB with the intermediate memory): runs of 2^20,
+    whose sums of ones are exact in fp32."""
+    tokens, vocab = (1 << 31) - 1 - 4096, 1024
+    ids = torch.arange(tokens, dtype=torch.int32, device="cuda").bitwise_and_(vocab - 1)
+    grad = gns.gns_embedding_backward(torch.ones(tokens, 1, dtype=torch.bfloat16, device="cuda"), ids, vocab, out_dtype=torch.float32)
+    want = torch.full((vocab,), tokens // vocab, dtype=torch.int64, device="cuda")
+    want[:tokens % vocab] += 1
+    assert torch.equal(grad[:, 0].long(), want)
+    del ids
+    gns.gns_release()
+    torch.cuda.empty_cache()
