@@ -163,3 +163,33 @@ def test_the_most_tokens(gns):
     del ids
     gns.gns_release()
     torch.cuda.empty_cache()
+
+
+@pytest.mark.parametrize("dtype,cols", [(torch.float32, 2056), (torch.float32, 4104), (torch.bfloat16, 2049), (torch.bfloat16, 8200)])
+@pytest.mark.parametrize("shares", [(0.99,), (0.5, 0.45), (0.3, 0.3, 0.3)])
+def test_frequent_ids_of_wide_rows(gns, dtype, cols, shares):
+    """One id, two and three that each span more than 128 runs, of rows of more than 16 strips:
+    their sums are shared among blocks, and joined by the last one of each, strip by strip."""
+    rng = np.random.default_rng(cols + len(shares))
+    tokens, vocab = 40000, 40
+    ids = rng.choice(vocab, tokens, p=[*shares, *[(1 - sum(shares)) / (vocab - len(shares))] * (vocab - len(shares))])
+    ids = torch.from_numpy(ids).cuda()
+    dy = strided(tokens, cols, 0, dtype, rng)
+    first = gns.gns_embedding_backward(dy, ids, vocab, out_dtype=torch.float32)
+    D = dy.double()
+    want, mag = (torch.zeros(vocab, cols, dtype=torch.float64, device="cuda").index_add_(0, ids, t) for t in (D, D.abs()))
+    counts = torch.bincount(ids, minlength=vocab)
+    # A run's tokens one after the other, its id's runs by a warp's share of a block's, 16 warps, eight blocks.
+    depth = (64 + counts / 64 / 128 + 16 + 8 + 2).cpu().numpy()[:, None]
+    assert_close(first, f64(want), f64(mag) * depth, 0.5, "dtable")
+    for _ in range(3):
+        assert torch.equal(gns.gns_embedding_backward(dy, ids, vocab, out_dtype=torch.float32), first)
+
+
+@pytest.mark.parametrize("cols", [2056, 2049])
+def test_ids_of_many_runs_in_wide_rows(gns, cols):
+    """33 to 128 runs, which one block of each strip joins, of more than 16 strips."""
+    rng = np.random.default_rng(cols)
+    ids = np.repeat(np.arange(6) * 3, [33 * 64, 40 * 64 + 5, 127 * 64, 64, 129 * 64, 100 * 64 + 63])
+    ids = torch.from_numpy(rng.permutation(ids)).cuda()
+    gradient(gns, strided(ids.numel(), cols, 0, torch.float32, rng), ids, 17, 0.5)
