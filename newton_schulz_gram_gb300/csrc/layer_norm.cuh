@@ -275,11 +275,14 @@ inline bool ring_shape(int p, int n, int copies, RingShape* s) {
     while (s->ctas < kMaxCtas && p > s->ctas * few * most) s->ctas *= 2;
     // A block of nine to eleven warps would leave the processor's other half idle, which
     // costs more than the exchange (8192 rows of 5120 bf16 values: 47 us, 39 by two CTAs).
-    if (s->ctas == 1 && p > 256 * few && p < 384 * few) s->ctas = 2;
+    // One of twelve does not (5760: 44 us forward and 69 backward, 52 and 77 by two CTAs;
+    // fp32 60 and 93, 64 and 90).
+    if (s->ctas == 1 && p > 256 * few && p <= 352 * few) s->ctas = 2;
     s->per_cta = (p + s->ctas - 1) / s->ctas;
     // fp32 rows that would leave a quarter or more of the pieces of 64 threads' sixteen
     // elements empty: single pieces, which need half the registers (65536 x 640: 61 and 82
-    // us instead of 70 and 107, 768: 74 and 98 instead of 79 and 118; bf16 gains nothing).
+    // us instead of 70 and 107, 768: 78 and 98 instead of 79 and 118; bf16 gains nothing; rows
+    // of less than a warp, whose lanes are a power of two, were not tried).
     const bool single = few == 4 && p > 128 && p <= 192;
     s->resident = single ? 1024 : 512;
     if (single) s->V = 1;

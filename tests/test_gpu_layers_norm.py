@@ -97,6 +97,15 @@ def test_unaligned_rows_that_end_beside_a_warp(gns, cols):
 
 
 @pytest.mark.parametrize("dtype", list(DTYPES))
+@pytest.mark.parametrize("cols", [4088, 4096, 4104, 5624, 5632, 5640, 6136, 6144, 6152, 8192, 8200])
+def test_rows_at_the_borders_of_one_block(gns, cols, dtype):
+    """Eight, eleven, twelve and sixteen warps of sixteen elements a thread, and a piece to either side."""
+    x, dy, res, w, b = inputs(309, cols, DTYPES[dtype], torch.float32, True, 0, cols)
+    check(gns, x, dy, res, w, b, False)
+    check(gns, x, dy, None, w, None, True)
+
+
+@pytest.mark.parametrize("dtype", list(DTYPES))
 @pytest.mark.parametrize("rows,cols", [(1, 5), (7, 3), (9, 1), (1001, 11), (700, 257), (33, 4093), (1300, 4093), (50, 14341), (11, 65001)])
 def test_what_lies_between_unaligned_rows_is_not_looked_at(gns, rows, cols, dtype):
     """Rows a whole 16 bytes further apart, NaN in the gaps: the same as without them, bit for bit."""
