@@ -447,6 +447,8 @@ int gns_layer_norm(const void* x, int64_t ldx, int64_t rows, int cols, int dtype
  * gns_layer_norm_backward: with h = (x - mean) rstd and g = weight dy,
  *   dx = residual + rstd (g - mean(g) - h mean(g h)), without mean(g) where rms,
  *   dweight = sum over the rows of dy h, dbias = sum over the rows of dy.
+ *   stats           of the forward pass: the mean is the one rounded to fp32, so that h is
+ *                   off by up to half a step of the mean in deviations.
  *   residual        the gradient that reaches x past the norm, NULL for 0.
  *   dweight, dbias  [cols] of weight_dtype, NULL where not wanted; fp32 sums in an
  *                   order that the sizes and the number of SMs give, rounded once.
@@ -476,12 +478,13 @@ int gns_moe_gate(const void* logits, int64_t ld, int tokens, int num_experts, in
 
 /*
  * gns_moe_balance: with N the rows whose lse is not -inf, c_e the slots of
- * expert e, p = exp(logit - lse) and P_e the mean of p_e over the N rows,
+ * expert e, p the softmax of a row's logits and P_e the mean of p_e over the N rows,
  *   loss = balance * num_experts / (N topk) * sum_e c_e P_e + z / N * sum lse^2
  * (balance alone where all loads and probabilities are level; z keeps the logits
  * small). 0 where N is 0.
  *   ids, lse  as gns_moe_gate writes them; an id outside 0 .. num_experts - 1
- *             counts for no expert.
+ *             counts for no expert. lse is looked at for N and for z alone: the
+ *             probabilities, here and in the gradient, are made from the logits.
  *   loss      device fp32 [1], counts int32 [num_experts + 1] (the c_e, then N),
  *             probs fp32 [num_experts] (the P_e), written.
  * Takes intermediate memory. Its gradient is part of gns_moe_gate_backward.
@@ -519,8 +522,10 @@ int gns_embedding(const void* ids, int id_bytes, int64_t tokens, const void* tab
  *   dtable[v] = scale * sum over the tokens t with ids[t] = v of dy[t],
  * 0 for a row without a token. dy is of dtype, dtable of out_dtype; fp32 sums in
  * token order, joined over runs of sorted tokens, rounded once. Takes intermediate
- * memory: 16 bytes per token, one per row of the table, and 8 cols bytes for each run:
- * of 64 tokens, of fewer where there are few, or of as many as leave 2048 runs.
+ * memory: 16 bytes per token, one per row of the table, 8 per column for each run (of
+ * 64 tokens, of fewer where there are few, or of as many as leave 2048 runs; the columns
+ * rounded up to 128 where rows are not 16-byte aligned), and less than 1 MB for the sort's
+ * counts and those of the runs' sums, of tables of up to 65536 columns.
  */
 int gns_embedding_backward(const void* dy, int64_t lddy, const void* ids, int id_bytes, int64_t tokens, int64_t vocab,
                            int64_t cols, int dtype, double scale, void* dtable, int64_t lddt, int out_dtype, void* stream);

@@ -10,10 +10,12 @@
 // Bound: HBM, x read and y written once; but the instructions of a row's 4096 values and
 // its two sums take about as long. Rows go through shared memory ahead of their use, as
 // 16-byte pieces or, unaligned, as the words that hold them; rows beyond that are read
-// three times. 16384 x 4096 bf16 with fp32 weights: 52 us (5.1 TB/s; issue slots 65%
+// three times. 16384 x 4096 bf16 with fp32 weights: 51 us (5.3 TB/s; issue slots 68%
 // busy with 16 warps a processor: 24, by one row at a time instead of two, took 53);
-// 262144 x 128: 20 (6.6); 4096 x 14336 by two CTAs a row: 69 (3.4); 65536 x 257: 24;
-// one row: 2.4 (from registers alone 2.9; 304 rows 2.9 and 5.0).
+// 262144 x 128: 21 (6.3); by two CTAs a row 8192 x 5120: 39 (4.3) and 4096 x 14336: 71 (3.3);
+// unaligned 65536 x 257: 24 (2.8) and 16384 x 4093: 70 (3.9); one row: 2.4 (from registers
+// alone 2.9; 304 rows 2.9 and 5.0). Rows made anew take a block 4 us each at 4000 columns:
+// 16384 x 4000 fp32 takes 93 us, 940 if all of it is 123456.789.
 #include <algorithm>
 
 #include "layer_norm.cuh"

@@ -311,7 +311,8 @@ inline unsigned ring_clusters(const RingShape& c, long long batches, int num_sms
 // A thread has pairs of columns, `stride` apart: of rows of less than a warp the number
 // of its lanes, else 32, a warp then having consecutive columns, so that every access
 // of a thread lies at a known offset from its first (16384 x 4093 bf16: 69 us forward and
-// 162 backward; 73 and 165 with columns a block's threads apart, whose offsets are sums).
+// 162 backward with a residual; 73 and 165 with columns a block's threads apart, whose offsets
+// are sums).
 constexpr int kLoosePairs = 8;
 
 struct LooseColumns {

@@ -7,11 +7,12 @@
 // second kernel adds the blocks' in their order. Which rows a block takes follows
 // from the sizes and the number of SMs alone, so results repeat.
 //
-// Bound: HBM, x, dy (and the residual) read and dx written once. 16384 x 4096 bf16 with
-// fp32 weights: 73 us (5.5 TB/s), with the residual 89 (6.1), of which the second kernel
-// is 6; 262144 x 128: 37 (5.5); 4096 x 14336 by two CTAs a row: 106 (4.4); unaligned
-// 65536 x 257: 56, 16384 x 4093: 162, by instructions (single elements to and from
-// shared memory, 30 a value).
+// Bound: HBM, x, dy (and the residual) read and dx written once. Without a residual
+// 16384 x 4096 bf16 with fp32 weights: 73 us (5.5 TB/s), of which the second kernel is 6;
+// 262144 x 128: 37 (5.5); unaligned 65536 x 257: 56 (1.8). With one 16384 x 4096: 89 (6.1);
+// by two CTAs a row 8192 x 5120: 68 (4.9) and 4096 x 14336: 107 (4.4); unaligned 16384 x
+// 4093: 162 (3.3), by instructions (single elements to and from shared memory, 60 for
+// each of the row).
 #include <algorithm>
 #include <type_traits>
 
